@@ -269,6 +269,93 @@ moe_status moe_profile_end(moe_handle *h, int32_t *kernel_ids, float *ms, int32_
 /* Free the host handle (not the packed buffer, which the caller owns). NULL is a no-op. */
 void moe_destroy(moe_handle *h);
 
+/* ---------------------------------------------------------------------------------------------
+ * The dense 8-bit path around the layer: the residual addition and RMS norm in front of it (its
+ * BF16 x, or 8-bit codes with a scale per token), quantisation per token, and dense products of
+ * 8-bit codes -- plain, and gated (gate and up product with silu(g) * u) -- as of a dense
+ * feed-forward block, a projection or a shared expert whose weights are held in 8 bits.
+ *
+ * Codes are signed 8-bit integers in row-major rows, one FP32 scale per row (per token of an
+ * activation, per output channel of a weight): value = code * scale. Matrices are given as a pointer
+ * and a row stride ("ld", in elements, at least the width); rows may start at any address that
+ * is a multiple of the element size. The conventions at the head of this file hold (device
+ * pointers, caller's stream, no allocation, deterministic results).
+ * ------------------------------------------------------------------------------------------- */
+
+/* Element types of the norm's and quantiser's rows and of the products' outputs. */
+typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type;
+
+/* Residual addition and RMS norm of T rows of H values, in FP32 throughout:
+ *   s = x + delta;   y = s / sqrt(mean(s^2) + eps) * weight
+ * Each requested output is rounded once from these values: `sum` = s in x's type, `out` = y in BF16,
+ * and `codes` / `scales` = y in 8 bits: scales[t] = max|y[t]| / 127, codes = y / scales[t] rounded to
+ * nearest even. A row of zeros has scale 0 and codes 0; a row with a NaN or an infinity in y has
+ * scale NaN and codes 0, so that a product of it is NaN as well. `sum` may be x itself (same pointer
+ * and stride); no other output may overlap an input or another output. */
+typedef struct {
+    const void *x;        /* x_type [T, H]                                          */
+    const void *delta;    /* bf16 [T, H] added to x, or NULL                        */
+    const void *weight;   /* bf16 [H], or NULL for ones                             */
+    void *sum;            /* x_type [T, H], or NULL                                 */
+    void *out;            /* bf16 [T, H], or NULL                                   */
+    int8_t *codes;        /* [T, H], or NULL                                        */
+    float *scales;        /* [T], exactly when codes is given                       */
+    int64_t ldx, ldd, lds, ldo, ldc;   /* row strides of x, delta, sum, out, codes  */
+    int32_t T, H;         /* T >= 0 (0 enqueues nothing), H >= 1                    */
+    int32_t x_type;       /* moe_type                                               */
+    float eps;            /* >= 0                                                   */
+} moe_norm_args;
+moe_status moe_norm(const moe_norm_args *a, void *stream);
+
+/* Rows of x (x_type [T, K]) in 8 bits: the last line of moe_norm's formula with y = x. */
+moe_status moe_quantise(const void *x, int32_t x_type, int64_t ldx, int32_t T, int32_t K, int8_t *codes,
+                        int64_t ldc, float *scales, void *stream);
+/* The values that codes stand for: out = bf16(codes * scales[t]). */
+moe_status moe_dequantise(const int8_t *codes, int64_t ldc, const float *scales, int32_t T, int32_t K, void *out,
+                          int64_t ldo, void *stream);
+
+/* A dense product of 8-bit codes, for T tokens x of K codes with scales sx and weights w of N rows:
+ *   p(w, sw)[t, n] = (sum_k x[t, k] w[n, k]) * sx[t] * sw[n]
+ *   glu = 0:  out = p(w, sw) + bias
+ *   glu = 1:  out = silu(p(w, sw)) * p(w_up, sw_up),  silu(g) = g / (1 + exp(-g))
+ * The sum is exact (32-bit integers, hence K <= MOE_LINEAR_MAX_K); everything after it is FP32,
+ * rounded once to out_type. */
+#define MOE_LINEAR_MAX_K 131071
+typedef struct {
+    int32_t n;            /* output channels, >= 1                    */
+    int32_t k;            /* input width, 1..MOE_LINEAR_MAX_K         */
+    int32_t glu;          /* 0 or 1                                   */
+    int32_t out_type;     /* moe_type                                 */
+} moe_linear_config;
+
+/* Canonical weights (device, caller-owned; read only by moe_linear_create's packing kernel). */
+typedef struct {
+    const int8_t *w;        /* [n, k], contiguous (the gate's when glu)  */
+    const float *scales;    /* [n]                                       */
+    const int8_t *w_up;     /* [n, k] (glu only, else NULL)              */
+    const float *scales_up; /* [n]    (glu only, else NULL)              */
+    const float *bias;      /* [n], or NULL; must be NULL when glu       */
+} moe_linear_weights;
+
+typedef struct moe_linear moe_linear;
+
+/* Sizes of the packed buffer and of the workspace for calls of up to T_max tokens (host only; either
+ * output may be NULL). */
+moe_status moe_linear_query(const moe_linear_config *cfg, int32_t T_max, size_t *packed_bytes,
+                            size_t *workspace_bytes);
+/* Validate, then enqueue the packing of the weights, scales and bias into `packed` (256-byte aligned):
+ * 16 rows x 64 codes per 1 KiB block in matrix-core operand order, padded with zeros to 16 rows and
+ * 128 codes, gate and up rows alternating per 16. `packed` must stay alive and unmodified until
+ * moe_linear_destroy; the handle itself is host memory. */
+moe_status moe_linear_create(const moe_linear_config *cfg, const moe_linear_weights *w, void *packed,
+                             size_t packed_bytes, void *stream, moe_linear **out);
+/* The product for T >= 0 tokens (0 enqueues nothing). x: codes [T, k]; scales [T]; out: out_type
+ * [T, n], must not overlap any input. workspace: 256-byte aligned, >= moe_linear_query(cfg, T). */
+moe_status moe_linear_forward(moe_linear *l, const int8_t *x, int64_t ldx, const float *scales, int32_t T, void *out,
+                              int64_t ldo, void *workspace, size_t workspace_bytes, void *stream);
+/* Free the host handle (not the packed buffer). NULL is a no-op. */
+void moe_linear_destroy(moe_linear *l);
+
 /* Static description of a status code. */
 const char *moe_strerror(moe_status s);
 

@@ -14,6 +14,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmxmoe.so")
 
 c_i32 = ctypes.c_int32
+c_i64 = ctypes.c_int64
 c_vp = ctypes.c_void_p
 c_size = ctypes.c_size_t
 
@@ -57,6 +58,25 @@ class MoeRouting(ctypes.Structure):
     _fields_ = [(n, c_vp) for n in ROUTING_FIELDS]
 
 
+TYPE_BF16 = 0
+TYPE_F32 = 1
+LINEAR_MAX_K = 131071   # MOE_LINEAR_MAX_K
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = ([(n, c_vp) for n in ("x", "delta", "weight", "sum", "out", "codes", "scales")]
+                + [(n, c_i64) for n in ("ldx", "ldd", "lds", "ldo", "ldc")]
+                + [("T", c_i32), ("H", c_i32), ("x_type", c_i32), ("eps", ctypes.c_float)])
+
+
+class LinearConfig(ctypes.Structure):
+    _fields_ = [("n", c_i32), ("k", c_i32), ("glu", c_i32), ("out_type", c_i32)]
+
+
+class LinearWeights(ctypes.Structure):
+    _fields_ = [(n, c_vp) for n in ("w", "scales", "w_up", "scales_up", "bias")]
+
+
 # name -> (restype, argtypes); the exported C symbols of the library
 SIGNATURES = {
     "moe_query": (c_i32, [ctypes.POINTER(MoeConfig), c_i32, ctypes.POINTER(c_size), ctypes.POINTER(c_size)]),
@@ -76,6 +96,15 @@ SIGNATURES = {
     "moe_profile_begin": (c_i32, [c_vp, c_i32]),
     "moe_profile_end": (c_i32, [c_vp, ctypes.POINTER(c_i32), ctypes.POINTER(ctypes.c_float), ctypes.POINTER(c_i32)]),
     "moe_destroy": (None, [c_vp]),
+    "moe_norm": (c_i32, [ctypes.POINTER(NormArgs), c_vp]),
+    "moe_quantise": (c_i32, [c_vp, c_i32, c_i64, c_i32, c_i32, c_vp, c_i64, c_vp, c_vp]),
+    "moe_dequantise": (c_i32, [c_vp, c_i64, c_vp, c_i32, c_i32, c_vp, c_i64, c_vp]),
+    "moe_linear_query": (c_i32, [ctypes.POINTER(LinearConfig), c_i32, ctypes.POINTER(c_size),
+                                 ctypes.POINTER(c_size)]),
+    "moe_linear_create": (c_i32, [ctypes.POINTER(LinearConfig), ctypes.POINTER(LinearWeights), c_vp, c_size, c_vp,
+                                  ctypes.POINTER(c_vp)]),
+    "moe_linear_forward": (c_i32, [c_vp, c_vp, c_i64, c_vp, c_i32, c_vp, c_i64, c_vp, c_size, c_vp]),
+    "moe_linear_destroy": (None, [c_vp]),
     "moe_strerror": (ctypes.c_char_p, [c_i32]),
 }
 
@@ -224,3 +253,21 @@ def profile_end(h, max_launches: int) -> list:
 
 def destroy(h) -> None:
     lib().moe_destroy(h)
+
+
+def linear_query(cfg: LinearConfig, T_max: int):
+    pb, wb = c_size(0), c_size(0)
+    check(lib().moe_linear_query(ctypes.byref(cfg), T_max, ctypes.byref(pb), ctypes.byref(wb)), "moe_linear_query")
+    return pb.value, wb.value
+
+
+def linear_create(cfg: LinearConfig, w, scales, w_up, scales_up, bias, packed, stream=None) -> c_vp:
+    lw = LinearWeights(ptr(w), ptr(scales), ptr(w_up), ptr(scales_up), ptr(bias))
+    h = c_vp()
+    check(lib().moe_linear_create(ctypes.byref(cfg), ctypes.byref(lw), ptr(packed), packed.numel(),
+                                  stream_handle(stream), ctypes.byref(h)), "moe_linear_create")
+    return h
+
+
+def linear_destroy(h) -> None:
+    lib().moe_linear_destroy(h)

@@ -1,0 +1,384 @@
+// norm.hip -- residual addition with RMS norm, quantisation per token, and its reading back.
+//
+// One pass: a row's values stay in registers, as FP32, from their load to the last output, so each
+// input is read once and each output written once; the row's sum of squares and its largest
+// magnitude are two reductions over the threads that share the row. Bound by HBM: per value about
+// eight FP32 operations for 5 to 13 bytes.
+#include "dense.hpp"
+#include "wave.hpp"
+
+namespace mxmoe {
+
+namespace {
+
+constexpr int CHUNK = 8;   // consecutive values per thread and load
+
+// Rows need not be aligned beyond their element size: the copies below compile to one wide global
+// access, which gfx950 serves at any byte address.
+template <typename T>
+__device__ inline T load_any(const void *p)
+{
+    T v;
+    __builtin_memcpy(&v, p, sizeof(T));
+    return v;
+}
+template <typename T>
+__device__ inline void store_any(void *p, const T &v) { __builtin_memcpy(p, &v, sizeof(T)); }
+
+// CHUNK values from column c on of a row of n values (zeros past n), as FP32.
+__device__ inline void load_row(const uint16_t *row, int c, int n, float *v)
+{
+    if (c + CHUNK <= n) {
+        const u32x4_t r = load_any<u32x4_t>(row + c);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[2 * i] = __uint_as_float(r[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < CHUNK; i++)
+            v[i] = c + i < n ? bf16_bits_to_f32(row[c + i]) : 0.f;
+    }
+}
+__device__ inline void load_row(const float *row, int c, int n, float *v)
+{
+    if (c + CHUNK <= n) {
+        const f32x4_t a = load_any<f32x4_t>(row + c), b = load_any<f32x4_t>(row + c + 4);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < CHUNK; i++)
+            v[i] = c + i < n ? row[c + i] : 0.f;
+    }
+}
+
+__device__ inline void store_row(uint16_t *row, int c, int n, const float *v)
+{
+    u32x4_t r;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        r[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    if (c + CHUNK <= n) {
+        store_any(row + c, r);
+    } else {
+#pragma unroll
+        for (int i = 0; i < CHUNK; i++)
+            if (c + i < n)
+                row[c + i] = (uint16_t)(r[i / 2] >> (16 * (i % 2)));
+    }
+}
+__device__ inline void store_row(float *row, int c, int n, const float *v)
+{
+    if (c + CHUNK <= n) {
+        store_any(row + c, f32x4_t{v[0], v[1], v[2], v[3]});
+        store_any(row + c + 4, f32x4_t{v[4], v[5], v[6], v[7]});
+    } else {
+#pragma unroll
+        for (int i = 0; i < CHUNK; i++)
+            if (c + i < n)
+                row[c + i] = v[i];
+    }
+}
+// Codes: v * f rounded to nearest even (|v * f| <= 127 up to rounding, which rint takes back).
+__device__ inline void store_codes(int8_t *row, int c, int n, const float *v, float up, float f)
+{
+    uint2 r{0u, 0u};
+#pragma unroll
+    for (int i = 0; i < CHUNK; i++) {
+        const uint32_t q = (uint32_t)(int)rintf(v[i] * up * f) & 0xFFu;
+        if (i < 4)
+            r.x |= q << (8 * i);
+        else
+            r.y |= q << (8 * (i - 4));
+    }
+    if (c + CHUNK <= n) {
+        store_any(row + c, r);
+    } else {
+#pragma unroll
+        for (int i = 0; i < CHUNK; i++)
+            if (c + i < n)
+                row[c + i] = (int8_t)((i < 4 ? r.x : r.y) >> (8 * (i % 4)));
+    }
+}
+
+// Reductions over the NT threads of a row, in a fixed order; every thread gets the result. `sh` holds
+// one word per wave and is not reused by the other reduction.
+template <int NT>
+__device__ inline float row_sum(float v, float *sh)
+{
+    v = wave_sum_f32(v);
+    if constexpr (NT > WAVE) {
+        if ((threadIdx.x & (WAVE - 1)) == 0)
+            sh[threadIdx.x / WAVE] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int w = 0; w < NT / WAVE; w++)
+            v += sh[w];
+    }
+    return v;
+}
+template <int NT>
+__device__ inline uint32_t row_max(uint32_t v, uint32_t *sh)
+{
+    v = wave_max_u32(v);
+    if constexpr (NT > WAVE) {
+        if ((threadIdx.x & (WAVE - 1)) == 0)
+            sh[threadIdx.x / WAVE] = v;
+        __syncthreads();
+        v = 0u;
+#pragma unroll
+        for (int w = 0; w < NT / WAVE; w++)
+            v = max(v, sh[w]);
+    }
+    return v;
+}
+
+// Scale of a row from the bits of its largest magnitude (as unsigned integers magnitudes order like
+// their values, with infinities and then NaNs above), and the two factors that take a value to its
+// code: `up` lifts tiny rows first, so that 127 / largest stays finite.
+__device__ inline float row_scale(uint32_t top, float &up, float &f)
+{
+    up = 1.f;
+    f = 0.f;
+    if (top == 0u)
+        return 0.f;
+    if (top >= 0x7F800000u)
+        return __uint_as_float(0x7FC00000u);
+    const float m = __uint_as_float(top);
+    if (m < 0x1p-60f)
+        up = 0x1p80f;
+    f = 127.f / (m * up);
+    return m / 127.f;
+}
+
+// NT threads per row (64: four rows per workgroup, one per wave; else one workgroup per row), NV
+// chunks of 8 values per thread; H <= NT * NV * 8.
+template <typename X, int NT, int NV, bool NORM>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_kernel(const moe_norm_args a)
+{
+    __shared__ float sh_sum[NT / WAVE];
+    __shared__ uint32_t sh_max[NT / WAVE];
+    constexpr int ROWS = NT < 256 ? 256 / NT : 1;
+    const int t = threadIdx.x % NT;
+    const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / NT;
+    if (ROWS > 1 && r >= a.T)
+        return;   // whole waves, and rows of one wave meet no barrier
+    const X *x = static_cast<const X *>(a.x) + r * a.ldx;
+    float v[NV][CHUNK];
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+        load_row(x, (t + i * NT) * CHUNK, a.H, v[i]);
+    if constexpr (NORM) {
+        if (a.delta) {
+            const uint16_t *d = static_cast<const uint16_t *>(a.delta) + r * a.ldd;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                float w[CHUNK];
+                load_row(d, (t + i * NT) * CHUNK, a.H, w);
+#pragma unroll
+                for (int j = 0; j < CHUNK; j++)
+                    v[i][j] += w[j];
+            }
+        }
+        if (a.sum) {
+            X *s = static_cast<X *>(a.sum) + r * a.lds;
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                store_row(s, (t + i * NT) * CHUNK, a.H, v[i]);
+        }
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+#pragma unroll
+            for (int j = 0; j < CHUNK; j++)
+                ss = fmaf(v[i][j], v[i][j], ss);
+        const float rstd = 1.f / sqrtf(row_sum<NT>(ss, sh_sum) / (float)a.H + a.eps);
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            float w[CHUNK];
+            if (a.weight)
+                load_row(static_cast<const uint16_t *>(a.weight), (t + i * NT) * CHUNK, a.H, w);
+#pragma unroll
+            for (int j = 0; j < CHUNK; j++)
+                v[i][j] = a.weight ? v[i][j] * rstd * w[j] : v[i][j] * rstd;
+        }
+        if (a.out) {
+            uint16_t *o = static_cast<uint16_t *>(a.out) + r * a.ldo;
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                store_row(o, (t + i * NT) * CHUNK, a.H, v[i]);
+        }
+        if (!a.codes)
+            return;
+    }
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+#pragma unroll
+        for (int j = 0; j < CHUNK; j++)   // columns past H hold 0, or 0 * rstd = NaN where rstd is not finite
+            top = max(top, (t + i * NT) * CHUNK + j < a.H ? __float_as_uint(v[i][j]) & 0x7FFFFFFFu : 0u);
+    float up, f;
+    const float scale = row_scale(row_max<NT>(top, sh_max), up, f);
+    if (t == 0)
+        a.scales[r] = scale;
+    int8_t *q = a.codes + r * a.ldc;
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        if (f == 0.f)   // zeros, or a row that holds no finite scale
+#pragma unroll
+            for (int j = 0; j < CHUNK; j++)
+                v[i][j] = 0.f;
+        store_codes(q, (t + i * NT) * CHUNK, a.H, v[i], up, f);
+    }
+}
+
+// Rows longer than the registers of one workgroup hold: three passes over the row, the second and
+// third out of cache. `sum` may be x, so it is written in the last pass only.
+template <typename X, bool NORM>
+__global__ __launch_bounds__(1024) void norm_long_kernel(const moe_norm_args a)
+{
+    constexpr int NT = 1024;
+    __shared__ float sh_sum[NT / WAVE];
+    __shared__ uint32_t sh_max[NT / WAVE];
+    const int t = threadIdx.x;
+    const int64_t r = blockIdx.x;
+    const X *x = static_cast<const X *>(a.x) + r * a.ldx;
+    const uint16_t *d = static_cast<const uint16_t *>(a.delta) + r * a.ldd;
+    auto summed = [&](int c, float *v) {
+        load_row(x, c, a.H, v);
+        if (NORM && a.delta) {
+            float w[CHUNK];
+            load_row(d, c, a.H, w);
+#pragma unroll
+            for (int j = 0; j < CHUNK; j++)
+                v[j] += w[j];
+        }
+    };
+    float rstd = 1.f;
+    if constexpr (NORM) {
+        float ss = 0.f;
+        for (int c = t * CHUNK; c < a.H; c += NT * CHUNK) {
+            float v[CHUNK];
+            summed(c, v);
+#pragma unroll
+            for (int j = 0; j < CHUNK; j++)
+                ss = fmaf(v[j], v[j], ss);
+        }
+        rstd = 1.f / sqrtf(row_sum<NT>(ss, sh_sum) / (float)a.H + a.eps);
+    }
+    auto scaled = [&](int c, float *v) {
+        if constexpr (NORM) {
+            float w[CHUNK];
+            if (a.weight)
+                load_row(static_cast<const uint16_t *>(a.weight), c, a.H, w);
+#pragma unroll
+            for (int j = 0; j < CHUNK; j++)
+                v[j] = a.weight ? v[j] * rstd * w[j] : v[j] * rstd;
+        }
+    };
+    float up = 1.f, f = 0.f;
+    if (a.codes) {
+        uint32_t top = 0u;
+        for (int c = t * CHUNK; c < a.H; c += NT * CHUNK) {
+            float v[CHUNK];
+            summed(c, v);
+            scaled(c, v);
+#pragma unroll
+            for (int j = 0; j < CHUNK; j++)
+                top = max(top, c + j < a.H ? __float_as_uint(v[j]) & 0x7FFFFFFFu : 0u);
+        }
+        const float scale = row_scale(row_max<NT>(top, sh_max), up, f);
+        if (t == 0)
+            a.scales[r] = scale;
+    }
+    for (int c = t * CHUNK; c < a.H; c += NT * CHUNK) {
+        float v[CHUNK];
+        summed(c, v);
+        if (NORM && a.sum)
+            store_row(static_cast<X *>(a.sum) + r * a.lds, c, a.H, v);
+        scaled(c, v);
+        if (NORM && a.out)
+            store_row(static_cast<uint16_t *>(a.out) + r * a.ldo, c, a.H, v);
+        if (a.codes) {
+            if (f == 0.f)
+#pragma unroll
+                for (int j = 0; j < CHUNK; j++)
+                    v[j] = 0.f;
+            store_codes(a.codes + r * a.ldc, c, a.H, v, up, f);
+        }
+    }
+}
+
+// 16 codes per thread.
+__global__ __launch_bounds__(256) void dequantise_kernel(const int8_t *codes, int64_t ldc, const float *scales, int K,
+                                                         int64_t chunks, int64_t total, uint16_t *out, int64_t ldo)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total)
+        return;
+    const int64_t r = i / chunks;
+    const int c = (int)(i % chunks) * 16;
+    const int8_t *q = codes + r * ldc + c;
+    uint16_t *o = out + r * ldo + c;
+    const float s = scales[r];
+    if (c + 16 <= K) {
+        const u32x4_t v = load_any<u32x4_t>(q);
+        u32x4_t w[2];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const uint32_t word = v[j / 2] >> (16 * (j % 2));
+            w[j / 4][j % 4] = pack_bf16x2((float)(int8_t)word * s, (float)(int8_t)(word >> 8) * s);
+        }
+        store_any(o, w[0]);
+        store_any(o + 8, w[1]);
+    } else {
+        for (int j = 0; c + j < K; j++)
+            o[j] = (uint16_t)f32_to_bf16_bits((float)q[j] * s);
+    }
+}
+
+template <typename X, bool NORM>
+hipError_t launch_rows(const moe_norm_args &a, hipStream_t st)
+{
+    const dim3 rows((unsigned)a.T), quarter((unsigned)((a.T + 3) / 4));
+    const int H = a.H;
+    if (H <= 64 * CHUNK)
+        hipLaunchKernelGGL((norm_kernel<X, 64, 1, NORM>), quarter, dim3(256), 0, st, a);
+    else if (H <= 256 * CHUNK)
+        hipLaunchKernelGGL((norm_kernel<X, 256, 1, NORM>), rows, dim3(256), 0, st, a);
+    else if (H <= 256 * CHUNK * 2)
+        hipLaunchKernelGGL((norm_kernel<X, 256, 2, NORM>), rows, dim3(256), 0, st, a);
+    else if (H <= 256 * CHUNK * 4)
+        hipLaunchKernelGGL((norm_kernel<X, 256, 4, NORM>), rows, dim3(256), 0, st, a);
+    else if (H <= 1024 * CHUNK * 2)
+        hipLaunchKernelGGL((norm_kernel<X, 1024, 2, NORM>), rows, dim3(1024), 0, st, a);
+    else
+        hipLaunchKernelGGL((norm_long_kernel<X, NORM>), rows, dim3(1024), 0, st, a);
+    return hipGetLastError();
+}
+
+} // namespace
+
+hipError_t launch_norm(const moe_norm_args &a, bool norm, hipStream_t st)
+{
+    if (a.x_type == MOE_TYPE_F32)
+        return norm ? launch_rows<float, true>(a, st) : launch_rows<float, false>(a, st);
+    return norm ? launch_rows<uint16_t, true>(a, st) : launch_rows<uint16_t, false>(a, st);
+}
+
+hipError_t launch_dequantise(const int8_t *codes, int64_t ldc, const float *scales, int32_t T, int32_t K, uint16_t *out,
+                             int64_t ldo, hipStream_t st)
+{
+    const int64_t chunks = (K + 15) / 16, total = T * chunks;
+    hipLaunchKernelGGL(dequantise_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st, codes, ldc, scales, K,
+                       chunks, total, out, ldo);
+    return hipGetLastError();
+}
+
+} // namespace mxmoe

@@ -1,0 +1,417 @@
+"""The dense 8-bit path on the GPU against plain 64-bit forms: norm, quantisation, products, gated
+products, and the block that runs them together. Bounds: tests/dense_ref.py."""
+import numpy as np
+import pytest
+import torch
+
+from tests import dense_ref as R
+from tests import gpu_helpers as G
+
+pytestmark = [pytest.mark.gpu, pytest.mark.timeout(120)]
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    G.ensure_built()
+    yield
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def rows(T, n, dtype, g, pad=0, offset=0, sigma=1.0):
+    """[T, n] normal rows on the GPU, `pad` elements apart, starting `offset` elements into a buffer."""
+    ld = n + pad
+    buf = torch.zeros(offset + T * ld + 8, dtype=dtype)
+    t = buf[offset:offset + T * ld].view(T, ld)[:, :n]
+    t.copy_(torch.randn(T, n, generator=g) * sigma)
+    d = buf.cuda()
+    return d[offset:offset + T * ld].view(T, ld)[:, :n]
+
+
+def codes_rows(T, n, g, pad=0, offset=0):
+    ld = n + pad
+    buf = torch.randint(-128, 128, (offset + T * ld + 8,), generator=g, dtype=torch.int8).cuda()
+    return buf[offset:offset + T * ld].view(T, ld)[:, :n]
+
+
+def guarded(T, n, dtype, pad=3):
+    """An output inside a larger buffer whose other elements must not change."""
+    buf = torch.full((T * (n + pad) + 64,), 77, dtype=dtype, device="cuda")
+    view = buf[32:32 + T * (n + pad)].view(T, n + pad)[:, :n]
+
+    def untouched():
+        b = buf.clone()
+        b[32:32 + T * (n + pad)].view(T, n + pad)[:, :n] = 77
+        return bool((b == 77).all())
+    return view, untouched
+
+
+# widths on both sides of every kernel's limit (512, 2048, 4096, 8192, 16384) and past the last
+WIDTHS = [1, 7, 8, 100, 511, 512, 513, 2048, 2051, 4096, 4097, 7168, 8193, 16384, 16391, 40001]
+
+
+@pytest.mark.parametrize("H", WIDTHS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_all_outputs(H, dtype):
+    from mxfp4_latent_mixture_sigmoid_amd import rms_norm
+    T, g = (3 if H > 512 else 9), gen(H)
+    x, d = rows(T, H, dtype, g, pad=5, offset=1), rows(T, H, BF16, g, pad=1, offset=3)
+    w = (1 + 0.1 * torch.randn(H, generator=g)).bfloat16().cuda()
+    out, ok_o = guarded(T, H, BF16)
+    codes, ok_q = guarded(T, H, torch.int8)
+    total, ok_s = guarded(T, H, dtype)
+    r = rms_norm(x, w, 1e-5, delta=d, sum=total, out=out, codes=codes)
+    s, y = R.norm(f64(x), f64(d), f64(w), float(np.float32(1e-5)))
+    size = R.B if dtype is BF16 else 0
+    R.check(f64(r.sum), s, np.abs(s) * (size + 2 * R.U), "sum")
+    # where x and delta cancel, y inherits the rounding of their sum: u of either
+    lost = 2 * R.U * (np.abs(f64(x)) + np.abs(f64(d))) * np.abs(y) / np.maximum(np.abs(s), 1e-30)
+    R.check(f64(r.out), y, np.abs(y) * (R.B + R.NORM_REL) + 2 * lost, "out")
+    if np.all(lost <= 0.01 * R.scales(y)[:, None]):
+        R.check_codes(r.codes.cpu().numpy(), f64(r.scales), y, R.NORM_REL + 2e-6, "codes")
+    assert ok_o() and ok_q() and ok_s()
+
+
+@pytest.mark.parametrize("T", [1, 2, 4, 5, 64, 1000])
+@pytest.mark.parametrize("H", [256, 1000, 7168])
+def test_norm_plain(T, H):
+    """No residual, no weight; one output at a time gives the bits of all at once."""
+    from mxfp4_latent_mixture_sigmoid_amd import rms_norm
+    x = rows(T, H, BF16, gen(T + H), sigma=3.0)
+    r = rms_norm(x, codes=True)
+    _, y = R.norm(f64(x), None, None, float(np.float32(1e-6)))
+    R.check(f64(r.out), y, np.abs(y) * (R.B + R.NORM_REL), "out")
+    R.check_codes(r.codes.cpu().numpy(), f64(r.scales), y, R.NORM_REL, "codes")
+    assert torch.equal(rms_norm(x).out, r.out)
+    only = rms_norm(x, out=False, codes=True)
+    assert only.out is None and only.sum is None
+    assert torch.equal(only.codes, r.codes) and torch.equal(only.scales, r.scales)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H", [130, 3000, 20000])
+def test_norm_sum_in_place(dtype, H):
+    from mxfp4_latent_mixture_sigmoid_amd import rms_norm
+    g = gen(H)
+    x, d = rows(6, H, dtype, g), rows(6, H, BF16, g)
+    apart = rms_norm(x, delta=d, sum=True, codes=True)
+    r = rms_norm(x, delta=d, sum=x, codes=True)
+    assert r.sum is x
+    for a, b in zip(r, apart):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("H", [64, 3000, 20000])
+def test_norm_rows_without_a_norm(H):
+    """Zero rows, NaN, infinities and values at both ends of the type, each in a row of its own."""
+    from mxfp4_latent_mixture_sigmoid_amd import rms_norm
+    x = rows(8, H, F32, gen(1))
+    x[1] = 0
+    x[2, H // 2] = float("nan")
+    x[3, 0] = float("inf")
+    x[4] = 1e-30
+    x[5] *= 1e15
+    x[6, 3] = -float("inf")
+    r = rms_norm(x, eps=1e-6, codes=True)
+    good = [0, 1, 4, 5, 7]
+    _, y = R.norm(f64(x)[good], None, None, float(np.float32(1e-6)))
+    R.check(f64(r.out)[good], y, np.abs(y) * (R.B + R.NORM_REL), "out")
+    R.check_codes(r.codes.cpu().numpy()[good], f64(r.scales)[good], y, R.NORM_REL, "codes")
+    assert torch.isnan(r.out[2]).all()
+    for row, col in ((3, 0), (6, 3)):     # inf / inf at the infinity, 0 elsewhere
+        nan = torch.isnan(r.out[row])
+        assert nan[col] and nan.sum() == 1 and (r.out[row][~nan] == 0).all()
+    for row in (2, 3, 6):
+        assert torch.isnan(r.scales[row]) and not r.codes[row].any()
+    zero = rms_norm(torch.zeros(2, H, device="cuda"), eps=0.0, codes=True)      # 0 / 0
+    assert torch.isnan(zero.out).all() and torch.isnan(zero.scales).all() and not zero.codes.any()
+
+
+@pytest.mark.parametrize("K", [1, 9, 512, 777, 2048, 14336, 16385, 33000])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_quantise_and_back(K, dtype):
+    from mxfp4_latent_mixture_sigmoid_amd import dequantise, quantise
+    T = 7
+    x = rows(T, K, dtype, gen(K), pad=3, offset=1)
+    x[1] = 0
+    x[2] *= 1e-36                # the lifted range: 127 / max|x| would overflow
+    x[3] *= 1e30
+    if K > 8:
+        x[4, 5] = float("nan")
+        x[5, 6] = -float("inf")
+    codes, ok_q = guarded(T, K, torch.int8)
+    codes, scales = quantise(x, codes=codes)
+    R.check_codes(codes.cpu().numpy(), f64(scales), f64(x), 0.0, "codes")
+    out, ok_o = guarded(T, K, BF16)
+    back = dequantise(codes, scales, out=out)
+    v = f64(codes) * f64(scales)[:, None]
+    R.check(f64(back), v, np.abs(v) * (R.B + R.U) + 2.0 ** -133, "values")
+    assert ok_q() and ok_o()
+
+
+def test_no_tokens():
+    from mxfp4_latent_mixture_sigmoid_amd import Int8Linear, dequantise, quantise, rms_norm
+    x = torch.empty(0, 96, dtype=BF16, device="cuda")
+    r = rms_norm(x, delta=x, sum=True, codes=True)
+    assert r.out.shape == r.codes.shape == (0, 96) and r.scales.shape == (0,)
+    q, s = quantise(x)
+    assert dequantise(q, s).shape == (0, 96)
+    w = torch.ones(40, 96, dtype=torch.int8, device="cuda")
+    assert Int8Linear(w, torch.ones(40, device="cuda"), T_max=0).forward(q, s).shape == (0, 40)
+
+
+def make(N, K, glu, g, bias=False, **kw):
+    from mxfp4_latent_mixture_sigmoid_amd import Int8Linear
+    w = [torch.randint(-128, 128, (N, K), generator=g, dtype=torch.int8).cuda() for _ in range(1 + glu)]
+    # products of a few units: codes of deviation ~74 each, so sums of ~5500 sqrt(K)
+    s = [((0.5 + torch.rand(N, generator=g)) / (2000 * K ** 0.5)).cuda() for _ in range(1 + glu)]
+    b = torch.randn(N, generator=g).cuda() if bias else None
+    layer = Int8Linear(w[0], s[0], bias=b, up_codes=w[1] if glu else None, up_scales=s[1] if glu else None, **kw)
+    return layer, [t.cpu().numpy() for t in w], [f64(t) for t in s], None if b is None else f64(b)
+
+
+def reference(x, sx, w, s, b, bf16):
+    """(result, allowed error). One rounding of the sum to FP32 and two of the scalings: 3 u of a product;
+    the gate's error reaches silu through exp(-g), at most |g| times relative; the FP32 functions
+    themselves a few units."""
+    p = R.product(x, w[0], sx, s[0])
+    if len(w) == 2:
+        u = R.product(x, w[1], sx, s[1])
+        ref = R.silu(p) * u
+        err = np.abs(ref) * ((24 + 6 * np.abs(p)) * R.U) + np.abs(u) * 2.0 ** -120
+    else:
+        ref = p + (0 if b is None else b)
+        err = 4 * R.U * (np.abs(p) + (0 if b is None else np.abs(b)))
+    return ref, err + (np.abs(ref) * R.B + 2.0 ** -133 if bf16 else 0)
+
+
+SIZES = [  # T, N, K, pad of x, offset of x: both sides of 16-row and 128-code blocks and of the tiles
+    (1, 1, 1, 0, 0), (1, 16, 128, 0, 0), (1, 700, 3584, 0, 0), (2, 17, 127, 0, 1), (3, 100, 129, 7, 0),
+    (15, 64, 64, 0, 0), (16, 65, 144, 0, 0), (17, 31, 1000, 8, 0), (31, 96, 272, 0, 3), (33, 48, 256, 16, 16),
+    (63, 200, 1111, 0, 0), (64, 129, 2048, 0, 0), (65, 127, 640, 0, 0), (100, 333, 777, 5, 2), (128, 256, 512, 0, 0),
+    (129, 257, 513, 0, 0), (200, 1000, 384, 0, 0), (256, 64, 4352, 0, 0), (300, 520, 96, 0, 0), (777, 1001, 1535, 1, 0),
+    (1500, 272, 160, 0, 0), (64, 3000, 7168, 0, 0), (40, 2064, 14336, 0, 0), (513, 515, 130, 0, 0),
+]
+
+
+@pytest.mark.parametrize("T,N,K,pad,offset", SIZES)
+@pytest.mark.parametrize("kind", ["bf16", "f32+bias", "glu", "glu f32"])
+def test_products(T, N, K, pad, offset, kind):
+    g = gen(T * 1000 + N + K)
+    out_dtype = F32 if "f32" in kind else BF16
+    layer, w, s, b = make(N, K, "glu" in kind, g, bias="bias" in kind, T_max=T, out_dtype=out_dtype)
+    x = codes_rows(T, K, g, pad, offset)
+    sx = (0.5 + torch.rand(T, generator=g)).cuda()
+    out, ok = guarded(T, N, out_dtype)
+    layer.forward(x, sx, out=out)
+    ref, err = reference(x.cpu().numpy(), f64(sx), w, s, b, out_dtype is BF16)
+    R.check(f64(out), ref, err, f"{kind} {T}x{N}x{K}")
+    assert ok()
+
+
+@pytest.mark.parametrize("T,N,K,glu", [(2048, 4096, 640, 0), (4100, 4200, 272, 0), (2304, 2100, 384, 1),
+                                       (1030, 1100, 1024, 0), (8192, 500, 128, 0), (300, 9000, 256, 1)])
+def test_products_large(T, N, K, glu):
+    """The large tiles, whole and ragged, against exact sums in FP64 on the GPU."""
+    g = gen(T + N)
+    layer, w, s, _ = make(N, K, glu, g, T_max=T)
+    x, sx = codes_rows(T, K, g), (0.5 + torch.rand(T, generator=g)).cuda()
+    out = layer.forward(x, sx).double()
+
+    def product(w, s):
+        w, s = torch.from_numpy(w).cuda().double(), torch.from_numpy(s).cuda()
+        return (x.double() @ w.t().contiguous()) * sx.double()[:, None] * s
+    p = product(w[0], s[0])
+    ref = p * torch.sigmoid(p) * product(w[1], s[1]) if glu else p
+    allowed = ref.abs() * (R.B + (24 + 6 * p.abs()) * R.U) + 1e-30
+    over = (out - ref).abs() - allowed
+    assert over.max() <= 0, (float(over.max()), int((over > 0).sum()))
+
+
+@pytest.mark.parametrize("T", [1, 16, 33, 64, 65, 200])
+def test_products_longest_sum(T):
+    """The widest sum, every code at the end of its range: 2^31 - 2^14 does not wrap."""
+    from mxfp4_latent_mixture_sigmoid_amd import Int8Linear, abi
+    K, N = abi.LINEAR_MAX_K, 20
+    w = torch.full((N, K), -128, dtype=torch.int8, device="cuda")
+    w[1::2] = 127
+    layer = Int8Linear(w, torch.ones(N, device="cuda"), T_max=T, out_dtype=F32)
+    x = torch.full((T, K), -128, dtype=torch.int8, device="cuda")
+    out = f64(layer.forward(x, torch.ones(T, device="cuda")))
+    assert np.array_equal(out[:, 0::2], np.full((T, N // 2), np.float64(np.float32(128 * 128 * K))))
+    assert np.array_equal(out[:, 1::2], np.full((T, N // 2), np.float64(np.float32(-128 * 127 * K))))
+
+
+@pytest.mark.parametrize("T", [3, 70])
+@pytest.mark.parametrize("glu", [0, 1])
+def test_products_of_a_row_without_scale(T, glu):
+    """A NaN scale marks its own row and no other; a zero scale gives zeros (or the bias)."""
+    g = gen(5)
+    layer, w, s, b = make(50, 300, glu, g, bias=not glu, T_max=T, out_dtype=F32)
+    x, sx = codes_rows(T, 300, g), torch.ones(T, device="cuda")
+    sx[1], sx[2] = float("nan"), 0.0
+    out = layer.forward(x, sx)
+    assert torch.isnan(out[1]).all() and torch.isfinite(out[0]).all() and torch.isfinite(out[2:]).all()
+    R.check(f64(out[2]), np.zeros(50) if glu else b, 0.0, "zero scale")
+
+
+def test_gate_far_out():
+    """Gates whose exponential overflows or vanishes: 0 and the gate itself."""
+    from mxfp4_latent_mixture_sigmoid_amd import Int8Linear
+    w = torch.tensor([[100], [-100]], dtype=torch.int8, device="cuda").repeat(8, 16)
+    one = torch.ones(16, device="cuda")
+    layer = Int8Linear(w, one, up_codes=w.abs(), up_scales=one, T_max=1, out_dtype=F32)
+    out = layer.forward(torch.ones(1, 16, dtype=torch.int8, device="cuda"), one[:1])[0]
+    assert (out[0::2] == 1600.0 * 1600.0).all() and (out[1::2] == 0).all()
+
+
+def test_outputs_past_32_bit_offsets():
+    """More than 2^31 outputs and code rows: the last rows and those around the boundary."""
+    from mxfp4_latent_mixture_sigmoid_amd import dequantise, quantise, rms_norm
+    N, K, T = 32768, 16, 66000
+    g = gen(9)
+    layer, w, s, _ = make(N, K, 0, g, T_max=T)
+    x, sx = codes_rows(T, K, g), (0.5 + torch.rand(T, generator=g)).cuda()
+    out = layer.forward(x, sx)
+    pick = [0, 65535, 65536, 65537, T - 1]
+    ref, err = reference(x[pick].cpu().numpy(), f64(sx[pick]), w, s, None, True)
+    R.check(f64(out[pick]), ref, err, "out")
+    codes, scales = quantise(out)
+    y = f64(out[pick])
+    R.check_codes(codes[pick].cpu().numpy(), f64(scales[pick]), y, 0.0, "codes")
+    back = f64(dequantise(codes, scales)[pick])
+    v = f64(codes[pick]) * f64(scales[pick])[:, None]
+    R.check(back, v, np.abs(v) * (R.B + R.U) + 2.0 ** -133, "values")
+    del codes, scales
+    total = rms_norm(out, delta=out, sum=out).out
+    s2, y2 = R.norm(2 * y, None, None, float(np.float32(1e-6)))
+    R.check(f64(out[pick]), s2, np.abs(s2) * R.B, "sum")
+    R.check(f64(total[pick]), y2, np.abs(y2) * (R.B + R.NORM_REL), "norm")
+
+
+def block(H, I, T_max, g):
+    from mxfp4_latent_mixture_sigmoid_amd import Int8FeedForward
+    mat = lambda n, k: (torch.randint(-127, 128, (n, k), generator=g, dtype=torch.int8).cuda(),      # noqa: E731
+                        ((0.5 + torch.rand(n, generator=g)) / (73 * k ** 0.5)).cuda())
+    m = (mat(I, H), mat(I, H), mat(H, I))
+    nw = (1 + 0.1 * torch.randn(H, generator=g)).bfloat16().cuda()
+    return Int8FeedForward(nw, *m, T_max=T_max), nw, m
+
+
+@pytest.mark.parametrize("T", [1, 5, 64, 130])
+def test_block(T):
+    """norm -> gated product -> quantisation -> down product, each step against the plain form of the
+    step's own inputs (codes may differ by one where a value lies between two)."""
+    from mxfp4_latent_mixture_sigmoid_amd import quantise, rms_norm
+    H, I, g = 384, 640, gen(T)
+    ff, nw, (gate, up, down) = block(H, I, T, g)
+    x, d = rows(T, H, BF16, g), rows(T, H, BF16, g)
+    y, total = ff.forward(x, delta=d)
+    r = rms_norm(x, nw, ff.eps, delta=d, sum=True, out=False, codes=True)
+    assert torch.equal(total, r.sum)
+    num = lambda p: (p[0].cpu().numpy(), f64(p[1]))                                                   # noqa: E731
+    h = ff.gated.forward(r.codes, r.scales)
+    ref, err = reference(r.codes.cpu().numpy(), f64(r.scales), [num(gate)[0], num(up)[0]], [num(gate)[1], num(up)[1]],
+                         None, True)
+    R.check(f64(h), ref, err, "h")
+    q, s = quantise(h)
+    ref, err = reference(q.cpu().numpy(), f64(s), [num(down)[0]], [num(down)[1]], None, True)
+    R.check(f64(y), ref, err, "y")
+    assert torch.equal(ff.forward(total)[0], ff.forward(total)[0])
+
+
+@pytest.mark.parametrize("T", [2, 64, 150])
+def test_block_on_another_stream(T):
+    H, I, g = 512, 768, gen(T)
+    ff, _, _ = block(H, I, T, g)
+    x, d = rows(T, H, BF16, g), rows(T, H, BF16, g)
+    want, _ = ff.forward(x, delta=d)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got, _ = ff.forward(x, delta=d, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T", [1, 40, 200])
+def test_block_in_a_graph(T):
+    """One captured block, replayed on new inputs with eager work and synchronisations between."""
+    H, I, g = 512, 768, gen(T)
+    ff, _, _ = block(H, I, T, g)
+    x, d = rows(T, H, BF16, g), rows(T, H, BF16, g)
+    ff.forward(x, delta=d)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, total = ff.forward(x, delta=d)
+    for k in range(4):
+        x.copy_(rows(T, H, BF16, g))
+        graph.replay()
+        if k % 2:
+            torch.cuda.synchronize()
+        got, got_total = y.clone(), total.clone()
+        want, want_total = ff.forward(x, delta=d)
+        assert torch.equal(got, want) and torch.equal(got_total, want_total), k
+
+
+def test_calls_repeat_bit_for_bit_and_interleave():
+    """Layers of different sizes called in turn on one stream, every result as on its own."""
+    g = gen(77)
+    made = []
+    for T, N, K in [(64, 640, 2048), (1, 320, 4096), (300, 500, 600), (17, 1000, 1536)]:
+        layer, *_ = make(N, K, 0, g, T_max=T)
+        made.append((layer, codes_rows(T, K, g), torch.ones(T, device="cuda")))
+    alone = []
+    for layer, x, sx in made:
+        alone.append(layer.forward(x, sx))
+        torch.cuda.synchronize()
+    for _ in range(3):
+        again = [layer.forward(x, sx) for layer, x, sx in made]
+        for a, b in zip(again, alone):
+            assert torch.equal(a, b)
+
+
+def test_smaller_calls_of_a_larger_layer():
+    """Every T up to T_max in one workspace, some after larger calls left their data in it."""
+    g = gen(3)
+    T, N, K = 150, 200, 900
+    layer, w, s, _ = make(N, K, 0, g, T_max=T)
+    x, sx = codes_rows(T, K, g), (0.5 + torch.rand(T, generator=g)).cuda()
+    ref, err = reference(x.cpu().numpy(), f64(sx), w, s, None, True)
+    for t in (150, 1, 64, 65, 16, 17, 149, 33):
+        R.check(f64(layer.forward(x[:t], sx[:t])), ref[:t], err[:t], f"T={t}")
+
+
+def test_python_refusals():
+    from mxfp4_latent_mixture_sigmoid_amd import Int8Linear, dequantise, quantise, rms_norm
+    x = torch.zeros(4, 32, dtype=BF16, device="cuda")
+    q = torch.zeros(4, 32, dtype=torch.int8, device="cuda")
+    s = torch.ones(4, device="cuda")
+    bad = [lambda: rms_norm(x.half()), lambda: rms_norm(x.t()), lambda: rms_norm(x.cpu()), lambda: rms_norm(x[0]),
+           lambda: rms_norm(x, weight=torch.ones(31, dtype=BF16, device="cuda")), lambda: rms_norm(x, delta=x[:3]),
+           lambda: rms_norm(x, weight=torch.ones(32, device="cuda")), lambda: rms_norm(x, scales=s),
+           lambda: rms_norm(x, out=x.float()), lambda: quantise(q), lambda: dequantise(x, s),
+           lambda: dequantise(q, s[:3]), lambda: dequantise(q, s.double()),
+           lambda: Int8Linear(x, s), lambda: Int8Linear(q, s[:3]), lambda: Int8Linear(q, s, up_codes=q),
+           lambda: Int8Linear(q, s, out_dtype=torch.float16), lambda: Int8Linear(q, s, bias=s, up_codes=q, up_scales=s)]
+    layer = Int8Linear(q, s, T_max=4)
+    bad += [lambda: layer.forward(q[:, :31], s), lambda: layer.forward(torch.cat([q, q]), torch.cat([s, s])),
+            lambda: layer.forward(q, s[:2]), lambda: layer.forward(x, s),
+            lambda: layer.forward(q, s, out=torch.empty(4, 5, dtype=BF16, device="cuda"))]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"case {i} was accepted")
+    layer.close()
+    with pytest.raises(RuntimeError):
+        layer.forward(q, s)
