@@ -261,11 +261,12 @@ def linear_query(cfg: LinearConfig, T_max: int):
     return pb.value, wb.value
 
 
-def linear_create(cfg: LinearConfig, w, scales, w_up, scales_up, bias, packed, stream=None) -> c_vp:
+def linear_create(cfg: LinearConfig, w, scales, w_up, scales_up, bias, packed, stream: int) -> c_vp:
+    """`stream`: the raw stream handle."""
     lw = LinearWeights(ptr(w), ptr(scales), ptr(w_up), ptr(scales_up), ptr(bias))
     h = c_vp()
     check(lib().moe_linear_create(ctypes.byref(cfg), ctypes.byref(lw), ptr(packed), packed.numel(),
-                                  stream_handle(stream), ctypes.byref(h)), "moe_linear_create")
+                                  c_vp(stream), ctypes.byref(h)), "moe_linear_create")
     return h
 
 

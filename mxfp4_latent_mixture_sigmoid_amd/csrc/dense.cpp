@@ -61,8 +61,8 @@ int64_t workspace_bytes_for(const moe_linear_config *c, int64_t T) { return alig
 
 bool linear_fits(const moe_linear_config *c, int64_t T)
 {
-    // the smallest tile is 64 x 64; restaging takes one thread per 16 codes
-    const int64_t tiles = ((T + 63) / 64) * ((i8_row_blocks(c->n, c->glu) + 3) / 4);
+    // the smallest tile of more than 64 tokens is 64 x 16; restaging takes one thread per 16 codes
+    const int64_t tiles = ((T + 63) / 64) * i8_row_blocks(c->n, c->glu);
     return tiles + 8 <= INT32_MAX && rows_fit(T, i8_stages(c->k) * I8_STAGE);
 }
 

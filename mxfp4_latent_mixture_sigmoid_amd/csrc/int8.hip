@@ -24,11 +24,12 @@ typedef __attribute__((address_space(3))) void *lds_ptr;
 
 // Direct global -> LDS load of 16 bytes per lane: lane l's from byte `off` of the window [base, base +
 // bytes) -- zeros when it lies outside -- to byte 16 l of `dst` (both wave-uniform but `off`).
+template <int CPOL = 0>
 __device__ inline void load_lds(const void *base, int bytes, int off, u32x4_t *dst)
 {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, bytes, 0x00020000), (lds_ptr)dst, 16, off, 0,
-        0, 0);
+        0, CPOL);
 }
 
 // Where chunk c (16 codes) of row r of a staged activation tile (rows of I8_STAGE bytes) lies: the
@@ -76,62 +77,52 @@ __device__ inline void store4(const I8Args &g, int r, int n, const float *v)
     }
 }
 
-// Epilogue of WMF x WNF fragments whose first row is m0 and first row block of w nb0. The weights are
-// the first operand, so lane (q = l / 16, c = l % 16) holds token row c and packed columns 4 q .. +3.
-template <int WMF, int WNF>
-__device__ inline void epilogue(const I8Args &g, const acc_t (*acc)[WNF], int m0, int nb0)
+// Outputs of one fragment of row block nb (a gate block with its up block's sums in `up` when glu), token
+// row r. The weights are the first matrix operand, so lane l holds row l % 16 and the packed
+// columns 4 (l / 16) .. +3.
+__device__ inline void emit(const I8Args &g, int r, float sx, int nb, acc_t sum, acc_t up)
 {
-    const int lane = threadIdx.x & (WAVE - 1), c = lane & 15, q = lane >> 4;
-    const int step = g.glu ? 2 : 1;
+    const int q = (threadIdx.x & (WAVE - 1)) >> 4;
+    const int n = (g.glu ? nb / 2 : nb) * 16 + 4 * q;
+    if (n >= g.N)
+        return;
+    const f32x4_t sw = *reinterpret_cast<const f32x4_t *>(g.sw + nb * 16 + 4 * q);
+    float v[4];
 #pragma unroll
-    for (int f = 0; f < WMF; f++) {
-        const int r = m0 + f * 16 + c;
-        if (r >= g.T)
-            continue;
-        const float sx = g.sx[r];
+    for (int i = 0; i < 4; i++)
+        v[i] = (float)sum[i] * sx * sw[i];
+    if (g.glu) {
+        const f32x4_t su = *reinterpret_cast<const f32x4_t *>(g.sw + nb * 16 + 16 + 4 * q);
 #pragma unroll
-        for (int j = 0; j < WNF; j++) {
-            const int nb = nb0 + j;
-            if (nb >= g.nblk || (g.glu && j % 2))
-                continue;
-            const int n = nb / step * 16 + 4 * q;
-            const f32x4_t sw = *reinterpret_cast<const f32x4_t *>(g.sw + nb * 16 + 4 * q);
-            float v[4];
+        for (int i = 0; i < 4; i++)
+            v[i] = silu_f32(v[i]) * ((float)up[i] * sx * su[i]);
+    } else if (g.bias) {
+        const f32x4_t b = *reinterpret_cast<const f32x4_t *>(g.bias + n);
 #pragma unroll
-            for (int i = 0; i < 4; i++)
-                v[i] = (float)acc[f][j][i] * sx * sw[i];
-            if (g.glu) {
-                if constexpr (WNF % 2 == 0) {
-                    const f32x4_t su = *reinterpret_cast<const f32x4_t *>(g.sw + nb * 16 + 16 + 4 * q);
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        v[i] = silu_f32(v[i]) * ((float)acc[f][j + (j + 1 < WNF)][i] * sx * su[i]);
-                }
-            } else if (g.bias) {
-                const f32x4_t b = *reinterpret_cast<const f32x4_t *>(g.bias + n);
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    v[i] += b[i];
-            }
-            if (n < g.N)
-                store4(g, r, n, v);
-        }
+        for (int i = 0; i < 4; i++)
+            v[i] += b[i];
     }
+    store4(g, r, n, v);
 }
 
-// Tiles of BM tokens x BN packed columns, NWM x NWN waves. Both operands pass through LDS in NBUF stages
-// of 128 codes, filled by direct global -> LDS loads: one instruction fills 1 KiB, of the activations 8
-// rows x 128 bytes (whole lines), of the weights one packed block. Rows past T and stages past K lie
-// outside the loads' windows and read as zeros without touching memory.
-template <int BM, int BN, int NWM, int NWN, int NBUF>
-__global__ __launch_bounds__(WAVE *NWM *NWN) void tile_kernel(const I8Args g, int gx, int gy)
+// Tiles of BM tokens x BN packed columns by KG groups of NWM x NWN waves; group k takes every KG-th stage of
+// 128 codes, and the groups' sums are added through LDS at the end. Both operands pass through LDS in
+// NBUF buffers of KG stages, filled by direct global -> LDS loads: one instruction fills 1 KiB, of the
+// activations 8 rows x 128 bytes (whole lines), of the weights one packed block. Rows past T and stages
+// past K lie outside the loads' windows and read as zeros without touching memory. ONCE: there is
+// one row tile, so weights are read once, and are not to displace the activations in the caches.
+template <int BM, int BN, int NWM, int NWN, int KG, int NBUF, bool ONCE>
+__global__ __launch_bounds__(WAVE *NWM *NWN *KG) void tile_kernel(const I8Args g, int gx, int gy)
 {
     constexpr int NW = NWM * NWN, WMF = BM / NWM / 16, WNF = BN / NWN / 16;
     constexpr int AL = BM / 8 / NW, BL = BN / 8 / NW;   // loads per wave and stage
-    static_assert(AL * NW * 8 == BM && BL * NW * 8 == BN && WNF % 2 == 0, "tile");
-    __shared__ u32x4_t lds[NBUF][(BM + BN) * 8];
+    constexpr int STAGE = (BM + BN) * 8;                // 16-byte slots
+    static_assert(AL * NW * 8 == BM && BL * NW * 8 == BN, "tile");
+    static_assert(KG == 1 || NBUF * STAGE >= NW * WMF * WNF * WAVE, "room for the groups' sums");
+    __shared__ u32x4_t lds[NBUF * KG * STAGE];
     const int lane = threadIdx.x & (WAVE - 1);
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int wv = wave % NW, kg = wave / NW;
     int bx, by;
     if (!tile_item(gx, gy, bx, by))
         return;
@@ -144,21 +135,22 @@ __global__ __launch_bounds__(WAVE *NWM *NWN) void tile_kernel(const I8Args g, in
     int aoff[AL];
 #pragma unroll
     for (int i = 0; i < AL; i++) {
-        const int j = wv * AL + i, row = j * 8 + (lane >> 3);
+        const int row = (wv * AL + i) * 8 + (lane >> 3);
         aoff[i] = row * (int)g.ldx + ((lane & 7) ^ swizzle(row)) * 16;
     }
-    auto issue = [&](int s) {
-        u32x4_t *buf = lds[s % NBUF];
-        const int k = s * I8_STAGE;
+    auto issue = [&](int it) {
+        u32x4_t *buf = &lds[(it % NBUF * KG + kg) * STAGE];
+        const int s = it * KG + kg, k = s * I8_STAGE;
         const bool in = s < nst;
         const int8_t *xs = xt + (in ? k : 0);
         const uint8_t *ws = wt + (in ? (int64_t)s * g.nblk * I8_STAGE_BYTES : 0);
 #pragma unroll
+        for (int i = 0; i < BL; i++)
+            load_lds<ONCE ? CPOL_NT : 0>(ws, in ? wbytes : 0, (wv * BL + i) * I8_BLOCK_BYTES + lane * 16,
+                                         &buf[BM * 8 + (wv * BL + i) * WAVE]);
+#pragma unroll
         for (int i = 0; i < AL; i++)
             load_lds(xs, in ? xbytes - k : 0, aoff[i], &buf[(wv * AL + i) * WAVE]);
-#pragma unroll
-        for (int i = 0; i < BL; i++)
-            load_lds(ws, in ? wbytes : 0, (wv * BL + i) * I8_BLOCK_BYTES + lane * 16, &buf[BM * 8 + (wv * BL + i) * WAVE]);
     };
     acc_t acc[WMF][WNF];
 #pragma unroll
@@ -167,18 +159,19 @@ __global__ __launch_bounds__(WAVE *NWM *NWN) void tile_kernel(const I8Args g, in
         for (int j = 0; j < WNF; j++)
             acc[f][j] = acc_t{0, 0, 0, 0};
     const int fa = (wv / NWN) * WMF, fb = (wv % NWN) * WNF;
+    const int nit = (nst + KG - 1) / KG;
 #pragma unroll
-    for (int s = 0; s < NBUF - 1; s++)
-        issue(s);
-    for (int s = 0; s < nst; s++) {
-        // This wave's part of stage s has landed and its reads of stage s - 1 are done; past the barrier,
-        // every wave's, so that the buffer of stage s - 1 can be filled again.
+    for (int it = 0; it < NBUF - 1; it++)
+        issue(it);
+    for (int it = 0; it < nit; it++) {
+        // This wave's part of these stages has landed and its reads of the last ones are done; past the
+        // barrier, every wave's, so that the last ones' buffer can be filled again.
         __builtin_amdgcn_s_waitcnt(vmcnt_lgkm_imm((NBUF - 2) * (AL + BL)));
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        issue(s + NBUF - 1);
-        const u32x4_t *buf = lds[s % NBUF];
+        issue(it + NBUF - 1);
+        const u32x4_t *buf = &lds[(it % NBUF * KG + kg) * STAGE];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
             u32x4_t a[WMF], b[WNF];
@@ -197,8 +190,44 @@ __global__ __launch_bounds__(WAVE *NWM *NWN) void tile_kernel(const I8Args g, in
         }
         asm volatile("" ::: "memory");
     }
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));   // nothing may land in LDS after the workgroup ends
-    epilogue<WMF, WNF>(g, acc, m0 + fa * 16, nb0 + fb);
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm_imm(0));   // nothing may land in LDS any more
+    if constexpr (KG > 1) {
+        __syncthreads();   // every wave is past its last stage: LDS holds the groups' sums from here
+        u32x4_t *mine = &lds[((kg * NW + wv) * WMF * WNF) * WAVE + lane];
+#pragma unroll
+        for (int f = 0; f < WMF; f++)
+#pragma unroll
+            for (int j = 0; j < WNF; j++)
+                mine[(f * WNF + j) * WAVE] = __builtin_bit_cast(u32x4_t, acc[f][j]);
+        __syncthreads();
+    }
+    // Group k finishes every KG-th fragment (or pair of a gate and an up fragment).
+    auto total = [&](int f, int j) {
+        if constexpr (KG == 1) {
+            return acc[f][j];
+        } else {
+            acc_t sum{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < KG; k++)
+                sum += __builtin_bit_cast(acc_t, lds[((k * NW + wv) * WMF * WNF + f * WNF + j) * WAVE + lane]);
+            return sum;
+        }
+    };
+#pragma unroll
+    for (int f = 0; f < WMF; f++) {
+        const int r = m0 + (fa + f) * 16 + (lane & 15);
+#pragma unroll
+        for (int j = 0; j < WNF; j++) {
+            const int nb = nb0 + fb + j, unit = g.glu ? (f * WNF + j) / 2 : f * WNF + j;
+            if (nb >= g.nblk || (g.glu && j % 2) || (KG > 1 && unit % KG != kg) || r >= g.T)
+                continue;
+            acc_t up{0, 0, 0, 0};
+            if constexpr (WNF % 2 == 0)   // launched with glu
+                if (g.glu)
+                    up = total(f, j | 1);
+            emit(g, r, g.sx[r], nb, total(f, j), up);
+        }
+    }
 }
 
 // Rows of K codes at any alignment -> rows of `width` codes (a multiple of 16), zero past K.
@@ -252,25 +281,60 @@ __global__ __launch_bounds__(256) void pack_vectors_kernel(const float *s, const
         bias_out[i] = n < N ? bias[n] : 0.f;
 }
 
-template <int BM, int BN, int NWM, int NWN, int NBUF>
+template <int BM, int BN, int NWM, int NWN, int KG, int NBUF>
 hipError_t launch_tile(const I8Args &g, hipStream_t st)
 {
     const int gx = (g.nblk * 16 + BN - 1) / BN, gy = (g.T + BM - 1) / BM;
-    const unsigned grid = (unsigned)((gx * gy + XCDS - 1) / XCDS * XCDS);
-    hipLaunchKernelGGL((tile_kernel<BM, BN, NWM, NWN, NBUF>), dim3(grid), dim3(WAVE * NWM * NWN), 0, st, g, gx, gy);
+    const dim3 grid((unsigned)((gx * gy + XCDS - 1) / XCDS * XCDS)), threads(WAVE * NWM * NWN * KG);
+    if (gy == 1)
+        hipLaunchKernelGGL((tile_kernel<BM, BN, NWM, NWN, KG, NBUF, true>), grid, threads, 0, st, g, gx, gy);
+    else
+        hipLaunchKernelGGL((tile_kernel<BM, BN, NWM, NWN, KG, NBUF, false>), grid, threads, 0, st, g, gx, gy);
     return hipGetLastError();
 }
 
 } // namespace
 
+// Tiles by the number of workgroups: the widest that still makes FILL of them, three quarters of the
+// card's 256 CUs, else the narrowest (16 columns; 32 when a gate and an up block have to be together),
+// with the K axis over more groups of waves the narrower the tile. Measured, microseconds (weights not in
+// any cache), chosen against the next wider or narrower tile: 1 x 3584 x 7168: 16 columns 7.4, 32 8.1;
+// 16 x 7168 x 4352: 32 8.4, 16 11.7, 64 9.8; 16 x 14336 x 3584: 64 10.7, 32 12.8, 128 14.3; 64 x 7168 x
+// 4352: 32 11.2, 64 13.1, 16 16.6; 64 x (2 x 14336) x 7168: 128 38.3, 64 42.6, 256 47.
 hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
 {
+    constexpr int64_t FILL = 192;
+    auto fills = [&](int bm, int bn) {
+        return (int64_t)((g.T + bm - 1) / bm) * ((g.nblk * 16 + bn - 1) / bn) >= FILL;
+    };
+    if (g.T <= 16) {
+        if (fills(16, 64))
+            return launch_tile<16, 64, 1, 2, 2, 4>(g, st);
+        if (fills(16, 32) || g.glu)
+            return launch_tile<16, 32, 1, 1, 4, 4>(g, st);
+        return launch_tile<16, 16, 1, 1, 8, 3>(g, st);
+    }
+    if (g.T <= 32) {
+        if (fills(32, 128))
+            return launch_tile<32, 128, 1, 4, 1, 4>(g, st);
+        if (fills(32, 64))
+            return launch_tile<32, 64, 1, 2, 2, 4>(g, st);
+        if (fills(32, 32) || g.glu)
+            return launch_tile<32, 32, 1, 1, 4, 3>(g, st);
+        return launch_tile<32, 16, 1, 1, 8, 3>(g, st);
+    }
     const int64_t area = (int64_t)g.T * g.nblk * 16;
     if (area >= (int64_t)256 * 256 * 256)
-        return launch_tile<256, 256, 2, 4, 2>(g, st);
+        return launch_tile<256, 256, 2, 4, 1, 2>(g, st);
     if (area >= (int64_t)128 * 128 * 256)
-        return launch_tile<128, 128, 2, 2, 2>(g, st);
-    return launch_tile<64, 64, 2, 2, 4>(g, st);
+        return launch_tile<128, 128, 2, 2, 1, 2>(g, st);
+    if (fills(64, 128))
+        return launch_tile<64, 128, 2, 4, 1, 3>(g, st);
+    if (fills(64, 64))
+        return launch_tile<64, 64, 2, 2, 2, 3>(g, st);
+    if (fills(64, 32) || g.glu)
+        return launch_tile<64, 32, 2, 1, 2, 3>(g, st);
+    return launch_tile<64, 16, 2, 1, 4, 3>(g, st);
 }
 
 hipError_t launch_i8_restage(const int8_t *x, int64_t ldx, int T, int K, int8_t *dst, hipStream_t st)

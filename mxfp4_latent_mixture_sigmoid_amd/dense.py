@@ -15,6 +15,7 @@ import torch
 from . import abi
 
 _TYPES = {torch.bfloat16: abi.TYPE_BF16, torch.float32: abi.TYPE_F32}
+_BF16, _INT8 = (torch.bfloat16,), (torch.int8,)
 _byref = ctypes.byref
 
 
@@ -26,19 +27,26 @@ class Normed(NamedTuple):
     sum: torch.Tensor | None
 
 
-def _rows(name, t, dtypes, device=None, shape=None):
-    """Row stride of a [T, width] tensor, after checking it."""
+def _bad_rows(name, t, dtypes, device, shape):
+    """Why `t` is not the matrix that _rows wants."""
     if t.dtype not in dtypes:
-        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+        return f"{name}: {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}"
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: expected two dimensions with contiguous rows, got shape {tuple(t.shape)}, "
-                         f"strides {t.stride()}")
+        return (f"{name}: expected two dimensions with contiguous rows, got shape {tuple(t.shape)}, "
+                f"strides {t.stride()}")
     if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name}: on {t.device}, expected {device if device is not None else 'a GPU'}")
-    # the stride of a single row means nothing to the caller (torch reports any value there)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+        return f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}"
+    return f"{name}: on {t.device}, expected {device if device is not None else 'a GPU'}"
+
+
+def _rows(name, t, dtypes, device=None, shape=None):
+    """Row stride of a [T, width] tensor on the GPU, after checking it."""
+    strides, sizes = t.stride(), t.shape
+    if (t.dtype not in dtypes or len(sizes) != 2 or (strides[1] != 1 and sizes[1] > 1)
+            or (shape is not None and sizes != shape) or (not t.is_cuda if device is None else t.device != device)):
+        raise ValueError(_bad_rows(name, t, dtypes, device, shape))
+    # the stride of a single row means nothing (torch reports any value there)
+    return strides[0] if sizes[0] > 1 else sizes[1]
 
 
 def _vector(name, t, n, dtype, device):
@@ -47,33 +55,31 @@ def _vector(name, t, n, dtype, device):
                          f"on {t.device}")
 
 
-class _on:
-    """Makes `device`, and `stream` when given, current around the allocation of outputs and the launch,
-    and lets the allocator know that `stream` uses tensors of other streams."""
-
-    def __init__(self, device, stream, *tensors):
-        self.device, self.stream, self.tensors = device, stream, tensors
-
-    def __enter__(self):
-        self.guard = torch.cuda.stream(self.stream) if self.stream is not None else torch.cuda.device(self.device)
-        self.guard.__enter__()
-        return abi.stream_handle()
-
-    def __exit__(self, *exc):
-        self.guard.__exit__(*exc)
-        if self.stream is not None:
-            for t in self.tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
+def _call(device, stream, tensors, f, *args):
+    """f(*args, stream handle) with `device` current, on `stream` when one is given: outputs are then
+    allocated for it, and the allocator learns that it uses tensors of other streams. On the current
+    device and stream it is the bare call, whose latency counts for single tokens."""
+    if stream is None:
+        index = device.index
+        if index == torch.cuda.current_device():
+            return f(*args, torch._C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(device):
+            return f(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.stream(stream):
+        got = f(*args, stream.cuda_stream)
+    for t in tensors:
+        if torch.is_tensor(t):
+            t.record_stream(stream)
+    return got
 
 
-def _output(name, want, T, width, dtype, device):
+def _output(name, want, x, T, width, dtype):
     """(tensor, row stride) of an output asked for by True, given as a tensor, or not wanted."""
+    if want is True:
+        return torch.empty((T, width), dtype=dtype, device=x.device), width
     if want is None or want is False:
         return None, 0
-    if want is True:
-        return torch.empty(T, width, dtype=dtype, device=device), width
-    return want, _rows(name, want, (dtype,), device, (T, width))
+    return want, _rows(name, want, (dtype,), x.device, (T, width))
 
 
 def rms_norm(x, weight=None, eps=1e-6, delta=None, sum=None, out=True, codes=False, scales=None, stream=None) -> Normed:
@@ -83,56 +89,65 @@ def rms_norm(x, weight=None, eps=1e-6, delta=None, sum=None, out=True, codes=Fal
     BF16) and ``codes`` (y as int8, with ``scales`` = max|y| / 127 per row) is False, True (allocated
     here) or a tensor to write into; ``sum`` may be x itself. A row of zeros has scale 0; a row with a
     NaN or an infinity has scale NaN and codes 0."""
+    return _call(x.device, stream, (x, weight, delta, sum, out, codes, scales), _rms_norm, x, weight, eps, delta, sum, out,
+                 codes, scales)
+
+
+def _rms_norm(x, weight, eps, delta, sum, out, codes, scales, stream):
     ldx = _rows("x", x, _TYPES)
     T, H = x.shape
-    dev = x.device
-    ldd = _rows("delta", delta, (torch.bfloat16,), dev, x.shape) if delta is not None else 0
+    dtype, ldd = x.dtype, 0
+    if delta is not None:
+        ldd = _rows("delta", delta, _BF16, x.device, x.shape)
     if weight is not None:
-        _vector("weight", weight, H, torch.bfloat16, dev)
-    with _on(dev, stream, x, delta, weight, *(t for t in (sum, out, codes, scales) if torch.is_tensor(t))) as st:
-        s, lds = _output("sum", sum, T, H, x.dtype, dev)
-        o, ldo = _output("out", out, T, H, torch.bfloat16, dev)
-        q, ldc = _output("codes", codes, T, H, torch.int8, dev)
+        _vector("weight", weight, H, torch.bfloat16, x.device)
+    s, lds = _output("sum", sum, x, T, H, dtype)
+    o, ldo = _output("out", out, x, T, H, torch.bfloat16)
+    q, ldc = _output("codes", codes, x, T, H, torch.int8)
+    if scales is not None:
         if q is None:
-            if scales is not None:
-                raise ValueError("scales given without codes")
-        elif scales is None:
-            scales = torch.empty(T, dtype=torch.float32, device=dev)
-        else:
-            _vector("scales", scales, T, torch.float32, dev)
-        a = abi.NormArgs(abi.ptr(x), abi.ptr(delta), abi.ptr(weight), abi.ptr(s), abi.ptr(o), abi.ptr(q),
-                         abi.ptr(scales), ldx, ldd, lds, ldo, ldc, T, H, _TYPES[x.dtype], eps)
-        abi.check(abi.lib().moe_norm(_byref(a), st), "moe_norm")
+            raise ValueError("scales given without codes")
+        _vector("scales", scales, T, torch.float32, x.device)
+    elif q is not None:
+        scales = torch.empty(T, dtype=torch.float32, device=x.device)
+    ptr = abi.ptr
+    a = abi.NormArgs(x.data_ptr(), ptr(delta), ptr(weight), ptr(s), ptr(o), ptr(q), ptr(scales), ldx, ldd, lds, ldo, ldc,
+                     T, H, _TYPES[dtype], eps)
+    abi.check(abi.lib().moe_norm(_byref(a), stream), "moe_norm")
     return Normed(o, q, scales, s)
 
 
 def quantise(x, codes=None, scales=None, stream=None):
     """Rows of x ([T, K] BF16 or FP32) as int8 codes with a scale each: scale = max|x| / 127,
     codes = x / scale rounded to nearest even. Returns (codes, scales), into the given tensors if any."""
+    return _call(x.device, stream, (x, codes, scales), _quantise, x, codes, scales)
+
+
+def _quantise(x, codes, scales, stream):
     ldx = _rows("x", x, _TYPES)
     T, K = x.shape
-    dev = x.device
-    with _on(dev, stream, x, codes, scales) as st:
-        q, ldc = _output("codes", True if codes is None else codes, T, K, torch.int8, dev)
-        if scales is None:
-            scales = torch.empty(T, dtype=torch.float32, device=dev)
-        else:
-            _vector("scales", scales, T, torch.float32, dev)
-        abi.check(abi.lib().moe_quantise(abi.ptr(x), _TYPES[x.dtype], ldx, T, K, abi.ptr(q), ldc, abi.ptr(scales), st),
-                  "moe_quantise")
+    q, ldc = _output("codes", True if codes is None else codes, x, T, K, torch.int8)
+    if scales is None:
+        scales = torch.empty(T, dtype=torch.float32, device=x.device)
+    else:
+        _vector("scales", scales, T, torch.float32, x.device)
+    abi.check(abi.lib().moe_quantise(x.data_ptr(), _TYPES[x.dtype], ldx, T, K, q.data_ptr(), ldc, scales.data_ptr(),
+                                     stream), "moe_quantise")
     return q, scales
 
 
 def dequantise(codes, scales, out=None, stream=None):
     """The values that codes stand for, bf16(codes * scales[:, None])."""
-    ldc = _rows("codes", codes, (torch.int8,))
+    return _call(codes.device, stream, (codes, scales, out), _dequantise, codes, scales, out)
+
+
+def _dequantise(codes, scales, out, stream):
+    ldc = _rows("codes", codes, _INT8)
     T, K = codes.shape
-    dev = codes.device
-    _vector("scales", scales, T, torch.float32, dev)
-    with _on(dev, stream, codes, scales, out) as st:
-        o, ldo = _output("out", True if out is None else out, T, K, torch.bfloat16, dev)
-        abi.check(abi.lib().moe_dequantise(abi.ptr(codes), ldc, abi.ptr(scales), T, K, abi.ptr(o), ldo, st),
-                  "moe_dequantise")
+    _vector("scales", scales, T, torch.float32, codes.device)
+    o, ldo = _output("out", True if out is None else out, codes, T, K, torch.bfloat16)
+    abi.check(abi.lib().moe_dequantise(codes.data_ptr(), ldc, scales.data_ptr(), T, K, o.data_ptr(), ldo, stream),
+              "moe_dequantise")
     return o
 
 
@@ -153,36 +168,41 @@ class Int8Linear:
             raise ValueError("up_codes and up_scales go together")
         if up_codes is not None and bias is not None:
             raise ValueError("the gated product takes no bias")
-        _rows("codes", codes, (torch.int8,))
+        _rows("codes", codes, _INT8)
         self.N, self.K = codes.shape
         self.device, self.T_max, self.out_dtype = codes.device, T_max, out_dtype
         _vector("scales", scales, self.N, torch.float32, self.device)
         if up_codes is not None:
-            _rows("up_codes", up_codes, (torch.int8,), self.device, codes.shape)
+            _rows("up_codes", up_codes, _INT8, self.device, codes.shape)
             _vector("up_scales", up_scales, self.N, torch.float32, self.device)
         if bias is not None:
             _vector("bias", bias, self.N, torch.float32, self.device)
         self.cfg = abi.LinearConfig(self.N, self.K, int(up_codes is not None), _TYPES[out_dtype])
-        packed_bytes, ws_bytes = abi.linear_query(self.cfg, T_max)
-        with _on(self.device, stream, codes, scales, bias, up_codes, up_scales):
-            codes = codes.contiguous()
-            up_codes = up_codes.contiguous() if up_codes is not None else None
-            self.packed = torch.empty(packed_bytes, dtype=torch.uint8, device=self.device)
-            self.workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=self.device)
-            self.handle = abi.linear_create(self.cfg, codes, scales, up_codes, up_scales, bias, self.packed)
+        _call(self.device, stream, (codes, scales, bias, up_codes, up_scales), self._pack, codes, scales, bias, up_codes,
+              up_scales)
+
+    def _pack(self, codes, scales, bias, up_codes, up_scales, stream):
+        packed_bytes, ws_bytes = abi.linear_query(self.cfg, self.T_max)
+        codes = codes.contiguous()
+        up_codes = up_codes.contiguous() if up_codes is not None else None
+        self.packed = torch.empty(packed_bytes, dtype=torch.uint8, device=self.device)
+        self.workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=self.device)
+        self.handle = abi.linear_create(self.cfg, codes, scales, up_codes, up_scales, bias, self.packed, stream)
+        self._buffers = self.workspace.data_ptr(), self.workspace.numel()
 
     def forward(self, x, scales, out=None, stream=None):
         """The product for codes x [T, K] with FP32 scales [T]; returns out [T, N]."""
-        ldx = _rows("x", x, (torch.int8,), self.device)
-        T = x.shape[0]
-        if x.shape[1] != self.K or T > self.T_max:
+        return _call(self.device, stream, (x, scales, out, self.packed, self.workspace), self._forward, x, scales, out)
+
+    def _forward(self, x, scales, out, stream):
+        ldx = _rows("x", x, _INT8, self.device)
+        T, K = x.shape
+        if K != self.K or T > self.T_max:
             raise ValueError(f"x: shape {tuple(x.shape)}, expected at most {self.T_max} rows of {self.K}")
         _vector("scales", scales, T, torch.float32, self.device)
-        with _on(self.device, stream, x, scales, out, self.packed, self.workspace) as st:
-            o, ldo = _output("out", True if out is None else out, T, self.N, self.out_dtype, self.device)
-            abi.check(abi.lib().moe_linear_forward(self.handle, abi.ptr(x), ldx, abi.ptr(scales), T, abi.ptr(o), ldo,
-                                                   abi.ptr(self.workspace), self.workspace.numel(), st),
-                      "moe_linear_forward")
+        o, ldo = _output("out", True if out is None else out, x, T, self.N, self.out_dtype)
+        abi.check(abi.lib().moe_linear_forward(self.handle, x.data_ptr(), ldx, scales.data_ptr(), T, o.data_ptr(), ldo,
+                                               *self._buffers, stream), "moe_linear_forward")
         return o
 
     def close(self):
