@@ -6,11 +6,14 @@
 // (dense.hpp); activations are read as they are.
 #include "dense.hpp"
 
+#include <type_traits>
+
 namespace mxmoe {
 
 namespace {
 
 typedef int32_t acc_t __attribute__((ext_vector_type(4)));
+constexpr int CUS = 256;
 constexpr int XCDS = 8;      // workgroups are dealt to the XCDs round-robin by linear id
 constexpr int GROUP_M = 4;   // row tiles per group, walked row-fastest
 
@@ -77,6 +80,38 @@ __device__ inline void store4(const I8Args &g, int r, int n, const float *v)
     }
 }
 
+// Sixteen bytes of outputs of token row r from column n on.
+__device__ inline void store16(const I8Args &g, int r, int n, u32x4_t v)
+{
+    if (g.out_type == MOE_TYPE_F32) {
+        float *o = static_cast<float *>(g.out) + r * g.ldo + n;
+        if (n + 4 <= g.N)
+            __builtin_memcpy(o, &v, 16);
+        else
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (n + i < g.N)
+                    o[i] = __uint_as_float(v[i]);
+    } else {
+        uint16_t *o = static_cast<uint16_t *>(g.out) + r * g.ldo + n;
+        if (n + 8 <= g.N)
+            __builtin_memcpy(o, &v, 16);
+        else
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (n + i < g.N)
+                    o[i] = (uint16_t)(v[i / 2] >> (16 * (i % 2)));
+    }
+}
+
+// g / (1 + exp(-g)) on the hardware's exponential and reciprocal, each within a unit in the last place: the
+// exponent's rounding costs |g| 2^-24 relative, far below the output's BF16 (and a few units of FP32).
+// exp overflows to infinity, whose reciprocal is 0.
+__device__ inline float silu(float g)
+{
+    return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * g));
+}
+
 // Outputs of one fragment of row block nb (a gate block with its up block's sums in `up` when glu), token
 // row r. The weights are the first matrix operand, so lane l holds row l % 16 and the packed
 // columns 4 (l / 16) .. +3.
@@ -95,7 +130,7 @@ __device__ inline void emit(const I8Args &g, int r, float sx, int nb, acc_t sum,
         const f32x4_t su = *reinterpret_cast<const f32x4_t *>(g.sw + nb * 16 + 16 + 4 * q);
 #pragma unroll
         for (int i = 0; i < 4; i++)
-            v[i] = silu_f32(v[i]) * ((float)up[i] * sx * su[i]);
+            v[i] = silu(v[i]) * ((float)up[i] * sx * su[i]);
     } else if (g.bias) {
         const f32x4_t b = *reinterpret_cast<const f32x4_t *>(g.bias + n);
 #pragma unroll
@@ -132,6 +167,7 @@ __global__ __launch_bounds__(WAVE *NWM *NWN *KG) void tile_kernel(const I8Args g
     const int xbytes = (min(g.T - m0, BM) - 1) * (int)g.ldx + g.K;
     const uint8_t *wt = g.w + (int64_t)nb0 * I8_STAGE_BYTES;
     const int wbytes = min(g.nblk - nb0, BN / 16) * I8_STAGE_BYTES;
+    const int64_t wstep = (int64_t)g.nblk * I8_STAGE_BYTES;
     int aoff[AL];
 #pragma unroll
     for (int i = 0; i < AL; i++) {
@@ -140,17 +176,16 @@ __global__ __launch_bounds__(WAVE *NWM *NWN *KG) void tile_kernel(const I8Args g
     }
     auto issue = [&](int it) {
         u32x4_t *buf = &lds[(it % NBUF * KG + kg) * STAGE];
-        const int s = it * KG + kg, k = s * I8_STAGE;
-        const bool in = s < nst;
-        const int8_t *xs = xt + (in ? k : 0);
-        const uint8_t *ws = wt + (in ? (int64_t)s * g.nblk * I8_STAGE_BYTES : 0);
+        const int s = it * KG + kg, last = min(s, nst - 1), in = -(int)(s < nst);   // past K: empty windows
+        const int8_t *xs = xt + last * I8_STAGE;
+        const uint8_t *ws = wt + last * wstep;
 #pragma unroll
         for (int i = 0; i < BL; i++)
-            load_lds<ONCE ? CPOL_NT : 0>(ws, in ? wbytes : 0, (wv * BL + i) * I8_BLOCK_BYTES + lane * 16,
+            load_lds<ONCE ? CPOL_NT : 0>(ws, wbytes & in, (wv * BL + i) * I8_BLOCK_BYTES + lane * 16,
                                          &buf[BM * 8 + (wv * BL + i) * WAVE]);
 #pragma unroll
         for (int i = 0; i < AL; i++)
-            load_lds(xs, in ? xbytes - k : 0, aoff[i], &buf[(wv * AL + i) * WAVE]);
+            load_lds(xs, (xbytes - last * I8_STAGE) & in, aoff[i], &buf[(wv * AL + i) * WAVE]);
     };
     acc_t acc[WMF][WNF];
 #pragma unroll
@@ -230,6 +265,202 @@ __global__ __launch_bounds__(WAVE *NWM *NWN *KG) void tile_kernel(const I8Args g
     }
 }
 
+// Many tokens, where the time is the matrix cores': 256 tokens x 256 packed columns by four waves of 128 x
+// 128, one per SIMD. Per 64 codes a wave multiplies for 1024 clocks (64
+// instructions) and reads 16 KiB of operands, so the LDS is busy 512 clocks with all reads and 256
+// with the loads' writes; eight waves of 128 x 64 would read 1.5 times as much and leave the LDS no
+// slack. A wave reads the operands of the next half stage, and issues the loads, between the instructions
+// that multiply the current one. The 160 KiB of LDS hold three 128-code stages of activations (whole
+// lines) and four 64-code halves of weights, loaded three to four halves ahead of their reads.
+// acc += a . b with the sums kept in accumulation registers (left to itself the compiler moves some of the 64
+// sums of a wave between register files around every instruction).
+__device__ inline void mfma_acc(u32x4_t a, u32x4_t b, acc_t &acc)
+{
+    asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+}
+
+// NF: column fragments per wave. With 7 of them a tile has 224 columns (and loads, but does not use, the
+// two row blocks after its own), which can fill the last round of workgroups better.
+template <int NF, bool GLU, bool F32>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void wide_kernel(const I8Args g, int gx, int gy)
+{
+    constexpr int BM = 256, BN = 256, MF = 8;                       // MF x NF fragments of 16 x 16 per wave
+    constexpr int ASLOT = BM * 8, BSLOT = BN * 4, NA = 3, NB = 4;   // 16-byte slots per stage / half; how many
+    constexpr int AL = BM / 8 / 4, BL = BN / 16 / 4;                // loads per wave per stage / half
+    static_assert(AL == 2 * BL, "loads alternate");
+    __shared__ u32x4_t lds[NA * ASLOT + NB * BSLOT];
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    int bx, by;
+    if (!tile_item(gx, gy, bx, by))
+        return;
+    const int m0 = by * BM, nb0 = bx * (2 * NF);
+    const int nst = (int)i8_stages(g.K);
+    const int8_t *xt = g.x + (int64_t)m0 * g.ldx;
+    const int xbytes = (min(g.T - m0, BM) - 1) * (int)g.ldx + g.K;
+    const uint8_t *wt = g.w + (int64_t)nb0 * I8_STAGE_BYTES;
+    const int wbytes = min(g.nblk - nb0, BN / 16) * I8_STAGE_BYTES;
+    const int64_t wstep = (int64_t)g.nblk * I8_STAGE_BYTES;
+    int aoff[AL];
+#pragma unroll
+    for (int i = 0; i < AL; i++) {
+        const int row = (wv * AL + i) * 8 + (lane >> 3);
+        aoff[i] = row * (int)g.ldx + ((lane & 7) ^ swizzle(row)) * 16;
+    }
+    // Load i of this wave's part of stage s (activations) or half hs % 2 of stage hs / 2 (weights).
+    auto load_a = [&](int s, int i) {
+        const int k = min(s, nst - 1) * I8_STAGE, bytes = (xbytes - k) & -(int)(s < nst);
+        load_lds(xt + k, bytes, aoff[i], &lds[s % NA * ASLOT + (wv * AL + i) * WAVE]);
+    };
+    auto load_b = [&](int hs, int i) {
+        const int64_t at = min(hs / 2, nst - 1) * wstep + hs % 2 * I8_BLOCK_BYTES;
+        const int bytes = (wbytes - hs % 2 * I8_BLOCK_BYTES) & -(int)(hs < 2 * nst);
+        load_lds(wt + at, bytes, (wv * BL + i) * I8_STAGE_BYTES + lane * 16,
+                 &lds[NA * ASLOT + hs % NB * BSLOT + (wv * BL + i) * WAVE]);
+    };
+    // The loads issued while half hs multiplies, i = 0..7: the weights of half hs + 4 and one half of those of a stage
+    // of activations, whose slots every wave has left. As many in every half, so that the wait for the next
+    // half's data is always for all but the last two halves' loads.
+    constexpr int PER = AL / 2 + BL;
+    auto load = [&](int hs, int i) {
+        if (i % 2)
+            load_b(hs + 4, i / 2);
+        else
+            load_a((hs + 5) / 2, hs % 2 ? i / 2 : AL / 2 + i / 2);
+    };
+    const int fa = wv / 2 * MF, fb = wv % 2 * NF;   // this wave's first fragments
+    const int r16 = lane & 15, ar = (fa * 16 + r16) * 8, ac = (lane >> 4) ^ swizzle(r16);
+    struct Operands {   // of half a stage
+        u32x4_t a[MF], b[NF];
+    };
+    // Read i of half hs, in the order of use: the first weights, the activations, the other weights.
+    auto read = [&](int hs, int i, Operands &o) {
+        if (i >= 1 && i <= MF)
+            o.a[i - 1] = lds[hs / 2 % NA * ASLOT + ar + (i - 1) * 16 * 8 + (ac ^ hs % 2 * 4)];
+        else
+            o.b[i ? i - MF : 0] = lds[NA * ASLOT + hs % NB * BSLOT + (fb + (i ? i - MF : 0)) * WAVE + lane];
+    };
+    acc_t acc[MF][NF];
+#pragma unroll
+    for (int f = 0; f < MF; f++)
+#pragma unroll
+        for (int j = 0; j < NF; j++)
+            acc[f][j] = acc_t{0, 0, 0, 0};
+    // One half stage: its MF * NF instructions, and among them the reads of the next half into the other
+    // operands and the loads. The order is fixed: left to itself the compiler gathers the reads at
+    // the end, right before the wait for them. Rows of fragments are walked back and forth, so that
+    // consecutive instructions share an operand.
+    auto half = [&](const Operands &now, int hs, Operands &next) {
+#pragma unroll
+        for (int i = 0; i < 2 * NF; i++) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const int j = i / 2, m = i % 2 * 4 + q, f = j % 2 ? MF - 1 - m : m;
+                mfma_acc(now.b[j], now.a[f], acc[f][j]);
+                if (q == 1 && i < MF + NF)
+                    read(hs + 1, i, next);
+                if (q == 2 && i + 2 * NF < MF + NF)
+                    read(hs + 1, i + 2 * NF, next);
+            }
+            if (i % 2)
+                load(hs, i / 2);
+            if (2 * NF < 2 * PER && i == 0)
+                load(hs, PER - 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto meet = [&](auto ahead) {   // all but the last loads have landed and this wave's reads are done; then every wave's
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(vmcnt_lgkm_imm(decltype(ahead)::value));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Stages 0 and 1 and the loads that halves -1, -2 and -3 would have issued.
+#pragma unroll
+    for (int i = 0; i < AL; i++)
+        load_a(0, i);
+#pragma unroll
+    for (int i = 0; i < BL; i++)
+        load_b(0, i);
+#pragma unroll
+    for (int i = 0; i < AL / 2; i++)
+        load_a(1, i);
+#pragma unroll
+    for (int i = 0; i < BL; i++)
+        load_b(1, i);
+#pragma unroll
+    for (int i = 0; i < PER; i++)
+        load(-2, i);
+#pragma unroll
+    for (int i = 0; i < PER; i++)
+        load(-1, i);
+    meet(std::integral_constant<int, 3 * PER>());
+    Operands even, odd;
+#pragma unroll
+    for (int i = 0; i < MF + NF; i++)
+        read(0, i, even);
+    for (int s = 0; s < nst; s++) {
+        meet(std::integral_constant<int, 2 * PER>());   // half 2s + 1 has landed; half 2s is in every wave's registers
+        half(even, 2 * s, odd);
+        meet(std::integral_constant<int, 2 * PER>());
+        half(odd, 2 * s + 1, even);
+    }
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm_imm(0));   // nothing may land in LDS any more
+    __syncthreads();                                 // and every wave is past its reads
+
+    asm volatile("s_nop 15\n\ts_nop 15");            // the last sums have left the matrix cores
+
+    // Epilogue, 16 tokens at a time through this wave's part of LDS, to store whole 16-byte pieces of rows.
+    // Lane (q = l / 16, c = l % 16) of fragment (f, j) holds token 16 f + c and packed columns 16 j + 4 q ..
+    // +3; when GLU, fragment j + 1 (odd) holds the up sums of fragment j.
+    constexpr int JO = GLU ? NF / 2 : NF, SIZE = F32 ? 4 : 2;        // output fragments, bytes per output
+    constexpr int PIECES = JO * 16 * SIZE / 16, PITCH = PIECES * 16 + 16;
+    static_assert(4 * 16 * PITCH <= (NA * ASLOT + NB * BSLOT) * 16, "room for the outputs");
+    uint8_t *stage = reinterpret_cast<uint8_t *>(lds) + wv * (16 * PITCH);
+    const int n1 = (nb0 + fb) / (GLU ? 2 : 1) * 16, q4 = 4 * (lane >> 4);   // first output column of this wave
+    f32x4_t sw[JO], other[JO];                                       // other: the up scales, or the bias
+#pragma unroll
+    for (int j = 0; j < JO; j++) {
+        const int col = min(nb0 + fb + j * (GLU ? 2 : 1), g.nblk - (GLU ? 2 : 1)) * 16 + q4;
+        sw[j] = *reinterpret_cast<const f32x4_t *>(g.sw + col);
+        if (GLU)
+            other[j] = *reinterpret_cast<const f32x4_t *>(g.sw + col + 16);
+        else
+            other[j] = g.bias ? *reinterpret_cast<const f32x4_t *>(g.bias + col) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    float sx[MF];
+#pragma unroll
+    for (int f = 0; f < MF; f++)
+        sx[f] = g.sx[min(m0 + (fa + f) * 16 + r16, g.T - 1)];
+#pragma unroll
+    for (int f = 0; f < MF; f++) {
+        uint8_t *at = stage + r16 * PITCH + q4 * SIZE;
+#pragma unroll
+        for (int j = 0; j < JO; j++) {
+            f32x4_t v;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                if constexpr (GLU)
+                    v[e] = silu((float)acc[f][2 * j][e] * sx[f] * sw[j][e]) *
+                           ((float)acc[f][2 * j + 1][e] * sx[f] * other[j][e]);
+                else
+                    v[e] = (float)acc[f][j][e] * sx[f] * sw[j][e] + other[j][e];
+            }
+            if constexpr (F32)
+                *reinterpret_cast<f32x4_t *>(at + j * 64) = v;
+            else
+                *reinterpret_cast<uint2 *>(at + j * 32) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        }
+#pragma unroll
+        for (int i = 0; i < (16 * PIECES + WAVE - 1) / WAVE; i++) {
+            const int p = i * WAVE + lane, r = p / PIECES, c = p % PIECES;
+            const int row = m0 + (fa + f) * 16 + r;
+            if (r < 16 && row < g.T)
+                store16(g, row, n1 + c * (16 / SIZE), *reinterpret_cast<const u32x4_t *>(stage + r * PITCH + c * 16));
+        }
+    }
+}
+
 // Rows of K codes at any alignment -> rows of `width` codes (a multiple of 16), zero past K.
 __global__ __launch_bounds__(256) void restage_kernel(const int8_t *x, int64_t ldx, int K, int chunks, int64_t total,
                                                       int8_t *dst)
@@ -295,18 +526,46 @@ hipError_t launch_tile(const I8Args &g, hipStream_t st)
 
 } // namespace
 
-// Tiles by the number of workgroups: the widest that still makes FILL of them, three quarters of the
-// card's 256 CUs, else the narrowest (16 columns; 32 when a gate and an up block have to be together),
-// with the K axis over more groups of waves the narrower the tile. Measured, microseconds (weights not in
-// any cache), chosen against the next wider or narrower tile: 1 x 3584 x 7168: 16 columns 7.4, 32 8.1;
-// 16 x 7168 x 4352: 32 8.4, 16 11.7, 64 9.8; 16 x 14336 x 3584: 64 10.7, 32 12.8, 128 14.3; 64 x 7168 x
-// 4352: 32 11.2, 64 13.1, 16 16.6; 64 x (2 x 14336) x 7168: 128 38.3, 64 42.6, 256 47.
+template <int NF, bool GLU, bool F32>
+hipError_t launch_wide_as(const I8Args &g, hipStream_t st)
+{
+    const int gx = (g.nblk + 2 * NF - 1) / (2 * NF), gy = (g.T + 255) / 256;
+    hipLaunchKernelGGL((wide_kernel<NF, GLU, F32>), dim3((unsigned)((gx * gy + XCDS - 1) / XCDS * XCDS)), dim3(256), 0, st,
+                       g, gx, gy);
+    return hipGetLastError();
+}
+
+// 224 columns where whole rounds of tiles over the CUs cost less with them than with 256: 8192 x 7168 outputs
+// are 4 rounds of 7 / 8 of a tile against 3.5 (so 4) of whole ones.
+hipError_t launch_wide(const I8Args &g, hipStream_t st)
+{
+    const bool f32 = g.out_type == MOE_TYPE_F32;
+    if (g.glu)
+        return f32 ? launch_wide_as<8, true, true>(g, st) : launch_wide_as<8, true, false>(g, st);
+    auto cost = [&](int nf) {
+        const int64_t tiles = (int64_t)((g.T + 255) / 256) * ((g.nblk + 2 * nf - 1) / (2 * nf));
+        return (tiles + CUS - 1) / CUS * nf;
+    };
+    if (cost(7) < cost(8))
+        return f32 ? launch_wide_as<7, false, true>(g, st) : launch_wide_as<7, false, false>(g, st);
+    return f32 ? launch_wide_as<8, false, true>(g, st) : launch_wide_as<8, false, false>(g, st);
+}
+
+// Tiles by the number of workgroups: the largest that still makes FILL of them, three quarters of the CUs,
+// else the narrowest (16 columns; 32 when a gate and an up block have to be together), with the K
+// axis over more groups of waves the narrower the tile. Measured, microseconds (weights not in any
+// cache), against the neighbours: 1 x 3584 x 7168 (tokens x columns x codes): 16 columns 7.4, 32 8.1; 16 x
+// 7168 x 4352: 32 8.4, 16 11.7, 64 9.8; 16 x 14336 x 3584: 64 10.7, 32 12.8, 128 14.3; 64 x 7168 x 4352: 32
+// 11.2, 64 13.1, 16 16.6; 64 x 28672 x 7168: 128 38.3, 64 42.6, 256 47; 7168 x 7168 weights and 128 tokens:
+// 64 x 64 20.8, 128 x 64 26.4; 256: 128 x 64 28.4, 64 x 64 37; 512: 128 x 128 39, 128 x 64 46; 1024: 128 x
+// 128 62, 256 x 256 80; 2048: 256 x 256 84, 128 x 128 120.
 hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
 {
-    constexpr int64_t FILL = 192;
-    auto fills = [&](int bm, int bn) {
-        return (int64_t)((g.T + bm - 1) / bm) * ((g.nblk * 16 + bn - 1) / bn) >= FILL;
+    constexpr int64_t FILL = CUS * 3 / 4;
+    auto tiles = [&](int bm, int bn) {
+        return (int64_t)((g.T + bm - 1) / bm) * ((g.nblk * 16 + bn - 1) / bn);
     };
+    auto fills = [&](int bm, int bn) { return tiles(bm, bn) >= FILL; };
     if (g.T <= 16) {
         if (fills(16, 64))
             return launch_tile<16, 64, 1, 2, 2, 4>(g, st);
@@ -323,17 +582,21 @@ hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
             return launch_tile<32, 32, 1, 1, 4, 3>(g, st);
         return launch_tile<32, 16, 1, 1, 8, 3>(g, st);
     }
-    const int64_t area = (int64_t)g.T * g.nblk * 16;
-    if (area >= (int64_t)256 * 256 * 256)
-        return launch_tile<256, 256, 2, 4, 1, 2>(g, st);
-    if (area >= (int64_t)128 * 128 * 256)
-        return launch_tile<128, 128, 2, 2, 1, 2>(g, st);
-    if (fills(64, 128))
+    if (g.T > 64) {
+        if (fills(256, 256))
+            return launch_wide(g, st);
+        if (fills(128, 128))   // two workgroups per CU share its LDS, or one takes three buffers: 512 tokens 39 us
+            return tiles(128, 128) > CUS ? launch_tile<128, 128, 2, 4, 1, 2>(g, st)   // against 53, 1024 tokens 74
+                                         : launch_tile<128, 128, 2, 4, 1, 3>(g, st);  // against 62
+        if (fills(128, 64))
+            return launch_tile<128, 64, 4, 2, 1, 3>(g, st);
+    } else if (fills(64, 128)) {
         return launch_tile<64, 128, 2, 4, 1, 3>(g, st);
+    }
     if (fills(64, 64))
         return launch_tile<64, 64, 2, 2, 2, 3>(g, st);
     if (fills(64, 32) || g.glu)
-        return launch_tile<64, 32, 2, 1, 2, 3>(g, st);
+        return launch_tile<64, 32, 2, 1, 4, 3>(g, st);
     return launch_tile<64, 16, 2, 1, 4, 3>(g, st);
 }
 
