@@ -12,6 +12,7 @@ namespace mxmoe {
 namespace {
 
 constexpr int CHUNK = 8;   // consecutive values per thread and load
+constexpr int MANY_ROWS = 1024;   // from here on the rows alone keep the card busy
 
 // Rows need not be aligned beyond their element size: the copies below compile to one wide global
 // access, which gfx950 serves at any byte address.
@@ -24,6 +25,15 @@ __device__ inline T load_any(const void *p)
 }
 template <typename T>
 __device__ inline void store_any(void *p, const T &v) { __builtin_memcpy(p, &v, sizeof(T)); }
+// The residual stream and the normalised BF16 rows leave past the caches: 8192 x 2048 rows with every output
+// 31 -> 24 us, 1024 x 14336 30 -> 22, 8192 x 7168 97 -> 91. The codes stay cached for the product that
+// reads them next (norm and reading back of 8192 x 7168: 109 us with both cached, 112 with neither, 105 so).
+template <typename T>
+__device__ inline void store_streamed(void *p, const T &v)
+{
+    typedef T Any __attribute__((aligned(1)));
+    __builtin_nontemporal_store(v, static_cast<Any *>(p));
+}
 
 // CHUNK values from column c on of a row of n values (zeros past n), as FP32.
 __device__ inline void load_row(const uint16_t *row, int c, int n, float *v)
@@ -64,7 +74,7 @@ __device__ inline void store_row(uint16_t *row, int c, int n, const float *v)
     for (int i = 0; i < 4; i++)
         r[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
     if (c + CHUNK <= n) {
-        store_any(row + c, r);
+        store_streamed(row + c, r);
     } else {
 #pragma unroll
         for (int i = 0; i < CHUNK; i++)
@@ -75,8 +85,8 @@ __device__ inline void store_row(uint16_t *row, int c, int n, const float *v)
 __device__ inline void store_row(float *row, int c, int n, const float *v)
 {
     if (c + CHUNK <= n) {
-        store_any(row + c, f32x4_t{v[0], v[1], v[2], v[3]});
-        store_any(row + c + 4, f32x4_t{v[4], v[5], v[6], v[7]});
+        store_streamed(row + c, f32x4_t{v[0], v[1], v[2], v[3]});
+        store_streamed(row + c + 4, f32x4_t{v[4], v[5], v[6], v[7]});
     } else {
 #pragma unroll
         for (int i = 0; i < CHUNK; i++)
@@ -343,6 +353,10 @@ __global__ __launch_bounds__(256) void dequantise_kernel(const int8_t *codes, in
     }
 }
 
+// One chunk of 8 values per thread up to 8192 columns, so that a row's loads are all in flight at once and its
+// reductions short: 1 x 7168, every output: 1024 threads 4.1 us, 512 with two chunks 4.8, 256 with four
+// 6.0; 8192 x 7168 FP32: 134, 139, 152. With many BF16 rows, two chunks keep more bytes in flight:
+// 8192 x 7168 to codes 78 us against 85.
 template <typename X, bool NORM>
 hipError_t launch_rows(const moe_norm_args &a, hipStream_t st)
 {
@@ -352,10 +366,12 @@ hipError_t launch_rows(const moe_norm_args &a, hipStream_t st)
         hipLaunchKernelGGL((norm_kernel<X, 64, 1, NORM>), quarter, dim3(256), 0, st, a);
     else if (H <= 256 * CHUNK)
         hipLaunchKernelGGL((norm_kernel<X, 256, 1, NORM>), rows, dim3(256), 0, st, a);
-    else if (H <= 256 * CHUNK * 2)
-        hipLaunchKernelGGL((norm_kernel<X, 256, 2, NORM>), rows, dim3(256), 0, st, a);
-    else if (H <= 256 * CHUNK * 4)
-        hipLaunchKernelGGL((norm_kernel<X, 256, 4, NORM>), rows, dim3(256), 0, st, a);
+    else if (H <= 512 * CHUNK)
+        hipLaunchKernelGGL((norm_kernel<X, 512, 1, NORM>), rows, dim3(512), 0, st, a);
+    else if (H <= 1024 * CHUNK && (a.T < MANY_ROWS || sizeof(X) == 4))
+        hipLaunchKernelGGL((norm_kernel<X, 1024, 1, NORM>), rows, dim3(1024), 0, st, a);
+    else if (H <= 512 * CHUNK * 2)
+        hipLaunchKernelGGL((norm_kernel<X, 512, 2, NORM>), rows, dim3(512), 0, st, a);
     else if (H <= 1024 * CHUNK * 2)
         hipLaunchKernelGGL((norm_kernel<X, 1024, 2, NORM>), rows, dim3(1024), 0, st, a);
     else

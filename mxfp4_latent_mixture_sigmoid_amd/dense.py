@@ -7,7 +7,6 @@ their last dimension has to be contiguous. Calls run on ``stream`` (default: the
 """
 from __future__ import annotations
 
-import ctypes
 from typing import NamedTuple
 
 import torch
@@ -16,7 +15,12 @@ from . import abi
 
 _TYPES = {torch.bfloat16: abi.TYPE_BF16, torch.float32: abi.TYPE_F32}
 _BF16, _INT8 = (torch.bfloat16,), (torch.int8,)
-_byref = ctypes.byref
+_pack = abi.NORM_ARGS.pack
+_raw_stream = torch._C._cuda_getCurrentRawStream   # of a GPU: its handle, without an object around it
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
 
 
 class Normed(NamedTuple):
@@ -27,7 +31,7 @@ class Normed(NamedTuple):
     sum: torch.Tensor | None
 
 
-def _bad_rows(name, t, dtypes, device, shape):
+def _bad_rows(name, t, dtypes, index, shape):
     """Why `t` is not the matrix that _rows wants."""
     if t.dtype not in dtypes:
         return f"{name}: {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}"
@@ -36,50 +40,52 @@ def _bad_rows(name, t, dtypes, device, shape):
                 f"strides {t.stride()}")
     if shape is not None and t.shape != shape:
         return f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}"
-    return f"{name}: on {t.device}, expected {device if device is not None else 'a GPU'}"
+    return f"{name}: on {t.device}, expected GPU {index}"
 
 
-def _rows(name, t, dtypes, device=None, shape=None):
-    """Row stride of a [T, width] tensor on the GPU, after checking it."""
+def _rows(name, t, dtypes, index, shape=None):
+    """Row stride of a [T, width] tensor on GPU `index`, after checking it."""
     strides, sizes = t.stride(), t.shape
-    if (t.dtype not in dtypes or len(sizes) != 2 or (strides[1] != 1 and sizes[1] > 1)
-            or (shape is not None and sizes != shape) or (not t.is_cuda if device is None else t.device != device)):
-        raise ValueError(_bad_rows(name, t, dtypes, device, shape))
+    if (t.dtype not in dtypes or len(strides) != 2 or (strides[1] != 1 and sizes[1] > 1)
+            or (shape is not None and sizes != shape) or t.get_device() != index):
+        raise ValueError(_bad_rows(name, t, dtypes, index, shape))
     # the stride of a single row means nothing (torch reports any value there)
     return strides[0] if sizes[0] > 1 else sizes[1]
 
 
-def _vector(name, t, n, dtype, device):
-    if t.dtype != dtype or t.shape != (n,) or (n > 1 and t.stride(0) != 1) or t.device != device:
-        raise ValueError(f"{name}: expected a contiguous {dtype} [{n}] on {device}, got {t.dtype} {tuple(t.shape)} "
+def _vector(name, t, n, dtype, index):
+    if t.dtype != dtype or t.shape != (n,) or (n > 1 and t.stride(0) != 1) or t.get_device() != index:
+        raise ValueError(f"{name}: expected a contiguous {dtype} [{n}] on GPU {index}, got {t.dtype} {tuple(t.shape)} "
                          f"on {t.device}")
 
 
-def _call(device, stream, tensors, f, *args):
-    """f(*args, stream handle) with `device` current, on `stream` when one is given: outputs are then
-    allocated for it, and the allocator learns that it uses tensors of other streams. On the current
-    device and stream it is the bare call, whose latency counts for single tokens."""
+def _call(x, stream, tensors, f, *args):
+    """f(*args, GPU index, stream handle) with x's GPU current, on `stream` when one is given: outputs
+    are then allocated for it, and the allocator learns that it uses tensors of other streams. On the
+    current GPU and stream it is the bare call, whose latency counts for single tokens."""
+    index = x.get_device()
+    if index < 0:
+        raise ValueError(f"expected tensors on a GPU, got one on {x.device}")
     if stream is None:
-        index = device.index
         if index == torch.cuda.current_device():
-            return f(*args, torch._C._cuda_getCurrentRawStream(index))
-        with torch.cuda.device(device):
-            return f(*args, torch._C._cuda_getCurrentRawStream(index))
+            return f(*args, index, _raw_stream(index))
+        with torch.cuda.device(index):
+            return f(*args, index, _raw_stream(index))
     with torch.cuda.stream(stream):
-        got = f(*args, stream.cuda_stream)
+        got = f(*args, index, stream.cuda_stream)
     for t in tensors:
         if torch.is_tensor(t):
             t.record_stream(stream)
     return got
 
 
-def _output(name, want, x, T, width, dtype):
-    """(tensor, row stride) of an output asked for by True, given as a tensor, or not wanted."""
+def _output(name, want, x, dtype, index):
+    """(tensor, row stride) of an output of x's shape asked for by True, given as a tensor, or not wanted."""
     if want is True:
-        return torch.empty((T, width), dtype=dtype, device=x.device), width
+        return torch.empty_like(x, dtype=dtype), x.shape[1]
     if want is None or want is False:
         return None, 0
-    return want, _rows(name, want, (dtype,), x.device, (T, width))
+    return want, _rows(name, want, (dtype,), index, x.shape)
 
 
 def rms_norm(x, weight=None, eps=1e-6, delta=None, sum=None, out=True, codes=False, scales=None, stream=None) -> Normed:
@@ -89,65 +95,68 @@ def rms_norm(x, weight=None, eps=1e-6, delta=None, sum=None, out=True, codes=Fal
     BF16) and ``codes`` (y as int8, with ``scales`` = max|y| / 127 per row) is False, True (allocated
     here) or a tensor to write into; ``sum`` may be x itself. A row of zeros has scale 0; a row with a
     NaN or an infinity has scale NaN and codes 0."""
-    return _call(x.device, stream, (x, weight, delta, sum, out, codes, scales), _rms_norm, x, weight, eps, delta, sum, out,
-                 codes, scales)
+    return _call(x, stream, (x, weight, delta, sum, out, codes, scales), _rms_norm, x, weight, eps, delta, sum, out, codes,
+                 scales)
 
 
-def _rms_norm(x, weight, eps, delta, sum, out, codes, scales, stream):
-    ldx = _rows("x", x, _TYPES)
+def _rms_norm(x, weight, eps, delta, sum, out, codes, scales, index, stream):
+    ldx = _rows("x", x, _TYPES, index)
     T, H = x.shape
     dtype, ldd = x.dtype, 0
     if delta is not None:
-        ldd = _rows("delta", delta, _BF16, x.device, x.shape)
+        ldd = _rows("delta", delta, _BF16, index, x.shape)
     if weight is not None:
-        _vector("weight", weight, H, torch.bfloat16, x.device)
-    s, lds = _output("sum", sum, x, T, H, dtype)
-    o, ldo = _output("out", out, x, T, H, torch.bfloat16)
-    q, ldc = _output("codes", codes, x, T, H, torch.int8)
+        _vector("weight", weight, H, torch.bfloat16, index)
+    s, lds = _output("sum", sum, x, dtype, index)
+    o, ldo = _output("out", out, x, torch.bfloat16, index)
+    q, ldc = _output("codes", codes, x, torch.int8, index)
     if scales is not None:
         if q is None:
             raise ValueError("scales given without codes")
-        _vector("scales", scales, T, torch.float32, x.device)
+        _vector("scales", scales, T, torch.float32, index)
     elif q is not None:
         scales = torch.empty(T, dtype=torch.float32, device=x.device)
-    ptr = abi.ptr
-    a = abi.NormArgs(x.data_ptr(), ptr(delta), ptr(weight), ptr(s), ptr(o), ptr(q), ptr(scales), ldx, ldd, lds, ldo, ldc,
-                     T, H, _TYPES[dtype], eps)
-    abi.check(abi.lib().moe_norm(_byref(a), stream), "moe_norm")
+    ptr = _ptr
+    status = abi.lib().moe_norm(_pack(x.data_ptr(), ptr(delta), ptr(weight), ptr(s), ptr(o), ptr(q), ptr(scales), ldx, ldd,
+                                      lds, ldo, ldc, T, H, _TYPES[dtype], eps), stream)
+    if status:
+        raise abi.MoEError(status, "moe_norm")
     return Normed(o, q, scales, s)
 
 
 def quantise(x, codes=None, scales=None, stream=None):
     """Rows of x ([T, K] BF16 or FP32) as int8 codes with a scale each: scale = max|x| / 127,
     codes = x / scale rounded to nearest even. Returns (codes, scales), into the given tensors if any."""
-    return _call(x.device, stream, (x, codes, scales), _quantise, x, codes, scales)
+    return _call(x, stream, (x, codes, scales), _quantise, x, codes, scales)
 
 
-def _quantise(x, codes, scales, stream):
-    ldx = _rows("x", x, _TYPES)
+def _quantise(x, codes, scales, index, stream):
+    ldx = _rows("x", x, _TYPES, index)
     T, K = x.shape
-    q, ldc = _output("codes", True if codes is None else codes, x, T, K, torch.int8)
+    q, ldc = _output("codes", True if codes is None else codes, x, torch.int8, index)
     if scales is None:
         scales = torch.empty(T, dtype=torch.float32, device=x.device)
     else:
-        _vector("scales", scales, T, torch.float32, x.device)
-    abi.check(abi.lib().moe_quantise(x.data_ptr(), _TYPES[x.dtype], ldx, T, K, q.data_ptr(), ldc, scales.data_ptr(),
-                                     stream), "moe_quantise")
+        _vector("scales", scales, T, torch.float32, index)
+    status = abi.lib().moe_quantise(x.data_ptr(), _TYPES[x.dtype], ldx, T, K, q.data_ptr(), ldc, scales.data_ptr(), stream)
+    if status:
+        raise abi.MoEError(status, "moe_quantise")
     return q, scales
 
 
 def dequantise(codes, scales, out=None, stream=None):
     """The values that codes stand for, bf16(codes * scales[:, None])."""
-    return _call(codes.device, stream, (codes, scales, out), _dequantise, codes, scales, out)
+    return _call(codes, stream, (codes, scales, out), _dequantise, codes, scales, out)
 
 
-def _dequantise(codes, scales, out, stream):
-    ldc = _rows("codes", codes, _INT8)
+def _dequantise(codes, scales, out, index, stream):
+    ldc = _rows("codes", codes, _INT8, index)
     T, K = codes.shape
-    _vector("scales", scales, T, torch.float32, codes.device)
-    o, ldo = _output("out", True if out is None else out, codes, T, K, torch.bfloat16)
-    abi.check(abi.lib().moe_dequantise(codes.data_ptr(), ldc, scales.data_ptr(), T, K, o.data_ptr(), ldo, stream),
-              "moe_dequantise")
+    _vector("scales", scales, T, torch.float32, index)
+    o, ldo = _output("out", True if out is None else out, codes, torch.bfloat16, index)
+    status = abi.lib().moe_dequantise(codes.data_ptr(), ldc, scales.data_ptr(), T, K, o.data_ptr(), ldo, stream)
+    if status:
+        raise abi.MoEError(status, "moe_dequantise")
     return o
 
 
@@ -168,42 +177,46 @@ class Int8Linear:
             raise ValueError("up_codes and up_scales go together")
         if up_codes is not None and bias is not None:
             raise ValueError("the gated product takes no bias")
-        _rows("codes", codes, _INT8)
-        self.N, self.K = codes.shape
-        self.device, self.T_max, self.out_dtype = codes.device, T_max, out_dtype
-        _vector("scales", scales, self.N, torch.float32, self.device)
-        if up_codes is not None:
-            _rows("up_codes", up_codes, _INT8, self.device, codes.shape)
-            _vector("up_scales", up_scales, self.N, torch.float32, self.device)
-        if bias is not None:
-            _vector("bias", bias, self.N, torch.float32, self.device)
-        self.cfg = abi.LinearConfig(self.N, self.K, int(up_codes is not None), _TYPES[out_dtype])
-        _call(self.device, stream, (codes, scales, bias, up_codes, up_scales), self._pack, codes, scales, bias, up_codes,
+        self.T_max, self.out_dtype = T_max, out_dtype
+        _call(codes, stream, (codes, scales, bias, up_codes, up_scales), self._create, codes, scales, bias, up_codes,
               up_scales)
 
-    def _pack(self, codes, scales, bias, up_codes, up_scales, stream):
+    def _create(self, codes, scales, bias, up_codes, up_scales, index, stream):
+        _rows("codes", codes, _INT8, index)
+        self.N, self.K = codes.shape
+        _vector("scales", scales, self.N, torch.float32, index)
+        if up_codes is not None:
+            _rows("up_codes", up_codes, _INT8, index, codes.shape)
+            _vector("up_scales", up_scales, self.N, torch.float32, index)
+            up_codes = up_codes.contiguous()
+        if bias is not None:
+            _vector("bias", bias, self.N, torch.float32, index)
+        self.cfg = abi.LinearConfig(self.N, self.K, int(up_codes is not None), _TYPES[self.out_dtype])
         packed_bytes, ws_bytes = abi.linear_query(self.cfg, self.T_max)
-        codes = codes.contiguous()
-        up_codes = up_codes.contiguous() if up_codes is not None else None
-        self.packed = torch.empty(packed_bytes, dtype=torch.uint8, device=self.device)
-        self.workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=self.device)
-        self.handle = abi.linear_create(self.cfg, codes, scales, up_codes, up_scales, bias, self.packed, stream)
+        self.packed = torch.empty(packed_bytes, dtype=torch.uint8, device=codes.device)
+        self.workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=codes.device)
+        self.handle = abi.linear_create(self.cfg, codes.contiguous(), scales, up_codes, up_scales, bias, self.packed, stream)
         self._buffers = self.workspace.data_ptr(), self.workspace.numel()
 
     def forward(self, x, scales, out=None, stream=None):
         """The product for codes x [T, K] with FP32 scales [T]; returns out [T, N]."""
-        return _call(self.device, stream, (x, scales, out, self.packed, self.workspace), self._forward, x, scales, out)
+        return _call(self.packed, stream, (x, scales, out, self.packed, self.workspace), self._forward, x, scales, out)
 
-    def _forward(self, x, scales, out, stream):
-        ldx = _rows("x", x, _INT8, self.device)
+    def _forward(self, x, scales, out, index, stream):
+        ldx = _rows("x", x, _INT8, index)
         T, K = x.shape
         if K != self.K or T > self.T_max:
             raise ValueError(f"x: shape {tuple(x.shape)}, expected at most {self.T_max} rows of {self.K}")
-        _vector("scales", scales, T, torch.float32, self.device)
-        o, ldo = _output("out", True if out is None else out, x, T, self.N, self.out_dtype)
-        abi.check(abi.lib().moe_linear_forward(self.handle, x.data_ptr(), ldx, scales.data_ptr(), T, o.data_ptr(), ldo,
-                                               *self._buffers, stream), "moe_linear_forward")
-        return o
+        _vector("scales", scales, T, torch.float32, index)
+        if out is None:
+            out, ldo = torch.empty((T, self.N), dtype=self.out_dtype, device=x.device), self.N
+        else:
+            ldo = _rows("out", out, (self.out_dtype,), index, (T, self.N))
+        status = abi.lib().moe_linear_forward(self.handle, x.data_ptr(), ldx, scales.data_ptr(), T, out.data_ptr(), ldo,
+                                              *self._buffers, stream)
+        if status:
+            raise abi.MoEError(status, "moe_linear_forward")
+        return out
 
     def close(self):
         if self.handle:

@@ -34,7 +34,12 @@ def _norm(**kw):
     a = dict(x=A, delta=None, weight=None, sum=None, out=A, codes=None, scales=None, ldx=64, ldd=64, lds=64, ldo=64,
              ldc=64, T=4, H=64, x_type=abi.TYPE_BF16, eps=1e-6)
     a.update(kw)
-    return abi.lib().moe_norm(ctypes.byref(abi.NormArgs(**a)), None)
+    return abi.lib().moe_norm(bytes(abi.NormArgs(**a)), None)
+
+
+def test_packed_norm_arguments_are_the_structure():
+    a = abi.NormArgs(*range(1, 16), 0.5)
+    assert abi.NORM_ARGS.pack(*range(1, 16), 0.5) == bytes(a)
 
 
 @pytest.mark.parametrize("kw", [

@@ -219,21 +219,38 @@ def test_products(T, N, K, pad, offset, kind):
     assert ok()
 
 
-@pytest.mark.parametrize("T,N,K,glu", [(2048, 4096, 640, 0), (4100, 4200, 272, 0), (2304, 2100, 384, 1),
-                                       (1030, 1100, 1024, 0), (8192, 500, 128, 0), (300, 9000, 256, 1)])
-def test_products_large(T, N, K, glu):
-    """The large tiles, whole and ragged, against exact sums in FP64 on the GPU."""
+# (tokens, outputs, codes): whole and ragged tiles of 128 x 64, 128 x 128 (two and three buffers), 256 x 224 and
+# 256 x 256, and sums of one to several 128-code stages
+LARGE = [(2048, 4096, 640, 0), (4100, 4200, 272, 0), (2304, 2100, 384, 1), (1030, 1100, 1024, 0), (8192, 500, 128, 0),
+         (300, 9000, 256, 1), (2048, 7168, 64, 0), (2050, 7170, 100, 0), (3584, 4096, 1152, 0), (1921, 6930, 515, 0),
+         (2048, 3584, 256, 1), (2300, 3900, 130, 1), (2048, 3600, 1, 1), (4096, 3584, 384, 0), (257, 6000, 336, 0)]
+
+
+@pytest.mark.parametrize("T,N,K,glu", LARGE)
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+def test_products_large(T, N, K, glu, out_dtype):
+    """The large tiles against exact sums in FP64 on the GPU."""
     g = gen(T + N)
-    layer, w, s, _ = make(N, K, glu, g, T_max=T)
+    layer, w, s, b = make(N, K, glu, g, bias=not glu and N % 3 == 0, T_max=T, out_dtype=out_dtype)
     x, sx = codes_rows(T, K, g), (0.5 + torch.rand(T, generator=g)).cuda()
-    out = layer.forward(x, sx).double()
+    buf, ok = guarded(T, N, out_dtype)
+    out = layer.forward(x, sx, out=buf).double()
+    assert ok()
 
     def product(w, s):
         w, s = torch.from_numpy(w).cuda().double(), torch.from_numpy(s).cuda()
         return (x.double() @ w.t().contiguous()) * sx.double()[:, None] * s
     p = product(w[0], s[0])
-    ref = p * torch.sigmoid(p) * product(w[1], s[1]) if glu else p
-    allowed = ref.abs() * (R.B + (24 + 6 * p.abs()) * R.U) + 1e-30
+    if glu:
+        u = product(w[1], s[1])
+        ref = p * torch.sigmoid(p) * u
+        allowed = ref.abs() * (24 + 6 * p.abs()) * R.U + u.abs() * 2.0 ** -120
+    else:
+        bias = 0 if b is None else torch.from_numpy(b).cuda()
+        ref = p + bias
+        allowed = 4 * R.U * (p.abs() + abs(bias))
+    if out_dtype is BF16:
+        allowed = allowed + ref.abs() * R.B + 2.0 ** -133
     over = (out - ref).abs() - allowed
     assert over.max() <= 0, (float(over.max()), int((over > 0).sum()))
 
