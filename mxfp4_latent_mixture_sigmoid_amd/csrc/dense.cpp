@@ -61,8 +61,9 @@ int64_t workspace_bytes_for(const moe_linear_config *c, int64_t T) { return alig
 
 bool linear_fits(const moe_linear_config *c, int64_t T)
 {
-    // the smallest tile of more than 64 tokens is 64 x 16; restaging takes one thread per 16 codes
-    const int64_t tiles = ((T + 63) / 64) * i8_row_blocks(c->n, c->glu);
+    // more than a few thousand workgroups come in tiles of 64 x 32 at least; restaging takes one thread per
+    // 16 codes
+    const int64_t tiles = ((T + 63) / 64) * ((i8_row_blocks(c->n, c->glu) + 1) / 2);
     return tiles + 8 <= INT32_MAX && rows_fit(T, i8_stages(c->k) * I8_STAGE);
 }
 

@@ -551,14 +551,15 @@ hipError_t launch_wide(const I8Args &g, hipStream_t st)
     return f32 ? launch_wide_as<8, false, true>(g, st) : launch_wide_as<8, false, false>(g, st);
 }
 
-// Tiles by the number of workgroups: the largest that still makes FILL of them, three quarters of the CUs,
-// else the narrowest (16 columns; 32 when a gate and an up block have to be together), with the K
-// axis over more groups of waves the narrower the tile. Measured, microseconds (weights not in any
-// cache), against the neighbours: 1 x 3584 x 7168 (tokens x columns x codes): 16 columns 7.4, 32 8.1; 16 x
-// 7168 x 4352: 32 8.4, 16 11.7, 64 9.8; 16 x 14336 x 3584: 64 10.7, 32 12.8, 128 14.3; 64 x 7168 x 4352: 32
-// 11.2, 64 13.1, 16 16.6; 64 x 28672 x 7168: 128 38.3, 64 42.6, 256 47; 7168 x 7168 weights and 128 tokens:
-// 64 x 64 20.8, 128 x 64 26.4; 256: 128 x 64 28.4, 64 x 64 37; 512: 128 x 128 39, 128 x 64 46; 1024: 128 x
-// 128 62, 256 x 256 80; 2048: 256 x 256 84, 128 x 128 120.
+// The largest tile that still makes FILL workgroups, three quarters of the CUs, else the smallest (16 columns; 32
+// when a gate and an up block have to be together), with the K axis over more groups of waves the
+// smaller the tile. Measured, microseconds (tokens x columns x codes; weights not in any cache), against
+// the neighbours: 1 x 3584 x 7168: 16 columns 7.4, 32 8.1; 16 x 7168 x 4352: 32 8.4, 16 11.7, 64 9.8; 16 x
+// 14336 x 3584: 64 10.7, 32 12.8, 128 14.3; 64 x 28672 x 7168: 64 x 128 38, 64 x 64 42; 64 x 7168 x 4352: 64 x
+// 32 11.2, 64 x 64 13.1; 64 x 3584 x 7168: 32 x 32 11.8, 64 x 16 12.4, 64 x 32 14.2; 184 x 160 x 11648: 16 x 16
+// 7.2, 32 x 16 8.8, 64 x 32 15.5; 1000 x 128 x 4096: 32 x 16 5.6, 16 x 16 7.3, 32 x 32 6.4; 7168 x 7168
+// weights and 128 tokens: 64 x 64 20.8, 128 x 64 26.4; 256: 128 x 64 28.4, 64 x 64 37; 512: 128 x 128 39,
+// 128 x 64 46; 1024: 128 x 128 62, wide 80; 2048: wide 84, 128 x 128 120.
 hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
 {
     constexpr int64_t FILL = CUS * 3 / 4;
@@ -573,31 +574,39 @@ hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
             return launch_tile<16, 32, 1, 1, 4, 4>(g, st);
         return launch_tile<16, 16, 1, 1, 8, 3>(g, st);
     }
-    if (g.T <= 32) {
+    if (g.T > 64) {
+        // A round of wide tiles (one per CU) takes about 1.5 times a round of 128 x 128 tiles (two per CU),
+        // whatever K; the wide ones come in whole rounds.
+        const int64_t rounds = (tiles(256, 256) + CUS - 1) / CUS, small = tiles(128, 128);
+        if (rounds * 3 * 2 * CUS <= 2 * (small > 2 * CUS ? small : 2 * CUS) && fills(256, 256))
+            return launch_wide(g, st);
+        if (small > CUS)   // two workgroups per CU share its LDS, or one takes three buffers: 512 tokens 39 us
+            return launch_tile<128, 128, 2, 4, 1, 2>(g, st);   // against 53, 1024 tokens 74 against 62
+        if (small >= FILL)
+            return launch_tile<128, 128, 2, 4, 1, 3>(g, st);
+        if (fills(128, 64))
+            return launch_tile<128, 64, 4, 2, 1, 3>(g, st);
+    } else if (g.T <= 32) {
         if (fills(32, 128))
             return launch_tile<32, 128, 1, 4, 1, 4>(g, st);
         if (fills(32, 64))
             return launch_tile<32, 64, 1, 2, 2, 4>(g, st);
-        if (fills(32, 32) || g.glu)
-            return launch_tile<32, 32, 1, 1, 4, 3>(g, st);
-        return launch_tile<32, 16, 1, 1, 8, 3>(g, st);
-    }
-    if (g.T > 64) {
-        if (fills(256, 256))
-            return launch_wide(g, st);
-        if (fills(128, 128))   // two workgroups per CU share its LDS, or one takes three buffers: 512 tokens 39 us
-            return tiles(128, 128) > CUS ? launch_tile<128, 128, 2, 4, 1, 2>(g, st)   // against 53, 1024 tokens 74
-                                         : launch_tile<128, 128, 2, 4, 1, 3>(g, st);  // against 62
-        if (fills(128, 64))
-            return launch_tile<128, 64, 4, 2, 1, 3>(g, st);
     } else if (fills(64, 128)) {
         return launch_tile<64, 128, 2, 4, 1, 3>(g, st);
     }
-    if (fills(64, 64))
-        return launch_tile<64, 64, 2, 2, 2, 3>(g, st);
-    if (fills(64, 32) || g.glu)
-        return launch_tile<64, 32, 2, 1, 4, 3>(g, st);
-    return launch_tile<64, 16, 2, 1, 4, 3>(g, st);
+    if (g.T > 32) {
+        if (fills(64, 64))
+            return launch_tile<64, 64, 2, 2, 2, 3>(g, st);
+        if (fills(64, 32))
+            return launch_tile<64, 32, 2, 1, 4, 3>(g, st);
+    }
+    if (fills(32, 32))
+        return launch_tile<32, 32, 1, 1, 4, 3>(g, st);
+    if (g.glu)
+        return launch_tile<16, 32, 1, 1, 4, 4>(g, st);
+    if (fills(32, 16))
+        return launch_tile<32, 16, 1, 1, 8, 3>(g, st);
+    return launch_tile<16, 16, 1, 1, 8, 3>(g, st);
 }
 
 hipError_t launch_i8_restage(const int8_t *x, int64_t ldx, int T, int K, int8_t *dst, hipStream_t st)
