@@ -51,9 +51,9 @@ bool valid_linear(const moe_linear_config *c)
     return c->n <= (1 << 26) && i8_row_blocks(c->n, c->glu) * i8_stages(c->k) * 2 * WAVE / 256 < INT32_MAX;
 }
 
-// Activations that the products' loads cannot take as they are (rows at 16-byte steps from a 16-byte
-// aligned address, K whole 16-byte chunks, a tile's rows within one load window) are first laid
-// out in the workspace.
+// Whether the products' direct loads to LDS can take the activations as they are: rows at 16-byte steps from a
+// 16-byte aligned address, K whole 16-byte chunks, a tile's rows within one load window. Others go
+// through registers or, in large products, are first laid out in the workspace.
 constexpr int64_t LD_MAX = 1 << 22;
 bool direct(const int8_t *x, int64_t ldx, int64_t K) { return aligned(x, 16) && ldx % 16 == 0 && K % 16 == 0 && ldx <= LD_MAX; }
 
@@ -186,15 +186,6 @@ moe_status moe_linear_forward(moe_linear *l, const int8_t *x, int64_t ldx, const
     I8Args g{};
     g.x = x;
     g.ldx = ldx;
-    g.K = c->k;
-    if (!direct(x, ldx, c->k)) {
-        int8_t *staged = static_cast<int8_t *>(workspace);
-        const hipError_t e = launch_i8_restage(x, ldx, T, c->k, staged, st);
-        if (e != hipSuccess)
-            return MOE_ERR_HIP;
-        g.x = staged;
-        g.ldx = g.K = (int)(i8_stages(c->k) * I8_STAGE);
-    }
     g.sx = scales;
     g.w = l->blocks;
     g.sw = l->scales;
@@ -203,9 +194,20 @@ moe_status moe_linear_forward(moe_linear *l, const int8_t *x, int64_t ldx, const
     g.ldo = ldo;
     g.T = T;
     g.N = c->n;
+    g.K = c->k;
     g.nblk = (int)i8_row_blocks(c->n, c->glu);
     g.glu = c->glu;
     g.out_type = c->out_type;
+    g.direct = direct(x, ldx, c->k);
+    if (!g.direct && !i8_takes_any_rows(g)) {
+        int8_t *staged = static_cast<int8_t *>(workspace);
+        const hipError_t e = launch_i8_restage(x, ldx, T, c->k, staged, st);
+        if (e != hipSuccess)
+            return MOE_ERR_HIP;
+        g.x = staged;
+        g.ldx = g.K = (int)(i8_stages(c->k) * I8_STAGE);
+        g.direct = 1;
+    }
     return hip_status(launch_i8_product(g, st));
 }
 

@@ -25,7 +25,7 @@ __host__ __device__ inline int64_t i8_row_blocks(int64_t n, bool glu) { return (
 __host__ __device__ inline int64_t i8_stages(int64_t k) { return (k + I8_STAGE - 1) / I8_STAGE; }
 
 struct I8Args {
-    const int8_t *x;       // codes [T, K], 16-byte aligned rows, K a multiple of 16
+    const int8_t *x;       // codes [T, K]
     int64_t ldx;
     const float *sx;       // [T]
     const uint8_t *w;      // packed blocks
@@ -36,7 +36,10 @@ struct I8Args {
     int T, N, K;           // N output columns
     int nblk;              // row blocks of w
     int glu, out_type;
+    int direct;            // rows at 16-byte steps and K in whole 16-byte chunks
 };
+// Whether the product of these sizes takes rows that are not `direct`; else they have to be restaged.
+bool i8_takes_any_rows(const I8Args &g);
 hipError_t launch_i8_product(const I8Args &g, hipStream_t st);
 // Codes [T, K] with any row alignment -> [T, I8_STAGE * stages] rows, zero-padded.
 hipError_t launch_i8_restage(const int8_t *x, int64_t ldx, int T, int K, int8_t *dst, hipStream_t st);

@@ -35,6 +35,13 @@ __device__ inline void load_lds(const void *base, int bytes, int off, u32x4_t *d
         0, CPOL);
 }
 
+// v without its first n bytes (n >= 0), zeros at the end.
+__device__ inline u32x4_t drop_bytes(u32x4_t v, int n)
+{
+    const unsigned __int128 x = __builtin_bit_cast(unsigned __int128, v);
+    return __builtin_bit_cast(u32x4_t, n < 16 ? x >> (8 * n) : (unsigned __int128)0);
+}
+
 // Where chunk c (16 codes) of row r of a staged activation tile (rows of I8_STAGE bytes) lies: the
 // operand reads -- 8 or 16 consecutive rows, one chunk -- then fall in distinct banks.
 __device__ inline int swizzle(int r) { return (r & 7) ^ ((r >> 3) & 1); }
@@ -146,13 +153,18 @@ __device__ inline void emit(const I8Args &g, int r, float sx, int nb, acc_t sum,
 // activations 8 rows x 128 bytes (whole lines), of the weights one packed block. Rows past T and stages
 // past K lie outside the loads' windows and read as zeros without touching memory. ONCE: there is
 // one row tile, so weights are read once, and are not to displace the activations in the caches.
-template <int BM, int BN, int NWM, int NWN, int KG, int NBUF, bool ONCE>
+// ANY: activations whose rows the direct loads cannot take (any address, any K >= 16) pass through
+// registers instead, loaded two iterations ahead and written to LDS one ahead (NBUF = 3); rows past T, whose
+// sums are never stored, repeat the last one -- or, in 16-token tiles, where they can be most, are not
+// loaded (4 x 1792 x 12288: 9.3 us against 14.2; the test costs fuller tiles 10 to 20%) -- and the
+// chunk that crosses K is loaded from 16 codes before K and shifted into place.
+template <int BM, int BN, int NWM, int NWN, int KG, int NBUF, bool ONCE, bool ANY>
 __global__ __launch_bounds__(WAVE *NWM *NWN *KG) void tile_kernel(const I8Args g, int gx, int gy)
 {
     constexpr int NW = NWM * NWN, WMF = BM / NWM / 16, WNF = BN / NWN / 16;
     constexpr int AL = BM / 8 / NW, BL = BN / 8 / NW;   // loads per wave and stage
     constexpr int STAGE = (BM + BN) * 8;                // 16-byte slots
-    static_assert(AL * NW * 8 == BM && BL * NW * 8 == BN, "tile");
+    static_assert(AL * NW * 8 == BM && BL * NW * 8 == BN && (!ANY || NBUF == 3), "tile");
     static_assert(KG == 1 || NBUF * STAGE >= NW * WMF * WNF * WAVE, "room for the groups' sums");
     __shared__ u32x4_t lds[NBUF * KG * STAGE];
     const int lane = threadIdx.x & (WAVE - 1);
@@ -168,24 +180,53 @@ __global__ __launch_bounds__(WAVE *NWM *NWN *KG) void tile_kernel(const I8Args g
     const uint8_t *wt = g.w + (int64_t)nb0 * I8_STAGE_BYTES;
     const int wbytes = min(g.nblk - nb0, BN / 16) * I8_STAGE_BYTES;
     const int64_t wstep = (int64_t)g.nblk * I8_STAGE_BYTES;
-    int aoff[AL];
+    int64_t arow[AL];   // byte offsets of this lane's rows, and codes of its chunks in a stage
+    int ak[AL];
 #pragma unroll
     for (int i = 0; i < AL; i++) {
         const int row = (wv * AL + i) * 8 + (lane >> 3);
-        aoff[i] = row * (int)g.ldx + ((lane & 7) ^ swizzle(row)) * 16;
+        arow[i] = !ANY || row < g.T - m0 ? row * g.ldx : BM == 16 ? -1 : (g.T - 1 - m0) * g.ldx;
+        ak[i] = ((lane & 7) ^ swizzle(row)) * 16;
     }
-    auto issue = [&](int it) {
-        u32x4_t *buf = &lds[(it % NBUF * KG + kg) * STAGE];
+    auto issue_w = [&](int it) {
         const int s = it * KG + kg, last = min(s, nst - 1), in = -(int)(s < nst);   // past K: empty windows
-        const int8_t *xs = xt + last * I8_STAGE;
+        u32x4_t *buf = &lds[(it % NBUF * KG + kg) * STAGE + BM * 8];
         const uint8_t *ws = wt + last * wstep;
 #pragma unroll
         for (int i = 0; i < BL; i++)
             load_lds<ONCE ? CPOL_NT : 0>(ws, wbytes & in, (wv * BL + i) * I8_BLOCK_BYTES + lane * 16,
-                                         &buf[BM * 8 + (wv * BL + i) * WAVE]);
+                                         &buf[(wv * BL + i) * WAVE]);
+    };
+    auto issue_x = [&](int it) {
+        const int s = it * KG + kg, last = min(s, nst - 1), in = -(int)(s < nst);
+        u32x4_t *buf = &lds[(it % NBUF * KG + kg) * STAGE];
 #pragma unroll
         for (int i = 0; i < AL; i++)
-            load_lds(xs, (xbytes - last * I8_STAGE) & in, aoff[i], &buf[(wv * AL + i) * WAVE]);
+            load_lds(xt + last * I8_STAGE, (xbytes - last * I8_STAGE) & in, (int)arow[i] + ak[i], &buf[(wv * AL + i) * WAVE]);
+    };
+    struct Rows {
+        u32x4_t v[AL];
+    };
+    auto load_x = [&](int it, Rows &r) {
+        const int s = min(it * KG + kg, nst - 1);   // past K: the last stage again, against zero weights
+#pragma unroll
+        for (int i = 0; i < AL; i++) {
+            const int k = s * I8_STAGE + ak[i];
+            if (BM > 16 || arow[i] >= 0)
+                __builtin_memcpy(&r.v[i], xt + arow[i] + min(k, g.K - 16), 16);
+        }
+    };
+    auto store_x = [&](int it, const Rows &r) {
+        const int s = min(it * KG + kg, nst - 1);
+        u32x4_t *buf = &lds[(it % NBUF * KG + kg) * STAGE];
+#pragma unroll
+        for (int i = 0; i < AL; i++) {
+            const int late = max(s * I8_STAGE + ak[i] - (g.K - 16), 0);   // bytes to drop at the front
+            u32x4_t v = r.v[i];
+            if ((s + 1) * I8_STAGE > g.K)   // the stage that crosses K
+                v = drop_bytes(v, late);
+            buf[(wv * AL + i) * WAVE + lane] = v;
+        }
     };
     acc_t acc[WMF][WNF];
 #pragma unroll
@@ -195,17 +236,15 @@ __global__ __launch_bounds__(WAVE *NWM *NWN *KG) void tile_kernel(const I8Args g
             acc[f][j] = acc_t{0, 0, 0, 0};
     const int fa = (wv / NWN) * WMF, fb = (wv % NWN) * WNF;
     const int nit = (nst + KG - 1) / KG;
-#pragma unroll
-    for (int it = 0; it < NBUF - 1; it++)
-        issue(it);
-    for (int it = 0; it < nit; it++) {
-        // This wave's part of these stages has landed and its reads of the last ones are done; past the
+    auto meet = [&]() {
+        // This wave's part of the next stages has landed and its reads of the last ones are done; past the
         // barrier, every wave's, so that the last ones' buffer can be filled again.
         __builtin_amdgcn_s_waitcnt(vmcnt_lgkm_imm((NBUF - 2) * (AL + BL)));
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        issue(it + NBUF - 1);
+    };
+    auto multiply = [&](int it) {
         const u32x4_t *buf = &lds[(it % NBUF * KG + kg) * STAGE];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
@@ -224,6 +263,38 @@ __global__ __launch_bounds__(WAVE *NWM *NWN *KG) void tile_kernel(const I8Args g
                     acc[f][j] = mfma(b[j], a[f], acc[f][j]);
         }
         asm volatile("" ::: "memory");
+    };
+    if constexpr (ANY) {
+        Rows even{}, odd{};
+        load_x(0, even);
+        issue_w(0);
+        load_x(1, odd);
+        issue_w(1);
+        store_x(0, even);
+        auto iteration = [&](int it, Rows &next, Rows &here) {
+            meet();
+            load_x(it + 2, next);
+            issue_w(it + 2);
+            multiply(it);
+            store_x(it + 1, here);
+        };
+        for (int it = 0; it < nit; it += 2) {
+            iteration(it, even, odd);
+            if (it + 1 < nit)
+                iteration(it + 1, odd, even);
+        }
+    } else {
+#pragma unroll
+        for (int it = 0; it < NBUF - 1; it++) {
+            issue_w(it);
+            issue_x(it);
+        }
+        for (int it = 0; it < nit; it++) {
+            meet();
+            issue_w(it + NBUF - 1);
+            issue_x(it + NBUF - 1);
+            multiply(it);
+        }
     }
     __builtin_amdgcn_s_waitcnt(vmcnt_lgkm_imm(0));   // nothing may land in LDS any more
     if constexpr (KG > 1) {
@@ -517,14 +588,16 @@ hipError_t launch_tile(const I8Args &g, hipStream_t st)
 {
     const int gx = (g.nblk * 16 + BN - 1) / BN, gy = (g.T + BM - 1) / BM;
     const dim3 grid((unsigned)((gx * gy + XCDS - 1) / XCDS * XCDS)), threads(WAVE * NWM * NWN * KG);
-    if (gy == 1)
-        hipLaunchKernelGGL((tile_kernel<BM, BN, NWM, NWN, KG, NBUF, true>), grid, threads, 0, st, g, gx, gy);
+    if (g.direct && gy == 1)
+        hipLaunchKernelGGL((tile_kernel<BM, BN, NWM, NWN, KG, NBUF, true, false>), grid, threads, 0, st, g, gx, gy);
+    else if (g.direct)
+        hipLaunchKernelGGL((tile_kernel<BM, BN, NWM, NWN, KG, NBUF, false, false>), grid, threads, 0, st, g, gx, gy);
+    else if (gy == 1)
+        hipLaunchKernelGGL((tile_kernel<BM, BN, NWM, NWN, KG, 3, true, true>), grid, threads, 0, st, g, gx, gy);
     else
-        hipLaunchKernelGGL((tile_kernel<BM, BN, NWM, NWN, KG, NBUF, false>), grid, threads, 0, st, g, gx, gy);
+        hipLaunchKernelGGL((tile_kernel<BM, BN, NWM, NWN, KG, 3, false, true>), grid, threads, 0, st, g, gx, gy);
     return hipGetLastError();
 }
-
-} // namespace
 
 template <int NF, bool GLU, bool F32>
 hipError_t launch_wide_as(const I8Args &g, hipStream_t st)
@@ -551,6 +624,30 @@ hipError_t launch_wide(const I8Args &g, hipStream_t st)
     return f32 ? launch_wide_as<8, false, true>(g, st) : launch_wide_as<8, false, false>(g, st);
 }
 
+constexpr int64_t FILL = CUS * 3 / 4;
+int64_t tile_count(const I8Args &g, int bm, int bn)
+{
+    return (int64_t)((g.T + bm - 1) / bm) * ((g.nblk * 16 + bn - 1) / bn);
+}
+
+// A round of wide tiles (one per CU) takes about 1.5 times a round of 128 x 128 tiles (two per CU), whatever K;
+// the wide ones come in whole rounds.
+bool wide_preferred(const I8Args &g)
+{
+    const int64_t wide = tile_count(g, 256, 256), small = tile_count(g, 128, 128), round = 2 * CUS;
+    return g.T > 64 && wide >= FILL && (wide + CUS - 1) / CUS * 3 * round <= 2 * (small > round ? small : round);
+}
+
+} // namespace
+
+// Passing rows through registers saves the restaging launch and its pass over x, and costs some of the products'
+// time: 1 x 1000 x 1000 3.8 us against 5.6, 450 x 512 x 1237 5.7 against 7.4, 777 x 1001 x 3583 12.3 against
+// 14.8, 64 x 7168 x 4351 14.0 against 14.3; but 64 x 28672 x 7167 44 against 39.
+bool i8_takes_any_rows(const I8Args &g)
+{
+    return g.K >= 16 && !wide_preferred(g) && (int64_t)g.T * g.nblk * 16 * g.K <= (int64_t)1 << 33;
+}
+
 // The largest tile that still makes FILL workgroups, three quarters of the CUs, else the smallest (16 columns; 32
 // when a gate and an up block have to be together), with the K axis over more groups of waves the
 // smaller the tile. Measured, microseconds (tokens x columns x codes; weights not in any cache), against
@@ -562,10 +659,7 @@ hipError_t launch_wide(const I8Args &g, hipStream_t st)
 // 128 x 64 46; 1024: 128 x 128 62, wide 80; 2048: wide 84, 128 x 128 120.
 hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
 {
-    constexpr int64_t FILL = CUS * 3 / 4;
-    auto tiles = [&](int bm, int bn) {
-        return (int64_t)((g.T + bm - 1) / bm) * ((g.nblk * 16 + bn - 1) / bn);
-    };
+    auto tiles = [&](int bm, int bn) { return tile_count(g, bm, bn); };
     auto fills = [&](int bm, int bn) { return tiles(bm, bn) >= FILL; };
     if (g.T <= 16) {
         if (fills(16, 64))
@@ -575,11 +669,9 @@ hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
         return launch_tile<16, 16, 1, 1, 8, 3>(g, st);
     }
     if (g.T > 64) {
-        // A round of wide tiles (one per CU) takes about 1.5 times a round of 128 x 128 tiles (two per CU),
-        // whatever K; the wide ones come in whole rounds.
-        const int64_t rounds = (tiles(256, 256) + CUS - 1) / CUS, small = tiles(128, 128);
-        if (rounds * 3 * 2 * CUS <= 2 * (small > 2 * CUS ? small : 2 * CUS) && fills(256, 256))
+        if (wide_preferred(g))
             return launch_wide(g, st);
+        const int64_t small = tiles(128, 128);
         if (small > CUS)   // two workgroups per CU share its LDS, or one takes three buffers: 512 tokens 39 us
             return launch_tile<128, 128, 2, 4, 1, 2>(g, st);   // against 53, 1024 tokens 74 against 62
         if (small >= FILL)

@@ -201,6 +201,11 @@ SIZES = [  # T, N, K, pad of x, offset of x: both sides of 16-row and 128-code b
     (63, 200, 1111, 0, 0), (64, 129, 2048, 0, 0), (65, 127, 640, 0, 0), (100, 333, 777, 5, 2), (128, 256, 512, 0, 0),
     (129, 257, 513, 0, 0), (200, 1000, 384, 0, 0), (256, 64, 4352, 0, 0), (300, 520, 96, 0, 0), (777, 1001, 1535, 1, 0),
     (1500, 272, 160, 0, 0), (64, 3000, 7168, 0, 0), (40, 2064, 14336, 0, 0), (513, 515, 130, 0, 0),
+    # rows at odd addresses: through registers (from 16 codes on) in every tile, or restaged
+    (5, 40, 15, 0, 1), (5, 40, 16, 1, 1), (7, 33, 31, 0, 0), (1, 3500, 257, 0, 7), (16, 7000, 143, 0, 0),
+    (16, 13000, 131, 2, 1), (32, 6200, 129, 0, 1), (30, 25000, 100, 3, 0), (64, 6300, 200, 1, 0), (64, 13000, 155, 1, 0),
+    (60, 24600, 130, 1, 0), (130, 5000, 129, 0, 1), (300, 4200, 137, 4, 0), (1000, 4000, 141, 0, 3), (700, 6000, 77, 0, 2),
+    (64, 14336, 9400, 1, 0),
 ]
 
 
