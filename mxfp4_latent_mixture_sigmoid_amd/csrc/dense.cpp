@@ -22,8 +22,8 @@ moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_
 bool valid_type(int32_t t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F32; }
 uintptr_t type_size(int32_t t) { return t == MOE_TYPE_F32 ? 4 : 2; }
 
-// One workgroup per row at most, or one thread per 16 values: grids below 2^31.
-bool rows_fit(int64_t T, int64_t width) { return T * ((width + 15) / 16) / 256 + 1 <= INT32_MAX; }
+// One thread per 16 values, fewer than 2^32 in a launch.
+bool chunks_fit(int64_t rows, int64_t width) { return rows * ((width + 15) / 16) <= (int64_t)UINT32_MAX - 256; }
 
 // A given matrix: rows at least `width` apart, element-aligned.
 bool valid_rows(const void *p, int64_t ld, int64_t width, uintptr_t size) { return p && ld >= width && aligned(p, size); }
@@ -42,13 +42,16 @@ LinearLayout linear_layout(const moe_linear_config *c)
     return L;
 }
 
-// Every index and grid of a product fits its type: packed rows below 2^31, and tiles, and blocks
-// of the packing kernel's grid.
 bool valid_linear(const moe_linear_config *c)
 {
-    if (!c || c->n < 1 || c->k < 1 || (c->glu != 0 && c->glu != 1) || !valid_type(c->out_type))
-        return false;
-    return c->n <= (1 << 26) && i8_row_blocks(c->n, c->glu) * i8_stages(c->k) * 2 * WAVE / 256 < INT32_MAX;
+    return c && c->n >= 1 && c->k >= 1 && (c->glu == 0 || c->glu == 1) && valid_type(c->out_type);
+}
+
+// The sum fits 32 bits, and the packing kernel's launch (a thread per 16 codes) and the packed rows their indexes.
+bool supported_linear(const moe_linear_config *c)
+{
+    const int64_t nblk = i8_row_blocks(c->n, c->glu);
+    return c->k <= MOE_LINEAR_MAX_K && nblk * 16 <= INT32_MAX / 2 && chunks_fit(nblk * 16, i8_stages(c->k) * I8_STAGE);
 }
 
 // Whether the products' direct loads to LDS can take the activations as they are: rows at 16-byte steps from a
@@ -59,12 +62,13 @@ bool direct(const int8_t *x, int64_t ldx, int64_t K) { return aligned(x, 16) && 
 
 int64_t workspace_bytes_for(const moe_linear_config *c, int64_t T) { return align_up(T * i8_stages(c->k) * I8_STAGE); }
 
+// More than a few hundred workgroups come in tiles of 128 x 128 at least, 512 threads each; restaging takes a
+// thread per 16 codes.
+constexpr int64_t XCD_PAD = 8;   // the grid is rounded up to the XCDs
 bool linear_fits(const moe_linear_config *c, int64_t T)
 {
-    // more than a few thousand workgroups come in tiles of 64 x 32 at least; restaging takes one thread per
-    // 16 codes
-    const int64_t tiles = ((T + 63) / 64) * ((i8_row_blocks(c->n, c->glu) + 1) / 2);
-    return tiles + 8 <= INT32_MAX && rows_fit(T, i8_stages(c->k) * I8_STAGE);
+    const int64_t tiles = ((T + 127) / 128) * ((i8_row_blocks(c->n, c->glu) + 7) / 8);
+    return tiles < (UINT32_MAX / 512) - XCD_PAD && chunks_fit(T, i8_stages(c->k) * I8_STAGE);
 }
 
 } // namespace
@@ -73,7 +77,7 @@ extern "C" {
 
 moe_status moe_norm(const moe_norm_args *a, void *stream)
 {
-    if (!a || a->T < 0 || a->H < 1 || !valid_type(a->x_type) || !(a->eps >= 0.f) || !rows_fit(a->T, a->H))
+    if (!a || a->T < 0 || a->H < 1 || !valid_type(a->x_type) || !(a->eps >= 0.f))
         return MOE_ERR_INVALID_ARG;
     if (a->T == 0)
         return MOE_OK;
@@ -91,7 +95,7 @@ moe_status moe_norm(const moe_norm_args *a, void *stream)
 moe_status moe_quantise(const void *x, int32_t x_type, int64_t ldx, int32_t T, int32_t K, int8_t *codes, int64_t ldc,
                         float *scales, void *stream)
 {
-    if (T < 0 || K < 1 || !valid_type(x_type) || !rows_fit(T, K))
+    if (T < 0 || K < 1 || !valid_type(x_type))
         return MOE_ERR_INVALID_ARG;
     if (T == 0)
         return MOE_OK;
@@ -112,7 +116,7 @@ moe_status moe_quantise(const void *x, int32_t x_type, int64_t ldx, int32_t T, i
 moe_status moe_dequantise(const int8_t *codes, int64_t ldc, const float *scales, int32_t T, int32_t K, void *out,
                           int64_t ldo, void *stream)
 {
-    if (T < 0 || K < 1 || !rows_fit(T, K))
+    if (T < 0 || K < 1 || !chunks_fit(T, K))
         return MOE_ERR_INVALID_ARG;
     if (T == 0)
         return MOE_OK;
@@ -124,10 +128,12 @@ moe_status moe_dequantise(const int8_t *codes, int64_t ldc, const float *scales,
 
 moe_status moe_linear_query(const moe_linear_config *cfg, int32_t T_max, size_t *packed_bytes, size_t *workspace_bytes)
 {
-    if (!valid_linear(cfg) || T_max < 0 || !linear_fits(cfg, T_max))
+    if (!valid_linear(cfg) || T_max < 0)
         return MOE_ERR_INVALID_ARG;
-    if (cfg->k > MOE_LINEAR_MAX_K)
+    if (!supported_linear(cfg))
         return MOE_ERR_UNSUPPORTED;
+    if (!linear_fits(cfg, T_max))
+        return MOE_ERR_INVALID_ARG;
     if (packed_bytes)
         *packed_bytes = (size_t)linear_layout(cfg).total;
     if (workspace_bytes)
@@ -142,7 +148,7 @@ moe_status moe_linear_create(const moe_linear_config *cfg, const moe_linear_weig
         *out = nullptr;
     if (!out || !valid_linear(cfg) || !w || !packed || !aligned(packed, 256))
         return MOE_ERR_INVALID_ARG;
-    if (cfg->k > MOE_LINEAR_MAX_K)
+    if (!supported_linear(cfg))
         return MOE_ERR_UNSUPPORTED;
     if (!w->w || !w->scales || !w->w_up != !cfg->glu || !w->scales_up != !cfg->glu || (cfg->glu && w->bias))
         return MOE_ERR_INVALID_ARG;

@@ -42,9 +42,22 @@ __device__ inline u32x4_t drop_bytes(u32x4_t v, int n)
     return __builtin_bit_cast(u32x4_t, n < 16 ? x >> (8 * n) : (unsigned __int128)0);
 }
 
-// Where chunk c (16 codes) of row r of a staged activation tile (rows of I8_STAGE bytes) lies: the
-// operand reads -- 8 or 16 consecutive rows, one chunk -- then fall in distinct banks.
-__device__ inline int swizzle(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+// Chunk c (16 codes) of row r of a staged activation tile (rows of I8_STAGE bytes) lies at chunk c ^ swizzle(r) of
+// that row. The operand read (lane l: row l % 16, chunk c0 + l / 16, c0 even) then falls on distinct chunk
+// places modulo 8, 16 and 32 in every group of 8, 16 and 32 consecutive lanes.
+__host__ __device__ constexpr int swizzle(int r) { return (((r >> 2) ^ (r << 1 & 2)) & 3) << 1 | (r >> 1 & 1); }
+constexpr bool swizzle_spreads(int lanes)
+{
+    for (int first = 0; first < 64; first += lanes)
+        for (int a = first; a < first + lanes; a++)
+            for (int b = a + 1; b < first + lanes; b++) {
+                const int pa = a % 16 * 8 + (a / 16 ^ swizzle(a % 16)), pb = b % 16 * 8 + (b / 16 ^ swizzle(b % 16));
+                if (pa % lanes == pb % lanes)
+                    return false;
+            }
+    return true;
+}
+static_assert(swizzle_spreads(8) && swizzle_spreads(16) && swizzle_spreads(32), "bank conflicts");
 
 // Linear workgroup id -> (column tile, row tile): each XCD takes a contiguous run of the items, which go
 // in groups of GROUP_M row tiles, so that the workgroups sharing one L2 share operands. False past the end.

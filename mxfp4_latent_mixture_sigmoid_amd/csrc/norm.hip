@@ -381,11 +381,33 @@ hipError_t launch_rows(const moe_norm_args &a, hipStream_t st)
 
 } // namespace
 
-hipError_t launch_norm(const moe_norm_args &a, bool norm, hipStream_t st)
+// A launch has fewer than 2^32 threads: more rows go in several launches.
+constexpr int MAX_ROWS = 1 << 21;
+
+hipError_t launch_norm(const moe_norm_args &all, bool norm, hipStream_t st)
 {
-    if (a.x_type == MOE_TYPE_F32)
-        return norm ? launch_rows<float, true>(a, st) : launch_rows<float, false>(a, st);
-    return norm ? launch_rows<uint16_t, true>(a, st) : launch_rows<uint16_t, false>(a, st);
+    const int size = all.x_type == MOE_TYPE_F32 ? 4 : 2;
+    auto from = [](auto p, int64_t bytes) {   // null stays null
+        return p ? reinterpret_cast<decltype(p)>(reinterpret_cast<uintptr_t>(p) + bytes) : p;
+    };
+    for (int64_t r = 0; r < all.T; r += MAX_ROWS) {
+        moe_norm_args a = all;
+        a.T = (int32_t)(all.T - r < MAX_ROWS ? all.T - r : MAX_ROWS);
+        a.x = from(all.x, r * all.ldx * size);
+        a.delta = from(all.delta, r * all.ldd * 2);
+        a.sum = from(all.sum, r * all.lds * size);
+        a.out = from(all.out, r * all.ldo * 2);
+        a.codes = from(all.codes, r * all.ldc);
+        a.scales = from(all.scales, r * 4);
+        hipError_t e;
+        if (a.x_type == MOE_TYPE_F32)
+            e = norm ? launch_rows<float, true>(a, st) : launch_rows<float, false>(a, st);
+        else
+            e = norm ? launch_rows<uint16_t, true>(a, st) : launch_rows<uint16_t, false>(a, st);
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_dequantise(const int8_t *codes, int64_t ldc, const float *scales, int32_t T, int32_t K, uint16_t *out,

@@ -182,20 +182,21 @@ class Int8Linear:
               up_scales)
 
     def _create(self, codes, scales, bias, up_codes, up_scales, index, stream):
+        codes = codes.contiguous()   # weights may be views in any order
         _rows("codes", codes, _INT8, index)
         self.N, self.K = codes.shape
         _vector("scales", scales, self.N, torch.float32, index)
         if up_codes is not None:
+            up_codes = up_codes.contiguous()
             _rows("up_codes", up_codes, _INT8, index, codes.shape)
             _vector("up_scales", up_scales, self.N, torch.float32, index)
-            up_codes = up_codes.contiguous()
         if bias is not None:
             _vector("bias", bias, self.N, torch.float32, index)
         self.cfg = abi.LinearConfig(self.N, self.K, int(up_codes is not None), _TYPES[self.out_dtype])
         packed_bytes, ws_bytes = abi.linear_query(self.cfg, self.T_max)
         self.packed = torch.empty(packed_bytes, dtype=torch.uint8, device=codes.device)
         self.workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=codes.device)
-        self.handle = abi.linear_create(self.cfg, codes.contiguous(), scales, up_codes, up_scales, bias, self.packed, stream)
+        self.handle = abi.linear_create(self.cfg, codes, scales, up_codes, up_scales, bias, self.packed, stream)
         self._buffers = self.workspace.data_ptr(), self.workspace.numel()
 
     def forward(self, x, scales, out=None, stream=None):

@@ -46,8 +46,7 @@ def test_packed_norm_arguments_are_the_structure():
     dict(T=-1), dict(H=0), dict(x_type=2), dict(eps=-1.0), dict(eps=float("nan")), dict(x=None), dict(out=None),
     dict(ldx=63), dict(ldo=63), dict(x=A + 1), dict(out=A + 1), dict(codes=A), dict(scales=A), dict(codes=A, scales=A + 2),
     dict(codes=A, scales=A, ldc=63), dict(delta=A, ldd=63), dict(delta=A + 1), dict(weight=A + 1), dict(sum=A, lds=65),
-    dict(sum=A + 2, lds=63), dict(x_type=abi.TYPE_F32, x=A + 2), dict(x_type=abi.TYPE_F32, sum=A + 2),
-    dict(T=2 ** 31 - 1, H=2 ** 31 - 1, ldx=2 ** 31, ldo=2 ** 31)])
+    dict(sum=A + 2, lds=63), dict(x_type=abi.TYPE_F32, x=A + 2), dict(x_type=abi.TYPE_F32, sum=A + 2)])
 def test_norm_refuses(kw):
     assert _norm(**kw) == BAD
 
@@ -90,7 +89,7 @@ def _cfg(n=64, k=64, glu=0, out_type=0):
     return abi.LinearConfig(n, k, glu, out_type)
 
 
-@pytest.mark.parametrize("kw", [dict(n=0), dict(k=0), dict(n=-1), dict(glu=2), dict(out_type=2), dict(n=2 ** 27)])
+@pytest.mark.parametrize("kw", [dict(n=0), dict(k=0), dict(n=-1), dict(glu=2), dict(out_type=2)])
 def test_linear_refuses_configs(kw):
     c = _cfg(**kw)
     assert abi.lib().moe_linear_query(ctypes.byref(c), 1, None, None) == BAD
@@ -106,7 +105,13 @@ def test_linear_sum_limit_and_token_limits():
     assert L.moe_linear_query(ctypes.byref(_cfg(k=abi.LINEAR_MAX_K + 1)), 1, None, None) == UNSUPPORTED
     assert abi.LINEAR_MAX_K * 128 * 128 < 2 ** 31 <= (abi.LINEAR_MAX_K + 1) * 128 * 128
     assert L.moe_linear_query(ctypes.byref(_cfg()), -1, None, None) == BAD
-    assert L.moe_linear_query(ctypes.byref(_cfg(n=2 ** 26)), 2 ** 31 - 1, None, None) == BAD
+    # more than 2^32 threads: 128 x 128 tiles of 512, packing or restaging 16 codes each
+    assert L.moe_linear_query(ctypes.byref(_cfg(n=2 ** 16)), 2 ** 20, None, None) == abi.Status.OK
+    assert L.moe_linear_query(ctypes.byref(_cfg(n=2 ** 16)), 2 ** 22, None, None) == BAD
+    assert L.moe_linear_query(ctypes.byref(_cfg(n=1, k=1)), 2 ** 31 - 1, None, None) == BAD
+    assert L.moe_linear_query(ctypes.byref(_cfg(n=2 ** 20, k=2 ** 17 - 1)), 1, None, None) == UNSUPPORTED
+    assert L.moe_linear_query(ctypes.byref(_cfg(n=2 ** 31 - 1)), 1, None, None) == UNSUPPORTED
+    assert L.moe_dequantise(A, 2 ** 16, A, 2 ** 22, 2 ** 16, A, 2 ** 16, None) == BAD
 
 
 @pytest.mark.parametrize("n,k,glu", [(1, 1, 0), (16, 128, 0), (17, 129, 0), (100, 1000, 1), (7168, 4352, 0)])

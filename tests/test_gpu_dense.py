@@ -321,6 +321,22 @@ def test_outputs_past_32_bit_offsets():
     R.check(f64(total[pick]), y2, np.abs(y2) * (R.B + R.NORM_REL), "norm")
 
 
+def test_more_rows_than_one_launch_takes():
+    from mxfp4_latent_mixture_sigmoid_amd import dequantise, quantise, rms_norm
+    T, H = 2 ** 21 + 5, 40
+    g = gen(12)
+    x = torch.randn(997, H, generator=g).bfloat16().cuda().repeat(T // 997 + 1, 1)[:T]
+    pick = [0, 996, 2 ** 21 - 1, 2 ** 21, T - 1]
+    r = rms_norm(x, delta=x, sum=True, codes=True)
+    s, y = R.norm(2 * f64(x[pick]), None, None, float(np.float32(1e-6)))
+    R.check(f64(r.sum[pick]), s, np.abs(s) * R.B, "sum")
+    R.check(f64(r.out[pick]), y, np.abs(y) * (R.B + R.NORM_REL), "out")
+    R.check_codes(r.codes[pick].cpu().numpy(), f64(r.scales[pick]), y, R.NORM_REL, "codes")
+    codes, scales = quantise(x)
+    assert torch.equal(codes[997:], codes[:-997]) and torch.equal(scales[997:], scales[:-997])
+    assert torch.equal(dequantise(codes[:997], scales[:997]), dequantise(codes, scales)[:997])
+
+
 def block(H, I, T_max, g):
     from mxfp4_latent_mixture_sigmoid_amd import Int8FeedForward
     mat = lambda n, k: (torch.randint(-127, 128, (n, k), generator=g, dtype=torch.int8).cuda(),      # noqa: E731
@@ -412,6 +428,29 @@ def test_smaller_calls_of_a_larger_layer():
     ref, err = reference(x.cpu().numpy(), f64(sx), w, s, None, True)
     for t in (150, 1, 64, 65, 16, 17, 149, 33):
         R.check(f64(layer.forward(x[:t], sx[:t])), ref[:t], err[:t], f"T={t}")
+
+
+def test_views_and_weights_in_any_order():
+    """Activations and outputs that are columns of wider buffers, single rows with arbitrary strides,
+    weights that are transposed views: the bits of contiguous ones."""
+    from mxfp4_latent_mixture_sigmoid_amd import Int8Linear, quantise, rms_norm
+    g = gen(21)
+    w = torch.randint(-128, 128, (96, 320), generator=g, dtype=torch.int8).cuda()
+    s = torch.rand(96, generator=g).cuda()
+    a = Int8Linear(w, s, T_max=40)
+    b = Int8Linear(w.t().contiguous().t(), s, T_max=40)
+    big = torch.randint(-128, 128, (40, 400), generator=g, dtype=torch.int8).cuda()
+    sx = torch.rand(40, generator=g).cuda()
+    want = a.forward(big[:, 37:357].contiguous(), sx)
+    wide = torch.zeros(40, 300, dtype=BF16, device="cuda")
+    assert b.forward(big[:, 37:357], sx, out=wide[:, 100:196]) is not None
+    assert torch.equal(wide[:, 100:196], want) and not wide[:, :100].any() and not wide[:, 196:].any()
+    one = big[7:8, 37:357]
+    assert torch.equal(a.forward(one, sx[7:8]), want[7:8])
+    assert torch.equal(a.forward(one.as_strided((1, 320), (1, 1), one.storage_offset()), sx[7:8]), want[7:8])
+    x = torch.randn(40, 400, generator=g).bfloat16().cuda()
+    for f in (lambda t: rms_norm(t).out, lambda t: quantise(t)[0], lambda t: quantise(t)[1]):
+        assert torch.equal(f(x[::2, 3:333]), f(x[::2, 3:333].contiguous()))
 
 
 def test_python_refusals():
