@@ -116,7 +116,7 @@ moe_status moe_quantise(const void *x, int32_t x_type, int64_t ldx, int32_t T, i
 moe_status moe_dequantise(const int8_t *codes, int64_t ldc, const float *scales, int32_t T, int32_t K, void *out,
                           int64_t ldo, void *stream)
 {
-    if (T < 0 || K < 1 || !chunks_fit(T, K))
+    if (T < 0 || K < 1)
         return MOE_ERR_INVALID_ARG;
     if (T == 0)
         return MOE_OK;

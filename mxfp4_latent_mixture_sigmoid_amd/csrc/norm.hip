@@ -35,22 +35,30 @@ __device__ inline void store_streamed(void *p, const T &v)
     __builtin_nontemporal_store(v, static_cast<Any *>(p));
 }
 
-// CHUNK values from column c on of a row of n values (zeros past n), as FP32.
-__device__ inline void load_row(const uint16_t *row, int c, int n, float *v)
+// CHUNK BF16 values from column c on of a row of n values (zeros past n).
+__device__ inline u32x4_t load_bf16(const uint16_t *row, int c, int n)
 {
-    if (c + CHUNK <= n) {
-        const u32x4_t r = load_any<u32x4_t>(row + c);
+    if (c + CHUNK <= n)
+        return load_any<u32x4_t>(row + c);
+    u32x4_t r;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            v[2 * i] = __uint_as_float(r[i] << 16);
-            v[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
-        }
-    } else {
+    for (int i = 0; i < 4; i++) {
+        const uint32_t lo = c + 2 * i < n ? row[c + 2 * i] : 0, hi = c + 2 * i + 1 < n ? row[c + 2 * i + 1] : 0;
+        r[i] = lo | hi << 16;
+    }
+    return r;
+}
+__device__ inline void unpack(u32x4_t r, float *v)
+{
 #pragma unroll
-        for (int i = 0; i < CHUNK; i++)
-            v[i] = c + i < n ? bf16_bits_to_f32(row[c + i]) : 0.f;
+    for (int i = 0; i < 4; i++) {
+        v[2 * i] = __uint_as_float(r[i] << 16);
+        v[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
     }
 }
+
+// The same as FP32, of either type.
+__device__ inline void load_row(const uint16_t *row, int c, int n, float *v) { unpack(load_bf16(row, c, n), v); }
 __device__ inline void load_row(const float *row, int c, int n, float *v)
 {
     if (c + CHUNK <= n) {
@@ -185,6 +193,11 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_kernel(const moe_nor
     for (int i = 0; i < NV; i++)
         load_row(x, (t + i * NT) * CHUNK, a.H, v[i]);
     if constexpr (NORM) {
+        u32x4_t weight[NV];   // loaded before anything waits or is stored
+        if (a.weight)
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                weight[i] = load_bf16(static_cast<const uint16_t *>(a.weight), (t + i * NT) * CHUNK, a.H);
         if (a.delta) {
             const uint16_t *d = static_cast<const uint16_t *>(a.delta) + r * a.ldd;
 #pragma unroll
@@ -213,7 +226,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_kernel(const moe_nor
         for (int i = 0; i < NV; i++) {
             float w[CHUNK];
             if (a.weight)
-                load_row(static_cast<const uint16_t *>(a.weight), (t + i * NT) * CHUNK, a.H, w);
+                unpack(weight[i], w);
 #pragma unroll
             for (int j = 0; j < CHUNK; j++)
                 v[i][j] = a.weight ? v[i][j] * rstd * w[j] : v[i][j] * rstd;
@@ -325,31 +338,41 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const moe_norm_args a)
     }
 }
 
-// 16 codes per thread.
+// One chunk of a row per thread.
 __global__ __launch_bounds__(256) void dequantise_kernel(const int8_t *codes, int64_t ldc, const float *scales, int K,
-                                                         int64_t chunks, int64_t total, uint16_t *out, int64_t ldo)
+                                                         uint32_t chunks, uint32_t total, uint16_t *out, int64_t ldo)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x;
     if (i >= total)
         return;
     const int64_t r = i / chunks;
-    const int c = (int)(i % chunks) * 16;
+    const int c = (int)(i % chunks) * CHUNK;
     const int8_t *q = codes + r * ldc + c;
-    uint16_t *o = out + r * ldo + c;
     const float s = scales[r];
-    if (c + 16 <= K) {
-        const u32x4_t v = load_any<u32x4_t>(q);
-        u32x4_t w[2];
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const uint32_t word = v[j / 2] >> (16 * (j % 2));
-            w[j / 4][j % 4] = pack_bf16x2((float)(int8_t)word * s, (float)(int8_t)(word >> 8) * s);
-        }
-        store_any(o, w[0]);
-        store_any(o + 8, w[1]);
+    uint2 w{0u, 0u};
+    if (c + CHUNK <= K) {
+        w = load_any<uint2>(q);
     } else {
-        for (int j = 0; c + j < K; j++)
-            o[j] = (uint16_t)f32_to_bf16_bits((float)q[j] * s);
+#pragma unroll
+        for (int j = 0; j < CHUNK; j++) {
+            const uint32_t b = c + j < K ? (uint8_t)q[j] : 0u;
+            (j < 4 ? w.x : w.y) |= b << (8 * (j % 4));
+        }
+    }
+    u32x4_t v;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const uint32_t pair = (j < 2 ? w.x : w.y) >> (16 * (j % 2));
+        v[j] = pack_bf16x2((float)(int8_t)pair * s, (float)(int8_t)(pair >> 8) * s);
+    }
+    uint16_t *o = out + r * ldo + c;
+    if (c + CHUNK <= K) {
+        store_any(o, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < CHUNK; j++)
+            if (c + j < K)
+                o[j] = (uint16_t)(v[j / 2] >> (16 * (j % 2)));
     }
 }
 
@@ -383,6 +406,7 @@ hipError_t launch_rows(const moe_norm_args &a, hipStream_t st)
 
 // A launch has fewer than 2^32 threads: more rows go in several launches.
 constexpr int MAX_ROWS = 1 << 21;
+constexpr int64_t MAX_THREADS = (int64_t)1 << 31;
 
 hipError_t launch_norm(const moe_norm_args &all, bool norm, hipStream_t st)
 {
@@ -413,10 +437,16 @@ hipError_t launch_norm(const moe_norm_args &all, bool norm, hipStream_t st)
 hipError_t launch_dequantise(const int8_t *codes, int64_t ldc, const float *scales, int32_t T, int32_t K, uint16_t *out,
                              int64_t ldo, hipStream_t st)
 {
-    const int64_t chunks = (K + 15) / 16, total = T * chunks;
-    hipLaunchKernelGGL(dequantise_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st, codes, ldc, scales, K,
-                       chunks, total, out, ldo);
-    return hipGetLastError();
+    const int64_t chunks = (K + CHUNK - 1) / CHUNK, rows = MAX_THREADS / chunks;
+    for (int64_t r = 0; r < T; r += rows) {
+        const int64_t total = (T - r < rows ? T - r : rows) * chunks;
+        hipLaunchKernelGGL(dequantise_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st, codes + r * ldc, ldc,
+                           scales + r, K, (uint32_t)chunks, (uint32_t)total, out + r * ldo, ldo);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 } // namespace mxmoe

@@ -111,7 +111,6 @@ def test_linear_sum_limit_and_token_limits():
     assert L.moe_linear_query(ctypes.byref(_cfg(n=1, k=1)), 2 ** 31 - 1, None, None) == BAD
     assert L.moe_linear_query(ctypes.byref(_cfg(n=2 ** 20, k=2 ** 17 - 1)), 1, None, None) == UNSUPPORTED
     assert L.moe_linear_query(ctypes.byref(_cfg(n=2 ** 31 - 1)), 1, None, None) == UNSUPPORTED
-    assert L.moe_dequantise(A, 2 ** 16, A, 2 ** 22, 2 ** 16, A, 2 ** 16, None) == BAD
 
 
 @pytest.mark.parametrize("n,k,glu", [(1, 1, 0), (16, 128, 0), (17, 129, 0), (100, 1000, 1), (7168, 4352, 0)])
