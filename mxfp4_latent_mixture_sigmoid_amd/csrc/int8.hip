@@ -124,12 +124,21 @@ __device__ inline void store16(const I8Args &g, int r, int n, u32x4_t v)
     }
 }
 
-// g / (1 + exp(-g)) on the hardware's exponential and reciprocal, each within a unit in the last place: the
-// exponent's rounding costs |g| 2^-24 relative, far below the output's BF16 (and a few units of FP32).
-// exp overflows to infinity, whose reciprocal is 0.
-__device__ inline float silu(float g)
+// An output from its exact sum, and from those of gate and up. Every kernel computes them by these steps,
+// each rounded to FP32 (no contraction), so that a token's outputs are the same bits in any batch.
+__device__ inline float scaled(int32_t sum, float sx, float sw, float bias)
 {
-    return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * g));
+#pragma clang fp contract(off)
+    return (float)sum * sx * sw + bias;
+}
+// g / (1 + exp(-g)) is taken on the hardware's exponential and reciprocal, each within a unit in the last
+// place: the exponent's rounding costs |g| 2^-24 relative, far below the output's BF16 (and a few units of
+// FP32). exp overflows to infinity, whose reciprocal is 0.
+__device__ inline float gated(int32_t gate, int32_t up, float sx, float sg, float su)
+{
+#pragma clang fp contract(off)
+    const float g = (float)gate * sx * sg, u = (float)up * sx * su;
+    return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * g)) * u;
 }
 
 // Outputs of one fragment of row block nb (a gate block with its up block's sums in `up` when glu), token
@@ -142,21 +151,15 @@ __device__ inline void emit(const I8Args &g, int r, float sx, int nb, acc_t sum,
     if (n >= g.N)
         return;
     const f32x4_t sw = *reinterpret_cast<const f32x4_t *>(g.sw + nb * 16 + 4 * q);
+    f32x4_t other{0.f, 0.f, 0.f, 0.f};   // the up scales, or the bias
+    if (g.glu)
+        other = *reinterpret_cast<const f32x4_t *>(g.sw + nb * 16 + 16 + 4 * q);
+    else if (g.bias)
+        other = *reinterpret_cast<const f32x4_t *>(g.bias + n);
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; i++)
-        v[i] = (float)sum[i] * sx * sw[i];
-    if (g.glu) {
-        const f32x4_t su = *reinterpret_cast<const f32x4_t *>(g.sw + nb * 16 + 16 + 4 * q);
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            v[i] = silu(v[i]) * ((float)up[i] * sx * su[i]);
-    } else if (g.bias) {
-        const f32x4_t b = *reinterpret_cast<const f32x4_t *>(g.bias + n);
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            v[i] += b[i];
-    }
+        v[i] = g.glu ? gated(sum[i], up[i], sx, sw[i], other[i]) : scaled(sum[i], sx, sw[i], other[i]);
     store4(g, r, n, v);
 }
 
@@ -551,10 +554,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 #pragma unroll
             for (int e = 0; e < 4; e++) {
                 if constexpr (GLU)
-                    v[e] = silu((float)acc[f][2 * j][e] * sx[f] * sw[j][e]) *
-                           ((float)acc[f][2 * j + 1][e] * sx[f] * other[j][e]);
+                    v[e] = gated(acc[f][2 * j][e], acc[f][2 * j + 1][e], sx[f], sw[j][e], other[j][e]);
                 else
-                    v[e] = (float)acc[f][j][e] * sx[f] * sw[j][e] + other[j][e];
+                    v[e] = scaled(acc[f][j][e], sx[f], sw[j][e], other[j][e]);
             }
             if constexpr (F32)
                 *reinterpret_cast<f32x4_t *>(at + j * 64) = v;

@@ -430,6 +430,23 @@ def test_smaller_calls_of_a_larger_layer():
         R.check(f64(layer.forward(x[:t], sx[:t])), ref[:t], err[:t], f"T={t}")
 
 
+@pytest.mark.parametrize("N,K,glu,out_dtype", [(7168, 400, 0, BF16), (7168, 272, 0, F32), (3584, 640, 1, BF16),
+                                               (3601, 130, 1, F32), (300, 4000, 0, F32), (6200, 257, 0, F32)])
+def test_a_token_in_any_batch(N, K, glu, out_dtype):
+    """A token's outputs are the same bits whatever batch, tile and row address it comes with."""
+    g = gen(N)
+    layer, *_ = make(N, K, glu, g, bias=not glu, T_max=2304, out_dtype=out_dtype)
+    x, sx = codes_rows(2304, K, g), (torch.rand(2304, generator=g) - 0.5).cuda()
+    whole = layer.forward(x, sx)
+    apart = codes_rows(1200, K, g, pad=3, offset=1)
+    for first, T in ((0, 1), (5, 7), (100, 16), (33, 17), (800, 33), (64, 64), (7, 100), (1000, 129), (50, 300),
+                     (11, 520), (0, 1100), (1200, 1104)):
+        assert torch.equal(layer.forward(x[first:first + T], sx[first:first + T]), whole[first:first + T]), T
+        if T <= 1200:
+            apart[:T].copy_(x[first:first + T])
+            assert torch.equal(layer.forward(apart[:T], sx[first:first + T]), whole[first:first + T]), (T, "unaligned")
+
+
 def test_views_and_weights_in_any_order():
     """Activations and outputs that are columns of wider buffers, single rows with arbitrary strides,
     weights that are transposed views: the bits of contiguous ones."""
