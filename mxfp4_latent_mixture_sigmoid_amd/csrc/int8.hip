@@ -355,8 +355,8 @@ __global__ __launch_bounds__(WAVE *NWM *NWN *KG) void tile_kernel(const I8Args g
     }
 }
 
-// Many tokens, where the time is the matrix cores': 256 tokens x 256 packed columns by four waves of 128 x
-// 128, one per SIMD. Per 64 codes a wave multiplies for 1024 clocks (64 instructions) and reads 16 KiB of
+// Many tokens, where the time is the matrix cores': the largest tile, 256 tokens x 256 packed columns, by four waves
+// of 128 x 128, one per SIMD. Per 64 codes a wave multiplies for 1024 clocks (64 instructions) and reads 16 KiB of
 // operands, so the LDS is busy 512 clocks with all reads and 256 with the loads' writes; eight waves of 128
 // x 64 would read 1.5 times as much and leave the LDS no slack. A wave reads the operands of the next half
 // stage, and issues the loads, between the instructions that multiply the current one. The 160 KiB of LDS hold three 128-code stages of activations (whole
@@ -389,15 +389,16 @@ __device__ inline void settle(acc_t (&acc)[MF][NF])
             asm volatile("" : "+a"(acc[f][j]));   // no copy of a sum moves across
 }
 
-// NF: column fragments per wave. With 7 of them a tile has 224 columns (and loads, but does not use, the
-// two row blocks after its own), which can fill the last round of workgroups better.
-template <int NF, bool GLU, bool F32>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void wide_kernel(const I8Args g, int gx, int gy)
+// MF and NF: row and column fragments per wave; tiles of 32 MF x 32 NF. 128-token tiles take 80 KiB of LDS or
+// less and half the registers, so that two workgroups share a CU. With 7 column fragments a tile loads, but
+// does not use, the two row blocks after its own.
+template <int MF, int NF, bool GLU, bool F32>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(MF == 8 ? 1 : 2)))
+void wide_kernel(const I8Args g, int gx, int gy)
 {
-    constexpr int BM = 256, BN = 256, MF = 8;                       // MF x NF fragments of 16 x 16 per wave
+    constexpr int BM = 32 * MF, BN = (NF + 1) / 2 * 64;             // MF x NF fragments of 16 x 16 per wave
     constexpr int ASLOT = BM * 8, BSLOT = BN * 4, NA = 3, NB = 4;   // 16-byte slots per stage / half; how many
     constexpr int AL = BM / 8 / 4, BL = BN / 16 / 4;                // loads per wave per stage / half
-    static_assert(AL == 2 * BL, "loads alternate");
     __shared__ u32x4_t lds[NA * ASLOT + NB * BSLOT];
     const int lane = threadIdx.x & (WAVE - 1);
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
@@ -428,15 +429,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         load_lds(wt + at, bytes, (wv * BL + i) * I8_STAGE_BYTES + lane * 16,
                  &lds[NA * ASLOT + hs % NB * BSLOT + (wv * BL + i) * WAVE]);
     };
-    // The loads issued while half hs multiplies, i = 0..7: the weights of half hs + 4 and one half of those of a stage
+    // The loads issued while half hs multiplies: the weights of half hs + 4 and one half of those of a stage
     // of activations, whose slots every wave has left. As many in every half, so that the wait for the next
     // half's data is always for all but the last two halves' loads.
     constexpr int PER = AL / 2 + BL;
     auto load = [&](int hs, int i) {
-        if (i % 2)
-            load_b(hs + 4, i / 2);
+        if (i < BL)
+            load_b(hs + 4, i);
         else
-            load_a((hs + 5) / 2, hs % 2 ? i / 2 : AL / 2 + i / 2);
+            load_a((hs + 5) / 2, i - BL + (hs % 2 ? 0 : AL / 2));
     };
     const int fa = wv / 2 * MF, fb = wv % 2 * NF;   // this wave's first fragments
     const int r16 = lane & 15, ar = (fa * 16 + r16) * 8, ac = (lane >> 4) ^ swizzle(r16);
@@ -461,22 +462,21 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // the end, right before the wait for them. Rows of fragments are walked back and forth, so that
     // consecutive instructions share an operand.
     auto half = [&](const Operands &now, int hs, Operands &next) {
+        constexpr int ALL = MF * NF, READS = MF + NF;
 #pragma unroll
-        for (int i = 0; i < 2 * NF; i++) {
+        for (int x = 0; x < ALL; x++) {
+            const int j = x / MF, f = j % 2 ? MF - 1 - x % MF : x % MF;
+            mfma_acc(now.b[j], now.a[f], acc[f][j]);
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const int j = i / 2, m = i % 2 * 4 + q, f = j % 2 ? MF - 1 - m : m;
-                mfma_acc(now.b[j], now.a[f], acc[f][j]);
-                if (q == 1 && i < MF + NF)
+            for (int i = 0; i < READS; i++)
+                if (x == i * ALL / READS + 1)
                     read(hs + 1, i, next);
-                if (q == 2 && i + 2 * NF < MF + NF)
-                    read(hs + 1, i + 2 * NF, next);
-            }
-            if (i % 2)
-                load(hs, i / 2);
-            if (2 * NF < 2 * PER && i == 0)
-                load(hs, PER - 1);
-            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < PER; i++)
+                if (x == i * ALL / PER + 1)
+                    load(hs, i);
+            if (x % 4 == 3)
+                __builtin_amdgcn_sched_barrier(0);
         }
     };
     auto meet = [&](auto ahead) {   // all but the last loads have landed and this wave's reads are done; then every wave's
@@ -640,29 +640,23 @@ hipError_t launch_tile(const I8Args &g, hipStream_t st)
     return hipGetLastError();
 }
 
-template <int NF, bool GLU, bool F32>
-hipError_t launch_wide_as(const I8Args &g, hipStream_t st)
-{
-    const int gx = (g.nblk + 2 * NF - 1) / (2 * NF), gy = (g.T + 255) / 256;
-    hipLaunchKernelGGL((wide_kernel<NF, GLU, F32>), dim3((unsigned)((gx * gy + XCDS - 1) / XCDS * XCDS)), dim3(256), 0, st,
-                       g, gx, gy);
-    return hipGetLastError();
-}
-
-// 224 columns where whole rounds of tiles over the CUs cost less with them than with 256: 8192 x 7168 outputs
-// are 4 rounds of 7 / 8 of a tile against 3.5 (so 4) of whole ones.
+template <int MF, int NF>
 hipError_t launch_wide(const I8Args &g, hipStream_t st)
 {
+    const int gx = (g.nblk + 2 * NF - 1) / (2 * NF), gy = (g.T + 32 * MF - 1) / (32 * MF);
+    const dim3 grid((unsigned)((gx * gy + XCDS - 1) / XCDS * XCDS)), threads(256);
     const bool f32 = g.out_type == MOE_TYPE_F32;
-    if (g.glu)
-        return f32 ? launch_wide_as<8, true, true>(g, st) : launch_wide_as<8, true, false>(g, st);
-    auto cost = [&](int nf) {
-        const int64_t tiles = (int64_t)((g.T + 255) / 256) * ((g.nblk + 2 * nf - 1) / (2 * nf));
-        return (tiles + CUS - 1) / CUS * nf;
-    };
-    if (cost(7) < cost(8))
-        return f32 ? launch_wide_as<7, false, true>(g, st) : launch_wide_as<7, false, false>(g, st);
-    return f32 ? launch_wide_as<8, false, true>(g, st) : launch_wide_as<8, false, false>(g, st);
+    if constexpr (NF % 2 == 0) {
+        if (g.glu && f32)
+            hipLaunchKernelGGL((wide_kernel<MF, NF, true, true>), grid, threads, 0, st, g, gx, gy);
+        else if (g.glu)
+            hipLaunchKernelGGL((wide_kernel<MF, NF, true, false>), grid, threads, 0, st, g, gx, gy);
+    }
+    if (!g.glu && f32)
+        hipLaunchKernelGGL((wide_kernel<MF, NF, false, true>), grid, threads, 0, st, g, gx, gy);
+    else if (!g.glu)
+        hipLaunchKernelGGL((wide_kernel<MF, NF, false, false>), grid, threads, 0, st, g, gx, gy);
+    return hipGetLastError();
 }
 
 constexpr int64_t FILL = CUS * 3 / 4;
@@ -671,37 +665,61 @@ int64_t tile_count(const I8Args &g, int bm, int bn)
     return (int64_t)((g.T + bm - 1) / bm) * ((g.nblk * 16 + bn - 1) / bn);
 }
 
-// A round of wide tiles (one per CU) takes about 1.5 times a round of 128 x 128 tiles (two per CU), whatever K;
-// the wide ones come in whole rounds.
-bool wide_preferred(const I8Args &g)
+// Many tokens: at least FILL tiles of 128 x 64.
+bool many(const I8Args &g) { return g.T > 64 && tile_count(g, 128, 64) >= FILL; }
+
+// Tiles for many tokens. 128 x 64 until there are FILL tiles of 128 x 128; then the shape with the least estimated time
+// among those of FILL tiles. A round of tiles over the CUs costs its K loop and a start and end worth some
+// codes more; measured, a round of 256 x 256 takes 10.3 ns x (K + 1000), of 256 x 224 9.4 ns x (K + 1400), of 256 x
+// 128 6.1 ns x (K + 800). Two 128 x 128 workgroups share a CU and overlap, so their rounds need not be whole: 7.6
+// ns x (K + 550) for 2 per CU. Microseconds, 7168 x 7168 weights, 256 x 256 / 256 x 128 / 128 x 128 / 128 x 64:
+// 256 tokens - / - / 36 / 29; 512 - / 50 / 36 / 45; 1024 78 / 53 / 60 / 80; 2048 82 / 101 / 113 / -. 2000 x 7000
+// outputs: 512 codes 18.9 / 20.3 / 17.3 / 20.3, 2048 codes 33.5 / 40.6 / 40.2 / 48. 8192 x 7168 outputs are 4 rounds
+// of 224 columns and 3.5, so 4, of 256: 605 against 619 with 14336 codes.
+hipError_t launch_many(const I8Args &g, hipStream_t st)
 {
-    const int64_t wide = tile_count(g, 256, 256), small = tile_count(g, 128, 128), round = 2 * CUS;
-    return g.T > 64 && wide >= FILL && (wide + CUS - 1) / CUS * 3 * round <= 2 * (small > round ? small : round);
+    const int64_t pairs = 2 * CUS, small = tile_count(g, 128, 128);
+    if (small < FILL)
+        return launch_wide<4, 2>(g, st);
+    auto cost = [&](int bm, int bn, int64_t rate, int64_t extra) {
+        const int64_t n = tile_count(g, bm, bn);
+        return n < FILL ? INT64_MAX : (n + CUS - 1) / CUS * rate * (g.K + extra);
+    };
+    const int64_t c256 = cost(256, 256, 103, 1000), c128 = cost(256, 128, 61, 800);
+    const int64_t c224 = g.glu ? INT64_MAX : cost(256, 224, 94, 1400); // 7 would part a gate from its up block
+    const int64_t cpair = (small > pairs * 7 / 8 ? small : pairs * 7 / 8) * 76 * (g.K + 550) / pairs;
+    if (cpair <= c128 && cpair <= c256 && cpair <= c224)
+        return launch_wide<4, 4>(g, st);
+    if (c128 <= c256 && c128 <= c224)
+        return launch_wide<8, 4>(g, st);
+    return c224 < c256 ? launch_wide<8, 7>(g, st) : launch_wide<8, 8>(g, st);
 }
 
 } // namespace
 
-// Passing rows through registers saves the restaging launch and its pass over x, and costs some of the products'
+// Passing rows through registers saves the restaging launch and its pass over x, and costs some of the product's
 // time: 1 x 1000 x 1000 3.8 us against 5.6, 450 x 512 x 1237 5.7 against 7.4, 777 x 1001 x 3583 12.3 against
-// 14.8, 64 x 7168 x 4351 14.0 against 14.3; but 64 x 28672 x 7167 44 against 39.
+// 14.8, 64 x 7168 x 4351 14.0 against 14.3; but 64 x 28672 x 7167 44 against 39. Many tokens are restaged: 600 x
+// 4096 x 2047 16.6 against 18.4 with 128 x 128 tiles fed from registers, 2504 x 1920 x 356 12.4 against 18.2, though 3000
+// x 1000 x 999 13.4 against 12.1.
 bool i8_takes_any_rows(const I8Args &g)
 {
-    return g.K >= 16 && !wide_preferred(g) && (int64_t)g.T * g.nblk * 16 * g.K <= (int64_t)1 << 33;
+    return g.K >= 16 && !many(g) && (int64_t)g.T * g.nblk * 16 * g.K <= (int64_t)1 << 33;
 }
 
-// The largest tile that still makes FILL workgroups, three quarters of the CUs, else the smallest (16 columns; 32
-// when a gate and an up block have to be together), with the K axis over more groups of waves the
-// smaller the tile. Measured, microseconds (tokens x columns x codes; weights not in any cache), against
+// Below that, the largest tile that still makes FILL workgroups, three quarters of the CUs, else the smallest (16
+// columns; 32 when a gate and an up block have to be together), with the K axis over more groups of waves
+// the smaller the tile. Measured, microseconds (tokens x columns x codes; weights not in any cache), against
 // the neighbours: 1 x 3584 x 7168: 16 columns 7.4, 32 8.1; 16 x 7168 x 4352: 32 8.4, 16 11.7, 64 9.8; 16 x
 // 14336 x 3584: 64 10.7, 32 12.8, 128 14.3; 64 x 28672 x 7168: 64 x 128 38, 64 x 64 42; 64 x 7168 x 4352: 64 x
-// 32 11.2, 64 x 64 13.1; 64 x 3584 x 7168: 32 x 32 11.8, 64 x 16 12.4, 64 x 32 14.2; 184 x 160 x 11648: 16 x 16
-// 7.2, 32 x 16 8.8, 64 x 32 15.5; 1000 x 128 x 4096: 32 x 16 5.6, 16 x 16 7.3, 32 x 32 6.4; 7168 x 7168
-// weights and 128 tokens: 64 x 64 20.8, 128 x 64 26.4; 256: 128 x 64 28.4, 64 x 64 37; 512: 128 x 128 39,
-// 128 x 64 46; 1024: 128 x 128 62, wide 80; 2048: wide 84, 128 x 128 120.
+// 32 11.2, 64 x 64 13.1; 64 x 3584 x 7168: 32 x 32 11.8, 64 x 16 12.4, 64 x 32 14.2; 128 x 7168 x 7168: 64 x 64
+// 20.8, 128 x 64 27; 184 x 160 x 11648: 16 x 16 7.2, 32 x 16 8.8, 64 x 32 15.5; 1000 x 128 x 4096: 32 x 16 5.6,
+// 16 x 16 7.3, 32 x 32 6.4.
 hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
 {
-    auto tiles = [&](int bm, int bn) { return tile_count(g, bm, bn); };
-    auto fills = [&](int bm, int bn) { return tiles(bm, bn) >= FILL; };
+    auto fills = [&](int bm, int bn) { return tile_count(g, bm, bn) >= FILL; };
+    if (many(g))
+        return launch_many(g, st);
     if (g.T <= 16) {
         if (fills(16, 64))
             return launch_tile<16, 64, 1, 2, 2, 4>(g, st);
@@ -709,25 +727,14 @@ hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
             return launch_tile<16, 32, 1, 1, 4, 4>(g, st);
         return launch_tile<16, 16, 1, 1, 8, 3>(g, st);
     }
-    if (g.T > 64) {
-        if (wide_preferred(g))
-            return launch_wide(g, st);
-        const int64_t small = tiles(128, 128);
-        if (small > CUS)   // two workgroups per CU share its LDS, or one takes three buffers: 512 tokens 39 us
-            return launch_tile<128, 128, 2, 4, 1, 2>(g, st);   // against 53, 1024 tokens 74 against 62
-        if (small >= FILL)
-            return launch_tile<128, 128, 2, 4, 1, 3>(g, st);
-        if (fills(128, 64))
-            return launch_tile<128, 64, 4, 2, 1, 3>(g, st);
-    } else if (g.T <= 32) {
+    if (g.T <= 32) {
         if (fills(32, 128))
             return launch_tile<32, 128, 1, 4, 1, 4>(g, st);
         if (fills(32, 64))
             return launch_tile<32, 64, 1, 2, 2, 4>(g, st);
-    } else if (fills(64, 128)) {
-        return launch_tile<64, 128, 2, 4, 1, 3>(g, st);
-    }
-    if (g.T > 32) {
+    } else {
+        if (g.T <= 64 && fills(64, 128))
+            return launch_tile<64, 128, 2, 4, 1, 3>(g, st);
         if (fills(64, 64))
             return launch_tile<64, 64, 2, 2, 2, 3>(g, st);
         if (fills(64, 32))

@@ -228,7 +228,9 @@ def test_products(T, N, K, pad, offset, kind):
 # 256 x 256, and sums of one to several 128-code stages
 LARGE = [(2048, 4096, 640, 0), (4100, 4200, 272, 0), (2304, 2100, 384, 1), (1030, 1100, 1024, 0), (8192, 500, 128, 0),
          (300, 9000, 256, 1), (2048, 7168, 64, 0), (2050, 7170, 100, 0), (3584, 4096, 1152, 0), (1921, 6930, 515, 0),
-         (2048, 3584, 256, 1), (2300, 3900, 130, 1), (2048, 3600, 1, 1), (4096, 3584, 384, 0), (257, 6000, 336, 0)]
+         (2048, 3584, 256, 1), (2300, 3900, 130, 1), (2048, 3600, 1, 1), (4096, 3584, 384, 0), (257, 6000, 336, 0),
+         (1793, 7169, 3300, 0), (2000, 7000, 1500, 0), (1700, 7010, 4200, 0), (1000, 7000, 2561, 0), (2047, 3501, 1700, 1),
+         (1000, 3500, 3400, 1), (300, 3000, 300, 1), (2040, 7000, 4097, 0)]
 
 
 @pytest.mark.parametrize("T,N,K,glu", LARGE)
@@ -445,6 +447,18 @@ def test_a_token_in_any_batch(N, K, glu, out_dtype):
         if T <= 1200:
             apart[:T].copy_(x[first:first + T])
             assert torch.equal(layer.forward(apart[:T], sx[first:first + T]), whole[first:first + T]), (T, "unaligned")
+
+
+@pytest.mark.parametrize("N,K,glu", [(7168, 4300, 0), (3584, 3000, 1), (6101, 4112, 0)])
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+def test_a_token_in_any_large_batch(N, K, glu, out_dtype):
+    """The same with K axes long enough for every tile of many tokens."""
+    g = gen(N + 1)
+    layer, *_ = make(N, K, glu, g, bias=not glu, T_max=2304, out_dtype=out_dtype)
+    x, sx = codes_rows(2304, K, g), (torch.rand(2304, generator=g) - 0.5).cuda()
+    whole = layer.forward(x, sx)
+    for first, T in ((3, 61), (1, 200), (77, 300), (640, 520), (200, 1000), (9, 1104), (500, 1700), (304, 2000)):
+        assert torch.equal(layer.forward(x[first:first + T], sx[first:first + T]), whole[first:first + T]), T
 
 
 def test_views_and_weights_in_any_order():
