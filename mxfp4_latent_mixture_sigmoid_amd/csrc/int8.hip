@@ -7,6 +7,7 @@
 #include "dense.hpp"
 
 #include <type_traits>
+#include <utility>
 
 namespace mxmoe {
 
@@ -141,192 +142,238 @@ __device__ inline float gated(int32_t gate, int32_t up, float sx, float sg, floa
     return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * g)) * u;
 }
 
-// Outputs of one fragment of row block nb (a gate block with its up block's sums in `up` when glu), token
-// row r. The weights are the first matrix operand, so lane l holds row l % 16 and the packed
-// columns 4 (l / 16) .. +3.
-__device__ inline void emit(const I8Args &g, int r, float sx, int nb, acc_t sum, acc_t up)
+// What one fragment's outputs take besides its sums: the token's scale, and for the lane's four columns their scales
+// and the up columns' scales or the bias.
+struct Factors {
+    float sx;
+    f32x4_t sw, other;
+};
+
+// The weights are the first matrix operand, so lane l of a fragment holds token row l % 16 and the packed
+// columns 4 (l / 16) .. +3 of row block nb. Rows and blocks past the end take the last ones' factors.
+__device__ inline Factors load_factors(const I8Args &g, int r, int nb)
 {
-    const int q = (threadIdx.x & (WAVE - 1)) >> 4;
-    const int n = (g.glu ? nb / 2 : nb) * 16 + 4 * q;
-    if (n >= g.N)
+    const int q = (threadIdx.x & (WAVE - 1)) >> 4, at = min(nb, g.nblk - (g.glu ? 2 : 1)) * 16 + 4 * q;
+    const float *other = g.glu ? g.sw + 16 : g.bias ? g.bias : g.sw;
+    Factors v{g.sx[min(r, g.T - 1)], *reinterpret_cast<const f32x4_t *>(g.sw + at),
+              *reinterpret_cast<const f32x4_t *>(other + at)};
+    if (!g.glu && !g.bias)
+        v.other = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    return v;
+}
+
+// Outputs of one fragment of row block nb (a gate block with its up block's sums in `up` when glu).
+__device__ inline void emit(const I8Args &g, int r, int nb, const Factors &c, acc_t sum, acc_t up)
+{
+    const int q = (threadIdx.x & (WAVE - 1)) >> 4, n = (g.glu ? nb / 2 : nb) * 16 + 4 * q;
+    if (r >= g.T || n >= g.N)
         return;
-    const f32x4_t sw = *reinterpret_cast<const f32x4_t *>(g.sw + nb * 16 + 4 * q);
-    f32x4_t other{0.f, 0.f, 0.f, 0.f};   // the up scales, or the bias
-    if (g.glu)
-        other = *reinterpret_cast<const f32x4_t *>(g.sw + nb * 16 + 16 + 4 * q);
-    else if (g.bias)
-        other = *reinterpret_cast<const f32x4_t *>(g.bias + n);
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; i++)
-        v[i] = g.glu ? gated(sum[i], up[i], sx, sw[i], other[i]) : scaled(sum[i], sx, sw[i], other[i]);
+        v[i] = g.glu ? gated(sum[i], up[i], c.sx, c.sw[i], c.other[i]) : scaled(sum[i], c.sx, c.sw[i], c.other[i]);
     store4(g, r, n, v);
 }
 
-// Tiles of BM tokens x BN packed columns by KG groups of NWM x NWN waves; group k takes every KG-th stage of
-// 128 codes, and the groups' sums are added through LDS at the end. Both operands pass through LDS in
-// NBUF buffers of KG stages, filled by direct global -> LDS loads: one instruction fills 1 KiB, of the
-// activations 8 rows x 128 bytes (whole lines), of the weights one packed block. Rows past T and stages
-// past K lie outside the loads' windows and read as zeros without touching memory. ONCE: there is
-// one row tile, so weights are read once, and are not to displace the activations in the caches.
-// ANY: activations whose rows the direct loads cannot take (any address, any K >= 16) pass through
-// registers instead, loaded two iterations ahead and written to LDS one ahead (NBUF = 3); rows past T, whose
-// sums are never stored, repeat the last one -- or, in 16-token tiles, where they can be most, are not
-// loaded (4 x 1792 x 12288: 9.3 us against 14.2; the test costs fuller tiles 10 to 20%) -- and the
-// chunk that crosses K is loaded from 16 codes before K and shifted into place.
-template <int BM, int BN, int NWM, int NWN, int KG, int NBUF, bool ONCE, bool ANY>
-__global__ __launch_bounds__(WAVE *NWM *NWN *KG) void tile_kernel(const I8Args g, int gx, int gy)
+// Sixteen bytes from byte `off` of the window [base, base + bytes), zeros when they lie outside.
+template <int CPOL>
+__device__ inline u32x4_t load_window(const void *base, int bytes, int off)
 {
-    constexpr int NW = NWM * NWN, WMF = BM / NWM / 16, WNF = BN / NWN / 16;
-    constexpr int AL = BM / 8 / NW, BL = BN / 8 / NW;   // loads per wave and stage
-    constexpr int STAGE = (BM + BN) * 8;                // 16-byte slots
-    static_assert(AL * NW * 8 == BM && BL * NW * 8 == BN && (!ANY || NBUF == 3), "tile");
-    static_assert(KG == 1 || NBUF * STAGE >= NW * WMF * WNF * WAVE, "room for the groups' sums");
-    __shared__ u32x4_t lds[NBUF * KG * STAGE];
+    return __builtin_amdgcn_raw_buffer_load_b128(
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, bytes, 0x00020000), off, 0, CPOL);
+}
+
+// f(0), f(1), ... with constants.
+template <int... I, class F>
+__device__ inline void each(std::integer_sequence<int, I...>, F f)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+
+// Tiles of 16 MF tokens x 16 NF NW packed columns by KG groups of NW waves; group k takes every KG-th stage of
+// 128 codes, and the groups' sums are added through LDS at the end. A wave has all rows of the tile and columns
+// of its own, so its weights go straight to registers, in the order they are packed in, and only the activations
+// pass through LDS, loaded directly to it, 8 rows x 128 bytes (whole lines) with an instruction; rows past T lie
+// outside the loads' window and read as zeros without touching memory. Loads run D - 1 stages ahead. With NW = 1 a
+// wave reads only what it loaded itself, and no barrier is met before the one for the sums.
+//
+// Bounds: the weights' bytes from memory (1 x 28672 x 7168: 36.0 us, 5.7 TB/s), and for several row or column tiles
+// the loads of a CU: 64 x 64 tiles take 64 + 64 bytes a code and CU, 65 GB/s of them (256 x 3584 x 7168: 19 us).
+// Weights through LDS as well cost 128 more bytes of its traffic a code in those tiles: 777 x 1001 x 3584
+// 11.1 us against 9.6, 1 x 3584 x 7168 7.3 against 6.9.
+//
+// ONCE: there is one row tile, so weights are read once, and are not to displace the activations in the caches.
+// ANY: activations whose rows the direct loads cannot take (any address, any K >= 16) pass through
+// registers on their way to LDS; rows past T, whose sums are never stored, repeat the last one -- or, in
+// 16-token tiles, where they can be most, are not loaded (4 x 1792 x 12288: 8.8 us against 12.4) -- and the chunk that
+// crosses K is loaded from 16 codes before K and shifted into place.
+template <int MF, int NF, int NW, int KG, int D, bool ONCE, bool ANY>
+__global__ __launch_bounds__(WAVE *NW *KG) __attribute__((amdgpu_waves_per_eu(NW * KG / 4)))
+void tile_kernel(const I8Args g, int gx, int gy)
+{
+    constexpr int AL = 2 * MF / NW, LOADS = AL + 2 * NF;      // loads per wave and stage
+    constexpr int STAGE = MF * 128;   // 16-byte slots of a stage's activations
+    constexpr int SUMS = KG > 1 ? KG * NW * MF * NF * WAVE : 0;
+    static_assert(AL * NW == 2 * MF && D >= 2 && (D - 1) * LOADS < 64, "tile");
+    __shared__ u32x4_t lds[D * KG * STAGE > SUMS ? D * KG * STAGE : SUMS];
     const int lane = threadIdx.x & (WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int wv = wave % NW, kg = wave / NW;
     int bx, by;
     if (!tile_item(gx, gy, bx, by))
         return;
-    const int m0 = by * BM, nb0 = bx * (BN / 16);
+    const int m0 = by * 16 * MF, nb0 = bx * NF * NW + wv * NF;
     const int nst = (int)i8_stages(g.K);
     const int8_t *xt = g.x + (int64_t)m0 * g.ldx;
-    const int xbytes = ANY ? 0 : (min(g.T - m0, BM) - 1) * (int)g.ldx + g.K;
-    const uint8_t *wt = g.w + (int64_t)nb0 * I8_STAGE_BYTES;
-    const int wbytes = min(g.nblk - nb0, BN / 16) * I8_STAGE_BYTES;
+    const int xbytes = ANY ? 0 : (min(g.T - m0, 16 * MF) - 1) * (int)g.ldx + g.K;
+    const uint8_t *wt = g.w + (int64_t)min(nb0, g.nblk - 1) * I8_STAGE_BYTES;
+    const int wbytes = max(min(g.nblk - nb0, NF), 0) * I8_STAGE_BYTES;
     const int64_t wstep = (int64_t)g.nblk * I8_STAGE_BYTES;
     int64_t arow[AL];   // byte offsets of this lane's rows, and codes of its chunks in a stage
     int ak[AL];
 #pragma unroll
     for (int i = 0; i < AL; i++) {
         const int row = (wv * AL + i) * 8 + (lane >> 3);
-        arow[i] = !ANY || row < g.T - m0 ? row * g.ldx : BM == 16 ? -1 : (g.T - 1 - m0) * g.ldx;
+        arow[i] = !ANY || row < g.T - m0 ? row * g.ldx : MF == 1 ? -1 : (g.T - 1 - m0) * g.ldx;
         ak[i] = ((lane & 7) ^ swizzle(row)) * 16;
     }
-    auto issue_w = [&](int it) {
-        const int s = it * KG + kg, last = min(s, nst - 1), in = -(int)(s < nst);   // past K: empty windows
-        u32x4_t *buf = &lds[(it % NBUF * KG + kg) * STAGE + BM * 8];
+    // Group k finishes every KG-th fragment (or pair of a gate and an up fragment); `row` and `col` are its i-th's place
+    // in the tile. Their factors are loaded first of all, so that the end does not wait for them.
+    constexpr int ENDS = (MF * NF + KG - 1) / KG;
+    constexpr int PAIRS = NF / 2 + NF % 2;
+    auto row = [&](int i) { return KG == 1 ? i / NF : g.glu ? (i * KG + kg) / PAIRS : (i * KG + kg) / NF; };
+    auto col = [&](int i) { return KG == 1 ? i % NF : g.glu ? (i * KG + kg) % PAIRS * 2 : (i * KG + kg) % NF; };
+    Factors factors[ENDS];
+#pragma unroll
+    for (int i = 0; i < ENDS; i++)
+        factors[i] = load_factors(g, m0 + row(i) * 16 + (lane & 15), nb0 + col(i));
+    struct Stage {
+        u32x4_t b[2][NF], x[ANY ? AL : 1];
+    } stage[D];
+    u32x4_t *group = &lds[kg * STAGE];   // this group's part of a buffer
+    auto load = [&](int it, int slot) {
+        const int s = __builtin_amdgcn_readfirstlane(it * KG + kg), last = min(s, nst - 1);
+        const int in = -(int)(s < nst);   // past K (another group's last): empty windows
+        Stage &q = stage[slot];
         const uint8_t *ws = wt + last * wstep;
 #pragma unroll
-        for (int i = 0; i < BL; i++)
-            load_lds<ONCE ? CPOL_NT : 0>(ws, wbytes & in, (wv * BL + i) * I8_BLOCK_BYTES + lane * 16,
-                                         &buf[(wv * BL + i) * WAVE]);
-    };
-    auto issue_x = [&](int it) {
-        const int s = it * KG + kg, last = min(s, nst - 1), in = -(int)(s < nst);
-        u32x4_t *buf = &lds[(it % NBUF * KG + kg) * STAGE];
+        for (int j = 0; j < NF; j++)
 #pragma unroll
-        for (int i = 0; i < AL; i++)
-            load_lds(xt + last * I8_STAGE, (xbytes - last * I8_STAGE) & in, (int)arow[i] + ak[i], &buf[(wv * AL + i) * WAVE]);
-    };
-    struct Rows {
-        u32x4_t v[AL];
-    };
-    auto load_x = [&](int it, Rows &r) {
-        const int s = min(it * KG + kg, nst - 1);   // past K: the last stage again, against zero weights
+            for (int h = 0; h < 2; h++)
+                q.b[h][j] = load_window<ONCE ? CPOL_NT : 0>(ws, wbytes & in, (j * 2 + h) * I8_BLOCK_BYTES + lane * 16);
 #pragma unroll
         for (int i = 0; i < AL; i++) {
-            const int k = s * I8_STAGE + ak[i];
-            if (BM > 16 || arow[i] >= 0)
-                __builtin_memcpy(&r.v[i], xt + arow[i] + min(k, g.K - 16), 16);
+            if constexpr (ANY) {
+                // past K: the last stage again, which is not used
+                if (MF > 1 || arow[i] >= 0)
+                    __builtin_memcpy(&q.x[i], xt + arow[i] + min(last * I8_STAGE + ak[i], g.K - 16), 16);
+            } else {
+                load_lds(xt + last * I8_STAGE, (xbytes - last * I8_STAGE) & in, (int)arow[i] + ak[i],
+                         &group[slot * KG * STAGE + (wv * AL + i) * WAVE]);
+            }
         }
+        // The counts below are of loads in this order.
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     };
-    auto store_x = [&](int it, const Rows &r) {
-        const int s = min(it * KG + kg, nst - 1);
-        u32x4_t *buf = &lds[(it % NBUF * KG + kg) * STAGE];
+    auto store_x = [&](int it, int slot) {
+        const int s = it * KG + kg;
 #pragma unroll
         for (int i = 0; i < AL; i++) {
-            const int late = max(s * I8_STAGE + ak[i] - (g.K - 16), 0);   // bytes to drop at the front
-            u32x4_t v = r.v[i];
+            u32x4_t v = stage[slot].x[i];
             if ((s + 1) * I8_STAGE > g.K)   // the stage that crosses K
-                v = drop_bytes(v, late);
-            buf[(wv * AL + i) * WAVE + lane] = v;
+                v = drop_bytes(v, max(s * I8_STAGE + ak[i] - (g.K - 16), 0));
+            group[slot * KG * STAGE + (wv * AL + i) * WAVE + lane] = v;
         }
     };
-    acc_t acc[WMF][WNF];
+    acc_t acc[MF][NF];
 #pragma unroll
-    for (int f = 0; f < WMF; f++)
+    for (int f = 0; f < MF; f++)
 #pragma unroll
-        for (int j = 0; j < WNF; j++)
+        for (int j = 0; j < NF; j++)
             acc[f][j] = acc_t{0, 0, 0, 0};
-    const int fa = (wv / NWN) * WMF, fb = (wv % NWN) * WNF;
-    const int nit = (nst + KG - 1) / KG;
-    // Loads that may still be on their way when the weights of the next stages have landed: those of the
-    // stages after them. Where rows are skipped their loads may not be issued, so that only the weights' count.
-    constexpr int LATER = ANY && BM == 16 ? BL : (NBUF - 2) * (AL + BL);
-    auto meet = [&]() {
-        // This wave's part of the next stages has landed and its reads of the last ones are done; past the
-        // barrier, every wave's, so that the last ones' buffer can be filled again.
-        __builtin_amdgcn_s_waitcnt(vmcnt_lgkm_imm(LATER));
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-    };
-    auto multiply = [&](int it) {
-        const u32x4_t *buf = &lds[(it % NBUF * KG + kg) * STAGE];
+    auto multiply = [&](int slot) {
+        const u32x4_t *at = &group[slot * KG * STAGE];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            u32x4_t a[WMF], b[WNF];
+            u32x4_t a[MF];
             const int r = lane & 15, c = (h * 4 + (lane >> 4)) ^ swizzle(r);
 #pragma unroll
-            for (int f = 0; f < WMF; f++)
-                a[f] = buf[((fa + f) * 16 + r) * 8 + c];
+            for (int f = 0; f < MF; f++)
+                a[f] = at[(f * 16 + r) * 8 + c];
 #pragma unroll
-            for (int j = 0; j < WNF; j++)
-                b[j] = buf[BM * 8 + ((fb + j) * 2 + h) * WAVE + lane];
+            for (int j = 0; j < NF; j++)
 #pragma unroll
-            for (int j = 0; j < WNF; j++)
-#pragma unroll
-                for (int f = 0; f < WMF; f++)
-                    acc[f][j] = mfma(b[j], a[f], acc[f][j]);
+                for (int f = 0; f < MF; f++)
+                    acc[f][j] = mfma(stage[slot].b[h][j], a[f], acc[f][j]);
         }
         asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     };
-    if constexpr (ANY) {
-        Rows even{}, odd{};
-        load_x(0, even);
-        issue_w(0);
-        load_x(1, odd);
-        issue_w(1);
-        store_x(0, even);
-        auto iteration = [&](int it, Rows &next, Rows &here) {
-            meet();
-            load_x(it + 2, next);
-            issue_w(it + 2);
-            multiply(it);
-            store_x(it + 1, here);
-        };
-        for (int it = 0; it < nit; it += 2) {
-            iteration(it, even, odd);
-            if (it + 1 < nit)
-                iteration(it + 1, odd, even);
+    // The activations of iteration `it` are in LDS: all but LATER stages' loads of this wave have landed. Its reads
+    // of the iteration before are done; with NW > 1, past the barrier, so are every wave's.
+    auto meet = [&](int it, int slot, auto later) {
+        if constexpr (ANY)
+            store_x(it, slot);
+        __builtin_amdgcn_s_waitcnt(vmcnt_lgkm_imm(ANY ? 63 : later * LOADS));
+        asm volatile("" ::: "memory");
+        if constexpr (NW > 1) {
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
         }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const int nit = NW > 1 ? (nst + KG - 1) / KG : (nst - kg + KG - 1) / KG;   // the same for waves that meet
+    auto step = [&](int it, auto d) {
+        if constexpr (NW == 1)
+            load(it + D - 1, (d + D - 1) % D);
+        meet(it, d, std::integral_constant<int, NW == 1 ? D - 1 : D - 2>{});
+        if constexpr (NW > 1)
+            load(it + D - 1, (d + D - 1) % D);
+    };
+    // No load is issued for stages that do not follow: an empty window costs a load's time in the address unit.
+    if (nit >= D - 1) {
+        int it = 0;
+#pragma unroll
+        for (int d = 0; d < D - 1; d++)
+            load(d, d);
+        for (; it + 2 * D - 2 < nit; it += D)
+            each(std::make_integer_sequence<int, D>{}, [&](auto d) {
+                step(it + d, d);
+                multiply(d);
+            });
+        each(std::make_integer_sequence<int, 2 * D - 2>{}, [&](auto d) {
+            if (it + d < nit) {
+                if (it + d + D - 1 < nit)
+                    step(it + d, std::integral_constant<int, d % D>{});
+                else
+                    meet(it + d, d % D, std::integral_constant<int, 0>{});
+                multiply(d % D);
+            }
+        });
     } else {
 #pragma unroll
-        for (int it = 0; it < NBUF - 1; it++) {
-            issue_w(it);
-            issue_x(it);
-        }
-        for (int it = 0; it < nit; it++) {
-            meet();
-            issue_w(it + NBUF - 1);
-            issue_x(it + NBUF - 1);
-            multiply(it);
-        }
+        for (int d = 0; d < D - 2; d++)
+            if (d < nit)
+                load(d, d);
+#pragma unroll
+        for (int d = 0; d < D - 2; d++)
+            if (d < nit) {
+                meet(d, d, std::integral_constant<int, 0>{});
+                multiply(d);
+            }
     }
     __builtin_amdgcn_s_waitcnt(vmcnt_lgkm_imm(0));   // nothing may land in LDS any more
     if constexpr (KG > 1) {
         __syncthreads();   // every wave is past its last stage: LDS holds the groups' sums from here
-        u32x4_t *mine = &lds[((kg * NW + wv) * WMF * WNF) * WAVE + lane];
+        u32x4_t *mine = &lds[wave * MF * NF * WAVE + lane];
 #pragma unroll
-        for (int f = 0; f < WMF; f++)
+        for (int f = 0; f < MF; f++)
 #pragma unroll
-            for (int j = 0; j < WNF; j++)
-                mine[(f * WNF + j) * WAVE] = __builtin_bit_cast(u32x4_t, acc[f][j]);
+            for (int j = 0; j < NF; j++)
+                mine[(f * NF + j) * WAVE] = __builtin_bit_cast(u32x4_t, acc[f][j]);
         __syncthreads();
     }
-    // Group k finishes every KG-th fragment (or pair of a gate and an up fragment).
     auto total = [&](int f, int j) {
         if constexpr (KG == 1) {
             return acc[f][j];
@@ -334,24 +381,20 @@ __global__ __launch_bounds__(WAVE *NWM *NWN *KG) void tile_kernel(const I8Args g
             acc_t sum{0, 0, 0, 0};
 #pragma unroll
             for (int k = 0; k < KG; k++)
-                sum += __builtin_bit_cast(acc_t, lds[((k * NW + wv) * WMF * WNF + f * WNF + j) * WAVE + lane]);
+                sum += __builtin_bit_cast(acc_t, lds[((k * NW + wv) * MF * NF + f * NF + j) * WAVE + lane]);
             return sum;
         }
     };
 #pragma unroll
-    for (int f = 0; f < WMF; f++) {
-        const int r = m0 + (fa + f) * 16 + (lane & 15);
-#pragma unroll
-        for (int j = 0; j < WNF; j++) {
-            const int nb = nb0 + fb + j, unit = g.glu ? (f * WNF + j) / 2 : f * WNF + j;
-            if (nb >= g.nblk || (g.glu && j % 2) || (KG > 1 && unit % KG != kg) || r >= g.T)
-                continue;
-            acc_t up{0, 0, 0, 0};
-            if constexpr (WNF % 2 == 0)   // launched with glu
-                if (g.glu)
-                    up = total(f, j | 1);
-            emit(g, r, g.sx[r], nb, total(f, j), up);
-        }
+    for (int i = 0; i < ENDS; i++) {
+        const int f = row(i), j = col(i), nb = nb0 + j;
+        if (f >= MF || nb >= g.nblk || (g.glu && j % 2))
+            continue;
+        acc_t up{0, 0, 0, 0};
+        if constexpr (NF % 2 == 0)   // launched with glu
+            if (g.glu)
+                up = total(f, j | 1);
+        emit(g, m0 + f * 16 + (lane & 15), nb, factors[i], total(f, j), up);
     }
 }
 
@@ -359,8 +402,9 @@ __global__ __launch_bounds__(WAVE *NWM *NWN *KG) void tile_kernel(const I8Args g
 // of 128 x 128, one per SIMD. Per 64 codes a wave multiplies for 1024 clocks (64 instructions) and reads 16 KiB of
 // operands, so the LDS is busy 512 clocks with all reads and 256 with the loads' writes; eight waves of 128
 // x 64 would read 1.5 times as much and leave the LDS no slack. A wave reads the operands of the next half
-// stage, and issues the loads, between the instructions that multiply the current one. The 160 KiB of LDS hold three 128-code stages of activations (whole
-// lines) and four 64-code halves of weights, loaded three to four halves ahead of their reads.
+// stage, and issues the loads, between the instructions that multiply the current one. The 160 KiB of LDS hold
+// three 128-code stages of activations (whole lines) and four 64-code halves of weights, loaded three to four
+// halves ahead of their reads.
 //
 // 8192 x (2 x 14336) x 7168 gated takes 1.20 ms, 2.8 POP/s (a library product of 8-bit codes of these sizes
 // without scales or gate: 1.58 ms), 8192 x 7168 x 14336 0.61 ms. The matrix cores are busy 69% of the
@@ -624,19 +668,19 @@ __global__ __launch_bounds__(256) void pack_vectors_kernel(const float *s, const
         bias_out[i] = n < N ? bias[n] : 0.f;
 }
 
-template <int BM, int BN, int NWM, int NWN, int KG, int NBUF>
+template <int MF, int NF, int NW, int KG, int D>
 hipError_t launch_tile(const I8Args &g, hipStream_t st)
 {
-    const int gx = (g.nblk * 16 + BN - 1) / BN, gy = (g.T + BM - 1) / BM;
-    const dim3 grid((unsigned)((gx * gy + XCDS - 1) / XCDS * XCDS)), threads(WAVE * NWM * NWN * KG);
+    const int gx = (g.nblk + NF * NW - 1) / (NF * NW), gy = (g.T + 16 * MF - 1) / (16 * MF);
+    const dim3 grid((unsigned)((gx * gy + XCDS - 1) / XCDS * XCDS)), threads(WAVE * NW * KG);
     if (g.direct && gy == 1)
-        hipLaunchKernelGGL((tile_kernel<BM, BN, NWM, NWN, KG, NBUF, true, false>), grid, threads, 0, st, g, gx, gy);
+        hipLaunchKernelGGL((tile_kernel<MF, NF, NW, KG, D, true, false>), grid, threads, 0, st, g, gx, gy);
     else if (g.direct)
-        hipLaunchKernelGGL((tile_kernel<BM, BN, NWM, NWN, KG, NBUF, false, false>), grid, threads, 0, st, g, gx, gy);
+        hipLaunchKernelGGL((tile_kernel<MF, NF, NW, KG, D, false, false>), grid, threads, 0, st, g, gx, gy);
     else if (gy == 1)
-        hipLaunchKernelGGL((tile_kernel<BM, BN, NWM, NWN, KG, 3, true, true>), grid, threads, 0, st, g, gx, gy);
+        hipLaunchKernelGGL((tile_kernel<MF, NF, NW, KG, D, true, true>), grid, threads, 0, st, g, gx, gy);
     else
-        hipLaunchKernelGGL((tile_kernel<BM, BN, NWM, NWN, KG, 3, false, true>), grid, threads, 0, st, g, gx, gy);
+        hipLaunchKernelGGL((tile_kernel<MF, NF, NW, KG, D, false, true>), grid, threads, 0, st, g, gx, gy);
     return hipGetLastError();
 }
 
@@ -698,10 +742,10 @@ hipError_t launch_many(const I8Args &g, hipStream_t st)
 } // namespace
 
 // Passing rows through registers saves the restaging launch and its pass over x, and costs some of the product's
-// time: 1 x 1000 x 1000 3.8 us against 5.6, 450 x 512 x 1237 5.7 against 7.4, 777 x 1001 x 3583 12.3 against
-// 14.8, 64 x 7168 x 4351 14.0 against 14.3; but 64 x 28672 x 7167 44 against 39. Many tokens are restaged: 600 x
-// 4096 x 2047 16.6 against 18.4 with 128 x 128 tiles fed from registers, 2504 x 1920 x 356 12.4 against 18.2, though 3000
-// x 1000 x 999 13.4 against 12.1.
+// time: 1 x 1000 x 1000 4.0 us against 5.6, 450 x 512 x 1237 5.0 against 7, 777 x 1001 x 3583 12.1 against
+// 12.5, 64 x 7168 x 4351 14.1 against 14.3; but 64 x 28672 x 7167 44 against 39. Many tokens are restaged: 600 x
+// 4096 x 2047 16.6 against 18.4 with 128 x 128 tiles fed from registers, 2504 x 1920 x 356 12.4 against 18.2, though
+// 3000 x 1000 x 999 13.4 against 12.1.
 bool i8_takes_any_rows(const I8Args &g)
 {
     return g.K >= 16 && !many(g) && (int64_t)g.T * g.nblk * 16 * g.K <= (int64_t)1 << 33;
@@ -710,43 +754,47 @@ bool i8_takes_any_rows(const I8Args &g)
 // Below that, the largest tile that still makes FILL workgroups, three quarters of the CUs, else the smallest (16
 // columns; 32 when a gate and an up block have to be together), with the K axis over more groups of waves
 // the smaller the tile. Measured, microseconds (tokens x columns x codes; weights not in any cache), against
-// the neighbours: 1 x 3584 x 7168: 16 columns 7.4, 32 8.1; 16 x 7168 x 4352: 32 8.4, 16 11.7, 64 9.8; 16 x
-// 14336 x 3584: 64 10.7, 32 12.8, 128 14.3; 64 x 28672 x 7168: 64 x 128 38, 64 x 64 42; 64 x 7168 x 4352: 64 x
-// 32 11.2, 64 x 64 13.1; 64 x 3584 x 7168: 32 x 32 11.8, 64 x 16 12.4, 64 x 32 14.2; 128 x 7168 x 7168: 64 x 64
-// 20.8, 128 x 64 27; 184 x 160 x 11648: 16 x 16 7.2, 32 x 16 8.8, 64 x 32 15.5; 1000 x 128 x 4096: 32 x 16 5.6,
-// 16 x 16 7.3, 32 x 32 6.4.
+// the neighbours: 1 x 3584 x 7168: 16 columns 6.6, 32 8.1; 16 x 7168 x 4352: 32 8.2, 16 10.3, 64 10.2; 16 x
+// 14336 x 3584: 64 10.9, 32 11.7, 128 15.3; 16 x 28672 x 7168: 128 36.2, 64 37.3; 32 x 3584 x 7168: 16 10.1, 32
+// 11.4; 32 x 7168 x 4352: 32 9.7, 64 12.2, 16 13.8; 32 x 14336 x 3584: 64 11.9, 32 15.8, 128 17; 32 x 28672 x 7168:
+// 128 37.1, 64 38.4; 64 x 28672 x 7168: 64 x 128 39.5, 64 x 64 48; 64 x 14336 x 3584: 64 x 64 15.0, 64 x 32 17.0, 64
+// x 128 19.1; 64 x 7168 x 4352: 64 x 32 11.5, 64 x 64 14.4; 64 x 3584 x 7168: 32 x 32 11.5, 64 x 32 14.2; 128 x 7168 x
+// 7168: 64 x 64 20.6, 64 x 32 27; 184 x 160 x 11648: 16 x 16 6.9, 32 x 16 8.2; 1000 x 128 x 4096: 32 x 16 5.5, 16 x
+// 16 6.0, 32 x 32 6.1.
 hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
 {
     auto fills = [&](int bm, int bn) { return tile_count(g, bm, bn) >= FILL; };
     if (many(g))
         return launch_many(g, st);
     if (g.T <= 16) {
+        if (fills(16, 128))
+            return launch_tile<1, 4, 2, 2, 3>(g, st);
         if (fills(16, 64))
-            return launch_tile<16, 64, 1, 2, 2, 4>(g, st);
+            return launch_tile<1, 2, 2, 4, 4>(g, st);
         if (fills(16, 32) || g.glu)
-            return launch_tile<16, 32, 1, 1, 4, 4>(g, st);
-        return launch_tile<16, 16, 1, 1, 8, 3>(g, st);
+            return launch_tile<1, 2, 1, 8, 5>(g, st);
+        return launch_tile<1, 1, 1, 8, 4>(g, st);
     }
     if (g.T <= 32) {
         if (fills(32, 128))
-            return launch_tile<32, 128, 1, 4, 1, 4>(g, st);
+            return launch_tile<2, 2, 4, 1, 4>(g, st);
         if (fills(32, 64))
-            return launch_tile<32, 64, 1, 2, 2, 4>(g, st);
+            return launch_tile<2, 2, 2, 4, 3>(g, st);
     } else {
         if (g.T <= 64 && fills(64, 128))
-            return launch_tile<64, 128, 2, 4, 1, 3>(g, st);
+            return launch_tile<4, 2, 4, 1, 4>(g, st);
         if (fills(64, 64))
-            return launch_tile<64, 64, 2, 2, 2, 3>(g, st);
+            return launch_tile<4, 2, 2, 4, 3>(g, st);
         if (fills(64, 32))
-            return launch_tile<64, 32, 2, 1, 4, 3>(g, st);
+            return launch_tile<4, 2, 1, 4, 3>(g, st);
     }
     if (fills(32, 32))
-        return launch_tile<32, 32, 1, 1, 4, 3>(g, st);
+        return launch_tile<2, 2, 1, 8, 3>(g, st);
     if (g.glu)
-        return launch_tile<16, 32, 1, 1, 4, 4>(g, st);
+        return launch_tile<1, 2, 1, 8, 5>(g, st);
     if (fills(32, 16))
-        return launch_tile<32, 16, 1, 1, 8, 3>(g, st);
-    return launch_tile<16, 16, 1, 1, 8, 3>(g, st);
+        return launch_tile<2, 1, 1, 8, 4>(g, st);
+    return launch_tile<1, 1, 1, 8, 4>(g, st);
 }
 
 hipError_t launch_i8_restage(const int8_t *x, int64_t ldx, int T, int K, int8_t *dst, hipStream_t st)
