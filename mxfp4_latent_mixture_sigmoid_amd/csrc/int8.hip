@@ -703,35 +703,36 @@ hipError_t launch_wide(const I8Args &g, hipStream_t st)
     return hipGetLastError();
 }
 
-constexpr int64_t FILL = CUS * 3 / 4;
 int64_t tile_count(const I8Args &g, int bm, int bn)
 {
     return (int64_t)((g.T + bm - 1) / bm) * ((g.nblk * 16 + bn - 1) / bn);
 }
+bool one_round(const I8Args &g, int bm, int bn) { return tile_count(g, bm, bn) <= CUS; }
 
-// Many tokens: at least FILL tiles of 128 x 64.
-bool many(const I8Args &g) { return g.T > 64 && tile_count(g, 128, 64) >= FILL; }
+// Many tokens: more than one round of 64 x 64 tiles.
+bool many(const I8Args &g) { return g.T > 64 && !one_round(g, 64, 64); }
 
-// Tiles for many tokens. 128 x 64 until there are FILL tiles of 128 x 128; then the shape with the least estimated time
-// among those of FILL tiles. A round of tiles over the CUs costs its K loop and a start and end worth some
-// codes more; measured, a round of 256 x 256 takes 10.3 ns x (K + 1000), of 256 x 224 9.4 ns x (K + 1400), of 256 x
-// 128 6.1 ns x (K + 800). Two 128 x 128 workgroups share a CU and overlap, so their rounds need not be whole: 7.6
-// ns x (K + 550) for 2 per CU. Microseconds, 7168 x 7168 weights, 256 x 256 / 256 x 128 / 128 x 128 / 128 x 64:
-// 256 tokens - / - / 36 / 29; 512 - / 50 / 36 / 45; 1024 78 / 53 / 60 / 80; 2048 82 / 101 / 113 / -. 2000 x 7000
-// outputs: 512 codes 18.9 / 20.3 / 17.3 / 20.3, 2048 codes 33.5 / 40.6 / 40.2 / 48. 8192 x 7168 outputs are 4 rounds
-// of 224 columns and 3.5, so 4, of 256: 605 against 619 with 14336 codes.
+// Tiles for many tokens: 128 x 64 if they are one round of workgroups, one for each CU; else the shape with the
+// least estimated time. A round of tiles over the CUs costs its K loop and a start and end worth some codes more;
+// measured, a round of 256 x 256 takes 10.3 ns x (K + 1000), of 256 x 224 9.4 ns x (K + 1400), of 256 x 128 6.1 ns x
+// (K + 800). Two 128 x 128 workgroups share a CU and overlap: 7.6 ns x (K + 550) for 2 per CU, 4.7 for one, and
+// a last round that is not full less. Microseconds, 7168 x 7168 weights, 256 x 256 / 256 x 128 / 128 x 128 / 128 x
+// 64: 256 tokens - / - / 36 / 29; 512 - / 50 / 36 / 45; 1024 78 / 53 / 60 / 80; 1280 74 / 94 / 81 / 96; 2048 82 / 101
+// / 113 / -. 2000 x 7000 outputs: 512 codes 18.9 / 20.3 / 17.3 / 20.3, 2048 codes 33.5 / 40.6 / 40.2 / 48; 928 x
+// 2416 x 4064 - / 30.9 / 20.0 / 25.7. 8192 x 7168 outputs are 4 rounds of 224 columns and 3.5, so 4, of 256: 605
+// against 619 with 14336 codes.
 hipError_t launch_many(const I8Args &g, hipStream_t st)
 {
-    const int64_t pairs = 2 * CUS, small = tile_count(g, 128, 128);
-    if (small < FILL)
+    if (one_round(g, 128, 64))
         return launch_wide<4, 2>(g, st);
-    auto cost = [&](int bm, int bn, int64_t rate, int64_t extra) {
-        const int64_t n = tile_count(g, bm, bn);
-        return n < FILL ? INT64_MAX : (n + CUS - 1) / CUS * rate * (g.K + extra);
+    auto cost = [&](int bn, int64_t rate, int64_t extra) {
+        return (tile_count(g, 256, bn) + CUS - 1) / CUS * rate * (g.K + extra);
     };
-    const int64_t c256 = cost(256, 256, 103, 1000), c128 = cost(256, 128, 61, 800);
-    const int64_t c224 = g.glu ? INT64_MAX : cost(256, 224, 94, 1400); // 7 would part a gate from its up block
-    const int64_t cpair = (small > pairs * 7 / 8 ? small : pairs * 7 / 8) * 76 * (g.K + 550) / pairs;
+    const int64_t c256 = cost(256, 103, 1000), c128 = cost(128, 61, 800);
+    const int64_t c224 = g.glu ? INT64_MAX : cost(224, 94, 1400);   // 7 would part a gate from its up block
+    const int64_t small = tile_count(g, 128, 128), rest = small % (2 * CUS);
+    const int64_t last = rest == 0 ? 0 : rest <= CUS ? 47 : (rest > 448 ? rest : 448) * 76 / (2 * CUS);
+    const int64_t cpair = (small / (2 * CUS) * 76 + last) * (g.K + 550);
     if (cpair <= c128 && cpair <= c256 && cpair <= c224)
         return launch_wide<4, 4>(g, st);
     if (c128 <= c256 && c128 <= c224)
@@ -751,50 +752,40 @@ bool i8_takes_any_rows(const I8Args &g)
     return g.K >= 16 && !many(g) && (int64_t)g.T * g.nblk * 16 * g.K <= (int64_t)1 << 33;
 }
 
-// Below that, the largest tile that still makes FILL workgroups, three quarters of the CUs, else the smallest (16
-// columns; 32 when a gate and an up block have to be together), with the K axis over more groups of waves
-// the smaller the tile. Measured, microseconds (tokens x columns x codes; weights not in any cache), against
-// the neighbours: 1 x 3584 x 7168: 16 columns 6.6, 32 8.1; 16 x 7168 x 4352: 32 8.2, 16 10.3, 64 10.2; 16 x
-// 14336 x 3584: 64 10.9, 32 11.7, 128 15.3; 16 x 28672 x 7168: 128 36.2, 64 37.3; 32 x 3584 x 7168: 16 10.1, 32
-// 11.4; 32 x 7168 x 4352: 32 9.7, 64 12.2, 16 13.8; 32 x 14336 x 3584: 64 11.9, 32 15.8, 128 17; 32 x 28672 x 7168:
-// 128 37.1, 64 38.4; 64 x 28672 x 7168: 64 x 128 39.5, 64 x 64 48; 64 x 14336 x 3584: 64 x 64 15.0, 64 x 32 17.0, 64
-// x 128 19.1; 64 x 7168 x 4352: 64 x 32 11.5, 64 x 64 14.4; 64 x 3584 x 7168: 32 x 32 11.5, 64 x 32 14.2; 128 x 7168 x
-// 7168: 64 x 64 20.6, 64 x 32 27; 184 x 160 x 11648: 16 x 16 6.9, 32 x 16 8.2; 1000 x 128 x 4096: 32 x 16 5.5, 16 x
-// 16 6.0, 32 x 32 6.1.
+// Below that, the smallest tile that is one round of workgroups, one for each CU: less work for each of them than
+// with larger tiles, and less to load than with several rounds of smaller ones. 16 columns, or 32 when a gate and an
+// up block have to be together, up to the most that a few tokens take; the smaller the tile, the more groups of waves
+// share the K axis. Measured, microseconds (tokens x columns x codes; the largest weights not in any cache), with the
+// neighbours: 1 x 4352 x 4096: 32 columns 6.7, 16 7.0, 64 8.7; 1 x 3584 x 7168: 16 6.6, 32 8.1; 1 x 10240 x 4096: 64
+// 10.3, 32 11.1; 16 x 28672 x 7168: 128 36.2, 64 37.3; 32 x 3584 x 7168: 32 x 16 9.2, 16 x 32 10.6, 16 x 16 12.1, 32
+// x 32 11.3; 32 x 10240 x 4096: 32 x 64 12.6, 32 x 32 15.0, 32 x 128 16.2; 32 x 18432 x 4096: 32 x 128 19.6, 32 x 64
+// 20.8; 64 x 4352 x 4096: 64 x 32 8.8, 32 x 32 10.9, 64 x 64 13.2; 64 x 10240 x 4096: 64 x 64 14.9, 64 x 32 16.7; 64
+// x 18432 x 4096: 64 x 128 22.7, 64 x 64 27.0; 727 x 232 x 7424: 32 x 32 8.5, 16 x 32 9.9, 64 x 32 10.5; 437 x 695 x
+// 752: 64 x 32 4.6, 64 x 64 5.6, 32 x 32 6.4; 355 x 1811 x 6256: 64 x 64 14.4, 64 x 32 19.5, 128 x 64 20.7; 438 x
+// 2943 x 1024: 128 x 64 7.8, 128 x 128 9.4, 64 x 64 11.3.
 hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
 {
-    auto fills = [&](int bm, int bn) { return tile_count(g, bm, bn) >= FILL; };
+    auto round = [&](int bm, int bn) { return one_round(g, bm, bn); };
     if (many(g))
         return launch_many(g, st);
-    if (g.T <= 16) {
-        if (fills(16, 128))
-            return launch_tile<1, 4, 2, 2, 3>(g, st);
-        if (fills(16, 64))
-            return launch_tile<1, 2, 2, 4, 4>(g, st);
-        if (fills(16, 32) || g.glu)
-            return launch_tile<1, 2, 1, 8, 5>(g, st);
+    if (!g.glu && round(16, 16))
         return launch_tile<1, 1, 1, 8, 4>(g, st);
+    if (g.T <= 16) {
+        if (round(16, 32))
+            return launch_tile<1, 2, 1, 8, 5>(g, st);
+        return round(16, 64) ? launch_tile<1, 2, 2, 4, 4>(g, st) : launch_tile<1, 4, 2, 2, 3>(g, st);
     }
-    if (g.T <= 32) {
-        if (fills(32, 128))
-            return launch_tile<2, 2, 4, 1, 4>(g, st);
-        if (fills(32, 64))
-            return launch_tile<2, 2, 2, 4, 3>(g, st);
-    } else {
-        if (g.T <= 64 && fills(64, 128))
-            return launch_tile<4, 2, 4, 1, 4>(g, st);
-        if (fills(64, 64))
-            return launch_tile<4, 2, 2, 4, 3>(g, st);
-        if (fills(64, 32))
-            return launch_tile<4, 2, 1, 4, 3>(g, st);
-    }
-    if (fills(32, 32))
-        return launch_tile<2, 2, 1, 8, 3>(g, st);
-    if (g.glu)
+    if (g.glu && round(16, 32))
         return launch_tile<1, 2, 1, 8, 5>(g, st);
-    if (fills(32, 16))
+    if (!g.glu && round(32, 16))
         return launch_tile<2, 1, 1, 8, 4>(g, st);
-    return launch_tile<1, 1, 1, 8, 4>(g, st);
+    if (round(32, 32))
+        return launch_tile<2, 2, 1, 8, 3>(g, st);
+    if (g.T <= 32)
+        return round(32, 64) ? launch_tile<2, 2, 2, 4, 3>(g, st) : launch_tile<2, 2, 4, 1, 4>(g, st);
+    if (round(64, 32))
+        return launch_tile<4, 2, 1, 4, 3>(g, st);
+    return g.T > 64 || round(64, 64) ? launch_tile<4, 2, 2, 4, 3>(g, st) : launch_tile<4, 2, 4, 1, 4>(g, st);
 }
 
 hipError_t launch_i8_restage(const int8_t *x, int64_t ldx, int T, int K, int8_t *dst, hipStream_t st)

@@ -224,8 +224,8 @@ def test_products(T, N, K, pad, offset, kind):
     assert ok()
 
 
-# (tokens, outputs, codes): whole and ragged tiles of 128 x 64, 128 x 128 (two and three buffers), 256 x 224 and
-# 256 x 256, and sums of one to several 128-code stages
+# (tokens, outputs, codes): whole and ragged tiles of 128 x 64, 128 x 128, 256 x 128, 256 x 224 and 256 x 256, and
+# sums of one to several 128-code stages
 LARGE = [(2048, 4096, 640, 0), (4100, 4200, 272, 0), (2304, 2100, 384, 1), (1030, 1100, 1024, 0), (8192, 500, 128, 0),
          (300, 9000, 256, 1), (2048, 7168, 64, 0), (2050, 7170, 100, 0), (3584, 4096, 1152, 0), (1921, 6930, 515, 0),
          (2048, 3584, 256, 1), (2300, 3900, 130, 1), (2048, 3600, 1, 1), (4096, 3584, 384, 0), (257, 6000, 336, 0),
@@ -430,6 +430,41 @@ def test_smaller_calls_of_a_larger_layer():
     ref, err = reference(x.cpu().numpy(), f64(sx), w, s, None, True)
     for t in (150, 1, 64, 65, 16, 17, 149, 33):
         R.check(f64(layer.forward(x[:t], sx[:t])), ref[:t], err[:t], f"T={t}")
+
+
+# (tokens, outputs, gated, 128-code stages up to): one for each tile of few tokens and of the smaller ones of many
+STAGES = [(1, 300, 0, 80), (16, 3000, 1, 90), (16, 13000, 0, 40), (16, 25000, 0, 16), (32, 3584, 0, 80), (32, 7168, 0, 60),
+          (31, 6200, 1, 30), (30, 25000, 0, 12), (64, 7168, 0, 30), (63, 6500, 1, 30), (60, 24600, 0, 12), (20, 2000, 1, 90),
+          (777, 1001, 0, 30), (150, 7168, 0, 12), (300, 6000, 0, 12), (600, 7000, 0, 12)]
+
+
+@pytest.mark.parametrize("T,N,glu,most", STAGES)
+def test_every_number_of_stages(T, N, glu, most):
+    """K axes that end at each place of the loops over stages: sums that FP32 holds exactly, with direct and with
+    unaligned rows. Gated: the up half, whose gate is a constant, against the same sums
+    (the reciprocal is within 2 U, two products and the expectation round once each)."""
+    from mxfp4_latent_mixture_sigmoid_amd import Int8Linear
+    g = torch.Generator(device="cuda").manual_seed(T)
+    for s in range(1, most + 1, 1 if most <= 16 else 1 + (T + N) % 2):
+        K = 128 * s - 16 * (s % 3)
+        w = torch.randint(-9, 10, (N, K), generator=g, dtype=torch.int8, device="cuda")
+        x = torch.randint(-9, 10, (T, K + 5), generator=g, dtype=torch.int8, device="cuda")
+        one, sx = torch.ones(N, device="cuda"), torch.ones(T, device="cuda")
+        if glu:   # the gate's sums are 127 * 9 or more, times 2^-3: silu is the identity there
+            x[:, 0] = 9
+            gate = torch.zeros_like(w)
+            gate[:, 0] = 127
+            layer = Int8Linear(gate, one / 8, up_codes=w, up_scales=one, T_max=T, out_dtype=F32)
+        else:
+            layer = Int8Linear(w, one, T_max=T, out_dtype=F32)
+        want = x[:, :K].float() @ w.t().float().contiguous()
+        want *= 9 * 127 / 8 if glu else 1
+        for rows in (x[:, :K].contiguous(), x[:, :K]):
+            got = layer.forward(rows, sx)
+            if glu:
+                assert ((got - want).abs() <= 5 * R.U * want.abs()).all(), s
+            else:
+                assert torch.equal(got, want), s
 
 
 @pytest.mark.parametrize("N,K,glu,out_dtype", [(7168, 400, 0, BF16), (7168, 272, 0, F32), (3584, 640, 1, BF16),
