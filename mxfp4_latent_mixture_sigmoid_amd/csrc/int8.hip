@@ -407,8 +407,8 @@ void tile_kernel(const I8Args g, int gx, int gy)
 // halves ahead of their reads.
 //
 // 8192 x (2 x 14336) x 7168 gated takes 1.20 ms, 2.8 POP/s (a library product of 8-bit codes of these sizes
-// without scales or gate: 1.58 ms), 8192 x 7168 x 14336 0.61 ms. The matrix cores are busy 69% of the
-// clocks, and the clock is what bounds it: with codes as they come the card runs this at 1.72 GHz of its 2.4
+// without scales or gate: 1.58 ms), 8192 x 7168 x 14336 0.61 ms. The matrix cores are busy 67 to 69% of the
+// clocks, and the clock is what bounds it: with codes as they come the card runs this at 1.72 to 1.75 GHz of its 2.4
 // (codes that are all zero: 1.0 ms), so that what is saved is energy. The 16x16x64 instruction moves a
 // fifth less through the register files than 32x32x32 (1.45 ms so), four waves 128 x 128 a third less
 // through the LDS than eight of 128 x 64 (1.42 ms).
