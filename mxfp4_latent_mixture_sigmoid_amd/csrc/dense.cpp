@@ -62,8 +62,8 @@ bool direct(const int8_t *x, int64_t ldx, int64_t K) { return aligned(x, 16) && 
 
 int64_t workspace_bytes_for(const moe_linear_config *c, int64_t T) { return align_up(T * i8_stages(c->k) * I8_STAGE); }
 
-// More than a few hundred workgroups come in tiles of 128 x 128 at least, 512 threads each; restaging takes a
-// thread per 16 codes.
+// More than a round of workgroups comes in tiles of 128 columns at least and of 128 rows or all there are, of 512
+// threads at most; restaging takes a thread per 16 codes.
 constexpr int64_t XCD_PAD = 8;   // the grid is rounded up to the XCDs
 bool linear_fits(const moe_linear_config *c, int64_t T)
 {

@@ -617,23 +617,28 @@ void wide_kernel(const I8Args g, int gx, int gy)
     }
 }
 
-// Rows of K codes at any alignment -> rows of `width` codes (a multiple of 16), zero past K.
-__global__ __launch_bounds__(256) void restage_kernel(const int8_t *x, int64_t ldx, int K, int chunks, int64_t total,
-                                                      int8_t *dst)
+// Rows of K codes at any alignment -> rows of 16 `chunks` codes, zero past K. The chunk that crosses K is loaded from 16
+// codes before K and shifted into place; one by one its codes took every wave 16 loads (4745 x 4657 codes: 10.3 us, so 12.1).
+__global__ __launch_bounds__(256) void restage_kernel(const int8_t *x, int64_t ldx, int K, uint32_t chunks,
+                                                      uint32_t total, int8_t *dst)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x;   // below 2^32: the host checks
     if (i >= total)
         return;
-    const int64_t r = i / chunks;
-    const int c = (int)(i % chunks) * 16;
-    const int8_t *s = x + r * ldx + c;
-    int8_t v[16];
-    if (c + 16 <= K)
-        __builtin_memcpy(v, s, 16);
-    else
+    const uint32_t r = i / chunks;
+    const int c = (int)(i - r * chunks) * 16;
+    const int8_t *s = x + r * ldx;
+    u32x4_t v{0, 0, 0, 0};
+    if (K >= 16) {
+        __builtin_memcpy(&v, s + min(c, K - 16), 16);
+        v = drop_bytes(v, max(c - (K - 16), 0));
+    } else {
+        int8_t few[16];
         for (int j = 0; j < 16; j++)
-            v[j] = c + j < K ? s[j] : (int8_t)0;
-    __builtin_memcpy(dst + i * 16, v, 16);
+            few[j] = c + j < K ? s[c + j] : (int8_t)0;
+        __builtin_memcpy(&v, few, 16);
+    }
+    *reinterpret_cast<u32x4_t *>(dst + (int64_t)i * 16) = v;
 }
 
 // One thread per lane of a block.
@@ -743,10 +748,10 @@ hipError_t launch_many(const I8Args &g, hipStream_t st)
 } // namespace
 
 // Passing rows through registers saves the restaging launch and its pass over x, and costs some of the product's
-// time: 1 x 1000 x 1000 4.0 us against 5.6, 450 x 512 x 1237 5.0 against 7, 777 x 1001 x 3583 12.1 against
-// 12.5, 64 x 7168 x 4351 14.1 against 14.3; but 64 x 28672 x 7167 44 against 39. Many tokens are restaged: 600 x
-// 4096 x 2047 16.6 against 18.4 with 128 x 128 tiles fed from registers, 2504 x 1920 x 356 12.4 against 18.2, though
-// 3000 x 1000 x 999 13.4 against 12.1.
+// time: 1 x 1000 x 1000 3.5 us against 5.1, 450 x 512 x 1237 5.2 against 6.7, 777 x 1001 x 3583 12.1 against
+// 12.6, 32 x 28672 x 7167 34.7 against 35.9; but 64 x 28672 x 7167 44.9 against 39.0. Many tokens are restaged: 600 x
+// 4096 x 2047 15.5 against 18.4 with 128 x 128 tiles fed from registers, 2504 x 1920 x 356 11.8 against 18.2, though
+// 3000 x 1000 x 999 13.2 against 12.1.
 bool i8_takes_any_rows(const I8Args &g)
 {
     return g.K >= 16 && !many(g) && (int64_t)g.T * g.nblk * 16 * g.K <= (int64_t)1 << 33;
@@ -790,9 +795,8 @@ hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
 
 hipError_t launch_i8_restage(const int8_t *x, int64_t ldx, int T, int K, int8_t *dst, hipStream_t st)
 {
-    const int chunks = (int)i8_stages(K) * (I8_STAGE / 16);
-    const int64_t total = (int64_t)T * chunks;
-    hipLaunchKernelGGL(restage_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st, x, ldx, K, chunks, total,
+    const uint32_t chunks = (uint32_t)i8_stages(K) * (I8_STAGE / 16), total = (uint32_t)T * chunks;
+    hipLaunchKernelGGL(restage_kernel, dim3((total + 255) / 256), dim3(256), 0, st, x, ldx, K, chunks, total,
                        dst);
     return hipGetLastError();
 }
