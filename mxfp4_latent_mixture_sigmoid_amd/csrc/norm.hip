@@ -378,23 +378,46 @@ __global__ __launch_bounds__(256) void dequantise_kernel(const int8_t *codes, in
 
 // One chunk of 8 values per thread up to 8192 columns, so that a row's loads are all in flight at once and its
 // reductions short: 1 x 7168, every output: 1024 threads 4.1 us, 512 with two chunks 4.8, 256 with four
-// 6.0; 8192 x 7168 FP32: 134, 139, 152. With many BF16 rows, two chunks keep more bytes in flight:
-// 8192 x 7168 to codes 78 us against 85.
+// 6.0; 8192 x 7168 FP32: 134, 139, 152. With many BF16 rows, two chunks keep more bytes in flight: 8192 x 7168 to
+// codes 78 us against 85, 8192 x 3000 sum and codes 34 against 41, 8192 x 5120 (320 threads) 51 against 58 with
+// 512; and up to 1024 columns a wave with two for any rows: 8192 x 1024 sum and codes 11.9 us against 17.3
+// with 256 threads (FP32 19.8 against 18.5), 4 x 1024 the same. 2560 columns by 320 threads: 8192 rows 29 us, by 512 35.
 template <typename X, bool NORM>
 hipError_t launch_rows(const moe_norm_args &a, hipStream_t st)
 {
     const dim3 rows((unsigned)a.T), quarter((unsigned)((a.T + 3) / 4));
     const int H = a.H;
-    if (H <= 64 * CHUNK)
+    if (H <= 64 * CHUNK) {
         hipLaunchKernelGGL((norm_kernel<X, 64, 1, NORM>), quarter, dim3(256), 0, st, a);
-    else if (H <= 256 * CHUNK)
+        return hipGetLastError();
+    }
+    if constexpr (sizeof(X) == 2) {
+        const bool many = a.T >= MANY_ROWS;
+        if (H <= 64 * CHUNK * 2) {
+            hipLaunchKernelGGL((norm_kernel<X, 64, 2, NORM>), quarter, dim3(256), 0, st, a);
+            return hipGetLastError();
+        }
+        if (H > 320 * CHUNK && H <= 256 * CHUNK * 2 && many) {
+            hipLaunchKernelGGL((norm_kernel<X, 256, 2, NORM>), rows, dim3(256), 0, st, a);
+            return hipGetLastError();
+        }
+        if (H > 512 * CHUNK && H <= 320 * CHUNK * 2 && many) {
+            hipLaunchKernelGGL((norm_kernel<X, 320, 2, NORM>), rows, dim3(320), 0, st, a);
+            return hipGetLastError();
+        }
+        if (H > 512 * CHUNK && H <= 512 * CHUNK * 2 && many) {
+            hipLaunchKernelGGL((norm_kernel<X, 512, 2, NORM>), rows, dim3(512), 0, st, a);
+            return hipGetLastError();
+        }
+    }
+    if (H <= 256 * CHUNK)
         hipLaunchKernelGGL((norm_kernel<X, 256, 1, NORM>), rows, dim3(256), 0, st, a);
+    else if (H <= 320 * CHUNK)
+        hipLaunchKernelGGL((norm_kernel<X, 320, 1, NORM>), rows, dim3(320), 0, st, a);
     else if (H <= 512 * CHUNK)
         hipLaunchKernelGGL((norm_kernel<X, 512, 1, NORM>), rows, dim3(512), 0, st, a);
-    else if (H <= 1024 * CHUNK && (a.T < MANY_ROWS || sizeof(X) == 4))
+    else if (H <= 1024 * CHUNK)
         hipLaunchKernelGGL((norm_kernel<X, 1024, 1, NORM>), rows, dim3(1024), 0, st, a);
-    else if (H <= 512 * CHUNK * 2)
-        hipLaunchKernelGGL((norm_kernel<X, 512, 2, NORM>), rows, dim3(512), 0, st, a);
     else if (H <= 1024 * CHUNK * 2)
         hipLaunchKernelGGL((norm_kernel<X, 1024, 2, NORM>), rows, dim3(1024), 0, st, a);
     else

@@ -56,7 +56,7 @@ def guarded(T, n, dtype, pad=3):
     return view, untouched
 
 
-# widths on both sides of every kernel's limit (512, 2048, 4096, 8192, 16384) and past the last
+# widths on both sides of every limit of few rows (512, 2048, 4096, 8192, 16384; 1024 and 2560 are below) and past the last
 WIDTHS = [1, 7, 8, 100, 511, 512, 513, 2048, 2051, 4096, 4097, 7168, 8193, 16384, 16391, 40001]
 
 
@@ -80,6 +80,32 @@ def test_norm_all_outputs(H, dtype):
     if np.all(lost <= 0.01 * R.scales(y)[:, None]):
         R.check_codes(r.codes.cpu().numpy(), f64(r.scales), y, R.NORM_REL + 2e-6, "codes")
     assert ok_o() and ok_q() and ok_s()
+
+
+@pytest.mark.parametrize("T,H", [(5, 1024), (6, 1025), (3, 2560), (3, 2561), (1025, 1000), (1024, 2048), (1030, 2555),
+                                 (1027, 2561), (1025, 4096), (1024, 4097), (1025, 5120), (1026, 5121), (1024, 8192),
+                                 (1023, 5000)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_many_rows(T, H, dtype):
+    """Both sides of the limits for many rows (1024), and of 1024, 2560 and 5120 columns."""
+    from mxfp4_latent_mixture_sigmoid_amd import quantise, rms_norm
+    g = gen(T + H)
+    x, d = rows(T, H, dtype, g, pad=3, offset=1, sigma=2.0), rows(T, H, BF16, g, pad=8)
+    w = (1 + 0.1 * torch.randn(H, generator=g)).bfloat16().cuda()
+    out, ok_o = guarded(T, H, BF16)
+    codes, ok_q = guarded(T, H, torch.int8)
+    total, ok_s = guarded(T, H, dtype)
+    r = rms_norm(x, w, 1e-5, delta=d, sum=total, out=out, codes=codes)
+    s, y = R.norm(f64(x), f64(d), f64(w), float(np.float32(1e-5)))
+    size = R.B if dtype is BF16 else 0
+    R.check(f64(r.sum), s, np.abs(s) * (size + 2 * R.U), "sum")
+    lost = 2 * R.U * (np.abs(f64(x)) + np.abs(f64(d))) * np.abs(y) / np.maximum(np.abs(s), 1e-30)
+    R.check(f64(r.out), y, np.abs(y) * (R.B + R.NORM_REL) + 2 * lost, "out")
+    assert ok_o() and ok_q() and ok_s()
+    got, want = f64(r.codes) * f64(r.scales)[:, None], y   # half a step, and the value's and the scale's error
+    assert (np.abs(got - want) <= R.scales(y)[:, None] * (0.5 + 127 * (R.NORM_REL + 4e-6)) + 2 * lost).all()
+    q, sc = quantise(x)
+    R.check_codes(q.cpu().numpy(), f64(sc), f64(x), 0.0, "quantise")
 
 
 @pytest.mark.parametrize("T", [1, 2, 4, 5, 64, 1000])
