@@ -381,7 +381,8 @@ __global__ __launch_bounds__(256) void dequantise_kernel(const int8_t *codes, in
 // 6.0; 8192 x 7168 FP32: 134, 139, 152. With many BF16 rows, two chunks keep more bytes in flight: 8192 x 7168 to
 // codes 78 us against 85, 8192 x 3000 sum and codes 34 against 41, 8192 x 5120 (320 threads) 51 against 58 with
 // 512; and up to 1024 columns a wave with two for any rows: 8192 x 1024 sum and codes 11.9 us against 17.3
-// with 256 threads (FP32 19.8 against 18.5), 4 x 1024 the same. 2560 columns by 320 threads: 8192 rows 29 us, by 512 35.
+// with 256 threads (FP32 19.8 against 18.5), 4 x 1024 the same. 2560 columns by 320 threads: 8192 rows 29 us, by
+// 512 35.
 template <typename X, bool NORM>
 hipError_t launch_rows(const moe_norm_args &a, hipStream_t st)
 {
