@@ -568,3 +568,25 @@ def test_python_refusals():
     layer.close()
     with pytest.raises(RuntimeError):
         layer.forward(q, s)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("K", [40, 500, 1000, 2500, 4000, 7168, 14336, 17000])
+def test_codes_are_the_quotients_by_the_stored_scale(K, dtype):
+    """scales = max|x| / 127 and codes = x / scale, each one FP32 division rounded once, bit for bit; many of the
+    values lie as near to a half between two codes as their type allows."""
+    from mxfp4_latent_mixture_sigmoid_amd import quantise
+    T, g = 60, gen(K)
+    top = torch.exp(2 * torch.randn(T, 1, generator=g)).to(dtype).float()
+    half = torch.randint(-127, 127, (T, K), generator=g) + 0.5
+    x = (top / 127 * half).to(dtype)
+    bits = {BF16: torch.int16, F32: torch.int32}[dtype]
+    x = (x.view(bits) + torch.randint(-1, 2, (T, K), generator=g).to(bits)).view(dtype)
+    x[:, :1] = top.to(dtype)
+    x[50:55] *= 2.0 ** -80       # rows that are lifted first
+    x[55:60] *= 2.0 ** 90
+    codes, scales = quantise(x.cuda())
+    f = x.float().numpy()
+    want = np.abs(f).max(1) / np.float32(127)
+    assert want.dtype == np.float32 and np.array_equal(scales.cpu().numpy(), want)
+    assert np.array_equal(codes.cpu().numpy(), np.rint(f / want[:, None]).astype(np.int8))
