@@ -282,6 +282,10 @@ void moe_destroy(moe_handle *h);
  * pointers, caller's stream, no allocation, deterministic results).
  * ------------------------------------------------------------------------------------------- */
 
+/* Largest row width of moe_norm, moe_quantise and moe_dequantise: 2^31 - 2^13, past which a column index and a
+ * step of the kernel do not fit 32 bits. Wider rows are MOE_ERR_UNSUPPORTED. */
+#define MOE_MAX_WIDTH 2147475456
+
 /* Element types of the norm's and quantiser's rows and of the products' outputs. */
 typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type;
 
@@ -301,7 +305,7 @@ typedef struct {
     int8_t *codes;        /* [T, H], or NULL                                        */
     float *scales;        /* [T], exactly when codes is given                       */
     int64_t ldx, ldd, lds, ldo, ldc;   /* row strides of x, delta, sum, out, codes  */
-    int32_t T, H;         /* T >= 0 (0 enqueues nothing), H >= 1                    */
+    int32_t T, H;         /* T >= 0 (0 enqueues nothing), H in 1..MOE_MAX_WIDTH     */
     int32_t x_type;       /* moe_type                                               */
     float eps;            /* >= 0                                                   */
 } moe_norm_args;

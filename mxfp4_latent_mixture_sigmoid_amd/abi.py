@@ -62,6 +62,7 @@ class MoeRouting(ctypes.Structure):
 TYPE_BF16 = 0
 TYPE_F32 = 1
 LINEAR_MAX_K = 131071   # MOE_LINEAR_MAX_K
+MAX_WIDTH = 2147475456  # MOE_MAX_WIDTH
 
 
 class NormArgs(ctypes.Structure):

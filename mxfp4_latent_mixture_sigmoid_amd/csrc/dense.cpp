@@ -79,6 +79,8 @@ moe_status moe_norm(const moe_norm_args *a, void *stream)
 {
     if (!a || a->T < 0 || a->H < 1 || !valid_type(a->x_type) || !(a->eps >= 0.f))
         return MOE_ERR_INVALID_ARG;
+    if (a->H > MOE_MAX_WIDTH)
+        return MOE_ERR_UNSUPPORTED;
     if (a->T == 0)
         return MOE_OK;
     if ((!a->sum && !a->out && !a->codes) || !a->codes != !a->scales)
@@ -97,6 +99,8 @@ moe_status moe_quantise(const void *x, int32_t x_type, int64_t ldx, int32_t T, i
 {
     if (T < 0 || K < 1 || !valid_type(x_type))
         return MOE_ERR_INVALID_ARG;
+    if (K > MOE_MAX_WIDTH)
+        return MOE_ERR_UNSUPPORTED;
     if (T == 0)
         return MOE_OK;
     if (!valid_rows(x, ldx, K, type_size(x_type)) || !valid_rows(codes, ldc, K, 1) || !scales || !aligned(scales, 4))
@@ -118,6 +122,8 @@ moe_status moe_dequantise(const int8_t *codes, int64_t ldc, const float *scales,
 {
     if (T < 0 || K < 1)
         return MOE_ERR_INVALID_ARG;
+    if (K > MOE_MAX_WIDTH)
+        return MOE_ERR_UNSUPPORTED;
     if (T == 0)
         return MOE_OK;
     if (!valid_rows(codes, ldc, K, 1) || !scales || !aligned(scales, 4) || !valid_rows(out, ldo, K, 2))

@@ -280,6 +280,7 @@ template <typename X, bool NORM>
 __global__ __launch_bounds__(1024) void norm_long_kernel(const moe_norm_args a)
 {
     constexpr int NT = 1024;
+    static_assert(MOE_MAX_WIDTH <= INT32_MAX - (NT * CHUNK - 1), "the column past the last fits its type");
     __shared__ float sh_sum[NT / WAVE];
     __shared__ uint32_t sh_max[NT / WAVE];
     const int t = threadIdx.x;
@@ -469,7 +470,7 @@ hipError_t launch_norm(const moe_norm_args &all, bool norm, hipStream_t st)
 hipError_t launch_dequantise(const int8_t *codes, int64_t ldc, const float *scales, int32_t T, int32_t K, uint16_t *out,
                              int64_t ldo, hipStream_t st)
 {
-    const int64_t chunks = (K + CHUNK - 1) / CHUNK, rows = MAX_THREADS / chunks;
+    const int64_t chunks = ((int64_t)K + CHUNK - 1) / CHUNK, rows = MAX_THREADS / chunks;
     for (int64_t r = 0; r < T; r += rows) {
         const int64_t total = (T - r < rows ? T - r : rows) * chunks;
         hipLaunchKernelGGL(dequantise_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st, codes + r * ldc, ldc,

@@ -149,3 +149,16 @@ def test_workspace_serves_every_smaller_batch(n, k, glu):
     sizes = sorted({0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 500, 512, 513, 1024, 3000, 8192})
     need = [abi.linear_query(c, T)[1] for T in sizes]
     assert need == sorted(need)
+
+
+@pytest.mark.parametrize("width", [abi.MAX_WIDTH + 1, 2 ** 31 - 8, 2 ** 31 - 7, 2 ** 31 - 1])
+@pytest.mark.parametrize("T", [0, 1])
+def test_rows_wider_than_the_kernels_indexes(width, T):
+    """Columns are 32-bit indexes that go up in steps of 8192: wider rows would wrap, and are refused by all three."""
+    L = abi.lib()
+    assert abi.MAX_WIDTH == 2 ** 31 - 8192
+    assert f"MOE_MAX_WIDTH {abi.MAX_WIDTH}" in open(os.path.join(ROOT, "include", "mxmoe.h")).read()
+    assert _norm(H=width, T=T, ldx=width, ldo=width) == UNSUPPORTED
+    assert L.moe_quantise(A, 0, width, T, width, A, width, A, None) == UNSUPPORTED
+    assert L.moe_dequantise(A, width, A, T, width, A, width, None) == UNSUPPORTED
+    assert _norm(H=abi.MAX_WIDTH, T=0) == abi.Status.OK
