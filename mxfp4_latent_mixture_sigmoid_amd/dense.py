@@ -15,6 +15,7 @@ from . import abi
 
 _TYPES = {torch.bfloat16: abi.TYPE_BF16, torch.float32: abi.TYPE_F32}
 _BF16, _INT8 = (torch.bfloat16,), (torch.int8,)
+_INT32_MAX = 2 ** 31 - 1   # rows and columns cross the C ABI as 32-bit integers, which ctypes cuts without a word
 _pack = abi.NORM_ARGS.pack
 _raw_stream = torch._C._cuda_getCurrentRawStream   # of a GPU: its handle, without an object around it
 _current_gpu = torch._C._cuda_getDevice
@@ -41,6 +42,8 @@ def _bad_rows(name, t, dtypes, index, shape):
                 f"strides {t.stride()}")
     if shape is not None and t.shape != shape:
         return f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}"
+    if max(t.shape) > _INT32_MAX:
+        return f"{name}: shape {tuple(t.shape)}, expected at most {_INT32_MAX} rows and columns"
     return f"{name}: on {t.device}, expected GPU {index}"
 
 
@@ -48,7 +51,8 @@ def _rows(name, t, dtypes, index, shape=None):
     """Row stride of a [T, width] tensor on GPU `index`, after checking it."""
     strides, sizes = t.stride(), t.shape
     if (t.dtype not in dtypes or len(strides) != 2 or (strides[1] != 1 and sizes[1] > 1)
-            or (shape is not None and sizes != shape) or t.get_device() != index):
+            or (shape is not None and sizes != shape) or sizes[0] > _INT32_MAX or sizes[1] > _INT32_MAX
+            or t.get_device() != index):
         raise ValueError(_bad_rows(name, t, dtypes, index, shape))
     # the stride of a single row means nothing (torch reports any value there)
     return strides[0] if sizes[0] > 1 else sizes[1]
@@ -183,6 +187,8 @@ class Int8Linear:
             raise ValueError("up_codes and up_scales go together")
         if up_codes is not None and bias is not None:
             raise ValueError("the gated product takes no bias")
+        if not 0 <= T_max <= _INT32_MAX:
+            raise ValueError(f"T_max: {T_max}, expected 0 to {_INT32_MAX}")
         self.T_max, self.out_dtype = T_max, out_dtype
         _call(codes, stream, (codes, scales, bias, up_codes, up_scales), self._create, codes, scales, bias, up_codes,
               up_scales)
