@@ -433,6 +433,16 @@ __device__ inline void settle(acc_t (&acc)[MF][NF])
             asm volatile("" : "+a"(acc[f][j]));   // no copy of a sum moves across
 }
 
+// Between what lanes of a wave write to LDS and what its other lanes read of it, or write over it next: the memory
+// model orders the two only past a fence and a barrier, though a wave's accesses to LDS are done in order anyway, so
+// that neither costs an instruction here.
+__device__ inline void meet_lanes()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // MF and NF: row and column fragments per wave; tiles of 32 MF x 32 NF. 128-token tiles take 80 KiB of LDS or
 // less and half the registers, so that two workgroups share a CU. With 7 column fragments a tile loads, but
 // does not use, the two row blocks after its own.
@@ -607,6 +617,7 @@ void wide_kernel(const I8Args g, int gx, int gy)
             else
                 *reinterpret_cast<uint2 *>(at + j * 32) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
         }
+        meet_lanes();
 #pragma unroll
         for (int i = 0; i < (16 * PIECES + WAVE - 1) / WAVE; i++) {
             const int p = i * WAVE + lane, r = p / PIECES, c = p % PIECES;
@@ -614,6 +625,7 @@ void wide_kernel(const I8Args g, int gx, int gy)
             if (r < 16 && row < g.T)
                 store16(g, row, n1 + c * (16 / SIZE), *reinterpret_cast<const u32x4_t *>(stage + r * PITCH + c * 16));
         }
+        meet_lanes();
     }
 }
 

@@ -590,3 +590,37 @@ def test_codes_are_the_quotients_by_the_stored_scale(K, dtype):
     want = np.abs(f).max(1) / np.float32(127)
     assert want.dtype == np.float32 and np.array_equal(scales.cpu().numpy(), want)
     assert np.array_equal(codes.cpu().numpy(), np.rint(f / want[:, None]).astype(np.int8))
+
+
+# one for each large tile, plain and gated: 128 x 64, 128 x 128, 256 x 128, 256 x 224, 256 x 256
+TILES = [(500, 4090, 128, 0), (1000, 4090, 128, 0), (1000, 8000, 3000, 0), (1800, 6900, 4096, 0), (2040, 8190, 2500, 0),
+         (500, 2040, 128, 1), (1000, 2040, 128, 1), (1020, 3500, 3400, 1), (2040, 3500, 3000, 1)]
+
+
+@pytest.mark.parametrize("T,N,K,glu", TILES)
+def test_every_output_of_the_large_tiles(T, N, K, glu):
+    """Outputs change hands between a wave's lanes on their way out: every one exact, in both types, call after call.
+    Gated: a gate of 127 * 9 / 8, whose silu is the value itself; 8 U for the hardware's exponential and
+    reciprocal and the products (and half a BF16 unit)."""
+    from mxfp4_latent_mixture_sigmoid_amd import Int8Linear
+    g = torch.Generator(device="cuda").manual_seed(N)
+    w = torch.randint(-9, 10, (N, K), generator=g, dtype=torch.int8, device="cuda")
+    x = torch.randint(-9, 10, (T, K), generator=g, dtype=torch.int8, device="cuda")
+    one, sx = torch.ones(N, device="cuda"), torch.ones(T, device="cuda")
+    gate = torch.zeros_like(w)
+    gate[:, 0] = 127
+    if glu:
+        x[:, 0] = 9
+    want = (x.float() @ w.t().float().contiguous()) * (9 * 127 / 8 if glu else 1)   # whole numbers below 2^24
+    for dtype in (F32, BF16):
+        kw = dict(T_max=T, out_dtype=dtype)
+        layer = Int8Linear(gate, one / 8, up_codes=w, up_scales=one, **kw) if glu else Int8Linear(w, one, **kw)
+        out, ok = guarded(T, N, dtype)
+        for _ in range(3):
+            out.zero_()
+            layer.forward(x, sx, out=out)
+            if glu:
+                assert ((out.float() - want).abs() <= (8 * R.U + (R.B if dtype is BF16 else 0)) * want.abs()).all()
+            else:
+                assert torch.equal(out, want.to(dtype))
+        assert ok()
