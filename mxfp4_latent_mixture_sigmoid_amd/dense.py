@@ -209,13 +209,14 @@ class Int8Linear:
         self.packed = torch.empty(packed_bytes, dtype=torch.uint8, device=codes.device)
         self.workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=codes.device)
         self.handle = abi.linear_create(self.cfg, codes, scales, up_codes, up_scales, bias, self.packed, stream)
+        self._streams = {stream}   # that the allocator knows to use the buffers: their own, and those of the calls
         self._buffers = self.workspace.data_ptr(), self.workspace.numel()
 
     def forward(self, x, scales, out=None, stream=None):
         """The product for codes x [T, K] with FP32 scales [T]; returns out [T, N]."""
         if stream is None and (index := self.packed.get_device()) == _current_gpu():
             return self._forward(x, scales, out, index, _raw_stream(index))
-        return _call(self.packed, stream, (x, scales, out, self.packed, self.workspace), self._forward, x, scales, out)
+        return _call(self.packed, stream, (x, scales, out), self._forward, x, scales, out)
 
     def _forward(self, x, scales, out, index, stream):
         ldx = _rows("x", x, _INT8, index)
@@ -228,6 +229,11 @@ class Int8Linear:
             out = torch.empty_strided((T, ldo), (ldo, 1), dtype=self.out_dtype, device=x.device)
         else:
             ldo = _rows("out", out, (self.out_dtype,), index, (T, self.N))
+        if stream not in self._streams:   # once for each: a layer dropped while it runs there keeps its memory that long
+            used = torch.cuda.current_stream(index)
+            self.packed.record_stream(used)
+            self.workspace.record_stream(used)
+            self._streams.add(stream)
         status = abi.lib().moe_linear_forward(self.handle, x.data_ptr(), ldx, scales.data_ptr(), T, out.data_ptr(), ldo,
                                               *self._buffers, stream)
         if status:

@@ -1,5 +1,7 @@
 """Host-side checks of the dense 8-bit path's Python functions: what they refuse before any GPU work, and how they
 treat streams. Tensors here have no GPU (device index -1) or are stand-ins; no call reaches the library."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -38,3 +40,36 @@ def test_token_limit_past_32_bits_is_refused(T_max):
     w, s = torch.zeros(4, 4, dtype=torch.int8), torch.zeros(4)
     with pytest.raises(ValueError, match="T_max"):
         dense.Int8Linear(w, s, T_max=T_max)
+
+
+class Buffer:
+    """Stands for a layer's own memory; keeps the streams it was recorded for."""
+
+    def __init__(self):
+        self.streams = []
+
+    def get_device(self):
+        return -1
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+def test_a_layer_tells_the_allocator_which_streams_use_it(monkeypatch):
+    """Built on stream 5, called under others: the packed weights are recorded for each of those, once."""
+    current = [5]
+    monkeypatch.setattr(dense, "_current_gpu", lambda: -1)
+    monkeypatch.setattr(dense, "_raw_stream", lambda index: current[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index=None: f"stream {current[0]}")
+    monkeypatch.setattr(dense.abi, "lib", lambda: SimpleNamespace(moe_linear_forward=lambda *a: 0))
+    monkeypatch.setattr(dense.abi, "linear_query", lambda cfg, T: (256, 256))
+    monkeypatch.setattr(dense.abi, "linear_create", lambda *a: None)
+    layer = object.__new__(dense.Int8Linear)
+    layer.handle, layer.T_max, layer.out_dtype = None, 4, torch.float32
+    q, s = torch.zeros(4, 8, dtype=torch.int8), torch.zeros(4)
+    layer._create(q, s, None, None, None, -1, 5)
+    layer.packed, layer.workspace = Buffer(), Buffer()
+    for handle in (5, 7, 7, 5, 9, 7):
+        current[0] = handle
+        layer.forward(q, s)
+    assert layer.packed.streams == ["stream 7", "stream 9"]

@@ -624,3 +624,28 @@ def test_every_output_of_the_large_tiles(T, N, K, glu):
             else:
                 assert torch.equal(out, want.to(dtype))
         assert ok()
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_memory_of_a_layer_dropped_while_it_runs(given):
+    """A layer built on one stream, called on a busy other one and dropped: its packed weights are not handed out
+    again before that call is done, and its result is right."""
+    g = gen(8)
+    layer, w, s, _ = make(512, 1024, 0, g, T_max=64)
+    x, sx = codes_rows(64, 1024, g), torch.ones(64, device="cuda")
+    want = layer.forward(x, sx)
+    torch.cuda.synchronize()
+    at, size = layer.packed.data_ptr(), layer.packed.numel()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    if given:
+        got = layer.forward(x, sx, stream=side)
+    else:
+        with torch.cuda.stream(side):
+            got = layer.forward(x, sx)
+    del layer
+    taken = [torch.full((size,), 1, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(t.data_ptr() != at for t in taken)
+    side.synchronize()
+    assert torch.equal(got, want)
