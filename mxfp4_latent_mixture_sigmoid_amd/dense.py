@@ -75,6 +75,8 @@ def _call(x, stream, tensors, f, *args):
     if stream is None:
         with torch.cuda.device(index):
             return f(*args, index, _raw_stream(index))
+    if stream.device_index != index:
+        raise ValueError(f"stream: on GPU {stream.device_index}, expected GPU {index}")
     with torch.cuda.stream(stream):
         got = f(*args, index, stream.cuda_stream)
     for t in tensors:

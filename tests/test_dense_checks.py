@@ -73,3 +73,12 @@ def test_a_layer_tells_the_allocator_which_streams_use_it(monkeypatch):
         current[0] = handle
         layer.forward(q, s)
     assert layer.packed.streams == ["stream 7", "stream 9"]
+
+
+def test_a_stream_of_another_gpu_is_refused():
+    x = SimpleNamespace(get_device=lambda: 0)
+    stream = SimpleNamespace(device_index=1, device=torch.device("cuda", 1), cuda_stream=3)
+    for f in (lambda: dense.rms_norm(x, stream=stream), lambda: dense.quantise(x, stream=stream),
+              lambda: dense.dequantise(x, None, stream=stream)):
+        with pytest.raises(ValueError, match="stream: on GPU 1, expected GPU 0"):
+            f()
