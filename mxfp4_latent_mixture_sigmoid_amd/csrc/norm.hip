@@ -142,19 +142,31 @@ __device__ inline void store_codes(int8_t *row, int c, int n, float *v, const Co
 }
 
 // Reductions over the NT threads of a row, in a fixed order; every thread gets the result. `sh` holds
-// one word per wave and is not reused by the other reduction.
-template <int NT>
-__device__ inline float row_sum(float v, float *sh)
+// one word per wave (and chunk) and is not reused by the other reduction.
+//
+// The sum is over part[i] of chunk t + i * NT of each thread t: each 64 consecutive chunks by their wave, then
+// those sums as lanes of one wave, in their place in the row. So it is the same bits whatever NT and NV, and a row's
+// norm does not depend on how many rows come with it, which the choice of the two looks at. (Adding a thread's chunks
+// up first saves a wave sum and no time: 8192 x 7168 sum and codes 74 us both. Adding the waves' sums one by one took
+// 16 registers more with 32 of them, and with those half of the waves: 8192 x 12288 223 us against 154.)
+template <int NT, int NV>
+__device__ inline float row_sum(const float *part, float *sh)
 {
-    v = wave_sum_f32(v);
-    if constexpr (NT > WAVE) {
-        if ((threadIdx.x & (WAVE - 1)) == 0)
-            sh[threadIdx.x / WAVE] = v;
-        __syncthreads();
-        v = 0.f;
+    constexpr int SUMS = NV * (NT / WAVE);
+    static_assert(SUMS <= WAVE, "one for each lane");
+    const int lane = threadIdx.x & (WAVE - 1);
+    float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < NT / WAVE; w++)
-            v += sh[w];
+    for (int i = 0; i < NV; i++) {
+        const float sum = wave_sum_f32(part[i]);
+        if (NT == WAVE)
+            v += sum;
+        else if (lane == 0)
+            sh[i * (NT / WAVE) + threadIdx.x / WAVE] = sum;
+    }
+    if constexpr (NT > WAVE) {
+        __syncthreads();
+        v = wave_sum_f32(lane < SUMS ? sh[lane] : 0.f);
     }
     return v;
 }
@@ -198,7 +210,7 @@ __device__ inline float row_scale(uint32_t top, Coder &k)
 template <typename X, int NT, int NV, bool NORM>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_kernel(const moe_norm_args a)
 {
-    __shared__ float sh_sum[NT / WAVE];
+    __shared__ float sh_sum[NV * (NT / WAVE)];
     __shared__ uint32_t sh_max[NT / WAVE];
     constexpr int ROWS = NT < 256 ? 256 / NT : 1;
     const int t = threadIdx.x % NT;
@@ -233,13 +245,15 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_kernel(const moe_nor
             for (int i = 0; i < NV; i++)
                 store_row(s, (t + i * NT) * CHUNK, a.H, v[i]);
         }
-        float ss = 0.f;
+        float ss[NV];
 #pragma unroll
-        for (int i = 0; i < NV; i++)
+        for (int i = 0; i < NV; i++) {
+            ss[i] = 0.f;
 #pragma unroll
             for (int j = 0; j < CHUNK; j++)
-                ss = fmaf(v[i][j], v[i][j], ss);
-        const float rstd = 1.f / sqrtf(row_sum<NT>(ss, sh_sum) / (float)a.H + a.eps);
+                ss[i] = fmaf(v[i][j], v[i][j], ss[i]);
+        }
+        const float rstd = 1.f / sqrtf(row_sum<NT, NV>(ss, sh_sum) / (float)a.H + a.eps);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             float w[CHUNK];
@@ -307,7 +321,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const moe_norm_args a)
             for (int j = 0; j < CHUNK; j++)
                 ss = fmaf(v[j], v[j], ss);
         }
-        rstd = 1.f / sqrtf(row_sum<NT>(ss, sh_sum) / (float)a.H + a.eps);
+        rstd = 1.f / sqrtf(row_sum<NT, 1>(&ss, sh_sum) / (float)a.H + a.eps);
     }
     auto scaled = [&](int c, float *v) {
         if constexpr (NORM) {

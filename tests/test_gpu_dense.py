@@ -649,3 +649,30 @@ def test_memory_of_a_layer_dropped_while_it_runs(given):
     assert all(t.data_ptr() != at for t in taken)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("H", [600, 1000, 1024, 2040, 2561, 3000, 4096, 4097, 5120, 5121, 7168, 8192, 9000])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_row_s_norm_in_any_batch(H, dtype):
+    """A row's norm is the same bits whatever batch it comes with (1024 rows take other kernels than 1023)."""
+    from mxfp4_latent_mixture_sigmoid_amd import quantise, rms_norm
+    T, g = 1500, gen(H)
+    x, d = rows(T, H, dtype, g, sigma=2.0), rows(T, H, BF16, g)
+    w = (1 + 0.1 * torch.randn(H, generator=g)).bfloat16().cuda()
+    whole, plain = rms_norm(x, w, delta=d, sum=True, codes=True), quantise(x)
+    for first, n in ((0, 1), (7, 64), (300, 1023), (400, 1024), (100, 1400)):
+        part = slice(first, first + n)
+        for a, b in zip(rms_norm(x[part], w, delta=d[part], sum=True, codes=True), whole):
+            assert torch.equal(a, b[part]), n
+        for a, b in zip(quantise(x[part]), plain):
+            assert torch.equal(a, b[part]), n
+
+
+def test_a_block_s_token_in_any_batch():
+    H, I, T, g = 3000, 1000, 1300, gen(4)
+    ff, _, _ = block(H, I, T, g)
+    x, d = rows(T, H, BF16, g), rows(T, H, BF16, g)
+    y, total = ff.forward(x, delta=d)
+    for first, n in ((0, 1), (5, 64), (200, 1000), (100, 1100)):
+        a, b = ff.forward(x[first:first + n], delta=d[first:first + n])
+        assert torch.equal(a, y[first:first + n]) and torch.equal(b, total[first:first + n]), n
