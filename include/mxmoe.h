@@ -294,9 +294,9 @@ typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type;
  * Each requested output is rounded once from these values: `sum` = s in x's type, `out` = y in BF16,
  * and `codes` / `scales` = y in 8 bits: scales[t] = max|y[t]| / 127, codes = y / scales[t] rounded to
  * nearest even. A row of zeros has scale 0 and codes 0; a row with a NaN or an infinity in y has
- * scale NaN and codes 0, so that a product of it is NaN as well. A row's outputs are the same bits whatever
- * rows come with it. `sum` may be x itself (same pointer
- * and stride); no other output may overlap an input or another output. */
+ * scale NaN and codes 0, so that a product of it is NaN as well. The norm holds for all finite values, also where
+ * their squares leave FP32's range. A row's outputs are the same bits whatever rows come with it. `sum`
+ * may be x itself (same pointer and stride); no other output may overlap an input or another output. */
 typedef struct {
     const void *x;        /* x_type [T, H]                                          */
     const void *delta;    /* bf16 [T, H] added to x, or NULL                        */

@@ -205,6 +205,26 @@ __device__ inline float row_scale(uint32_t top, Coder &k)
     return stored;
 }
 
+// 1 / sqrt(mean(s^2) + eps) for rows whose squares leave FP32's range: sums past it (values of 2e17 and more in a row
+// of 7168) would take the whole row to zero, and squares below it are lost where mean + eps is under 2^-120 (with an
+// eps that small). Such a row's squares are taken of its values times 2^-80 or 2^100, where no sum of the widest row
+// leaves the range again. The power is given back last for the large, y = s * rstd * 2^-80, and first for the
+// small, y = s * 2^100 * rstd, so that no product underflows that y does not. Rows with a NaN or an infinity come
+// here too, and have the same outputs as without it.
+struct Far {
+    float squares;         // what values are multiplied by before they are squared
+    float before, after;   // and before and after they are multiplied by rstd
+};
+__device__ inline bool in_range(float mean_eps) { return mean_eps >= 0x1p-120f && mean_eps < __builtin_inff(); }
+__device__ inline Far far_factors(float mean_eps)
+{
+    return mean_eps < 0x1p-120f ? Far{0x1p100f, 0x1p100f, 1.f} : Far{0x1p-80f, 1.f, 0x1p-80f};
+}
+__device__ inline float far_rstd(float sum, float H, float eps, const Far &f)
+{
+    return 1.f / sqrtf(sum / H + eps * f.squares * f.squares);
+}
+
 // NT threads per row (64: four rows per workgroup, one per wave; else one workgroup per row), NV
 // chunks of 8 values per thread; H <= NT * NV * 8.
 template <typename X, int NT, int NV, bool NORM>
@@ -253,7 +273,29 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_kernel(const moe_nor
             for (int j = 0; j < CHUNK; j++)
                 ss[i] = fmaf(v[i][j], v[i][j], ss[i]);
         }
-        const float rstd = 1.f / sqrtf(row_sum<NT, NV>(ss, sh_sum) / (float)a.H + a.eps);
+        const float mean = row_sum<NT, NV>(ss, sh_sum) / (float)a.H + a.eps;
+        float rstd = 1.f / sqrtf(mean);
+        if (!in_range(mean)) {   // the same in the whole row
+            const Far far = far_factors(mean);
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                ss[i] = 0.f;
+#pragma unroll
+                for (int j = 0; j < CHUNK; j++) {
+                    const float s = v[i][j] * far.squares;
+                    ss[i] = fmaf(s, s, ss[i]);
+                }
+            }
+            if constexpr (NT > WAVE)
+                __syncthreads();   // every thread has read the first sums
+            rstd = far_rstd(row_sum<NT, NV>(ss, sh_sum), (float)a.H, a.eps, far);
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+#pragma unroll
+                for (int j = 0; j < CHUNK; j++)
+                    v[i][j] = v[i][j] * far.before * rstd * far.after;
+            rstd = 1.f;
+        }
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             float w[CHUNK];
@@ -312,16 +354,28 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const moe_norm_args a)
         }
     };
     float rstd = 1.f;
+    Far far{1.f, 1.f, 1.f};
     if constexpr (NORM) {
-        float ss = 0.f;
-        for (int c = t * CHUNK; c < a.H; c += NT * CHUNK) {
-            float v[CHUNK];
-            summed(c, v);
+        auto squares = [&] {
+            float ss = 0.f;
+            for (int c = t * CHUNK; c < a.H; c += NT * CHUNK) {
+                float v[CHUNK];
+                summed(c, v);
 #pragma unroll
-            for (int j = 0; j < CHUNK; j++)
-                ss = fmaf(v[j], v[j], ss);
+                for (int j = 0; j < CHUNK; j++) {
+                    const float s = v[j] * far.squares;
+                    ss = fmaf(s, s, ss);
+                }
+            }
+            return row_sum<NT, 1>(&ss, sh_sum);
+        };
+        const float mean = squares() / (float)a.H + a.eps;
+        rstd = 1.f / sqrtf(mean);
+        if (!in_range(mean)) {   // the same in the whole row
+            far = far_factors(mean);
+            __syncthreads();   // every thread has read the first sums
+            rstd = far_rstd(squares(), (float)a.H, a.eps, far);
         }
-        rstd = 1.f / sqrtf(row_sum<NT, 1>(&ss, sh_sum) / (float)a.H + a.eps);
     }
     auto scaled = [&](int c, float *v) {
         if constexpr (NORM) {
@@ -329,8 +383,10 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const moe_norm_args a)
             if (a.weight)
                 load_row(static_cast<const uint16_t *>(a.weight), c, a.H, w);
 #pragma unroll
-            for (int j = 0; j < CHUNK; j++)
-                v[j] = a.weight ? v[j] * rstd * w[j] : v[j] * rstd;
+            for (int j = 0; j < CHUNK; j++) {
+                const float y = v[j] * far.before * rstd * far.after;
+                v[j] = a.weight ? y * w[j] : y;
+            }
         }
     };
     Coder coder{0.f, 0.f, 0.f};

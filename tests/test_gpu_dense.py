@@ -676,3 +676,30 @@ def test_a_block_s_token_in_any_batch():
     for first, n in ((0, 1), (5, 64), (200, 1000), (100, 1100)):
         a, b = ff.forward(x[first:first + n], delta=d[first:first + n])
         assert torch.equal(a, y[first:first + n]) and torch.equal(b, total[first:first + n]), n
+
+
+@pytest.mark.parametrize("H", [64, 700, 1500, 3000, 7168, 9000, 20000])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6, 1e30])
+def test_norm_of_rows_whose_squares_leave_the_range(H, dtype, eps):
+    """Rows up to both ends of the type: their squares overflow or vanish, their norm does not. (Bounds as
+    elsewhere, and a BF16 subnormal's half unit, 2^-134.)"""
+    from mxfp4_latent_mixture_sigmoid_amd import rms_norm
+    g, eps32 = gen(H), float(np.float32(eps))
+    sizes = [1.0, 1e15, 2e17, 1e19, 1e25, 3e37, 1e-12, 1e-18, 1e-22, 1e-30, 1e-36, 1e-38, 3e-40, 1e-44]
+    x = (torch.randn(len(sizes) + 2, H, generator=g).clamp(-9, 9).double()
+         * torch.tensor(sizes + [1.0, 0.0]).double()[:, None]).to(dtype)
+    x[len(sizes), 3] = 2.0 ** 120           # one value that is all of the row's norm
+    for n in (1, 1100 if H in (3000, 7168) else 2):
+        xs = x.cuda().repeat(n, 1)
+        w = (1 + 0.1 * torch.randn(H, generator=g)).bfloat16().cuda()
+        r = rms_norm(xs, w, eps, codes=True)
+        _, y = R.norm(f64(x), None, f64(w), eps32)
+        live = np.isfinite(y).all(1)         # 0 / 0 in a row of zeros, as the formula has it
+        assert live.sum() >= len(sizes) - (dtype is BF16)
+        for part in (slice(0, len(x)), slice((n - 1) * len(x), n * len(x))):
+            out, scales, codes = f64(r.out[part]), f64(r.scales[part]), r.codes[part].cpu().numpy()
+            R.check(out[live], y[live], np.abs(y[live]) * (R.B + R.NORM_REL) + 2.0 ** -133, "out")
+            big = live & (np.abs(y).max(1) > 1e-30)      # scales with all their bits
+            R.check_codes(codes[big], scales[big], y[big], R.NORM_REL, "codes")
+            assert np.isnan(out[~live]).all()
