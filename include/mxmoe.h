@@ -344,8 +344,8 @@ typedef struct {
 
 typedef struct moe_linear moe_linear;
 
-/* Sizes of the packed buffer and of the workspace for calls of up to T_max tokens (host only; either
- * output may be NULL). */
+/* Sizes of the packed buffer and of the workspace that any call of up to T_max tokens can do with (host only;
+ * either output may be NULL). */
 moe_status moe_linear_query(const moe_linear_config *cfg, int32_t T_max, size_t *packed_bytes,
                             size_t *workspace_bytes);
 /* Validate, then enqueue the packing of the weights, scales and bias into `packed` (256-byte aligned):
@@ -355,7 +355,9 @@ moe_status moe_linear_query(const moe_linear_config *cfg, int32_t T_max, size_t 
 moe_status moe_linear_create(const moe_linear_config *cfg, const moe_linear_weights *w, void *packed,
                              size_t packed_bytes, void *stream, moe_linear **out);
 /* The product for T >= 0 tokens (0 enqueues nothing). x: codes [T, k]; scales [T]; out: out_type
- * [T, n], must not overlap any input. workspace: 256-byte aligned, >= moe_linear_query(cfg, T). */
+ * [T, n], must not overlap any input. workspace: 256-byte aligned, moe_linear_query(cfg, T) bytes; rows that the
+ * kernels take as they are need none (NULL, 0) -- always those at 16-byte steps of at most 2^22 from a 16-byte
+ * aligned address with k a multiple of 16. MOE_ERR_BUFFER_TOO_SMALL, and nothing enqueued, if it is needed. */
 moe_status moe_linear_forward(moe_linear *l, const int8_t *x, int64_t ldx, const float *scales, int32_t T, void *out,
                               int64_t ldo, void *workspace, size_t workspace_bytes, void *stream);
 /* Free the host handle (not the packed buffer). NULL is a no-op. */

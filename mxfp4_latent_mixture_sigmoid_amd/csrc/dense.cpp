@@ -190,10 +190,9 @@ moe_status moe_linear_forward(moe_linear *l, const int8_t *x, int64_t ldx, const
         return MOE_OK;
     const moe_linear_config *c = &l->cfg;
     if (!valid_rows(x, ldx, c->k, 1) || !scales || !aligned(scales, 4) ||
-        !valid_rows(out, ldo, c->n, type_size(c->out_type)) || !workspace || !aligned(workspace, 256))
+        !valid_rows(out, ldo, c->n, type_size(c->out_type)) || !aligned(workspace, 256) ||
+        (!workspace && workspace_bytes))
         return MOE_ERR_INVALID_ARG;
-    if (workspace_bytes < (size_t)workspace_bytes_for(c, T))
-        return MOE_ERR_BUFFER_TOO_SMALL;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     I8Args g{};
     g.x = x;
@@ -212,6 +211,8 @@ moe_status moe_linear_forward(moe_linear *l, const int8_t *x, int64_t ldx, const
     g.out_type = c->out_type;
     g.direct = direct(x, ldx, c->k);
     if (!g.direct && !i8_takes_any_rows(g)) {
+        if (workspace_bytes < (size_t)workspace_bytes_for(c, T))
+            return MOE_ERR_BUFFER_TOO_SMALL;
         int8_t *staged = static_cast<int8_t *>(workspace);
         const hipError_t e = launch_i8_restage(x, ldx, T, c->k, staged, st);
         if (e != hipSuccess)

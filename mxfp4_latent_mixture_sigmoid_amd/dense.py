@@ -177,8 +177,9 @@ class Int8Linear:
     with ``up_codes`` the gated form silu((x . w^T) * sx * scales) * ((x . w_up^T) * sx * up_scales).
 
     codes, up_codes: int8 [N, K]; scales, up_scales: FP32 [N]; bias: FP32 [N]. They are read only while
-    the packing kernel runs on ``stream`` and may be dropped after construction. Calls of one layer
-    that overlap on different streams share its workspace and have to be serialised by the caller."""
+    the packing kernel runs on ``stream`` and may be dropped after construction. Beside the packed weights a
+    layer holds no device memory, and its calls may overlap on different streams; a call whose rows have to be laid
+    out first (many unaligned ones) allocates room for them."""
 
     def __init__(self, codes, scales, bias=None, up_codes=None, up_scales=None, T_max=8192, out_dtype=torch.bfloat16,
                  stream=None):
@@ -207,12 +208,11 @@ class Int8Linear:
         if bias is not None:
             _vector("bias", bias, self.N, torch.float32, index)
         self.cfg = abi.LinearConfig(self.N, self.K, int(up_codes is not None), _TYPES[self.out_dtype])
-        packed_bytes, ws_bytes = abi.linear_query(self.cfg, self.T_max)
+        packed_bytes, _ = abi.linear_query(self.cfg, self.T_max)
         self.packed = torch.empty(packed_bytes, dtype=torch.uint8, device=codes.device)
-        self.workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=codes.device)
         self.handle = abi.linear_create(self.cfg, codes, scales, up_codes, up_scales, bias, self.packed, stream)
-        self._streams = {stream}   # that the allocator knows to use the buffers: their own, and those of the calls
-        self._buffers = self.workspace.data_ptr(), self.workspace.numel()
+        self._two_rows = abi.linear_query(self.cfg, 2)[1]   # room for rows is in proportion to them, up to its alignment
+        self._streams = {stream}   # that the allocator knows to use the weights: their own, and those of the calls
 
     def forward(self, x, scales, out=None, stream=None):
         """The product for codes x [T, K] with FP32 scales [T]; returns out [T, N]."""
@@ -232,12 +232,15 @@ class Int8Linear:
         else:
             ldo = _rows("out", out, (self.out_dtype,), index, (T, self.N))
         if stream not in self._streams:   # once for each: a layer dropped while it runs there keeps its memory that long
-            used = torch.cuda.current_stream(index)
-            self.packed.record_stream(used)
-            self.workspace.record_stream(used)
+            self.packed.record_stream(torch.cuda.current_stream(index))
             self._streams.add(stream)
-        status = abi.lib().moe_linear_forward(self.handle, x.data_ptr(), ldx, scales.data_ptr(), T, out.data_ptr(), ldo,
-                                              *self._buffers, stream)
+        forward = abi.lib().moe_linear_forward
+        status = forward(self.handle, x.data_ptr(), ldx, scales.data_ptr(), T, out.data_ptr(), ldo, None, 0, stream)
+        if status == abi.Status.BUFFER_TOO_SMALL:   # rows to be laid out first
+            size = (T + 1) // 2 * self._two_rows   # asking again would take 1 us
+            room = torch.empty(size, dtype=torch.uint8, device=x.device)
+            status = forward(self.handle, x.data_ptr(), ldx, scales.data_ptr(), T, out.data_ptr(), ldo, room.data_ptr(),
+                             size, stream)
         if status:
             raise abi.MoEError(status, "moe_linear_forward")
         return out

@@ -162,3 +162,13 @@ def test_rows_wider_than_the_kernels_indexes(width, T):
     assert L.moe_quantise(A, 0, width, T, width, A, width, A, None) == UNSUPPORTED
     assert L.moe_dequantise(A, width, A, T, width, A, width, None) == UNSUPPORTED
     assert _norm(H=abi.MAX_WIDTH, T=0) == abi.Status.OK
+
+
+@pytest.mark.parametrize("n,k,glu", [(100, 1000, 0), (16, 1, 0), (14336, 7168, 1), (33, 20000, 0), (7, 127, 1)])
+def test_workspace_is_in_proportion_to_the_tokens(n, k, glu):
+    """What callers scale from the size for two tokens serves any number of them."""
+    c = _cfg(n, k, glu)
+    two = abi.linear_query(c, 2)[1]
+    for T in (1, 2, 3, 7, 64, 129, 1000, 8191):
+        need = abi.linear_query(c, T)[1]
+        assert need <= (T + 1) // 2 * two < need + two

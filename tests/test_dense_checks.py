@@ -82,3 +82,28 @@ def test_a_stream_of_another_gpu_is_refused():
               lambda: dense.dequantise(x, None, stream=stream)):
         with pytest.raises(ValueError, match="stream: on GPU 1, expected GPU 0"):
             f()
+
+
+def test_room_is_allocated_only_when_the_library_asks(monkeypatch):
+    """The first call offers no workspace; only where that is refused is one of the queried size allocated."""
+    calls, needs = [], [False]
+
+    def forward(handle, x, ldx, scales, T, out, ldo, room, size, stream):
+        calls.append((room, size))
+        return dense.abi.Status.BUFFER_TOO_SMALL if needs[0] and size < 512 else dense.abi.Status.OK
+    monkeypatch.setattr(dense, "_current_gpu", lambda: -1)
+    monkeypatch.setattr(dense, "_raw_stream", lambda index: 5)
+    monkeypatch.setattr(dense.abi, "lib", lambda: SimpleNamespace(moe_linear_forward=forward))
+    monkeypatch.setattr(dense.abi, "linear_query", lambda cfg, T: (256, 128 * T))
+    monkeypatch.setattr(dense.abi, "linear_create", lambda *a: None)
+    q, s = torch.zeros(4, 8, dtype=torch.int8), torch.zeros(4)
+    layer = object.__new__(dense.Int8Linear)
+    layer.handle, layer.T_max, layer.out_dtype = None, 8192, torch.float32
+    layer._create(q, s, None, None, None, -1, 5)
+    held = sum(v.numel() for v in vars(layer).values() if torch.is_tensor(v))
+    assert held == 256   # the packed weights alone
+    layer.forward(q, s)
+    needs[0] = True
+    layer.forward(q, s)
+    assert calls[:2] == [(None, 0), (None, 0)] and len(calls) == 3
+    assert calls[2][0] and calls[2][1] == 512

@@ -703,3 +703,51 @@ def test_norm_of_rows_whose_squares_leave_the_range(H, dtype, eps):
             big = live & (np.abs(y).max(1) > 1e-30)      # scales with all their bits
             R.check_codes(codes[big], scales[big], y[big], R.NORM_REL, "codes")
             assert np.isnan(out[~live]).all()
+
+
+def test_workspace_only_where_rows_are_laid_out_first():
+    """Aligned rows need no workspace; many unaligned ones are refused without one, with nothing written."""
+    from mxfp4_latent_mixture_sigmoid_amd import abi
+    g, (T, N, K) = gen(31), (1000, 4000, 144)
+    layer, w, s, _ = make(N, K, 0, g, T_max=8192)
+    held = [v.numel() for v in vars(layer).values() if torch.is_tensor(v)]
+    assert held == [abi.linear_query(layer.cfg, 8192)[0]]   # the packed weights, not T_max rows as well
+    x, sx = codes_rows(T, K, g), torch.ones(T, device="cuda")
+    apart = codes_rows(T, K, g, pad=1, offset=3)
+    apart.copy_(x)
+    out, ok = guarded(T, N, BF16)
+    size = abi.linear_query(layer.cfg, T)[1]
+    room = torch.empty(size, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def call(rows, at, size):
+        return abi.lib().moe_linear_forward(layer.handle, rows.data_ptr(), rows.stride(0), sx.data_ptr(), T, out.data_ptr(),
+                                            out.stride(0), at, size, stream)
+    for at, n, want in ((None, 0, abi.Status.BUFFER_TOO_SMALL), (room.data_ptr(), size - 1, abi.Status.BUFFER_TOO_SMALL),
+                        (None, size, abi.Status.INVALID_ARG), (room.data_ptr() + 64, size, abi.Status.INVALID_ARG)):
+        assert call(apart, at, n) == want
+    torch.cuda.synchronize()
+    assert (out == 77).all()
+    assert call(x, None, 0) == abi.Status.OK
+    aligned = out.clone()
+    out.zero_()
+    assert call(apart, room.data_ptr(), size) == abi.Status.OK
+    assert torch.equal(out, aligned) and ok()
+    ref, err = reference(x.cpu().numpy(), f64(sx), w, s, None, True)
+    R.check(f64(aligned), ref, err, "aligned")
+
+
+def test_unaligned_calls_of_one_layer_on_two_streams():
+    """Calls that lay their rows out first, of one layer, overlapping on two streams: each has room of its own."""
+    g, (T, N, K) = gen(32), (2000, 4000, 1001)
+    layer, *_ = make(N, K, 0, g, T_max=T)
+    xs, sx = [codes_rows(T, K, g) for _ in range(2)], torch.ones(T, device="cuda")
+    want = [layer.forward(x, sx) for x in xs]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in xs]
+    got = [[], []]
+    for _ in range(10):
+        for k, (x, side) in enumerate(zip(xs, sides)):
+            got[k].append(layer.forward(x, sx, stream=side))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[k]) for k in (0, 1) for y in got[k])
