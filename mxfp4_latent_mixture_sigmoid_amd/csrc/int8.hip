@@ -685,17 +685,20 @@ __global__ __launch_bounds__(256) void pack_vectors_kernel(const float *s, const
         bias_out[i] = n < N ? bias[n] : 0.f;
 }
 
-template <int MF, int NF, int NW, int KG, int D>
+// ONE: launched for one row tile at most, so that only its form for one is built.
+template <int MF, int NF, int NW, int KG, int D, bool ONE = false>
 hipError_t launch_tile(const I8Args &g, hipStream_t st)
 {
     const int gx = (g.nblk + NF * NW - 1) / (NF * NW), gy = (g.T + 16 * MF - 1) / (16 * MF);
     const dim3 grid((unsigned)((gx * gy + XCDS - 1) / XCDS * XCDS)), threads(WAVE * NW * KG);
-    if (g.direct && gy == 1)
+    if (gy == 1 && g.direct)
         hipLaunchKernelGGL((tile_kernel<MF, NF, NW, KG, D, true, false>), grid, threads, 0, st, g, gx, gy);
-    else if (g.direct)
-        hipLaunchKernelGGL((tile_kernel<MF, NF, NW, KG, D, false, false>), grid, threads, 0, st, g, gx, gy);
     else if (gy == 1)
         hipLaunchKernelGGL((tile_kernel<MF, NF, NW, KG, D, true, true>), grid, threads, 0, st, g, gx, gy);
+    else if constexpr (ONE)
+        return hipErrorInvalidValue;
+    else if (g.direct)
+        hipLaunchKernelGGL((tile_kernel<MF, NF, NW, KG, D, false, false>), grid, threads, 0, st, g, gx, gy);
     else
         hipLaunchKernelGGL((tile_kernel<MF, NF, NW, KG, D, false, true>), grid, threads, 0, st, g, gx, gy);
     return hipGetLastError();
@@ -790,7 +793,7 @@ hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
     if (g.T <= 16) {
         if (round(16, 32))
             return launch_tile<1, 2, 1, 8, 5>(g, st);
-        return round(16, 64) ? launch_tile<1, 2, 2, 4, 4>(g, st) : launch_tile<1, 4, 2, 2, 3>(g, st);
+        return round(16, 64) ? launch_tile<1, 2, 2, 4, 4, true>(g, st) : launch_tile<1, 4, 2, 2, 3, true>(g, st);
     }
     if (g.glu && round(16, 32))
         return launch_tile<1, 2, 1, 8, 5>(g, st);
@@ -799,10 +802,10 @@ hipError_t launch_i8_product(const I8Args &g, hipStream_t st)
     if (round(32, 32))
         return launch_tile<2, 2, 1, 8, 3>(g, st);
     if (g.T <= 32)
-        return round(32, 64) ? launch_tile<2, 2, 2, 4, 3>(g, st) : launch_tile<2, 2, 4, 1, 4>(g, st);
+        return round(32, 64) ? launch_tile<2, 2, 2, 4, 3, true>(g, st) : launch_tile<2, 2, 4, 1, 4, true>(g, st);
     if (round(64, 32))
         return launch_tile<4, 2, 1, 4, 3>(g, st);
-    return g.T > 64 || round(64, 64) ? launch_tile<4, 2, 2, 4, 3>(g, st) : launch_tile<4, 2, 4, 1, 4>(g, st);
+    return g.T > 64 || round(64, 64) ? launch_tile<4, 2, 2, 4, 3>(g, st) : launch_tile<4, 2, 4, 1, 4, true>(g, st);
 }
 
 hipError_t launch_i8_restage(const int8_t *x, int64_t ldx, int T, int K, int8_t *dst, hipStream_t st)
