@@ -751,3 +751,20 @@ def test_unaligned_calls_of_one_layer_on_two_streams():
             got[k].append(layer.forward(x, sx, stream=side))
     torch.cuda.synchronize()
     assert all(torch.equal(y, want[k]) for k in (0, 1) for y in got[k])
+
+
+@pytest.mark.parametrize("H", WIDTHS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_codes_of_every_width(H, dtype):
+    """Codes and scales of rows whose residual cancels nowhere (x and delta of one sign), so that they are known to
+    the norm's own error at every width."""
+    from mxfp4_latent_mixture_sigmoid_amd import rms_norm
+    T, g = 5, gen(H + 1)
+    x, d = rows(T, H, dtype, g, pad=3, offset=1), rows(T, H, BF16, g, pad=2)
+    d.copy_(d.abs() * x.sign().to(BF16))
+    w = (1 + 0.1 * torch.randn(H, generator=g)).bfloat16().cuda()
+    codes, ok = guarded(T, H, torch.int8)
+    r = rms_norm(x, w, 1e-5, delta=d, out=False, codes=codes)
+    _, y = R.norm(f64(x), f64(d), f64(w), float(np.float32(1e-5)))
+    R.check_codes(r.codes.cpu().numpy(), f64(r.scales), y, R.NORM_REL + 2 * R.U, "codes")
+    assert ok()
