@@ -324,7 +324,8 @@ moe_status moe_dequantise(const int8_t *codes, int64_t ldc, const float *scales,
  *   glu = 0:  out = p(w, sw) + bias
  *   glu = 1:  out = silu(p(w, sw)) * p(w_up, sw_up),  silu(g) = g / (1 + exp(-g))
  * The sum is exact (32-bit integers, hence K <= MOE_LINEAR_MAX_K); everything after it is FP32,
- * rounded once to out_type. */
+ * rounded once to out_type. The gate's exponential is the hardware's: FP32 outputs of large negative gates g
+ * are off by about 3 |g| 2^-24 of themselves, two thirds of it from g's own rounding. */
 #define MOE_LINEAR_MAX_K 131071
 typedef struct {
     int32_t n;            /* output channels, >= 1                    */

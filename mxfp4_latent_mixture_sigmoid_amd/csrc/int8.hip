@@ -133,8 +133,9 @@ __device__ inline float scaled(int32_t sum, float sx, float sw, float bias)
     return (float)sum * sx * sw + bias;
 }
 // g / (1 + exp(-g)) is taken on the hardware's exponential and reciprocal, each within a unit in the last
-// place: the exponent's rounding costs |g| 2^-24 relative, far below the output's BF16 (and a few units of
-// FP32). exp overflows to infinity, whose reciprocal is 0.
+// place. The exponent's rounding costs |g| 2^-24 relative, beside the 2 |g| 2^-24 that g's own two roundings do: far
+// below the output's BF16; in FP32 outputs up to 84 x 2^-24 for gates of -40 to -20, where FP32 with a library's exponential
+// has 64, and 11.5 against 9 for gates of -5 to 5. exp overflows to infinity, whose reciprocal is 0.
 __device__ inline float gated(int32_t gate, int32_t up, float sx, float sg, float su)
 {
 #pragma clang fp contract(off)
@@ -406,10 +407,11 @@ void tile_kernel(const I8Args g, int gx, int gy)
 // three 128-code stages of activations (whole lines) and four 64-code halves of weights, loaded three to four
 // halves ahead of their reads.
 //
-// 8192 x (2 x 14336) x 7168 gated takes 1.20 ms, 2.8 POP/s (a library product of 8-bit codes of these sizes
-// without scales or gate: 1.58 ms), 8192 x 7168 x 14336 0.61 ms. The matrix cores are busy 67 to 69% of the
-// clocks, and the clock is what bounds it: with codes as they come the card runs this at 1.72 to 1.75 GHz of its 2.4
-// (codes that are all zero: 1.0 ms), so that what is saved is energy. The 16x16x64 instruction moves a
+// 8192 x (2 x 14336) x 7168 gated takes 1.20 to 1.26 ms, 2.7 to 2.8 POP/s (a library product of 8-bit codes of these
+// sizes without scales or gate: 1.58 ms), 8192 x 7168 x 14336 0.61 to 0.67 ms. The gated one is 2.4 M clocks whatever the
+// codes, 67% of them multiplication (1331 us at 1.79 GHz in one profiled run); a tile's loop takes 20.3 clocks a code
+// for 16 of multiplication, its start and end 27000 clocks that nothing overlaps. Codes that are all zero run at 2.3 to
+// 2.4 GHz (1.05 ms), codes as they come at 1.6 to 1.9: energy sets the clock. The 16x16x64 instruction moves a
 // fifth less through the register files than 32x32x32 (1.45 ms so), four waves 128 x 128 a third less
 // through the LDS than eight of 128 x 64 (1.42 ms).
 
@@ -763,8 +765,11 @@ hipError_t launch_many(const I8Args &g, hipStream_t st)
 } // namespace
 
 // Passing rows through registers saves the restaging launch and its pass over x, and costs some of the product's
-// time: 1 x 1000 x 1000 3.5 us against 5.1, 450 x 512 x 1237 5.2 against 6.7, 777 x 1001 x 3583 12.1 against
-// 12.6, 32 x 28672 x 7167 34.7 against 35.9; but 64 x 28672 x 7167 44.9 against 39.0. Many tokens are restaged: 600 x
+// time. Registers against restaging, rows of odd stride, weights from memory: 1 x 1000 x 1000 3.3 us against 5.0, 300 x 3000
+// x 999 6.9 / 8.6, 777 x 1001 x 3583 15.8 / 14.9, 32 x 28672 x 7167 36.6 / 38.0, 64 x 14336 x 4095 19.0 / 18.8; from 2^32
+// operations on mostly longer: 64 x 14336 x 7167 29.6 / 28.2, 256 x 4096 x 7167 25.0 / 22.3, 64 x 7168 x 14335 41.0 / 32.5,
+// 64 x 28672 x 7167 43.9 / 40.3, 500 x 2040 x 14335 45.1 / 35.6. Strides of whole 16 bytes stay ahead: 64 x 28672 x 7167
+// 36.9 / 39.5, 256 x 4096 x 28671 64 / 68. The limit, of 2^33, is between the two. Many tokens are restaged: 600 x
 // 4096 x 2047 15.5 against 18.4 with 128 x 128 tiles fed from registers, 2504 x 1920 x 356 11.8 against 18.2, though
 // 3000 x 1000 x 999 13.2 against 12.1.
 bool i8_takes_any_rows(const I8Args &g)

@@ -461,7 +461,10 @@ __global__ __launch_bounds__(256) void dequantise_kernel(const int8_t *codes, in
 // codes 78 us against 85, 8192 x 3000 sum and codes 34 against 41, 8192 x 5120 (320 threads) 51 against 58 with
 // 512; and up to 1024 columns a wave with two for any rows: 8192 x 1024 sum and codes 11.9 us against 17.3
 // with 256 threads (FP32 19.8 against 18.5), 4 x 1024 the same. 2560 columns by 320 threads: 8192 rows 29 us, by
-// 512 35.
+// 512 35. "Many" is from 1024 rows on; sum and codes with one chunk against two at 256 / 512 / 1000 / 1536 / 4096 rows: 2568
+// columns 4.7 : 5.3 / 6.0 : 6.4 / 8.1 : 8.0 / 10.7 : 10.0 / 25.3 : 21.6 us, 4096 4.6 : 4.7 / 5.9 : 6.0 / 8.6 : 8.1 / 11.9 :
+// 11.3 / 26.9 : 24.9, 7168 5.7 : 5.8 / 8.3 : 8.2 / 14.3 : 14.4 / 21.5 : 20.9 / 45.7 : 41.4. Where one chunk leaves many
+// threads idle (5120 columns) or none (8192), two are ahead from 128 rows on: 7.5 : 6.7 and 8.7 : 8.1 at 512.
 template <typename X, bool NORM>
 hipError_t launch_rows(const moe_norm_args &a, hipStream_t st)
 {

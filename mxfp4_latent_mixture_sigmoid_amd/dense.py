@@ -2,8 +2,8 @@
 per token, products of 8-bit codes (plain and gated), and a dense feed-forward block of them.
 
 Torch provides device memory and the stream; all arithmetic runs in the HIP library. Codes are int8
-[rows, width] tensors with one FP32 scale per row. Row-major inputs may be views with any row stride;
-their last dimension has to be contiguous. Calls run on ``stream`` (default: the current stream).
+[rows, width] tensors with one FP32 scale per row. Row-major tensors may be views with any row stride of at
+least their width; their last dimension has to be contiguous. Calls run on ``stream`` (default: the current stream).
 """
 from __future__ import annotations
 
