@@ -768,3 +768,43 @@ def test_norm_codes_of_every_width(H, dtype):
     _, y = R.norm(f64(x), f64(d), f64(w), float(np.float32(1e-5)))
     R.check_codes(r.codes.cpu().numpy(), f64(r.scales), y, R.NORM_REL + 2 * R.U, "codes")
     assert ok()
+
+
+@pytest.mark.parametrize("H", [70001, 2 ** 20, 2 ** 24 + 3])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_of_long_rows_of_equal_values(H, dtype):
+    """The sum of very many squares is as exact as that of a few: scale = value / rms / 127 to the norm's error."""
+    from mxfp4_latent_mixture_sigmoid_amd import rms_norm
+    for value in (1.1, 0.3):
+        x = torch.full((2, H), value, dtype=dtype, device="cuda")
+        x[1, ::2] *= -2
+        r = rms_norm(x, eps=1e-6, codes=True)
+        v = f64(x[:, :2])                                     # each row repeats its first two values
+        odd = H % 2
+        mean = ((H + odd) // 2 * v[:, 0] ** 2 + (H // 2) * v[:, 1] ** 2) / H
+        y = v / np.sqrt(mean + float(np.float32(1e-6)))[:, None]
+        R.check_codes(r.codes[:, :2].cpu().numpy(), f64(r.scales), y, R.NORM_REL, "codes")
+        R.check(f64(r.out[:, :2]), y, np.abs(y) * (R.B + R.NORM_REL), "out")
+        assert torch.equal(r.codes[:, 2:4], r.codes[:, :2]) and torch.equal(r.out[:, -2:].sort(1)[0], r.out[:, :2].sort(1)[0])
+
+
+@pytest.mark.parametrize("T,N,K", [(600, 4096, 2047), (5, 40, 15)])
+def test_rows_laid_out_first_in_a_graph(T, N, K):
+    """A captured call that allocates room for its rows, replayed on new codes with eager calls of the layer between."""
+    g = gen(K)
+    layer, *_ = make(N, K, 0, g, T_max=T)
+    x, sx = codes_rows(T, K, g, pad=2, offset=1), torch.ones(T, device="cuda")
+    layer.forward(x, sx)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer.forward(x, sx)
+    other = codes_rows(T, K, g, pad=2, offset=1)
+    for k in range(4):
+        x.copy_(codes_rows(T, K, g))
+        graph.replay()
+        noise = layer.forward(other, sx)
+        if k % 2:
+            torch.cuda.synchronize()
+        got = y.clone()
+        assert torch.equal(got, layer.forward(x, sx)) and torch.equal(noise, layer.forward(other, sx)), k
