@@ -312,6 +312,39 @@ typedef struct {
 } moe_norm_args;
 moe_status moe_norm(const moe_norm_args *a, void *stream);
 
+/* Activation of moe_block_norm's gate. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_SIGMOID = 1, MOE_GATE_TANH = 2 } moe_gate_act;
+
+/* What stands between two blocks of a decoder, for T rows of H values, in FP32 throughout: the norm after the one, its
+ * gate, the scaled residual addition, and the norm before the next:
+ *   n = y / sqrt(mean(y^2) + eps) * post_weight
+ *   s = residual_scale * x + scale * a(gate) * n
+ *   out = s / sqrt(mean(s^2) + eps) * weight
+ * Each requested output is rounded once from these values: `sum` = s in x's type, `out` in BF16, `codes` / `scales`
+ * = out's values in 8 bits, as moe_norm's. The gate is a value for every element (gate_width = H), a row for all tokens
+ * (gate_width = H, ldg = 0) or one value per token (gate_width = 1). Both norms hold for all finite values. A row's outputs
+ * are the same bits whatever rows come with it. `sum` may be x itself (same pointer and stride); no other output may
+ * overlap an input or another output. */
+typedef struct {
+    const void *x;            /* x_type [T, H]: the residual stream                        */
+    const void *y;            /* bf16 [T, H]: the block's output                           */
+    const void *post_weight;  /* bf16 [H], or NULL for ones                                */
+    const void *weight;       /* bf16 [H], or NULL for ones                                */
+    const void *gate;         /* bf16 [T, gate_width], or NULL for ones                    */
+    void *sum;                /* x_type [T, H], or NULL                                    */
+    void *out;                /* bf16 [T, H], or NULL                                      */
+    int8_t *codes;            /* [T, H], or NULL                                           */
+    float *scales;            /* [T], exactly when codes is given                          */
+    int64_t ldx, ldy, ldg, lds, ldo, ldc;   /* row strides; ldg >= 0                       */
+    int32_t T, H;             /* T >= 0 (0 enqueues nothing), H in 1..MOE_MAX_WIDTH        */
+    int32_t x_type;           /* moe_type                                                  */
+    int32_t gate_act;         /* moe_gate_act; MOE_GATE_NONE without a gate                */
+    int32_t gate_width;       /* H or 1; 0 without a gate                                  */
+    float eps;                /* >= 0                                                      */
+    float scale, residual_scale;   /* finite                                               */
+} moe_block_norm_args;
+moe_status moe_block_norm(const moe_block_norm_args *a, void *stream);
+
 /* Rows of x (x_type [T, K]) in 8 bits: the last line of moe_norm's formula with y = x. */
 moe_status moe_quantise(const void *x, int32_t x_type, int64_t ldx, int32_t T, int32_t K, int8_t *codes,
                         int64_t ldc, float *scales, void *stream);

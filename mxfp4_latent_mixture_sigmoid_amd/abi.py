@@ -76,6 +76,20 @@ class NormArgs(ctypes.Structure):
 NORM_ARGS = struct.Struct("7P5q3if")
 
 
+GATE_NONE, GATE_SIGMOID, GATE_TANH = 0, 1, 2
+
+
+class BlockNormArgs(ctypes.Structure):
+    """moe_block_norm_args; calls pass the same bytes packed by BLOCK_NORM_ARGS."""
+    _fields_ = ([(n, c_vp) for n in ("x", "y", "post_weight", "weight", "gate", "sum", "out", "codes", "scales")]
+                + [(n, c_i64) for n in ("ldx", "ldy", "ldg", "lds", "ldo", "ldc")]
+                + [(n, c_i32) for n in ("T", "H", "x_type", "gate_act", "gate_width")]
+                + [(n, ctypes.c_float) for n in ("eps", "scale", "residual_scale")])
+
+
+BLOCK_NORM_ARGS = struct.Struct("9P6q5i3f")
+
+
 class LinearConfig(ctypes.Structure):
     _fields_ = [("n", c_i32), ("k", c_i32), ("glu", c_i32), ("out_type", c_i32)]
 
@@ -104,6 +118,7 @@ SIGNATURES = {
     "moe_profile_end": (c_i32, [c_vp, ctypes.POINTER(c_i32), ctypes.POINTER(ctypes.c_float), ctypes.POINTER(c_i32)]),
     "moe_destroy": (None, [c_vp]),
     "moe_norm": (c_i32, [ctypes.c_char_p, c_vp]),                 # const moe_norm_args *, see NORM_ARGS
+    "moe_block_norm": (c_i32, [ctypes.c_char_p, c_vp]),           # const moe_block_norm_args *, see BLOCK_NORM_ARGS
     "moe_quantise": (c_i32, [c_vp, c_i32, c_i64, c_i32, c_i32, c_vp, c_i64, c_vp, c_vp]),
     "moe_dequantise": (c_i32, [c_vp, c_i64, c_vp, c_i32, c_i32, c_vp, c_i64, c_vp]),
     "moe_linear_query": (c_i32, [ctypes.POINTER(LinearConfig), c_i32, ctypes.POINTER(c_size),

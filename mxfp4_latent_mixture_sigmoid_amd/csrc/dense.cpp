@@ -3,6 +3,7 @@
 #include "dense.hpp"
 
 #include <climits>
+#include <cmath>
 #include <new>
 
 using namespace mxmoe;
@@ -92,6 +93,30 @@ moe_status moe_norm(const moe_norm_args *a, void *stream)
         (a->codes && (a->ldc < a->H || !aligned(a->scales, 4))) || (a->sum == a->x && a->lds != a->ldx))
         return MOE_ERR_INVALID_ARG;
     return hip_status(launch_norm(*a, true, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_block_norm(const moe_block_norm_args *a, void *stream)
+{
+    if (!a || a->T < 0 || a->H < 1 || !valid_type(a->x_type) || !(a->eps >= 0.f) || !std::isfinite(a->scale) ||
+        !std::isfinite(a->residual_scale))
+        return MOE_ERR_INVALID_ARG;
+    if (a->gate ? (a->gate_width != 1 && a->gate_width != a->H) || a->gate_act < MOE_GATE_NONE || a->gate_act > MOE_GATE_TANH
+                : a->gate_width != 0 || a->gate_act != MOE_GATE_NONE)
+        return MOE_ERR_INVALID_ARG;
+    if (a->H > MOE_MAX_WIDTH)
+        return MOE_ERR_UNSUPPORTED;
+    if (a->T == 0)
+        return MOE_OK;
+    if ((!a->sum && !a->out && !a->codes) || !a->codes != !a->scales)
+        return MOE_ERR_INVALID_ARG;
+    const uintptr_t sz = type_size(a->x_type);
+    if (!valid_rows(a->x, a->ldx, a->H, sz) || !valid_rows(a->y, a->ldy, a->H, 2) ||
+        (a->gate && (a->ldg < 0 || (a->ldg && a->ldg < a->gate_width) || !aligned(a->gate, 2))) ||
+        (a->post_weight && !aligned(a->post_weight, 2)) || (a->weight && !aligned(a->weight, 2)) ||
+        (a->sum && !valid_rows(a->sum, a->lds, a->H, sz)) || (a->out && !valid_rows(a->out, a->ldo, a->H, 2)) ||
+        (a->codes && (a->ldc < a->H || !aligned(a->scales, 4))) || (a->sum == a->x && a->lds != a->ldx))
+        return MOE_ERR_INVALID_ARG;
+    return hip_status(launch_block_norm(*a, static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_quantise(const void *x, int32_t x_type, int64_t ldx, int32_t T, int32_t K, int8_t *codes, int64_t ldc,

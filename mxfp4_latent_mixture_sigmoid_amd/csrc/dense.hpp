@@ -8,6 +8,7 @@ namespace mxmoe {
 
 // moe_norm, or (norm = false) the quantisation of x's rows alone.
 hipError_t launch_norm(const moe_norm_args &a, bool norm, hipStream_t st);
+hipError_t launch_block_norm(const moe_block_norm_args &a, hipStream_t st);
 hipError_t launch_dequantise(const int8_t *codes, int64_t ldc, const float *scales, int32_t T, int32_t K, uint16_t *out,
                              int64_t ldo, hipStream_t st);
 

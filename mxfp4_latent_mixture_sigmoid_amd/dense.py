@@ -1,5 +1,6 @@
-"""The dense 8-bit path around the mixture layer: RMS norm with the residual's addition, quantisation
-per token, products of 8-bit codes (plain and gated), and a dense feed-forward block of them.
+"""What stands around the mixture layer: RMS norm with the residual's addition, the norms between two blocks with gate and
+residual scale, and the dense 8-bit path: quantisation per token, products of 8-bit codes (plain and gated), and a dense
+feed-forward block of them.
 
 Torch provides device memory and the stream; all arithmetic runs in the HIP library. Codes are int8
 [rows, width] tensors with one FP32 scale per row. Row-major tensors may be views with any row stride of at
@@ -17,6 +18,8 @@ _TYPES = {torch.bfloat16: abi.TYPE_BF16, torch.float32: abi.TYPE_F32}
 _BF16, _INT8 = (torch.bfloat16,), (torch.int8,)
 _INT32_MAX = 2 ** 31 - 1   # rows and columns cross the C ABI as 32-bit integers, which ctypes cuts without a word
 _pack = abi.NORM_ARGS.pack
+_pack_block = abi.BLOCK_NORM_ARGS.pack
+_GATES = {None: abi.GATE_NONE, "none": abi.GATE_NONE, "sigmoid": abi.GATE_SIGMOID, "tanh": abi.GATE_TANH}
 _raw_stream = torch._C._cuda_getCurrentRawStream   # of a GPU: its handle, without an object around it
 _current_gpu = torch._C._cuda_getDevice
 
@@ -129,6 +132,82 @@ def _rms_norm(x, weight, eps, delta, sum, out, codes, scales, index, stream):
                                       lds, ldo, ldc, T, H, _TYPES[dtype], eps), stream)
     if status:
         raise abi.MoEError(status, "moe_norm")
+    return Normed(o, q, scales, s)
+
+
+def block_norm(x, y, post_weight=None, weight=None, eps=1e-6, gate=None, gate_act=None, scale=1.0, residual_scale=1.0,
+               sum=True, out=True, codes=False, scales=None, stream=None) -> Normed:
+    """What stands between two blocks: the norm after the one, its gate, the scaled residual addition, and the norm
+    before the next, row by row in FP32:
+
+        n = y / sqrt(mean(y^2) + eps) * post_weight
+        s = residual_scale * x + scale * a(gate) * n
+        out = s / sqrt(mean(s^2) + eps) * weight
+
+    x: [T, H] BF16 or FP32, the residual stream; y: [T, H] BF16, the block's output; post_weight, weight: BF16 [H],
+    optional; gate: BF16, a value for every element ([T, H]), for every column ([H] or [1, H]) or for every token ([T, 1]),
+    with a = ``gate_act``: None, "sigmoid" or "tanh". Each of ``sum`` (s in x's type), ``out`` (BF16) and ``codes`` (int8,
+    with ``scales``) is False, True (allocated here) or a tensor to write into; ``sum`` may be x itself. Rows that have no
+    scale as ``rms_norm``'s."""
+    if stream is None and (index := x.get_device()) >= 0 and index == _current_gpu():
+        return _block_norm(x, y, post_weight, weight, eps, gate, gate_act, scale, residual_scale, sum, out, codes, scales,
+                           index, _raw_stream(index))
+    return _call(x, stream, (x, y, post_weight, weight, gate, sum, out, codes, scales), _block_norm, x, y, post_weight,
+                 weight, eps, gate, gate_act, scale, residual_scale, sum, out, codes, scales)
+
+
+def _gate(gate, T, H, index):
+    """(width, row stride) of the gate."""
+    shape, strides = gate.shape, gate.stride()
+    if gate.dtype is not torch.bfloat16 or gate.get_device() != index or len(shape) not in (1, 2):
+        raise ValueError(f"gate: expected bfloat16 [{T}, {H}], [{T}, 1], [1, {H}] or [{H}] on GPU {index}, got {gate.dtype} "
+                         f"{tuple(shape)} on {gate.device}")
+    n = shape[-1]
+    if n not in (1, H) or (shape[0] not in (1, T) if len(shape) == 2 else n != H):
+        raise ValueError(f"gate: shape {tuple(shape)}, expected [{T}, {H}], [{T}, 1], [1, {H}] or [{H}]")
+    if n > 1 and strides[-1] == 0 and len(shape) == 2:   # one per token, expanded over the columns
+        n = 1
+    elif n > 1 and strides[-1] != 1:
+        raise ValueError(f"gate: expected contiguous rows, got strides {strides}")
+    ld = strides[0] if len(shape) == 2 and shape[0] > 1 else 0
+    if 0 < ld < n:
+        raise ValueError(f"gate: rows overlap (strides {strides})")
+    return n, ld
+
+
+def _block_norm(x, y, post_weight, weight, eps, gate, gate_act, scale, residual_scale, sum, out, codes, scales, index,
+                stream):
+    ldx = _rows("x", x, _TYPES, index)
+    T, H = x.shape
+    dtype = x.dtype
+    ldy = _rows("y", y, _BF16, index, x.shape)
+    if post_weight is not None:
+        _vector("post_weight", post_weight, H, torch.bfloat16, index)
+    if weight is not None:
+        _vector("weight", weight, H, torch.bfloat16, index)
+    act = _GATES.get(gate_act)
+    if act is None:
+        raise ValueError(f"gate_act: {gate_act!r}, expected None, 'sigmoid' or 'tanh'")
+    width = ldg = 0
+    if gate is not None:
+        width, ldg = _gate(gate, T, H, index)
+    elif act:
+        raise ValueError("gate_act given without a gate")
+    s, lds = _output("sum", sum, x, dtype, index)
+    o, ldo = _output("out", out, x, torch.bfloat16, index)
+    q, ldc = _output("codes", codes, x, torch.int8, index)
+    if scales is not None:
+        if q is None:
+            raise ValueError("scales given without codes")
+        _vector("scales", scales, T, torch.float32, index)
+    elif q is not None:
+        scales = torch.empty(T, dtype=torch.float32, device=x.device)
+    ptr = _ptr
+    status = abi.lib().moe_block_norm(
+        _pack_block(x.data_ptr(), y.data_ptr(), ptr(post_weight), ptr(weight), ptr(gate), ptr(s), ptr(o), ptr(q), ptr(scales),
+                    ldx, ldy, ldg, lds, ldo, ldc, T, H, _TYPES[dtype], act, width, eps, scale, residual_scale), stream)
+    if status:
+        raise abi.MoEError(status, "moe_block_norm")
     return Normed(o, q, scales, s)
 
 
