@@ -397,6 +397,51 @@ moe_status moe_linear_forward(moe_linear *l, const int8_t *x, int64_t ldx, const
 /* Free the host handle (not the packed buffer). NULL is a no-op. */
 void moe_linear_destroy(moe_linear *l);
 
+/* A dense product of BF16 values with FP32 sums, for T tokens x and weights w of N rows:
+ *   glu = 0:  out = a(x . w^T + bias) + residual
+ *   glu = 1:  out = a(x . w^T) * (x . w_up^T) + residual
+ * Everything after the sum is FP32, rounded once to out_type. A token's sums are added in an order that depends on the
+ * sizes (T among them), so that its last bits may; the same call gives the same bits. silu and gelu_tanh use the
+ * hardware's exponential: off by about 2 |v| 2^-24 of themselves where v is large and negative. */
+typedef enum {
+    MOE_LINEAR_NONE = 0,       /* v                                                     */
+    MOE_LINEAR_SILU = 1,       /* v / (1 + exp(-v))                                     */
+    MOE_LINEAR_GELU = 2,       /* v / 2 (1 + erf(v / sqrt(2)))                          */
+    MOE_LINEAR_GELU_TANH = 3,  /* v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3)))     */
+    MOE_LINEAR_RELU = 4        /* max(v, 0)                                             */
+} moe_linear_act;
+#define MOE_DENSE_MAX_K 131072
+typedef struct {
+    int32_t n;            /* output channels, >= 1                    */
+    int32_t k;            /* input width, 1..MOE_DENSE_MAX_K    */
+    int32_t glu;          /* 0 or 1                                   */
+    int32_t act;          /* moe_linear_act (of the gate when glu)    */
+    int32_t out_type;     /* moe_type                                 */
+} moe_dense_config;
+
+/* Canonical weights (device, caller-owned; read only by moe_dense_create's packing kernels). */
+typedef struct {
+    const void *w;          /* bf16 [n, k], contiguous (the gate's when glu) */
+    const void *w_up;       /* bf16 [n, k] (glu only, else NULL)             */
+    const float *bias;      /* [n], or NULL; must be NULL when glu           */
+} moe_dense_weights;
+
+typedef struct moe_dense moe_dense;
+
+/* As moe_linear_query, moe_linear_create and moe_linear_destroy. */
+moe_status moe_dense_query(const moe_dense_config *cfg, int32_t T_max, size_t *packed_bytes,
+                                 size_t *workspace_bytes);
+moe_status moe_dense_create(const moe_dense_config *cfg, const moe_dense_weights *w, void *packed,
+                                  size_t packed_bytes, void *stream, moe_dense **out);
+/* The product for T >= 0 tokens (0 enqueues nothing). x: bf16 [T, k]; residual: [T, n] of res_type (moe_type), or NULL; it
+ * may be out itself (same type, pointer and stride); out: out_type [T, n], must not overlap any other input. workspace: as
+ * moe_linear_forward's; rows at 16-byte steps of at most 2^22 bytes from a 16-byte aligned address with k a multiple of 64
+ * never need one. */
+moe_status moe_dense_forward(moe_dense *l, const void *x, int64_t ldx, const void *residual, int32_t res_type,
+                                   int64_t ldr, int32_t T, void *out, int64_t ldo, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+void moe_dense_destroy(moe_dense *l);
+
 /* Static description of a status code. */
 const char *moe_strerror(moe_status s);
 

@@ -1,12 +1,13 @@
 """MI355X (gfx950) routed-expert forward of an MXFP4 Stable LatentMoE layer.
 
 The compute path is the HIP library ``libmxmoe.so`` behind the C ABI in ``include/mxmoe.h``;
-``abi`` binds it with ctypes and ``MoELayer`` manages device buffers with torch. ``dense`` is the 8-bit
-path around the layer: ``rms_norm``, ``block_norm``, ``quantise``, ``dequantise``, ``Int8Linear``, ``Int8FeedForward``.
+``abi`` binds it with ctypes and ``MoELayer`` manages device buffers with torch. ``dense`` is the dense
+path around the layer: ``rms_norm``, ``block_norm``, ``quantise``, ``dequantise``, ``Int8Linear``, ``Bf16Linear``,
+``Int8FeedForward``.
 """
 from . import abi  # noqa: F401
 
-_DENSE = ("rms_norm", "block_norm", "quantise", "dequantise", "Int8Linear", "Int8FeedForward")
+_DENSE = ("rms_norm", "block_norm", "quantise", "dequantise", "Int8Linear", "Bf16Linear", "Int8FeedForward")
 __all__ = ["abi", "MoELayer", *_DENSE]
 
 

@@ -98,6 +98,18 @@ class LinearWeights(ctypes.Structure):
     _fields_ = [(n, c_vp) for n in ("w", "scales", "w_up", "scales_up", "bias")]
 
 
+DENSE_MAX_K = 131072   # MOE_DENSE_MAX_K
+LINEAR_NONE, LINEAR_SILU, LINEAR_GELU, LINEAR_GELU_TANH, LINEAR_RELU = range(5)
+
+
+class DenseConfig(ctypes.Structure):
+    _fields_ = [("n", c_i32), ("k", c_i32), ("glu", c_i32), ("act", c_i32), ("out_type", c_i32)]
+
+
+class DenseWeights(ctypes.Structure):
+    _fields_ = [(n, c_vp) for n in ("w", "w_up", "bias")]
+
+
 # name -> (restype, argtypes); the exported C symbols of the library
 SIGNATURES = {
     "moe_query": (c_i32, [ctypes.POINTER(MoeConfig), c_i32, ctypes.POINTER(c_size), ctypes.POINTER(c_size)]),
@@ -127,6 +139,12 @@ SIGNATURES = {
                                   ctypes.POINTER(c_vp)]),
     "moe_linear_forward": (c_i32, [c_vp, c_vp, c_i64, c_vp, c_i32, c_vp, c_i64, c_vp, c_size, c_vp]),
     "moe_linear_destroy": (None, [c_vp]),
+    "moe_dense_query": (c_i32, [ctypes.POINTER(DenseConfig), c_i32, ctypes.POINTER(c_size),
+                                      ctypes.POINTER(c_size)]),
+    "moe_dense_create": (c_i32, [ctypes.POINTER(DenseConfig), ctypes.POINTER(DenseWeights), c_vp, c_size,
+                                       c_vp, ctypes.POINTER(c_vp)]),
+    "moe_dense_forward": (c_i32, [c_vp, c_vp, c_i64, c_vp, c_i32, c_i64, c_i32, c_vp, c_i64, c_vp, c_size, c_vp]),
+    "moe_dense_destroy": (None, [c_vp]),
     "moe_strerror": (ctypes.c_char_p, [c_i32]),
 }
 
@@ -294,3 +312,23 @@ def linear_create(cfg: LinearConfig, w, scales, w_up, scales_up, bias, packed, s
 
 def linear_destroy(h) -> None:
     lib().moe_linear_destroy(h)
+
+
+def dense_query(cfg: DenseConfig, T_max: int):
+    pb, wb = c_size(0), c_size(0)
+    check(lib().moe_dense_query(ctypes.byref(cfg), T_max, ctypes.byref(pb), ctypes.byref(wb)),
+          "moe_dense_query")
+    return pb.value, wb.value
+
+
+def dense_create(cfg: DenseConfig, w, w_up, bias, packed, stream: int) -> c_vp:
+    """`stream`: the raw stream handle."""
+    lw = DenseWeights(ptr(w), ptr(w_up), ptr(bias))
+    h = c_vp()
+    check(lib().moe_dense_create(ctypes.byref(cfg), ctypes.byref(lw), ptr(packed), packed.numel(), c_vp(stream),
+                                       ctypes.byref(h)), "moe_dense_create")
+    return h
+
+
+def dense_destroy(h) -> None:
+    lib().moe_dense_destroy(h)

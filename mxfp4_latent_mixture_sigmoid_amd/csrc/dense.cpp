@@ -1,4 +1,4 @@
-// dense.cpp -- the C ABI of the dense 8-bit path declared in include/mxmoe.h: validation, packed-buffer
+// dense.cpp -- the C ABI of the dense path around the layer (8-bit and BF16) declared in include/mxmoe.h: validation, packed-buffer
 // and workspace layouts, launches on the caller's stream.
 #include "dense.hpp"
 
@@ -12,6 +12,12 @@ struct moe_linear {
     moe_linear_config cfg;
     uint8_t *blocks;
     const float *scales, *bias;
+};
+
+struct moe_dense {
+    moe_dense_config cfg;
+    uint8_t *blocks;
+    const float *bias;
 };
 
 namespace {
@@ -35,9 +41,9 @@ struct LinearLayout {
 
 LinearLayout linear_layout(const moe_linear_config *c)
 {
-    const int64_t nblk = i8_row_blocks(c->n, c->glu);
+    const int64_t nblk = row_blocks(c->n, c->glu);
     LinearLayout L;
-    L.scales = align_up(nblk * i8_stages(c->k) * I8_STAGE_BYTES);
+    L.scales = align_up(nblk * stages(c->k) * STAGE_BYTES);
     L.bias = align_up(L.scales + nblk * 16 * 4);
     L.total = align_up(L.bias + nblk * 16 * 4);
     return L;
@@ -48,12 +54,30 @@ bool valid_linear(const moe_linear_config *c)
     return c && c->n >= 1 && c->k >= 1 && (c->glu == 0 || c->glu == 1) && valid_type(c->out_type);
 }
 
-// The sum fits 32 bits, and the packing kernel's launch (a thread per 16 codes) and the packed rows their indexes.
-bool supported_linear(const moe_linear_config *c)
+// The packing kernel's launch (a thread per 16 bytes) and the packed rows fit their indexes. k: bytes of a row.
+bool packs(int64_t n, bool glu, int64_t k)
 {
-    const int64_t nblk = i8_row_blocks(c->n, c->glu);
-    return c->k <= MOE_LINEAR_MAX_K && nblk * 16 <= INT32_MAX / 2 && chunks_fit(nblk * 16, i8_stages(c->k) * I8_STAGE);
+    const int64_t rows = row_blocks(n, glu) * 16;
+    return rows <= INT32_MAX / 2 && chunks_fit(rows, stages(k) * STAGE_K);
 }
+
+// ... and the sum fits 32 bits.
+bool supported_linear(const moe_linear_config *c) { return c->k <= MOE_LINEAR_MAX_K && packs(c->n, c->glu, c->k); }
+
+bool valid_dense(const moe_dense_config *c)
+{
+    return c && c->n >= 1 && c->k >= 1 && (c->glu == 0 || c->glu == 1) && valid_type(c->out_type) &&
+           c->act >= MOE_LINEAR_NONE && c->act <= MOE_LINEAR_RELU;
+}
+bool supported_dense(const moe_dense_config *c)
+{
+    return c->k <= MOE_DENSE_MAX_K && packs(c->n, c->glu, 2 * (int64_t)c->k);
+}
+int64_t dense_bias_at(const moe_dense_config *c)
+{
+    return align_up(row_blocks(c->n, c->glu) * stages(2 * (int64_t)c->k) * STAGE_BYTES);
+}
+int64_t dense_packed_bytes(const moe_dense_config *c) { return align_up(dense_bias_at(c) + row_blocks(c->n, false) * 16 * 4); }
 
 // Whether the products' direct loads to LDS can take the activations as they are: rows at 16-byte steps from a
 // 16-byte aligned address, K whole 16-byte chunks, a tile's rows within one load window. Others go
@@ -61,16 +85,17 @@ bool supported_linear(const moe_linear_config *c)
 constexpr int64_t LD_MAX = 1 << 22;
 bool direct(const int8_t *x, int64_t ldx, int64_t K) { return aligned(x, 16) && ldx % 16 == 0 && K % 16 == 0 && ldx <= LD_MAX; }
 
-int64_t workspace_bytes_for(const moe_linear_config *c, int64_t T) { return align_up(T * i8_stages(c->k) * I8_STAGE); }
+int64_t workspace_bytes_for(int64_t k, int64_t T) { return align_up(T * stages(k) * STAGE_K); }
 
 // More than a round of workgroups comes in tiles of 128 columns at least and of 128 rows or all there are, of 512
-// threads at most; restaging takes a thread per 16 codes.
+// threads at most; restaging takes a thread per 16 bytes.
 constexpr int64_t XCD_PAD = 8;   // the grid is rounded up to the XCDs
-bool linear_fits(const moe_linear_config *c, int64_t T)
+bool product_fits(int64_t n, bool glu, int64_t k, int64_t T)
 {
-    const int64_t tiles = ((T + 127) / 128) * ((i8_row_blocks(c->n, c->glu) + 7) / 8);
-    return tiles < (UINT32_MAX / 512) - XCD_PAD && chunks_fit(T, i8_stages(c->k) * I8_STAGE);
+    const int64_t tiles = ((T + 127) / 128) * ((row_blocks(n, glu) + 7) / 8);
+    return tiles < (UINT32_MAX / 512) - XCD_PAD && chunks_fit(T, stages(k) * STAGE_K);
 }
+bool linear_fits(const moe_linear_config *c, int64_t T) { return product_fits(c->n, c->glu, c->k, T); }
 
 } // namespace
 
@@ -168,7 +193,7 @@ moe_status moe_linear_query(const moe_linear_config *cfg, int32_t T_max, size_t 
     if (packed_bytes)
         *packed_bytes = (size_t)linear_layout(cfg).total;
     if (workspace_bytes)
-        *workspace_bytes = (size_t)workspace_bytes_for(cfg, T_max);
+        *workspace_bytes = (size_t)workspace_bytes_for(cfg->k, T_max);
     return MOE_OK;
 }
 
@@ -231,24 +256,127 @@ moe_status moe_linear_forward(moe_linear *l, const int8_t *x, int64_t ldx, const
     g.T = T;
     g.N = c->n;
     g.K = c->k;
-    g.nblk = (int)i8_row_blocks(c->n, c->glu);
+    g.nblk = (int)row_blocks(c->n, c->glu);
     g.glu = c->glu;
     g.out_type = c->out_type;
     g.direct = direct(x, ldx, c->k);
     if (!g.direct && !i8_takes_any_rows(g)) {
-        if (workspace_bytes < (size_t)workspace_bytes_for(c, T))
+        if (workspace_bytes < (size_t)workspace_bytes_for(c->k, T))
             return MOE_ERR_BUFFER_TOO_SMALL;
         int8_t *staged = static_cast<int8_t *>(workspace);
-        const hipError_t e = launch_i8_restage(x, ldx, T, c->k, staged, st);
+        const hipError_t e = launch_restage(x, ldx, T, c->k, staged, st);
         if (e != hipSuccess)
             return MOE_ERR_HIP;
         g.x = staged;
-        g.ldx = g.K = (int)(i8_stages(c->k) * I8_STAGE);
+        g.ldx = g.K = (int)(stages(c->k) * STAGE_K);
         g.direct = 1;
     }
     return hip_status(launch_i8_product(g, st));
 }
 
 void moe_linear_destroy(moe_linear *l) { delete l; }
+
+moe_status moe_dense_query(const moe_dense_config *cfg, int32_t T_max, size_t *packed_bytes,
+                                 size_t *workspace_bytes)
+{
+    if (!valid_dense(cfg) || T_max < 0)
+        return MOE_ERR_INVALID_ARG;
+    if (!supported_dense(cfg))
+        return MOE_ERR_UNSUPPORTED;
+    if (!product_fits(cfg->n, cfg->glu, 2 * (int64_t)cfg->k, T_max))
+        return MOE_ERR_INVALID_ARG;
+    if (packed_bytes)
+        *packed_bytes = (size_t)dense_packed_bytes(cfg);
+    if (workspace_bytes)
+        *workspace_bytes = (size_t)workspace_bytes_for(2 * (int64_t)cfg->k, T_max);
+    return MOE_OK;
+}
+
+moe_status moe_dense_create(const moe_dense_config *cfg, const moe_dense_weights *w, void *packed,
+                                  size_t packed_bytes, void *stream, moe_dense **out)
+{
+    if (out)
+        *out = nullptr;
+    if (!out || !valid_dense(cfg) || !w || !packed || !aligned(packed, 256))
+        return MOE_ERR_INVALID_ARG;
+    if (!supported_dense(cfg))
+        return MOE_ERR_UNSUPPORTED;
+    if (!w->w || !w->w_up != !cfg->glu || (cfg->glu && w->bias) || !aligned(w->w, 2) || !aligned(w->w_up, 2) ||
+        !aligned(w->bias, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (packed_bytes < (size_t)dense_packed_bytes(cfg))
+        return MOE_ERR_BUFFER_TOO_SMALL;
+    moe_dense *l = new (std::nothrow) moe_dense;
+    if (!l)
+        return MOE_ERR_HIP;
+    uint8_t *p = static_cast<uint8_t *>(packed);
+    float *bias = reinterpret_cast<float *>(p + dense_bias_at(cfg));
+    l->cfg = *cfg;
+    l->blocks = p;
+    l->bias = w->bias ? bias : nullptr;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = launch_pack_product(w->w, w->w_up, cfg->n, 2 * (int64_t)cfg->k, p, st);
+    if (e == hipSuccess && w->bias)
+        e = launch_pack_vectors(nullptr, nullptr, w->bias, cfg->n, row_blocks(cfg->n, false), nullptr, bias, st);
+    if (e != hipSuccess) {
+        delete l;
+        return MOE_ERR_HIP;
+    }
+    *out = l;
+    return MOE_OK;
+}
+
+moe_status moe_dense_forward(moe_dense *l, const void *x, int64_t ldx, const void *residual, int32_t res_type,
+                                   int64_t ldr, int32_t T, void *out, int64_t ldo, void *workspace, size_t workspace_bytes,
+                                   void *stream)
+{
+    if (!l || T < 0)
+        return MOE_ERR_INVALID_ARG;
+    const moe_dense_config *c = &l->cfg;
+    const int64_t k = 2 * (int64_t)c->k;
+    if (!product_fits(c->n, c->glu, k, T))
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0)
+        return MOE_OK;
+    if (!valid_rows(x, ldx, c->k, 2) || !valid_rows(out, ldo, c->n, type_size(c->out_type)) || !aligned(workspace, 256) ||
+        (!workspace && workspace_bytes) ||
+        (residual && (!valid_type(res_type) || !valid_rows(residual, ldr, c->n, type_size(res_type)) ||
+                      (residual == out && (res_type != c->out_type || ldr != ldo)))))
+        return MOE_ERR_INVALID_ARG;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    Bf16Args g{};
+    g.x = static_cast<const int8_t *>(x);
+    g.ldx = 2 * ldx;
+    g.w = l->blocks;
+    g.bias = l->bias;
+    g.residual = residual;
+    g.res_type = res_type;
+    g.ldr = ldr;
+    g.out = out;
+    g.ldo = ldo;
+    g.T = T;
+    g.N = c->n;
+    g.K = (int)k;
+    g.nblk = (int)row_blocks(c->n, c->glu);
+    g.glu = c->glu;
+    g.act = c->act;
+    g.out_type = c->out_type;
+    // Direct loads would bring what lies behind a row's end into its last stage: nothing for whole numbers times the
+    // weights' zeros, but a NaN or an infinity there is one.
+    g.direct = k % STAGE_K == 0 && direct(g.x, g.ldx, k);
+    if (!g.direct && !bf16_takes_any_rows(g)) {
+        if (workspace_bytes < (size_t)workspace_bytes_for(k, T))
+            return MOE_ERR_BUFFER_TOO_SMALL;
+        int8_t *staged = static_cast<int8_t *>(workspace);
+        if (launch_restage(g.x, g.ldx, T, (int)k, staged, st) != hipSuccess)
+            return MOE_ERR_HIP;
+        g.x = staged;
+        g.ldx = g.K = (int)(stages(k) * STAGE_K);
+        g.direct = 1;
+    }
+    return hip_status(launch_bf16_product(g, st));
+}
+
+void moe_dense_destroy(moe_dense *l) { delete l; }
 
 } // extern "C"

@@ -1,6 +1,6 @@
 """What stands around the mixture layer: RMS norm with the residual's addition, the norms between two blocks with gate and
-residual scale, and the dense 8-bit path: quantisation per token, products of 8-bit codes (plain and gated), and a dense
-feed-forward block of them.
+residual scale, and the dense 8-bit path: quantisation per token, products of 8-bit codes (plain and gated) and a dense
+feed-forward block of them; and products of BF16 values with bias, activation and residual.
 
 Torch provides device memory and the stream; all arithmetic runs in the HIP library. Codes are int8
 [rows, width] tensors with one FP32 scale per row. Row-major tensors may be views with any row stride of at
@@ -19,6 +19,8 @@ _BF16, _INT8 = (torch.bfloat16,), (torch.int8,)
 _INT32_MAX = 2 ** 31 - 1   # rows and columns cross the C ABI as 32-bit integers, which ctypes cuts without a word
 _pack = abi.NORM_ARGS.pack
 _pack_block = abi.BLOCK_NORM_ARGS.pack
+_ACTIVATIONS = {None: abi.LINEAR_NONE, "none": abi.LINEAR_NONE, "silu": abi.LINEAR_SILU, "gelu": abi.LINEAR_GELU,
+                "gelu_tanh": abi.LINEAR_GELU_TANH, "relu": abi.LINEAR_RELU}
 _GATES = {None: abi.GATE_NONE, "none": abi.GATE_NONE, "sigmoid": abi.GATE_SIGMOID, "tanh": abi.GATE_TANH}
 _raw_stream = torch._C._cuda_getCurrentRawStream   # of a GPU: its handle, without an object around it
 _current_gpu = torch._C._cuda_getDevice
@@ -327,6 +329,91 @@ class Int8Linear:
     def close(self):
         if self.handle:
             abi.linear_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Bf16Linear:
+    """A dense product of BF16 values with weights packed once: out = a(x . w^T + bias) + residual, or with ``up_weight``
+    the gated form a(x . w^T) * (x . w_up^T) + residual, with FP32 sums and one rounding to ``out_dtype``.
+
+    weight, up_weight: BF16 [N, K]; bias: FP32 [N]; activation a: None, "silu", "gelu", "gelu_tanh" or "relu". The weights
+    are read only while the packing kernels run on ``stream`` and may be dropped after construction. Memory and overlapping
+    calls as of ``Int8Linear``."""
+
+    def __init__(self, weight, bias=None, up_weight=None, activation=None, T_max=8192, out_dtype=torch.bfloat16, stream=None):
+        self.handle = None
+        if out_dtype not in _TYPES:
+            raise ValueError(f"out_dtype: {out_dtype}, expected bfloat16 or float32")
+        if activation not in _ACTIVATIONS:
+            raise ValueError(f"activation: {activation!r}, expected None, 'silu', 'gelu', 'gelu_tanh' or 'relu'")
+        if up_weight is not None and bias is not None:
+            raise ValueError("the gated product takes no bias")
+        if not 0 <= T_max <= _INT32_MAX:
+            raise ValueError(f"T_max: {T_max}, expected 0 to {_INT32_MAX}")
+        self.T_max, self.out_dtype, self.activation = T_max, out_dtype, activation
+        _call(weight, stream, (weight, bias, up_weight), self._create, weight, bias, up_weight)
+
+    def _create(self, weight, bias, up_weight, index, stream):
+        weight = weight.contiguous()   # weights may be views in any order
+        _rows("weight", weight, _BF16, index)
+        self.N, self.K = weight.shape
+        if up_weight is not None:
+            up_weight = up_weight.contiguous()
+            _rows("up_weight", up_weight, _BF16, index, weight.shape)
+        if bias is not None:
+            _vector("bias", bias, self.N, torch.float32, index)
+        self.cfg = abi.DenseConfig(self.N, self.K, int(up_weight is not None), _ACTIVATIONS[self.activation],
+                                        _TYPES[self.out_dtype])
+        packed_bytes, _ = abi.dense_query(self.cfg, self.T_max)
+        self.packed = torch.empty(packed_bytes, dtype=torch.uint8, device=weight.device)
+        self.handle = abi.dense_create(self.cfg, weight, up_weight, bias, self.packed, stream)
+        self._two_rows = abi.dense_query(self.cfg, 2)[1]   # as Int8Linear's
+        self._streams = {stream}
+
+    def forward(self, x, residual=None, out=None, stream=None):
+        """The product for x [T, K] BF16; residual [T, N] BF16 or FP32, optional, which may be ``out`` itself; returns out
+        [T, N]."""
+        if stream is None and (index := self.packed.get_device()) == _current_gpu():
+            return self._forward(x, residual, out, index, _raw_stream(index))
+        return _call(self.packed, stream, (x, residual, out), self._forward, x, residual, out)
+
+    def _forward(self, x, residual, out, index, stream):
+        ldx = _rows("x", x, _BF16, index)
+        T, K = x.shape
+        if K != self.K or T > self.T_max:
+            raise ValueError(f"x: shape {tuple(x.shape)}, expected at most {self.T_max} rows of {self.K}")
+        res, res_type, ldr = 0, 0, 0
+        if residual is not None:
+            ldr = _rows("residual", residual, _TYPES, index, (T, self.N))
+            res, res_type = residual.data_ptr(), _TYPES[residual.dtype]
+        if out is None:
+            ldo = self.N
+            out = torch.empty_strided((T, ldo), (ldo, 1), dtype=self.out_dtype, device=x.device)
+        else:
+            ldo = _rows("out", out, (self.out_dtype,), index, (T, self.N))
+        if stream not in self._streams:   # as Int8Linear's
+            self.packed.record_stream(torch.cuda.current_stream(index))
+            self._streams.add(stream)
+        forward = abi.lib().moe_dense_forward
+        status = forward(self.handle, x.data_ptr(), ldx, res, res_type, ldr, T, out.data_ptr(), ldo, None, 0, stream)
+        if status == abi.Status.BUFFER_TOO_SMALL:   # rows to be laid out first
+            size = (T + 1) // 2 * self._two_rows
+            room = torch.empty(size, dtype=torch.uint8, device=x.device)
+            status = forward(self.handle, x.data_ptr(), ldx, res, res_type, ldr, T, out.data_ptr(), ldo, room.data_ptr(),
+                             size, stream)
+        if status:
+            raise abi.MoEError(status, "moe_dense_forward")
+        return out
+
+    def close(self):
+        if self.handle:
+            abi.dense_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
