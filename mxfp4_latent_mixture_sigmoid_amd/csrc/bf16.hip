@@ -17,26 +17,54 @@ __device__ inline float silu_of(float gate, float v)
     return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * gate));
 }
 
-__device__ inline float activated(float v, int act)
+// v Phi(v) by Abramowitz and Stegun 7.1.26, erfc(x) = t (a1 + t (.. a5)) exp(-x^2) with t = 1 / (1 + p x), off by at most
+// 1.5 x 10^-7: 1.3 |v| 2^-24 of the result. The library's erff, with its branches, in the place of this 256 times in a
+// large tile's epilogue is more than the compiler unrolls.
+__device__ inline float gelu(float v)
+{
+    const float x = fabsf(v) * 0.70710678f, t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+    const float poly = fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                            0.254829592f);
+    const float tail = 0.5f * t * poly * __builtin_amdgcn_exp2f(-1.44269504f * x * x);   // Phi(-|v|)
+    return v * (v < 0.f ? tail : 1.f - tail);
+}
+
+template <int ACT>
+__device__ inline float activated(float v)
+{
+    if constexpr (ACT == MOE_LINEAR_SILU)
+        return silu_of(v, v);
+    if constexpr (ACT == MOE_LINEAR_GELU)
+        return gelu(v);
+    if constexpr (ACT == MOE_LINEAR_GELU_TANH)   // v / 2 (1 + tanh(c)) = v / (1 + exp(-2 c))
+        return silu_of(1.59576912f * fmaf(0.044715f * v * v, v, v), v);
+    if constexpr (ACT == MOE_LINEAR_RELU)
+        return v < 0.f ? 0.f : v;   // NaN stays
+    return v;
+}
+
+// f with the activation as a constant.
+template <class F>
+__device__ inline void with_activation(int act, F f)
 {
     switch (act) {
     case MOE_LINEAR_SILU:
-        return silu_of(v, v);
+        return f(std::integral_constant<int, MOE_LINEAR_SILU>{});
     case MOE_LINEAR_GELU:
-        return 0.5f * v * (1.f + erff(0.70710678f * v));
-    case MOE_LINEAR_GELU_TANH:   // v / 2 (1 + tanh(c)) = v / (1 + exp(-2 c))
-        return silu_of(1.59576912f * fmaf(0.044715f * v * v, v, v), v);
+        return f(std::integral_constant<int, MOE_LINEAR_GELU>{});
+    case MOE_LINEAR_GELU_TANH:
+        return f(std::integral_constant<int, MOE_LINEAR_GELU_TANH>{});
     case MOE_LINEAR_RELU:
-        return v < 0.f ? 0.f : v;   // NaN stays
+        return f(std::integral_constant<int, MOE_LINEAR_RELU>{});
     default:
-        return v;
+        return f(std::integral_constant<int, MOE_LINEAR_NONE>{});
     }
 }
 
-// N consecutive values of row r of the residual from column n on, zeros past the end.
-template <int N>
+// Four consecutive values of row r of the residual from column n on, zeros past the end.
 __device__ inline void load_residual(const Bf16Args &g, int r, int n, float *v)
 {
+    constexpr int N = 4;
 #pragma unroll
     for (int i = 0; i < N; i++)
         v[i] = 0.f;
@@ -67,6 +95,58 @@ __device__ inline void load_residual(const Bf16Args &g, int r, int n, float *v)
     }
 }
 
+// Eight consecutive values of the residual, as they come from memory.
+struct Piece {
+    u32x4_t lo, hi;
+    // of row r from column n on; nothing past the end
+    __device__ void load(const Bf16Args &g, int r, int n)
+    {
+        if (!g.residual || r >= g.T || n >= g.N)
+            return;
+        const int size = g.res_type == MOE_TYPE_F32 ? 4 : 2;
+        const uint8_t *p = static_cast<const uint8_t *>(g.residual) + (r * g.ldr + n) * size;
+        if (n + 8 <= g.N) {
+            __builtin_memcpy(&lo, p, 16);
+            if (size == 4)
+                __builtin_memcpy(&hi, p + 16, 16);
+            return;
+        }
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (n + i < g.N)
+                w[i] = size == 4 ? reinterpret_cast<const uint32_t *>(p)[i] : reinterpret_cast<const uint16_t *>(p)[i];
+            else
+                w[i] = 0;
+        lo = size == 4 ? u32x4_t{w[0], w[1], w[2], w[3]}
+                       : u32x4_t{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+        hi = u32x4_t{w[4], w[5], w[6], w[7]};
+    }
+    __device__ void add(const Bf16Args &g, float *v) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (g.res_type == MOE_TYPE_F32)
+                v[i] += __uint_as_float(i < 4 ? lo[i] : hi[i - 4]);
+            else
+                v[i] += __uint_as_float(i % 2 ? lo[i / 2] & 0xFFFF0000u : lo[i / 2] << 16);
+    }
+};
+
+__device__ inline void store8(const Bf16Args &g, int r, int n, const float *v)
+{
+    if (g.out_type == MOE_TYPE_F32) {
+        u32x4_t lo, hi;
+        __builtin_memcpy(&lo, v, 16);
+        __builtin_memcpy(&hi, v + 4, 16);
+        store16(g, r, n, lo);
+        store16(g, r, n + 4, hi);
+    } else {
+        store16(g, r, n, u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                 pack_bf16x2(v[6], v[7])});
+    }
+}
+
 struct Bf16 {
     using Args = Bf16Args;
     using Acc = f32x4_t;
@@ -91,7 +171,7 @@ struct Bf16 {
         if (g.bias)
             v.bias = *reinterpret_cast<const f32x4_t *>(g.bias + n);
         float res[4];
-        load_residual<4>(g, r, n, res);
+        load_residual(g, r, n, res);
         v.residual = f32x4_t{res[0], res[1], res[2], res[3]};
         return v;
     }
@@ -103,77 +183,91 @@ struct Bf16 {
         if (r >= g.T || n >= g.N)
             return;
         float v[4];
+        with_activation(g.act, [&](auto act) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const float a = activated(sum[i] + c.bias[i], g.act);
-            v[i] = (g.glu ? a * up[i] : a) + c.residual[i];
-        }
+            for (int i = 0; i < 4; i++) {
+                const float a = activated<act>(sum[i] + c.bias[i]);
+                v[i] = (g.glu ? a * up[i] : a) + c.residual[i];
+            }
+        });
         store4(g, r, n, v);
     }
 
-    // Epilogue of the large tiles, 16 tokens at a time through this wave's part of LDS (in FP32, so that the residual is
-    // added before the one rounding), to read the residual and store whole 16-byte pieces of rows. Lane (q = l / 16, c =
-    // l % 16) of fragment (f, j) holds token 16 f + c and packed columns 16 j + 4 q .. +3; when GLU, fragment j + 1 (odd)
-    // holds the up sums of fragment j. The residual of the next 16 tokens is on its way while these are worked on.
+    // Epilogue of the large tiles: half of this wave's sums at a time through its part of LDS, in FP32, so that the residual
+    // is added before the one rounding, and is read, and the outputs stored, in whole 16-byte pieces of rows. Lane (q = l /
+    // 16, c = l % 16) of fragment (f, j) holds token 16 f + c and packed columns 16 j + 4 q .. +3; when GLU, fragment j + 1
+    // (odd) holds the up sums of fragment j. What follows the way through LDS is a loop, one piece of 8 outputs per
+    // lane and round, G rounds a step, whose residuals are loaded a step ahead: unrolled over all sums the code was too
+    // long for the compiler, which then kept the sums in memory (11 ms for 8192 x 7168 x 7168).
+    template <int MF, int NF>
+    static constexpr int pitch() { return NF * 64 + 16; }   // bytes of a token's sums
     template <int MF, int NF, bool GLU, bool>
-    static constexpr int finish_bytes() { return 4 * 16 * ((GLU ? NF / 2 : NF) * 64 + 16); }
+    static constexpr int finish_bytes() { return 4 * MF * 8 * pitch<MF, NF>(); }
     template <int MF, int NF, bool GLU, bool>
     static __device__ void finish(const Bf16Args &g, Acc (&acc)[MF][NF], u32x4_t *lds, int m0, int nb0, int wv)
     {
-        const int lane = threadIdx.x & (WAVE - 1), r16 = lane & 15, fa = wv / 2 * MF, fb = wv % 2 * NF;
-        constexpr int JO = GLU ? NF / 2 : NF, PITCH = JO * 64 + 16;      // output fragments, bytes of a row in LDS
-        constexpr int PIECES = JO * 2, ROUNDS = (16 * PIECES + WAVE - 1) / WAVE;   // of 8 outputs, per row and lane
-        uint8_t *stage = reinterpret_cast<uint8_t *>(lds) + wv * (16 * PITCH);
-        const int n1 = (nb0 + fb) / (GLU ? 2 : 1) * 16, q4 = 4 * (lane >> 4);   // first output column of this wave
-        f32x4_t bias[JO];
+        const int lane = threadIdx.x & (WAVE - 1), fa = wv / 2 * MF, fb = wv % 2 * NF;
+        constexpr int PITCH = pitch<MF, NF>(), PIECES = (GLU ? NF / 2 : NF) * 2;   // pieces of a row
+        constexpr int ROUNDS = MF * 8 * PIECES / WAVE, G = ROUNDS % 4 == 0 ? 4 : ROUNDS % 2 == 0 ? 2 : 1;
+        static_assert(ROUNDS * WAVE == MF * 8 * PIECES && ROUNDS % G == 0, "whole rounds");
+        uint8_t *stage = reinterpret_cast<uint8_t *>(lds) + wv * (MF * 8 * PITCH);
+        const int n1 = (nb0 + fb) / (GLU ? 2 : 1) * 16;   // first output column of this wave
 #pragma unroll
-        for (int j = 0; j < JO; j++)
-            bias[j] = !GLU && g.bias ? *reinterpret_cast<const f32x4_t *>(g.bias + min(nb0 + fb + j, g.nblk - 1) * 16 + q4)
-                                     : f32x4_t{0.f, 0.f, 0.f, 0.f};
-        float res[2][ROUNDS][8];
-        auto load = [&](int f) {
+        for (int half = 0; half < 2; half++) {
+            const int r1 = m0 + fa * 16 + half * MF * 8;
+            Piece next[G];
+            auto load = [&](int round) {
 #pragma unroll
-            for (int i = 0; i < ROUNDS; i++) {
-                const int p = i * WAVE + lane, r = p / PIECES;
-                load_residual<8>(g, r < 16 ? m0 + (fa + f) * 16 + r : g.T, n1 + p % PIECES * 8, res[f % 2][i]);
-            }
-        };
-        load(0);
-#pragma unroll
-        for (int f = 0; f < MF; f++) {
-            if (f + 1 < MF)
-                load(f + 1);
-            uint8_t *at = stage + r16 * PITCH + q4 * 4;
-#pragma unroll
-            for (int j = 0; j < JO; j++) {
-                f32x4_t v;
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    if constexpr (GLU)
-                        v[e] = activated(acc[f][2 * j][e], g.act) * acc[f][2 * j + 1][e];
-                    else
-                        v[e] = activated(acc[f][j][e] + bias[j][e], g.act);
+                for (int i = 0; i < G; i++) {
+                    const int p = (round + i) * WAVE + lane;
+                    next[i].load(g, r1 + p / PIECES, n1 + p % PIECES * 8);
                 }
-                *reinterpret_cast<f32x4_t *>(at + j * 64) = v;
-            }
-            meet_lanes();
+            };
+            load(0);
 #pragma unroll
-            for (int i = 0; i < ROUNDS; i++) {
-                const int p = i * WAVE + lane, r = p / PIECES, c = p % PIECES;
-                const int row = m0 + (fa + f) * 16 + r, n = n1 + c * 8;
-                if (r >= 16 || row >= g.T)
-                    continue;
-                f32x4_t lo = *reinterpret_cast<const f32x4_t *>(stage + r * PITCH + c * 32);
-                f32x4_t hi = *reinterpret_cast<const f32x4_t *>(stage + r * PITCH + c * 32 + 16);
-                const float *s = res[f % 2][i];
-                lo += f32x4_t{s[0], s[1], s[2], s[3]};
-                hi += f32x4_t{s[4], s[5], s[6], s[7]};
-                if (g.out_type == MOE_TYPE_F32) {
-                    store16(g, row, n, __builtin_bit_cast(u32x4_t, lo));
-                    store16(g, row, n + 4, __builtin_bit_cast(u32x4_t, hi));
-                } else {
-                    store16(g, row, n, u32x4_t{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]),
-                                               pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])});
+            for (int f = 0; f < MF / 2; f++)
+#pragma unroll
+                for (int j = 0; j < NF; j++)
+                    *reinterpret_cast<f32x4_t *>(stage + (f * 16 + (lane & 15)) * PITCH + j * 64 + (lane >> 4) * 16) =
+                        acc[half * MF / 2 + f][j];
+            meet_lanes();
+#pragma unroll 1
+            for (int round = 0; round < ROUNDS; round += G) {
+                Piece now[G];
+#pragma unroll
+                for (int i = 0; i < G; i++)
+                    now[i] = next[i];
+                if (round + G < ROUNDS)
+                    load(round + G);
+#pragma unroll
+                for (int i = 0; i < G; i++) {
+                    const int p = (round + i) * WAVE + lane, r = p / PIECES, c = p % PIECES, n = n1 + c * 8;
+                    const uint8_t *at = stage + r * PITCH + (GLU ? c / 2 * 128 + c % 2 * 32 : c * 32);
+                    if (r1 + r >= g.T || n >= g.N)
+                        continue;
+                    float v[8], up[8];
+                    __builtin_memcpy(v, __builtin_assume_aligned(at, 16), 32);
+                    if constexpr (GLU)
+                        __builtin_memcpy(up, __builtin_assume_aligned(at + 64, 16), 32);
+                    else if (g.bias) {   // padded to 16 columns
+                        float b[8];
+                        __builtin_memcpy(b, __builtin_assume_aligned(g.bias + n, 16), 32);
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            v[e] += b[e];
+                    }
+                    with_activation(g.act, [&](auto act) {
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            v[e] = activated<act>(v[e]);
+                    });
+                    if constexpr (GLU)
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            v[e] *= up[e];
+                    if (g.residual)
+                        now[i].add(g, v);
+                    store8(g, r1 + r, n, v);
                 }
             }
             meet_lanes();
