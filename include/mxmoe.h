@@ -213,6 +213,21 @@ moe_status moe_route_forward(moe_handle *h, const void *x, int32_t T, const floa
 moe_status moe_route_forward_static(moe_handle *h, const void *x, int32_t T, const float *logit_bias,
                                     float *logits_out, const moe_routing *r, void *out, void *stream);
 
+/* The whole layer for up to MOE_DECODE_MAX_T tokens in two kernels: a few tokens' step (page "Kimi K3.1 Pro on AMD
+ * Instinct GPUs", sections "Serving with ATOM / What we optimized", paragraph "Mono decode", and "Serving with vLLM / What
+ * we optimized", paragraph on fused low-latency decode). It computes what moe_route_forward does on the same packed
+ * weights, without the arrays of moe_routing, and without rounding an expert's output y to BF16 before the weighted sum,
+ * which it adds in an order of its own: outputs are near moe_route_forward's, not the same bits; ids and weights follow
+ * from logits whose sums are added in another order too. A token's outputs are the same bits whatever tokens come with it.
+ * x: bf16 [T, Hin]; logit_bias: fp32 [E] or NULL; logits_out: fp32 [T, E] or NULL; topk_ids [T, K] and topk_w [T, K] or
+ * NULL; out: bf16 [T, H] (or [T, Lt]); x and out 16-byte aligned, no output overlaps an input or another output.
+ * workspace: 256-byte aligned, moe_decode_query's bytes, not shared by calls that overlap; its contents do not matter.
+ * T = 0 enqueues nothing. MOE_ERR_UNSUPPORTED for more tokens and for configurations with a quantised stage. */
+#define MOE_DECODE_MAX_T 16
+moe_status moe_decode_query(const moe_config *cfg, int32_t T, size_t *workspace_bytes);
+moe_status moe_decode(moe_handle *h, const void *x, int32_t T, const float *logit_bias, float *logits_out,
+                      int32_t *topk_ids, float *topk_w, void *out, void *workspace, size_t workspace_bytes, void *stream);
+
 /* The whole few-token step as one HIP graph (the fused decode step: route, grouping, expert
  * products, combine and shared experts replayed as a unit; page "Kimi K3.1 Pro on AMD Instinct
  * GPUs", sections "Serving with ATOM / What we optimized", paragraph "Mono decode", and "Serving

@@ -121,6 +121,8 @@ SIGNATURES = {
     "moe_route_forward": (c_i32, [c_vp, c_vp, c_i32, c_vp, c_vp, ctypes.POINTER(MoeRouting), c_vp, c_vp, c_size,
                                   c_vp]),
     "moe_route_forward_static": (c_i32, [c_vp, c_vp, c_i32, c_vp, c_vp, ctypes.POINTER(MoeRouting), c_vp, c_vp]),
+    "moe_decode_query": (c_i32, [ctypes.POINTER(MoeConfig), c_i32, ctypes.POINTER(c_size)]),
+    "moe_decode": (c_i32, [c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
     "moe_graph_create": (c_i32, [c_vp, c_vp, c_i32, c_vp, c_vp, ctypes.POINTER(MoeRouting), c_vp, c_vp, c_size,
                                  ctypes.POINTER(c_vp)]),
     "moe_graph_launch": (c_i32, [c_vp, c_vp]),
@@ -251,6 +253,15 @@ def route_forward_static(h, x, T, routing: dict, out, logit_bias=None, logits_ou
     rs = routing_struct(routing)
     check(lib().moe_route_forward_static(h, ptr(x), T, ptr(logit_bias), ptr(logits_out), ctypes.byref(rs), ptr(out),
                                          stream_handle(stream)), "moe_route_forward_static")
+
+
+DECODE_MAX_T = 16   # MOE_DECODE_MAX_T
+
+
+def decode_query(cfg: MoeConfig, T: int) -> int:
+    wb = c_size(0)
+    check(lib().moe_decode_query(ctypes.byref(cfg), T, ctypes.byref(wb)), "moe_decode_query")
+    return wb.value
 
 
 def graph_create(h, x, T, routing: dict, out, workspace, logit_bias=None, logits_out=None):

@@ -1,5 +1,6 @@
 // api.cpp -- the C ABI declared in include/mxmoe.h: validation, packed-buffer and workspace
 // layouts, and the launch sequence of moe_route / moe_forward on the caller's stream.
+#include "decode.hpp"
 #include "kernels.hpp"
 #include "mxmoe.h"
 
@@ -1027,6 +1028,127 @@ moe_status moe_route_forward_static(moe_handle *h, const void *x, int32_t T, con
     // earlier in the same call
     return route_forward_impl(h, x, T, logit_bias, logits_out, r, out, W, static_cast<uint8_t *>(ws),
                               static_cast<hipStream_t>(stream));
+}
+
+} // extern "C"
+
+namespace {
+
+struct DecodeLayout {
+    int64_t counters, logits, ids, weights, list, pairs, shares, z, acat, h, total;
+    int64_t most;   // distinct experts
+};
+
+DecodeLayout decode_layout(const moe_config *c, int64_t T)
+{
+    DecodeLayout L{};
+    const int64_t E = c->n_experts, K = c->top_k, S = c->has_latent_proj ? c->n_shared : 0;
+    L.most = std::min(T * K, E);
+    int64_t off = 0;
+    auto part = [&](int64_t &at, int64_t bytes) {
+        at = off;
+        off = align_up(off + bytes);
+    };
+    part(L.counters, DECODE_COUNTERS * DECODE_COUNTER_WORDS * 4);
+    part(L.logits, T * E * 4);
+    part(L.ids, T * K * 4);
+    part(L.weights, T * K * 4);
+    part(L.list, L.most * 4);
+    part(L.pairs, L.most * DECODE_MAX_T * 4);
+    part(L.shares, L.most * DECODE_MAX_T * 4);
+    part(L.z, c->has_latent_proj ? T * c->latent * 2 : 0);
+    part(L.acat, c->has_latent_proj ? T * (c->latent + S * c->shared_inter) * 2 : 0);
+    part(L.h, T * K * c->inter * 2);
+    L.total = off;
+    return L;
+}
+
+// T in range, no quantised stage, 32-bit byte offsets, and fewer than 2^32 threads in a launch.
+bool decode_supported(const moe_config *c, int64_t T)
+{
+    if (T > MOE_DECODE_MAX_T || c->stage1 != MOE_STAGE1_BF16 || c->stage2 != MOE_STAGE2_BF16)
+        return false;
+    const int64_t S = c->has_latent_proj ? c->n_shared : 0, most = std::min(T * c->top_k, (int64_t)c->n_experts);
+    const int64_t items = 4 + most * (c->inter / 16) + c->latent / 16 + c->hidden / 16;
+    const int64_t front = S * c->shared_inter / 16 + c->latent / 16 + 64;
+    return T * c->top_k * c->inter * 2 <= INT_MAX && T * (c->latent + S * (int64_t)c->shared_inter) * 2 <= INT_MAX &&
+           items <= (1 << 24) - 1 && front <= (1 << 23) - 1;
+}
+
+} // namespace
+
+extern "C" {
+
+moe_status moe_decode_query(const moe_config *cfg, int32_t T, size_t *workspace_bytes)
+{
+    if (!valid_config(cfg) || T < 0 || !workspace_bytes)
+        return MOE_ERR_INVALID_ARG;
+    if (!decode_supported(cfg, T))
+        return MOE_ERR_UNSUPPORTED;
+    *workspace_bytes = (size_t)decode_layout(cfg, T).total;
+    return MOE_OK;
+}
+
+moe_status moe_decode(moe_handle *h, const void *x, int32_t T, const float *logit_bias, float *logits_out,
+                      int32_t *topk_ids, float *topk_w, void *out, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!h || T < 0)
+        return MOE_ERR_INVALID_ARG;
+    const moe_config *c = &h->cfg;
+    if (!decode_supported(c, T))
+        return MOE_ERR_UNSUPPORTED;
+    if (T == 0)
+        return MOE_OK;
+    if (!x || !out || !aligned(x, 16) || !aligned(out, 16) || x == out || !aligned(logit_bias, 4) ||
+        !aligned(logits_out, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) || (const void *)logits_out == x ||
+        (logits_out && (void *)logits_out == out) || !workspace || !aligned(workspace, ALIGN))
+        return MOE_ERR_INVALID_ARG;
+    const DecodeLayout L = decode_layout(c, T);
+    if (workspace_bytes < (size_t)L.total)
+        return MOE_ERR_BUFFER_TOO_SMALL;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const bool lat = c->has_latent_proj != 0, apart = shared_apart(c);
+    const int64_t shared = lat ? (int64_t)c->n_shared * c->shared_inter : 0;
+    DecodeArgs a{};
+    a.x = static_cast<const uint16_t *>(x);
+    a.bias = logit_bias;
+    a.T = T;
+    a.Hin = h->Hin;
+    a.H = c->hidden;
+    a.Lt = c->latent;
+    a.E = c->n_experts;
+    a.K = c->top_k;
+    a.I = c->inter;
+    a.shared = (int)shared;
+    a.has_latent = lat;
+    a.w_router = h->packed + h->off_router;
+    a.n_router_rows = h->E_pad;
+    a.w_latent = h->packed + h->off_xside;
+    a.n_latent_rows = c->latent + (apart ? 0 : 2 * shared);
+    a.w_shared = h->packed + (apart ? h->off_shared : h->off_xside);
+    a.n_shared_rows = apart ? 2 * shared : a.n_latent_rows;
+    a.shared_at = apart ? 0 : c->latent;
+    a.w_out = h->packed + h->off_outside;
+    a.gateup = h->packed + h->off_gateup;
+    a.down = h->packed + h->off_down;
+    a.gateup_stride = h->gateup_stride;
+    a.down_stride = h->down_stride;
+    a.counters = reinterpret_cast<uint32_t *>(ws + L.counters);
+    a.logits = logits_out ? logits_out : reinterpret_cast<float *>(ws + L.logits);
+    a.ids = reinterpret_cast<int32_t *>(ws + L.ids);
+    a.weights = reinterpret_cast<float *>(ws + L.weights);
+    a.list = reinterpret_cast<int32_t *>(ws + L.list);
+    a.pairs = reinterpret_cast<int32_t *>(ws + L.pairs);
+    a.shares = reinterpret_cast<float *>(ws + L.shares);
+    a.most = (int)L.most;
+    a.z = lat ? reinterpret_cast<uint16_t *>(ws + L.z) : const_cast<uint16_t *>(a.x);
+    a.acat = reinterpret_cast<uint16_t *>(ws + L.acat);
+    a.ldcat = (int)(c->latent + shared);
+    a.h = reinterpret_cast<uint16_t *>(ws + L.h);
+    a.ids_out = topk_ids;
+    a.weights_out = topk_w;
+    a.out = static_cast<uint16_t *>(out);
+    return hip_status(launch_decode(a, static_cast<hipStream_t>(stream)));
 }
 
 struct moe_graph {

@@ -2,9 +2,28 @@
 calls the C ABI (torch provides device memory and the stream; all arithmetic runs in HIP)."""
 from __future__ import annotations
 
+from typing import NamedTuple
+
 import torch
 
 from . import abi
+
+
+class Decoded(NamedTuple):
+    """What ``MoELayer.decode`` computes: the layer's output, and the experts of each token with their weights."""
+    out: torch.Tensor       # BF16 [T, H] ([T, latent] without latent projections)
+    ids: torch.Tensor       # int32 [T, K], in rank order
+    weights: torch.Tensor   # FP32 [T, K]
+
+
+def _dense(name, t, shape, dtype, index):
+    """t, checked to be a contiguous tensor of that shape and type on GPU `index`; a new one where it is None."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{name}: expected a contiguous {dtype} {list(shape)} on GPU {index}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    return t
 
 
 class MoELayer:
@@ -34,6 +53,7 @@ class MoELayer:
         self.packed = torch.empty(packed_bytes, dtype=torch.uint8, device=self.device)
         self.workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=self.device)
         self.handle = abi.create(self.cfg, weights, self.packed, stream)
+        self._decode_bytes, self._streams = {}, set()   # decode's workspace by token count; streams that its calls ran on
 
     def alloc_routing(self, T: int) -> dict:
         d, P = self.device, max(T * self.K, 1)
@@ -73,6 +93,49 @@ class MoELayer:
             out = torch.empty(max(T, 1), self.H, dtype=torch.bfloat16, device=self.device)
         abi.route_forward_static(self.handle, x, T, routing, out, logit_bias, logits_out, stream)
         return out
+
+    def decode(self, x, out=None, logit_bias=None, logits_out=None, ids=None, weights=None, stream=None) -> Decoded:
+        """The whole layer for x [T, Hin] BF16 of at most 16 tokens, in two kernels: what route_forward computes, without its
+        routing arrays, and not the same bits (an expert's output is not rounded before the weighted sum). Outputs go into
+        the given tensors if any (contiguous; logits_out FP32 [T, E]). The call allocates its own workspace, so that calls
+        may overlap on different streams and in captured graphs."""
+        index = self.packed.get_device()
+        if stream is not None and stream.device_index != index:
+            raise ValueError(f"stream: on GPU {stream.device_index}, expected GPU {index}")
+        if stream is None:
+            with torch.cuda.device(index):
+                return self._decode(x, out, logit_bias, logits_out, ids, weights, index,
+                                    torch.cuda.current_stream(index).cuda_stream)
+        with torch.cuda.stream(stream):   # what is allocated here belongs to it
+            got = self._decode(x, out, logit_bias, logits_out, ids, weights, index, stream.cuda_stream)
+        for t in (x, out, logit_bias, logits_out, ids, weights):
+            if t is not None:
+                t.record_stream(stream)
+        return got
+
+    def _decode(self, x, out, logit_bias, logits_out, ids, weights, index, stream):
+        Hin = self.H if self.cfg.has_latent_proj else self.Lt
+        if x.dim() != 2 or x.shape[1] != Hin or x.shape[0] > abi.DECODE_MAX_T:
+            raise ValueError(f"x: shape {tuple(x.shape)}, expected at most {abi.DECODE_MAX_T} rows of {Hin}")
+        T = x.shape[0]
+        x = _dense("x", x, (T, Hin), torch.bfloat16, index)
+        out = _dense("out", out, (T, self.H), torch.bfloat16, index)
+        ids = _dense("ids", ids, (T, self.K), torch.int32, index)
+        weights = _dense("weights", weights, (T, self.K), torch.float32, index)
+        if logit_bias is not None:
+            _dense("logit_bias", logit_bias, (self.E,), torch.float32, index)
+        if logits_out is not None:
+            _dense("logits_out", logits_out, (T, self.E), torch.float32, index)
+        size = self._decode_bytes.get(T)
+        if size is None:
+            size = self._decode_bytes[T] = abi.decode_query(self.cfg, T)
+        room = torch.empty(size, dtype=torch.uint8, device=x.device)
+        if stream not in self._streams:   # once for each: a layer dropped while it runs there keeps its memory that long
+            self.packed.record_stream(torch.cuda.current_stream(index))
+            self._streams.add(stream)
+        abi.check(abi.lib().moe_decode(self.handle, x.data_ptr(), T, abi.ptr(logit_bias), abi.ptr(logits_out), ids.data_ptr(),
+                                       weights.data_ptr(), out.data_ptr(), room.data_ptr(), size, stream), "moe_decode")
+        return Decoded(out, ids, weights)
 
     def graph(self, x, T, routing, out, logit_bias=None, logits_out=None):
         """route_forward captured as one HIP graph on these buffers (see StepGraph)."""
