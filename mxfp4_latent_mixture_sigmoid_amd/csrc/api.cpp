@@ -1035,7 +1035,7 @@ moe_status moe_route_forward_static(moe_handle *h, const void *x, int32_t T, con
 namespace {
 
 struct DecodeLayout {
-    int64_t counters, logits, ids, weights, list, pairs, shares, z, acat, h, total;
+    int64_t counters, column_counters, partial, logits, weights, list, pairs, z, z_rest, acat, h, total;
     int64_t most;   // distinct experts
 };
 
@@ -1049,15 +1049,17 @@ DecodeLayout decode_layout(const moe_config *c, int64_t T)
         at = off;
         off = align_up(off + bytes);
     };
-    part(L.counters, DECODE_COUNTERS * DECODE_COUNTER_WORDS * 4);
+    const int64_t lat = c->has_latent_proj ? 1 : 0, Lt = c->latent, parts = T > 1 ? DECODE_PARTS : 0;
+    part(L.counters, DECODE_COUNTER_LINES * DECODE_COUNTER_WORDS * 4);
+    part(L.column_counters, parts ? Lt / 16 * 4 : 0);
+    part(L.partial, Lt / 16 * parts * 256 * 4);
     part(L.logits, T * E * 4);
-    part(L.ids, T * K * 4);
     part(L.weights, T * K * 4);
     part(L.list, L.most * 4);
-    part(L.pairs, L.most * DECODE_MAX_T * 4);
-    part(L.shares, L.most * DECODE_MAX_T * 4);
-    part(L.z, c->has_latent_proj ? T * c->latent * 2 : 0);
-    part(L.acat, c->has_latent_proj ? T * (c->latent + S * c->shared_inter) * 2 : 0);
+    part(L.pairs, L.most * DECODE_MAX_T * 2);
+    part(L.z, lat * T * Lt * 2);
+    part(L.z_rest, lat * T * Lt * 2);
+    part(L.acat, lat * T * (Lt + S * c->shared_inter) * 2);
     part(L.h, T * K * c->inter * 2);
     L.total = off;
     return L;
@@ -1069,7 +1071,7 @@ bool decode_supported(const moe_config *c, int64_t T)
     if (T > MOE_DECODE_MAX_T || c->stage1 != MOE_STAGE1_BF16 || c->stage2 != MOE_STAGE2_BF16)
         return false;
     const int64_t S = c->has_latent_proj ? c->n_shared : 0, most = std::min(T * c->top_k, (int64_t)c->n_experts);
-    const int64_t items = 4 + most * (c->inter / 16) + c->latent / 16 + c->hidden / 16;
+    const int64_t items = 4 + most * (c->inter / 16) + c->latent / 16 * DECODE_PARTS + c->hidden / 16;
     const int64_t front = S * c->shared_inter / 16 + c->latent / 16 + 64;
     return T * c->top_k * c->inter * 2 <= INT_MAX && T * (c->latent + S * (int64_t)c->shared_inter) * 2 <= INT_MAX &&
            items <= (1 << 24) - 1 && front <= (1 << 23) - 1;
@@ -1135,11 +1137,12 @@ moe_status moe_decode(moe_handle *h, const void *x, int32_t T, const float *logi
     a.down_stride = h->down_stride;
     a.counters = reinterpret_cast<uint32_t *>(ws + L.counters);
     a.logits = logits_out ? logits_out : reinterpret_cast<float *>(ws + L.logits);
-    a.ids = reinterpret_cast<int32_t *>(ws + L.ids);
     a.weights = reinterpret_cast<float *>(ws + L.weights);
     a.list = reinterpret_cast<int32_t *>(ws + L.list);
-    a.pairs = reinterpret_cast<int32_t *>(ws + L.pairs);
-    a.shares = reinterpret_cast<float *>(ws + L.shares);
+    a.pairs = reinterpret_cast<int16_t *>(ws + L.pairs);
+    a.column_counters = reinterpret_cast<uint32_t *>(ws + L.column_counters);
+    a.partial = reinterpret_cast<float *>(ws + L.partial);
+    a.z_rest = reinterpret_cast<uint16_t *>(ws + L.z_rest);
     a.most = (int)L.most;
     a.z = lat ? reinterpret_cast<uint16_t *>(ws + L.z) : const_cast<uint16_t *>(a.x);
     a.acat = reinterpret_cast<uint16_t *>(ws + L.acat);

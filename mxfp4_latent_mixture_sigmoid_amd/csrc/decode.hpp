@@ -8,9 +8,12 @@ namespace mxmoe {
 
 constexpr int DECODE_MAX_T = MOE_DECODE_MAX_T;   // the rows of a matrix-core tile
 
-// Counters, on cache lines of their own.
-enum { DECODE_TICKET, DECODE_TOP, DECODE_READY, DECODE_GATE, DECODE_DOWN, DECODE_COUNTERS };
+// Counters and flags (each flag in 64 places), one to a cache line.
+enum { DECODE_TICKET, DECODE_GATE, DECODE_DOWN, DECODE_COUNTERS };
+enum { DECODE_READY, DECODE_GATE_DONE, DECODE_DOWN_DONE, DECODE_FLAGS };
 constexpr int DECODE_COUNTER_WORDS = 32;
+constexpr int DECODE_COUNTER_LINES = DECODE_COUNTERS + DECODE_FLAGS * 64;
+constexpr int DECODE_PARTS = 4;   // workgroups that share 16 columns of the down product, for more than one token
 
 struct DecodeArgs {
     const uint16_t *x;               // [T, Hin]
@@ -23,15 +26,16 @@ struct DecodeArgs {
     int64_t n_router_rows, n_latent_rows, n_shared_rows, shared_at;   // rows of their matrices; the shared ones' first row
     int64_t gateup_stride, down_stride;
     // workspace
-    uint32_t *counters;
+    uint32_t *counters;              // DECODE_COUNTER_LINES lines
+    uint32_t *column_counters;       // [Lt / 16] arrivals of a column block's parts
+    float *partial;                  // [Lt / 16][DECODE_PARTS][16][16] their sums
     float *logits;                   // [T, E]
-    int32_t *ids;                    // [T, K]
     float *weights;                  // [T, K]
     int32_t *list;                   // [most] distinct experts, ascending
-    int32_t *pairs;                  // [most, 16] the pair of (expert, token), or -1
-    float *shares;                   // [most, 16] its weight
+    int16_t *pairs;                  // [most, 16] the pair of (expert, token), or -1
     int most;                        // min(T K, E)
     uint16_t *z;                     // [T, Lt]; x itself without latent projections
+    uint16_t *z_rest;                // [T, Lt] what z's rounding left; unused without latent projections
     uint16_t *acat;                  // [T, ldcat]: zc, then h_s
     int ldcat;
     uint16_t *h;                     // [T K, I]
@@ -41,13 +45,15 @@ struct DecodeArgs {
     uint16_t *out;                   // [T, H] ([T, Lt] without latent projections)
 };
 
-// Work items of the second kernel, in the order in which they are taken.
+// Work items of the second kernel, in the order in which they are taken. One token's experts are few enough for one
+// workgroup to a column block; more are shared by DECODE_PARTS.
 struct DecodeItems {
-    int top, gate, down, out;
+    int top, gate, down, out, parts;
 };
 __host__ __device__ inline DecodeItems decode_items(const DecodeArgs &a)
 {
-    return {(a.T + 3) / 4, a.most * (a.I / 16), a.Lt / 16, a.has_latent ? a.H / 16 : 0};
+    const int parts = a.T == 1 ? 1 : DECODE_PARTS;
+    return {1, a.most * (a.I / 16), a.Lt / 16 * parts, a.has_latent ? a.H / 16 : 0, parts};
 }
 
 hipError_t launch_decode(const DecodeArgs &a, hipStream_t st);
