@@ -228,6 +228,10 @@ moe_status moe_decode_query(const moe_config *cfg, int32_t T, size_t *workspace_
 moe_status moe_decode(moe_handle *h, const void *x, int32_t T, const float *logit_bias, float *logits_out,
                       int32_t *topk_ids, float *topk_w, void *out, void *workspace, size_t workspace_bytes, void *stream);
 
+/* Test hook: how often a workgroup of later moe_decode calls asks for what it waits for (negative: the default) before it
+ * does other workgroups' work that has not been started. Results are the same bits. */
+void moe_decode_patience(int32_t times);
+
 /* The whole few-token step as one HIP graph (the fused decode step: route, grouping, expert
  * products, combine and shared experts replayed as a unit; page "Kimi K3.1 Pro on AMD Instinct
  * GPUs", sections "Serving with ATOM / What we optimized", paragraph "Mono decode", and "Serving

@@ -1034,8 +1034,10 @@ moe_status moe_route_forward_static(moe_handle *h, const void *x, int32_t T, con
 
 namespace {
 
+int decode_patience = DECODE_PATIENCE;
+
 struct DecodeLayout {
-    int64_t counters, column_counters, partial, logits, weights, list, pairs, z, z_rest, acat, h, total;
+    int64_t counters, claims, column_counters, partial, logits, weights, list, pairs, z, z_rest, acat, h, total;
     int64_t most;   // distinct experts
 };
 
@@ -1051,6 +1053,7 @@ DecodeLayout decode_layout(const moe_config *c, int64_t T)
     };
     const int64_t lat = c->has_latent_proj ? 1 : 0, Lt = c->latent, parts = T > 1 ? DECODE_PARTS : 0;
     part(L.counters, DECODE_COUNTER_LINES * DECODE_COUNTER_WORDS * 4);
+    part(L.claims, (1 + L.most * (c->inter / 16) + Lt / 16 * std::max<int64_t>(parts, 1) + lat * c->hidden / 16) * 4);
     part(L.column_counters, parts ? Lt / 16 * 4 : 0);
     part(L.partial, Lt / 16 * parts * 256 * 4);
     part(L.logits, T * E * 4);
@@ -1073,13 +1076,18 @@ bool decode_supported(const moe_config *c, int64_t T)
     const int64_t S = c->has_latent_proj ? c->n_shared : 0, most = std::min(T * c->top_k, (int64_t)c->n_experts);
     const int64_t items = 4 + most * (c->inter / 16) + c->latent / 16 * DECODE_PARTS + c->hidden / 16;
     const int64_t front = S * c->shared_inter / 16 + c->latent / 16 + 64;
-    return T * c->top_k * c->inter * 2 <= INT_MAX && T * (c->latent + S * (int64_t)c->shared_inter) * 2 <= INT_MAX &&
-           items <= (1 << 24) - 1 && front <= (1 << 23) - 1;
+    const int64_t Hin = c->has_latent_proj ? c->hidden : c->latent, cat = c->latent + S * (int64_t)c->shared_inter;
+    const int64_t widest = std::max({(c->latent + 2 * S * (int64_t)c->shared_inter) * Hin, (c->n_experts + 15) * Hin,
+                                     c->has_latent_proj ? cat * c->hidden : 0, T * c->top_k * c->inter, T * cat, T * Hin,
+                                     c->latent * 2 * (int64_t)MX_STEP, c->inter * (int64_t)MX_STEP});
+    return widest * 2 < DECODE_MAX_WINDOW && items <= (1 << 24) - 1 && front <= (1 << 23) - 1;
 }
 
 } // namespace
 
 extern "C" {
+
+void moe_decode_patience(int32_t times) { decode_patience = times < 0 ? DECODE_PATIENCE : times; }
 
 moe_status moe_decode_query(const moe_config *cfg, int32_t T, size_t *workspace_bytes)
 {
@@ -1141,6 +1149,8 @@ moe_status moe_decode(moe_handle *h, const void *x, int32_t T, const float *logi
     a.list = reinterpret_cast<int32_t *>(ws + L.list);
     a.pairs = reinterpret_cast<int16_t *>(ws + L.pairs);
     a.column_counters = reinterpret_cast<uint32_t *>(ws + L.column_counters);
+    a.claims = reinterpret_cast<uint32_t *>(ws + L.claims);
+    a.patience = decode_patience;
     a.partial = reinterpret_cast<float *>(ws + L.partial);
     a.z_rest = reinterpret_cast<uint16_t *>(ws + L.z_rest);
     a.most = (int)L.most;

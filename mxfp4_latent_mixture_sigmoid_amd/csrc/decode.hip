@@ -5,9 +5,9 @@
 // and shared matrices in BF16, 16 experts in MXFP4).
 //
 //  front_kernel  what only needs x: the router's logits, z = x W_down^T, h_s = bf16(silu(x Wg_s^T) (x Wu_s^T)).
-//  rest_kernel   everything after it, one work item per workgroup, taken in the order of a ticket counter:
+//  rest_kernel   everything after it, in work items, one for each workgroup:
 //    top    the top-K of every token; the list of distinct experts and each one's tokens
-//    gate   (expert, 16 or 32 inner channels): h = bf16(silu(z Wg^T) (z Wu^T)) of the expert's tokens
+//    gate   (expert, 16 inner channels): h = bf16(silu(z Wg^T) (z Wu^T)) of the expert's tokens
 //    down   16 latent columns of every chosen expert, or of a quarter of them: zc = bf16(sum w (h Wd^T)), summed in FP32
 //    out    16 output columns: out = bf16([zc | h_s] [W_up | W_ds]^T)
 //
@@ -15,12 +15,20 @@
 // expert's gate, up and product (0.4% of a small layer's output in the mean square, against 0.3% without); the
 // remainders are rows 8 to 15 of the tile for up to 8 tokens, at no cost, and a second operand for more.
 //
-// Kinds wait for each other. An item waits only for items of earlier kinds, all of which have lower tickets, and a ticket
-// is drawn by a workgroup that already runs: so whatever an item waits for is done or
-// being worked on, and the waits end however many workgroups the card holds at once and whatever else runs on it. What one
-// workgroup hands to another goes through agent-coherent stores and loads (sync.hpp). A counter that hundreds of
-// workgroups ask for is a queue at one memory channel (1057 of them: 100 us): the last to arrive therefore writes a flag in
-// 64 places, and each workgroup asks for one of them. The front kernel clears counters and flags for the rest kernel.
+// Kinds wait for each other on flags. A workgroup takes the item of its number by claiming it; it waits for a flag PATIENCE
+// times, far longer than a call takes, and if the flag has not come by then (its workgroups may not even have started:
+// another call's, which wait for theirs, may hold their places) it claims and does whatever item of an earlier kind is
+// still free, in order, and waits again. Then every item that it waits for is done or being worked on by a workgroup that
+// runs, so that all waits end, however many workgroups the card holds at once and whatever else runs on it. (Drawing
+// items from one ticket counter gives that too, but additions to one address take 12 ns each: 1057 workgroups kept the
+// top-K's loads waiting for 9 us behind theirs.) For the same reason arrivals are counted at 16 counters first, and the
+// last one writes its flag in 64 places, each asked for by a part of the workgroups. What one workgroup hands to another
+// goes through agent-coherent stores and loads (sync.hpp). The front kernel clears counters, flags and claims.
+//
+// Two things set the pace of code that runs once. Instructions come from memory at about 1 KiB a microsecond the first
+// time: so the top-K is written to be short, and while an item waits it goes once through what it will do, with empty
+// windows for its loads and stores (`go` = 0). And a load under a condition is a wait for the loads before it: so no
+// load has one; loads past the end lie outside their window, which costs nothing.
 #include "decode.hpp"
 #include "select.hpp"
 #include "sync.hpp"
@@ -32,7 +40,9 @@ namespace {
 constexpr int ROWS = DECODE_MAX_T, HALF = ROWS / 2;
 constexpr int FRONT_WAVES = 8, REST_WAVES = 4;
 constexpr int FLAGS = WAVE;                 // places of a flag
-constexpr int STAGE_WORDS = 2048;           // LDS of a wave for its activations, where they fit
+constexpr int ARMS = DECODE_ARMS;
+constexpr int STAGE_WORDS = 1856;           // LDS of a wave for its activations, where they fit
+constexpr int LDS_WORDS = REST_WAVES * STAGE_WORDS + REST_WAVES * 512;   // of an item; four workgroups share a CU
 
 __device__ inline uint32_t *counter(const DecodeArgs &a, int i) { return a.counters + i * DECODE_COUNTER_WORDS; }
 __device__ inline uint32_t *flag(const DecodeArgs &a, int i, int place)
@@ -42,7 +52,20 @@ __device__ inline uint32_t *flag(const DecodeArgs &a, int i, int place)
 
 __device__ inline int lane_id() { return threadIdx.x & (WAVE - 1); }
 __device__ inline int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE); }
-constexpr u32x4_t ZERO = {0u, 0u, 0u, 0u};
+
+// Windows for loads and stores: those outside read zeros and write nothing, without touching memory. `go` = 0: an empty one.
+constexpr int OUTSIDE = DECODE_MAX_WINDOW;   // an offset past every window
+__device__ inline __amdgpu_buffer_rsrc_t window(const void *base, int64_t bytes, int go) { return flat_rsrc(base, go ? bytes : 0); }
+template <int CPOL>
+__device__ inline u32x4_t fetch16(__amdgpu_buffer_rsrc_t w, int offset)
+{
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(w, offset, 0, CPOL));
+}
+template <int CPOL>
+__device__ inline uint32_t fetch4(__amdgpu_buffer_rsrc_t w, int offset)
+{
+    return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(w, offset, 0, CPOL);
+}
 
 // Lane l's four sums of a fragment are those of rows 4 (l / 16) .. +3 in column l % 16.
 __device__ inline void store_sums(float *red, f32x4_t v)
@@ -72,37 +95,32 @@ template <int NB, int DEPTH, int AHEAD>
 struct Bf16Part {
     static_assert(DEPTH % AHEAD == 0, "slots");
     u32x4_t b[DEPTH][NB];
-    const uint8_t *w, *at;   // the matrix, and the next step's first block
-    int64_t N, K;
-    int nb0, s0, s1, next, pitch;   // next step, blocks from a row block to the next one in its K chunk
+    __amdgpu_buffer_rsrc_t w;
+    int s0, s1, next, at, jump, last, tail;   // steps; the next step's first block
 
-    __device__ void seek()
-    {
-        at = w + bf16_block_index(nb0, next, N, K) * BF16_BLOCK_BYTES;
-        pitch = min(BF16_CHUNK_STEPS, (int)(K / BF16_STEP) - next / BF16_CHUNK_STEPS * BF16_CHUNK_STEPS);
-    }
     // Steps are loaded one after another, each into slot (step - s0) % DEPTH.
     __device__ void load(int slot)
     {
-        if (next >= s1)
-            return;
+        const int pitch = next >= last ? tail : BF16_CHUNK_STEPS;   // blocks from a row block to the next in this K chunk
+        const int off = next < s1 ? at * BF16_BLOCK_BYTES : OUTSIDE;
 #pragma unroll
         for (int j = 0; j < NB; j++)
-            b[slot][j] = load16_nt(at + j * pitch * BF16_BLOCK_BYTES + lane_id() * 16);
-        at += BF16_BLOCK_BYTES;
-        if (++next % BF16_CHUNK_STEPS == 0)
-            seek();
+            b[slot][j] = fetch16<CPOL_NT>(w, off + (next < s1 ? j * pitch * BF16_BLOCK_BYTES : 0) + lane_id() * 16);
+        next++;
+        at += next % BF16_CHUNK_STEPS == 0 ? next == last ? jump + 1 - (BF16_CHUNK_STEPS - tail) * block : jump + 1 : 1;
     }
-    __device__ void start(const uint8_t *weights, int64_t rows, int64_t width, int block, int wave, int waves)
+    int block;
+    __device__ void start(const uint8_t *weights, int64_t N, int64_t K, int nb, int wave, int waves, int go = 1)
     {
-        w = weights;
-        N = rows;
-        K = width;
-        nb0 = block;
         const int steps = (int)(K / BF16_STEP);
+        w = window(weights, N * K * 2, go);
         next = s0 = steps * wave / waves;
         s1 = steps * (wave + 1) / waves;
-        seek();
+        block = nb;
+        last = steps / BF16_CHUNK_STEPS * BF16_CHUNK_STEPS;   // the first step of a last chunk of `tail` steps
+        tail = steps % BF16_CHUNK_STEPS;
+        jump = BF16_CHUNK_STEPS * (int)(N / 16) - BF16_CHUNK_STEPS;   // from the end of a chunk's part to the next one's
+        at = (int)bf16_block_index(nb, next, N, K);
 #pragma unroll
         for (int i = 0; i < DEPTH; i++)
             load(i);
@@ -115,53 +133,55 @@ struct Bf16Part {
         const int lane = lane_id(), n = s1 - s0, pitch = n * 16 + 4;   // words of a token's part in LDS
         const int r = lane & 15, c = lane >> 4;
         if (T * pitch <= STAGE_WORDS) {
+#pragma unroll 1
             for (int i0 = 0; i0 < T * n * 4; i0 += 4 * WAVE) {
                 u32x4_t v[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const int at = i0 + i * WAVE + lane;
-                    if (at < T * n * 4)
-                        v[i] = get(at / (n * 4), s0 * BF16_STEP + at % (n * 4) * 8);
+                    const int at = min(i0 + i * WAVE + lane, T * n * 4 - 1);
+                    v[i] = get(at / (n * 4), s0 * BF16_STEP + at % (n * 4) * 8);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const int at = i0 + i * WAVE + lane;
-                    if (at < T * n * 4)
-                        *reinterpret_cast<u32x4_t *>(stage + at / (n * 4) * pitch + at % (n * 4) * 4) = v[i];
+                    const int at = min(i0 + i * WAVE + lane, T * n * 4 - 1);
+                    *reinterpret_cast<u32x4_t *>(stage + at / (n * 4) * pitch + at % (n * 4) * 4) = v[i];
                 }
             }
-            // rows past the tokens repeat the last one: their sums are not used
+            // rows past the tokens repeat the last one: their sums are not used. Steps past the end multiply zeros.
             const uint32_t *mine = stage + min(r, T - 1) * pitch + c * 4;
-            for (int s = s0; s < s1; s += DEPTH)
+#pragma unroll 1
+            for (int s = 0; s < n; s += DEPTH)
 #pragma unroll
-                for (int i = 0; i < DEPTH; i++)
-                    if (s + i < s1) {
-                        const u32x4_t x = *reinterpret_cast<const u32x4_t *>(mine + (s + i - s0) * 16);
+                for (int i = 0; i < DEPTH; i++) {
+                    const u32x4_t x = *reinterpret_cast<const u32x4_t *>(mine + min(s + i, n - 1) * 16);
 #pragma unroll
-                        for (int j = 0; j < NB; j++)
-                            acc[j] = mfma16(as_bf16x8(x), as_bf16x8(b[i][j]), acc[j]);
-                        load(i);
-                    }
+                    for (int j = 0; j < NB; j++)
+                        acc[j] = step(x, b[i][j], acc[j], s + i < n);
+                    load(i);
+                }
             return;
         }
         u32x4_t x[AHEAD];
-        auto operand = [&](int s, int slot) {
-            if (s < s1)
-                x[slot] = r < T ? get(r, s * BF16_STEP + c * 8) : ZERO;
-        };
+        auto operand = [&](int s, int slot) { x[slot] = get(min(r, T - 1), (s0 + min(s, n - 1)) * BF16_STEP + c * 8); };
 #pragma unroll
         for (int i = 0; i < AHEAD; i++)
-            operand(s0 + i, i);
-        for (int s = s0; s < s1; s += DEPTH)
+            operand(i, i);
+#pragma unroll 1
+        for (int s = 0; s < n; s += DEPTH)
 #pragma unroll
-            for (int i = 0; i < DEPTH; i++)
-                if (s + i < s1) {
+            for (int i = 0; i < DEPTH; i++) {
 #pragma unroll
-                    for (int j = 0; j < NB; j++)
-                        acc[j] = mfma16(as_bf16x8(x[i % AHEAD]), as_bf16x8(b[i][j]), acc[j]);
-                    load(i);
-                    operand(s + i + AHEAD, i % AHEAD);
-                }
+                for (int j = 0; j < NB; j++)
+                    acc[j] = step(x[i % AHEAD], b[i][j], acc[j], s + i < n);
+                load(i);
+                operand(s + i + AHEAD, i % AHEAD);
+            }
+    }
+    // A step past the end adds nothing, whatever the activations are.
+    static __device__ f32x4_t step(u32x4_t x, u32x4_t w, f32x4_t acc, bool in)
+    {
+        const f32x4_t v = mfma16(as_bf16x8(x), as_bf16x8(w), acc);
+        return in ? v : acc;
     }
 };
 
@@ -187,10 +207,14 @@ __global__ __launch_bounds__(WAVE *FRONT_WAVES, 4) void front_kernel(const Decod
     __shared__ uint32_t lds[FRONT_WAVES * STAGE_WORDS];
     const float *red = reinterpret_cast<const float *>(lds);
     const int t = threadIdx.x;
-    if (blockIdx.x == 0 && t < DECODE_COUNTERS + DECODE_FLAGS * FLAGS)
+    static_assert(DECODE_COUNTER_LINES <= WAVE * FRONT_WAVES, "a thread each");
+    if (blockIdx.x == 0 && t < DECODE_COUNTER_LINES)
         a.counters[t * DECODE_COUNTER_WORDS] = 0u;
-    if (blockIdx.x == 0 && a.T > 1)
-        for (int i = t; i < a.Lt / 16; i += WAVE * FRONT_WAVES)
+    const int threads = gridDim.x * WAVE * FRONT_WAVES, number = blockIdx.x * WAVE * FRONT_WAVES + t;
+    for (int i = number; i < decode_item_count(decode_items(a)); i += threads)
+        a.claims[i] = 0u;
+    if (a.T > 1)
+        for (int i = number; i < a.Lt / 16; i += threads)
             a.column_counters[i] = 0u;
     const int pairs = a.shared / 16, latent = a.has_latent ? a.Lt / 16 : 0;
     int item = blockIdx.x;
@@ -222,13 +246,16 @@ __global__ __launch_bounds__(WAVE *FRONT_WAVES, 4) void front_kernel(const Decod
     }
 }
 
-// Until flag i is set. One thread asks; what follows in any thread is after the answer. Returns the flag less one.
+// Until flag i is set: its value less one, or -1 when patience runs out (HELP: never). One thread asks; what follows in any
+// thread is after the answer.
+template <bool HELP>
 __device__ inline int wait_for(const DecodeArgs &a, int i, uint32_t *sh)
 {
     if (threadIdx.x == 0) {
         const uint32_t *at = flag(a, i, blockIdx.x % FLAGS);
         uint32_t v;
-        while ((v = __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) == 0u)
+        int left = a.patience;
+        while ((v = __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) == 0u && (HELP || left-- > 0))
             __builtin_amdgcn_s_sleep(2);
         *sh = v - 1;
     }
@@ -237,6 +264,20 @@ __device__ inline int wait_for(const DecodeArgs &a, int i, uint32_t *sh)
     __syncthreads();
     asm volatile("" ::: "memory");
     return v;
+}
+
+// Whether item `i` is this workgroup's now.
+__device__ inline bool claim(const DecodeArgs &a, int i, uint32_t *sh)
+{
+    if (threadIdx.x == 0) {
+        uint32_t *at = a.claims + i;
+        *sh = __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0u &&
+              __hip_atomic_fetch_add(at, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0u;
+    }
+    __syncthreads();
+    const bool mine = __builtin_amdgcn_readfirstlane((int)*sh) != 0;
+    __syncthreads();
+    return mine;
 }
 
 __device__ inline void set_flag(const DecodeArgs &a, int i, uint32_t v)   // by a wave
@@ -252,46 +293,132 @@ __device__ inline void stores_done()
     __syncthreads();
 }
 
-// This workgroup's arrival at a counter after its stores; true in the first wave of the last of `all` to arrive.
-__device__ inline bool arrive(uint32_t *at, uint32_t all)
+__device__ inline bool last_at(uint32_t *at, int all)   // by a wave
+{
+    uint32_t before = 0u;
+    if (lane_id() == 0)
+        before = __hip_atomic_fetch_add(at, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return __builtin_amdgcn_readfirstlane((int)before) == all - 1;
+}
+
+// Arrival number i of `all` at counter set `at` after this workgroup's stores; true in the first wave of the last to
+// arrive. Additions to one address take 12 ns each, so the arrivals are counted at ARMS counters first.
+__device__ inline bool arrive(const DecodeArgs &a, int set, int i, int all)
 {
     stores_done();
     if (wave_id() != 0)
         return false;
-    uint32_t before = 0u;
-    if (lane_id() == 0)
-        before = __hip_atomic_fetch_add(at, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    return (uint32_t)__builtin_amdgcn_readfirstlane((int)before) == all - 1;
+    const int arm = i % ARMS, at = set * (ARMS + 1);
+    return last_at(counter(a, at + arm), (all - arm + ARMS - 1) / ARMS) && last_at(counter(a, at + ARMS), min(all, ARMS));
 }
 
-template <int SLOTS>
+// select_best of select.hpp in little code, from a token's logits in memory; the keys are kept in LDS (`words`, E rounded up to
+// 256), four of a lane side by side. No key of an expert is 0, which stands for none (only a NaN with every bit set
+// would have it), so that ids are always in range.
+__device__ inline void select_short(const float *logits, int E, int K, uint32_t *words, uint64_t *scratch, int *id, float *weight)
+{
+    constexpr int QUADS = DECODE_MAX_E / (4 * WAVE);
+    const int lane = lane_id(), quads = (E + 4 * WAVE - 1) / (4 * WAVE);
+    const auto row = flat_rsrc(logits, (int64_t)E * 4);
+    u32x4_t raw[QUADS];
+#pragma unroll
+    for (int q = 0; q < QUADS; q++)
+        raw[q] = fetch16<0>(row, (q * WAVE + lane) * 16);
+#pragma unroll
+    for (int q = 0; q < QUADS; q++)
+        *reinterpret_cast<u32x4_t *>(words + (q * WAVE + lane) * 4) = raw[q];
+    uint32_t top = 0u;
+#pragma unroll 1
+    for (int q = 0; q < quads; q++) {
+        u32x4_t v = *reinterpret_cast<const u32x4_t *>(words + (q * WAVE + lane) * 4);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            v[j] = (q * WAVE + lane) * 4 + j < E ? max(order_key(__uint_as_float(v[j])), 1u) : 0u;
+            top = max(top, v[j]);
+        }
+        *reinterpret_cast<u32x4_t *>(words + (q * WAVE + lane) * 4) = v;
+    }
+    uint32_t bound = 0u;
+#pragma unroll 1
+    for (uint32_t bit = 1u << 31; bit; bit >>= 1)
+        if ((int)__popcll(__ballot(top >= (bound | bit))) >= K)
+            bound |= bit;
+    int total = 0;
+#pragma unroll 1
+    for (int q = 0; q < quads; q++) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(words + (q * WAVE + lane) * 4);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const bool in = v[j] != 0u && v[j] >= bound;
+            const uint64_t all = __ballot(in);
+            const int at = total + (int)__popcll(all & ((1ull << lane) - 1));
+            if (in && at < WAVE)
+                scratch[at] = ((uint64_t)v[j] << 32) | (uint32_t)~(uint32_t)((q * WAVE + lane) * 4 + j);
+            total += (int)__popcll(all);
+        }
+    }
+    uint64_t mine = 0;
+    if (total <= WAVE) {
+        mine = lane < total ? scratch[lane] : 0;
+        int rank = 0;
+#pragma unroll 2
+        for (int m = 0; m < total; m++) {
+            const uint64_t other = ((uint64_t)__builtin_amdgcn_readlane((int)(mine >> 32), m) << 32) |
+                                   (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)mine, m);
+            rank += other > mine;
+        }
+        if (lane < total && rank < K)
+            scratch[rank] = mine;
+        mine = lane < K ? scratch[lane] : 0;
+    } else {   // heavy ties: one maximum after another
+#pragma unroll 1
+        for (int k = 0; k < K; k++) {
+            uint64_t best = 0;
+#pragma unroll 1
+            for (int e = lane; e < E; e += WAVE)
+                if (words[e]) {
+                    const uint64_t v = ((uint64_t)words[e] << 32) | (uint32_t)~(uint32_t)e;
+                    best = v > best ? v : best;
+                }
+            const uint32_t high = wave_max_u32((uint32_t)(best >> 32));
+            const uint32_t low = wave_max_u32((uint32_t)(best >> 32) == high ? (uint32_t)best : 0u);
+            if (lane == k)
+                mine = ((uint64_t)high << 32) | low;
+            if (((uint64_t)high << 32 | low) == best)
+                words[~low] = 0u;
+        }
+    }
+    const float s = lane < K ? 1.0f / (1.0f + expf(-key_value((uint32_t)(mine >> 32)))) : 0.0f;
+    *id = (int)~(uint32_t)mine;
+    *weight = s / wave_sum_f32(s);
+}
+
 __device__ inline void top_item(const DecodeArgs &a, uint32_t *words)
 {
     __shared__ uint64_t scratch[REST_WAVES][WAVE];
     const int lane = lane_id(), wv = wave_id();
     const int T = a.T, K = a.K, E = a.E, P = T * K;
-    uint32_t *masks = words;              // of an expert's tokens
-    int *chosen = reinterpret_cast<int *>(words + E), *sh = chosen + P;
     constexpr int NTHR = WAVE * REST_WAVES;
-    for (int e = threadIdx.x; e < E; e += NTHR)
-        masks[e] = 0u;
+    // whether any token chose an expert, then its place in the list; the experts of the pairs; then the waves' keys, and
+    // after them the list's pairs, two to a word
+    int *ranks = reinterpret_cast<int *>(words), *chosen = ranks + DECODE_MAX_E, *sh = chosen + ROWS * 32;
+    uint32_t *table = words + DECODE_MAX_E + ROWS * 32 + 16, *mine = table + wv * DECODE_MAX_E;
+    const bool little = P <= WAVE;   // one wave makes the list
+    if (!little)
+        for (int i = threadIdx.x; i < E; i += NTHR)
+            ranks[i] = 0;
     __syncthreads();
     const auto weights = flat_rsrc(a.weights, (int64_t)P * 4);
+#pragma unroll 1
     for (int t = wv; t < T; t += REST_WAVES) {
-        uint32_t key[SLOTS];
-#pragma unroll
-        for (int j = 0; j < SLOTS; j++) {
-            const int e = lane + WAVE * j;
-            // no key is 0, which stands for no expert (only a NaN with every bit set has it): ids are always in range
-            key[j] = e < E ? max(order_key(a.logits[(int64_t)t * E + e]), 1u) : 0u;
-        }
         int id;
         float w;
-        select_best<SLOTS>(K, key, scratch[wv], &id, &w);
+        select_short(a.logits + (int64_t)t * E, E, K, mine, scratch[wv], &id, &w);
         if (lane < K) {
             const int p = t * K + lane;
             chosen[p] = id;
-            atomicOr(&masks[id], 1u << t);
+            if (!little)
+                ranks[id] = 1;
             store4_sc1(weights, p * 4, __float_as_uint(w));
             if (a.ids_out)
                 a.ids_out[p] = id;
@@ -300,31 +427,51 @@ __device__ inline void top_item(const DecodeArgs &a, uint32_t *words)
         }
     }
     __syncthreads();
-    // the experts that any token chose, and for each the pairs of its tokens, two to a word
-    const int per = (E + NTHR - 1) / NTHR, e0 = (int)threadIdx.x * per, e1 = min(E, e0 + per);
-    int n = 0, count;
-    for (int e = e0; e < e1; e++)
-        n += masks[e] != 0u;
-    int rank = block_excl_scan(n, sh, &count);
+    // the distinct experts in ascending order, and for each the pairs of its tokens
     const auto list = flat_rsrc(a.list, (int64_t)a.most * 4), pairs = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
-    for (int e = e0; e < e1; e++) {
-        const uint32_t mask = masks[e];
-        if (mask == 0u)
-            continue;
-        store4_sc1(list, rank * 4, (uint32_t)e);
-        for (int r = 0; r < ROWS; r += 2) {
-            uint32_t two = 0u;
-            for (int i = 0; i < 2; i++) {
-                int p = -1;
-                if (mask >> (r + i) & 1u)
-                    for (int j = 0; j < K; j++)
-                        if (chosen[(r + i) * K + j] == e)
-                            p = (r + i) * K + j;
-                two |= (uint32_t)(p & 0xFFFF) << (16 * i);
-            }
-            store4_sc1(pairs, (rank * ROWS + r) * 2, two);
+    for (int i = threadIdx.x; i < a.most * (ROWS / 2); i += NTHR)
+        table[i] = ~0u;
+    int count;
+    if (little) {
+        __syncthreads();
+        if (wv != 0) {
+            stores_done();
+            return;
         }
-        rank++;
+        const int e = lane < P ? chosen[lane] : -1;   // lane p: pair p
+        bool first = lane < P;
+        int rank = 0;
+#pragma unroll 2
+        for (int p = 0; p < P; p++)
+            first = first && !(p < lane && __builtin_amdgcn_readlane(e, p) == e);
+        const uint64_t firsts = __ballot(first);
+#pragma unroll 2
+        for (int p = 0; p < P; p++)
+            rank += (firsts >> p & 1) && __builtin_amdgcn_readlane(e, p) < e;
+        count = (int)__popcll(firsts);
+        if (first)
+            store4_sc1(list, rank * 4, (uint32_t)e);
+        if (lane < P)
+            reinterpret_cast<int16_t *>(table)[rank * ROWS + lane / K] = (int16_t)lane;
+        for (int i = lane; i < count * (ROWS / 2); i += WAVE)
+            store4_sc1(pairs, i * 4, table[i]);
+    } else {
+        const int per = (E + NTHR - 1) / NTHR, e0 = (int)threadIdx.x * per, e1 = min(E, e0 + per);
+        int n = 0;
+        for (int e = e0; e < e1; e++)
+            n += ranks[e];
+        int rank = block_excl_scan(n, sh, &count);
+        for (int e = e0; e < e1; e++)
+            if (ranks[e]) {
+                store4_sc1(list, rank * 4, (uint32_t)e);
+                ranks[e] = rank++;
+            }
+        __syncthreads();
+        for (int p = threadIdx.x; p < P; p += NTHR)
+            reinterpret_cast<int16_t *>(table)[ranks[chosen[p]] * ROWS + p / K] = (int16_t)p;
+        __syncthreads();
+        for (int i = threadIdx.x; i < count * (ROWS / 2); i += NTHR)
+            store4_sc1(pairs, i * 4, table[i]);
     }
     stores_done();
     if (wv == 0)
@@ -340,212 +487,292 @@ __device__ inline f32x4_t mx_step(u32x4_t codes, uint32_t scales, const u32x4_t 
     return acc;
 }
 
-// NP pairs of 16 gate and 16 up channels of one expert; the waves share the K axis. Up to 8 tokens: one operand, whose
-// rows 8 .. 15 are the remainders of rows 0 .. 7; more: two operands (PARTS).
-template <int NP, int PARTS>
-__device__ inline void gate_item(const DecodeArgs &a, int item, float *red, uint32_t *sh)
+// A pair of 16 gate and 16 up channels of one expert; the waves share the K axis. Up to 8 tokens: one operand, whose rows
+// 8 .. 15 are the remainders of rows 0 .. 7; more: two operands (PARTS). STAGED: z's part of this wave fits its LDS.
+template <int PARTS, bool STAGED, bool HELP>
+__device__ inline bool gate_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
 {
     __shared__ uint32_t tokens[ROWS / 2];   // the expert's pairs, two to a word
-    const int lane = lane_id(), wv = wave_id();
-    const int groups = (a.I / 16 + NP - 1) / NP, r = item / groups, cp = item % groups * NP, np = min(NP, a.I / 16 - cp);
-    const int experts = wait_for(a, DECODE_READY, sh);
-    if (r >= experts)
-        return;
-    const int e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
-    if (threadIdx.x < ROWS / 2)
-        tokens[threadIdx.x] = load4_sc1(flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2), (r * ROWS + 2 * (int)threadIdx.x) * 2);
-    const int steps = a.Lt / MX_STEP, s0 = steps * wv / REST_WAVES, s1 = steps * (wv + 1) / REST_WAVES;
-    const uint8_t *w = a.gateup + e * a.gateup_stride + (int64_t)2 * cp * steps * MX_BLOCK_BYTES;
-    constexpr int BATCH = PARTS == 1 ? 7 : 4, NB = 2 * NP;   // steps in flight
-    const int row = PARTS == 1 ? lane & 7 : lane & 15;
-    const bool rest = PARTS == 1 && (lane & 8);
-    const uint16_t *x0 = (rest ? a.z_rest : a.z) + (int64_t)row * a.Lt + 8 * (lane >> 4);
-    const uint16_t *x1 = a.z_rest + (int64_t)row * a.Lt + 8 * (lane >> 4);
-    const bool live0 = row < a.T && (!rest || a.has_latent), live1 = row < a.T && a.has_latent;
-    f32x4_t acc[PARTS][NB] = {};
-    for (int s = s0; s < s1; s += BATCH) {
-        u32x4_t codes[BATCH][NB];
-        uint32_t scales[BATCH][NB];
+    const int lane = lane_id(), wv = wave_id(), t = threadIdx.x;
+    const int pairs16 = a.I / 16, r = item / pairs16, cp = item % pairs16;
+    const int steps = a.Lt / MX_STEP, s0 = steps * wv / REST_WAVES, n = steps * (wv + 1) / REST_WAVES - s0;
+    constexpr int BATCH = PARTS == 1 ? 7 : 4;   // steps in flight
+    // rows past the tokens repeat the last one: their sums are not used
+    const int row = min(PARTS == 1 ? lane & 7 : lane & 15, a.T - 1), c = lane >> 4;
+    const bool rest = PARTS == 1 && (lane & 8) && a.has_latent;
+    uint32_t *stage = lds + wv * STAGE_WORDS;
+    float *red = reinterpret_cast<float *>(lds + REST_WAVES * STAGE_WORDS);
+    const int pitch = n * MX_STEP / 2 + 4;   // words of a staged row
+    if constexpr (STAGED) {
+        const int rows = a.has_latent ? 2 * a.T : a.T, chunks = n * 16;   // of 8 values
+#pragma unroll 1
+        for (int i = lane; i < rows * chunks; i += WAVE) {
+            const int k = i / chunks, j = i % chunks;
+            const uint16_t *z = (k < a.T ? a.z + (int64_t)k * a.Lt : a.z_rest + (int64_t)(k - a.T) * a.Lt) + s0 * MX_STEP;
+            *reinterpret_cast<u32x4_t *>(stage + k * pitch + j * 4) = load16(z + j * 8);
+        }
+    }
+    const uint32_t *staged = stage + (row + (rest ? a.T : 0)) * pitch + c * 4;
+    const int z_bytes = a.T * a.Lt * 2, at0 = row * a.Lt * 2 + c * 16;
+    const auto h = flat_rsrc(a.h, (int64_t)a.T * a.K * a.I * 2);
+    int experts = 0;
+#pragma unroll 1
+    for (int go = !HELP && a.T <= HALF && blockIdx.x < 1024 ? 0 : 1; go < 2; go++) {
+        int e = 0;
+        if (go) {
+            experts = wait_for<HELP>(a, DECODE_READY, sh);
+            if (r >= experts)
+                return experts >= 0;
+            e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
+            if (t < ROWS / 2)
+                tokens[t] = load4_sc1(flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2), (r * ROWS + 2 * t) * 2);
+        }
+        const auto w = window(a.gateup + e * a.gateup_stride + (int64_t)2 * cp * steps * MX_BLOCK_BYTES,
+                              2 * (int64_t)steps * MX_BLOCK_BYTES, go);
+        const auto z0 = window(a.z, z_bytes, go), z1 = window(a.has_latent ? a.z_rest : a.z, z_bytes, go);
+        f32x4_t acc[PARTS][2] = {};
+#pragma unroll 1
+        for (int s = 0; s < n; s += BATCH) {
+            u32x4_t codes[BATCH][2];
+            uint32_t scales[BATCH][2];
 #pragma unroll
-        for (int i = 0; i < BATCH; i++)
-            if (s + i < s1)
+            for (int i = 0; i < BATCH; i++)
 #pragma unroll
-                for (int j = 0; j < NB; j++)
-                    if (j < 2 * np) {
-                        const uint8_t *blk = w + ((int64_t)j * steps + s + i) * MX_BLOCK_BYTES;
-                        codes[i][j] = load16_nt(blk + lane * 16);
-                        scales[i][j] = load4_nt(blk + MX_CODE_BYTES + 4 * (lane & 15));
-                    }
-        asm volatile("" ::: "memory");
+                for (int j = 0; j < 2; j++) {
+                    const int off = s + i < n ? (j * steps + s0 + s + i) * MX_BLOCK_BYTES : OUTSIDE;
+                    codes[i][j] = fetch16<CPOL_NT>(w, off + lane * 16);
+                    scales[i][j] = fetch4<CPOL_NT>(w, off + MX_CODE_BYTES + 4 * (lane & 15));
+                }
+            asm volatile("" ::: "memory");
 #pragma unroll
-        for (int i = 0; i < BATCH; i++)
-            if (s + i < s1) {
+            for (int i = 0; i < BATCH; i++) {   // steps past the end: zeros times finite numbers, or zeros
                 u32x4_t x[PARTS][4];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    x[0][j] = live0 ? load16(x0 + (s + i) * MX_STEP + 32 * j) : ZERO;
-                    if constexpr (PARTS == 2)
-                        x[1][j] = live1 ? load16(x1 + (s + i) * MX_STEP + 32 * j) : ZERO;
+                    if constexpr (STAGED) {
+                        x[0][j] = *reinterpret_cast<const u32x4_t *>(staged + min(s + i, n - 1) * (MX_STEP / 2) + j * 16);
+                    } else {
+                        const int off = s + i < n ? at0 + ((s0 + s + i) * MX_STEP + 32 * j) * 2 : OUTSIDE;
+                        if constexpr (PARTS == 1) {
+                            x[0][j] = load16((rest ? a.z_rest : a.z) + (at0 / 2 + (s0 + min(s + i, n - 1)) * MX_STEP + 32 * j));
+                        } else {
+                            x[0][j] = fetch16<0>(z0, off);
+                            x[1][j] = fetch16<0>(z1, off);
+                        }
+                    }
                 }
 #pragma unroll
-                for (int j = 0; j < NB; j++)
-                    if (j < 2 * np)
+                for (int j = 0; j < 2; j++)
 #pragma unroll
-                        for (int p = 0; p < PARTS; p++)
-                            acc[p][j] = mx_step(codes[i][j], scales[i][j], x[p], acc[p][j]);
+                    for (int p = 0; p < PARTS; p++) {
+                        const f32x4_t v = mx_step(codes[i][j], scales[i][j], x[p], acc[p][j]);
+                        acc[p][j] = s + i < n ? v : acc[p][j];
+                    }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            f32x4_t v = acc[0][j];
+            if constexpr (PARTS == 2)
+                if (a.has_latent)
+                    v += acc[1][j];
+            store_sums(red + (wv * 2 + j) * 256, v);
+        }
+        __syncthreads();
+        // two channels of a token per thread
+        const int token = t / 8, ch = t % 8 * 2;
+        auto sum = [&](int j, int at) {
+            float v = 0.f;
+#pragma unroll
+            for (int k = 0; k < REST_WAVES; k++) {
+                const float *p = red + (k * 2 + j) * 256 + at;
+                v += PARTS == 1 && a.has_latent ? p[0] + p[HALF * 16] : p[0];
+            }
+            return v;
+        };
+        if (token < a.T) {
+            const int pair = (int16_t)(tokens[token / 2] >> (16 * (token % 2))), at = token * 16 + ch;
+            const float v0 = silu_f32(sum(0, at)) * sum(1, at), v1 = silu_f32(sum(0, at + 1)) * sum(1, at + 1);
+            const int off = go && pair >= 0 ? (pair * a.I + cp * 16 + ch) * 2 : OUTSIDE;
+            store4_sc1(h, off, pack_bf16x2(v0, v1));
+        }
+    }
+    if (arrive(a, DECODE_GATE, item, experts * pairs16))
+        set_flag(a, DECODE_GATE_DONE, 0u);
+    return true;
+}
+
+constexpr int PARTS_MAX = DECODE_PARTS;
+// What a workgroup of the down product knows of the routing (in LDS), and its share of the work.
+struct DownPart {
+    const int16_t *pairs;      // [experts][16]: the pair of (expert, token), or -1
+    const float *weights;      // of the pairs
+    const uint32_t *own;       // this wave's own experts: rank, and number above
+    int count, col, parts;
+    float *red;
+};
+
+// The experts of this wave, in units of up to STEPS blocks of one expert: weights RING units ahead, the first before h is
+// known, with everything that is looked up of the unit. IN_LDS: all of h fits there; else an operand is loaded when it is needed.
+// False when patience runs out.
+template <bool IN_LDS, bool HELP>
+__device__ inline bool down_part(const DecodeArgs &a, const DownPart &q, uint32_t *staged, uint32_t *sh)
+{
+    constexpr int STEPS = 3, RING = IN_LDS ? 4 : 2, NTHR = WAVE * REST_WAVES;
+    const int lane = lane_id(), wv = wave_id();
+    const int steps = a.I / MX_STEP, groups = (steps + STEPS - 1) / STEPS, units = q.count * groups, P = a.T * a.K;
+    const int h_pitch = IN_LDS ? a.I / 2 + 4 : a.I / 2;   // words of a row
+    struct Unit {
+        u32x4_t codes[STEPS];
+        uint32_t scales[STEPS];
+        int row;         // words to the operand's row: any where the token did not choose the expert
+        f32x4_t share;   // the weights of the sums' tokens, -1 where they did not choose it
+        int part;        // the expert's, for parts = 1
+    } ring[RING];
+    f32x4_t sums[PARTS_MAX];
+#pragma unroll 1
+    for (int go = !HELP && a.T <= 2 ? 0 : 1; go < 2; go++) {
+        const auto h = window(a.h, (int64_t)P * a.I * 2, go);
+        int at = 0, at_group = 0;   // the next unit: own expert and group
+        auto load = [&](Unit &u) {
+            const bool in = at < q.count;
+            const uint32_t own = q.own[in ? at : 0];
+            const int r = in ? own & 0xFFFF : 0, e = __builtin_amdgcn_readfirstlane((int)(own >> 16));
+            const auto w = window(a.down + (in ? e : 0) * a.down_stride + ((int64_t)q.col * steps + at_group * STEPS) * MX_BLOCK_BYTES,
+                                  (int64_t)min(steps - at_group * STEPS, STEPS) * MX_BLOCK_BYTES, go && in);
+#pragma unroll
+            for (int s = 0; s < STEPS; s++) {
+                u.codes[s] = fetch16<CPOL_NT>(w, s * MX_BLOCK_BYTES + lane * 16);
+                u.scales[s] = fetch4<CPOL_NT>(w, s * MX_BLOCK_BYTES + MX_CODE_BYTES + 4 * (lane & 15));
+            }
+            u.row = max((int)q.pairs[r * ROWS + (lane & 15)], 0) * h_pitch + at_group * STEPS * (MX_STEP / 2) + 4 * (lane >> 4);
+            u.part = q.parts == 1 ? e / REST_WAVES % PARTS_MAX : 0;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int p = q.pairs[r * ROWS + 4 * (lane >> 4) + j];
+                u.share[j] = p >= 0 ? q.weights[max(p, 0)] : -1.f;
+            }
+            const bool end = at_group + 1 == groups;
+            at += end;
+            at_group = end ? 0 : at_group + 1;
+        };
+#pragma unroll
+        for (int d = 0; d < RING; d++)
+            load(ring[d]);
+        asm volatile("" ::: "memory");
+        if (go && wait_for<HELP>(a, DECODE_GATE_DONE, sh) < 0)
+            return false;
+        if constexpr (IN_LDS) {
+            const int chunks = a.I / 8;
+#pragma unroll 1
+            for (int i0 = threadIdx.x; i0 < P * chunks; i0 += 4 * NTHR) {
+                u32x4_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    v[k] = fetch16<CPOL_SC1>(h, min(i0 + k * NTHR, P * chunks - 1) * 16);
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const int i = min(i0 + k * NTHR, P * chunks - 1);
+                    *reinterpret_cast<u32x4_t *>(staged + i / chunks * h_pitch + i % chunks * 4) = v[k];
+                }
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int k = 0; k < PARTS_MAX; k++)
+            sums[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        f32x4_t y = {};
+        int group = 0;
+#pragma unroll 1
+        for (int u0 = 0; u0 < units; u0 += RING)
+#pragma unroll
+            for (int d = 0; d < RING; d++) {
+                Unit &u = ring[d];
+                u32x4_t x[IN_LDS ? 1 : STEPS][4];
+                auto operand = [&](int s, u32x4_t (&x)[4]) {   // past the row's end, where the weights are zeros: anything
+                    const int word = u.row + (group * STEPS + s < steps ? s * (MX_STEP / 2) : 0);
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        if constexpr (IN_LDS)
+                            x[j] = *reinterpret_cast<const u32x4_t *>(staged + word + j * 16);
+                        else
+                            x[j] = fetch16<CPOL_SC1>(h, (word + j * 16) * 4);
+                };
+                if constexpr (!IN_LDS)
+#pragma unroll
+                    for (int s = 0; s < STEPS; s++)
+                        operand(s, x[s]);
+#pragma unroll
+                for (int s = 0; s < STEPS; s++) {
+                    if constexpr (IN_LDS)
+                        operand(s, x[0]);
+                    const f32x4_t v = mx_step(u.codes[s], u.scales[s], x[IN_LDS ? 0 : s], y);
+                    y = group * STEPS + s < steps ? v : y;
+                    __builtin_amdgcn_sched_barrier(0);   // no more operands at a time than there are registers for
+                }
+                const bool end = group + 1 == groups;
+                if (end) {   // the expert's values times the weights of its tokens
+#pragma unroll
+                    for (int k = 0; k < PARTS_MAX; k++)
+                        if (k == u.part && u0 + d < units)
+#pragma unroll
+                            for (int j = 0; j < 4; j++)   // values that are not finite reach the expert's own tokens only
+                                sums[k][j] = u.share[j] < 0.f ? sums[k][j] : fmaf(u.share[j], y[j], sums[k][j]);
+                    y = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                }
+                group = end ? 0 : group + 1;
+                load(u);
             }
     }
 #pragma unroll
-    for (int j = 0; j < NB; j++) {
-        f32x4_t v = acc[0][j];
-        if constexpr (PARTS == 2)
-            v += acc[1][j];
-        store_sums(red + (wv * NB + j) * 256, v);
-    }
-    __syncthreads();
-    // two channels of a row per thread
-    auto sum = [&](int b, int at) {
-        if constexpr (PARTS == 2)
-            return total<REST_WAVES>(red + b * 256, NB * 256, at);
-        float v = 0.f;
-#pragma unroll
-        for (int k = 0; k < REST_WAVES; k++)
-            v += red[(k * NB + b) * 256 + at] + red[(k * NB + b) * 256 + HALF * 16 + at];
-        return v;
-    };
-    const auto h = flat_rsrc(a.h, (int64_t)a.T * a.K * a.I * 2);
-    for (int i = threadIdx.x; i < np * a.T * 8; i += WAVE * REST_WAVES) {
-        const int c = i % 8 * 2, token = i / 8 % a.T, b = i / 8 / a.T, pair = (int16_t)(tokens[token / 2] >> (16 * (token % 2)));
-        if (pair < 0)
-            continue;
-        float v[2];
-#pragma unroll
-        for (int k = 0; k < 2; k++)
-            v[k] = silu_f32(sum(2 * b, token * 16 + c + k)) * sum(2 * b + 1, token * 16 + c + k);
-        store4_sc1(h, (pair * a.I + (cp + b) * 16 + c) * 2, pack_bf16x2(v[0], v[1]));
-    }
-    if (arrive(counter(a, DECODE_GATE), (uint32_t)(experts * groups)))
-        set_flag(a, DECODE_GATE_DONE, 0u);
+    for (int k = 0; k < PARTS_MAX; k++)
+        if (k < PARTS_MAX / q.parts)
+            store_sums(q.red + (k * REST_WAVES + wv) * 256, sums[k]);
+    return true;
 }
 
 // 16 latent columns of every chosen expert (parts = 1) or of part `part` of 4. Experts fall into 16 classes by their number
 // e: part e / 4 % 4, wave e % 4. A class is added in ascending order, the classes of a part in wave order, the parts in
 // order: so a token's sum is added in an order that its own experts alone decide, and its outputs are the same bits
 // whatever tokens come with it. With four parts the last workgroup to arrive at the columns adds them.
-constexpr int PARTS_MAX = DECODE_PARTS;
-__device__ inline void down_item(const DecodeArgs &a, int item, int parts, uint32_t *lds, uint32_t *sh)
+template <bool HELP>
+__device__ inline bool down_item(const DecodeArgs &a, int item, int parts, uint32_t *lds, uint32_t *sh)
 {
-    constexpr int NTHR = WAVE * REST_WAVES, MOST = ROWS * 32;   // distinct experts
-    // the waves' sums; then the routing: the pairs of (expert, token), or -1, their weights, the experts, and the ranks of
-    // each wave's own experts
+    constexpr int NTHR = WAVE * REST_WAVES;
+    // the waves' sums; then the routing: the pairs of (expert, token), or -1, their weights, each wave's own experts; then h
     float *red = reinterpret_cast<float *>(lds);
     int16_t *pairs = reinterpret_cast<int16_t *>(lds + (parts == 1 ? PARTS_MAX : 1) * REST_WAVES * 256);
     float *weights = reinterpret_cast<float *>(pairs + a.most * ROWS);
-    uint16_t *list = reinterpret_cast<uint16_t *>(weights + MOST), *own = list + MOST + wave_id() * MOST;
+    uint32_t *own = reinterpret_cast<uint32_t *>(weights + a.T * a.K) + wave_id() * a.most;
     const int lane = lane_id(), wv = wave_id(), part = parts == 1 ? 0 : item % parts, col = parts == 1 ? item : item / parts;
-    const int experts = wait_for(a, DECODE_READY, sh);
-    {
-        const auto gl = flat_rsrc(a.list, (int64_t)a.most * 4), gp = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
-        const auto gw = flat_rsrc(a.weights, (int64_t)a.T * a.K * 4);
-        for (int i = threadIdx.x; i < experts; i += NTHR)
-            list[i] = (uint16_t)load4_sc1(gl, i * 4);
-        for (int i = threadIdx.x; i < experts * (ROWS / 2); i += NTHR)
-            reinterpret_cast<uint32_t *>(pairs)[i] = load4_sc1(gp, i * 4);
-        for (int i = threadIdx.x; i < a.T * a.K; i += NTHR)
-            weights[i] = __uint_as_float(load4_sc1(gw, i * 4));
+    const int experts = wait_for<HELP>(a, DECODE_READY, sh);
+    if (experts < 0)
+        return false;
+    const auto gl = flat_rsrc(a.list, (int64_t)a.most * 4), gp = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
+    const auto gw = flat_rsrc(a.weights, (int64_t)a.T * a.K * 4);
+    int count = 0;
+#pragma unroll 1
+    for (int r0 = 0; r0 < experts; r0 += WAVE) {
+        const int r = r0 + lane, e = (int)fetch4<CPOL_SC1>(gl, r < experts ? r * 4 : OUTSIDE);
+        const bool mine = r < experts && e % REST_WAVES == wv && (parts == 1 || e / REST_WAVES % PARTS_MAX == part);
+        const uint64_t all = __ballot(mine);
+        if (mine)
+            own[count + __popcll(all & ((1ull << lane) - 1))] = (uint32_t)(r | e << 16);
+        count += (int)__popcll(all);
     }
+#pragma unroll 1
+    for (int i = threadIdx.x; i < experts * (ROWS / 2); i += NTHR)
+        reinterpret_cast<uint32_t *>(pairs)[i] = load4_sc1(gp, i * 4);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < a.T * a.K; i += NTHR)
+        weights[i] = __uint_as_float(load4_sc1(gw, i * 4));
     __syncthreads();
-    int count = 0, ends[PARTS_MAX];   // of the experts of part 0, 0 .. 1, ...
-#pragma unroll
-    for (int k = 0; k < PARTS_MAX; k++) {
-        if (parts == 1 || k == part)
-            for (int r0 = 0; r0 < experts; r0 += WAVE) {
-                const int r = r0 + lane, e = r < experts ? list[r] : -1;
-                const bool mine = e >= 0 && e % REST_WAVES == wv && e / REST_WAVES % PARTS_MAX == k;
-                const uint64_t all = __ballot(mine);
-                if (mine)
-                    own[count + __popcll(all & ((1ull << lane) - 1))] = (uint16_t)r;
-                count += (int)__popcll(all);
-            }
-        ends[k] = count;
-    }
-    __syncthreads();
-    // The blocks of this wave, expert by expert: DEPTH blocks ahead, the first weights before h is known. `at` and `of`
-    // walk over (expert, step) for the weights and for the activations.
-    constexpr int DEPTH = 3;
-    const int steps = a.I / MX_STEP;
-    const auto h = flat_rsrc(a.h, (int64_t)a.T * a.K * a.I * 2);
-    struct Walk {
-        int i, s;   // own expert, step
-    };
-    Walk at{0, 0}, of{0, 0};
-    const uint8_t *blk = nullptr;
-    int pair = -1;
-    u32x4_t codes[DEPTH], x[DEPTH][4];
-    uint32_t scales[DEPTH];
-    auto load = [&](int slot) {
-        if (at.i >= count)
-            return;
-        if (at.s == 0)
-            blk = a.down + __builtin_amdgcn_readfirstlane((int)list[own[at.i]]) * a.down_stride + (int64_t)col * steps * MX_BLOCK_BYTES;
-        codes[slot] = load16_nt(blk + lane * 16);
-        scales[slot] = load4_nt(blk + MX_CODE_BYTES + 4 * (lane & 15));
-        blk += MX_BLOCK_BYTES;
-        if (++at.s == steps)
-            at = Walk{at.i + 1, 0};
-    };
-    auto operand = [&](int slot) {
-        if (of.i >= count)
-            return;
-        if (of.s == 0)
-            pair = pairs[own[of.i] * ROWS + (lane & 15)];
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-            x[slot][j] = pair >= 0 ? __builtin_bit_cast(u32x4_t, load16_sc1(h, (pair * a.I + of.s * MX_STEP + 32 * j + 8 * (lane >> 4)) * 2))
-                                   : ZERO;
-        if (++of.s == steps)
-            of = Walk{of.i + 1, 0};
-    };
-#pragma unroll
-    for (int d = 0; d < DEPTH; d++)
-        load(d);
-    asm volatile("" ::: "memory");
-    wait_for(a, DECODE_GATE_DONE, sh);
-#pragma unroll
-    for (int d = 0; d < DEPTH; d++)
-        operand(d);
-    f32x4_t sum = {}, y = {};
-    int k = 0;   // the class being added
-    auto end_classes = [&](int i) {   // those that own expert i is past
-        while (k < PARTS_MAX && i >= ends[k]) {
-            if (parts == 1 || k == part)
-                store_sums(red + ((parts == 1 ? k : 0) * REST_WAVES + wv) * 256, sum);
-            sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            k++;
-        }
-    };
-    Walk now{0, 0};
-    end_classes(0);
-    while (now.i < count)
-#pragma unroll
-        for (int d = 0; d < DEPTH; d++) {
-            if (now.i >= count)
-                break;
-            y = mx_step(codes[d], scales[d], x[d], y);
-            load(d);
-            operand(d);
-            if (++now.s == steps) {   // the expert's values times the weights of its tokens
-                const int16_t *of_rows = pairs + own[now.i] * ROWS + 4 * (lane >> 4);
-#pragma unroll
-                for (int j = 0; j < 4; j++) {   // values that are not finite reach the expert's own tokens only
-                    const int p = of_rows[j];
-                    sum[j] = p >= 0 ? fmaf(weights[max(p, 0)], y[j], sum[j]) : sum[j];
-                }
-                y = f32x4_t{0.f, 0.f, 0.f, 0.f};
-                now = Walk{now.i + 1, 0};
-                end_classes(now.i);
-            }
-        }
+    uint32_t *staged = reinterpret_cast<uint32_t *>(weights + a.T * a.K) + REST_WAVES * a.most;
+    staged += (4 - (staged - lds) % 4) % 4;
+    const DownPart q{pairs, weights, own, count, col, parts, red};
+    const bool in_lds = (int)(staged - lds) + a.T * a.K * (a.I / 2 + 4) <= LDS_WORDS;
+    if (!(in_lds ? down_part<true, HELP>(a, q, staged, sh) : down_part<false, HELP>(a, q, staged, sh)))
+        return false;
     __syncthreads();
     const int t = threadIdx.x, row = t / 16, c = t % 16;
     float v = 0.f;
@@ -557,14 +784,17 @@ __device__ inline void down_item(const DecodeArgs &a, int item, int parts, uint3
         const auto partial = flat_rsrc(a.partial + (int64_t)col * PARTS_MAX * 256, PARTS_MAX * 256 * 4);
         if (row < a.T)
             store4_sc1(partial, (part * 256 + t) * 4, __float_as_uint(total<REST_WAVES>(red, 256, t)));
-        const bool last = arrive(a.column_counters + col, PARTS_MAX);
-        if (t == 0)
-            *sh = last;
+        stores_done();
+        if (wv == 0) {
+            const bool last = last_at(a.column_counters + col, PARTS_MAX);
+            if (t == 0)
+                *sh = last;
+        }
         __syncthreads();
         const bool mine = *sh != 0u;
         __syncthreads();
         if (!mine)
-            return;
+            return true;
         if (row < a.T)
 #pragma unroll
             for (int p = 0; p < PARTS_MAX; p++)
@@ -578,67 +808,76 @@ __device__ inline void down_item(const DecodeArgs &a, int item, int parts, uint3
         else
             *reinterpret_cast<uint32_t *>(a.out + (int64_t)row * a.Lt + col * 16 + c) = two;
     }
-    if (a.has_latent && arrive(counter(a, DECODE_DOWN), (uint32_t)(a.Lt / 16)))
+    if (a.has_latent && arrive(a, DECODE_DOWN, col, a.Lt / 16))
         set_flag(a, DECODE_DOWN_DONE, 0u);
+    return true;
 }
 
-__device__ inline void out_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
+template <bool HELP>
+__device__ inline bool out_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
 {
-    const int wv = wave_id();
-    Bf16Part<1, 12, 4> part;
-    part.start(a.w_out, a.H, a.ldcat, item, wv, REST_WAVES);
-    wait_for(a, DECODE_DOWN_DONE, sh);
-    const auto acat = flat_rsrc(a.acat, (int64_t)a.T * a.ldcat * 2);
-    f32x4_t acc[1] = {};
-    part.finish(a.T, lds + wv * STAGE_WORDS, acc,
-                [&](int r, int k) { return __builtin_bit_cast(u32x4_t, load16_sc1(acat, (r * a.ldcat + k) * 2)); });
-    __syncthreads();
-    float *red = reinterpret_cast<float *>(lds);
-    store_sums(red + wv * 256, acc[0]);
-    __syncthreads();
-    const int t = threadIdx.x, row = t / 8, c = t % 8 * 2;
-    if (row < a.T && row < ROWS)
-        *reinterpret_cast<uint32_t *>(a.out + (int64_t)row * a.H + item * 16 + c) =
-            pack_bf16x2(total<REST_WAVES>(red, 256, row * 16 + c), total<REST_WAVES>(red, 256, row * 16 + c + 1));
+    const int wv = wave_id(), t = threadIdx.x, row = t / 8, c = t % 8 * 2;
+    float *red = reinterpret_cast<float *>(lds + REST_WAVES * STAGE_WORDS);
+    const auto out = flat_rsrc(a.out, (int64_t)a.T * a.H * 2);
+#pragma unroll 1
+    for (int go = !HELP && a.T <= 2 ? 0 : 1; go < 2; go++) {
+        Bf16Part<1, 12, 4> part;
+        part.start(a.w_out, a.H, a.ldcat, item, wv, REST_WAVES, go);
+        if (go && wait_for<HELP>(a, DECODE_DOWN_DONE, sh) < 0)
+            return false;
+        const auto acat = window(a.acat, (int64_t)a.T * a.ldcat * 2, go);
+        f32x4_t acc[1] = {};
+        part.finish(a.T, lds + wv * STAGE_WORDS, acc, [&](int r, int k) { return fetch16<CPOL_SC1>(acat, (r * a.ldcat + k) * 2); });
+        store_sums(red + wv * 256, acc[0]);
+        __syncthreads();
+        if (row < a.T && row < ROWS)
+            __builtin_amdgcn_raw_buffer_store_b32((int)pack_bf16x2(total<REST_WAVES>(red, 256, row * 16 + c),
+                                                                   total<REST_WAVES>(red, 256, row * 16 + c + 1)),
+                                                  out, go ? (row * a.H + item * 16 + c) * 2 : OUTSIDE, 0, 0);
+        __syncthreads();
+    }
+    return true;
 }
 
-template <int SLOTS, bool FEW>
-__global__ __launch_bounds__(WAVE *REST_WAVES, 4) void rest_kernel(const DecodeArgs a)
+// Item i, as numbered by decode_items. False when patience ran out before anything was handed on (HELP: never).
+template <bool FEW, bool HELP>
+__device__ inline bool do_item(const DecodeArgs &a, const DecodeItems &n, int i, uint32_t *lds, uint32_t *sh)
 {
-    // the items' activations, sums over the waves, and the routing as they need it
-    constexpr int TOP = SLOTS * WAVE + ROWS * 32 + 16, ITEM = REST_WAVES * STAGE_WORDS;
-    constexpr int DOWN = REST_WAVES * 256 + ROWS * 32 * (ROWS / 2 + 1) + (1 + REST_WAVES) * ROWS * 16;
-    static_assert(TOP <= ITEM && DOWN <= ITEM && REST_WAVES * 1024 <= ITEM, "room");
-    static_assert(PARTS_MAX * REST_WAVES * 256 + 32 * (ROWS / 2) + ROWS * 32 + (1 + REST_WAVES) * ROWS * 16 <= ITEM, "room");
-    __shared__ uint32_t lds[ITEM];
+    if (i < n.top) {
+        top_item(a, lds);
+        return true;
+    }
+    i -= n.top;
+    if (i < n.gate) {
+        if constexpr (FEW)
+            if (a.T * (a.has_latent ? 2 : 1) * ((a.Lt / MX_STEP + REST_WAVES - 1) / REST_WAVES * MX_STEP / 2 + 4) <= STAGE_WORDS)
+                return gate_item<1, true, HELP>(a, i, lds, sh);
+        return gate_item<FEW ? 1 : 2, false, HELP>(a, i, lds, sh);
+    }
+    i -= n.gate;
+    if (i < n.down)
+        return down_item<HELP>(a, i, n.parts, lds, sh);
+    return out_item<HELP>(a, i - n.down, lds, sh);
+}
+
+template <bool FEW>
+__global__ __launch_bounds__(WAVE *REST_WAVES, 3) void rest_kernel(const DecodeArgs a)
+{
+    constexpr int TOP = DECODE_MAX_E + ROWS * 32 + 16, MOST = ROWS * 32;   // MOST: pairs, and distinct experts
+    static_assert(TOP + REST_WAVES * DECODE_MAX_E <= LDS_WORDS && TOP + MOST * (ROWS / 2) <= LDS_WORDS, "room for the list");
+    static_assert(REST_WAVES * 256 + MOST * (ROWS / 2 + 1 + REST_WAVES) <= LDS_WORDS, "room for the routing");
+    static_assert(PARTS_MAX * REST_WAVES * 256 + 32 * (ROWS / 2 + 1 + REST_WAVES) <= LDS_WORDS, "... and one token's sums");
+    __shared__ alignas(16) uint32_t lds[LDS_WORDS];
     __shared__ uint32_t sh;
-    float *red = reinterpret_cast<float *>(lds);
-    if (threadIdx.x == 0)
-        sh = __hip_atomic_fetch_add(counter(a, DECODE_TICKET), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    int item = __builtin_amdgcn_readfirstlane((int)sh);
-    __syncthreads();
     const DecodeItems n = decode_items(a);
-    if (item < n.top)
-        return top_item<SLOTS>(a, lds);
-    item -= n.top;
-    if (item < n.gate)
-        return gate_item<1, FEW ? 1 : 2>(a, item, red, &sh);
-    item -= n.gate;
-    if (item < n.down)
-        return down_item(a, item, n.parts, lds, &sh);
-    out_item(a, item - n.down, lds, &sh);
-}
-
-template <int SLOTS>
-void launch_rest(const DecodeArgs &a, hipStream_t st)
-{
-    const DecodeItems n = decode_items(a);
-    const dim3 grid((unsigned)(n.top + n.gate + n.down + n.out)), threads(WAVE * REST_WAVES);
-    if (a.T <= HALF)
-        hipLaunchKernelGGL((rest_kernel<SLOTS, true>), grid, threads, 0, st, a);
-    else
-        hipLaunchKernelGGL((rest_kernel<SLOTS, false>), grid, threads, 0, st, a);
+    const int item = blockIdx.x;
+    if (!claim(a, item, &sh) || do_item<FEW, false>(a, n, item, lds, &sh))
+        return;
+    const int kind = item < n.top + n.gate ? n.top : item < n.top + n.gate + n.down ? n.top + n.gate : n.top + n.gate + n.down;
+#pragma unroll 1
+    for (int i = 0; i <= kind; i++)   // the earlier kinds' items that are still free, and then this one
+        if (i == kind || claim(a, i, &sh))
+            do_item<FEW, true>(a, n, i == kind ? item : i, lds, &sh);
 }
 
 } // namespace
@@ -650,10 +889,12 @@ hipError_t launch_decode(const DecodeArgs &a, hipStream_t st)
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    if (a.E <= 4 * WAVE)
-        launch_rest<4>(a, st);
+    const DecodeItems n = decode_items(a);
+    const dim3 grid((unsigned)decode_item_count(n)), threads(WAVE * REST_WAVES);
+    if (a.T <= HALF)
+        hipLaunchKernelGGL((rest_kernel<true>), grid, threads, 0, st, a);
     else
-        launch_rest<16>(a, st);
+        hipLaunchKernelGGL((rest_kernel<false>), grid, threads, 0, st, a);
     return hipGetLastError();
 }
 

@@ -8,11 +8,17 @@ namespace mxmoe {
 
 constexpr int DECODE_MAX_T = MOE_DECODE_MAX_T;   // the rows of a matrix-core tile
 
-// Counters and flags (each flag in 64 places), one to a cache line.
-enum { DECODE_TICKET, DECODE_GATE, DECODE_DOWN, DECODE_COUNTERS };
-enum { DECODE_READY, DECODE_GATE_DONE, DECODE_DOWN_DONE, DECODE_FLAGS };
+constexpr int DECODE_MAX_E = 1024;
+constexpr int DECODE_MAX_WINDOW = 0x7FFF0000;    // bytes of a matrix, of h and of [zc | h_s]
+
+// One to a cache line: two sets of arrival counters, each of DECODE_ARMS and one more for their last arrivals; three flags,
+// each in 64 places.
+enum { DECODE_GATE, DECODE_DOWN };
+enum { DECODE_READY, DECODE_GATE_DONE, DECODE_DOWN_DONE };
+constexpr int DECODE_ARMS = 16, DECODE_COUNTERS = 2 * (DECODE_ARMS + 1);
+constexpr int DECODE_PATIENCE = 1000;   // times that a flag is asked for, about a microsecond each
 constexpr int DECODE_COUNTER_WORDS = 32;
-constexpr int DECODE_COUNTER_LINES = DECODE_COUNTERS + DECODE_FLAGS * 64;
+constexpr int DECODE_COUNTER_LINES = DECODE_COUNTERS + 3 * 64;
 constexpr int DECODE_PARTS = 4;   // workgroups that share 16 columns of the down product, for more than one token
 
 struct DecodeArgs {
@@ -28,6 +34,8 @@ struct DecodeArgs {
     // workspace
     uint32_t *counters;              // DECODE_COUNTER_LINES lines
     uint32_t *column_counters;       // [Lt / 16] arrivals of a column block's parts
+    uint32_t *claims;                // [items] of the second kernel
+    int patience;
     float *partial;                  // [Lt / 16][DECODE_PARTS][16][16] their sums
     float *logits;                   // [T, E]
     float *weights;                  // [T, K]
@@ -45,7 +53,7 @@ struct DecodeArgs {
     uint16_t *out;                   // [T, H] ([T, Lt] without latent projections)
 };
 
-// Work items of the second kernel, in the order in which they are taken. One token's experts are few enough for one
+// Work items of the second kernel, numbered kind after kind. One token's experts are few enough for one
 // workgroup to a column block; more are shared by DECODE_PARTS.
 struct DecodeItems {
     int top, gate, down, out, parts;
@@ -55,6 +63,8 @@ __host__ __device__ inline DecodeItems decode_items(const DecodeArgs &a)
     const int parts = a.T == 1 ? 1 : DECODE_PARTS;
     return {1, a.most * (a.I / 16), a.Lt / 16 * parts, a.has_latent ? a.H / 16 : 0, parts};
 }
+
+__host__ __device__ inline int decode_item_count(const DecodeItems &n) { return n.top + n.gate + n.down + n.out; }
 
 hipError_t launch_decode(const DecodeArgs &a, hipStream_t st);
 

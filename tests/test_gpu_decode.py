@@ -280,3 +280,27 @@ def test_in_a_step_with_the_norms_and_a_projection():
         eager = step()
         torch.cuda.synchronize()
         assert torch.equal(held[3].out, eager[3].out) and torch.equal(held[2].sum, eager[2].sum)
+
+
+@pytest.fixture
+def impatient():
+    """Workgroups ask once for what they wait for, and then do each other's work."""
+    from mxfp4_latent_mixture_sigmoid_amd import abi
+    abi.lib().moe_decode_patience(0)
+    yield
+    abi.lib().moe_decode_patience(-1)
+
+
+@pytest.mark.parametrize("s", [shape(T=1, E=70, K=8), shape(T=4, S=2, K=16), shape(T=16, E=200, K=8, Lt=512),
+                               shape(T=2, H=0, latent=False, S=0, Is=0, E=61, K=6)], ids=lambda s: f"{s.T}")
+def test_helping(s, impatient):
+    from mxfp4_latent_mixture_sigmoid_amd import abi
+    inp = make_inputs(s)
+    layer, x = G.make_layer(s, inp, T_max=s.T), tokens(inp)
+    got = [layer.decode(x) for _ in range(3)]
+    torch.cuda.synchronize()
+    abi.lib().moe_decode_patience(-1)
+    want = layer.decode(x)
+    for r in got:
+        for a, b in zip(r, want):
+            assert torch.equal(a, b)
