@@ -39,6 +39,7 @@ namespace {
 
 constexpr int ROWS = DECODE_MAX_T, HALF = ROWS / 2;
 constexpr int FRONT_WAVES = 8, REST_WAVES = 4;
+constexpr int OUT_DEPTH = 24;
 constexpr int FLAGS = WAVE;                 // places of a flag
 constexpr int ARMS = DECODE_ARMS;
 constexpr int STAGE_WORDS = 1856;           // LDS of a wave for its activations, where they fit
@@ -91,9 +92,11 @@ __device__ inline float total(const float *red, int stride, int at)
 // DEPTH steps ahead, the first before anything is known of the activations. Those go through LDS where the wave's part of
 // them fits (few tokens: a step's operand would be a load with 4 T lanes of use), else straight to registers, AHEAD
 // steps ahead.
-template <int NB, int DEPTH, int AHEAD>
+template <int NB, int DEPTH, int AHEAD, bool STAGED>
 struct Bf16Part {
     static_assert(DEPTH % AHEAD == 0, "slots");
+    // Whether K values of T tokens, divided among the waves, fit their parts of LDS.
+    static __device__ bool fits(int T, int K, int waves) { return T * ((K / BF16_STEP + waves - 1) / waves * 16 + 4) <= STAGE_WORDS; }
     u32x4_t b[DEPTH][NB];
     __amdgpu_buffer_rsrc_t w;
     int s0, s1, next, at, jump, last, tail;   // steps; the next step's first block
@@ -132,7 +135,7 @@ struct Bf16Part {
     {
         const int lane = lane_id(), n = s1 - s0, pitch = n * 16 + 4;   // words of a token's part in LDS
         const int r = lane & 15, c = lane >> 4;
-        if (T * pitch <= STAGE_WORDS) {
+        if constexpr (STAGED) {
 #pragma unroll 1
             for (int i0 = 0; i0 < T * n * 4; i0 += 4 * WAVE) {
                 u32x4_t v[4];
@@ -158,6 +161,8 @@ struct Bf16Part {
                     for (int j = 0; j < NB; j++)
                         acc[j] = step(x, b[i][j], acc[j], s + i < n);
                     load(i);
+                    if (i % 4 == 3)
+                        __builtin_amdgcn_sched_barrier(0);   // not all operands at once
                 }
             return;
         }
@@ -191,9 +196,15 @@ __device__ inline void front_product(const DecodeArgs &a, const uint8_t *w, int6
 {
     const int wv = wave_id();
     f32x4_t acc[NB] = {};
-    Bf16Part<NB, NB == 1 ? 8 : 4, 4> part;
-    part.start(w, rows, a.Hin, block, wv, FRONT_WAVES);
-    part.finish(a.T, lds + wv * STAGE_WORDS, acc, [&](int r, int k) { return load16(a.x + (int64_t)r * a.Hin + k); });
+    auto run = [&](auto part) {
+        part.start(w, rows, a.Hin, block, wv, FRONT_WAVES);
+        part.finish(a.T, lds + wv * STAGE_WORDS, acc, [&](int r, int k) { return load16(a.x + (int64_t)r * a.Hin + k); });
+    };
+    using Staged = Bf16Part<NB, NB == 1 ? 16 : 8, 4, true>;
+    if (Staged::fits(a.T, a.Hin, FRONT_WAVES))
+        run(Staged());
+    else
+        run(Bf16Part<NB, NB == 1 ? 8 : 4, 4, false>());
     __syncthreads();
     float *red = reinterpret_cast<float *>(lds);
 #pragma unroll
@@ -403,10 +414,8 @@ __device__ inline void top_item(const DecodeArgs &a, uint32_t *words)
     // after them the list's pairs, two to a word
     int *ranks = reinterpret_cast<int *>(words), *chosen = ranks + DECODE_MAX_E, *sh = chosen + ROWS * 32;
     uint32_t *table = words + DECODE_MAX_E + ROWS * 32 + 16, *mine = table + wv * DECODE_MAX_E;
-    const bool little = P <= WAVE;   // one wave makes the list
-    if (!little)
-        for (int i = threadIdx.x; i < E; i += NTHR)
-            ranks[i] = 0;
+    for (int i = threadIdx.x; i < E; i += NTHR)
+        ranks[i] = 0;
     __syncthreads();
     const auto weights = flat_rsrc(a.weights, (int64_t)P * 4);
 #pragma unroll 1
@@ -417,8 +426,7 @@ __device__ inline void top_item(const DecodeArgs &a, uint32_t *words)
         if (lane < K) {
             const int p = t * K + lane;
             chosen[p] = id;
-            if (!little)
-                ranks[id] = 1;
+            ranks[id] = 1;
             store4_sc1(weights, p * 4, __float_as_uint(w));
             if (a.ids_out)
                 a.ids_out[p] = id;
@@ -431,48 +439,22 @@ __device__ inline void top_item(const DecodeArgs &a, uint32_t *words)
     const auto list = flat_rsrc(a.list, (int64_t)a.most * 4), pairs = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
     for (int i = threadIdx.x; i < a.most * (ROWS / 2); i += NTHR)
         table[i] = ~0u;
-    int count;
-    if (little) {
-        __syncthreads();
-        if (wv != 0) {
-            stores_done();
-            return;
-        }
-        const int e = lane < P ? chosen[lane] : -1;   // lane p: pair p
-        bool first = lane < P;
-        int rank = 0;
-#pragma unroll 2
-        for (int p = 0; p < P; p++)
-            first = first && !(p < lane && __builtin_amdgcn_readlane(e, p) == e);
-        const uint64_t firsts = __ballot(first);
-#pragma unroll 2
-        for (int p = 0; p < P; p++)
-            rank += (firsts >> p & 1) && __builtin_amdgcn_readlane(e, p) < e;
-        count = (int)__popcll(firsts);
-        if (first)
+    const int per = (E + NTHR - 1) / NTHR, e0 = (int)threadIdx.x * per, e1 = min(E, e0 + per);
+    int n = 0, count;
+    for (int e = e0; e < e1; e++)
+        n += ranks[e];
+    int rank = block_excl_scan(n, sh, &count);
+    for (int e = e0; e < e1; e++)
+        if (ranks[e]) {
             store4_sc1(list, rank * 4, (uint32_t)e);
-        if (lane < P)
-            reinterpret_cast<int16_t *>(table)[rank * ROWS + lane / K] = (int16_t)lane;
-        for (int i = lane; i < count * (ROWS / 2); i += WAVE)
-            store4_sc1(pairs, i * 4, table[i]);
-    } else {
-        const int per = (E + NTHR - 1) / NTHR, e0 = (int)threadIdx.x * per, e1 = min(E, e0 + per);
-        int n = 0;
-        for (int e = e0; e < e1; e++)
-            n += ranks[e];
-        int rank = block_excl_scan(n, sh, &count);
-        for (int e = e0; e < e1; e++)
-            if (ranks[e]) {
-                store4_sc1(list, rank * 4, (uint32_t)e);
-                ranks[e] = rank++;
-            }
-        __syncthreads();
-        for (int p = threadIdx.x; p < P; p += NTHR)
-            reinterpret_cast<int16_t *>(table)[ranks[chosen[p]] * ROWS + p / K] = (int16_t)p;
-        __syncthreads();
-        for (int i = threadIdx.x; i < count * (ROWS / 2); i += NTHR)
-            store4_sc1(pairs, i * 4, table[i]);
-    }
+            ranks[e] = rank++;
+        }
+    __syncthreads();
+    for (int p = threadIdx.x; p < P; p += NTHR)
+        reinterpret_cast<int16_t *>(table)[ranks[chosen[p]] * ROWS + p / K] = (int16_t)p;
+    __syncthreads();
+    for (int i = threadIdx.x; i < count * (ROWS / 2); i += NTHR)
+        store4_sc1(pairs, i * 4, table[i]);
     stores_done();
     if (wv == 0)
         set_flag(a, DECODE_READY, (uint32_t)count);
@@ -496,7 +478,7 @@ __device__ inline bool gate_item(const DecodeArgs &a, int item, uint32_t *lds, u
     const int lane = lane_id(), wv = wave_id(), t = threadIdx.x;
     const int pairs16 = a.I / 16, r = item / pairs16, cp = item % pairs16;
     const int steps = a.Lt / MX_STEP, s0 = steps * wv / REST_WAVES, n = steps * (wv + 1) / REST_WAVES - s0;
-    constexpr int BATCH = PARTS == 1 ? 7 : 4;   // steps in flight
+    constexpr int BATCH = PARTS == 1 ? 7 : 4, AHEAD = STAGED ? 1 : PARTS == 1 ? 3 : 2;   // steps in flight
     // rows past the tokens repeat the last one: their sums are not used
     const int row = min(PARTS == 1 ? lane & 7 : lane & 15, a.T - 1), c = lane >> 4;
     const bool rest = PARTS == 1 && (lane & 8) && a.has_latent;
@@ -544,30 +526,37 @@ __device__ inline bool gate_item(const DecodeArgs &a, int item, uint32_t *lds, u
                     scales[i][j] = fetch4<CPOL_NT>(w, off + MX_CODE_BYTES + 4 * (lane & 15));
                 }
             asm volatile("" ::: "memory");
+            // operands AHEAD steps ahead of their use; steps past the end multiply zeros
+            u32x4_t x[AHEAD][PARTS][4];
+            auto operand = [&](int i, u32x4_t (&x)[PARTS][4]) {
+                const int k = min(s + i, n - 1);
 #pragma unroll
-            for (int i = 0; i < BATCH; i++) {   // steps past the end: zeros times finite numbers, or zeros
-                u32x4_t x[PARTS][4];
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
+                for (int j = 0; j < 4; j++)
                     if constexpr (STAGED) {
-                        x[0][j] = *reinterpret_cast<const u32x4_t *>(staged + min(s + i, n - 1) * (MX_STEP / 2) + j * 16);
+                        x[0][j] = *reinterpret_cast<const u32x4_t *>(staged + k * (MX_STEP / 2) + j * 16);
                     } else {
-                        const int off = s + i < n ? at0 + ((s0 + s + i) * MX_STEP + 32 * j) * 2 : OUTSIDE;
-                        if constexpr (PARTS == 1) {
-                            x[0][j] = load16((rest ? a.z_rest : a.z) + (at0 / 2 + (s0 + min(s + i, n - 1)) * MX_STEP + 32 * j));
-                        } else {
-                            x[0][j] = fetch16<0>(z0, off);
+                        const int off = at0 + ((s0 + k) * MX_STEP + 32 * j) * 2;
+                        x[0][j] = PARTS == 1 ? load16(reinterpret_cast<const uint8_t *>(rest ? a.z_rest : a.z) + off)
+                                             : fetch16<0>(z0, off);
+                        if constexpr (PARTS == 2)
                             x[1][j] = fetch16<0>(z1, off);
-                        }
                     }
-                }
+            };
+#pragma unroll
+            for (int i = 0; i < AHEAD; i++)
+                operand(i, x[i]);
+#pragma unroll
+            for (int i = 0; i < BATCH; i++) {
 #pragma unroll
                 for (int j = 0; j < 2; j++)
 #pragma unroll
                     for (int p = 0; p < PARTS; p++) {
-                        const f32x4_t v = mx_step(codes[i][j], scales[i][j], x[p], acc[p][j]);
+                        const f32x4_t v = mx_step(codes[i][j], scales[i][j], x[i % AHEAD][p], acc[p][j]);
                         acc[p][j] = s + i < n ? v : acc[p][j];
                     }
+                if (i + AHEAD < BATCH)
+                    operand(i + AHEAD, x[i % AHEAD]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
 #pragma unroll
@@ -608,17 +597,17 @@ struct DownPart {
     const int16_t *pairs;      // [experts][16]: the pair of (expert, token), or -1
     const float *weights;      // of the pairs
     const uint32_t *own;       // this wave's own experts: rank, and number above
-    int count, col, parts;
+    int count, col;
     float *red;
 };
 
 // The experts of this wave, in units of up to STEPS blocks of one expert: weights RING units ahead, the first before h is
 // known, with everything that is looked up of the unit. IN_LDS: all of h fits there; else an operand is loaded when it is needed.
 // False when patience runs out.
-template <bool IN_LDS, bool HELP>
+template <int SUMS, bool IN_LDS, bool HELP>
 __device__ inline bool down_part(const DecodeArgs &a, const DownPart &q, uint32_t *staged, uint32_t *sh)
 {
-    constexpr int STEPS = 3, RING = IN_LDS ? 4 : 2, NTHR = WAVE * REST_WAVES;
+    constexpr int STEPS = 3, RING = SUMS > 1 ? 3 : 2, NTHR = WAVE * REST_WAVES;
     const int lane = lane_id(), wv = wave_id();
     const int steps = a.I / MX_STEP, groups = (steps + STEPS - 1) / STEPS, units = q.count * groups, P = a.T * a.K;
     const int h_pitch = IN_LDS ? a.I / 2 + 4 : a.I / 2;   // words of a row
@@ -629,7 +618,7 @@ __device__ inline bool down_part(const DecodeArgs &a, const DownPart &q, uint32_
         f32x4_t share;   // the weights of the sums' tokens, -1 where they did not choose it
         int part;        // the expert's, for parts = 1
     } ring[RING];
-    f32x4_t sums[PARTS_MAX];
+    f32x4_t sums[SUMS];
 #pragma unroll 1
     for (int go = !HELP && a.T <= 2 ? 0 : 1; go < 2; go++) {
         const auto h = window(a.h, (int64_t)P * a.I * 2, go);
@@ -646,7 +635,7 @@ __device__ inline bool down_part(const DecodeArgs &a, const DownPart &q, uint32_
                 u.scales[s] = fetch4<CPOL_NT>(w, s * MX_BLOCK_BYTES + MX_CODE_BYTES + 4 * (lane & 15));
             }
             u.row = max((int)q.pairs[r * ROWS + (lane & 15)], 0) * h_pitch + at_group * STEPS * (MX_STEP / 2) + 4 * (lane >> 4);
-            u.part = q.parts == 1 ? e / REST_WAVES % PARTS_MAX : 0;
+            u.part = SUMS > 1 ? e / REST_WAVES % PARTS_MAX : 0;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 const int p = q.pairs[r * ROWS + 4 * (lane >> 4) + j];
@@ -679,55 +668,52 @@ __device__ inline bool down_part(const DecodeArgs &a, const DownPart &q, uint32_
             __syncthreads();
         }
 #pragma unroll
-        for (int k = 0; k < PARTS_MAX; k++)
+        for (int k = 0; k < SUMS; k++)
             sums[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        f32x4_t y = {};
+        f32x4_t y[STEPS] = {};   // three chains of sums, each over every third block
         int group = 0;
 #pragma unroll 1
         for (int u0 = 0; u0 < units; u0 += RING)
 #pragma unroll
             for (int d = 0; d < RING; d++) {
                 Unit &u = ring[d];
-                u32x4_t x[IN_LDS ? 1 : STEPS][4];
-                auto operand = [&](int s, u32x4_t (&x)[4]) {   // past the row's end, where the weights are zeros: anything
+                u32x4_t x[STEPS][4];
+#pragma unroll
+                for (int s = 0; s < STEPS; s++) {   // past the row's end, where the weights are zeros: anything
                     const int word = u.row + (group * STEPS + s < steps ? s * (MX_STEP / 2) : 0);
 #pragma unroll
                     for (int j = 0; j < 4; j++)
                         if constexpr (IN_LDS)
-                            x[j] = *reinterpret_cast<const u32x4_t *>(staged + word + j * 16);
+                            x[s][j] = *reinterpret_cast<const u32x4_t *>(staged + word + j * 16);
                         else
-                            x[j] = fetch16<CPOL_SC1>(h, (word + j * 16) * 4);
-                };
-                if constexpr (!IN_LDS)
-#pragma unroll
-                    for (int s = 0; s < STEPS; s++)
-                        operand(s, x[s]);
+                            x[s][j] = fetch16<CPOL_SC1>(h, (word + j * 16) * 4);
+                }
 #pragma unroll
                 for (int s = 0; s < STEPS; s++) {
-                    if constexpr (IN_LDS)
-                        operand(s, x[0]);
-                    const f32x4_t v = mx_step(u.codes[s], u.scales[s], x[IN_LDS ? 0 : s], y);
-                    y = group * STEPS + s < steps ? v : y;
-                    __builtin_amdgcn_sched_barrier(0);   // no more operands at a time than there are registers for
+                    const f32x4_t v = mx_step(u.codes[s], u.scales[s], x[s], y[s]);
+                    y[s] = group * STEPS + s < steps ? v : y[s];
                 }
                 const bool end = group + 1 == groups;
                 if (end) {   // the expert's values times the weights of its tokens
+                    const f32x4_t v = y[0] + y[1] + y[2];
 #pragma unroll
-                    for (int k = 0; k < PARTS_MAX; k++)
+                    for (int k = 0; k < SUMS; k++)
                         if (k == u.part && u0 + d < units)
 #pragma unroll
                             for (int j = 0; j < 4; j++)   // values that are not finite reach the expert's own tokens only
-                                sums[k][j] = u.share[j] < 0.f ? sums[k][j] : fmaf(u.share[j], y[j], sums[k][j]);
-                    y = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                                sums[k][j] = u.share[j] < 0.f ? sums[k][j] : fmaf(u.share[j], v[j], sums[k][j]);
+#pragma unroll
+                    for (int s = 0; s < STEPS; s++)
+                        y[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
                 }
+                __builtin_amdgcn_sched_barrier(0);   // no more at a time than there are registers for
                 group = end ? 0 : group + 1;
                 load(u);
             }
     }
 #pragma unroll
-    for (int k = 0; k < PARTS_MAX; k++)
-        if (k < PARTS_MAX / q.parts)
-            store_sums(q.red + (k * REST_WAVES + wv) * 256, sums[k]);
+    for (int k = 0; k < SUMS; k++)
+        store_sums(q.red + (k * REST_WAVES + wv) * 256, sums[k]);
     return true;
 }
 
@@ -769,9 +755,10 @@ __device__ inline bool down_item(const DecodeArgs &a, int item, int parts, uint3
     __syncthreads();
     uint32_t *staged = reinterpret_cast<uint32_t *>(weights + a.T * a.K) + REST_WAVES * a.most;
     staged += (4 - (staged - lds) % 4) % 4;
-    const DownPart q{pairs, weights, own, count, col, parts, red};
+    const DownPart q{pairs, weights, own, count, col, red};
     const bool in_lds = (int)(staged - lds) + a.T * a.K * (a.I / 2 + 4) <= LDS_WORDS;
-    if (!(in_lds ? down_part<true, HELP>(a, q, staged, sh) : down_part<false, HELP>(a, q, staged, sh)))
+    if (!(parts == 1 ? in_lds ? down_part<PARTS_MAX, true, HELP>(a, q, staged, sh) : down_part<PARTS_MAX, false, HELP>(a, q, staged, sh)
+                     : down_part<1, false, HELP>(a, q, staged, sh)))
         return false;
     __syncthreads();
     const int t = threadIdx.x, row = t / 16, c = t % 16;
@@ -819,24 +806,30 @@ __device__ inline bool out_item(const DecodeArgs &a, int item, uint32_t *lds, ui
     const int wv = wave_id(), t = threadIdx.x, row = t / 8, c = t % 8 * 2;
     float *red = reinterpret_cast<float *>(lds + REST_WAVES * STAGE_WORDS);
     const auto out = flat_rsrc(a.out, (int64_t)a.T * a.H * 2);
+    auto run = [&](auto part) {
 #pragma unroll 1
-    for (int go = !HELP && a.T <= 2 ? 0 : 1; go < 2; go++) {
-        Bf16Part<1, 12, 4> part;
-        part.start(a.w_out, a.H, a.ldcat, item, wv, REST_WAVES, go);
-        if (go && wait_for<HELP>(a, DECODE_DOWN_DONE, sh) < 0)
-            return false;
-        const auto acat = window(a.acat, (int64_t)a.T * a.ldcat * 2, go);
-        f32x4_t acc[1] = {};
-        part.finish(a.T, lds + wv * STAGE_WORDS, acc, [&](int r, int k) { return fetch16<CPOL_SC1>(acat, (r * a.ldcat + k) * 2); });
-        store_sums(red + wv * 256, acc[0]);
-        __syncthreads();
-        if (row < a.T && row < ROWS)
-            __builtin_amdgcn_raw_buffer_store_b32((int)pack_bf16x2(total<REST_WAVES>(red, 256, row * 16 + c),
-                                                                   total<REST_WAVES>(red, 256, row * 16 + c + 1)),
-                                                  out, go ? (row * a.H + item * 16 + c) * 2 : OUTSIDE, 0, 0);
-        __syncthreads();
-    }
-    return true;
+        for (int go = !HELP && a.T <= 2 ? 0 : 1; go < 2; go++) {
+            part.start(a.w_out, a.H, a.ldcat, item, wv, REST_WAVES, go);
+            if (go && wait_for<HELP>(a, DECODE_DOWN_DONE, sh) < 0)
+                return false;
+            const auto acat = window(a.acat, (int64_t)a.T * a.ldcat * 2, go);
+            f32x4_t acc[1] = {};
+            part.finish(a.T, lds + wv * STAGE_WORDS, acc,
+                        [&](int r, int k) { return fetch16<CPOL_SC1>(acat, (r * a.ldcat + k) * 2); });
+            store_sums(red + wv * 256, acc[0]);
+            __syncthreads();
+            if (row < a.T && row < ROWS)
+                __builtin_amdgcn_raw_buffer_store_b32((int)pack_bf16x2(total<REST_WAVES>(red, 256, row * 16 + c),
+                                                                       total<REST_WAVES>(red, 256, row * 16 + c + 1)),
+                                                      out, go ? (row * a.H + item * 16 + c) * 2 : OUTSIDE, 0, 0);
+            __syncthreads();
+        }
+        return true;
+    };
+    using Staged = Bf16Part<1, OUT_DEPTH, 4, true>;   // all of a wave's weights at the widths of a TP8 share, and some more
+    if (Staged::fits(a.T, a.ldcat, REST_WAVES))
+        return run(Staged());
+    return run(Bf16Part<1, 12, 4, false>());
 }
 
 // Item i, as numbered by decode_items. False when patience ran out before anything was handed on (HELP: never).
