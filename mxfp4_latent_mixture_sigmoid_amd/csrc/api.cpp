@@ -1055,7 +1055,7 @@ DecodeLayout decode_layout(const moe_config *c, int64_t T)
     part(L.counters, DECODE_COUNTER_LINES * DECODE_COUNTER_WORDS * 4);
     part(L.claims, (1 + L.most * (c->inter / 16) + Lt / 16 * std::max<int64_t>(parts, 1) + lat * c->hidden / 16) * 4);
     part(L.column_counters, parts ? Lt / 16 * 4 : 0);
-    part(L.partial, Lt / 16 * parts * 256 * 4);
+    part(L.partial, parts ? Lt * T * K * 4 : 0);
     part(L.logits, T * E * 4);
     part(L.weights, T * K * 4);
     part(L.list, L.most * 4);
@@ -1079,7 +1079,8 @@ bool decode_supported(const moe_config *c, int64_t T)
     const int64_t Hin = c->has_latent_proj ? c->hidden : c->latent, cat = c->latent + S * (int64_t)c->shared_inter;
     const int64_t widest = std::max({(c->latent + 2 * S * (int64_t)c->shared_inter) * Hin, (c->n_experts + 15) * Hin,
                                      c->has_latent_proj ? cat * c->hidden : 0, T * c->top_k * c->inter, T * cat, T * Hin,
-                                     c->latent * 2 * (int64_t)MX_STEP, c->inter * (int64_t)MX_STEP});
+                                     c->latent * 2 * (int64_t)MX_STEP, c->inter * (int64_t)MX_STEP,
+                                     32 * T * c->top_k});
     return widest * 2 < DECODE_MAX_WINDOW && items <= (1 << 24) - 1 && front <= (1 << 23) - 1;
 }
 

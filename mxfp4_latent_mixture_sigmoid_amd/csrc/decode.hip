@@ -7,8 +7,8 @@
 //  front_kernel  what only needs x: the router's logits, z = x W_down^T, h_s = bf16(silu(x Wg_s^T) (x Wu_s^T)).
 //  rest_kernel   everything after it, in work items, one for each workgroup:
 //    top    the top-K of every token; the list of distinct experts and each one's tokens
-//    gate   (expert, 16 inner channels): h = bf16(silu(z Wg^T) (z Wu^T)) of the expert's tokens
-//    down   16 latent columns of every chosen expert, or of a quarter of them: zc = bf16(sum w (h Wd^T)), summed in FP32
+//    gate   (expert, 16 or 64 inner channels): h = bf16(silu(z Wg^T) (z Wu^T)) of the expert's tokens
+//    down   16 latent columns of every chosen expert, or of a quarter of them: zc = bf16(sum w (h Wd^T)), in slot order
 //    out    16 output columns: out = bf16([zc | h_s] [W_up | W_ds]^T)
 //
 // z is kept in two BF16 parts, the rounded value and what the rounding left, because its rounding alone reaches every
@@ -278,11 +278,12 @@ __device__ inline int wait_for(const DecodeArgs &a, int i, uint32_t *sh)
 }
 
 // Whether item `i` is this workgroup's now.
+template <bool HELP>
 __device__ inline bool claim(const DecodeArgs &a, int i, uint32_t *sh)
 {
     if (threadIdx.x == 0) {
         uint32_t *at = a.claims + i;
-        *sh = __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0u &&
+        *sh = !(HELP && __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0u) &&
               __hip_atomic_fetch_add(at, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0u;
     }
     __syncthreads();
@@ -469,50 +470,39 @@ __device__ inline f32x4_t mx_step(u32x4_t codes, uint32_t scales, const u32x4_t 
     return acc;
 }
 
-// A pair of 16 gate and 16 up channels of one expert; the waves share the K axis. Up to 8 tokens: one operand, whose rows
-// 8 .. 15 are the remainders of rows 0 .. 7; more: two operands (PARTS). STAGED: z's part of this wave fits its LDS.
-template <int PARTS, bool STAGED, bool HELP>
-__device__ inline bool gate_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
+// The experts' gate and up product with one token: a pair of 16 gate and 16 up channels per workgroup, whose waves share the
+// K axis; each wave's part of z (and of its remainders, row 8 of the operand) is in LDS before the expert is known.
+template <bool HELP>
+__device__ inline bool gate_one(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
 {
-    __shared__ uint32_t tokens[ROWS / 2];   // the expert's pairs, two to a word
     const int lane = lane_id(), wv = wave_id(), t = threadIdx.x;
     const int pairs16 = a.I / 16, r = item / pairs16, cp = item % pairs16;
     const int steps = a.Lt / MX_STEP, s0 = steps * wv / REST_WAVES, n = steps * (wv + 1) / REST_WAVES - s0;
-    constexpr int BATCH = PARTS == 1 ? 7 : 4, AHEAD = STAGED ? 1 : PARTS == 1 ? 3 : 2;   // steps in flight
-    // rows past the tokens repeat the last one: their sums are not used
-    const int row = min(PARTS == 1 ? lane & 7 : lane & 15, a.T - 1), c = lane >> 4;
-    const bool rest = PARTS == 1 && (lane & 8) && a.has_latent;
+    constexpr int BATCH = 7;   // steps in flight
     uint32_t *stage = lds + wv * STAGE_WORDS;
     float *red = reinterpret_cast<float *>(lds + REST_WAVES * STAGE_WORDS);
-    const int pitch = n * MX_STEP / 2 + 4;   // words of a staged row
-    if constexpr (STAGED) {
-        const int rows = a.has_latent ? 2 * a.T : a.T, chunks = n * 16;   // of 8 values
+    const int pitch = n * MX_STEP / 2 + 4, chunks = n * 16;   // words of a staged row; 16-byte pieces
 #pragma unroll 1
-        for (int i = lane; i < rows * chunks; i += WAVE) {
-            const int k = i / chunks, j = i % chunks;
-            const uint16_t *z = (k < a.T ? a.z + (int64_t)k * a.Lt : a.z_rest + (int64_t)(k - a.T) * a.Lt) + s0 * MX_STEP;
-            *reinterpret_cast<u32x4_t *>(stage + k * pitch + j * 4) = load16(z + j * 8);
-        }
+    for (int i = lane; i < 2 * chunks; i += WAVE) {
+        const int k = i >= chunks, j = i - k * chunks;
+        *reinterpret_cast<u32x4_t *>(stage + k * pitch + j * 4) = load16((k && a.has_latent ? a.z_rest : a.z) + s0 * MX_STEP + j * 8);
     }
-    const uint32_t *staged = stage + (row + (rest ? a.T : 0)) * pitch + c * 4;
-    const int z_bytes = a.T * a.Lt * 2, at0 = row * a.Lt * 2 + c * 16;
-    const auto h = flat_rsrc(a.h, (int64_t)a.T * a.K * a.I * 2);
+    const uint32_t *staged = stage + (lane & 8 ? pitch : 0) + (lane >> 4) * 4;   // rows 1 .. 7, 9 .. 15 are not used
+    const auto h = flat_rsrc(a.h, (int64_t)a.K * a.I * 2);
     int experts = 0;
 #pragma unroll 1
-    for (int go = !HELP && a.T <= HALF && blockIdx.x < 1024 ? 0 : 1; go < 2; go++) {
-        int e = 0;
+    for (int go = HELP ? 1 : 0; go < 2; go++) {
+        int e = 0, pair = 0;
         if (go) {
             experts = wait_for<HELP>(a, DECODE_READY, sh);
             if (r >= experts)
                 return experts >= 0;
             e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
-            if (t < ROWS / 2)
-                tokens[t] = load4_sc1(flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2), (r * ROWS + 2 * t) * 2);
+            pair = (int)(load4_sc1(flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2), r * ROWS * 2) & 0xFFFFu);
         }
         const auto w = window(a.gateup + e * a.gateup_stride + (int64_t)2 * cp * steps * MX_BLOCK_BYTES,
                               2 * (int64_t)steps * MX_BLOCK_BYTES, go);
-        const auto z0 = window(a.z, z_bytes, go), z1 = window(a.has_latent ? a.z_rest : a.z, z_bytes, go);
-        f32x4_t acc[PARTS][2] = {};
+        f32x4_t acc[2] = {};
 #pragma unroll 1
         for (int s = 0; s < n; s += BATCH) {
             u32x4_t codes[BATCH][2];
@@ -526,64 +516,38 @@ __device__ inline bool gate_item(const DecodeArgs &a, int item, uint32_t *lds, u
                     scales[i][j] = fetch4<CPOL_NT>(w, off + MX_CODE_BYTES + 4 * (lane & 15));
                 }
             asm volatile("" ::: "memory");
-            // operands AHEAD steps ahead of their use; steps past the end multiply zeros
-            u32x4_t x[AHEAD][PARTS][4];
-            auto operand = [&](int i, u32x4_t (&x)[PARTS][4]) {
-                const int k = min(s + i, n - 1);
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    if constexpr (STAGED) {
-                        x[0][j] = *reinterpret_cast<const u32x4_t *>(staged + k * (MX_STEP / 2) + j * 16);
-                    } else {
-                        const int off = at0 + ((s0 + k) * MX_STEP + 32 * j) * 2;
-                        x[0][j] = PARTS == 1 ? load16(reinterpret_cast<const uint8_t *>(rest ? a.z_rest : a.z) + off)
-                                             : fetch16<0>(z0, off);
-                        if constexpr (PARTS == 2)
-                            x[1][j] = fetch16<0>(z1, off);
-                    }
-            };
-#pragma unroll
-            for (int i = 0; i < AHEAD; i++)
-                operand(i, x[i]);
 #pragma unroll
             for (int i = 0; i < BATCH; i++) {
+                u32x4_t x[4];
 #pragma unroll
-                for (int j = 0; j < 2; j++)
+                for (int j = 0; j < 4; j++)
+                    x[j] = *reinterpret_cast<const u32x4_t *>(staged + min(s + i, n - 1) * (MX_STEP / 2) + j * 16);
 #pragma unroll
-                    for (int p = 0; p < PARTS; p++) {
-                        const f32x4_t v = mx_step(codes[i][j], scales[i][j], x[i % AHEAD][p], acc[p][j]);
-                        acc[p][j] = s + i < n ? v : acc[p][j];
-                    }
-                if (i + AHEAD < BATCH)
-                    operand(i + AHEAD, x[i % AHEAD]);
+                for (int j = 0; j < 2; j++) {
+                    const f32x4_t v = mx_step(codes[i][j], scales[i][j], x, acc[j]);
+                    acc[j] = s + i < n ? v : acc[j];
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-            f32x4_t v = acc[0][j];
-            if constexpr (PARTS == 2)
-                if (a.has_latent)
-                    v += acc[1][j];
-            store_sums(red + (wv * 2 + j) * 256, v);
-        }
+        store_sums(red + (wv * 2) * 256, acc[0]);
+        store_sums(red + (wv * 2 + 1) * 256, acc[1]);
         __syncthreads();
-        // two channels of a token per thread
-        const int token = t / 8, ch = t % 8 * 2;
-        auto sum = [&](int j, int at) {
-            float v = 0.f;
+        if (t < 8) {   // two channels per thread
+            float v[2][2];
 #pragma unroll
-            for (int k = 0; k < REST_WAVES; k++) {
-                const float *p = red + (k * 2 + j) * 256 + at;
-                v += PARTS == 1 && a.has_latent ? p[0] + p[HALF * 16] : p[0];
-            }
-            return v;
-        };
-        if (token < a.T) {
-            const int pair = (int16_t)(tokens[token / 2] >> (16 * (token % 2))), at = token * 16 + ch;
-            const float v0 = silu_f32(sum(0, at)) * sum(1, at), v1 = silu_f32(sum(0, at + 1)) * sum(1, at + 1);
-            const int off = go && pair >= 0 ? (pair * a.I + cp * 16 + ch) * 2 : OUTSIDE;
-            store4_sc1(h, off, pack_bf16x2(v0, v1));
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    v[j][i] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < REST_WAVES; k++) {
+                        const float *p = red + (k * 2 + j) * 256 + 2 * t + i;
+                        v[j][i] += a.has_latent ? p[0] + p[HALF * 16] : p[0];
+                    }
+                }
+            store4_sc1(h, go ? (pair * a.I + cp * 16 + 2 * t) * 2 : OUTSIDE,
+                       pack_bf16x2(silu_f32(v[0][0]) * v[1][0], silu_f32(v[0][1]) * v[1][1]));
         }
     }
     if (arrive(a, DECODE_GATE, item, experts * pairs16))
@@ -591,56 +555,181 @@ __device__ inline bool gate_item(const DecodeArgs &a, int item, uint32_t *lds, u
     return true;
 }
 
-constexpr int PARTS_MAX = DECODE_PARTS;
-// What a workgroup of the down product knows of the routing (in LDS), and its share of the work.
-struct DownPart {
-    const int16_t *pairs;      // [experts][16]: the pair of (expert, token), or -1
-    const float *weights;      // of the pairs
-    const uint32_t *own;       // this wave's own experts: rank, and number above
-    int count, col;
-    float *red;
-};
-
-// The experts of this wave, in units of up to STEPS blocks of one expert: weights RING units ahead, the first before h is
-// known, with everything that is looked up of the unit. IN_LDS: all of h fits there; else an operand is loaded when it is needed.
-// False when patience runs out.
-template <int SUMS, bool IN_LDS, bool HELP>
-__device__ inline bool down_part(const DecodeArgs &a, const DownPart &q, uint32_t *staged, uint32_t *sh)
+// ... with several: four such pairs per workgroup, one to a wave, each over all of K, so that z goes through LDS once for
+// them all, STEPS steps at a time; weights come a chunk of as many steps ahead. Up to 8 tokens: one operand, whose rows
+// 8 .. 15 are the remainders of rows 0 .. 7; more: two operands (PARTS). K is summed in four quarters, as above, so that a
+// token's h is the same bits whatever tokens come with it.
+template <int PARTS, bool HELP>
+__device__ inline bool gate_many(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
 {
-    constexpr int STEPS = 3, RING = SUMS > 1 ? 3 : 2, NTHR = WAVE * REST_WAVES;
+    constexpr int STEPS = 4, PITCH = STEPS * MX_STEP / 2 + 4, NTHR = WAVE * REST_WAVES;   // words of a row in LDS
+    constexpr int PIECES = STEPS * 16 * 16 * PARTS / NTHR;   // 16-byte pieces of a chunk per thread
+    static_assert(16 * PARTS * PITCH <= LDS_WORDS, "room for a chunk");
+    const int lane = lane_id(), wv = wave_id(), t = threadIdx.x;
+    const int groups = a.I / 16 / REST_WAVES, r = item / groups, cp = item % groups * REST_WAVES + wv;
+    const int steps = a.Lt / MX_STEP;
+    // piece i of this thread: 8 values of row i (t / 16 ..): a token's z, or HALF or ROWS rows further its remainders.
+    // Rows past the tokens repeat the last one: their sums are not used.
+    const auto z0 = flat_rsrc(a.z, (int64_t)a.T * a.Lt * 2), z1 = flat_rsrc(a.has_latent ? a.z_rest : a.z, (int64_t)a.T * a.Lt * 2);
+    u32x4_t zs[PIECES];
+    auto fetch = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < PIECES; i++) {
+            const int p = i * NTHR + t, row = p / (STEPS * 16), c = p % (STEPS * 16);
+            const int token = min(row % (PARTS == 1 ? HALF : ROWS), a.T - 1), k = s * MX_STEP + c * 8;
+            zs[i] = fetch16<0>(row >= (PARTS == 1 ? HALF : ROWS) ? z1 : z0, k < a.Lt ? (token * a.Lt + k) * 2 : OUTSIDE);
+        }
+    };
+    fetch(0);
+    const int experts = wait_for<HELP>(a, DECODE_READY, sh);
+    if (r >= experts)
+        return experts >= 0;
+    const int e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
+    // the pairs of this lane's rows 4 (l / 16) .. +3
+    const auto pairs = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
+    const uint32_t pair01 = load4_sc1(pairs, (r * ROWS + 4 * (lane >> 4)) * 2), pair23 = load4_sc1(pairs, (r * ROWS + 4 * (lane >> 4)) * 2 + 4);
+    const auto w = window(a.gateup + e * a.gateup_stride + (int64_t)2 * cp * steps * MX_BLOCK_BYTES,
+                          2 * (int64_t)steps * MX_BLOCK_BYTES, 1);
+    struct Chunk {
+        u32x4_t codes[STEPS][2];
+        uint32_t scales[STEPS][2];
+    } now, next;
+    auto load = [&](int s, Chunk &q) {
+#pragma unroll
+        for (int i = 0; i < STEPS; i++)
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int off = s + i < steps ? (j * steps + s + i) * MX_BLOCK_BYTES : OUTSIDE;
+                q.codes[i][j] = fetch16<CPOL_NT>(w, off + lane * 16);
+                q.scales[i][j] = fetch4<CPOL_NT>(w, off + MX_CODE_BYTES + 4 * (lane & 15));
+            }
+    };
+    load(0, now);
+    f32x4_t acc[PARTS][2] = {}, sum[2] = {};
+    int quarter = 1;   // ends at this many fourths of the steps; with fewer than four, some are empty
+    while (steps * quarter / REST_WAVES == 0)
+        quarter++;
+    const uint32_t *mine = lds + (lane & 15) * PITCH + (lane >> 4) * 4;
+#pragma unroll 1
+    for (int s = 0; s < steps; s += STEPS) {
+        __syncthreads();   // every wave is past the chunk before this one
+#pragma unroll
+        for (int i = 0; i < PIECES; i++) {
+            const int p = i * NTHR + t;
+            *reinterpret_cast<u32x4_t *>(lds + p / (STEPS * 16) * PITCH + p % (STEPS * 16) * 4) = zs[i];
+        }
+        fetch(s + STEPS);
+        load(s + STEPS, next);
+        asm volatile("" ::: "memory");
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < STEPS; i++) {   // steps past the end multiply zeros
+#pragma unroll
+            for (int p = 0; p < PARTS; p++) {
+                u32x4_t x[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    x[j] = *reinterpret_cast<const u32x4_t *>(mine + p * ROWS * PITCH + i * (MX_STEP / 2) + j * 16);
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+                    acc[p][j] = mx_step(now.codes[i][j], now.scales[i][j], x, acc[p][j]);
+            }
+            if (s + i + 1 == steps * quarter / REST_WAVES) {
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const float rest = PARTS == 1 ? __shfl_xor(acc[0][j][k], 32) : acc[PARTS - 1][j][k];
+                        sum[j][k] += a.has_latent ? acc[0][j][k] + rest : acc[0][j][k];
+                    }
+#pragma unroll
+                    for (int p = 0; p < PARTS; p++)
+                        acc[p][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                }
+                while (steps * quarter / REST_WAVES == s + i + 1)
+                    quarter++;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        now = next;
+    }
+    // two channels to a word; rows of the upper half of the lanes are remainders where PARTS = 1
+    const auto h = flat_rsrc(a.h, (int64_t)a.T * a.K * a.I * 2);
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const float v = silu_f32(sum[0][k]) * sum[1][k], after = __shfl_down(v, 1);
+        const int pair = (int16_t)((k < 2 ? pair01 : pair23) >> (16 * (k % 2))), token = 4 * (lane >> 4) + k;
+        const bool keep = pair >= 0 && token < a.T && lane % 2 == 0;
+        store4_sc1(h, keep ? (pair * a.I + cp * 16 + (lane & 15)) * 2 : OUTSIDE, pack_bf16x2(v, after));
+    }
+    if (arrive(a, DECODE_GATE, item, experts * groups))
+        set_flag(a, DECODE_GATE_DONE, 0u);
+    return true;
+}
+
+// 16 latent columns of every chosen expert, by `parts` workgroups: expert number r of the list is workgroup r % parts's, and
+// of its own the i-th is wave i % 4's. Every expert's y goes to memory (or, of one workgroup, to LDS) by pairs of token and
+// slot; the last workgroup to arrive at the columns adds each token's in slot order: so a token's outputs are the same
+// bits whatever tokens come with it.
+//
+// Experts come in units of up to STEPS blocks: weights RING units ahead, the first before h is known, with everything that
+// is looked up of a unit. IN_LDS: all of h fits there; else an operand is loaded when it is needed. False when patience
+// runs out.
+struct DownPart {
+    int16_t *pairs;      // LDS: [experts][16] the pair of (expert, token), or -1
+    uint16_t *list;      // LDS: [experts]
+    float *y;            // LDS: [pairs][16], for one workgroup
+    uint32_t *staged;    // LDS: h
+    int col, part, parts;
+};
+template <bool IN_LDS, bool HELP>
+__device__ inline bool down_part(const DecodeArgs &a, const DownPart &q, uint32_t *sh)
+{
+    constexpr int STEPS = 3, RING = IN_LDS ? 4 : 2, NTHR = WAVE * REST_WAVES;
     const int lane = lane_id(), wv = wave_id();
-    const int steps = a.I / MX_STEP, groups = (steps + STEPS - 1) / STEPS, units = q.count * groups, P = a.T * a.K;
+    const int steps = a.I / MX_STEP, groups = (steps + STEPS - 1) / STEPS, P = a.T * a.K;
     const int h_pitch = IN_LDS ? a.I / 2 + 4 : a.I / 2;   // words of a row
     struct Unit {
         u32x4_t codes[STEPS];
         uint32_t scales[STEPS];
-        int row;         // words to the operand's row: any where the token did not choose the expert
-        f32x4_t share;   // the weights of the sums' tokens, -1 where they did not choose it
-        int part;        // the expert's, for parts = 1
+        int row;           // words to the operand's row: any where the token did not choose the expert
+        uint2 pairs;       // of the sums' rows
     } ring[RING];
-    f32x4_t sums[SUMS];
+    const auto y_out = flat_rsrc(a.partial + (int64_t)q.col * P * 16, (int64_t)P * 64);
 #pragma unroll 1
     for (int go = !HELP && a.T <= 2 ? 0 : 1; go < 2; go++) {
+        int count = 0;   // own experts
+        if (go) {
+            const int experts = wait_for<HELP>(a, DECODE_READY, sh);
+            if (experts < 0)
+                return false;
+            const auto gl = flat_rsrc(a.list, (int64_t)a.most * 4), gp = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
+#pragma unroll 1
+            for (int i = threadIdx.x; i < experts * (ROWS / 2); i += NTHR)
+                reinterpret_cast<uint32_t *>(q.pairs)[i] = load4_sc1(gp, i * 4);
+#pragma unroll 1
+            for (int i = threadIdx.x; i < experts; i += NTHR)
+                q.list[i] = (uint16_t)load4_sc1(gl, i * 4);
+            __syncthreads();
+            const int first = q.part + q.parts * wv;
+            count = first < experts ? (experts - first - 1) / (q.parts * REST_WAVES) + 1 : 0;
+        }
+        const int units = go ? count * groups : RING;
         const auto h = window(a.h, (int64_t)P * a.I * 2, go);
         int at = 0, at_group = 0;   // the next unit: own expert and group
         auto load = [&](Unit &u) {
-            const bool in = at < q.count;
-            const uint32_t own = q.own[in ? at : 0];
-            const int r = in ? own & 0xFFFF : 0, e = __builtin_amdgcn_readfirstlane((int)(own >> 16));
-            const auto w = window(a.down + (in ? e : 0) * a.down_stride + ((int64_t)q.col * steps + at_group * STEPS) * MX_BLOCK_BYTES,
-                                  (int64_t)min(steps - at_group * STEPS, STEPS) * MX_BLOCK_BYTES, go && in);
+            const bool in = at < count;
+            const int r = in ? q.part + q.parts * (wv + REST_WAVES * at) : 0;
+            const int e = in ? __builtin_amdgcn_readfirstlane((int)q.list[r]) : 0;
+            const auto w = window(a.down + e * a.down_stride + ((int64_t)q.col * steps + at_group * STEPS) * MX_BLOCK_BYTES,
+                                  (int64_t)min(steps - at_group * STEPS, STEPS) * MX_BLOCK_BYTES, in);
 #pragma unroll
             for (int s = 0; s < STEPS; s++) {
                 u.codes[s] = fetch16<CPOL_NT>(w, s * MX_BLOCK_BYTES + lane * 16);
                 u.scales[s] = fetch4<CPOL_NT>(w, s * MX_BLOCK_BYTES + MX_CODE_BYTES + 4 * (lane & 15));
             }
-            u.row = max((int)q.pairs[r * ROWS + (lane & 15)], 0) * h_pitch + at_group * STEPS * (MX_STEP / 2) + 4 * (lane >> 4);
-            u.part = SUMS > 1 ? e / REST_WAVES % PARTS_MAX : 0;
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const int p = q.pairs[r * ROWS + 4 * (lane >> 4) + j];
-                u.share[j] = p >= 0 ? q.weights[max(p, 0)] : -1.f;
-            }
+            u.row = min(max((int)q.pairs[r * ROWS + (lane & 15)], 0), P - 1) * h_pitch + at_group * STEPS * (MX_STEP / 2) + 4 * (lane >> 4);
+            u.pairs = *reinterpret_cast<const uint2 *>(q.pairs + r * ROWS + 4 * (lane >> 4));
             const bool end = at_group + 1 == groups;
             at += end;
             at_group = end ? 0 : at_group + 1;
@@ -662,14 +751,11 @@ __device__ inline bool down_part(const DecodeArgs &a, const DownPart &q, uint32_
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
                     const int i = min(i0 + k * NTHR, P * chunks - 1);
-                    *reinterpret_cast<u32x4_t *>(staged + i / chunks * h_pitch + i % chunks * 4) = v[k];
+                    *reinterpret_cast<u32x4_t *>(q.staged + i / chunks * h_pitch + i % chunks * 4) = v[k];
                 }
             }
             __syncthreads();
         }
-#pragma unroll
-        for (int k = 0; k < SUMS; k++)
-            sums[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         f32x4_t y[STEPS] = {};   // three chains of sums, each over every third block
         int group = 0;
 #pragma unroll 1
@@ -684,7 +770,7 @@ __device__ inline bool down_part(const DecodeArgs &a, const DownPart &q, uint32_
 #pragma unroll
                     for (int j = 0; j < 4; j++)
                         if constexpr (IN_LDS)
-                            x[s][j] = *reinterpret_cast<const u32x4_t *>(staged + word + j * 16);
+                            x[s][j] = *reinterpret_cast<const u32x4_t *>(q.staged + word + j * 16);
                         else
                             x[s][j] = fetch16<CPOL_SC1>(h, (word + j * 16) * 4);
                 }
@@ -694,14 +780,18 @@ __device__ inline bool down_part(const DecodeArgs &a, const DownPart &q, uint32_
                     y[s] = group * STEPS + s < steps ? v : y[s];
                 }
                 const bool end = group + 1 == groups;
-                if (end) {   // the expert's values times the weights of its tokens
+                if (end) {
                     const f32x4_t v = y[0] + y[1] + y[2];
+                    const bool live = go && u0 + d < units;
 #pragma unroll
-                    for (int k = 0; k < SUMS; k++)
-                        if (k == u.part && u0 + d < units)
-#pragma unroll
-                            for (int j = 0; j < 4; j++)   // values that are not finite reach the expert's own tokens only
-                                sums[k][j] = u.share[j] < 0.f ? sums[k][j] : fmaf(u.share[j], v[j], sums[k][j]);
+                    for (int j = 0; j < 4; j++) {
+                        const int pair = (int16_t)((j < 2 ? u.pairs.x : u.pairs.y) >> (16 * (j % 2)));
+                        const bool keep = live && pair >= 0;
+                        if (q.parts > 1)
+                            store4_sc1(y_out, keep ? (pair * 16 + (lane & 15)) * 4 : OUTSIDE, __float_as_uint(v[j]));
+                        else if (keep)
+                            q.y[pair * 16 + (lane & 15)] = v[j];
+                    }
 #pragma unroll
                     for (int s = 0; s < STEPS; s++)
                         y[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -711,91 +801,63 @@ __device__ inline bool down_part(const DecodeArgs &a, const DownPart &q, uint32_
                 load(u);
             }
     }
-#pragma unroll
-    for (int k = 0; k < SUMS; k++)
-        store_sums(q.red + (k * REST_WAVES + wv) * 256, sums[k]);
     return true;
 }
 
-// 16 latent columns of every chosen expert (parts = 1) or of part `part` of 4. Experts fall into 16 classes by their number
-// e: part e / 4 % 4, wave e % 4. A class is added in ascending order, the classes of a part in wave order, the parts in
-// order: so a token's sum is added in an order that its own experts alone decide, and its outputs are the same bits
-// whatever tokens come with it. With four parts the last workgroup to arrive at the columns adds them.
 template <bool HELP>
 __device__ inline bool down_item(const DecodeArgs &a, int item, int parts, uint32_t *lds, uint32_t *sh)
 {
-    constexpr int NTHR = WAVE * REST_WAVES;
-    // the waves' sums; then the routing: the pairs of (expert, token), or -1, their weights, each wave's own experts; then h
-    float *red = reinterpret_cast<float *>(lds);
-    int16_t *pairs = reinterpret_cast<int16_t *>(lds + (parts == 1 ? PARTS_MAX : 1) * REST_WAVES * 256);
-    float *weights = reinterpret_cast<float *>(pairs + a.most * ROWS);
-    uint32_t *own = reinterpret_cast<uint32_t *>(weights + a.T * a.K) + wave_id() * a.most;
-    const int lane = lane_id(), wv = wave_id(), part = parts == 1 ? 0 : item % parts, col = parts == 1 ? item : item / parts;
-    const int experts = wait_for<HELP>(a, DECODE_READY, sh);
-    if (experts < 0)
+    const int wv = wave_id(), t = threadIdx.x, row = t / 16, c = t % 16, K = a.K, P = a.T * K;
+    DownPart q;
+    q.pairs = reinterpret_cast<int16_t *>(lds);
+    q.list = reinterpret_cast<uint16_t *>(lds + a.most * (ROWS / 2));
+    uint32_t *after = lds + a.most * (ROWS / 2) + (a.most + 7) / 8 * 4;
+    q.y = reinterpret_cast<float *>(after);
+    q.staged = after + (parts == 1 ? P * 16 : 0);
+    q.col = item / parts;
+    q.part = item % parts;
+    q.parts = parts;
+    const bool in_lds = (int)(q.staged - lds) + P * (a.I / 2 + 4) <= LDS_WORDS;
+    if (!(in_lds ? down_part<true, HELP>(a, q, sh) : down_part<false, HELP>(a, q, sh)))
         return false;
-    const auto gl = flat_rsrc(a.list, (int64_t)a.most * 4), gp = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
-    const auto gw = flat_rsrc(a.weights, (int64_t)a.T * a.K * 4);
-    int count = 0;
-#pragma unroll 1
-    for (int r0 = 0; r0 < experts; r0 += WAVE) {
-        const int r = r0 + lane, e = (int)fetch4<CPOL_SC1>(gl, r < experts ? r * 4 : OUTSIDE);
-        const bool mine = r < experts && e % REST_WAVES == wv && (parts == 1 || e / REST_WAVES % PARTS_MAX == part);
-        const uint64_t all = __ballot(mine);
-        if (mine)
-            own[count + __popcll(all & ((1ull << lane) - 1))] = (uint32_t)(r | e << 16);
-        count += (int)__popcll(all);
-    }
-#pragma unroll 1
-    for (int i = threadIdx.x; i < experts * (ROWS / 2); i += NTHR)
-        reinterpret_cast<uint32_t *>(pairs)[i] = load4_sc1(gp, i * 4);
-#pragma unroll 1
-    for (int i = threadIdx.x; i < a.T * a.K; i += NTHR)
-        weights[i] = __uint_as_float(load4_sc1(gw, i * 4));
-    __syncthreads();
-    uint32_t *staged = reinterpret_cast<uint32_t *>(weights + a.T * a.K) + REST_WAVES * a.most;
-    staged += (4 - (staged - lds) % 4) % 4;
-    const DownPart q{pairs, weights, own, count, col, red};
-    const bool in_lds = (int)(staged - lds) + a.T * a.K * (a.I / 2 + 4) <= LDS_WORDS;
-    if (!(parts == 1 ? in_lds ? down_part<PARTS_MAX, true, HELP>(a, q, staged, sh) : down_part<PARTS_MAX, false, HELP>(a, q, staged, sh)
-                     : down_part<1, false, HELP>(a, q, staged, sh)))
-        return false;
-    __syncthreads();
-    const int t = threadIdx.x, row = t / 16, c = t % 16;
-    float v = 0.f;
-    if (parts == 1) {
-#pragma unroll
-        for (int p = 0; p < PARTS_MAX; p++)
-            v += total<REST_WAVES>(red + p * REST_WAVES * 256, 256, t);
-    } else {
-        const auto partial = flat_rsrc(a.partial + (int64_t)col * PARTS_MAX * 256, PARTS_MAX * 256 * 4);
-        if (row < a.T)
-            store4_sc1(partial, (part * 256 + t) * 4, __float_as_uint(total<REST_WAVES>(red, 256, t)));
+    if (parts > 1) {
         stores_done();
         if (wv == 0) {
-            const bool last = last_at(a.column_counters + col, PARTS_MAX);
+            const bool last = last_at(a.column_counters + q.col, parts);
             if (t == 0)
                 *sh = last;
         }
-        __syncthreads();
-        const bool mine = *sh != 0u;
-        __syncthreads();
-        if (!mine)
-            return true;
-        if (row < a.T)
+    }
+    __syncthreads();
+    const bool mine = parts == 1 || *sh != 0u;
+    __syncthreads();
+    if (!mine)
+        return true;
+    const auto weights = flat_rsrc(a.weights, (int64_t)P * 4), y = flat_rsrc(a.partial + (int64_t)q.col * P * 16, (int64_t)P * 64);
+    float v = 0.f;
+#pragma unroll 1
+    for (int j0 = 0; j0 < K; j0 += 8) {   // slots past the last are a weight of zero times zero
+        float w[8], ys[8];
 #pragma unroll
-            for (int p = 0; p < PARTS_MAX; p++)
-                v += __uint_as_float(load4_sc1(partial, (p * 256 + t) * 4));
+        for (int j = 0; j < 8; j++) {
+            const int pair = row * K + j0 + j;
+            const bool in = row < a.T && j0 + j < K;
+            w[j] = __uint_as_float(fetch4<CPOL_SC1>(weights, in ? pair * 4 : OUTSIDE));
+            ys[j] = parts == 1 ? q.y[(in ? pair : 0) * 16 + c] : __uint_as_float(fetch4<CPOL_SC1>(y, in ? (pair * 16 + c) * 4 : OUTSIDE));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            v = j0 + j < K ? fmaf(w[j], ys[j], v) : v;
     }
     // two columns to a word
     const uint32_t two = pack_bf16x2(v, __shfl_down(v, 1));
     if (row < a.T && c % 2 == 0) {
         if (a.has_latent)
-            store4_sc1(flat_rsrc(a.acat, (int64_t)a.T * a.ldcat * 2), (row * a.ldcat + col * 16 + c) * 2, two);
+            store4_sc1(flat_rsrc(a.acat, (int64_t)a.T * a.ldcat * 2), (row * a.ldcat + q.col * 16 + c) * 2, two);
         else
-            *reinterpret_cast<uint32_t *>(a.out + (int64_t)row * a.Lt + col * 16 + c) = two;
+            *reinterpret_cast<uint32_t *>(a.out + (int64_t)row * a.Lt + q.col * 16 + c) = two;
     }
-    if (a.has_latent && arrive(a, DECODE_DOWN, col, a.Lt / 16))
+    if (a.has_latent && arrive(a, DECODE_DOWN, q.col, a.Lt / 16))
         set_flag(a, DECODE_DOWN_DONE, 0u);
     return true;
 }
@@ -843,9 +905,9 @@ __device__ inline bool do_item(const DecodeArgs &a, const DecodeItems &n, int i,
     i -= n.top;
     if (i < n.gate) {
         if constexpr (FEW)
-            if (a.T * (a.has_latent ? 2 : 1) * ((a.Lt / MX_STEP + REST_WAVES - 1) / REST_WAVES * MX_STEP / 2 + 4) <= STAGE_WORDS)
-                return gate_item<1, true, HELP>(a, i, lds, sh);
-        return gate_item<FEW ? 1 : 2, false, HELP>(a, i, lds, sh);
+            if (decode_gate_one(a))
+                return gate_one<HELP>(a, i, lds, sh);
+        return gate_many<FEW ? 1 : 2, HELP>(a, i, lds, sh);
     }
     i -= n.gate;
     if (i < n.down)
@@ -858,18 +920,18 @@ __global__ __launch_bounds__(WAVE *REST_WAVES, 3) void rest_kernel(const DecodeA
 {
     constexpr int TOP = DECODE_MAX_E + ROWS * 32 + 16, MOST = ROWS * 32;   // MOST: pairs, and distinct experts
     static_assert(TOP + REST_WAVES * DECODE_MAX_E <= LDS_WORDS && TOP + MOST * (ROWS / 2) <= LDS_WORDS, "room for the list");
-    static_assert(REST_WAVES * 256 + MOST * (ROWS / 2 + 1 + REST_WAVES) <= LDS_WORDS, "room for the routing");
-    static_assert(PARTS_MAX * REST_WAVES * 256 + 32 * (ROWS / 2 + 1 + REST_WAVES) <= LDS_WORDS, "... and one token's sums");
+    static_assert(MOST * (ROWS / 2) + MOST / 2 <= LDS_WORDS && 32 * (ROWS / 2) + 16 + 32 * 16 <= LDS_WORDS, "... and the routing");
+    static_assert(STAGE_WORDS == DECODE_STAGE_WORDS && REST_WAVES == 4, "what decode.hpp says");
     __shared__ alignas(16) uint32_t lds[LDS_WORDS];
     __shared__ uint32_t sh;
     const DecodeItems n = decode_items(a);
     const int item = blockIdx.x;
-    if (!claim(a, item, &sh) || do_item<FEW, false>(a, n, item, lds, &sh))
+    if (!claim<false>(a, item, &sh) || do_item<FEW, false>(a, n, item, lds, &sh))
         return;
     const int kind = item < n.top + n.gate ? n.top : item < n.top + n.gate + n.down ? n.top + n.gate : n.top + n.gate + n.down;
 #pragma unroll 1
     for (int i = 0; i <= kind; i++)   // the earlier kinds' items that are still free, and then this one
-        if (i == kind || claim(a, i, &sh))
+        if (i == kind || claim<true>(a, i, &sh))
             do_item<FEW, true>(a, n, i == kind ? item : i, lds, &sh);
 }
 

@@ -20,6 +20,7 @@ constexpr int DECODE_PATIENCE = 1000;   // times that a flag is asked for, about
 constexpr int DECODE_COUNTER_WORDS = 32;
 constexpr int DECODE_COUNTER_LINES = DECODE_COUNTERS + 3 * 64;
 constexpr int DECODE_PARTS = 4;   // workgroups that share 16 columns of the down product, for more than one token
+constexpr int DECODE_STAGE_WORDS = 1856;         // LDS of a wave for its activations
 
 struct DecodeArgs {
     const uint16_t *x;               // [T, Hin]
@@ -36,7 +37,7 @@ struct DecodeArgs {
     uint32_t *column_counters;       // [Lt / 16] arrivals of a column block's parts
     uint32_t *claims;                // [items] of the second kernel
     int patience;
-    float *partial;                  // [Lt / 16][DECODE_PARTS][16][16] their sums
+    float *partial;                  // [Lt / 16][T K][16] their y
     float *logits;                   // [T, E]
     float *weights;                  // [T, K]
     int32_t *list;                   // [most] distinct experts, ascending
@@ -58,12 +59,16 @@ struct DecodeArgs {
 struct DecodeItems {
     int top, gate, down, out, parts;
 };
+// One token's gate and up product by 16 channels, where a wave's part of z and of its remainders fits its LDS; else by 64.
+__host__ __device__ inline bool decode_gate_one(const DecodeArgs &a)
+{
+    return a.T == 1 && 2 * ((a.Lt / 128 + 3) / 4 * 64 + 4) <= DECODE_STAGE_WORDS;
+}
 __host__ __device__ inline DecodeItems decode_items(const DecodeArgs &a)
 {
     const int parts = a.T == 1 ? 1 : DECODE_PARTS;
-    return {1, a.most * (a.I / 16), a.Lt / 16 * parts, a.has_latent ? a.H / 16 : 0, parts};
+    return {1, a.most * (a.I / (decode_gate_one(a) ? 16 : 64)), a.Lt / 16 * parts, a.has_latent ? a.H / 16 : 0, parts};
 }
-
 __host__ __device__ inline int decode_item_count(const DecodeItems &n) { return n.top + n.gate + n.down + n.out; }
 
 hipError_t launch_decode(const DecodeArgs &a, hipStream_t st);

@@ -32,7 +32,7 @@ def query(cfg, T):
 def test_sizes():
     up = lambda v: (v + 255) // 256 * 256          # noqa: E731
     st, size = query(config(), 5)
-    assert st == 0 and size == (up((2 * 17 + 3 * 64) * 32 * 4) + up((1 + 20 * 8 + 16 * 4 + 16) * 4) + up(16 * 4) + up(16 * 4 * 256 * 4) + up(5 * 40 * 4) + up(5 * 4 * 4)
+    assert st == 0 and size == (up((2 * 17 + 3 * 64) * 32 * 4) + up((1 + 20 * 8 + 16 * 4 + 16) * 4) + up(16 * 4) + up(256 * 20 * 4) + up(5 * 40 * 4) + up(5 * 4 * 4)
                                 + up(20 * 4) + up(20 * 16 * 2) + 2 * up(5 * 256 * 2) + up(5 * 320 * 2) + up(20 * 128 * 2))
     assert query(config(), 0)[0] == 0 and query(config(), abi.DECODE_MAX_T)[0] == 0
 
