@@ -1037,7 +1037,7 @@ namespace {
 int decode_patience = DECODE_PATIENCE;
 
 struct DecodeLayout {
-    int64_t counters, claims, column_counters, partial, logits, weights, list, pairs, z, z_rest, acat, h, total;
+    int64_t counters, claims, partial, logits, weights, chosen, list, pairs, z, z_rest, acat, h, total;
     int64_t most;   // distinct experts
 };
 
@@ -1051,13 +1051,14 @@ DecodeLayout decode_layout(const moe_config *c, int64_t T)
         at = off;
         off = align_up(off + bytes);
     };
-    const int64_t lat = c->has_latent_proj ? 1 : 0, Lt = c->latent, parts = T > 1 ? DECODE_PARTS : 0;
-    part(L.counters, DECODE_COUNTER_LINES * DECODE_COUNTER_WORDS * 4);
-    part(L.claims, (1 + L.most * (c->inter / 16) + Lt / 16 * std::max<int64_t>(parts, 1) + lat * c->hidden / 16) * 4);
-    part(L.column_counters, parts ? Lt / 16 * 4 : 0);
-    part(L.partial, parts ? Lt * T * K * 4 : 0);
+    const int64_t lat = c->has_latent_proj ? 1 : 0, Lt = c->latent,
+                  groups = (Lt + DECODE_DOWN_COLUMNS - 1) / DECODE_DOWN_COLUMNS, quads = (T + 3) / 4;
+    part(L.counters, (DECODE_SHARED_LINES + L.most + groups) * DECODE_COUNTER_WORDS * 4);
+    part(L.claims, (quads + L.most * (c->inter / 16 + groups) + quads * groups + lat * c->hidden / 16) * 4);
+    part(L.partial, T * K * Lt * 4);
     part(L.logits, T * E * 4);
     part(L.weights, T * K * 4);
+    part(L.chosen, T * K * 4);
     part(L.list, L.most * 4);
     part(L.pairs, L.most * DECODE_MAX_T * 2);
     part(L.z, lat * T * Lt * 2);
@@ -1074,13 +1075,14 @@ bool decode_supported(const moe_config *c, int64_t T)
     if (T > MOE_DECODE_MAX_T || c->stage1 != MOE_STAGE1_BF16 || c->stage2 != MOE_STAGE2_BF16)
         return false;
     const int64_t S = c->has_latent_proj ? c->n_shared : 0, most = std::min(T * c->top_k, (int64_t)c->n_experts);
-    const int64_t items = 4 + most * (c->inter / 16) + c->latent / 16 * DECODE_PARTS + c->hidden / 16;
+    const int64_t groups = (c->latent + DECODE_DOWN_COLUMNS - 1) / DECODE_DOWN_COLUMNS;
+    const int64_t items = 4 + most * (c->inter / 16 + groups) + 4 * groups + c->hidden / 16;
     const int64_t front = S * c->shared_inter / 16 + c->latent / 16 + 64;
     const int64_t Hin = c->has_latent_proj ? c->hidden : c->latent, cat = c->latent + S * (int64_t)c->shared_inter;
     const int64_t widest = std::max({(c->latent + 2 * S * (int64_t)c->shared_inter) * Hin, (c->n_experts + 15) * Hin,
                                      c->has_latent_proj ? cat * c->hidden : 0, T * c->top_k * c->inter, T * cat, T * Hin,
                                      c->latent * 2 * (int64_t)MX_STEP, c->inter * (int64_t)MX_STEP,
-                                     32 * T * c->top_k});
+                                     2 * T * c->top_k * c->latent});
     return widest * 2 < DECODE_MAX_WINDOW && items <= (1 << 24) - 1 && front <= (1 << 23) - 1;
 }
 
@@ -1149,7 +1151,7 @@ moe_status moe_decode(moe_handle *h, const void *x, int32_t T, const float *logi
     a.weights = reinterpret_cast<float *>(ws + L.weights);
     a.list = reinterpret_cast<int32_t *>(ws + L.list);
     a.pairs = reinterpret_cast<int16_t *>(ws + L.pairs);
-    a.column_counters = reinterpret_cast<uint32_t *>(ws + L.column_counters);
+    a.chosen = reinterpret_cast<int32_t *>(ws + L.chosen);
     a.claims = reinterpret_cast<uint32_t *>(ws + L.claims);
     a.patience = decode_patience;
     a.partial = reinterpret_cast<float *>(ws + L.partial);

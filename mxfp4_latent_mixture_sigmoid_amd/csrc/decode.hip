@@ -8,7 +8,8 @@
 //  rest_kernel   everything after it, in work items, one for each workgroup:
 //    top    the top-K of every token; the list of distinct experts and each one's tokens
 //    gate   (expert, 16 or 64 inner channels): h = bf16(silu(z Wg^T) (z Wu^T)) of the expert's tokens
-//    down   16 latent columns of every chosen expert, or of a quarter of them: zc = bf16(sum w (h Wd^T)), in slot order
+//    down   (expert, 256 latent columns): y = h Wd^T of the expert's tokens, in FP32
+//    sums   (4 tokens, 256 latent columns): zc = bf16(sum w y), in slot order
 //    out    16 output columns: out = bf16([zc | h_s] [W_up | W_ds]^T)
 //
 // z is kept in two BF16 parts, the rounded value and what the rounding left, because its rounding alone reaches every
@@ -21,8 +22,9 @@
 // still free, in order, and waits again. Then every item that it waits for is done or being worked on by a workgroup that
 // runs, so that all waits end, however many workgroups the card holds at once and whatever else runs on it. (Drawing
 // items from one ticket counter gives that too, but additions to one address take 12 ns each: 1057 workgroups kept the
-// top-K's loads waiting for 9 us behind theirs.) For the same reason arrivals are counted at 16 counters first, and the
-// last one writes its flag in 64 places, each asked for by a part of the workgroups. What one workgroup hands to another
+// top-K's loads waiting for 9 us behind theirs.) For the same reason a flag that every workgroup asks for is written in 64
+// places; the gate items of an expert, and the down items of 256 columns, have a counter of their own, on which the few
+// items wait that need them. What one workgroup hands to another
 // goes through agent-coherent stores and loads (sync.hpp). The front kernel clears counters, flags and claims.
 //
 // Two things set the pace of code that runs once. Instructions come from memory at about 1 KiB a microsecond the first
@@ -41,15 +43,12 @@ constexpr int ROWS = DECODE_MAX_T, HALF = ROWS / 2;
 constexpr int FRONT_WAVES = 8, REST_WAVES = 4;
 constexpr int OUT_DEPTH = 24;
 constexpr int FLAGS = WAVE;                 // places of a flag
-constexpr int ARMS = DECODE_ARMS;
 constexpr int STAGE_WORDS = 1856;           // LDS of a wave for its activations, where they fit
 constexpr int LDS_WORDS = REST_WAVES * STAGE_WORDS + REST_WAVES * 512;   // of an item; four workgroups share a CU
 
 __device__ inline uint32_t *counter(const DecodeArgs &a, int i) { return a.counters + i * DECODE_COUNTER_WORDS; }
-__device__ inline uint32_t *flag(const DecodeArgs &a, int i, int place)
-{
-    return a.counters + (DECODE_COUNTERS + i * FLAGS + place) * DECODE_COUNTER_WORDS;
-}
+__device__ inline uint32_t *flag(const DecodeArgs &a, int i, int place) { return counter(a, DECODE_FLAGS + i * FLAGS + place); }
+__device__ inline uint32_t ask(const uint32_t *at) { return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
 __device__ inline int lane_id() { return threadIdx.x & (WAVE - 1); }
 __device__ inline int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE); }
@@ -218,15 +217,11 @@ __global__ __launch_bounds__(WAVE *FRONT_WAVES, 4) void front_kernel(const Decod
     __shared__ uint32_t lds[FRONT_WAVES * STAGE_WORDS];
     const float *red = reinterpret_cast<const float *>(lds);
     const int t = threadIdx.x;
-    static_assert(DECODE_COUNTER_LINES <= WAVE * FRONT_WAVES, "a thread each");
-    if (blockIdx.x == 0 && t < DECODE_COUNTER_LINES)
-        a.counters[t * DECODE_COUNTER_WORDS] = 0u;
     const int threads = gridDim.x * WAVE * FRONT_WAVES, number = blockIdx.x * WAVE * FRONT_WAVES + t;
+    for (int i = number; i < decode_counter_lines(a); i += threads)
+        a.counters[i * DECODE_COUNTER_WORDS] = 0u;
     for (int i = number; i < decode_item_count(decode_items(a)); i += threads)
         a.claims[i] = 0u;
-    if (a.T > 1)
-        for (int i = number; i < a.Lt / 16; i += threads)
-            a.column_counters[i] = 0u;
     const int pairs = a.shared / 16, latent = a.has_latent ? a.Lt / 16 : 0;
     int item = blockIdx.x;
     const int row = t / 16, col = t % 16;
@@ -257,24 +252,32 @@ __global__ __launch_bounds__(WAVE *FRONT_WAVES, 4) void front_kernel(const Decod
     }
 }
 
-// Until flag i is set: its value less one, or -1 when patience runs out (HELP: never). One thread asks; what follows in any
-// thread is after the answer.
+// Until the flag or counter at `at` is at least `least`: its value, or -1 when patience runs out (HELP: never). `v` is what it
+// was before. One thread asks; what follows in any thread is after the answer.
 template <bool HELP>
-__device__ inline int wait_for(const DecodeArgs &a, int i, uint32_t *sh)
+__device__ inline int wait_for(const DecodeArgs &a, const uint32_t *at, uint32_t least, uint32_t *sh, uint32_t v = 0u)
 {
     if (threadIdx.x == 0) {
-        const uint32_t *at = flag(a, i, blockIdx.x % FLAGS);
-        uint32_t v;
         int left = a.patience;
-        while ((v = __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) == 0u && (HELP || left-- > 0))
-            __builtin_amdgcn_s_sleep(2);
-        *sh = v - 1;
+        while (v < least && (HELP || left-- > 0)) {
+            v = ask(at);
+            if (v < least)
+                __builtin_amdgcn_s_sleep(2);
+        }
+        *sh = v < least ? ~0u : v;
     }
     __syncthreads();
-    const int v = __builtin_amdgcn_readfirstlane((int)*sh);
+    const int got = __builtin_amdgcn_readfirstlane((int)*sh);
     __syncthreads();
     asm volatile("" ::: "memory");
-    return v;
+    return got;
+}
+// Until the experts are known: how many, or -1.
+template <bool HELP>
+__device__ inline int wait_ready(const DecodeArgs &a, uint32_t ready, uint32_t *sh)
+{
+    const int v = wait_for<HELP>(a, flag(a, DECODE_READY, blockIdx.x % FLAGS), 1u, sh, ready);
+    return v < 0 ? v : v - 1;
 }
 
 // Whether item `i` is this workgroup's now.
@@ -283,7 +286,7 @@ __device__ inline bool claim(const DecodeArgs &a, int i, uint32_t *sh)
 {
     if (threadIdx.x == 0) {
         uint32_t *at = a.claims + i;
-        *sh = !(HELP && __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0u) &&
+        *sh = !(HELP && ask(at) != 0u) &&
               __hip_atomic_fetch_add(at, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0u;
     }
     __syncthreads();
@@ -313,15 +316,12 @@ __device__ inline bool last_at(uint32_t *at, int all)   // by a wave
     return __builtin_amdgcn_readfirstlane((int)before) == all - 1;
 }
 
-// Arrival number i of `all` at counter set `at` after this workgroup's stores; true in the first wave of the last to
-// arrive. Additions to one address take 12 ns each, so the arrivals are counted at ARMS counters first.
-__device__ inline bool arrive(const DecodeArgs &a, int set, int i, int all)
+// Counts this workgroup after its stores.
+__device__ inline void arrive(uint32_t *at)
 {
     stores_done();
-    if (wave_id() != 0)
-        return false;
-    const int arm = i % ARMS, at = set * (ARMS + 1);
-    return last_at(counter(a, at + arm), (all - arm + ARMS - 1) / ARMS) && last_at(counter(a, at + ARMS), min(all, ARMS));
+    if (threadIdx.x == 0)
+        __hip_atomic_fetch_add(at, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // select_best of select.hpp in little code, from a token's logits in memory; the keys are kept in LDS (`words`, E rounded up to
@@ -405,7 +405,8 @@ __device__ inline void select_short(const float *logits, int E, int K, uint32_t 
     *weight = s / wave_sum_f32(s);
 }
 
-__device__ inline void top_item(const DecodeArgs &a, uint32_t *words)
+// The top-K of four tokens, one to a wave; the last of these items to arrive makes the list.
+__device__ inline void top_item(const DecodeArgs &a, int item, int items, uint32_t *words, uint32_t *sh)
 {
     __shared__ uint64_t scratch[REST_WAVES][WAVE];
     const int lane = lane_id(), wv = wave_id();
@@ -413,38 +414,55 @@ __device__ inline void top_item(const DecodeArgs &a, uint32_t *words)
     constexpr int NTHR = WAVE * REST_WAVES;
     // whether any token chose an expert, then its place in the list; the experts of the pairs; then the waves' keys, and
     // after them the list's pairs, two to a word
-    int *ranks = reinterpret_cast<int *>(words), *chosen = ranks + DECODE_MAX_E, *sh = chosen + ROWS * 32;
+    int *ranks = reinterpret_cast<int *>(words), *chosen = ranks + DECODE_MAX_E, *scan = chosen + ROWS * 32;
     uint32_t *table = words + DECODE_MAX_E + ROWS * 32 + 16, *mine = table + wv * DECODE_MAX_E;
-    for (int i = threadIdx.x; i < E; i += NTHR)
-        ranks[i] = 0;
-    __syncthreads();
-    const auto weights = flat_rsrc(a.weights, (int64_t)P * 4);
-#pragma unroll 1
-    for (int t = wv; t < T; t += REST_WAVES) {
+    const auto weights = flat_rsrc(a.weights, (int64_t)P * 4), all = flat_rsrc(a.chosen, (int64_t)P * 4);
+    const int t = item * REST_WAVES + wv;
+    if (t < T) {
         int id;
         float w;
         select_short(a.logits + (int64_t)t * E, E, K, mine, scratch[wv], &id, &w);
         if (lane < K) {
             const int p = t * K + lane;
             chosen[p] = id;
-            ranks[id] = 1;
             store4_sc1(weights, p * 4, __float_as_uint(w));
+            store4_sc1(all, items > 1 ? p * 4 : OUTSIDE, (uint32_t)id);
             if (a.ids_out)
                 a.ids_out[p] = id;
             if (a.weights_out)
                 a.weights_out[p] = w;
         }
     }
+    for (int i = threadIdx.x; i < E; i += NTHR)
+        ranks[i] = 0;
+    if (items > 1) {
+        stores_done();
+        if (wv == 0) {
+            const bool last = last_at(counter(a, DECODE_TOP), items);
+            if (lane == 0)
+                *sh = last;
+        }
+        __syncthreads();
+        const bool last = *sh != 0u;
+        __syncthreads();
+        if (!last)
+            return;
+        for (int p = threadIdx.x; p < P; p += NTHR)
+            chosen[p] = min((int)load4_sc1(all, p * 4), E - 1);
+    }
     __syncthreads();
+    for (int p = threadIdx.x; p < P; p += NTHR)
+        ranks[chosen[p]] = 1;
     // the distinct experts in ascending order, and for each the pairs of its tokens
     const auto list = flat_rsrc(a.list, (int64_t)a.most * 4), pairs = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
     for (int i = threadIdx.x; i < a.most * (ROWS / 2); i += NTHR)
         table[i] = ~0u;
+    __syncthreads();
     const int per = (E + NTHR - 1) / NTHR, e0 = (int)threadIdx.x * per, e1 = min(E, e0 + per);
     int n = 0, count;
     for (int e = e0; e < e1; e++)
         n += ranks[e];
-    int rank = block_excl_scan(n, sh, &count);
+    int rank = block_excl_scan(n, scan, &count);
     for (int e = e0; e < e1; e++)
         if (ranks[e]) {
             store4_sc1(list, rank * 4, (uint32_t)e);
@@ -470,12 +488,13 @@ __device__ inline f32x4_t mx_step(u32x4_t codes, uint32_t scales, const u32x4_t 
     return acc;
 }
 
-// The experts' gate and up product with one token: a pair of 16 gate and 16 up channels per workgroup, whose waves share the
-// K axis; each wave's part of z (and of its remainders, row 8 of the operand) is in LDS before the expert is known.
+// The experts' gate and up product with one or two tokens: a pair of 16 gate and 16 up channels per workgroup, whose waves
+// share the K axis; each wave's part of z (and of its remainders, rows 8 and 9 of the operand) is in LDS before the expert
+// is known.
 template <bool HELP>
-__device__ inline bool gate_one(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
+__device__ inline bool gate_few(const DecodeArgs &a, int item, uint32_t ready, uint32_t *lds, uint32_t *sh)
 {
-    const int lane = lane_id(), wv = wave_id(), t = threadIdx.x;
+    const int lane = lane_id(), wv = wave_id(), t = threadIdx.x, T = a.T;
     const int pairs16 = a.I / 16, r = item / pairs16, cp = item % pairs16;
     const int steps = a.Lt / MX_STEP, s0 = steps * wv / REST_WAVES, n = steps * (wv + 1) / REST_WAVES - s0;
     constexpr int BATCH = 7;   // steps in flight
@@ -483,22 +502,22 @@ __device__ inline bool gate_one(const DecodeArgs &a, int item, uint32_t *lds, ui
     float *red = reinterpret_cast<float *>(lds + REST_WAVES * STAGE_WORDS);
     const int pitch = n * MX_STEP / 2 + 4, chunks = n * 16;   // words of a staged row; 16-byte pieces
 #pragma unroll 1
-    for (int i = lane; i < 2 * chunks; i += WAVE) {
-        const int k = i >= chunks, j = i - k * chunks;
-        *reinterpret_cast<u32x4_t *>(stage + k * pitch + j * 4) = load16((k && a.has_latent ? a.z_rest : a.z) + s0 * MX_STEP + j * 8);
-    }
-    const uint32_t *staged = stage + (lane & 8 ? pitch : 0) + (lane >> 4) * 4;   // rows 1 .. 7, 9 .. 15 are not used
-    const auto h = flat_rsrc(a.h, (int64_t)a.K * a.I * 2);
-    int experts = 0;
+    for (int row = 0; row < 2 * T; row++)   // z of the tokens, then the remainders
+        for (int j = lane; j < chunks; j += WAVE)
+            *reinterpret_cast<u32x4_t *>(stage + row * pitch + j * 4) =
+                load16((row >= T && a.has_latent ? a.z_rest : a.z) + (int64_t)(row >= T ? row - T : row) * a.Lt + s0 * MX_STEP + j * 8);
+    // rows T .. 7 and 8 + T .. 15 of the operand repeat the last token: their sums are not used
+    const uint32_t *staged = stage + (min(lane & 7, T - 1) + (lane & 8 ? T : 0)) * pitch + (lane >> 4) * 4;
+    const auto h = flat_rsrc(a.h, (int64_t)T * a.K * a.I * 2);
 #pragma unroll 1
     for (int go = HELP ? 1 : 0; go < 2; go++) {
-        int e = 0, pair = 0;
+        int e = 0, pair = -1;
         if (go) {
-            experts = wait_for<HELP>(a, DECODE_READY, sh);
+            const int experts = wait_ready<HELP>(a, ready, sh);
             if (r >= experts)
                 return experts >= 0;
             e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
-            pair = (int)(load4_sc1(flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2), r * ROWS * 2) & 0xFFFFu);
+            pair = (int16_t)(load4_sc1(flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2), r * ROWS * 2) >> (t & 8 ? 16 : 0));
         }
         const auto w = window(a.gateup + e * a.gateup_stride + (int64_t)2 * cp * steps * MX_BLOCK_BYTES,
                               2 * (int64_t)steps * MX_BLOCK_BYTES, go);
@@ -533,7 +552,7 @@ __device__ inline bool gate_one(const DecodeArgs &a, int item, uint32_t *lds, ui
         store_sums(red + (wv * 2) * 256, acc[0]);
         store_sums(red + (wv * 2 + 1) * 256, acc[1]);
         __syncthreads();
-        if (t < 8) {   // two channels per thread
+        if (t < 8 * T) {   // two channels of a token per thread
             float v[2][2];
 #pragma unroll
             for (int j = 0; j < 2; j++)
@@ -542,29 +561,28 @@ __device__ inline bool gate_one(const DecodeArgs &a, int item, uint32_t *lds, ui
                     v[j][i] = 0.f;
 #pragma unroll
                     for (int k = 0; k < REST_WAVES; k++) {
-                        const float *p = red + (k * 2 + j) * 256 + 2 * t + i;
+                        const float *p = red + (k * 2 + j) * 256 + t / 8 * 16 + 2 * (t % 8) + i;
                         v[j][i] += a.has_latent ? p[0] + p[HALF * 16] : p[0];
                     }
                 }
-            store4_sc1(h, go ? (pair * a.I + cp * 16 + 2 * t) * 2 : OUTSIDE,
+            store4_sc1(h, go && pair >= 0 ? (pair * a.I + cp * 16 + 2 * (t % 8)) * 2 : OUTSIDE,
                        pack_bf16x2(silu_f32(v[0][0]) * v[1][0], silu_f32(v[0][1]) * v[1][1]));
         }
     }
-    if (arrive(a, DECODE_GATE, item, experts * pairs16))
-        set_flag(a, DECODE_GATE_DONE, 0u);
+    arrive(decode_gates(a, r));
     return true;
 }
 
 // ... with several: four such pairs per workgroup, one to a wave, each over all of K, so that z goes through LDS once for
-// them all, STEPS steps at a time; weights come a chunk of as many steps ahead. Up to 8 tokens: one operand, whose rows
+// them all, a chunk of STEPS steps at a time; a chunk's weights and z are loaded while the one before it is multiplied. Up to 8 tokens: one operand, whose rows
 // 8 .. 15 are the remainders of rows 0 .. 7; more: two operands (PARTS). K is summed in four quarters, as above, so that a
 // token's h is the same bits whatever tokens come with it.
 template <int PARTS, bool HELP>
-__device__ inline bool gate_many(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
+__device__ inline bool gate_many(const DecodeArgs &a, int item, uint32_t ready, uint32_t *lds, uint32_t *sh)
 {
-    constexpr int STEPS = 4, PITCH = STEPS * MX_STEP / 2 + 4, NTHR = WAVE * REST_WAVES;   // words of a row in LDS
+    constexpr int STEPS = 4 / PARTS, PITCH = STEPS * MX_STEP / 2 + 4, NTHR = WAVE * REST_WAVES;   // words of a row in LDS
     constexpr int PIECES = STEPS * 16 * 16 * PARTS / NTHR;   // 16-byte pieces of a chunk per thread
-    static_assert(16 * PARTS * PITCH <= LDS_WORDS, "room for a chunk");
+    static_assert(2 * ROWS * PARTS * PITCH <= LDS_WORDS, "room for two chunks");
     const int lane = lane_id(), wv = wave_id(), t = threadIdx.x;
     const int groups = a.I / 16 / REST_WAVES, r = item / groups, cp = item % groups * REST_WAVES + wv;
     const int steps = a.Lt / MX_STEP;
@@ -581,7 +599,7 @@ __device__ inline bool gate_many(const DecodeArgs &a, int item, uint32_t *lds, u
         }
     };
     fetch(0);
-    const int experts = wait_for<HELP>(a, DECODE_READY, sh);
+    const int experts = wait_ready<HELP>(a, ready, sh);
     if (r >= experts)
         return experts >= 0;
     const int e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
@@ -609,14 +627,15 @@ __device__ inline bool gate_many(const DecodeArgs &a, int item, uint32_t *lds, u
     int quarter = 1;   // ends at this many fourths of the steps; with fewer than four, some are empty
     while (steps * quarter / REST_WAVES == 0)
         quarter++;
-    const uint32_t *mine = lds + (lane & 15) * PITCH + (lane >> 4) * 4;
+    int half = 0;   // which half of LDS: a wave that writes it has seen every wave past the chunk before the last
 #pragma unroll 1
-    for (int s = 0; s < steps; s += STEPS) {
-        __syncthreads();   // every wave is past the chunk before this one
+    for (int s = 0; s < steps; s += STEPS, half ^= 1) {
+        uint32_t *chunk = lds + half * ROWS * PARTS * PITCH;
+        const uint32_t *mine = chunk + (lane & 15) * PITCH + (lane >> 4) * 4;
 #pragma unroll
         for (int i = 0; i < PIECES; i++) {
             const int p = i * NTHR + t;
-            *reinterpret_cast<u32x4_t *>(lds + p / (STEPS * 16) * PITCH + p % (STEPS * 16) * 4) = zs[i];
+            *reinterpret_cast<u32x4_t *>(chunk + p / (STEPS * 16) * PITCH + p % (STEPS * 16) * 4) = zs[i];
         }
         fetch(s + STEPS);
         load(s + STEPS, next);
@@ -662,203 +681,132 @@ __device__ inline bool gate_many(const DecodeArgs &a, int item, uint32_t *lds, u
         const bool keep = pair >= 0 && token < a.T && lane % 2 == 0;
         store4_sc1(h, keep ? (pair * a.I + cp * 16 + (lane & 15)) * 2 : OUTSIDE, pack_bf16x2(v, after));
     }
-    if (arrive(a, DECODE_GATE, item, experts * groups))
-        set_flag(a, DECODE_GATE_DONE, 0u);
+    arrive(decode_gates(a, r));
     return true;
 }
 
-// 16 latent columns of every chosen expert, by `parts` workgroups: expert number r of the list is workgroup r % parts's, and
-// of its own the i-th is wave i % 4's. Every expert's y goes to memory (or, of one workgroup, to LDS) by pairs of token and
-// slot; the last workgroup to arrive at the columns adds each token's in slot order: so a token's outputs are the same
-// bits whatever tokens come with it.
-//
-// Experts come in units of up to STEPS blocks: weights RING units ahead, the first before h is known, with everything that
-// is looked up of a unit. IN_LDS: all of h fits there; else an operand is loaded when it is needed. False when patience
-// runs out.
-struct DownPart {
-    int16_t *pairs;      // LDS: [experts][16] the pair of (expert, token), or -1
-    uint16_t *list;      // LDS: [experts]
-    float *y;            // LDS: [pairs][16], for one workgroup
-    uint32_t *staged;    // LDS: h
-    int col, part, parts;
-};
-template <bool IN_LDS, bool HELP>
-__device__ inline bool down_part(const DecodeArgs &a, const DownPart &q, uint32_t *sh)
+// 256 latent columns of one expert's down product, 64 to a wave: y of its tokens' pairs, to memory. The weights of AHEAD
+// steps are loaded before h is known, which takes that expert's gate items only. Each column of a pair is one chain of
+// sums over K, the same whatever tokens come with it.
+template <bool HELP>
+__device__ inline bool down_item(const DecodeArgs &a, int item, uint32_t ready, uint32_t *sh)
 {
-    constexpr int STEPS = 3, RING = IN_LDS ? 4 : 2, NTHR = WAVE * REST_WAVES;
-    const int lane = lane_id(), wv = wave_id();
-    const int steps = a.I / MX_STEP, groups = (steps + STEPS - 1) / STEPS, P = a.T * a.K;
-    const int h_pitch = IN_LDS ? a.I / 2 + 4 : a.I / 2;   // words of a row
-    struct Unit {
-        u32x4_t codes[STEPS];
-        uint32_t scales[STEPS];
-        int row;           // words to the operand's row: any where the token did not choose the expert
-        uint2 pairs;       // of the sums' rows
-    } ring[RING];
-    const auto y_out = flat_rsrc(a.partial + (int64_t)q.col * P * 16, (int64_t)P * 64);
+    constexpr int AHEAD = 3, NB = DECODE_DOWN_COLUMNS / (16 * REST_WAVES);
+    const int lane = lane_id(), groups = decode_groups(a), r = item / groups, g = item % groups;
+    const int steps = a.I / MX_STEP, P = a.T * a.K, col = (g * REST_WAVES + wave_id()) * NB, blocks = min(NB, a.Lt / 16 - col);
 #pragma unroll 1
-    for (int go = !HELP && a.T <= 2 ? 0 : 1; go < 2; go++) {
-        int count = 0;   // own experts
+    for (int go = HELP ? 1 : 0; go < 2; go++) {
+        int e = 0, x_row = OUTSIDE;
+        uint32_t pair01 = ~0u, pair23 = ~0u, arrived = 0u;
         if (go) {
-            const int experts = wait_for<HELP>(a, DECODE_READY, sh);
-            if (experts < 0)
-                return false;
-            const auto gl = flat_rsrc(a.list, (int64_t)a.most * 4), gp = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
-#pragma unroll 1
-            for (int i = threadIdx.x; i < experts * (ROWS / 2); i += NTHR)
-                reinterpret_cast<uint32_t *>(q.pairs)[i] = load4_sc1(gp, i * 4);
-#pragma unroll 1
-            for (int i = threadIdx.x; i < experts; i += NTHR)
-                q.list[i] = (uint16_t)load4_sc1(gl, i * 4);
-            __syncthreads();
-            const int first = q.part + q.parts * wv;
-            count = first < experts ? (experts - first - 1) / (q.parts * REST_WAVES) + 1 : 0;
+            const int experts = wait_ready<HELP>(a, ready, sh);
+            if (r >= experts)
+                return experts >= 0;
+            const auto pairs = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
+            const uint32_t two = load4_sc1(pairs, (r * ROWS + (lane & 14)) * 2);
+            pair01 = load4_sc1(pairs, (r * ROWS + 4 * (lane >> 4)) * 2);   // of the sums' rows
+            pair23 = load4_sc1(pairs, (r * ROWS + 4 * (lane >> 4)) * 2 + 4);
+            e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
+            arrived = ask(decode_gates(a, r));
+            const int pair = (int16_t)(lane & 1 ? two >> 16 : two);
+            x_row = pair >= 0 ? (pair * a.I + 8 * (lane >> 4)) * 2 : OUTSIDE;
         }
-        const int units = go ? count * groups : RING;
-        const auto h = window(a.h, (int64_t)P * a.I * 2, go);
-        int at = 0, at_group = 0;   // the next unit: own expert and group
-        auto load = [&](Unit &u) {
-            const bool in = at < count;
-            const int r = in ? q.part + q.parts * (wv + REST_WAVES * at) : 0;
-            const int e = in ? __builtin_amdgcn_readfirstlane((int)q.list[r]) : 0;
-            const auto w = window(a.down + e * a.down_stride + ((int64_t)q.col * steps + at_group * STEPS) * MX_BLOCK_BYTES,
-                                  (int64_t)min(steps - at_group * STEPS, STEPS) * MX_BLOCK_BYTES, in);
+        const int n = go ? steps : 1;
+        const auto w = window(a.down + e * a.down_stride + (int64_t)col * steps * MX_BLOCK_BYTES,
+                              (int64_t)steps * MX_BLOCK_BYTES * blocks, go && blocks > 0);
+        const auto h = window(a.h, (int64_t)P * a.I * 2, go), y = window(a.partial, (int64_t)P * a.Lt * 4, go);
+        u32x4_t codes[AHEAD][NB], x[AHEAD][4];
+        uint32_t scales[AHEAD][NB];
+        auto load = [&](int slot, int s) {
 #pragma unroll
-            for (int s = 0; s < STEPS; s++) {
-                u.codes[s] = fetch16<CPOL_NT>(w, s * MX_BLOCK_BYTES + lane * 16);
-                u.scales[s] = fetch4<CPOL_NT>(w, s * MX_BLOCK_BYTES + MX_CODE_BYTES + 4 * (lane & 15));
+            for (int j = 0; j < NB; j++) {
+                const int off = s < n ? (j * steps + s) * MX_BLOCK_BYTES : OUTSIDE;
+                codes[slot][j] = fetch16<CPOL_NT>(w, off + lane * 16);
+                scales[slot][j] = fetch4<CPOL_NT>(w, off + MX_CODE_BYTES + 4 * (lane & 15));
             }
-            u.row = min(max((int)q.pairs[r * ROWS + (lane & 15)], 0), P - 1) * h_pitch + at_group * STEPS * (MX_STEP / 2) + 4 * (lane >> 4);
-            u.pairs = *reinterpret_cast<const uint2 *>(q.pairs + r * ROWS + 4 * (lane >> 4));
-            const bool end = at_group + 1 == groups;
-            at += end;
-            at_group = end ? 0 : at_group + 1;
+        };
+        auto load_x = [&](int slot, int s) {
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                x[slot][j] = fetch16<CPOL_SC1>(h, s < n && x_row != OUTSIDE ? x_row + (s * MX_STEP + j * 32) * 2 : OUTSIDE);
         };
 #pragma unroll
-        for (int d = 0; d < RING; d++)
-            load(ring[d]);
+        for (int i = 0; i < AHEAD; i++)
+            load(i, i);
         asm volatile("" ::: "memory");
-        if (go && wait_for<HELP>(a, DECODE_GATE_DONE, sh) < 0)
+        if (go && wait_for<HELP>(a, decode_gates(a, r), (uint32_t)decode_gate_items(a), sh, arrived) < 0)
             return false;
-        if constexpr (IN_LDS) {
-            const int chunks = a.I / 8;
+#pragma unroll
+        for (int i = 0; i < AHEAD; i++)
+            load_x(i, i);
+        f32x4_t acc[NB] = {};
 #pragma unroll 1
-            for (int i0 = threadIdx.x; i0 < P * chunks; i0 += 4 * NTHR) {
-                u32x4_t v[4];
+        for (int s = 0; s < n; s += AHEAD)
 #pragma unroll
-                for (int k = 0; k < 4; k++)
-                    v[k] = fetch16<CPOL_SC1>(h, min(i0 + k * NTHR, P * chunks - 1) * 16);
+            for (int i = 0; i < AHEAD; i++) {   // steps past the end multiply zeros
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const int i = min(i0 + k * NTHR, P * chunks - 1);
-                    *reinterpret_cast<u32x4_t *>(q.staged + i / chunks * h_pitch + i % chunks * 4) = v[k];
-                }
+                for (int j = 0; j < NB; j++)
+                    acc[j] = mx_step(codes[i][j], scales[i][j], x[i], acc[j]);
+                __builtin_amdgcn_sched_barrier(0);
+                load(i, s + i + AHEAD);
+                load_x(i, s + i + AHEAD);
             }
-            __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int pair = (int16_t)((k < 2 ? pair01 : pair23) >> (16 * (k % 2)));
+#pragma unroll
+            for (int j = 0; j < NB; j++)
+                store4_sc1(y, pair >= 0 && j < blocks ? (pair * a.Lt + (col + j) * 16 + (lane & 15)) * 4 : OUTSIDE, __float_as_uint(acc[j][k]));
         }
-        f32x4_t y[STEPS] = {};   // three chains of sums, each over every third block
-        int group = 0;
-#pragma unroll 1
-        for (int u0 = 0; u0 < units; u0 += RING)
-#pragma unroll
-            for (int d = 0; d < RING; d++) {
-                Unit &u = ring[d];
-                u32x4_t x[STEPS][4];
-#pragma unroll
-                for (int s = 0; s < STEPS; s++) {   // past the row's end, where the weights are zeros: anything
-                    const int word = u.row + (group * STEPS + s < steps ? s * (MX_STEP / 2) : 0);
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        if constexpr (IN_LDS)
-                            x[s][j] = *reinterpret_cast<const u32x4_t *>(q.staged + word + j * 16);
-                        else
-                            x[s][j] = fetch16<CPOL_SC1>(h, (word + j * 16) * 4);
-                }
-#pragma unroll
-                for (int s = 0; s < STEPS; s++) {
-                    const f32x4_t v = mx_step(u.codes[s], u.scales[s], x[s], y[s]);
-                    y[s] = group * STEPS + s < steps ? v : y[s];
-                }
-                const bool end = group + 1 == groups;
-                if (end) {
-                    const f32x4_t v = y[0] + y[1] + y[2];
-                    const bool live = go && u0 + d < units;
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int pair = (int16_t)((j < 2 ? u.pairs.x : u.pairs.y) >> (16 * (j % 2)));
-                        const bool keep = live && pair >= 0;
-                        if (q.parts > 1)
-                            store4_sc1(y_out, keep ? (pair * 16 + (lane & 15)) * 4 : OUTSIDE, __float_as_uint(v[j]));
-                        else if (keep)
-                            q.y[pair * 16 + (lane & 15)] = v[j];
-                    }
-#pragma unroll
-                    for (int s = 0; s < STEPS; s++)
-                        y[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-                }
-                __builtin_amdgcn_sched_barrier(0);   // no more at a time than there are registers for
-                group = end ? 0 : group + 1;
-                load(u);
-            }
     }
+    arrive(decode_columns(a, g));
     return true;
 }
 
+// The weighted sum of the experts' y, in slot order: 256 latent columns of four tokens.
 template <bool HELP>
-__device__ inline bool down_item(const DecodeArgs &a, int item, int parts, uint32_t *lds, uint32_t *sh)
+__device__ inline bool sum_item(const DecodeArgs &a, int item, uint32_t ready, uint32_t *sh)
 {
-    const int wv = wave_id(), t = threadIdx.x, row = t / 16, c = t % 16, K = a.K, P = a.T * K;
-    DownPart q;
-    q.pairs = reinterpret_cast<int16_t *>(lds);
-    q.list = reinterpret_cast<uint16_t *>(lds + a.most * (ROWS / 2));
-    uint32_t *after = lds + a.most * (ROWS / 2) + (a.most + 7) / 8 * 4;
-    q.y = reinterpret_cast<float *>(after);
-    q.staged = after + (parts == 1 ? P * 16 : 0);
-    q.col = item / parts;
-    q.part = item % parts;
-    q.parts = parts;
-    const bool in_lds = (int)(q.staged - lds) + P * (a.I / 2 + 4) <= LDS_WORDS;
-    if (!(in_lds ? down_part<true, HELP>(a, q, sh) : down_part<false, HELP>(a, q, sh)))
-        return false;
-    if (parts > 1) {
-        stores_done();
-        if (wv == 0) {
-            const bool last = last_at(a.column_counters + q.col, parts);
-            if (t == 0)
-                *sh = last;
-        }
-    }
-    __syncthreads();
-    const bool mine = parts == 1 || *sh != 0u;
-    __syncthreads();
-    if (!mine)
-        return true;
-    const auto weights = flat_rsrc(a.weights, (int64_t)P * 4), y = flat_rsrc(a.partial + (int64_t)q.col * P * 16, (int64_t)P * 64);
-    float v = 0.f;
+    constexpr int SLOTS = 8;   // loaded at a time
+    const int groups = decode_groups(a), g = item % groups, K = a.K, P = a.T * K;
+    const int token = item / groups * 4 + wave_id(), col = g * DECODE_DOWN_COLUMNS + lane_id() * 4;
+    const bool live = token < a.T && col < a.Lt;
 #pragma unroll 1
-    for (int j0 = 0; j0 < K; j0 += 8) {   // slots past the last are a weight of zero times zero
-        float w[8], ys[8];
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const int pair = row * K + j0 + j;
-            const bool in = row < a.T && j0 + j < K;
-            w[j] = __uint_as_float(fetch4<CPOL_SC1>(weights, in ? pair * 4 : OUTSIDE));
-            ys[j] = parts == 1 ? q.y[(in ? pair : 0) * 16 + c] : __uint_as_float(fetch4<CPOL_SC1>(y, in ? (pair * 16 + c) * 4 : OUTSIDE));
+    for (int go = HELP ? 1 : 0; go < 2; go++) {
+        if (go) {
+            const int experts = wait_ready<HELP>(a, ready, sh);
+            if (experts < 0 || wait_for<HELP>(a, decode_columns(a, g), (uint32_t)experts, sh) < 0)
+                return false;
         }
+        const auto weights = window(a.weights, (int64_t)P * 4, go), y = window(a.partial, (int64_t)P * a.Lt * 4, go);
+        f32x4_t v = {};
+#pragma unroll 1
+        for (int j0 = 0; j0 < K; j0 += SLOTS) {   // slots past the last are skipped, not added: y may hold anything
+            u32x4_t ys[SLOTS];
+            float w[SLOTS];
 #pragma unroll
-        for (int j = 0; j < 8; j++)
-            v = j0 + j < K ? fmaf(w[j], ys[j], v) : v;
+            for (int j = 0; j < SLOTS; j++) {
+                const int pair = token * K + j0 + j;
+                const bool in = live && j0 + j < K;
+                w[j] = __uint_as_float(fetch4<CPOL_SC1>(weights, in ? pair * 4 : OUTSIDE));
+                ys[j] = fetch16<CPOL_SC1>(y, in ? (pair * a.Lt + col) * 4 : OUTSIDE);
+            }
+#pragma unroll
+            for (int j = 0; j < SLOTS; j++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    v[i] = j0 + j < K ? fmaf(w[j], __uint_as_float(ys[j][i]), v[i]) : v[i];
+        }
+        const auto to = a.has_latent ? window(a.acat, (int64_t)a.T * a.ldcat * 2, go) : window(a.out, (int64_t)a.T * a.Lt * 2, go);
+        const int at = live ? (token * (a.has_latent ? a.ldcat : a.Lt) + col) * 2 : OUTSIDE;
+        store4_sc1(to, at, pack_bf16x2(v[0], v[1]));
+        store4_sc1(to, at + 4, pack_bf16x2(v[2], v[3]));
     }
-    // two columns to a word
-    const uint32_t two = pack_bf16x2(v, __shfl_down(v, 1));
-    if (row < a.T && c % 2 == 0) {
-        if (a.has_latent)
-            store4_sc1(flat_rsrc(a.acat, (int64_t)a.T * a.ldcat * 2), (row * a.ldcat + q.col * 16 + c) * 2, two);
-        else
-            *reinterpret_cast<uint32_t *>(a.out + (int64_t)row * a.Lt + q.col * 16 + c) = two;
+    if (a.has_latent) {
+        stores_done();
+        if (wave_id() == 0 && last_at(counter(a, DECODE_SUMS), decode_items(a).sums))
+            set_flag(a, DECODE_SUMS_DONE, 0u);
     }
-    if (a.has_latent && arrive(a, DECODE_DOWN, q.col, a.Lt / 16))
-        set_flag(a, DECODE_DOWN_DONE, 0u);
     return true;
 }
 
@@ -872,7 +820,7 @@ __device__ inline bool out_item(const DecodeArgs &a, int item, uint32_t *lds, ui
 #pragma unroll 1
         for (int go = !HELP && a.T <= 2 ? 0 : 1; go < 2; go++) {
             part.start(a.w_out, a.H, a.ldcat, item, wv, REST_WAVES, go);
-            if (go && wait_for<HELP>(a, DECODE_DOWN_DONE, sh) < 0)
+            if (go && wait_for<HELP>(a, flag(a, DECODE_SUMS_DONE, blockIdx.x % FLAGS), 1u, sh) < 0)
                 return false;
             const auto acat = window(a.acat, (int64_t)a.T * a.ldcat * 2, go);
             f32x4_t acc[1] = {};
@@ -894,25 +842,29 @@ __device__ inline bool out_item(const DecodeArgs &a, int item, uint32_t *lds, ui
     return run(Bf16Part<1, 12, 4, false>());
 }
 
-// Item i, as numbered by decode_items. False when patience ran out before anything was handed on (HELP: never).
+// Item i, as numbered by decode_items. `ready`: the flag of that name a while ago. False when patience ran out before anything
+// was handed on (HELP: never).
 template <bool FEW, bool HELP>
-__device__ inline bool do_item(const DecodeArgs &a, const DecodeItems &n, int i, uint32_t *lds, uint32_t *sh)
+__device__ inline bool do_item(const DecodeArgs &a, const DecodeItems &n, int i, uint32_t ready, uint32_t *lds, uint32_t *sh)
 {
     if (i < n.top) {
-        top_item(a, lds);
+        top_item(a, i, n.top, lds, sh);
         return true;
     }
     i -= n.top;
     if (i < n.gate) {
         if constexpr (FEW)
-            if (decode_gate_one(a))
-                return gate_one<HELP>(a, i, lds, sh);
-        return gate_many<FEW ? 1 : 2, HELP>(a, i, lds, sh);
+            if (decode_gate_few(a))
+                return gate_few<HELP>(a, i, ready, lds, sh);
+        return gate_many<FEW ? 1 : 2, HELP>(a, i, ready, lds, sh);
     }
     i -= n.gate;
     if (i < n.down)
-        return down_item<HELP>(a, i, n.parts, lds, sh);
-    return out_item<HELP>(a, i - n.down, lds, sh);
+        return down_item<HELP>(a, i, ready, sh);
+    i -= n.down;
+    if (i < n.sums)
+        return sum_item<HELP>(a, i, ready, sh);
+    return out_item<HELP>(a, i - n.sums, lds, sh);
 }
 
 template <bool FEW>
@@ -920,19 +872,24 @@ __global__ __launch_bounds__(WAVE *REST_WAVES, 3) void rest_kernel(const DecodeA
 {
     constexpr int TOP = DECODE_MAX_E + ROWS * 32 + 16, MOST = ROWS * 32;   // MOST: pairs, and distinct experts
     static_assert(TOP + REST_WAVES * DECODE_MAX_E <= LDS_WORDS && TOP + MOST * (ROWS / 2) <= LDS_WORDS, "room for the list");
-    static_assert(MOST * (ROWS / 2) + MOST / 2 <= LDS_WORDS && 32 * (ROWS / 2) + 16 + 32 * 16 <= LDS_WORDS, "... and the routing");
     static_assert(STAGE_WORDS == DECODE_STAGE_WORDS && REST_WAVES == 4, "what decode.hpp says");
     __shared__ alignas(16) uint32_t lds[LDS_WORDS];
     __shared__ uint32_t sh;
     const DecodeItems n = decode_items(a);
     const int item = blockIdx.x;
-    if (!claim<false>(a, item, &sh) || do_item<FEW, false>(a, n, item, lds, &sh))
+    const uint32_t ready = ask(flag(a, DECODE_READY, item % FLAGS));   // comes with the claim
+    if (!claim<false>(a, item, &sh) || do_item<FEW, false>(a, n, item, ready, lds, &sh))
         return;
-    const int kind = item < n.top + n.gate ? n.top : item < n.top + n.gate + n.down ? n.top + n.gate : n.top + n.gate + n.down;
+    int kind = 0;   // the first item of this one's kind
+    for (const int size : {n.top, n.gate, n.down, n.sums})
+        if (item >= kind + size)
+            kind += size;
+        else
+            break;
 #pragma unroll 1
     for (int i = 0; i <= kind; i++)   // the earlier kinds' items that are still free, and then this one
         if (i == kind || claim<true>(a, i, &sh))
-            do_item<FEW, true>(a, n, i == kind ? item : i, lds, &sh);
+            do_item<FEW, true>(a, n, i == kind ? item : i, 0u, lds, &sh);
 }
 
 } // namespace

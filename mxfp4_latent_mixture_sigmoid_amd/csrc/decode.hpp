@@ -11,16 +11,14 @@ constexpr int DECODE_MAX_T = MOE_DECODE_MAX_T;   // the rows of a matrix-core ti
 constexpr int DECODE_MAX_E = 1024;
 constexpr int DECODE_MAX_WINDOW = 0x7FFF0000;    // bytes of a matrix, of h and of [zc | h_s]
 
-// One to a cache line: two sets of arrival counters, each of DECODE_ARMS and one more for their last arrivals; three flags,
-// each in 64 places.
-enum { DECODE_GATE, DECODE_DOWN };
-enum { DECODE_READY, DECODE_GATE_DONE, DECODE_DOWN_DONE };
-constexpr int DECODE_ARMS = 16, DECODE_COUNTERS = 2 * (DECODE_ARMS + 1);
-constexpr int DECODE_PATIENCE = 1000;   // times that a flag is asked for, about a microsecond each
-constexpr int DECODE_COUNTER_WORDS = 32;
-constexpr int DECODE_COUNTER_LINES = DECODE_COUNTERS + 3 * 64;
-constexpr int DECODE_PARTS = 4;   // workgroups that share 16 columns of the down product, for more than one token
-constexpr int DECODE_STAGE_WORDS = 1856;         // LDS of a wave for its activations
+// One to a cache line: two counters; two flags, each in 64 places; then a counter for every expert of the list and one for every
+// 256 columns.
+enum { DECODE_TOP, DECODE_SUMS, DECODE_FLAGS };
+enum { DECODE_READY, DECODE_SUMS_DONE };
+constexpr int DECODE_COUNTER_WORDS = 32, DECODE_SHARED_LINES = DECODE_FLAGS + 2 * 64;
+constexpr int DECODE_PATIENCE = 1000;        // times that a flag is asked for, about a microsecond each
+constexpr int DECODE_DOWN_COLUMNS = 256;     // of a workgroup in the down product
+constexpr int DECODE_STAGE_WORDS = 1856;     // LDS of a wave for its activations
 
 struct DecodeArgs {
     const uint16_t *x;               // [T, Hin]
@@ -33,13 +31,13 @@ struct DecodeArgs {
     int64_t n_router_rows, n_latent_rows, n_shared_rows, shared_at;   // rows of their matrices; the shared ones' first row
     int64_t gateup_stride, down_stride;
     // workspace
-    uint32_t *counters;              // DECODE_COUNTER_LINES lines
-    uint32_t *column_counters;       // [Lt / 16] arrivals of a column block's parts
+    uint32_t *counters;              // decode_counter_lines of them
     uint32_t *claims;                // [items] of the second kernel
     int patience;
-    float *partial;                  // [Lt / 16][T K][16] their y
+    float *partial;                  // [T K, Lt] y
     float *logits;                   // [T, E]
     float *weights;                  // [T, K]
+    int32_t *chosen;                 // [T, K] experts
     int32_t *list;                   // [most] distinct experts, ascending
     int16_t *pairs;                  // [most, 16] the pair of (expert, token), or -1
     int most;                        // min(T K, E)
@@ -54,22 +52,33 @@ struct DecodeArgs {
     uint16_t *out;                   // [T, H] ([T, Lt] without latent projections)
 };
 
-// Work items of the second kernel, numbered kind after kind. One token's experts are few enough for one
-// workgroup to a column block; more are shared by DECODE_PARTS.
-struct DecodeItems {
-    int top, gate, down, out, parts;
-};
-// One token's gate and up product by 16 channels, where a wave's part of z and of its remainders fits its LDS; else by 64.
-__host__ __device__ inline bool decode_gate_one(const DecodeArgs &a)
+// One or two tokens' gate and up product by 16 channels, where a wave's part of z and of its remainders fits its LDS; else by
+// 64. (Two tokens: TWO us against MANY.)
+__host__ __device__ inline bool decode_gate_few(const DecodeArgs &a)
 {
-    return a.T == 1 && 2 * ((a.Lt / 128 + 3) / 4 * 64 + 4) <= DECODE_STAGE_WORDS;
+    return a.T <= 2 && 2 * a.T * ((a.Lt / 128 + 3) / 4 * 64 + 4) <= DECODE_STAGE_WORDS;
 }
+__host__ __device__ inline int decode_gate_items(const DecodeArgs &a) { return a.I / (decode_gate_few(a) ? 16 : 64); }   // of an expert
+__host__ __device__ inline int decode_groups(const DecodeArgs &a) { return (a.Lt + DECODE_DOWN_COLUMNS - 1) / DECODE_DOWN_COLUMNS; }
+
+// Work items of the second kernel, numbered kind after kind.
+struct DecodeItems {
+    int top, gate, down, sums, out;
+};
 __host__ __device__ inline DecodeItems decode_items(const DecodeArgs &a)
 {
-    const int parts = a.T == 1 ? 1 : DECODE_PARTS;
-    return {1, a.most * (a.I / (decode_gate_one(a) ? 16 : 64)), a.Lt / 16 * parts, a.has_latent ? a.H / 16 : 0, parts};
+    return {(a.T + 3) / 4, a.most * decode_gate_items(a), a.most * decode_groups(a), (a.T + 3) / 4 * decode_groups(a),
+            a.has_latent ? a.H / 16 : 0};
 }
-__host__ __device__ inline int decode_item_count(const DecodeItems &n) { return n.top + n.gate + n.down + n.out; }
+__host__ __device__ inline int decode_item_count(const DecodeItems &n) { return n.top + n.gate + n.down + n.sums + n.out; }
+
+// Arrivals of the list's expert r at its h; of the down items at the columns of group g.
+__host__ __device__ inline int decode_counter_lines(const DecodeArgs &a) { return DECODE_SHARED_LINES + a.most + decode_groups(a); }
+__host__ __device__ inline uint32_t *decode_gates(const DecodeArgs &a, int r)
+{
+    return a.counters + (DECODE_SHARED_LINES + r) * DECODE_COUNTER_WORDS;
+}
+__host__ __device__ inline uint32_t *decode_columns(const DecodeArgs &a, int g) { return decode_gates(a, a.most + g); }
 
 hipError_t launch_decode(const DecodeArgs &a, hipStream_t st);
 
