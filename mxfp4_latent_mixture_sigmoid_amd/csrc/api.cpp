@@ -1054,9 +1054,10 @@ DecodeLayout decode_layout(const moe_config *c, int64_t T)
     const int64_t lat = c->has_latent_proj ? 1 : 0, Lt = c->latent,
                   groups = (Lt + DECODE_DOWN_COLUMNS - 1) / DECODE_DOWN_COLUMNS, quads = (T + 3) / 4;
     part(L.counters, (DECODE_SHARED_LINES + L.most + groups) * DECODE_COUNTER_WORDS * 4);
-    part(L.claims, (quads + L.most * (c->inter / 16 + groups) + quads * groups + lat * c->hidden / 16) * 4);
+    part(L.claims, ((E + 15) / 16 * DECODE_ROUTER_PARTS + lat * (Lt + S * c->shared_inter + c->hidden) / 16 + quads * (1 + groups) +
+                    L.most * (c->inter / 16 + groups)) * 4);
     part(L.partial, T * K * Lt * 4);
-    part(L.logits, T * E * 4);
+    part(L.logits, DECODE_ROUTER_PARTS * T * E * 4);
     part(L.weights, T * K * 4);
     part(L.chosen, T * K * 4);
     part(L.list, L.most * 4);
@@ -1076,14 +1077,13 @@ bool decode_supported(const moe_config *c, int64_t T)
         return false;
     const int64_t S = c->has_latent_proj ? c->n_shared : 0, most = std::min(T * c->top_k, (int64_t)c->n_experts);
     const int64_t groups = (c->latent + DECODE_DOWN_COLUMNS - 1) / DECODE_DOWN_COLUMNS;
-    const int64_t items = 4 + most * (c->inter / 16 + groups) + 4 * groups + c->hidden / 16;
-    const int64_t front = S * c->shared_inter / 16 + c->latent / 16 + 64;
+    const int64_t items = 4 + most * (c->inter / 16 + groups) + 4 * groups + (c->n_experts * DECODE_ROUTER_PARTS + c->hidden + c->latent + S * c->shared_inter) / 16 + 4;
     const int64_t Hin = c->has_latent_proj ? c->hidden : c->latent, cat = c->latent + S * (int64_t)c->shared_inter;
     const int64_t widest = std::max({(c->latent + 2 * S * (int64_t)c->shared_inter) * Hin, (c->n_experts + 15) * Hin,
                                      c->has_latent_proj ? cat * c->hidden : 0, T * c->top_k * c->inter, T * cat, T * Hin,
                                      c->latent * 2 * (int64_t)MX_STEP, c->inter * (int64_t)MX_STEP,
                                      2 * T * c->top_k * c->latent});
-    return widest * 2 < DECODE_MAX_WINDOW && items <= (1 << 24) - 1 && front <= (1 << 23) - 1;
+    return widest * 2 < DECODE_MAX_WINDOW && items <= (1 << 24) - 1;
 }
 
 } // namespace
@@ -1147,7 +1147,8 @@ moe_status moe_decode(moe_handle *h, const void *x, int32_t T, const float *logi
     a.gateup_stride = h->gateup_stride;
     a.down_stride = h->down_stride;
     a.counters = reinterpret_cast<uint32_t *>(ws + L.counters);
-    a.logits = logits_out ? logits_out : reinterpret_cast<float *>(ws + L.logits);
+    a.logits = reinterpret_cast<float *>(ws + L.logits);
+    a.logits_out = logits_out;
     a.weights = reinterpret_cast<float *>(ws + L.weights);
     a.list = reinterpret_cast<int32_t *>(ws + L.list);
     a.pairs = reinterpret_cast<int16_t *>(ws + L.pairs);

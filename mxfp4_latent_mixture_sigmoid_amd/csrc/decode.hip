@@ -40,7 +40,7 @@ namespace mxmoe {
 namespace {
 
 constexpr int ROWS = DECODE_MAX_T, HALF = ROWS / 2;
-constexpr int FRONT_WAVES = 8, REST_WAVES = 4;
+constexpr int REST_WAVES = 4, ROUTER_PARTS = DECODE_ROUTER_PARTS;
 constexpr int OUT_DEPTH = 24;
 constexpr int FLAGS = WAVE;                 // places of a flag
 constexpr int STAGE_WORDS = 1856;           // LDS of a wave for its activations, where they fit
@@ -189,69 +189,6 @@ struct Bf16Part {
     }
 };
 
-// Items: pairs of shared gate and up blocks first, which take twice as long, then the latent's blocks, then the router's.
-template <int NB>
-__device__ inline void front_product(const DecodeArgs &a, const uint8_t *w, int64_t rows, int block, uint32_t *lds)
-{
-    const int wv = wave_id();
-    f32x4_t acc[NB] = {};
-    auto run = [&](auto part) {
-        part.start(w, rows, a.Hin, block, wv, FRONT_WAVES);
-        part.finish(a.T, lds + wv * STAGE_WORDS, acc, [&](int r, int k) { return load16(a.x + (int64_t)r * a.Hin + k); });
-    };
-    using Staged = Bf16Part<NB, NB == 1 ? 16 : 8, 4, true>;
-    if (Staged::fits(a.T, a.Hin, FRONT_WAVES))
-        run(Staged());
-    else
-        run(Bf16Part<NB, NB == 1 ? 8 : 4, 4, false>());
-    __syncthreads();
-    float *red = reinterpret_cast<float *>(lds);
-#pragma unroll
-    for (int j = 0; j < NB; j++)
-        store_sums(red + (wv * NB + j) * 256, acc[j]);
-    __syncthreads();
-}
-
-__global__ __launch_bounds__(WAVE *FRONT_WAVES, 4) void front_kernel(const DecodeArgs a)
-{
-    __shared__ uint32_t lds[FRONT_WAVES * STAGE_WORDS];
-    const float *red = reinterpret_cast<const float *>(lds);
-    const int t = threadIdx.x;
-    const int threads = gridDim.x * WAVE * FRONT_WAVES, number = blockIdx.x * WAVE * FRONT_WAVES + t;
-    for (int i = number; i < decode_counter_lines(a); i += threads)
-        a.counters[i * DECODE_COUNTER_WORDS] = 0u;
-    for (int i = number; i < decode_item_count(decode_items(a)); i += threads)
-        a.claims[i] = 0u;
-    const int pairs = a.shared / 16, latent = a.has_latent ? a.Lt / 16 : 0;
-    int item = blockIdx.x;
-    const int row = t / 16, col = t % 16;
-    if (item < pairs) {
-        front_product<2>(a, a.w_shared, a.n_shared_rows, (int)(a.shared_at / 16) + 2 * item, lds);
-        if (t < 256 && row < a.T) {
-            const float g = total<FRONT_WAVES>(red, 512, t), u = total<FRONT_WAVES>(red, 512, 256 + t);
-            a.acat[(int64_t)row * a.ldcat + a.Lt + item * 16 + col] = (uint16_t)f32_to_bf16_bits(silu_f32(g) * u);
-        }
-        return;
-    }
-    item -= pairs;
-    const bool z = item < latent;
-    if (!z)
-        item -= latent;
-    front_product<1>(a, z ? a.w_latent : a.w_router, z ? a.n_latent_rows : a.n_router_rows, item, lds);
-    if (t >= 256 || row >= a.T)
-        return;
-    const float v = total<FRONT_WAVES>(red, 256, t);
-    const int n = item * 16 + col;
-    if (z) {
-        const uint32_t high = f32_to_bf16_bits(v);
-        const int64_t at = (int64_t)row * a.Lt + n;
-        a.z[at] = (uint16_t)high;
-        a.z_rest[at] = (uint16_t)f32_to_bf16_bits(v - bf16_bits_to_f32(high));
-    } else if (n < a.E) {
-        a.logits[(int64_t)row * a.E + n] = a.bias ? v + a.bias[n] : v;
-    }
-}
-
 // Until the flag or counter at `at` is at least `least`: its value, or -1 when patience runs out (HELP: never). `v` is what it
 // was before. One thread asks; what follows in any thread is after the answer.
 template <bool HELP>
@@ -272,12 +209,21 @@ __device__ inline int wait_for(const DecodeArgs &a, const uint32_t *at, uint32_t
     asm volatile("" ::: "memory");
     return got;
 }
+struct Seen {   // two flags as they were a while ago
+    uint32_t ready, z;
+};
 // Until the experts are known: how many, or -1.
 template <bool HELP>
-__device__ inline int wait_ready(const DecodeArgs &a, uint32_t ready, uint32_t *sh)
+__device__ inline int wait_ready(const DecodeArgs &a, const Seen &seen, uint32_t *sh)
 {
-    const int v = wait_for<HELP>(a, flag(a, DECODE_READY, blockIdx.x % FLAGS), 1u, sh, ready);
+    const int v = wait_for<HELP>(a, flag(a, DECODE_READY, blockIdx.x % FLAGS), 1u, sh, seen.ready);
     return v < 0 ? v : v - 1;
+}
+// Until z is there.
+template <bool HELP>
+__device__ inline bool wait_z(const DecodeArgs &a, const Seen &seen, uint32_t *sh)
+{
+    return !a.has_latent || wait_for<HELP>(a, flag(a, DECODE_Z_DONE, blockIdx.x % FLAGS), 1u, sh, seen.z) >= 0;
 }
 
 // Whether item `i` is this workgroup's now.
@@ -324,50 +270,157 @@ __device__ inline void arrive(uint32_t *at)
         __hip_atomic_fetch_add(at, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// select_best of select.hpp in little code, from a token's logits in memory; the keys are kept in LDS (`words`, E rounded up to
-// 256), four of a lane side by side. No key of an expert is 0, which stands for none (only a NaN with every bit set
-// would have it), so that ids are always in range.
-__device__ inline void select_short(const float *logits, int E, int K, uint32_t *words, uint64_t *scratch, int *id, float *weight)
+// ... after its part of [zc | h_s].
+__device__ inline void arrive_out(const DecodeArgs &a)
+{
+    stores_done();
+    const DecodeItems n = decode_items(a);
+    if (wave_id() == 0 && last_at(counter(a, DECODE_CAT), n.shared + n.sums))
+        set_flag(a, DECODE_CAT_DONE, 0u);
+}
+
+// 16 columns (NB = 2: two such blocks) of a BF16 product over x; the waves share the K axis and leave their sums in LDS. The
+// weights are asked for before the item is claimed. False when another workgroup has it.
+template <int NB, bool HELP>
+__device__ inline bool front_product(const DecodeArgs &a, const uint8_t *w, int64_t rows, int block, uint32_t *lds, uint32_t *sh, int part_of_k = 0, int parts = 1)
+{
+    const int wv = wave_id();
+    const auto x = flat_rsrc(a.x, (int64_t)a.T * a.Hin * 2);
+    f32x4_t acc[NB] = {};
+    auto run = [&](auto part) {
+        part.start(w, rows, a.Hin, block, part_of_k * REST_WAVES + wv, parts * REST_WAVES);
+        if (!HELP && !claim<false>(a, blockIdx.x, sh))
+            return false;
+        part.finish(a.T, lds + wv * STAGE_WORDS, acc, [&](int r, int k) { return fetch16<0>(x, (r * a.Hin + k) * 2); });
+        return true;
+    };
+    using Staged = Bf16Part<NB, 16 / NB, 4, true>;
+    if (!(Staged::fits(a.T, a.Hin, parts * REST_WAVES) ? run(Staged()) : run(Bf16Part<NB, 16 / NB, 8, false>())))
+        return false;
+    __syncthreads();
+    float *red = reinterpret_cast<float *>(lds);
+#pragma unroll
+    for (int j = 0; j < NB; j++)
+        store_sums(red + (wv * NB + j) * 256, acc[j]);
+    __syncthreads();
+    return true;
+}
+
+// 16 experts' logits over one of ROUTER_PARTS parts of x. (All front items run at once and share the memory's rate: so the
+// router's are short, and the top-K is done before z.)
+template <bool HELP>
+__device__ inline void router_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
+{
+    const int part = item % ROUTER_PARTS, block = item / ROUTER_PARTS;
+    if (!front_product<1, HELP>(a, a.w_router, a.n_router_rows, block, lds, sh, part, ROUTER_PARTS))
+        return;
+    const int t = threadIdx.x, row = t / 16, n = block * 16 + t % 16;
+    const float v = total<REST_WAVES>(reinterpret_cast<const float *>(lds), 256, t);
+    if (row < a.T && n < a.E)
+        store4_sc1(flat_rsrc(a.logits, (int64_t)ROUTER_PARTS * a.T * a.E * 4), ((part * a.T + row) * a.E + n) * 4, __float_as_uint(v));
+    arrive(counter(a, DECODE_ROUTER));
+}
+
+// 16 latent columns.
+template <bool HELP>
+__device__ inline void latent_item(const DecodeArgs &a, int item, int items, uint32_t *lds, uint32_t *sh)
+{
+    if (!front_product<1, HELP>(a, a.w_latent, a.n_latent_rows, item, lds, sh))
+        return;
+    const int t = threadIdx.x, row = t / 8, c = t % 8 * 2;
+    if (row < a.T) {   // a wave each of 8 rows: at most 16 rows, two waves
+        const float *red = reinterpret_cast<const float *>(lds);
+        const float v0 = total<REST_WAVES>(red, 256, row * 16 + c), v1 = total<REST_WAVES>(red, 256, row * 16 + c + 1);
+        const uint32_t high = pack_bf16x2(v0, v1);
+        const int at = (row * a.Lt + item * 16 + c) * 2;
+        store4_sc1(flat_rsrc(a.z, (int64_t)a.T * a.Lt * 2), at, high);
+        store4_sc1(flat_rsrc(a.z_rest, (int64_t)a.T * a.Lt * 2), at,
+                   pack_bf16x2(v0 - __uint_as_float(high << 16), v1 - __uint_as_float(high & 0xFFFF0000u)));
+    }
+    stores_done();
+    if (wave_id() != 0)
+        return;
+    const int arm = item % DECODE_ARMS;   // additions to one address take 12 ns each
+    if (last_at(counter(a, DECODE_Z + arm), (items - arm + DECODE_ARMS - 1) / DECODE_ARMS) &&
+        last_at(counter(a, DECODE_Z + DECODE_ARMS), min(items, DECODE_ARMS)))
+        set_flag(a, DECODE_Z_DONE, 0u);
+}
+
+// 16 channels of the shared experts.
+template <bool HELP>
+__device__ inline void shared_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
+{
+    if (!front_product<2, HELP>(a, a.w_shared, a.n_shared_rows, (int)(a.shared_at / 16) + 2 * item, lds, sh))
+        return;
+    const int t = threadIdx.x, row = t / 8, c = t % 8 * 2;
+    if (row < a.T) {
+        const float *red = reinterpret_cast<const float *>(lds) + row * 16 + c;
+        float v[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            v[i] = silu_f32(total<REST_WAVES>(red, 512, i)) * total<REST_WAVES>(red, 512, 256 + i);
+        store4_sc1(flat_rsrc(a.acat, (int64_t)a.T * a.ldcat * 2), (row * a.ldcat + a.Lt + item * 16 + c) * 2, pack_bf16x2(v[0], v[1]));
+    }
+    arrive_out(a);
+}
+
+// select_best of select.hpp in little code, for token t, from its logits' parts in memory. No key of an expert is 0, which stands for none (only a NaN with every bit set
+// would have it), so that ids are always in range. `go` = 0: keys that are all different in place of the logits.
+__device__ inline void select_short(const DecodeArgs &a, int t, int go, uint32_t *words, uint64_t *scratch, int *id, float *weight)
 {
     constexpr int QUADS = DECODE_MAX_E / (4 * WAVE);
-    const int lane = lane_id(), quads = (E + 4 * WAVE - 1) / (4 * WAVE);
-    const auto row = flat_rsrc(logits, (int64_t)E * 4);
-    u32x4_t raw[QUADS];
+    const int lane = lane_id(), E = a.E, K = a.K;
+    const auto bias = window(a.bias, (int64_t)E * 4, a.bias != nullptr), logits = window(a.logits_out + (int64_t)t * E, (int64_t)E * 4, go && a.logits_out);
+    u32x4_t raw[QUADS][ROUTER_PARTS + 1];
 #pragma unroll
-    for (int q = 0; q < QUADS; q++)
-        raw[q] = fetch16<0>(row, (q * WAVE + lane) * 16);
+    for (int p = 0; p < ROUTER_PARTS; p++) {
+        const auto row = window(a.logits + ((int64_t)p * a.T + t) * E, (int64_t)E * 4, go);
 #pragma unroll
-    for (int q = 0; q < QUADS; q++)
-        *reinterpret_cast<u32x4_t *>(words + (q * WAVE + lane) * 4) = raw[q];
-    uint32_t top = 0u;
-#pragma unroll 1
-    for (int q = 0; q < quads; q++) {
-        u32x4_t v = *reinterpret_cast<const u32x4_t *>(words + (q * WAVE + lane) * 4);
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            v[j] = (q * WAVE + lane) * 4 + j < E ? max(order_key(__uint_as_float(v[j])), 1u) : 0u;
-            top = max(top, v[j]);
-        }
-        *reinterpret_cast<u32x4_t *>(words + (q * WAVE + lane) * 4) = v;
+        for (int q = 0; q < QUADS; q++)
+            raw[q][p] = fetch16<CPOL_SC1>(row, (q * WAVE + lane) * 16);
     }
-    uint32_t bound = 0u;
-#pragma unroll 1
-    for (uint32_t bit = 1u << 31; bit; bit >>= 1)
-        if ((int)__popcll(__ballot(top >= (bound | bit))) >= K)
-            bound |= bit;
-    int total = 0;
-#pragma unroll 1
-    for (int q = 0; q < quads; q++) {
-        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(words + (q * WAVE + lane) * 4);
+#pragma unroll
+    for (int q = 0; q < QUADS; q++)
+        raw[q][ROUTER_PARTS] = fetch16<0>(bias, (q * WAVE + lane) * 16);
+    uint32_t keys[QUADS * 4], top = 0u;
+#pragma unroll
+    for (int q = 0; q < QUADS; q++) {
+        u32x4_t sum;
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const bool in = v[j] != 0u && v[j] >= bound;
-            const uint64_t all = __ballot(in);
-            const int at = total + (int)__popcll(all & ((1ull << lane) - 1));
-            if (in && at < WAVE)
-                scratch[at] = ((uint64_t)v[j] << 32) | (uint32_t)~(uint32_t)((q * WAVE + lane) * 4 + j);
-            total += (int)__popcll(all);
+            float v = __uint_as_float(raw[q][0][j]);
+#pragma unroll
+            for (int p = 1; p < ROUTER_PARTS; p++)
+                v += __uint_as_float(raw[q][p][j]);
+            v = a.bias ? v + __uint_as_float(raw[q][ROUTER_PARTS][j]) : v;
+            sum[j] = __float_as_uint(v);
+            const int e = (q * WAVE + lane) * 4 + j;
+            const uint32_t key = e < E ? go ? max(order_key(v), 1u) : 1u + e : 0u;
+            keys[q * 4 + j] = key;
+            top = max(top, key);
         }
+        __builtin_amdgcn_raw_buffer_store_b128(sum, logits, (q * WAVE + lane) * 16, 0, 0);
+    }
+    // K lanes hold a key of at least `bound`, so the best K keys are among those
+    uint32_t bound = 0u;
+    int held = WAVE;
+#pragma unroll 1
+    for (uint32_t bit = 1u << 31; bit && held != K; bit >>= 1) {
+        const int n = (int)__popcll(__ballot(top >= (bound | bit)));
+        if (n >= K) {
+            bound |= bit;
+            held = n;
+        }
+    }
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < QUADS * 4; i++) {
+        const bool in = keys[i] != 0u && keys[i] >= bound;
+        const uint64_t all = __ballot(in);
+        const int at = total + (int)__popcll(all & ((1ull << lane) - 1));
+        if (in && at < WAVE)
+            scratch[at] = ((uint64_t)keys[i] << 32) | (uint32_t)~(uint32_t)((i / 4 * WAVE + lane) * 4 + i % 4);
+        total += (int)__popcll(all);
     }
     uint64_t mine = 0;
     if (total <= WAVE) {
@@ -383,6 +436,9 @@ __device__ inline void select_short(const float *logits, int E, int K, uint32_t 
             scratch[rank] = mine;
         mine = lane < K ? scratch[lane] : 0;
     } else {   // heavy ties: one maximum after another
+#pragma unroll
+        for (int i = 0; i < QUADS * 4; i++)
+            words[(i / 4 * WAVE + lane) * 4 + i % 4] = keys[i];
 #pragma unroll 1
         for (int k = 0; k < K; k++) {
             uint64_t best = 0;
@@ -405,8 +461,10 @@ __device__ inline void select_short(const float *logits, int E, int K, uint32_t 
     *weight = s / wave_sum_f32(s);
 }
 
-// The top-K of four tokens, one to a wave; the last of these items to arrive makes the list.
-__device__ inline void top_item(const DecodeArgs &a, int item, int items, uint32_t *words, uint32_t *sh)
+// The top-K of four tokens, one to a wave; the last of these items to arrive makes the list: the distinct experts in ascending
+// order, and for each the pairs of its tokens.
+template <bool HELP>
+__device__ inline bool top_item(const DecodeArgs &a, int item, int items, uint32_t *words, uint32_t *sh)
 {
     __shared__ uint64_t scratch[REST_WAVES][WAVE];
     const int lane = lane_id(), wv = wave_id();
@@ -416,67 +474,75 @@ __device__ inline void top_item(const DecodeArgs &a, int item, int items, uint32
     // after them the list's pairs, two to a word
     int *ranks = reinterpret_cast<int *>(words), *chosen = ranks + DECODE_MAX_E, *scan = chosen + ROWS * 32;
     uint32_t *table = words + DECODE_MAX_E + ROWS * 32 + 16, *mine = table + wv * DECODE_MAX_E;
-    const auto weights = flat_rsrc(a.weights, (int64_t)P * 4), all = flat_rsrc(a.chosen, (int64_t)P * 4);
     const int t = item * REST_WAVES + wv;
-    if (t < T) {
-        int id;
-        float w;
-        select_short(a.logits + (int64_t)t * E, E, K, mine, scratch[wv], &id, &w);
-        if (lane < K) {
-            const int p = t * K + lane;
-            chosen[p] = id;
-            store4_sc1(weights, p * 4, __float_as_uint(w));
-            store4_sc1(all, items > 1 ? p * 4 : OUTSIDE, (uint32_t)id);
-            if (a.ids_out)
-                a.ids_out[p] = id;
-            if (a.weights_out)
-                a.weights_out[p] = w;
-        }
-    }
-    for (int i = threadIdx.x; i < E; i += NTHR)
-        ranks[i] = 0;
-    if (items > 1) {
-        stores_done();
-        if (wv == 0) {
-            const bool last = last_at(counter(a, DECODE_TOP), items);
-            if (lane == 0)
-                *sh = last;
-        }
-        __syncthreads();
-        const bool last = *sh != 0u;
-        __syncthreads();
-        if (!last)
-            return;
+#pragma unroll 1
+    for (int go = HELP ? 1 : 0; go < 2; go++) {
+        if (go && wait_for<HELP>(a, counter(a, DECODE_ROUTER), (uint32_t)(a.n_router_rows / 16 * ROUTER_PARTS), sh) < 0)
+            return false;
+        const auto weights = window(a.weights, (int64_t)P * 4, go), all = window(a.chosen, (int64_t)P * 4, go);
         for (int p = threadIdx.x; p < P; p += NTHR)
-            chosen[p] = min((int)load4_sc1(all, p * 4), E - 1);
-    }
-    __syncthreads();
-    for (int p = threadIdx.x; p < P; p += NTHR)
-        ranks[chosen[p]] = 1;
-    // the distinct experts in ascending order, and for each the pairs of its tokens
-    const auto list = flat_rsrc(a.list, (int64_t)a.most * 4), pairs = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
-    for (int i = threadIdx.x; i < a.most * (ROWS / 2); i += NTHR)
-        table[i] = ~0u;
-    __syncthreads();
-    const int per = (E + NTHR - 1) / NTHR, e0 = (int)threadIdx.x * per, e1 = min(E, e0 + per);
-    int n = 0, count;
-    for (int e = e0; e < e1; e++)
-        n += ranks[e];
-    int rank = block_excl_scan(n, scan, &count);
-    for (int e = e0; e < e1; e++)
-        if (ranks[e]) {
-            store4_sc1(list, rank * 4, (uint32_t)e);
-            ranks[e] = rank++;
+            chosen[p] = 0;
+        for (int i = threadIdx.x; i < E; i += NTHR)
+            ranks[i] = 0;
+        __syncthreads();
+        if (t < T) {
+            int id;
+            float w;
+            select_short(a, t, go, mine, scratch[wv], &id, &w);
+            if (lane < K) {
+                const int p = t * K + lane;
+                chosen[p] = id;
+                store4_sc1(weights, p * 4, __float_as_uint(w));
+                store4_sc1(all, items > 1 ? p * 4 : OUTSIDE, (uint32_t)id);
+                if (go && a.ids_out)
+                    a.ids_out[p] = id;
+                if (go && a.weights_out)
+                    a.weights_out[p] = w;
+            }
         }
-    __syncthreads();
-    for (int p = threadIdx.x; p < P; p += NTHR)
-        reinterpret_cast<int16_t *>(table)[ranks[chosen[p]] * ROWS + p / K] = (int16_t)p;
-    __syncthreads();
-    for (int i = threadIdx.x; i < count * (ROWS / 2); i += NTHR)
-        store4_sc1(pairs, i * 4, table[i]);
-    stores_done();
-    if (wv == 0)
-        set_flag(a, DECODE_READY, (uint32_t)count);
+        if (go && items > 1) {
+            stores_done();
+            if (wv == 0) {
+                const bool last = last_at(counter(a, DECODE_TOP), items);
+                if (lane == 0)
+                    *sh = last;
+            }
+            __syncthreads();
+            const bool last = *sh != 0u;
+            __syncthreads();
+            if (!last)
+                return true;
+            for (int p = threadIdx.x; p < P; p += NTHR)
+                chosen[p] = min((int)load4_sc1(all, p * 4), E - 1);
+        }
+        __syncthreads();
+        for (int p = threadIdx.x; p < P; p += NTHR)
+            ranks[chosen[p]] = 1;
+        const auto list = window(a.list, (int64_t)a.most * 4, go), pairs = window(a.pairs, (int64_t)a.most * ROWS * 2, go);
+        for (int i = threadIdx.x; i < a.most * (ROWS / 2); i += NTHR)
+            table[i] = ~0u;
+        __syncthreads();
+        const int per = (E + NTHR - 1) / NTHR, e0 = (int)threadIdx.x * per, e1 = min(E, e0 + per);
+        int n = 0, count;
+        for (int e = e0; e < e1; e++)
+            n += ranks[e];
+        int rank = block_excl_scan(n, scan, &count);
+        for (int e = e0; e < e1; e++)
+            if (ranks[e]) {
+                store4_sc1(list, rank * 4, (uint32_t)e);
+                ranks[e] = rank++;
+            }
+        __syncthreads();
+        for (int p = threadIdx.x; p < P; p += NTHR)
+            reinterpret_cast<int16_t *>(table)[ranks[chosen[p]] * ROWS + p / K] = (int16_t)p;
+        __syncthreads();
+        for (int i = threadIdx.x; i < count * (ROWS / 2); i += NTHR)
+            store4_sc1(pairs, i * 4, table[i]);
+        stores_done();
+        if (go && wv == 0)
+            set_flag(a, DECODE_READY, (uint32_t)count);
+    }
+    return true;
 }
 
 // One MX block times a step's activations.
@@ -489,10 +555,10 @@ __device__ inline f32x4_t mx_step(u32x4_t codes, uint32_t scales, const u32x4_t 
 }
 
 // The experts' gate and up product with one or two tokens: a pair of 16 gate and 16 up channels per workgroup, whose waves
-// share the K axis; each wave's part of z (and of its remainders, rows 8 and 9 of the operand) is in LDS before the expert
-// is known.
+// share the K axis; each wave's part of z (and of its remainders, rows 8 and 9 of the operand) goes through LDS. The first
+// weights are asked for before z is there.
 template <bool HELP>
-__device__ inline bool gate_few(const DecodeArgs &a, int item, uint32_t ready, uint32_t *lds, uint32_t *sh)
+__device__ inline bool gate_few(const DecodeArgs &a, int item, const Seen &seen, uint32_t *lds, uint32_t *sh)
 {
     const int lane = lane_id(), wv = wave_id(), t = threadIdx.x, T = a.T;
     const int pairs16 = a.I / 16, r = item / pairs16, cp = item % pairs16;
@@ -501,11 +567,6 @@ __device__ inline bool gate_few(const DecodeArgs &a, int item, uint32_t ready, u
     uint32_t *stage = lds + wv * STAGE_WORDS;
     float *red = reinterpret_cast<float *>(lds + REST_WAVES * STAGE_WORDS);
     const int pitch = n * MX_STEP / 2 + 4, chunks = n * 16;   // words of a staged row; 16-byte pieces
-#pragma unroll 1
-    for (int row = 0; row < 2 * T; row++)   // z of the tokens, then the remainders
-        for (int j = lane; j < chunks; j += WAVE)
-            *reinterpret_cast<u32x4_t *>(stage + row * pitch + j * 4) =
-                load16((row >= T && a.has_latent ? a.z_rest : a.z) + (int64_t)(row >= T ? row - T : row) * a.Lt + s0 * MX_STEP + j * 8);
     // rows T .. 7 and 8 + T .. 15 of the operand repeat the last token: their sums are not used
     const uint32_t *staged = stage + (min(lane & 7, T - 1) + (lane & 8 ? T : 0)) * pitch + (lane >> 4) * 4;
     const auto h = flat_rsrc(a.h, (int64_t)T * a.K * a.I * 2);
@@ -513,7 +574,7 @@ __device__ inline bool gate_few(const DecodeArgs &a, int item, uint32_t ready, u
     for (int go = HELP ? 1 : 0; go < 2; go++) {
         int e = 0, pair = -1;
         if (go) {
-            const int experts = wait_ready<HELP>(a, ready, sh);
+            const int experts = wait_ready<HELP>(a, seen, sh);
             if (r >= experts)
                 return experts >= 0;
             e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
@@ -521,20 +582,42 @@ __device__ inline bool gate_few(const DecodeArgs &a, int item, uint32_t ready, u
         }
         const auto w = window(a.gateup + e * a.gateup_stride + (int64_t)2 * cp * steps * MX_BLOCK_BYTES,
                               2 * (int64_t)steps * MX_BLOCK_BYTES, go);
+        u32x4_t codes[BATCH][2];
+        uint32_t scales[BATCH][2];
+        auto load = [&](int slot, int s) {
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int off = s < n ? (j * steps + s0 + s) * MX_BLOCK_BYTES : OUTSIDE;
+                codes[slot][j] = fetch16<CPOL_NT>(w, off + lane * 16);
+                scales[slot][j] = fetch4<CPOL_NT>(w, off + MX_CODE_BYTES + 4 * (lane & 15));
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < BATCH; i++)
+            load(i, i);
+        asm volatile("" ::: "memory");
+        if (go && !wait_z<HELP>(a, seen, sh))
+            return false;
+        const auto z0 = window(a.z, (int64_t)T * a.Lt * 2, go), z1 = window(a.has_latent ? a.z_rest : a.z, (int64_t)T * a.Lt * 2, go);
+#pragma unroll 1
+        for (int i0 = 0; i0 < 2 * T * chunks; i0 += 4 * WAVE) {   // z of the tokens, then the remainders
+            u32x4_t v[4];
+            int to[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int p = min(i0 + i * WAVE + lane, 2 * T * chunks - 1), row = p / chunks, j = p % chunks;
+                const int off = ((row >= T ? row - T : row) * a.Lt + s0 * MX_STEP + j * 8) * 2;
+                const u32x4_t v0 = fetch16<CPOL_SC1>(z0, row < T ? off : OUTSIDE), v1 = fetch16<CPOL_SC1>(z1, row < T ? OUTSIDE : off);
+                v[i] = v0 | v1;
+                to[i] = row * pitch + j * 4;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                *reinterpret_cast<u32x4_t *>(stage + to[i]) = v[i];
+        }
         f32x4_t acc[2] = {};
 #pragma unroll 1
-        for (int s = 0; s < n; s += BATCH) {
-            u32x4_t codes[BATCH][2];
-            uint32_t scales[BATCH][2];
-#pragma unroll
-            for (int i = 0; i < BATCH; i++)
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    const int off = s + i < n ? (j * steps + s0 + s + i) * MX_BLOCK_BYTES : OUTSIDE;
-                    codes[i][j] = fetch16<CPOL_NT>(w, off + lane * 16);
-                    scales[i][j] = fetch4<CPOL_NT>(w, off + MX_CODE_BYTES + 4 * (lane & 15));
-                }
-            asm volatile("" ::: "memory");
+        for (int s = 0; s < n; s += BATCH)
 #pragma unroll
             for (int i = 0; i < BATCH; i++) {
                 u32x4_t x[4];
@@ -547,8 +630,8 @@ __device__ inline bool gate_few(const DecodeArgs &a, int item, uint32_t ready, u
                     acc[j] = s + i < n ? v : acc[j];
                 }
                 __builtin_amdgcn_sched_barrier(0);
+                load(i, s + i + BATCH);
             }
-        }
         store_sums(red + (wv * 2) * 256, acc[0]);
         store_sums(red + (wv * 2 + 1) * 256, acc[1]);
         __syncthreads();
@@ -578,7 +661,7 @@ __device__ inline bool gate_few(const DecodeArgs &a, int item, uint32_t ready, u
 // 8 .. 15 are the remainders of rows 0 .. 7; more: two operands (PARTS). K is summed in four quarters, as above, so that a
 // token's h is the same bits whatever tokens come with it.
 template <int PARTS, bool HELP>
-__device__ inline bool gate_many(const DecodeArgs &a, int item, uint32_t ready, uint32_t *lds, uint32_t *sh)
+__device__ inline bool gate_many(const DecodeArgs &a, int item, const Seen &seen, uint32_t *lds, uint32_t *sh)
 {
     constexpr int STEPS = 4 / PARTS, PITCH = STEPS * MX_STEP / 2 + 4, NTHR = WAVE * REST_WAVES;   // words of a row in LDS
     constexpr int PIECES = STEPS * 16 * 16 * PARTS / NTHR;   // 16-byte pieces of a chunk per thread
@@ -587,19 +670,18 @@ __device__ inline bool gate_many(const DecodeArgs &a, int item, uint32_t ready, 
     const int groups = a.I / 16 / REST_WAVES, r = item / groups, cp = item % groups * REST_WAVES + wv;
     const int steps = a.Lt / MX_STEP;
     // piece i of this thread: 8 values of row i (t / 16 ..): a token's z, or HALF or ROWS rows further its remainders.
-    // Rows past the tokens repeat the last one: their sums are not used.
+    // Rows past the tokens are zeros.
     const auto z0 = flat_rsrc(a.z, (int64_t)a.T * a.Lt * 2), z1 = flat_rsrc(a.has_latent ? a.z_rest : a.z, (int64_t)a.T * a.Lt * 2);
     u32x4_t zs[PIECES];
     auto fetch = [&](int s) {
 #pragma unroll
         for (int i = 0; i < PIECES; i++) {
             const int p = i * NTHR + t, row = p / (STEPS * 16), c = p % (STEPS * 16);
-            const int token = min(row % (PARTS == 1 ? HALF : ROWS), a.T - 1), k = s * MX_STEP + c * 8;
-            zs[i] = fetch16<0>(row >= (PARTS == 1 ? HALF : ROWS) ? z1 : z0, k < a.Lt ? (token * a.Lt + k) * 2 : OUTSIDE);
+            const int token = row % (PARTS == 1 ? HALF : ROWS), k = s * MX_STEP + c * 8;
+            zs[i] = fetch16<CPOL_SC1>(row >= (PARTS == 1 ? HALF : ROWS) ? z1 : z0, k < a.Lt && token < a.T ? (token * a.Lt + k) * 2 : OUTSIDE);
         }
     };
-    fetch(0);
-    const int experts = wait_ready<HELP>(a, ready, sh);
+    const int experts = wait_ready<HELP>(a, seen, sh);
     if (r >= experts)
         return experts >= 0;
     const int e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
@@ -623,6 +705,10 @@ __device__ inline bool gate_many(const DecodeArgs &a, int item, uint32_t ready, 
             }
     };
     load(0, now);
+    asm volatile("" ::: "memory");
+    if (!wait_z<HELP>(a, seen, sh))
+        return false;
+    fetch(0);
     f32x4_t acc[PARTS][2] = {}, sum[2] = {};
     int quarter = 1;   // ends at this many fourths of the steps; with fewer than four, some are empty
     while (steps * quarter / REST_WAVES == 0)
@@ -689,7 +775,7 @@ __device__ inline bool gate_many(const DecodeArgs &a, int item, uint32_t ready, 
 // steps are loaded before h is known, which takes that expert's gate items only. Each column of a pair is one chain of
 // sums over K, the same whatever tokens come with it.
 template <bool HELP>
-__device__ inline bool down_item(const DecodeArgs &a, int item, uint32_t ready, uint32_t *sh)
+__device__ inline bool down_item(const DecodeArgs &a, int item, const Seen &seen, uint32_t *sh)
 {
     constexpr int AHEAD = 3, NB = DECODE_DOWN_COLUMNS / (16 * REST_WAVES);
     const int lane = lane_id(), groups = decode_groups(a), r = item / groups, g = item % groups;
@@ -699,7 +785,7 @@ __device__ inline bool down_item(const DecodeArgs &a, int item, uint32_t ready, 
         int e = 0, x_row = OUTSIDE;
         uint32_t pair01 = ~0u, pair23 = ~0u, arrived = 0u;
         if (go) {
-            const int experts = wait_ready<HELP>(a, ready, sh);
+            const int experts = wait_ready<HELP>(a, seen, sh);
             if (r >= experts)
                 return experts >= 0;
             const auto pairs = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
@@ -765,7 +851,7 @@ __device__ inline bool down_item(const DecodeArgs &a, int item, uint32_t ready, 
 
 // The weighted sum of the experts' y, in slot order: 256 latent columns of four tokens.
 template <bool HELP>
-__device__ inline bool sum_item(const DecodeArgs &a, int item, uint32_t ready, uint32_t *sh)
+__device__ inline bool sum_item(const DecodeArgs &a, int item, const Seen &seen, uint32_t *sh)
 {
     constexpr int SLOTS = 8;   // loaded at a time
     const int groups = decode_groups(a), g = item % groups, K = a.K, P = a.T * K;
@@ -774,7 +860,7 @@ __device__ inline bool sum_item(const DecodeArgs &a, int item, uint32_t ready, u
 #pragma unroll 1
     for (int go = HELP ? 1 : 0; go < 2; go++) {
         if (go) {
-            const int experts = wait_ready<HELP>(a, ready, sh);
+            const int experts = wait_ready<HELP>(a, seen, sh);
             if (experts < 0 || wait_for<HELP>(a, decode_columns(a, g), (uint32_t)experts, sh) < 0)
                 return false;
         }
@@ -802,11 +888,8 @@ __device__ inline bool sum_item(const DecodeArgs &a, int item, uint32_t ready, u
         store4_sc1(to, at, pack_bf16x2(v[0], v[1]));
         store4_sc1(to, at + 4, pack_bf16x2(v[2], v[3]));
     }
-    if (a.has_latent) {
-        stores_done();
-        if (wave_id() == 0 && last_at(counter(a, DECODE_SUMS), decode_items(a).sums))
-            set_flag(a, DECODE_SUMS_DONE, 0u);
-    }
+    if (a.has_latent)
+        arrive_out(a);
     return true;
 }
 
@@ -820,7 +903,7 @@ __device__ inline bool out_item(const DecodeArgs &a, int item, uint32_t *lds, ui
 #pragma unroll 1
         for (int go = !HELP && a.T <= 2 ? 0 : 1; go < 2; go++) {
             part.start(a.w_out, a.H, a.ldcat, item, wv, REST_WAVES, go);
-            if (go && wait_for<HELP>(a, flag(a, DECODE_SUMS_DONE, blockIdx.x % FLAGS), 1u, sh) < 0)
+            if (go && wait_for<HELP>(a, flag(a, DECODE_CAT_DONE, blockIdx.x % FLAGS), 1u, sh) < 0)
                 return false;
             const auto acat = window(a.acat, (int64_t)a.T * a.ldcat * 2, go);
             f32x4_t acc[1] = {};
@@ -839,36 +922,48 @@ __device__ inline bool out_item(const DecodeArgs &a, int item, uint32_t *lds, ui
     using Staged = Bf16Part<1, OUT_DEPTH, 4, true>;   // all of a wave's weights at the widths of a TP8 share, and some more
     if (Staged::fits(a.T, a.ldcat, REST_WAVES))
         return run(Staged());
-    return run(Bf16Part<1, 12, 4, false>());
+    return run(Bf16Part<1, OUT_DEPTH, 8, false>());
 }
 
-// Item i, as numbered by decode_items. `ready`: the flag of that name a while ago. False when patience ran out before anything
-// was handed on (HELP: never).
+// Item i, as numbered by decode_items. False when patience ran out before anything was handed on (HELP: never).
 template <bool FEW, bool HELP>
-__device__ inline bool do_item(const DecodeArgs &a, const DecodeItems &n, int i, uint32_t ready, uint32_t *lds, uint32_t *sh)
+__device__ inline bool do_item(const DecodeArgs &a, const DecodeItems &n, int i, const Seen &seen, uint32_t *lds, uint32_t *sh)
 {
-    if (i < n.top) {
-        top_item(a, i, n.top, lds, sh);
+    if (i < n.router) {
+        router_item<HELP>(a, i, lds, sh);
         return true;
     }
+    i -= n.router;
+    if (i < n.latent) {
+        latent_item<HELP>(a, i, n.latent, lds, sh);
+        return true;
+    }
+    i -= n.latent;
+    if (i < n.top)
+        return top_item<HELP>(a, i, n.top, lds, sh);
     i -= n.top;
     if (i < n.gate) {
         if constexpr (FEW)
             if (decode_gate_few(a))
-                return gate_few<HELP>(a, i, ready, lds, sh);
-        return gate_many<FEW ? 1 : 2, HELP>(a, i, ready, lds, sh);
+                return gate_few<HELP>(a, i, seen, lds, sh);
+        return gate_many<FEW ? 1 : 2, HELP>(a, i, seen, lds, sh);
     }
     i -= n.gate;
+    if (i < n.shared) {
+        shared_item<HELP>(a, i, lds, sh);
+        return true;
+    }
+    i -= n.shared;
     if (i < n.down)
-        return down_item<HELP>(a, i, ready, sh);
+        return down_item<HELP>(a, i, seen, sh);
     i -= n.down;
     if (i < n.sums)
-        return sum_item<HELP>(a, i, ready, sh);
+        return sum_item<HELP>(a, i, seen, sh);
     return out_item<HELP>(a, i - n.sums, lds, sh);
 }
 
 template <bool FEW>
-__global__ __launch_bounds__(WAVE *REST_WAVES, 3) void rest_kernel(const DecodeArgs a)
+__global__ __launch_bounds__(WAVE *REST_WAVES, 3) void decode_kernel(const DecodeArgs a)
 {
     constexpr int TOP = DECODE_MAX_E + ROWS * 32 + 16, MOST = ROWS * 32;   // MOST: pairs, and distinct experts
     static_assert(TOP + REST_WAVES * DECODE_MAX_E <= LDS_WORDS && TOP + MOST * (ROWS / 2) <= LDS_WORDS, "room for the list");
@@ -877,11 +972,13 @@ __global__ __launch_bounds__(WAVE *REST_WAVES, 3) void rest_kernel(const DecodeA
     __shared__ uint32_t sh;
     const DecodeItems n = decode_items(a);
     const int item = blockIdx.x;
-    const uint32_t ready = ask(flag(a, DECODE_READY, item % FLAGS));   // comes with the claim
-    if (!claim<false>(a, item, &sh) || do_item<FEW, false>(a, n, item, ready, lds, &sh))
+    const bool late = item < n.router + n.latent ||   // claimed in front_product
+                      (item >= n.router + n.latent + n.top + n.gate && item < n.router + n.latent + n.top + n.gate + n.shared);
+    const Seen seen{ask(flag(a, DECODE_READY, item % FLAGS)), ask(flag(a, DECODE_Z_DONE, item % FLAGS))};   // come with the claim
+    if ((!late && !claim<false>(a, item, &sh)) || do_item<FEW, false>(a, n, item, seen, lds, &sh))
         return;
     int kind = 0;   // the first item of this one's kind
-    for (const int size : {n.top, n.gate, n.down, n.sums})
+    for (const int size : {n.router, n.latent, n.top, n.gate, n.shared, n.down, n.sums})
         if (item >= kind + size)
             kind += size;
         else
@@ -889,24 +986,33 @@ __global__ __launch_bounds__(WAVE *REST_WAVES, 3) void rest_kernel(const DecodeA
 #pragma unroll 1
     for (int i = 0; i <= kind; i++)   // the earlier kinds' items that are still free, and then this one
         if (i == kind || claim<true>(a, i, &sh))
-            do_item<FEW, true>(a, n, i == kind ? item : i, 0u, lds, &sh);
+            do_item<FEW, true>(a, n, i == kind ? item : i, Seen{0u, 0u}, lds, &sh);
+}
+
+// Counters, flags and claims at zero.
+__global__ __launch_bounds__(256) void clear_kernel(const DecodeArgs a)
+{
+    const int lines = decode_counter_lines(a), i = blockIdx.x * 256 + threadIdx.x;
+    if (i < lines)
+        a.counters[i * DECODE_COUNTER_WORDS] = 0u;
+    else if (i - lines < decode_item_count(decode_items(a)))
+        a.claims[i - lines] = 0u;
 }
 
 } // namespace
 
 hipError_t launch_decode(const DecodeArgs &a, hipStream_t st)
 {
-    const unsigned front = (unsigned)(a.shared / 16 + (a.has_latent ? a.Lt / 16 : 0) + a.n_router_rows / 16);
-    hipLaunchKernelGGL(front_kernel, dim3(front), dim3(WAVE * FRONT_WAVES), 0, st, a);
+    const int items = decode_item_count(decode_items(a));
+    hipLaunchKernelGGL(clear_kernel, dim3((unsigned)((items + decode_counter_lines(a) + 255) / 256)), dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    const DecodeItems n = decode_items(a);
-    const dim3 grid((unsigned)decode_item_count(n)), threads(WAVE * REST_WAVES);
+    const dim3 grid((unsigned)items), threads(WAVE * REST_WAVES);
     if (a.T <= HALF)
-        hipLaunchKernelGGL((rest_kernel<true>), grid, threads, 0, st, a);
+        hipLaunchKernelGGL((decode_kernel<true>), grid, threads, 0, st, a);
     else
-        hipLaunchKernelGGL((rest_kernel<false>), grid, threads, 0, st, a);
+        hipLaunchKernelGGL((decode_kernel<false>), grid, threads, 0, st, a);
     return hipGetLastError();
 }
 

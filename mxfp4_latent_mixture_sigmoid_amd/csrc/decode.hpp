@@ -11,13 +11,15 @@ constexpr int DECODE_MAX_T = MOE_DECODE_MAX_T;   // the rows of a matrix-core ti
 constexpr int DECODE_MAX_E = 1024;
 constexpr int DECODE_MAX_WINDOW = 0x7FFF0000;    // bytes of a matrix, of h and of [zc | h_s]
 
-// One to a cache line: two counters; two flags, each in 64 places; then a counter for every expert of the list and one for every
-// 256 columns.
-enum { DECODE_TOP, DECODE_SUMS, DECODE_FLAGS };
-enum { DECODE_READY, DECODE_SUMS_DONE };
-constexpr int DECODE_COUNTER_WORDS = 32, DECODE_SHARED_LINES = DECODE_FLAGS + 2 * 64;
+// One to a cache line: counters (z has DECODE_ARMS and one more for their last arrivals); three flags, each in 64 places; then
+// a counter for every expert of the list and one for every 256 columns.
+constexpr int DECODE_ARMS = 16;
+enum { DECODE_ROUTER, DECODE_TOP, DECODE_CAT, DECODE_Z, DECODE_FLAGS = DECODE_Z + DECODE_ARMS + 1 };
+enum { DECODE_READY, DECODE_Z_DONE, DECODE_CAT_DONE };
+constexpr int DECODE_COUNTER_WORDS = 32, DECODE_SHARED_LINES = DECODE_FLAGS + 3 * 64;
 constexpr int DECODE_PATIENCE = 1000;        // times that a flag is asked for, about a microsecond each
 constexpr int DECODE_DOWN_COLUMNS = 256;     // of a workgroup in the down product
+constexpr int DECODE_ROUTER_PARTS = 4;       // workgroups that share 16 of the router's rows
 constexpr int DECODE_STAGE_WORDS = 1856;     // LDS of a wave for its activations
 
 struct DecodeArgs {
@@ -32,10 +34,10 @@ struct DecodeArgs {
     int64_t gateup_stride, down_stride;
     // workspace
     uint32_t *counters;              // decode_counter_lines of them
-    uint32_t *claims;                // [items] of the second kernel
+    uint32_t *claims;                // [items]
     int patience;
     float *partial;                  // [T K, Lt] y
-    float *logits;                   // [T, E]
+    float *logits;                   // [DECODE_ROUTER_PARTS, T, E]
     float *weights;                  // [T, K]
     int32_t *chosen;                 // [T, K] experts
     int32_t *list;                   // [most] distinct experts, ascending
@@ -47,6 +49,7 @@ struct DecodeArgs {
     int ldcat;
     uint16_t *h;                     // [T K, I]
     // outputs
+    float *logits_out;               // [T, E], or null
     int32_t *ids_out;                // [T, K], or null
     float *weights_out;              // [T, K], or null
     uint16_t *out;                   // [T, H] ([T, Lt] without latent projections)
@@ -61,16 +64,20 @@ __host__ __device__ inline bool decode_gate_few(const DecodeArgs &a)
 __host__ __device__ inline int decode_gate_items(const DecodeArgs &a) { return a.I / (decode_gate_few(a) ? 16 : 64); }   // of an expert
 __host__ __device__ inline int decode_groups(const DecodeArgs &a) { return (a.Lt + DECODE_DOWN_COLUMNS - 1) / DECODE_DOWN_COLUMNS; }
 
-// Work items of the second kernel, numbered kind after kind.
+// Work items, numbered kind after kind; a kind waits for earlier ones only.
 struct DecodeItems {
-    int top, gate, down, sums, out;
+    int router, latent, top, gate, shared, down, sums, out;
 };
 __host__ __device__ inline DecodeItems decode_items(const DecodeArgs &a)
 {
-    return {(a.T + 3) / 4, a.most * decode_gate_items(a), a.most * decode_groups(a), (a.T + 3) / 4 * decode_groups(a),
-            a.has_latent ? a.H / 16 : 0};
+    const int quads = (a.T + 3) / 4, groups = decode_groups(a);
+    return {(int)(a.n_router_rows / 16) * DECODE_ROUTER_PARTS, a.has_latent ? a.Lt / 16 : 0, quads, a.most * decode_gate_items(a), a.shared / 16,
+            a.most * groups, quads * groups, a.has_latent ? a.H / 16 : 0};
 }
-__host__ __device__ inline int decode_item_count(const DecodeItems &n) { return n.top + n.gate + n.down + n.sums + n.out; }
+__host__ __device__ inline int decode_item_count(const DecodeItems &n)
+{
+    return n.router + n.latent + n.top + n.gate + n.shared + n.down + n.sums + n.out;
+}
 
 // Arrivals of the list's expert r at its h; of the down items at the columns of group g.
 __host__ __device__ inline int decode_counter_lines(const DecodeArgs &a) { return DECODE_SHARED_LINES + a.most + decode_groups(a); }

@@ -32,8 +32,8 @@ def query(cfg, T):
 def test_sizes():
     up = lambda v: (v + 255) // 256 * 256          # noqa: E731
     st, size = query(config(), 5)
-    assert st == 0 and size == (up((2 + 2 * 64 + 20 + 1) * 32 * 4) + up((2 + 20 * (8 + 1) + 2 * 1 + 16) * 4) + up(20 * 256 * 4)
-                                + up(5 * 40 * 4) + 2 * up(5 * 4 * 4) + up(20 * 4) + up(20 * 16 * 2) + 2 * up(5 * 256 * 2)
+    assert st == 0 and size == (up((20 + 3 * 64 + 20 + 1) * 32 * 4) + up((4 * 3 + 36 + 2 * (1 + 1) + 20 * (8 + 1)) * 4) + up(20 * 256 * 4)
+                                + up(4 * 5 * 40 * 4) + 2 * up(5 * 4 * 4) + up(20 * 4) + up(20 * 16 * 2) + 2 * up(5 * 256 * 2)
                                 + up(5 * 320 * 2) + up(20 * 128 * 2))
     assert query(config(), 0)[0] == 0 and query(config(), abi.DECODE_MAX_T)[0] == 0
 
