@@ -41,34 +41,33 @@ namespace {
 
 constexpr int ROWS = DECODE_MAX_T, HALF = ROWS / 2;
 constexpr int REST_WAVES = 4, ROUTER_PARTS = DECODE_ROUTER_PARTS;
-constexpr int OUT_DEPTH = 24;
 constexpr int FLAGS = WAVE;                 // places of a flag
 constexpr int STAGE_WORDS = 1856;           // LDS of a wave for its activations, where they fit
-constexpr int LDS_WORDS = REST_WAVES * STAGE_WORDS + REST_WAVES * 512;   // of an item; four workgroups share a CU
+constexpr int LDS_WORDS = REST_WAVES * STAGE_WORDS + REST_WAVES * 512;   // of an item; three workgroups share a CU
 
-__device__ inline uint32_t *counter(const DecodeArgs &a, int i) { return a.counters + i * DECODE_COUNTER_WORDS; }
-__device__ inline uint32_t *flag(const DecodeArgs &a, int i, int place) { return counter(a, DECODE_FLAGS + i * FLAGS + place); }
-__device__ inline uint32_t ask(const uint32_t *at) { return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ uint32_t *counter(const DecodeArgs &a, int i) { return a.counters + i * DECODE_COUNTER_WORDS; }
+__device__ __forceinline__ uint32_t *flag(const DecodeArgs &a, int i, int place) { return counter(a, DECODE_FLAGS + i * FLAGS + place); }
+__device__ __forceinline__ uint32_t ask(const uint32_t *at) { return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
-__device__ inline int lane_id() { return threadIdx.x & (WAVE - 1); }
-__device__ inline int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE); }
+__device__ __forceinline__ int lane_id() { return threadIdx.x & (WAVE - 1); }
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE); }
 
 // Windows for loads and stores: those outside read zeros and write nothing, without touching memory. `go` = 0: an empty one.
 constexpr int OUTSIDE = DECODE_MAX_WINDOW;   // an offset past every window
-__device__ inline __amdgpu_buffer_rsrc_t window(const void *base, int64_t bytes, int go) { return flat_rsrc(base, go ? bytes : 0); }
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const void *base, int64_t bytes, int go) { return flat_rsrc(base, go ? bytes : 0); }
 template <int CPOL>
-__device__ inline u32x4_t fetch16(__amdgpu_buffer_rsrc_t w, int offset)
+__device__ __forceinline__ u32x4_t fetch16(__amdgpu_buffer_rsrc_t w, int offset)
 {
     return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(w, offset, 0, CPOL));
 }
 template <int CPOL>
-__device__ inline uint32_t fetch4(__amdgpu_buffer_rsrc_t w, int offset)
+__device__ __forceinline__ uint32_t fetch4(__amdgpu_buffer_rsrc_t w, int offset)
 {
     return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(w, offset, 0, CPOL);
 }
 
 // Lane l's four sums of a fragment are those of rows 4 (l / 16) .. +3 in column l % 16.
-__device__ inline void store_sums(float *red, f32x4_t v)
+__device__ __forceinline__ void store_sums(float *red, f32x4_t v)
 {
     const int lane = lane_id();
 #pragma unroll
@@ -78,7 +77,7 @@ __device__ inline void store_sums(float *red, f32x4_t v)
 
 // Sum of one element over the waves' fragments, in wave order.
 template <int WAVES>
-__device__ inline float total(const float *red, int stride, int at)
+__device__ __forceinline__ float total(const float *red, int stride, int at)
 {
     float v = 0.f;
 #pragma unroll
@@ -166,7 +165,7 @@ struct Bf16Part {
             return;
         }
         u32x4_t x[AHEAD];
-        auto operand = [&](int s, int slot) { x[slot] = get(min(r, T - 1), (s0 + min(s, n - 1)) * BF16_STEP + c * 8); };
+        auto operand = [&](int s, int slot) __attribute__((always_inline)) { x[slot] = get(min(r, T - 1), (s0 + min(s, n - 1)) * BF16_STEP + c * 8); };
 #pragma unroll
         for (int i = 0; i < AHEAD; i++)
             operand(i, i);
@@ -192,7 +191,7 @@ struct Bf16Part {
 // Until the flag or counter at `at` is at least `least`: its value, or -1 when patience runs out (HELP: never). `v` is what it
 // was before. One thread asks; what follows in any thread is after the answer.
 template <bool HELP>
-__device__ inline int wait_for(const DecodeArgs &a, const uint32_t *at, uint32_t least, uint32_t *sh, uint32_t v = 0u)
+__device__ __forceinline__ int wait_for(const DecodeArgs &a, const uint32_t *at, uint32_t least, uint32_t *sh, uint32_t v = 0u)
 {
     if (threadIdx.x == 0) {
         int left = a.patience;
@@ -214,21 +213,21 @@ struct Seen {   // two flags as they were a while ago
 };
 // Until the experts are known: how many, or -1.
 template <bool HELP>
-__device__ inline int wait_ready(const DecodeArgs &a, const Seen &seen, uint32_t *sh)
+__device__ __forceinline__ int wait_ready(const DecodeArgs &a, const Seen &seen, uint32_t *sh)
 {
     const int v = wait_for<HELP>(a, flag(a, DECODE_READY, blockIdx.x % FLAGS), 1u, sh, seen.ready);
     return v < 0 ? v : v - 1;
 }
 // Until z is there.
 template <bool HELP>
-__device__ inline bool wait_z(const DecodeArgs &a, const Seen &seen, uint32_t *sh)
+__device__ __forceinline__ bool wait_z(const DecodeArgs &a, const Seen &seen, uint32_t *sh)
 {
     return !a.has_latent || wait_for<HELP>(a, flag(a, DECODE_Z_DONE, blockIdx.x % FLAGS), 1u, sh, seen.z) >= 0;
 }
 
 // Whether item `i` is this workgroup's now.
 template <bool HELP>
-__device__ inline bool claim(const DecodeArgs &a, int i, uint32_t *sh)
+__device__ __forceinline__ bool claim(const DecodeArgs &a, int i, uint32_t *sh)
 {
     if (threadIdx.x == 0) {
         uint32_t *at = a.claims + i;
@@ -241,20 +240,20 @@ __device__ inline bool claim(const DecodeArgs &a, int i, uint32_t *sh)
     return mine;
 }
 
-__device__ inline void set_flag(const DecodeArgs &a, int i, uint32_t v)   // by a wave
+__device__ __forceinline__ void set_flag(const DecodeArgs &a, int i, uint32_t v)   // by a wave
 {
     __hip_atomic_store(flag(a, i, lane_id()), v + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // Every wave's stores have completed.
-__device__ inline void stores_done()
+__device__ __forceinline__ void stores_done()
 {
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     asm volatile("" ::: "memory");
     __syncthreads();
 }
 
-__device__ inline bool last_at(uint32_t *at, int all)   // by a wave
+__device__ __forceinline__ bool last_at(uint32_t *at, int all)   // by a wave
 {
     uint32_t before = 0u;
     if (lane_id() == 0)
@@ -263,7 +262,7 @@ __device__ inline bool last_at(uint32_t *at, int all)   // by a wave
 }
 
 // Counts this workgroup after its stores.
-__device__ inline void arrive(uint32_t *at)
+__device__ __forceinline__ void arrive(uint32_t *at)
 {
     stores_done();
     if (threadIdx.x == 0)
@@ -271,7 +270,7 @@ __device__ inline void arrive(uint32_t *at)
 }
 
 // ... after its part of [zc | h_s].
-__device__ inline void arrive_out(const DecodeArgs &a)
+__device__ __forceinline__ void arrive_out(const DecodeArgs &a)
 {
     stores_done();
     const DecodeItems n = decode_items(a);
@@ -282,16 +281,16 @@ __device__ inline void arrive_out(const DecodeArgs &a)
 // 16 columns (NB = 2: two such blocks) of a BF16 product over x; the waves share the K axis and leave their sums in LDS. The
 // weights are asked for before the item is claimed. False when another workgroup has it.
 template <int NB, bool HELP>
-__device__ inline bool front_product(const DecodeArgs &a, const uint8_t *w, int64_t rows, int block, uint32_t *lds, uint32_t *sh, int part_of_k = 0, int parts = 1)
+__device__ __forceinline__ bool front_product(const DecodeArgs &a, const uint8_t *w, int64_t rows, int block, uint32_t *lds, uint32_t *sh, int part_of_k = 0, int parts = 1)
 {
     const int wv = wave_id();
     const auto x = flat_rsrc(a.x, (int64_t)a.T * a.Hin * 2);
     f32x4_t acc[NB] = {};
-    auto run = [&](auto part) {
+    auto run = [&](auto part) __attribute__((always_inline)) {
         part.start(w, rows, a.Hin, block, part_of_k * REST_WAVES + wv, parts * REST_WAVES);
         if (!HELP && !claim<false>(a, blockIdx.x, sh))
             return false;
-        part.finish(a.T, lds + wv * STAGE_WORDS, acc, [&](int r, int k) { return fetch16<0>(x, (r * a.Hin + k) * 2); });
+        part.finish(a.T, lds + wv * STAGE_WORDS, acc, [&](int r, int k) __attribute__((always_inline)) { return fetch16<0>(x, (r * a.Hin + k) * 2); });
         return true;
     };
     using Staged = Bf16Part<NB, 16 / NB, 4, true>;
@@ -309,7 +308,7 @@ __device__ inline bool front_product(const DecodeArgs &a, const uint8_t *w, int6
 // 16 experts' logits over one of ROUTER_PARTS parts of x. (All front items run at once and share the memory's rate: so the
 // router's are short, and the top-K is done before z.)
 template <bool HELP>
-__device__ inline void router_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
+__device__ __forceinline__ void router_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
 {
     const int part = item % ROUTER_PARTS, block = item / ROUTER_PARTS;
     if (!front_product<1, HELP>(a, a.w_router, a.n_router_rows, block, lds, sh, part, ROUTER_PARTS))
@@ -323,7 +322,7 @@ __device__ inline void router_item(const DecodeArgs &a, int item, uint32_t *lds,
 
 // 16 latent columns.
 template <bool HELP>
-__device__ inline void latent_item(const DecodeArgs &a, int item, int items, uint32_t *lds, uint32_t *sh)
+__device__ __forceinline__ void latent_item(const DecodeArgs &a, int item, int items, uint32_t *lds, uint32_t *sh)
 {
     if (!front_product<1, HELP>(a, a.w_latent, a.n_latent_rows, item, lds, sh))
         return;
@@ -348,7 +347,7 @@ __device__ inline void latent_item(const DecodeArgs &a, int item, int items, uin
 
 // 16 channels of the shared experts.
 template <bool HELP>
-__device__ inline void shared_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
+__device__ __forceinline__ void shared_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
 {
     if (!front_product<2, HELP>(a, a.w_shared, a.n_shared_rows, (int)(a.shared_at / 16) + 2 * item, lds, sh))
         return;
@@ -366,7 +365,7 @@ __device__ inline void shared_item(const DecodeArgs &a, int item, uint32_t *lds,
 
 // select_best of select.hpp in little code, for token t, from its logits' parts in memory. No key of an expert is 0, which stands for none (only a NaN with every bit set
 // would have it), so that ids are always in range. `go` = 0: keys that are all different in place of the logits.
-__device__ inline void select_short(const DecodeArgs &a, int t, int go, uint32_t *words, uint64_t *scratch, int *id, float *weight)
+__device__ __forceinline__ void select_short(const DecodeArgs &a, int t, int go, uint32_t *words, uint64_t *scratch, int *id, float *weight)
 {
     constexpr int QUADS = DECODE_MAX_E / (4 * WAVE);
     const int lane = lane_id(), E = a.E, K = a.K;
@@ -464,9 +463,8 @@ __device__ inline void select_short(const DecodeArgs &a, int t, int go, uint32_t
 // The top-K of four tokens, one to a wave; the last of these items to arrive makes the list: the distinct experts in ascending
 // order, and for each the pairs of its tokens.
 template <bool HELP>
-__device__ inline bool top_item(const DecodeArgs &a, int item, int items, uint32_t *words, uint32_t *sh)
+__device__ __forceinline__ bool top_item(const DecodeArgs &a, int item, int items, uint32_t *words, uint32_t *sh)
 {
-    __shared__ uint64_t scratch[REST_WAVES][WAVE];
     const int lane = lane_id(), wv = wave_id();
     const int T = a.T, K = a.K, E = a.E, P = T * K;
     constexpr int NTHR = WAVE * REST_WAVES;
@@ -474,6 +472,7 @@ __device__ inline bool top_item(const DecodeArgs &a, int item, int items, uint32
     // after them the list's pairs, two to a word
     int *ranks = reinterpret_cast<int *>(words), *chosen = ranks + DECODE_MAX_E, *scan = chosen + ROWS * 32;
     uint32_t *table = words + DECODE_MAX_E + ROWS * 32 + 16, *mine = table + wv * DECODE_MAX_E;
+    uint64_t *scratch = reinterpret_cast<uint64_t *>(table + REST_WAVES * DECODE_MAX_E) + wv * WAVE;
     const int t = item * REST_WAVES + wv;
 #pragma unroll 1
     for (int go = HELP ? 1 : 0; go < 2; go++) {
@@ -488,7 +487,7 @@ __device__ inline bool top_item(const DecodeArgs &a, int item, int items, uint32
         if (t < T) {
             int id;
             float w;
-            select_short(a, t, go, mine, scratch[wv], &id, &w);
+            select_short(a, t, go, mine, scratch, &id, &w);
             if (lane < K) {
                 const int p = t * K + lane;
                 chosen[p] = id;
@@ -546,7 +545,7 @@ __device__ inline bool top_item(const DecodeArgs &a, int item, int items, uint32
 }
 
 // One MX block times a step's activations.
-__device__ inline f32x4_t mx_step(u32x4_t codes, uint32_t scales, const u32x4_t (&x)[4], f32x4_t acc)
+__device__ __forceinline__ f32x4_t mx_step(u32x4_t codes, uint32_t scales, const u32x4_t (&x)[4], f32x4_t acc)
 {
 #pragma unroll
     for (int j = 0; j < 4; j++)
@@ -558,7 +557,7 @@ __device__ inline f32x4_t mx_step(u32x4_t codes, uint32_t scales, const u32x4_t 
 // share the K axis; each wave's part of z (and of its remainders, rows 8 and 9 of the operand) goes through LDS. The first
 // weights are asked for before z is there.
 template <bool HELP>
-__device__ inline bool gate_few(const DecodeArgs &a, int item, const Seen &seen, uint32_t *lds, uint32_t *sh)
+__device__ __forceinline__ bool gate_few(const DecodeArgs &a, int item, const Seen &seen, uint32_t *lds, uint32_t *sh)
 {
     const int lane = lane_id(), wv = wave_id(), t = threadIdx.x, T = a.T;
     const int pairs16 = a.I / 16, r = item / pairs16, cp = item % pairs16;
@@ -584,7 +583,7 @@ __device__ inline bool gate_few(const DecodeArgs &a, int item, const Seen &seen,
                               2 * (int64_t)steps * MX_BLOCK_BYTES, go);
         u32x4_t codes[BATCH][2];
         uint32_t scales[BATCH][2];
-        auto load = [&](int slot, int s) {
+        auto load = [&](int slot, int s) __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 const int off = s < n ? (j * steps + s0 + s) * MX_BLOCK_BYTES : OUTSIDE;
@@ -600,21 +599,20 @@ __device__ inline bool gate_few(const DecodeArgs &a, int item, const Seen &seen,
             return false;
         const auto z0 = window(a.z, (int64_t)T * a.Lt * 2, go), z1 = window(a.has_latent ? a.z_rest : a.z, (int64_t)T * a.Lt * 2, go);
 #pragma unroll 1
-        for (int i0 = 0; i0 < 2 * T * chunks; i0 += 4 * WAVE) {   // z of the tokens, then the remainders
-            u32x4_t v[4];
-            int to[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int p = min(i0 + i * WAVE + lane, 2 * T * chunks - 1), row = p / chunks, j = p % chunks;
-                const int off = ((row >= T ? row - T : row) * a.Lt + s0 * MX_STEP + j * 8) * 2;
-                const u32x4_t v0 = fetch16<CPOL_SC1>(z0, row < T ? off : OUTSIDE), v1 = fetch16<CPOL_SC1>(z1, row < T ? OUTSIDE : off);
-                v[i] = v0 | v1;
-                to[i] = row * pitch + j * 4;
+        for (int row = 0; row < T; row++)
+#pragma unroll 1
+            for (int j = lane; j < chunks; j += 2 * WAVE) {
+                const int off = (row * a.Lt + s0 * MX_STEP + j * 8) * 2, off2 = j + WAVE < chunks ? off + WAVE * 16 : OUTSIDE;
+                uint32_t *to = stage + row * pitch + j * 4;
+                const u32x4_t v0 = fetch16<CPOL_SC1>(z0, off), v1 = fetch16<CPOL_SC1>(z0, off2);
+                const u32x4_t v2 = fetch16<CPOL_SC1>(z1, off), v3 = fetch16<CPOL_SC1>(z1, off2);
+                *reinterpret_cast<u32x4_t *>(to) = v0;
+                *reinterpret_cast<u32x4_t *>(to + T * pitch) = v2;
+                if (j + WAVE < chunks) {
+                    *reinterpret_cast<u32x4_t *>(to + WAVE * 4) = v1;
+                    *reinterpret_cast<u32x4_t *>(to + WAVE * 4 + T * pitch) = v3;
+                }
             }
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                *reinterpret_cast<u32x4_t *>(stage + to[i]) = v[i];
-        }
         f32x4_t acc[2] = {};
 #pragma unroll 1
         for (int s = 0; s < n; s += BATCH)
@@ -657,13 +655,13 @@ __device__ inline bool gate_few(const DecodeArgs &a, int item, const Seen &seen,
 }
 
 // ... with several: four such pairs per workgroup, one to a wave, each over all of K, so that z goes through LDS once for
-// them all, a chunk of STEPS steps at a time; a chunk's weights and z are loaded while the one before it is multiplied. Up to 8 tokens: one operand, whose rows
+// them all, a chunk of STEPS steps at a time, each loaded a chunk ahead; weights come AHEAD steps ahead. Up to 8 tokens: one operand, whose rows
 // 8 .. 15 are the remainders of rows 0 .. 7; more: two operands (PARTS). K is summed in four quarters, as above, so that a
 // token's h is the same bits whatever tokens come with it.
 template <int PARTS, bool HELP>
-__device__ inline bool gate_many(const DecodeArgs &a, int item, const Seen &seen, uint32_t *lds, uint32_t *sh)
+__device__ __forceinline__ bool gate_many(const DecodeArgs &a, int item, const Seen &seen, uint32_t *lds, uint32_t *sh)
 {
-    constexpr int STEPS = 4 / PARTS, PITCH = STEPS * MX_STEP / 2 + 4, NTHR = WAVE * REST_WAVES;   // words of a row in LDS
+    constexpr int AHEAD = 4, STEPS = AHEAD / PARTS, PITCH = STEPS * MX_STEP / 2 + 4, NTHR = WAVE * REST_WAVES;   // words of a row in LDS
     constexpr int PIECES = STEPS * 16 * 16 * PARTS / NTHR;   // 16-byte pieces of a chunk per thread
     static_assert(2 * ROWS * PARTS * PITCH <= LDS_WORDS, "room for two chunks");
     const int lane = lane_id(), wv = wave_id(), t = threadIdx.x;
@@ -673,7 +671,7 @@ __device__ inline bool gate_many(const DecodeArgs &a, int item, const Seen &seen
     // Rows past the tokens are zeros.
     const auto z0 = flat_rsrc(a.z, (int64_t)a.T * a.Lt * 2), z1 = flat_rsrc(a.has_latent ? a.z_rest : a.z, (int64_t)a.T * a.Lt * 2);
     u32x4_t zs[PIECES];
-    auto fetch = [&](int s) {
+    auto fetch = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < PIECES; i++) {
             const int p = i * NTHR + t, row = p / (STEPS * 16), c = p % (STEPS * 16);
@@ -690,21 +688,19 @@ __device__ inline bool gate_many(const DecodeArgs &a, int item, const Seen &seen
     const uint32_t pair01 = load4_sc1(pairs, (r * ROWS + 4 * (lane >> 4)) * 2), pair23 = load4_sc1(pairs, (r * ROWS + 4 * (lane >> 4)) * 2 + 4);
     const auto w = window(a.gateup + e * a.gateup_stride + (int64_t)2 * cp * steps * MX_BLOCK_BYTES,
                           2 * (int64_t)steps * MX_BLOCK_BYTES, 1);
-    struct Chunk {
-        u32x4_t codes[STEPS][2];
-        uint32_t scales[STEPS][2];
-    } now, next;
-    auto load = [&](int s, Chunk &q) {
+    u32x4_t codes[AHEAD][2];
+    uint32_t scales[AHEAD][2];
+    auto load = [&](int slot, int s) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < STEPS; i++)
-#pragma unroll
-            for (int j = 0; j < 2; j++) {
-                const int off = s + i < steps ? (j * steps + s + i) * MX_BLOCK_BYTES : OUTSIDE;
-                q.codes[i][j] = fetch16<CPOL_NT>(w, off + lane * 16);
-                q.scales[i][j] = fetch4<CPOL_NT>(w, off + MX_CODE_BYTES + 4 * (lane & 15));
-            }
+        for (int j = 0; j < 2; j++) {
+            const int off = s < steps ? (j * steps + s) * MX_BLOCK_BYTES : OUTSIDE;
+            codes[slot][j] = fetch16<CPOL_NT>(w, off + lane * 16);
+            scales[slot][j] = fetch4<CPOL_NT>(w, off + MX_CODE_BYTES + 4 * (lane & 15));
+        }
     };
-    load(0, now);
+#pragma unroll
+    for (int i = 0; i < AHEAD; i++)
+        load(i, i);
     asm volatile("" ::: "memory");
     if (!wait_z<HELP>(a, seen, sh))
         return false;
@@ -715,49 +711,50 @@ __device__ inline bool gate_many(const DecodeArgs &a, int item, const Seen &seen
         quarter++;
     int half = 0;   // which half of LDS: a wave that writes it has seen every wave past the chunk before the last
 #pragma unroll 1
-    for (int s = 0; s < steps; s += STEPS, half ^= 1) {
-        uint32_t *chunk = lds + half * ROWS * PARTS * PITCH;
-        const uint32_t *mine = chunk + (lane & 15) * PITCH + (lane >> 4) * 4;
+    for (int s = 0; s < steps; s += AHEAD)
 #pragma unroll
-        for (int i = 0; i < PIECES; i++) {
-            const int p = i * NTHR + t;
-            *reinterpret_cast<u32x4_t *>(chunk + p / (STEPS * 16) * PITCH + p % (STEPS * 16) * 4) = zs[i];
-        }
-        fetch(s + STEPS);
-        load(s + STEPS, next);
-        asm volatile("" ::: "memory");
-        __syncthreads();
+        for (int c = 0; c < PARTS; c++, half ^= 1) {
+            uint32_t *chunk = lds + half * ROWS * PARTS * PITCH;
+            const uint32_t *mine = chunk + (lane & 15) * PITCH + (lane >> 4) * 4;
 #pragma unroll
-        for (int i = 0; i < STEPS; i++) {   // steps past the end multiply zeros
-#pragma unroll
-            for (int p = 0; p < PARTS; p++) {
-                u32x4_t x[4];
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    x[j] = *reinterpret_cast<const u32x4_t *>(mine + p * ROWS * PITCH + i * (MX_STEP / 2) + j * 16);
-#pragma unroll
-                for (int j = 0; j < 2; j++)
-                    acc[p][j] = mx_step(now.codes[i][j], now.scales[i][j], x, acc[p][j]);
+            for (int i = 0; i < PIECES; i++) {
+                const int p = i * NTHR + t;
+                *reinterpret_cast<u32x4_t *>(chunk + p / (STEPS * 16) * PITCH + p % (STEPS * 16) * 4) = zs[i];
             }
-            if (s + i + 1 == steps * quarter / REST_WAVES) {
+            fetch(s + (c + 1) * STEPS);
+            __syncthreads();
 #pragma unroll
-                for (int j = 0; j < 2; j++) {
+            for (int i = 0; i < STEPS; i++) {   // steps past the end multiply zeros
+                const int slot = c * STEPS + i;
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const float rest = PARTS == 1 ? __shfl_xor(acc[0][j][k], 32) : acc[PARTS - 1][j][k];
-                        sum[j][k] += a.has_latent ? acc[0][j][k] + rest : acc[0][j][k];
-                    }
+                for (int p = 0; p < PARTS; p++) {
+                    u32x4_t x[4];
 #pragma unroll
-                    for (int p = 0; p < PARTS; p++)
-                        acc[p][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                    for (int j = 0; j < 4; j++)
+                        x[j] = *reinterpret_cast<const u32x4_t *>(mine + p * ROWS * PITCH + i * (MX_STEP / 2) + j * 16);
+#pragma unroll
+                    for (int j = 0; j < 2; j++)
+                        acc[p][j] = mx_step(codes[slot][j], scales[slot][j], x, acc[p][j]);
                 }
-                while (steps * quarter / REST_WAVES == s + i + 1)
-                    quarter++;
+                if (s + slot + 1 == steps * quarter / REST_WAVES) {
+#pragma unroll
+                    for (int j = 0; j < 2; j++) {
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const float rest = PARTS == 1 ? __shfl_xor(acc[0][j][k], 32) : acc[PARTS - 1][j][k];
+                            sum[j][k] += a.has_latent ? acc[0][j][k] + rest : acc[0][j][k];
+                        }
+#pragma unroll
+                        for (int p = 0; p < PARTS; p++)
+                            acc[p][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                    }
+                    while (steps * quarter / REST_WAVES == s + slot + 1)
+                        quarter++;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                load(slot, s + slot + AHEAD);
             }
-            __builtin_amdgcn_sched_barrier(0);
         }
-        now = next;
-    }
     // two channels to a word; rows of the upper half of the lanes are remainders where PARTS = 1
     const auto h = flat_rsrc(a.h, (int64_t)a.T * a.K * a.I * 2);
 #pragma unroll
@@ -771,39 +768,50 @@ __device__ inline bool gate_many(const DecodeArgs &a, int item, const Seen &seen
     return true;
 }
 
-// 256 latent columns of one expert's down product, 64 to a wave: y of its tokens' pairs, to memory. The weights of AHEAD
-// steps are loaded before h is known, which takes that expert's gate items only. Each column of a pair is one chain of
-// sums over K, the same whatever tokens come with it.
+// 256 latent columns of one expert's down product, 64 to a wave: y of its tokens' pairs, to memory. The weights of STEPS steps
+// are loaded before h is known, which takes that expert's gate items only; h goes through LDS, STEPS steps at a time. Each
+// column of a pair is one chain of sums over K, the same whatever tokens come with it.
 template <bool HELP>
-__device__ inline bool down_item(const DecodeArgs &a, int item, const Seen &seen, uint32_t *sh)
+__device__ __forceinline__ bool down_item(const DecodeArgs &a, int item, const Seen &seen, uint32_t *lds, uint32_t *sh)
 {
-    constexpr int AHEAD = 3, NB = DECODE_DOWN_COLUMNS / (16 * REST_WAVES);
-    const int lane = lane_id(), groups = decode_groups(a), r = item / groups, g = item % groups;
+    constexpr int STEPS = 3, NB = DECODE_DOWN_COLUMNS / (16 * REST_WAVES), NTHR = WAVE * REST_WAVES;
+    constexpr int PITCH = STEPS * MX_STEP / 2 + 4, PER_ROW = STEPS * MX_STEP / 8, PIECES = ROWS * PER_ROW / NTHR;
+    static_assert(2 * ROWS * PITCH + ROWS / 2 <= LDS_WORDS && PIECES * NTHR == ROWS * PER_ROW, "room for two chunks and the pairs; pieces");
+    const int lane = lane_id(), t = threadIdx.x, groups = decode_groups(a), r = item / groups, g = item % groups;
     const int steps = a.I / MX_STEP, P = a.T * a.K, col = (g * REST_WAVES + wave_id()) * NB, blocks = min(NB, a.Lt / 16 - col);
 #pragma unroll 1
     for (int go = HELP ? 1 : 0; go < 2; go++) {
-        int e = 0, x_row = OUTSIDE;
-        uint32_t pair01 = ~0u, pair23 = ~0u, arrived = 0u;
+        int e = 0, from[PIECES];   // this thread's pieces of h: the pair's row and the column, in bytes
+#pragma unroll
+        for (int i = 0; i < PIECES; i++)
+            from[i] = OUTSIDE;
+        uint32_t arrived = 0u;
         if (go) {
             const int experts = wait_ready<HELP>(a, seen, sh);
             if (r >= experts)
                 return experts >= 0;
             const auto pairs = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
-            const uint32_t two = load4_sc1(pairs, (r * ROWS + (lane & 14)) * 2);
-            pair01 = load4_sc1(pairs, (r * ROWS + 4 * (lane >> 4)) * 2);   // of the sums' rows
-            pair23 = load4_sc1(pairs, (r * ROWS + 4 * (lane >> 4)) * 2 + 4);
+#pragma unroll
+            for (int i = 0; i < PIECES; i++)
+                from[i] = (int)load4_sc1(pairs, (r * ROWS + (i * NTHR + t) / PER_ROW / 2 * 2) * 2);
+            const uint32_t two = load4_sc1(pairs, (r * ROWS + t % (ROWS / 2) * 2) * 2);
             e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
             arrived = ask(decode_gates(a, r));
-            const int pair = (int16_t)(lane & 1 ? two >> 16 : two);
-            x_row = pair >= 0 ? (pair * a.I + 8 * (lane >> 4)) * 2 : OUTSIDE;
+            if (t < ROWS / 2)
+                lds[2 * ROWS * PITCH + t] = two;
+#pragma unroll
+            for (int i = 0; i < PIECES; i++) {
+                const int pair = (int16_t)((i * NTHR + t) / PER_ROW % 2 ? from[i] >> 16 : from[i]);
+                from[i] = pair >= 0 ? (pair * a.I + (i * NTHR + t) % PER_ROW * 8) * 2 : OUTSIDE;
+            }
         }
         const int n = go ? steps : 1;
         const auto w = window(a.down + e * a.down_stride + (int64_t)col * steps * MX_BLOCK_BYTES,
                               (int64_t)steps * MX_BLOCK_BYTES * blocks, go && blocks > 0);
         const auto h = window(a.h, (int64_t)P * a.I * 2, go), y = window(a.partial, (int64_t)P * a.Lt * 4, go);
-        u32x4_t codes[AHEAD][NB], x[AHEAD][4];
-        uint32_t scales[AHEAD][NB];
-        auto load = [&](int slot, int s) {
+        u32x4_t codes[STEPS][NB], hs[PIECES];
+        uint32_t scales[STEPS][NB];
+        auto load = [&](int slot, int s) __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < NB; j++) {
                 const int off = s < n ? (j * steps + s) * MX_BLOCK_BYTES : OUTSIDE;
@@ -811,39 +819,51 @@ __device__ inline bool down_item(const DecodeArgs &a, int item, const Seen &seen
                 scales[slot][j] = fetch4<CPOL_NT>(w, off + MX_CODE_BYTES + 4 * (lane & 15));
             }
         };
-        auto load_x = [&](int slot, int s) {
+        auto fetch = [&](int s) __attribute__((always_inline)) {   // zeros past the row's end
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-                x[slot][j] = fetch16<CPOL_SC1>(h, s < n && x_row != OUTSIDE ? x_row + (s * MX_STEP + j * 32) * 2 : OUTSIDE);
+            for (int i = 0; i < PIECES; i++)
+                hs[i] = fetch16<CPOL_SC1>(h, from[i] != OUTSIDE && s * MX_STEP + (i * NTHR + t) % PER_ROW * 8 < n * MX_STEP
+                                                 ? from[i] + s * MX_STEP * 2 : OUTSIDE);
         };
 #pragma unroll
-        for (int i = 0; i < AHEAD; i++)
+        for (int i = 0; i < STEPS; i++)
             load(i, i);
         asm volatile("" ::: "memory");
         if (go && wait_for<HELP>(a, decode_gates(a, r), (uint32_t)decode_gate_items(a), sh, arrived) < 0)
             return false;
-#pragma unroll
-        for (int i = 0; i < AHEAD; i++)
-            load_x(i, i);
+        fetch(0);
         f32x4_t acc[NB] = {};
+        int half = 0;   // which half of LDS, as in gate_many
 #pragma unroll 1
-        for (int s = 0; s < n; s += AHEAD)
+        for (int s = 0; s < n; s += STEPS, half ^= 1) {
+            uint32_t *chunk = lds + half * ROWS * PITCH;
+            const uint32_t *mine = chunk + (lane & 15) * PITCH + (lane >> 4) * 4;
 #pragma unroll
-            for (int i = 0; i < AHEAD; i++) {   // steps past the end multiply zeros
+            for (int i = 0; i < PIECES; i++)
+                *reinterpret_cast<u32x4_t *>(chunk + (i * NTHR + t) / PER_ROW * PITCH + (i * NTHR + t) % PER_ROW * 4) = hs[i];
+            fetch(s + STEPS);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < STEPS; i++) {   // steps past the end multiply zeros
+                u32x4_t x[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    x[j] = *reinterpret_cast<const u32x4_t *>(mine + i * (MX_STEP / 2) + j * 16);
 #pragma unroll
                 for (int j = 0; j < NB; j++)
-                    acc[j] = mx_step(codes[i][j], scales[i][j], x[i], acc[j]);
+                    acc[j] = mx_step(codes[i][j], scales[i][j], x, acc[j]);
                 __builtin_amdgcn_sched_barrier(0);
-                load(i, s + i + AHEAD);
-                load_x(i, s + i + AHEAD);
+                load(i, s + i + STEPS);
             }
+        }
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-            const int pair = (int16_t)((k < 2 ? pair01 : pair23) >> (16 * (k % 2)));
+            const int pair = reinterpret_cast<const int16_t *>(lds + 2 * ROWS * PITCH)[4 * (lane >> 4) + k];
 #pragma unroll
             for (int j = 0; j < NB; j++)
-                store4_sc1(y, pair >= 0 && j < blocks ? (pair * a.Lt + (col + j) * 16 + (lane & 15)) * 4 : OUTSIDE, __float_as_uint(acc[j][k]));
+                store4_sc1(y, go && pair >= 0 && pair < P && j < blocks ? (pair * a.Lt + (col + j) * 16 + (lane & 15)) * 4 : OUTSIDE, __float_as_uint(acc[j][k]));
         }
+        __syncthreads();   // LDS is free for the next pass
     }
     arrive(decode_columns(a, g));
     return true;
@@ -851,7 +871,7 @@ __device__ inline bool down_item(const DecodeArgs &a, int item, const Seen &seen
 
 // The weighted sum of the experts' y, in slot order: 256 latent columns of four tokens.
 template <bool HELP>
-__device__ inline bool sum_item(const DecodeArgs &a, int item, const Seen &seen, uint32_t *sh)
+__device__ __forceinline__ bool sum_item(const DecodeArgs &a, int item, const Seen &seen, uint32_t *sh)
 {
     constexpr int SLOTS = 8;   // loaded at a time
     const int groups = decode_groups(a), g = item % groups, K = a.K, P = a.T * K;
@@ -894,12 +914,12 @@ __device__ inline bool sum_item(const DecodeArgs &a, int item, const Seen &seen,
 }
 
 template <bool HELP>
-__device__ inline bool out_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
+__device__ __forceinline__ bool out_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
 {
     const int wv = wave_id(), t = threadIdx.x, row = t / 8, c = t % 8 * 2;
     float *red = reinterpret_cast<float *>(lds + REST_WAVES * STAGE_WORDS);
     const auto out = flat_rsrc(a.out, (int64_t)a.T * a.H * 2);
-    auto run = [&](auto part) {
+    auto run = [&](auto part) __attribute__((always_inline)) {
 #pragma unroll 1
         for (int go = !HELP && a.T <= 2 ? 0 : 1; go < 2; go++) {
             part.start(a.w_out, a.H, a.ldcat, item, wv, REST_WAVES, go);
@@ -908,7 +928,7 @@ __device__ inline bool out_item(const DecodeArgs &a, int item, uint32_t *lds, ui
             const auto acat = window(a.acat, (int64_t)a.T * a.ldcat * 2, go);
             f32x4_t acc[1] = {};
             part.finish(a.T, lds + wv * STAGE_WORDS, acc,
-                        [&](int r, int k) { return fetch16<CPOL_SC1>(acat, (r * a.ldcat + k) * 2); });
+                        [&](int r, int k) __attribute__((always_inline)) { return fetch16<CPOL_SC1>(acat, (r * a.ldcat + k) * 2); });
             store_sums(red + wv * 256, acc[0]);
             __syncthreads();
             if (row < a.T && row < ROWS)
@@ -919,54 +939,62 @@ __device__ inline bool out_item(const DecodeArgs &a, int item, uint32_t *lds, ui
         }
         return true;
     };
-    using Staged = Bf16Part<1, OUT_DEPTH, 4, true>;   // all of a wave's weights at the widths of a TP8 share, and some more
+    using Staged = Bf16Part<1, 16, 4, true>;
     if (Staged::fits(a.T, a.ldcat, REST_WAVES))
         return run(Staged());
-    return run(Bf16Part<1, OUT_DEPTH, 8, false>());
+    return run(Bf16Part<1, 16, 8, false>());
+}
+
+// The kernel's arguments, read from memory again: they do not fit the scalar registers all at once.
+__device__ __forceinline__ const DecodeArgs &arguments()
+{
+    auto *at = (const __attribute__((address_space(4))) DecodeArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(at));
+    return *(const DecodeArgs *)at;
 }
 
 // Item i, as numbered by decode_items. False when patience ran out before anything was handed on (HELP: never).
 template <bool FEW, bool HELP>
-__device__ inline bool do_item(const DecodeArgs &a, const DecodeItems &n, int i, const Seen &seen, uint32_t *lds, uint32_t *sh)
+__device__ __forceinline__ bool do_item(const DecodeItems &n, int i, const Seen &seen, uint32_t *lds, uint32_t *sh)
 {
     if (i < n.router) {
-        router_item<HELP>(a, i, lds, sh);
+        router_item<HELP>(arguments(), i, lds, sh);
         return true;
     }
     i -= n.router;
     if (i < n.latent) {
-        latent_item<HELP>(a, i, n.latent, lds, sh);
+        latent_item<HELP>(arguments(), i, n.latent, lds, sh);
         return true;
     }
     i -= n.latent;
     if (i < n.top)
-        return top_item<HELP>(a, i, n.top, lds, sh);
+        return top_item<HELP>(arguments(), i, n.top, lds, sh);
     i -= n.top;
     if (i < n.gate) {
         if constexpr (FEW)
-            if (decode_gate_few(a))
-                return gate_few<HELP>(a, i, seen, lds, sh);
-        return gate_many<FEW ? 1 : 2, HELP>(a, i, seen, lds, sh);
+            if (decode_gate_few(arguments()))
+                return gate_few<HELP>(arguments(), i, seen, lds, sh);
+        return gate_many<FEW ? 1 : 2, HELP>(arguments(), i, seen, lds, sh);
     }
     i -= n.gate;
     if (i < n.shared) {
-        shared_item<HELP>(a, i, lds, sh);
+        shared_item<HELP>(arguments(), i, lds, sh);
         return true;
     }
     i -= n.shared;
     if (i < n.down)
-        return down_item<HELP>(a, i, seen, sh);
+        return down_item<HELP>(arguments(), i, seen, lds, sh);
     i -= n.down;
     if (i < n.sums)
-        return sum_item<HELP>(a, i, seen, sh);
-    return out_item<HELP>(a, i - n.sums, lds, sh);
+        return sum_item<HELP>(arguments(), i, seen, sh);
+    return out_item<HELP>(arguments(), i - n.sums, lds, sh);
 }
 
 template <bool FEW>
 __global__ __launch_bounds__(WAVE *REST_WAVES, 3) void decode_kernel(const DecodeArgs a)
 {
     constexpr int TOP = DECODE_MAX_E + ROWS * 32 + 16, MOST = ROWS * 32;   // MOST: pairs, and distinct experts
-    static_assert(TOP + REST_WAVES * DECODE_MAX_E <= LDS_WORDS && TOP + MOST * (ROWS / 2) <= LDS_WORDS, "room for the list");
+    static_assert(TOP % 2 == 0 && TOP + REST_WAVES * (DECODE_MAX_E + 2 * WAVE) <= LDS_WORDS && TOP + MOST * (ROWS / 2) <= LDS_WORDS, "room for the list");
     static_assert(STAGE_WORDS == DECODE_STAGE_WORDS && REST_WAVES == 4, "what decode.hpp says");
     __shared__ alignas(16) uint32_t lds[LDS_WORDS];
     __shared__ uint32_t sh;
@@ -975,7 +1003,7 @@ __global__ __launch_bounds__(WAVE *REST_WAVES, 3) void decode_kernel(const Decod
     const bool late = item < n.router + n.latent ||   // claimed in front_product
                       (item >= n.router + n.latent + n.top + n.gate && item < n.router + n.latent + n.top + n.gate + n.shared);
     const Seen seen{ask(flag(a, DECODE_READY, item % FLAGS)), ask(flag(a, DECODE_Z_DONE, item % FLAGS))};   // come with the claim
-    if ((!late && !claim<false>(a, item, &sh)) || do_item<FEW, false>(a, n, item, seen, lds, &sh))
+    if ((!late && !claim<false>(a, item, &sh)) || do_item<FEW, false>(n, item, seen, lds, &sh))
         return;
     int kind = 0;   // the first item of this one's kind
     for (const int size : {n.router, n.latent, n.top, n.gate, n.shared, n.down, n.sums})
@@ -986,7 +1014,7 @@ __global__ __launch_bounds__(WAVE *REST_WAVES, 3) void decode_kernel(const Decod
 #pragma unroll 1
     for (int i = 0; i <= kind; i++)   // the earlier kinds' items that are still free, and then this one
         if (i == kind || claim<true>(a, i, &sh))
-            do_item<FEW, true>(a, n, i == kind ? item : i, Seen{0u, 0u}, lds, &sh);
+            do_item<FEW, true>(n, i == kind ? item : i, Seen{0u, 0u}, lds, &sh);
 }
 
 // Counters, flags and claims at zero.
