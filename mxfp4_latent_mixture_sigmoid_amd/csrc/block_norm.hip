@@ -289,6 +289,8 @@ hipError_t launch_rows(const moe_block_norm_args &a, hipStream_t st)
     const int H = a.H;
     if (H <= 64 * CHUNK)
         hipLaunchKernelGGL((block_norm_kernel<X, 64, 1>), quarter, dim3(256), 0, st, a);
+    else if (H <= 64 * CHUNK * 2)
+        hipLaunchKernelGGL((block_norm_kernel<X, 64, 2>), quarter, dim3(256), 0, st, a);
     else if (H <= 256 * CHUNK)
         hipLaunchKernelGGL((block_norm_kernel<X, 256, 1>), rows, dim3(256), 0, st, a);
     else if (H <= 512 * CHUNK)
