@@ -1065,7 +1065,7 @@ DecodeLayout decode_layout(const moe_config *c, int64_t T)
     part(L.z, lat * T * Lt * 2);
     part(L.z_rest, lat * T * Lt * 2);
     part(L.acat, lat * T * (Lt + S * c->shared_inter) * 2);
-    part(L.h, T * K * c->inter * 2);
+    part(L.h, 2 * T * K * c->inter * 2);
     L.total = off;
     return L;
 }
@@ -1080,9 +1080,9 @@ bool decode_supported(const moe_config *c, int64_t T)
     const int64_t items = 4 + most * (c->inter / 16 + groups) + 4 * groups + (c->n_experts * DECODE_ROUTER_PARTS + c->hidden + c->latent + S * c->shared_inter) / 16 + 4;
     const int64_t Hin = c->has_latent_proj ? c->hidden : c->latent, cat = c->latent + S * (int64_t)c->shared_inter;
     const int64_t widest = std::max({(c->latent + 2 * S * (int64_t)c->shared_inter) * Hin, (c->n_experts + 15) * Hin,
-                                     c->has_latent_proj ? cat * c->hidden : 0, T * c->top_k * c->inter, T * cat, T * Hin,
+                                     c->has_latent_proj ? cat * c->hidden : 0, 2 * T * c->top_k * c->inter, T * cat, T * Hin,
                                      c->latent * 2 * (int64_t)MX_STEP, c->inter * (int64_t)MX_STEP,
-                                     2 * T * c->top_k * c->latent});
+                                     2 * T * c->top_k * c->latent, c->latent * (int64_t)c->inter / 2});
     return widest * 2 < DECODE_MAX_WINDOW && items <= (1 << 24) - 1;
 }
 

@@ -1,20 +1,26 @@
-// decode.hip -- the whole layer for up to 16 tokens in two kernels.
+// decode.hip -- the whole layer for up to 16 tokens in one kernel, after a small one that clears its counters.
 //
 // The tokens are one row tile of the matrix-core instruction, so every weight is read once, from memory, and
 // multiplied with all tokens at once: the time is the weights' (184 MB for one token of a TP8 share: the router, latent
-// and shared matrices in BF16, 16 experts in MXFP4).
+// and shared matrices in BF16, 16 experts in MXFP4; 640 MB and 220 experts for 16). The kernel is a list of work items,
+// one for each workgroup, numbered kind after kind:
+//    router  (16 experts, a quarter of x): their part of x W_r^T
+//    latent  16 columns of z = x W_down^T
+//    top     the top-K of 4 tokens; the list of distinct experts and each one's tokens
+//    gate    (expert, 16 or 64 inner channels): h = silu(z Wg^T) (z Wu^T) of the expert's tokens
+//    shared  16 channels of h_s = bf16(silu(x Wg_s^T) (x Wu_s^T))
+//    down    (expert, 256 or 512 latent columns): y = h Wd^T of the expert's tokens, in FP32
+//    sums    (4 tokens, 256 latent columns): zc = bf16(sum w y), in slot order
+//    out     16 output columns: out = bf16([zc | h_s] [W_up | W_ds]^T)
+// so that the memory's rate is not lost at the borders of launches: an item's first weights are asked for before what it
+// waits for is there. One token takes 54 us (3.4 TB/s), and 68 as separate launches (moe_route_forward); 4 tokens 81 and
+// 82, 8 112 and 104, 16 190 and 136: from about five on an item's start, 5 us of claiming and looking up while its place
+// waits, costs more than the launches. One token's way: z after 16 us, the experts 19, h 31, y 37, zc 41, out 52.
 //
-//  front_kernel  what only needs x: the router's logits, z = x W_down^T, h_s = bf16(silu(x Wg_s^T) (x Wu_s^T)).
-//  rest_kernel   everything after it, in work items, one for each workgroup:
-//    top    the top-K of every token; the list of distinct experts and each one's tokens
-//    gate   (expert, 16 or 64 inner channels): h = bf16(silu(z Wg^T) (z Wu^T)) of the expert's tokens
-//    down   (expert, 256 latent columns): y = h Wd^T of the expert's tokens, in FP32
-//    sums   (4 tokens, 256 latent columns): zc = bf16(sum w y), in slot order
-//    out    16 output columns: out = bf16([zc | h_s] [W_up | W_ds]^T)
-//
-// z is kept in two BF16 parts, the rounded value and what the rounding left, because its rounding alone reaches every
-// expert's gate, up and product (0.4% of a small layer's output in the mean square, against 0.3% without); the
-// remainders are rows 8 to 15 of the tile for up to 8 tokens, at no cost, and a second operand for more.
+// z and h are kept in two BF16 parts, the rounded value and what the rounding left: their rounding alone reaches every
+// expert's products (0.4% of the layer's output in the mean square; with both, zc's, h_s's and the output's own are what is
+// left, 0.24%). The remainders are rows 8 to 15 of the tile for up to 8 tokens, at no cost that was seen, and a second
+// operand for more (16 tokens: 190 us, 178 with h rounded).
 //
 // Kinds wait for each other on flags. A workgroup takes the item of its number by claiming it; it waits for a flag PATIENCE
 // times, far longer than a call takes, and if the flag has not come by then (its workgroups may not even have started:
@@ -24,13 +30,15 @@
 // items from one ticket counter gives that too, but additions to one address take 12 ns each: 1057 workgroups kept the
 // top-K's loads waiting for 9 us behind theirs.) For the same reason a flag that every workgroup asks for is written in 64
 // places; the gate items of an expert, and the down items of 256 columns, have a counter of their own, on which the few
-// items wait that need them. What one workgroup hands to another
-// goes through agent-coherent stores and loads (sync.hpp). The front kernel clears counters, flags and claims.
+// items wait that need them. What one workgroup hands to another goes through agent-coherent stores and loads (sync.hpp).
 //
 // Two things set the pace of code that runs once. Instructions come from memory at about 1 KiB a microsecond the first
-// time: so the top-K is written to be short, and while an item waits it goes once through what it will do, with empty
-// windows for its loads and stores (`go` = 0). And a load under a condition is a wait for the loads before it: so no
-// load has one; loads past the end lie outside their window, which costs nothing.
+// time: so while an item waits it goes once through what it will do, with empty windows for its loads and stores
+// (`go` = 0). And a load under a condition is a wait for the loads before it: so no load of weights has one; loads past the
+// end lie outside their window, which costs nothing.
+//
+// Three workgroups share a CU (168 registers a thread). With four of 128, whose items spill some, more of them start
+// early, but one token took 61 us.
 #include "decode.hpp"
 #include "select.hpp"
 #include "sync.hpp"
@@ -42,7 +50,7 @@ namespace {
 constexpr int ROWS = DECODE_MAX_T, HALF = ROWS / 2;
 constexpr int REST_WAVES = 4, ROUTER_PARTS = DECODE_ROUTER_PARTS;
 constexpr int FLAGS = WAVE;                 // places of a flag
-constexpr int STAGE_WORDS = 1856;           // LDS of a wave for its activations, where they fit
+constexpr int STAGE_WORDS = DECODE_STAGE_WORDS;
 constexpr int LDS_WORDS = REST_WAVES * STAGE_WORDS + REST_WAVES * 512;   // of an item; three workgroups share a CU
 
 __device__ __forceinline__ uint32_t *counter(const DecodeArgs &a, int i) { return a.counters + i * DECODE_COUNTER_WORDS; }
@@ -73,6 +81,14 @@ __device__ __forceinline__ void store_sums(float *red, f32x4_t v)
 #pragma unroll
     for (int i = 0; i < 4; i++)
         red[(4 * (lane >> 4) + i) * 16 + (lane & 15)] = v[i];
+}
+
+// Two values as BF16 and what that rounding left, in BF16 as well: 16 bits of each value in all.
+__device__ __forceinline__ void split(float v0, float v1, uint32_t &high, uint32_t &rest)
+{
+    high = pack_bf16x2(v0, v1);
+    const float h0 = __uint_as_float(high << 16), h1 = __uint_as_float(high & 0xFFFF0000u);
+    rest = pack_bf16x2(fabsf(h0) < INFINITY ? v0 - h0 : 0.f, fabsf(h1) < INFINITY ? v1 - h1 : 0.f);
 }
 
 // Sum of one element over the waves' fragments, in wave order.
@@ -330,11 +346,11 @@ __device__ __forceinline__ void latent_item(const DecodeArgs &a, int item, int i
     if (row < a.T) {   // a wave each of 8 rows: at most 16 rows, two waves
         const float *red = reinterpret_cast<const float *>(lds);
         const float v0 = total<REST_WAVES>(red, 256, row * 16 + c), v1 = total<REST_WAVES>(red, 256, row * 16 + c + 1);
-        const uint32_t high = pack_bf16x2(v0, v1);
+        uint32_t high, rest;
+        split(v0, v1, high, rest);
         const int at = (row * a.Lt + item * 16 + c) * 2;
         store4_sc1(flat_rsrc(a.z, (int64_t)a.T * a.Lt * 2), at, high);
-        store4_sc1(flat_rsrc(a.z_rest, (int64_t)a.T * a.Lt * 2), at,
-                   pack_bf16x2(v0 - __uint_as_float(high << 16), v1 - __uint_as_float(high & 0xFFFF0000u)));
+        store4_sc1(flat_rsrc(a.z_rest, (int64_t)a.T * a.Lt * 2), at, rest);
     }
     stores_done();
     if (wave_id() != 0)
@@ -552,6 +568,30 @@ __device__ __forceinline__ f32x4_t mx_step(u32x4_t codes, uint32_t scales, const
         acc = mfma16(as_bf16x8(x[j]), mx_dequant8(codes[j], e8m0_to_f32((scales >> (8 * j)) & 0xFFu)), acc);
     return acc;
 }
+// N of them times one operand or two, a sum each.
+template <int PARTS, int N>
+__device__ __forceinline__ void mx_steps(const u32x4_t (&codes)[N], const uint32_t (&scales)[N], const uint32_t *rows, int second,
+                                         f32x4_t (&acc)[PARTS][N])
+{
+    u32x4_t x[PARTS][4];
+#pragma unroll
+    for (int p = 0; p < PARTS; p++)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            x[p][i] = *reinterpret_cast<const u32x4_t *>(rows + p * second + i * 16);
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const auto w = mx_dequant8(codes[j][i], e8m0_to_f32((scales[j] >> (8 * i)) & 0xFFu));
+#pragma unroll
+            for (int p = 0; p < PARTS; p++)
+                acc[p][j] = mfma16(as_bf16x8(x[p][i]), w, acc[p][j]);
+        }
+        if (PARTS == 2)
+            __builtin_amdgcn_sched_barrier(0);   // no more weights at a time than there are registers for
+    }
+}
 
 // The experts' gate and up product with one or two tokens: a pair of 16 gate and 16 up channels per workgroup, whose waves
 // share the K axis; each wave's part of z (and of its remainders, rows 8 and 9 of the operand) goes through LDS. The first
@@ -568,7 +608,8 @@ __device__ __forceinline__ bool gate_few(const DecodeArgs &a, int item, const Se
     const int pitch = n * MX_STEP / 2 + 4, chunks = n * 16;   // words of a staged row; 16-byte pieces
     // rows T .. 7 and 8 + T .. 15 of the operand repeat the last token: their sums are not used
     const uint32_t *staged = stage + (min(lane & 7, T - 1) + (lane & 8 ? T : 0)) * pitch + (lane >> 4) * 4;
-    const auto h = flat_rsrc(a.h, (int64_t)T * a.K * a.I * 2);
+    const int P = T * a.K;
+    const auto h = flat_rsrc(a.h, (int64_t)P * a.I * 4);
 #pragma unroll 1
     for (int go = HELP ? 1 : 0; go < 2; go++) {
         int e = 0, pair = -1;
@@ -646,8 +687,10 @@ __device__ __forceinline__ bool gate_few(const DecodeArgs &a, int item, const Se
                         v[j][i] += a.has_latent ? p[0] + p[HALF * 16] : p[0];
                     }
                 }
-            store4_sc1(h, go && pair >= 0 ? (pair * a.I + cp * 16 + 2 * (t % 8)) * 2 : OUTSIDE,
-                       pack_bf16x2(silu_f32(v[0][0]) * v[1][0], silu_f32(v[0][1]) * v[1][1]));
+            uint32_t high, rest;
+            split(silu_f32(v[0][0]) * v[1][0], silu_f32(v[0][1]) * v[1][1], high, rest);
+            store4_sc1(h, go && pair >= 0 ? (pair * a.I + cp * 16 + 2 * (t % 8)) * 2 : OUTSIDE, high);
+            store4_sc1(h, go && pair >= 0 ? ((P + pair) * a.I + cp * 16 + 2 * (t % 8)) * 2 : OUTSIDE, rest);
         }
     }
     arrive(decode_gates(a, r));
@@ -726,16 +769,7 @@ __device__ __forceinline__ bool gate_many(const DecodeArgs &a, int item, const S
 #pragma unroll
             for (int i = 0; i < STEPS; i++) {   // steps past the end multiply zeros
                 const int slot = c * STEPS + i;
-#pragma unroll
-                for (int p = 0; p < PARTS; p++) {
-                    u32x4_t x[4];
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        x[j] = *reinterpret_cast<const u32x4_t *>(mine + p * ROWS * PITCH + i * (MX_STEP / 2) + j * 16);
-#pragma unroll
-                    for (int j = 0; j < 2; j++)
-                        acc[p][j] = mx_step(codes[slot][j], scales[slot][j], x, acc[p][j]);
-                }
+                mx_steps<PARTS>(codes[slot], scales[slot], mine + i * (MX_STEP / 2), ROWS * PITCH, acc);
                 if (s + slot + 1 == steps * quarter / REST_WAVES) {
 #pragma unroll
                     for (int j = 0; j < 2; j++) {
@@ -756,32 +790,39 @@ __device__ __forceinline__ bool gate_many(const DecodeArgs &a, int item, const S
             }
         }
     // two channels to a word; rows of the upper half of the lanes are remainders where PARTS = 1
-    const auto h = flat_rsrc(a.h, (int64_t)a.T * a.K * a.I * 2);
+    const int P = a.T * a.K;
+    const auto h = flat_rsrc(a.h, (int64_t)P * a.I * 4);
 #pragma unroll
     for (int k = 0; k < 4; k++) {
         const float v = silu_f32(sum[0][k]) * sum[1][k], after = __shfl_down(v, 1);
         const int pair = (int16_t)((k < 2 ? pair01 : pair23) >> (16 * (k % 2))), token = 4 * (lane >> 4) + k;
         const bool keep = pair >= 0 && token < a.T && lane % 2 == 0;
-        store4_sc1(h, keep ? (pair * a.I + cp * 16 + (lane & 15)) * 2 : OUTSIDE, pack_bf16x2(v, after));
+        uint32_t high, rest;
+        split(v, after, high, rest);
+        store4_sc1(h, keep ? (pair * a.I + cp * 16 + (lane & 15)) * 2 : OUTSIDE, high);
+        store4_sc1(h, keep ? ((P + pair) * a.I + cp * 16 + (lane & 15)) * 2 : OUTSIDE, rest);
     }
     arrive(decode_gates(a, r));
     return true;
 }
 
-// 256 latent columns of one expert's down product, 64 to a wave: y of its tokens' pairs, to memory. The weights of STEPS steps
-// are loaded before h is known, which takes that expert's gate items only; h goes through LDS, STEPS steps at a time. Each
-// column of a pair is one chain of sums over K, the same whatever tokens come with it.
-template <bool HELP>
+// decode_down_span times 256 latent columns of one expert's down product, 64 of 256 to a wave: y of its tokens' pairs, to
+// memory. The weights come in units of STEPS steps, a unit ahead, the first before h is known, which takes that expert's
+// gate items only. h and its remainders go through LDS, STEPS steps at a time (once for all columns, if those are all): one
+// operand for up to 8 tokens, two for more (PARTS). Each column of a pair is two chains of sums over K, h's and the
+// remainders', the same whatever tokens come with it.
+template <int PARTS, bool HELP>
 __device__ __forceinline__ bool down_item(const DecodeArgs &a, int item, const Seen &seen, uint32_t *lds, uint32_t *sh)
 {
     constexpr int STEPS = 3, NB = DECODE_DOWN_COLUMNS / (16 * REST_WAVES), NTHR = WAVE * REST_WAVES;
-    constexpr int PITCH = STEPS * MX_STEP / 2 + 4, PER_ROW = STEPS * MX_STEP / 8, PIECES = ROWS * PER_ROW / NTHR;
-    static_assert(2 * ROWS * PITCH + ROWS / 2 <= LDS_WORDS && PIECES * NTHR == ROWS * PER_ROW, "room for two chunks and the pairs; pieces");
-    const int lane = lane_id(), t = threadIdx.x, groups = decode_groups(a), r = item / groups, g = item % groups;
-    const int steps = a.I / MX_STEP, P = a.T * a.K, col = (g * REST_WAVES + wave_id()) * NB, blocks = min(NB, a.Lt / 16 - col);
+    constexpr int PITCH = STEPS * MX_STEP / 2 + 4, PER_ROW = STEPS * MX_STEP / 8, TOKENS = PARTS == 1 ? HALF : ROWS;
+    constexpr int PIECES = 2 * TOKENS * PER_ROW / NTHR;
+    static_assert(2 * ROWS * PITCH + ROWS / 2 <= LDS_WORDS && PIECES * NTHR == 2 * TOKENS * PER_ROW, "room; pieces");
+    const int lane = lane_id(), t = threadIdx.x, span = decode_down_span(a), per = decode_down_items(a), r = item / per, g0 = item % per * span;
+    const int groups = min(span, decode_groups(a) - g0), steps = a.I / MX_STEP, P = a.T * a.K, blocks = a.Lt / 16;
 #pragma unroll 1
     for (int go = HELP ? 1 : 0; go < 2; go++) {
-        int e = 0, from[PIECES];   // this thread's pieces of h: the pair's row and the column, in bytes
+        int e = 0, from[PIECES];   // this thread's pieces of h and the remainders: the row and the column, in bytes
 #pragma unroll
         for (int i = 0; i < PIECES; i++)
             from[i] = OUTSIDE;
@@ -793,7 +834,7 @@ __device__ __forceinline__ bool down_item(const DecodeArgs &a, int item, const S
             const auto pairs = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
 #pragma unroll
             for (int i = 0; i < PIECES; i++)
-                from[i] = (int)load4_sc1(pairs, (r * ROWS + (i * NTHR + t) / PER_ROW / 2 * 2) * 2);
+                from[i] = (int)load4_sc1(pairs, (r * ROWS + (i * NTHR + t) / PER_ROW % TOKENS / 2 * 2) * 2);
             const uint32_t two = load4_sc1(pairs, (r * ROWS + t % (ROWS / 2) * 2) * 2);
             e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
             arrived = ask(decode_gates(a, r));
@@ -802,19 +843,18 @@ __device__ __forceinline__ bool down_item(const DecodeArgs &a, int item, const S
 #pragma unroll
             for (int i = 0; i < PIECES; i++) {
                 const int pair = (int16_t)((i * NTHR + t) / PER_ROW % 2 ? from[i] >> 16 : from[i]);
-                from[i] = pair >= 0 ? (pair * a.I + (i * NTHR + t) % PER_ROW * 8) * 2 : OUTSIDE;
+                from[i] = pair >= 0 ? ((pair + (i * NTHR + t) / PER_ROW / TOKENS * P) * a.I + (i * NTHR + t) % PER_ROW * 8) * 2 : OUTSIDE;
             }
         }
-        const int n = go ? steps : 1;
-        const auto w = window(a.down + e * a.down_stride + (int64_t)col * steps * MX_BLOCK_BYTES,
-                              (int64_t)steps * MX_BLOCK_BYTES * blocks, go && blocks > 0);
-        const auto h = window(a.h, (int64_t)P * a.I * 2, go), y = window(a.partial, (int64_t)P * a.Lt * 4, go);
+        const int n = go ? steps : 1, units = go ? groups * ((steps + STEPS - 1) / STEPS) : 1;
+        const auto w = window(a.down + e * a.down_stride, (int64_t)blocks * steps * MX_BLOCK_BYTES, go);
+        const auto h = window(a.h, (int64_t)P * a.I * 4, go), y = window(a.partial, (int64_t)P * a.Lt * 4, go);
         u32x4_t codes[STEPS][NB], hs[PIECES];
         uint32_t scales[STEPS][NB];
-        auto load = [&](int slot, int s) __attribute__((always_inline)) {
+        auto load = [&](int slot, int col, int s) __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < NB; j++) {
-                const int off = s < n ? (j * steps + s) * MX_BLOCK_BYTES : OUTSIDE;
+                const int off = s < n && col + j < blocks ? ((col + j) * steps + s) * MX_BLOCK_BYTES : OUTSIDE;
                 codes[slot][j] = fetch16<CPOL_NT>(w, off + lane * 16);
                 scales[slot][j] = fetch4<CPOL_NT>(w, off + MX_CODE_BYTES + 4 * (lane & 15));
             }
@@ -825,47 +865,58 @@ __device__ __forceinline__ bool down_item(const DecodeArgs &a, int item, const S
                 hs[i] = fetch16<CPOL_SC1>(h, from[i] != OUTSIDE && s * MX_STEP + (i * NTHR + t) % PER_ROW * 8 < n * MX_STEP
                                                  ? from[i] + s * MX_STEP * 2 : OUTSIDE);
         };
+        int col = (g0 * REST_WAVES + wave_id()) * NB, s = 0;   // the unit's first column block and step
 #pragma unroll
         for (int i = 0; i < STEPS; i++)
-            load(i, i);
+            load(i, col, i);
         asm volatile("" ::: "memory");
         if (go && wait_for<HELP>(a, decode_gates(a, r), (uint32_t)decode_gate_items(a), sh, arrived) < 0)
             return false;
-        fetch(0);
-        f32x4_t acc[NB] = {};
-        int half = 0;   // which half of LDS, as in gate_many
+        f32x4_t acc[PARTS][NB] = {};
+        const uint32_t *mine = lds + (lane & 15) * PITCH + (lane >> 4) * 4;
 #pragma unroll 1
-        for (int s = 0; s < n; s += STEPS, half ^= 1) {
-            uint32_t *chunk = lds + half * ROWS * PITCH;
-            const uint32_t *mine = chunk + (lane & 15) * PITCH + (lane >> 4) * 4;
+        for (int u = 0; u < units; u++) {
+            if (u == 0 || n > STEPS) {   // another part of h
+                fetch(s);
+                __syncthreads();
 #pragma unroll
-            for (int i = 0; i < PIECES; i++)
-                *reinterpret_cast<u32x4_t *>(chunk + (i * NTHR + t) / PER_ROW * PITCH + (i * NTHR + t) % PER_ROW * 4) = hs[i];
-            fetch(s + STEPS);
-            __syncthreads();
+                for (int i = 0; i < PIECES; i++)
+                    *reinterpret_cast<u32x4_t *>(lds + (i * NTHR + t) / PER_ROW * PITCH + (i * NTHR + t) % PER_ROW * 4) = hs[i];
+                __syncthreads();
+            }
+            const bool end = s + STEPS >= n;   // of these columns
+            const int next = u + 1 == units ? blocks : end ? col + NB * REST_WAVES : col, next_s = end ? 0 : s + STEPS;
 #pragma unroll
             for (int i = 0; i < STEPS; i++) {   // steps past the end multiply zeros
-                u32x4_t x[4];
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    x[j] = *reinterpret_cast<const u32x4_t *>(mine + i * (MX_STEP / 2) + j * 16);
-#pragma unroll
-                for (int j = 0; j < NB; j++)
-                    acc[j] = mx_step(codes[i][j], scales[i][j], x, acc[j]);
+                mx_steps<PARTS>(codes[i], scales[i], mine + i * (MX_STEP / 2), ROWS * PITCH, acc);
                 __builtin_amdgcn_sched_barrier(0);
-                load(i, s + i + STEPS);
+                load(i, next, next_s + i);
             }
-        }
+            if (end) {
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-            const int pair = reinterpret_cast<const int16_t *>(lds + 2 * ROWS * PITCH)[4 * (lane >> 4) + k];
+                for (int k = 0; k < 4; k++) {
+                    const int pair = reinterpret_cast<const int16_t *>(lds + 2 * ROWS * PITCH)[4 * (lane >> 4) + k];
 #pragma unroll
-            for (int j = 0; j < NB; j++)
-                store4_sc1(y, go && pair >= 0 && pair < P && j < blocks ? (pair * a.Lt + (col + j) * 16 + (lane & 15)) * 4 : OUTSIDE, __float_as_uint(acc[j][k]));
+                    for (int j = 0; j < NB; j++) {
+                        const float rest = PARTS == 1 ? __shfl_xor(acc[0][j][k], 32) : acc[PARTS - 1][j][k];
+                        store4_sc1(y, go && pair >= 0 && pair < P && col + j < blocks ? (pair * a.Lt + (col + j) * 16 + (lane & 15)) * 4 : OUTSIDE,
+                                   __float_as_uint(acc[0][j][k] + rest));
+                    }
+                }
+#pragma unroll
+                for (int p = 0; p < PARTS; p++)
+#pragma unroll
+                    for (int j = 0; j < NB; j++)
+                        acc[p][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            }
+            col = next;
+            s = next_s;
         }
         __syncthreads();   // LDS is free for the next pass
     }
-    arrive(decode_columns(a, g));
+    stores_done();
+    if (t < groups)
+        __hip_atomic_fetch_add(decode_columns(a, g0 + t), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     return true;
 }
 
@@ -983,7 +1034,7 @@ __device__ __forceinline__ bool do_item(const DecodeItems &n, int i, const Seen 
     }
     i -= n.shared;
     if (i < n.down)
-        return down_item<HELP>(arguments(), i, seen, lds, sh);
+        return down_item<FEW ? 1 : 2, HELP>(arguments(), i, seen, lds, sh);
     i -= n.down;
     if (i < n.sums)
         return sum_item<HELP>(arguments(), i, seen, sh);
@@ -995,7 +1046,7 @@ __global__ __launch_bounds__(WAVE *REST_WAVES, 3) void decode_kernel(const Decod
 {
     constexpr int TOP = DECODE_MAX_E + ROWS * 32 + 16, MOST = ROWS * 32;   // MOST: pairs, and distinct experts
     static_assert(TOP % 2 == 0 && TOP + REST_WAVES * (DECODE_MAX_E + 2 * WAVE) <= LDS_WORDS && TOP + MOST * (ROWS / 2) <= LDS_WORDS, "room for the list");
-    static_assert(STAGE_WORDS == DECODE_STAGE_WORDS && REST_WAVES == 4, "what decode.hpp says");
+    static_assert(REST_WAVES == 4, "what decode.hpp says");
     __shared__ alignas(16) uint32_t lds[LDS_WORDS];
     __shared__ uint32_t sh;
     const DecodeItems n = decode_items(a);

@@ -1,4 +1,4 @@
-// decode.hpp -- launch interface of the layer for a few tokens in two kernels.
+// decode.hpp -- launch interface of the layer for a few tokens.
 #pragma once
 
 #include "common.hpp"
@@ -47,7 +47,7 @@ struct DecodeArgs {
     uint16_t *z_rest;                // [T, Lt] what z's rounding left; unused without latent projections
     uint16_t *acat;                  // [T, ldcat]: zc, then h_s
     int ldcat;
-    uint16_t *h;                     // [T K, I]
+    uint16_t *h;                     // [2, T K, I]: and what its rounding left
     // outputs
     float *logits_out;               // [T, E], or null
     int32_t *ids_out;                // [T, K], or null
@@ -56,13 +56,21 @@ struct DecodeArgs {
 };
 
 // One or two tokens' gate and up product by 16 channels, where a wave's part of z and of its remainders fits its LDS; else by
-// 64. (Two tokens: TWO us against MANY.)
+// 64. (One token: 54 us, 57 by 64; two, whose experts seldom agree: 65 and 64, but a wave waits for less.)
 __host__ __device__ inline bool decode_gate_few(const DecodeArgs &a)
 {
     return a.T <= 2 && 2 * a.T * ((a.Lt / 128 + 3) / 4 * 64 + 4) <= DECODE_STAGE_WORDS;
 }
 __host__ __device__ inline int decode_gate_items(const DecodeArgs &a) { return a.I / (decode_gate_few(a) ? 16 : 64); }   // of an expert
 __host__ __device__ inline int decode_groups(const DecodeArgs &a) { return (a.Lt + DECODE_DOWN_COLUMNS - 1) / DECODE_DOWN_COLUMNS; }
+
+// Groups of 256 columns of a down item, whose look-ups and h are then shared. (8 tokens: 114 us with 1, 112 with 2; 4 tokens:
+// 81 with 2, 87 with 4. One or two tokens have few items as it is.)
+__host__ __device__ inline int decode_down_span(const DecodeArgs &a) { return a.T <= 2 ? 1 : 2; }
+__host__ __device__ inline int decode_down_items(const DecodeArgs &a)   // of an expert
+{
+    return (decode_groups(a) + decode_down_span(a) - 1) / decode_down_span(a);
+}
 
 // Work items, numbered kind after kind; a kind waits for earlier ones only.
 struct DecodeItems {
@@ -72,7 +80,7 @@ __host__ __device__ inline DecodeItems decode_items(const DecodeArgs &a)
 {
     const int quads = (a.T + 3) / 4, groups = decode_groups(a);
     return {(int)(a.n_router_rows / 16) * DECODE_ROUTER_PARTS, a.has_latent ? a.Lt / 16 : 0, quads, a.most * decode_gate_items(a), a.shared / 16,
-            a.most * groups, quads * groups, a.has_latent ? a.H / 16 : 0};
+            a.most * decode_down_items(a), quads * groups, a.has_latent ? a.H / 16 : 0};
 }
 __host__ __device__ inline int decode_item_count(const DecodeItems &n)
 {

@@ -95,7 +95,7 @@ class MoELayer:
         return out
 
     def decode(self, x, out=None, logit_bias=None, logits_out=None, ids=None, weights=None, stream=None) -> Decoded:
-        """The whole layer for x [T, Hin] BF16 of at most 16 tokens, in two kernels: what route_forward computes, without its
+        """The whole layer for x [T, Hin] BF16 of at most 16 tokens, in one launch: what route_forward computes, without its
         routing arrays, and not the same bits (an expert's output is not rounded before the weighted sum). Outputs go into
         the given tensors if any (contiguous; logits_out FP32 [T, E]). The call allocates its own workspace, so that calls
         may overlap on different streams and in captured graphs."""

@@ -34,7 +34,7 @@ def test_sizes():
     st, size = query(config(), 5)
     assert st == 0 and size == (up((20 + 3 * 64 + 20 + 1) * 32 * 4) + up((4 * 3 + 36 + 2 * (1 + 1) + 20 * (8 + 1)) * 4) + up(20 * 256 * 4)
                                 + up(4 * 5 * 40 * 4) + 2 * up(5 * 4 * 4) + up(20 * 4) + up(20 * 16 * 2) + 2 * up(5 * 256 * 2)
-                                + up(5 * 320 * 2) + up(20 * 128 * 2))
+                                + up(5 * 320 * 2) + up(2 * 20 * 128 * 2))
     assert query(config(), 0)[0] == 0 and query(config(), abi.DECODE_MAX_T)[0] == 0
 
 
