@@ -593,32 +593,30 @@ __device__ __forceinline__ void mx_steps(const u32x4_t (&codes)[N], const uint32
     }
 }
 
-// The experts' gate and up product with one or two tokens: a pair of 16 gate and 16 up channels per workgroup, whose waves
-// share the K axis; each wave's part of z (and of its remainders, rows 8 and 9 of the operand) goes through LDS. The first
-// weights are asked for before z is there.
+// The experts' gate and up product with one token: a pair of 16 gate and 16 up channels per workgroup, whose waves share the
+// K axis; each wave's part of z (and of its remainders, row 8 of the operand) goes through LDS. The first weights are asked
+// for before z is there.
 template <bool HELP>
-__device__ __forceinline__ bool gate_few(const DecodeArgs &a, int item, const Seen &seen, uint32_t *lds, uint32_t *sh)
+__device__ __forceinline__ bool gate_one(const DecodeArgs &a, int item, const Seen &seen, uint32_t *lds, uint32_t *sh)
 {
-    const int lane = lane_id(), wv = wave_id(), t = threadIdx.x, T = a.T;
+    const int lane = lane_id(), wv = wave_id(), t = threadIdx.x;
     const int pairs16 = a.I / 16, r = item / pairs16, cp = item % pairs16;
     const int steps = a.Lt / MX_STEP, s0 = steps * wv / REST_WAVES, n = steps * (wv + 1) / REST_WAVES - s0;
     constexpr int BATCH = 7;   // steps in flight
     uint32_t *stage = lds + wv * STAGE_WORDS;
     float *red = reinterpret_cast<float *>(lds + REST_WAVES * STAGE_WORDS);
     const int pitch = n * MX_STEP / 2 + 4, chunks = n * 16;   // words of a staged row; 16-byte pieces
-    // rows T .. 7 and 8 + T .. 15 of the operand repeat the last token: their sums are not used
-    const uint32_t *staged = stage + (min(lane & 7, T - 1) + (lane & 8 ? T : 0)) * pitch + (lane >> 4) * 4;
-    const int P = T * a.K;
-    const auto h = flat_rsrc(a.h, (int64_t)P * a.I * 4);
+    const uint32_t *staged = stage + (lane & 8 ? pitch : 0) + (lane >> 4) * 4;   // sums of rows 1 .. 7, 9 .. 15 are not used
+    const auto h = flat_rsrc(a.h, (int64_t)a.K * a.I * 4);
 #pragma unroll 1
     for (int go = HELP ? 1 : 0; go < 2; go++) {
-        int e = 0, pair = -1;
+        int e = 0, pair = 0;
         if (go) {
             const int experts = wait_ready<HELP>(a, seen, sh);
             if (r >= experts)
                 return experts >= 0;
             e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
-            pair = (int16_t)(load4_sc1(flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2), r * ROWS * 2) >> (t & 8 ? 16 : 0));
+            pair = (int)(load4_sc1(flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2), r * ROWS * 2) & 0xFFFFu);
         }
         const auto w = window(a.gateup + e * a.gateup_stride + (int64_t)2 * cp * steps * MX_BLOCK_BYTES,
                               2 * (int64_t)steps * MX_BLOCK_BYTES, go);
@@ -638,22 +636,20 @@ __device__ __forceinline__ bool gate_few(const DecodeArgs &a, int item, const Se
         asm volatile("" ::: "memory");
         if (go && !wait_z<HELP>(a, seen, sh))
             return false;
-        const auto z0 = window(a.z, (int64_t)T * a.Lt * 2, go), z1 = window(a.has_latent ? a.z_rest : a.z, (int64_t)T * a.Lt * 2, go);
+        const auto z0 = window(a.z, (int64_t)a.Lt * 2, go), z1 = window(a.has_latent ? a.z_rest : a.z, (int64_t)a.Lt * 2, go);
 #pragma unroll 1
-        for (int row = 0; row < T; row++)
-#pragma unroll 1
-            for (int j = lane; j < chunks; j += 2 * WAVE) {
-                const int off = (row * a.Lt + s0 * MX_STEP + j * 8) * 2, off2 = j + WAVE < chunks ? off + WAVE * 16 : OUTSIDE;
-                uint32_t *to = stage + row * pitch + j * 4;
-                const u32x4_t v0 = fetch16<CPOL_SC1>(z0, off), v1 = fetch16<CPOL_SC1>(z0, off2);
-                const u32x4_t v2 = fetch16<CPOL_SC1>(z1, off), v3 = fetch16<CPOL_SC1>(z1, off2);
-                *reinterpret_cast<u32x4_t *>(to) = v0;
-                *reinterpret_cast<u32x4_t *>(to + T * pitch) = v2;
-                if (j + WAVE < chunks) {
-                    *reinterpret_cast<u32x4_t *>(to + WAVE * 4) = v1;
-                    *reinterpret_cast<u32x4_t *>(to + WAVE * 4 + T * pitch) = v3;
-                }
+        for (int j = lane; j < chunks; j += 2 * WAVE) {
+            const int off = (s0 * MX_STEP + j * 8) * 2, off2 = j + WAVE < chunks ? off + WAVE * 16 : OUTSIDE;
+            uint32_t *to = stage + j * 4;
+            const u32x4_t v0 = fetch16<CPOL_SC1>(z0, off), v1 = fetch16<CPOL_SC1>(z0, off2);
+            const u32x4_t v2 = fetch16<CPOL_SC1>(z1, off), v3 = fetch16<CPOL_SC1>(z1, off2);
+            *reinterpret_cast<u32x4_t *>(to) = v0;
+            *reinterpret_cast<u32x4_t *>(to + pitch) = v2;
+            if (j + WAVE < chunks) {
+                *reinterpret_cast<u32x4_t *>(to + WAVE * 4) = v1;
+                *reinterpret_cast<u32x4_t *>(to + WAVE * 4 + pitch) = v3;
             }
+        }
         f32x4_t acc[2] = {};
 #pragma unroll 1
         for (int s = 0; s < n; s += BATCH)
@@ -674,7 +670,7 @@ __device__ __forceinline__ bool gate_few(const DecodeArgs &a, int item, const Se
         store_sums(red + (wv * 2) * 256, acc[0]);
         store_sums(red + (wv * 2 + 1) * 256, acc[1]);
         __syncthreads();
-        if (t < 8 * T) {   // two channels of a token per thread
+        if (t < 8) {   // two channels per thread
             float v[2][2];
 #pragma unroll
             for (int j = 0; j < 2; j++)
@@ -683,14 +679,14 @@ __device__ __forceinline__ bool gate_few(const DecodeArgs &a, int item, const Se
                     v[j][i] = 0.f;
 #pragma unroll
                     for (int k = 0; k < REST_WAVES; k++) {
-                        const float *p = red + (k * 2 + j) * 256 + t / 8 * 16 + 2 * (t % 8) + i;
+                        const float *p = red + (k * 2 + j) * 256 + 2 * t + i;
                         v[j][i] += a.has_latent ? p[0] + p[HALF * 16] : p[0];
                     }
                 }
             uint32_t high, rest;
             split(silu_f32(v[0][0]) * v[1][0], silu_f32(v[0][1]) * v[1][1], high, rest);
-            store4_sc1(h, go && pair >= 0 ? (pair * a.I + cp * 16 + 2 * (t % 8)) * 2 : OUTSIDE, high);
-            store4_sc1(h, go && pair >= 0 ? ((P + pair) * a.I + cp * 16 + 2 * (t % 8)) * 2 : OUTSIDE, rest);
+            store4_sc1(h, go ? (pair * a.I + cp * 16 + 2 * t) * 2 : OUTSIDE, high);
+            store4_sc1(h, go ? ((a.K + pair) * a.I + cp * 16 + 2 * t) * 2 : OUTSIDE, rest);
         }
     }
     arrive(decode_gates(a, r));
@@ -1023,8 +1019,8 @@ __device__ __forceinline__ bool do_item(const DecodeItems &n, int i, const Seen 
     i -= n.top;
     if (i < n.gate) {
         if constexpr (FEW)
-            if (decode_gate_few(arguments()))
-                return gate_few<HELP>(arguments(), i, seen, lds, sh);
+            if (decode_gate_one(arguments()))
+                return gate_one<HELP>(arguments(), i, seen, lds, sh);
         return gate_many<FEW ? 1 : 2, HELP>(arguments(), i, seen, lds, sh);
     }
     i -= n.gate;

@@ -55,13 +55,13 @@ struct DecodeArgs {
     uint16_t *out;                   // [T, H] ([T, Lt] without latent projections)
 };
 
-// One or two tokens' gate and up product by 16 channels, where a wave's part of z and of its remainders fits its LDS; else by
-// 64. (One token: 54 us, 57 by 64; two, whose experts seldom agree: 65 and 64, but a wave waits for less.)
-__host__ __device__ inline bool decode_gate_few(const DecodeArgs &a)
+// One token's gate and up product by 16 channels, where a wave's part of z and of its remainders fits its LDS; else by 64.
+// (One token: 54 us, 57 by 64; two, with twice the experts: 65 us by 16, 64 by 64.)
+__host__ __device__ inline bool decode_gate_one(const DecodeArgs &a)
 {
-    return a.T <= 2 && 2 * a.T * ((a.Lt / 128 + 3) / 4 * 64 + 4) <= DECODE_STAGE_WORDS;
+    return a.T == 1 && 2 * ((a.Lt / 128 + 3) / 4 * 64 + 4) <= DECODE_STAGE_WORDS;
 }
-__host__ __device__ inline int decode_gate_items(const DecodeArgs &a) { return a.I / (decode_gate_few(a) ? 16 : 64); }   // of an expert
+__host__ __device__ inline int decode_gate_items(const DecodeArgs &a) { return a.I / (decode_gate_one(a) ? 16 : 64); }   // of an expert
 __host__ __device__ inline int decode_groups(const DecodeArgs &a) { return (a.Lt + DECODE_DOWN_COLUMNS - 1) / DECODE_DOWN_COLUMNS; }
 
 // Groups of 256 columns of a down item, whose look-ups and h are then shared. (8 tokens: 114 us with 1, 112 with 2; 4 tokens:

@@ -1,4 +1,4 @@
-"""The whole layer for a few tokens in two kernels (MoELayer.decode). Bounds: tests/decode_ref.py."""
+"""The whole layer for a few tokens in one kernel (MoELayer.decode). Bounds: tests/decode_ref.py."""
 import numpy as np
 import pytest
 import torch
