@@ -5,6 +5,9 @@
 //
 // One pass, as in norm.hip: a row's x, y and gate are read once into registers, three reductions over the row's
 // threads (the two sums of squares, the largest magnitude), every output is written once from FP32 values.
+//
+// Memory bounds many rows: 8192 x 7168 of FP32 with a gate row and every output, 763 MB, 154 us (5.0 TB/s, a copy's rate); 4096
+// rows of BF16 41 us (5.7 TB/s). Few rows take three times a load and a reduction: one row 4.9 us.
 #include "rows.hpp"
 
 namespace mxmoe {
@@ -285,6 +288,10 @@ __global__ __launch_bounds__(1024) void block_norm_long_kernel(const moe_block_n
 template <typename X>
 hipError_t launch_rows(const moe_block_norm_args &a, hipStream_t st)
 {
+    // The fewest threads with one chunk each, in whole powers of two; under a row of 1024 one wave takes two, since
+    // workgroups that hold four rows need no barrier. 8192 BF16 rows, us: of 512 values 64 x 1 8.0, 256 x 1 19.5; of 1024 64 x 2
+    // 12.0, 256 x 1 20.1; of 2048 256 x 1 23.3, 512 x 1 35.4; of 3584 512 x 1 40.1, 256 x 2 43.0. 4096 rows of 7168: 1024 x 1 41.0,
+    // 512 x 2 45.7, 256 x 4 48.1.
     const dim3 rows((unsigned)a.T), quarter((unsigned)((a.T + 3) / 4));
     const int H = a.H;
     if (H <= 64 * CHUNK)

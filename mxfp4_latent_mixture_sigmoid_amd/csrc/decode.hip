@@ -414,7 +414,9 @@ __device__ __forceinline__ void select_short(const DecodeArgs &a, int t, int go,
             keys[q * 4 + j] = key;
             top = max(top, key);
         }
-        __builtin_amdgcn_raw_buffer_store_b128(sum, logits, (q * WAVE + lane) * 16, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            __builtin_amdgcn_raw_buffer_store_b32((int)sum[j], logits, (q * WAVE + lane) * 16 + j * 4, 0, 0);
     }
     // K lanes hold a key of at least `bound`, so the best K keys are among those
     uint32_t bound = 0u;

@@ -1,4 +1,6 @@
 """The whole layer for a few tokens in one kernel (MoELayer.decode). Bounds: tests/decode_ref.py."""
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -304,3 +306,11 @@ def test_helping(s, impatient):
     for r in got:
         for a, b in zip(r, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [1, 5])
+def test_the_example_runs(T, capsys):
+    import runpy
+    example = runpy.run_path(os.path.join(os.path.dirname(__file__), "..", "examples", "decode_step.py"))
+    example["main"]([str(T), "tiny"])
+    assert f"{T} tokens" in capsys.readouterr().out
