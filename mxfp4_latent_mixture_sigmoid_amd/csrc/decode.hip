@@ -289,8 +289,7 @@ __device__ __forceinline__ void arrive(uint32_t *at)
 __device__ __forceinline__ void arrive_out(const DecodeArgs &a)
 {
     stores_done();
-    const DecodeItems n = decode_items(a);
-    if (wave_id() == 0 && last_at(counter(a, DECODE_CAT), n.shared + n.sums))
+    if (wave_id() == 0 && last_at(counter(a, DECODE_CAT), a.items.shared + a.items.sums))
         set_flag(a, DECODE_CAT_DONE, 0u);
 }
 
@@ -1047,7 +1046,7 @@ __global__ __launch_bounds__(WAVE *REST_WAVES, 3) void decode_kernel(const Decod
     static_assert(REST_WAVES == 4, "what decode.hpp says");
     __shared__ alignas(16) uint32_t lds[LDS_WORDS];
     __shared__ uint32_t sh;
-    const DecodeItems n = decode_items(a);
+    const DecodeItems n = a.items;
     const int item = blockIdx.x;
     const bool late = item < n.router + n.latent ||   // claimed in front_product
                       (item >= n.router + n.latent + n.top + n.gate && item < n.router + n.latent + n.top + n.gate + n.shared);
@@ -1067,21 +1066,23 @@ __global__ __launch_bounds__(WAVE *REST_WAVES, 3) void decode_kernel(const Decod
 }
 
 // Counters, flags and claims at zero.
-__global__ __launch_bounds__(256) void clear_kernel(const DecodeArgs a)
+__global__ __launch_bounds__(256) void clear_kernel(uint32_t *counters, int lines, uint32_t *claims, int items)
 {
-    const int lines = decode_counter_lines(a), i = blockIdx.x * 256 + threadIdx.x;
+    const int i = blockIdx.x * 256 + threadIdx.x;
     if (i < lines)
-        a.counters[i * DECODE_COUNTER_WORDS] = 0u;
-    else if (i - lines < decode_item_count(decode_items(a)))
-        a.claims[i - lines] = 0u;
+        counters[i * DECODE_COUNTER_WORDS] = 0u;
+    else if (i - lines < items)
+        claims[i - lines] = 0u;
 }
 
 } // namespace
 
-hipError_t launch_decode(const DecodeArgs &a, hipStream_t st)
+hipError_t launch_decode(const DecodeArgs &args, hipStream_t st)
 {
-    const int items = decode_item_count(decode_items(a));
-    hipLaunchKernelGGL(clear_kernel, dim3((unsigned)((items + decode_counter_lines(a) + 255) / 256)), dim3(256), 0, st, a);
+    DecodeArgs a = args;
+    a.items = decode_items(a);
+    const int items = decode_item_count(a.items), lines = decode_counter_lines(a);
+    hipLaunchKernelGGL(clear_kernel, dim3((unsigned)((items + lines + 255) / 256)), dim3(256), 0, st, a.counters, lines, a.claims, items);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;

@@ -22,6 +22,10 @@ constexpr int DECODE_DOWN_COLUMNS = 256;     // of a workgroup in the down produ
 constexpr int DECODE_ROUTER_PARTS = 4;       // workgroups that share 16 of the router's rows
 constexpr int DECODE_STAGE_WORDS = 1856;     // LDS of a wave for its activations
 
+// Work items, numbered kind after kind; a kind waits for earlier ones only.
+struct DecodeItems {
+    int router, latent, top, gate, shared, down, sums, out;
+};
 struct DecodeArgs {
     const uint16_t *x;               // [T, Hin]
     const float *bias;               // [E], or null
@@ -48,6 +52,7 @@ struct DecodeArgs {
     uint16_t *acat;                  // [T, ldcat]: zc, then h_s
     int ldcat;
     uint16_t *h;                     // [2, T K, I]: and what its rounding left
+    DecodeItems items;               // decode_items of the above
     // outputs
     float *logits_out;               // [T, E], or null
     int32_t *ids_out;                // [T, K], or null
@@ -72,23 +77,19 @@ __host__ __device__ inline int decode_down_items(const DecodeArgs &a)   // of an
     return (decode_groups(a) + decode_down_span(a) - 1) / decode_down_span(a);
 }
 
-// Work items, numbered kind after kind; a kind waits for earlier ones only.
-struct DecodeItems {
-    int router, latent, top, gate, shared, down, sums, out;
-};
-__host__ __device__ inline DecodeItems decode_items(const DecodeArgs &a)
+inline DecodeItems decode_items(const DecodeArgs &a)
 {
     const int quads = (a.T + 3) / 4, groups = decode_groups(a);
     return {(int)(a.n_router_rows / 16) * DECODE_ROUTER_PARTS, a.has_latent ? a.Lt / 16 : 0, quads, a.most * decode_gate_items(a), a.shared / 16,
             a.most * decode_down_items(a), quads * groups, a.has_latent ? a.H / 16 : 0};
 }
-__host__ __device__ inline int decode_item_count(const DecodeItems &n)
+inline int decode_item_count(const DecodeItems &n)
 {
     return n.router + n.latent + n.top + n.gate + n.shared + n.down + n.sums + n.out;
 }
 
 // Arrivals of the list's expert r at its h; of the down items at the columns of group g.
-__host__ __device__ inline int decode_counter_lines(const DecodeArgs &a) { return DECODE_SHARED_LINES + a.most + decode_groups(a); }
+inline int decode_counter_lines(const DecodeArgs &a) { return DECODE_SHARED_LINES + a.most + decode_groups(a); }
 __host__ __device__ inline uint32_t *decode_gates(const DecodeArgs &a, int r)
 {
     return a.counters + (DECODE_SHARED_LINES + r) * DECODE_COUNTER_WORDS;
