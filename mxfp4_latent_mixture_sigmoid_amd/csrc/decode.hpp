@@ -69,9 +69,10 @@ __host__ __device__ inline bool decode_gate_one(const DecodeArgs &a)
 __host__ __device__ inline int decode_gate_items(const DecodeArgs &a) { return a.I / (decode_gate_one(a) ? 16 : 64); }   // of an expert
 __host__ __device__ inline int decode_groups(const DecodeArgs &a) { return (a.Lt + DECODE_DOWN_COLUMNS - 1) / DECODE_DOWN_COLUMNS; }
 
-// Groups of 256 columns of a down item, whose look-ups and h are then shared. (8 tokens: 114 us with 1, 112 with 2; 4 tokens:
-// 81 with 2, 87 with 4. One or two tokens have few items as it is.)
-__host__ __device__ inline int decode_down_span(const DecodeArgs &a) { return a.T <= 2 ? 1 : 2; }
+// Groups of 256 columns of a down item, whose look-ups and h are then shared: two, where there are more items than places (3
+// on each of 256 CUs). 8 tokens: 114 us with one, 112 with two; 4 tokens 81 with two, 87 with four; a layer of 512 latent
+// columns, 3 tokens of 6 experts, 24 us with one, 27 with two.
+__host__ __device__ inline int decode_down_span(const DecodeArgs &a) { return a.most * decode_groups(a) <= 768 ? 1 : 2; }
 __host__ __device__ inline int decode_down_items(const DecodeArgs &a)   // of an expert
 {
     return (decode_groups(a) + decode_down_span(a) - 1) / decode_down_span(a);
