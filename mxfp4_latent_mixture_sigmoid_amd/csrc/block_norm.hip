@@ -6,7 +6,7 @@
 // One pass, as in norm.hip: a row's x, y and gate are read once into registers, three reductions over the row's
 // threads (the two sums of squares, the largest magnitude), every output is written once from FP32 values.
 //
-// Memory bounds many rows: 8192 x 7168 of FP32 with a gate row and every output, 763 MB, 154 us (5.0 TB/s, a copy's rate); 4096
+// Memory bounds many rows: 8192 x 7168 of FP32 with a gate row and every output, 763 MB, 155 us (4.9 TB/s, nearly a copy's rate); 4096
 // rows of BF16 41 us (5.7 TB/s). Few rows take three times a load and a reduction: one row 4.9 us.
 #include "rows.hpp"
 
