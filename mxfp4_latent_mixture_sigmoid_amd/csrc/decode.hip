@@ -103,12 +103,12 @@ __device__ __forceinline__ float total(const float *red, int stride, int at)
 }
 
 // A wave's part of a BF16 product: 32-wide steps s0 .. s1 - 1 of NB row blocks, all T tokens at once. The weights are loaded
-// DEPTH steps ahead, the first before anything is known of the activations. Those go through LDS where the wave's part of
-// them fits (few tokens: a step's operand would be a load with 4 T lanes of use), else straight to registers, AHEAD
-// steps ahead.
-template <int NB, int DEPTH, int AHEAD, bool STAGED>
+// DEPTH steps ahead, the first before anything is known of the activations. Those go through the wave's part of LDS: all of
+// them where they fit (CHUNK = 0: few tokens), else CHUNK steps at a time, each chunk loaded while the one before it is
+// multiplied. (Straight to registers a step's operand is 64 bytes of every row: 8 tokens 111 us in place of 104.)
+template <int NB, int DEPTH, int CHUNK>
 struct Bf16Part {
-    static_assert(DEPTH % AHEAD == 0, "slots");
+    static_assert(CHUNK == 0 || DEPTH % CHUNK == 0, "slots");
     // Whether K values of T tokens, divided among the waves, fit their parts of LDS.
     static __device__ bool fits(int T, int K, int waves) { return T * ((K / BF16_STEP + waves - 1) / waves * 16 + 4) <= STAGE_WORDS; }
     u32x4_t b[DEPTH][NB];
@@ -143,20 +143,22 @@ struct Bf16Part {
             load(i);
         asm volatile("" ::: "memory");   // issued here
     }
-    // get(row, k): 16 bytes of a token's activations from column k on.
+    // get(row, k, in): 16 bytes of a token's activations from column k on, or zeros.
     template <class Get>
-    __device__ void finish(int T, uint32_t *stage, f32x4_t (&acc)[NB], Get get)
+    __device__ __forceinline__ void finish(int T, uint32_t *stage, f32x4_t (&acc)[NB], Get get)
     {
-        const int lane = lane_id(), n = s1 - s0, pitch = n * 16 + 4;   // words of a token's part in LDS
-        const int r = lane & 15, c = lane >> 4;
-        if constexpr (STAGED) {
+        const int lane = lane_id(), n = s1 - s0;
+        // rows past the tokens repeat the last one: their sums are not used. Steps past the end multiply zeros.
+        const int r = min(lane & 15, T - 1), c = lane >> 4;
+        if constexpr (CHUNK == 0) {
+            const int pitch = n * 16 + 4;   // words of a token's part in LDS
 #pragma unroll 1
             for (int i0 = 0; i0 < T * n * 4; i0 += 4 * WAVE) {
                 u32x4_t v[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const int at = min(i0 + i * WAVE + lane, T * n * 4 - 1);
-                    v[i] = get(at / (n * 4), s0 * BF16_STEP + at % (n * 4) * 8);
+                    v[i] = get(at / (n * 4), s0 * BF16_STEP + at % (n * 4) * 8, true);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
@@ -164,8 +166,7 @@ struct Bf16Part {
                     *reinterpret_cast<u32x4_t *>(stage + at / (n * 4) * pitch + at % (n * 4) * 4) = v[i];
                 }
             }
-            // rows past the tokens repeat the last one: their sums are not used. Steps past the end multiply zeros.
-            const uint32_t *mine = stage + min(r, T - 1) * pitch + c * 4;
+            const uint32_t *mine = stage + r * pitch + c * 4;
 #pragma unroll 1
             for (int s = 0; s < n; s += DEPTH)
 #pragma unroll
@@ -178,23 +179,40 @@ struct Bf16Part {
                     if (i % 4 == 3)
                         __builtin_amdgcn_sched_barrier(0);   // not all operands at once
                 }
-            return;
-        }
-        u32x4_t x[AHEAD];
-        auto operand = [&](int s, int slot) __attribute__((always_inline)) { x[slot] = get(min(r, T - 1), (s0 + min(s, n - 1)) * BF16_STEP + c * 8); };
+        } else {
+            constexpr int PITCH = CHUNK * 16 + 4, PER_ROW = CHUNK * 4, PIECES = STAGE_WORDS / PITCH * PER_ROW / WAVE;
+            static_assert(STAGE_WORDS / PITCH * PER_ROW % WAVE == 0, "pieces");
+            u32x4_t v[PIECES];
+            auto fetch = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < AHEAD; i++)
-            operand(i, i);
+                for (int i = 0; i < PIECES; i++) {
+                    const int at = i * WAVE + lane, row = at / PER_ROW, col = at % PER_ROW;
+                    v[i] = get(row, (s0 + s) * BF16_STEP + col * 8, row < T && s + col / 4 < n);
+                }
+            };
+            const uint32_t *mine = stage + r * PITCH + c * 4;
+            fetch(0);
 #pragma unroll 1
-        for (int s = 0; s < n; s += DEPTH)
+            for (int s = 0; s < n; s += DEPTH)
 #pragma unroll
-            for (int i = 0; i < DEPTH; i++) {
+                for (int h = 0; h < DEPTH; h += CHUNK) {
 #pragma unroll
-                for (int j = 0; j < NB; j++)
-                    acc[j] = step(x[i % AHEAD], b[i][j], acc[j], s + i < n);
-                load(i);
-                operand(s + i + AHEAD, i % AHEAD);
-            }
+                    for (int i = 0; i < PIECES; i++)
+                        *reinterpret_cast<u32x4_t *>(stage + (i * WAVE + lane) / PER_ROW * PITCH + (i * WAVE + lane) % PER_ROW * 4) = v[i];
+                    fetch(s + h + CHUNK);
+#pragma unroll
+                    for (int i = 0; i < CHUNK; i++) {
+                        const u32x4_t x = *reinterpret_cast<const u32x4_t *>(mine + i * 16);
+#pragma unroll
+                        for (int j = 0; j < NB; j++)
+                            acc[j] = step(x, b[h + i][j], acc[j], s + h + i < n);
+                        load(h + i);
+                        if (i % 4 == 3)
+                            __builtin_amdgcn_sched_barrier(0);
+                    }
+                    asm volatile("" ::: "memory");   // the chunk is read before it is overwritten
+                }
+        }
     }
     // A step past the end adds nothing, whatever the activations are.
     static __device__ f32x4_t step(u32x4_t x, u32x4_t w, f32x4_t acc, bool in)
@@ -305,11 +323,11 @@ __device__ __forceinline__ bool front_product(const DecodeArgs &a, const uint8_t
         part.start(w, rows, a.Hin, block, part_of_k * REST_WAVES + wv, parts * REST_WAVES);
         if (!HELP && !claim<false>(a, blockIdx.x, sh))
             return false;
-        part.finish(a.T, lds + wv * STAGE_WORDS, acc, [&](int r, int k) __attribute__((always_inline)) { return fetch16<0>(x, (r * a.Hin + k) * 2); });
+        part.finish(a.T, lds + wv * STAGE_WORDS, acc, [&](int r, int k, bool in) __attribute__((always_inline)) { return fetch16<0>(x, in ? (r * a.Hin + k) * 2 : OUTSIDE); });
         return true;
     };
-    using Staged = Bf16Part<NB, 16 / NB, 4, true>;
-    if (!(Staged::fits(a.T, a.Hin, parts * REST_WAVES) ? run(Staged()) : run(Bf16Part<NB, 16 / NB, 8, false>())))
+    using Staged = Bf16Part<NB, 16 / NB, 0>;
+    if (!(Staged::fits(a.T, a.Hin, parts * REST_WAVES) ? run(Staged()) : run(Bf16Part<NB, 14 / NB, 7>())))
         return false;
     __syncthreads();
     float *red = reinterpret_cast<float *>(lds);
@@ -961,7 +979,7 @@ __device__ __forceinline__ bool sum_item(const DecodeArgs &a, int item, const Se
     return true;
 }
 
-template <bool HELP>
+template <bool FEW, bool HELP>
 __device__ __forceinline__ bool out_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
 {
     const int wv = wave_id(), t = threadIdx.x, row = t / 8, c = t % 8 * 2;
@@ -976,7 +994,7 @@ __device__ __forceinline__ bool out_item(const DecodeArgs &a, int item, uint32_t
             const auto acat = window(a.acat, (int64_t)a.T * a.ldcat * 2, go);
             f32x4_t acc[1] = {};
             part.finish(a.T, lds + wv * STAGE_WORDS, acc,
-                        [&](int r, int k) __attribute__((always_inline)) { return fetch16<CPOL_SC1>(acat, (r * a.ldcat + k) * 2); });
+                        [&](int r, int k, bool in) __attribute__((always_inline)) { return fetch16<CPOL_SC1>(acat, in ? (r * a.ldcat + k) * 2 : OUTSIDE); });
             store_sums(red + wv * 256, acc[0]);
             __syncthreads();
             if (row < a.T && row < ROWS)
@@ -987,10 +1005,10 @@ __device__ __forceinline__ bool out_item(const DecodeArgs &a, int item, uint32_t
         }
         return true;
     };
-    using Staged = Bf16Part<1, 16, 4, true>;
-    if (Staged::fits(a.T, a.ldcat, REST_WAVES))
-        return run(Staged());
-    return run(Bf16Part<1, 16, 8, false>());
+    if constexpr (FEW)
+        if (using Staged = Bf16Part<1, 16, 0>; Staged::fits(a.T, a.ldcat, REST_WAVES))
+            return run(Staged());
+    return run(Bf16Part<1, 14, FEW ? 14 : 7>());
 }
 
 // The kernel's arguments, read from memory again: they do not fit the scalar registers all at once.
@@ -1035,7 +1053,7 @@ __device__ __forceinline__ bool do_item(const DecodeItems &n, int i, const Seen 
     i -= n.down;
     if (i < n.sums)
         return sum_item<HELP>(arguments(), i, seen, sh);
-    return out_item<HELP>(arguments(), i - n.sums, lds, sh);
+    return out_item<FEW, HELP>(arguments(), i - n.sums, lds, sh);
 }
 
 template <bool FEW>
@@ -1043,7 +1061,7 @@ __global__ __launch_bounds__(WAVE *REST_WAVES, 3) void decode_kernel(const Decod
 {
     constexpr int TOP = DECODE_MAX_E + ROWS * 32 + 16, MOST = ROWS * 32;   // MOST: pairs, and distinct experts
     static_assert(TOP % 2 == 0 && TOP + REST_WAVES * (DECODE_MAX_E + 2 * WAVE) <= LDS_WORDS && TOP + MOST * (ROWS / 2) <= LDS_WORDS, "room for the list");
-    static_assert(REST_WAVES == 4, "what decode.hpp says");
+    static_assert(REST_WAVES == 4 && STAGE_WORDS >= HALF * (14 * 16 + 4) && STAGE_WORDS >= ROWS * (7 * 16 + 4), "what the items assume");
     __shared__ alignas(16) uint32_t lds[LDS_WORDS];
     __shared__ uint32_t sh;
     const DecodeItems n = a.items;
