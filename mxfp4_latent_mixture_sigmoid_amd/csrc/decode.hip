@@ -607,7 +607,7 @@ __device__ __forceinline__ void mx_steps(const u32x4_t (&codes)[N], const uint32
             for (int p = 0; p < PARTS; p++)
                 acc[p][j] = mfma16(as_bf16x8(x[p][i]), w, acc[p][j]);
         }
-        if (PARTS == 2)
+        if (PARTS == 2 && N > 2)
             __builtin_amdgcn_sched_barrier(0);   // no more weights at a time than there are registers for
     }
 }
