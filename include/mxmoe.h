@@ -219,7 +219,7 @@ moe_status moe_route_forward_static(moe_handle *h, const void *x, int32_t T, con
  * on the same packed weights, without the arrays of moe_routing, and nearer to the exact result: z and an expert's inner
  * values are kept in two BF16 parts, its output y in FP32 until the weighted sum. So outputs are near moe_route_forward's,
  * not the same bits; ids and weights follow from logits whose sums are added in another order too. A token's outputs are the
- * same bits whatever tokens come with it. It is the faster of the two for up to four tokens.
+ * same bits whatever tokens come with it. It is the faster of the two for up to about eight tokens.
  * x: bf16 [T, Hin]; logit_bias: fp32 [E] or NULL; logits_out: fp32 [T, E] or NULL; topk_ids [T, K] and topk_w [T, K] or
  * NULL; out: bf16 [T, H] (or [T, Lt]); x and out 16-byte aligned, no output overlaps an input or another output.
  * workspace: 256-byte aligned, moe_decode_query's bytes, not shared by calls that overlap; its contents do not matter.

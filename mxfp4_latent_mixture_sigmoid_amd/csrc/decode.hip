@@ -13,14 +13,14 @@
 //    sums    (4 tokens, 256 latent columns): zc = bf16(sum w y), in slot order
 //    out     16 output columns: out = bf16([zc | h_s] [W_up | W_ds]^T)
 // so that the memory's rate is not lost at the borders of launches: an item's first weights are asked for before what it
-// waits for is there. One token takes 53 us (3.5 TB/s), and 68 as separate launches (moe_route_forward); 4 tokens 81 and
-// 82, 8 111 and 104, 16 188 and 136: from about five on an item's start, 5 us of claiming and looking up while its place
+// waits for is there. One token takes 53 us (3.5 TB/s), and 68 as separate launches (moe_route_forward); 4 tokens 75 and
+// 82, 8 104 and 104, 16 173 and 136: with many experts an item's start, 5 us of claiming and looking up while its place
 // waits, costs more than the launches. One token's way: z after 16 us, the experts 19, h 31, y 37, zc 41, out 52.
 //
 // z and h are kept in two BF16 parts, the rounded value and what the rounding left: their rounding alone reaches every
 // expert's products (0.4% of the layer's output in the mean square; with both, zc's, h_s's and the output's own are what is
 // left, 0.24%). The remainders are rows 8 to 15 of the tile for up to 8 tokens, at no cost that was seen, and a second
-// operand for more (16 tokens: 188 us, 178 with h rounded).
+// operand for more (16 tokens: 190 us, 178 with h rounded, when it was added).
 //
 // Kinds wait for each other on flags. A workgroup takes the item of its number by claiming it; it waits for a flag PATIENCE
 // times, far longer than a call takes, and if the flag has not come by then (its workgroups may not even have started:
@@ -987,7 +987,7 @@ __device__ __forceinline__ bool out_item(const DecodeArgs &a, int item, uint32_t
     const auto out = flat_rsrc(a.out, (int64_t)a.T * a.H * 2);
     auto run = [&](auto part) __attribute__((always_inline)) {
 #pragma unroll 1
-        for (int go = !HELP && a.T <= 2 ? 0 : 1; go < 2; go++) {
+        for (int go = !HELP && a.T <= 2 ? 0 : 1; go < 2; go++) {   // of more tokens it delays the weights (4: 84 us, 81 without)
             part.start(a.w_out, a.H, a.ldcat, item, wv, REST_WAVES, go);
             if (go && wait_for<HELP>(a, flag(a, DECODE_CAT_DONE, blockIdx.x % FLAGS), 1u, sh) < 0)
                 return false;
