@@ -242,8 +242,9 @@ __device__ __forceinline__ int wait_for(const DecodeArgs &a, const uint32_t *at,
     asm volatile("" ::: "memory");
     return got;
 }
-struct Seen {   // two flags as they were a while ago
-    uint32_t ready, z;
+struct Seen {
+    uint32_t ready, z;   // two flags as they were a while ago
+    int first_pass;      // 0: none through the code before the experts are known (they are, or this is a helper)
 };
 // Until the experts are known: how many, or -1.
 template <bool HELP>
@@ -259,17 +260,17 @@ __device__ __forceinline__ bool wait_z(const DecodeArgs &a, const Seen &seen, ui
     return !a.has_latent || wait_for<HELP>(a, flag(a, DECODE_Z_DONE, blockIdx.x % FLAGS), 1u, sh, seen.z) >= 0;
 }
 
-// Whether item `i` is this workgroup's now.
+// Whether item `i` is this workgroup's now. `also` goes into *sh beside the answer.
 template <bool HELP>
-__device__ __forceinline__ bool claim(const DecodeArgs &a, int i, uint32_t *sh)
+__device__ __forceinline__ bool claim(const DecodeArgs &a, int i, uint32_t *sh, uint32_t also = 0u)
 {
     if (threadIdx.x == 0) {
         uint32_t *at = a.claims + i;
-        *sh = !(HELP && ask(at) != 0u) &&
-              __hip_atomic_fetch_add(at, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0u;
+        const bool free = !(HELP && ask(at) != 0u) && __hip_atomic_fetch_add(at, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0u;
+        *sh = (free ? 1u : 0u) | also;
     }
     __syncthreads();
-    const bool mine = __builtin_amdgcn_readfirstlane((int)*sh) != 0;
+    const bool mine = (__builtin_amdgcn_readfirstlane((int)*sh) & 1) != 0;
     __syncthreads();
     return mine;
 }
@@ -628,7 +629,7 @@ __device__ __forceinline__ bool gate_one(const DecodeArgs &a, int item, const Se
     const uint32_t *staged = stage + (lane & 8 ? pitch : 0) + (lane >> 4) * 4;   // sums of rows 1 .. 7, 9 .. 15 are not used
     const auto h = flat_rsrc(a.h, (int64_t)a.K * a.I * 4);
 #pragma unroll 1
-    for (int go = HELP ? 1 : 0; go < 2; go++) {
+    for (int go = 1 - seen.first_pass; go < 2; go++) {
         int e = 0, pair = 0;
         if (go) {
             const int experts = wait_ready<HELP>(a, seen, sh);
@@ -726,7 +727,8 @@ __device__ __forceinline__ bool gate_many(const DecodeArgs &a, int item, const S
     const int groups = a.I / 16 / REST_WAVES, r = item / groups, cp = item % groups * REST_WAVES + wv;
     const int steps = a.Lt / MX_STEP;
     // piece i of this thread: 8 values of row i (t / 16 ..): a token's z, or HALF or ROWS rows further its remainders.
-    // Rows past the tokens are zeros.
+    // Rows past the tokens are zeros, and everything in the first pass.
+    int z_there = 0;
     const auto z0 = flat_rsrc(a.z, (int64_t)a.T * a.Lt * 2), z1 = flat_rsrc(a.has_latent ? a.z_rest : a.z, (int64_t)a.T * a.Lt * 2);
     u32x4_t zs[PIECES];
     auto fetch = [&](int s) __attribute__((always_inline)) {
@@ -734,88 +736,97 @@ __device__ __forceinline__ bool gate_many(const DecodeArgs &a, int item, const S
         for (int i = 0; i < PIECES; i++) {
             const int p = i * NTHR + t, row = p / (STEPS * 16), c = p % (STEPS * 16);
             const int token = row % (PARTS == 1 ? HALF : ROWS), k = s * MX_STEP + c * 8;
-            zs[i] = fetch16<CPOL_SC1>(row >= (PARTS == 1 ? HALF : ROWS) ? z1 : z0, k < a.Lt && token < a.T ? (token * a.Lt + k) * 2 : OUTSIDE);
+            zs[i] = fetch16<CPOL_SC1>(row >= (PARTS == 1 ? HALF : ROWS) ? z1 : z0, z_there && k < a.Lt && token < a.T ? (token * a.Lt + k) * 2 : OUTSIDE);
         }
     };
-    const int experts = wait_ready<HELP>(a, seen, sh);
-    if (r >= experts)
-        return experts >= 0;
-    const int e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
-    // the pairs of this lane's rows 4 (l / 16) .. +3
-    const auto pairs = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
-    const uint32_t pair01 = load4_sc1(pairs, (r * ROWS + 4 * (lane >> 4)) * 2), pair23 = load4_sc1(pairs, (r * ROWS + 4 * (lane >> 4)) * 2 + 4);
-    const auto w = window(a.gateup + e * a.gateup_stride + (int64_t)2 * cp * steps * MX_BLOCK_BYTES,
-                          2 * (int64_t)steps * MX_BLOCK_BYTES, 1);
-    u32x4_t codes[AHEAD][2];
-    uint32_t scales[AHEAD][2];
-    auto load = [&](int slot, int s) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-            const int off = s < steps ? (j * steps + s) * MX_BLOCK_BYTES : OUTSIDE;
-            codes[slot][j] = fetch16<CPOL_NT>(w, off + lane * 16);
-            scales[slot][j] = fetch4<CPOL_NT>(w, off + MX_CODE_BYTES + 4 * (lane & 15));
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < AHEAD; i++)
-        load(i, i);
-    asm volatile("" ::: "memory");
-    if (!wait_z<HELP>(a, seen, sh))
-        return false;
-    fetch(0);
-    f32x4_t acc[PARTS][2] = {}, sum[2] = {};
-    int quarter = 1;   // ends at this many fourths of the steps; with fewer than four, some are empty
-    while (steps * quarter / REST_WAVES == 0)
-        quarter++;
-    int half = 0;   // which half of LDS: a wave that writes it has seen every wave past the chunk before the last
 #pragma unroll 1
-    for (int s = 0; s < steps; s += AHEAD)
-#pragma unroll
-        for (int c = 0; c < PARTS; c++, half ^= 1) {
-            uint32_t *chunk = lds + half * ROWS * PARTS * PITCH;
-            const uint32_t *mine = chunk + (lane & 15) * PITCH + (lane >> 4) * 4;
-#pragma unroll
-            for (int i = 0; i < PIECES; i++) {
-                const int p = i * NTHR + t;
-                *reinterpret_cast<u32x4_t *>(chunk + p / (STEPS * 16) * PITCH + p % (STEPS * 16) * 4) = zs[i];
-            }
-            fetch(s + (c + 1) * STEPS);
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < STEPS; i++) {   // steps past the end multiply zeros
-                const int slot = c * STEPS + i;
-                mx_steps<PARTS>(codes[slot], scales[slot], mine + i * (MX_STEP / 2), ROWS * PITCH, acc);
-                if (s + slot + 1 == steps * quarter / REST_WAVES) {
-#pragma unroll
-                    for (int j = 0; j < 2; j++) {
-#pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            const float rest = PARTS == 1 ? __shfl_xor(acc[0][j][k], 32) : acc[PARTS - 1][j][k];
-                            sum[j][k] += a.has_latent ? acc[0][j][k] + rest : acc[0][j][k];
-                        }
-#pragma unroll
-                        for (int p = 0; p < PARTS; p++)
-                            acc[p][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-                    }
-                    while (steps * quarter / REST_WAVES == s + slot + 1)
-                        quarter++;
-                }
-                __builtin_amdgcn_sched_barrier(0);
-                load(slot, s + slot + AHEAD);
-            }
+    for (int go = 1 - seen.first_pass; go < 2; go++) {
+        int e = 0;
+        uint32_t pair01 = ~0u, pair23 = ~0u;   // the pairs of this lane's rows 4 (l / 16) .. +3
+        if (go) {
+            const int experts = wait_ready<HELP>(a, seen, sh);
+            if (r >= experts)
+                return experts >= 0;
+            e = __builtin_amdgcn_readfirstlane((int)load4_sc1(flat_rsrc(a.list, (int64_t)a.most * 4), r * 4));
+            const auto pairs = flat_rsrc(a.pairs, (int64_t)a.most * ROWS * 2);
+            pair01 = load4_sc1(pairs, (r * ROWS + 4 * (lane >> 4)) * 2);
+            pair23 = load4_sc1(pairs, (r * ROWS + 4 * (lane >> 4)) * 2 + 4);
         }
-    // two channels to a word; rows of the upper half of the lanes are remainders where PARTS = 1
-    const int P = a.T * a.K;
-    const auto h = flat_rsrc(a.h, (int64_t)P * a.I * 4);
+        const auto w = window(a.gateup + e * a.gateup_stride + (int64_t)2 * cp * steps * MX_BLOCK_BYTES,
+                              2 * (int64_t)steps * MX_BLOCK_BYTES, go);
+        u32x4_t codes[AHEAD][2];
+        uint32_t scales[AHEAD][2];
+        auto load = [&](int slot, int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-        const float v = silu_f32(sum[0][k]) * sum[1][k], after = __shfl_down(v, 1);
-        const int pair = (int16_t)((k < 2 ? pair01 : pair23) >> (16 * (k % 2))), token = 4 * (lane >> 4) + k;
-        const bool keep = pair >= 0 && token < a.T && lane % 2 == 0;
-        uint32_t high, rest;
-        split(v, after, high, rest);
-        store4_sc1(h, keep ? (pair * a.I + cp * 16 + (lane & 15)) * 2 : OUTSIDE, high);
-        store4_sc1(h, keep ? ((P + pair) * a.I + cp * 16 + (lane & 15)) * 2 : OUTSIDE, rest);
+            for (int j = 0; j < 2; j++) {
+                const int off = s < steps ? (j * steps + s) * MX_BLOCK_BYTES : OUTSIDE;
+                codes[slot][j] = fetch16<CPOL_NT>(w, off + lane * 16);
+                scales[slot][j] = fetch4<CPOL_NT>(w, off + MX_CODE_BYTES + 4 * (lane & 15));
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < AHEAD; i++)
+            load(i, i);
+        asm volatile("" ::: "memory");
+        if (go && !wait_z<HELP>(a, seen, sh))
+            return false;
+        z_there = go;
+        fetch(0);
+        f32x4_t acc[PARTS][2] = {}, sum[2] = {};
+        int quarter = 1;   // ends at this many fourths of the steps; with fewer than four, some are empty
+        while (steps * quarter / REST_WAVES == 0)
+            quarter++;
+        int half = 0;   // which half of LDS: a wave that writes it has seen every wave past the chunk before the last
+#pragma unroll 1
+        for (int s = 0; s < (go ? steps : 1); s += AHEAD)
+#pragma unroll
+            for (int c = 0; c < PARTS; c++, half ^= 1) {
+                uint32_t *chunk = lds + half * ROWS * PARTS * PITCH;
+                const uint32_t *mine = chunk + (lane & 15) * PITCH + (lane >> 4) * 4;
+#pragma unroll
+                for (int i = 0; i < PIECES; i++) {
+                    const int p = i * NTHR + t;
+                    *reinterpret_cast<u32x4_t *>(chunk + p / (STEPS * 16) * PITCH + p % (STEPS * 16) * 4) = zs[i];
+                }
+                fetch(s + (c + 1) * STEPS);
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < STEPS; i++) {   // steps past the end multiply zeros
+                    const int slot = c * STEPS + i;
+                    mx_steps<PARTS>(codes[slot], scales[slot], mine + i * (MX_STEP / 2), ROWS * PITCH, acc);
+                    if (s + slot + 1 == steps * quarter / REST_WAVES) {
+#pragma unroll
+                        for (int j = 0; j < 2; j++) {
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {
+                                const float rest = PARTS == 1 ? __shfl_xor(acc[0][j][k], 32) : acc[PARTS - 1][j][k];
+                                sum[j][k] += a.has_latent ? acc[0][j][k] + rest : acc[0][j][k];
+                            }
+#pragma unroll
+                            for (int p = 0; p < PARTS; p++)
+                                acc[p][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                        }
+                        while (steps * quarter / REST_WAVES == s + slot + 1)
+                            quarter++;
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    load(slot, s + slot + AHEAD);
+                }
+            }
+        // two channels to a word; rows of the upper half of the lanes are remainders where PARTS = 1
+        const int P = a.T * a.K;
+        const auto h = flat_rsrc(a.h, (int64_t)P * a.I * 4);
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float v = silu_f32(sum[0][k]) * sum[1][k], after = __shfl_down(v, 1);
+            const int pair = (int16_t)((k < 2 ? pair01 : pair23) >> (16 * (k % 2))), token = 4 * (lane >> 4) + k;
+            const bool keep = go && pair >= 0 && token < a.T && lane % 2 == 0;
+            uint32_t high, rest;
+            split(v, after, high, rest);
+            store4_sc1(h, keep ? (pair * a.I + cp * 16 + (lane & 15)) * 2 : OUTSIDE, high);
+            store4_sc1(h, keep ? ((P + pair) * a.I + cp * 16 + (lane & 15)) * 2 : OUTSIDE, rest);
+        }
+        __syncthreads();   // LDS is free for the next pass
     }
     arrive(decode_gates(a, r));
     return true;
@@ -836,7 +847,7 @@ __device__ __forceinline__ bool down_item(const DecodeArgs &a, int item, const S
     const int lane = lane_id(), t = threadIdx.x, span = decode_down_span(a), per = decode_down_items(a), r = item / per, g0 = item % per * span;
     const int groups = min(span, decode_groups(a) - g0), steps = a.I / MX_STEP, P = a.T * a.K, blocks = a.Lt / 16;
 #pragma unroll 1
-    for (int go = HELP ? 1 : 0; go < 2; go++) {
+    for (int go = 1 - seen.first_pass; go < 2; go++) {
         int e = 0, from[PIECES];   // this thread's pieces of h and the remainders: the row and the column, in bytes
 #pragma unroll
         for (int i = 0; i < PIECES; i++)
@@ -1068,8 +1079,14 @@ __global__ __launch_bounds__(WAVE *REST_WAVES, 3) void decode_kernel(const Decod
     const int item = blockIdx.x;
     const bool late = item < n.router + n.latent ||   // claimed in front_product
                       (item >= n.router + n.latent + n.top + n.gate && item < n.router + n.latent + n.top + n.gate + n.shared);
-    const Seen seen{ask(flag(a, DECODE_READY, item % FLAGS)), ask(flag(a, DECODE_Z_DONE, item % FLAGS))};   // come with the claim
-    if ((!late && !claim<false>(a, item, &sh)) || do_item<FEW, false>(n, item, seen, lds, &sh))
+    Seen seen{ask(flag(a, DECODE_READY, item % FLAGS)), ask(flag(a, DECODE_Z_DONE, item % FLAGS)), 0};   // come with the claim
+    if (!late) {
+        if (!claim<false>(a, item, &sh, seen.ready == 0u ? 2u : 0u))
+            return;
+        seen.first_pass = __builtin_amdgcn_readfirstlane((int)sh) >> 1;   // one wave's answer for all
+        __syncthreads();
+    }
+    if (do_item<FEW, false>(n, item, seen, lds, &sh))
         return;
     int kind = 0;   // the first item of this one's kind
     for (const int size : {n.router, n.latent, n.top, n.gate, n.shared, n.down, n.sums})
@@ -1080,7 +1097,7 @@ __global__ __launch_bounds__(WAVE *REST_WAVES, 3) void decode_kernel(const Decod
 #pragma unroll 1
     for (int i = 0; i <= kind; i++)   // the earlier kinds' items that are still free, and then this one
         if (i == kind || claim<true>(a, i, &sh))
-            do_item<FEW, true>(n, i == kind ? item : i, Seen{0u, 0u}, lds, &sh);
+            do_item<FEW, true>(n, i == kind ? item : i, Seen{0u, 0u, 0}, lds, &sh);
 }
 
 // Counters, flags and claims at zero.
