@@ -14,7 +14,7 @@
 //    out     16 output columns: out = bf16([zc | h_s] [W_up | W_ds]^T)
 // so that the memory's rate is not lost at the borders of launches: an item's first weights are asked for before what it
 // waits for is there. One token takes 53 us (3.5 TB/s), and 68 as separate launches (moe_route_forward); 4 tokens 75 and
-// 82, 8 104 and 104, 16 173 and 136: with many experts an item's start, 5 us of claiming and looking up while its place
+// 82, 8 97 and 103, 16 170 and 136: with many experts an item's start, 5 us of claiming and looking up while its place
 // waits, costs more than the launches. One token's way: z after 16 us, the experts 19, h 31, y 37, zc 41, out 52.
 //
 // z and h are kept in two BF16 parts, the rounded value and what the rounding left: their rounding alone reaches every
@@ -35,7 +35,8 @@
 // Two things set the pace of code that runs once. Instructions come from memory at about 1 KiB a microsecond the first
 // time: so while an item waits it goes once through what it will do, with empty windows for its loads and stores
 // (`go` = 0). And a load under a condition is a wait for the loads before it: so no load of weights has one; loads past the
-// end lie outside their window, which costs nothing.
+// end lie outside their window, which costs nothing. Workgroups that start when the experts are known leave the first pass out
+// (with it in every down item, and none before the gate items of several tokens, 8 tokens took 104 us, 97 so).
 //
 // Three workgroups share a CU (168 registers a thread). With four of 128, whose items spill some, more of them start
 // early, but one token took 61 us.

@@ -54,6 +54,8 @@ SHAPES_FEW = [
     shape(T=12, E=1024, K=3, H=512), shape(T=13, I=384, Lt=384), shape(T=16, E=33, K=32, I=256, S=3, Is=32),
     shape(T=16, H=1024, Lt=1152, E=100, K=6), shape(T=1, H=0, latent=False, S=0, Is=0, Lt=512),
     shape(T=6, H=0, latent=False, S=0, Is=0, E=61, K=6, I=512), shape(T=16, H=0, latent=False, S=0, Is=0, E=16, K=16),
+    # more down items than places: two groups of columns to an item, the last one short, over one part of K and over two
+    shape(T=8, Lt=896, E=260, K=32), shape(T=16, Lt=384, E=400, K=30, I=512),
     shape(T=16, E=90, routing="zipf"), shape(T=3, E=1, K=1), shape(T=16, E=1, K=1), shape(T=11, H=128, Lt=128, Is=32),
 ]
 
