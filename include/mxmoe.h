@@ -216,8 +216,9 @@ moe_status moe_route_forward_static(moe_handle *h, const void *x, int32_t T, con
 /* The whole layer for up to MOE_DECODE_MAX_T tokens in one kernel (and one that clears its counters): a few tokens' step
  * (page "Kimi K3.1 Pro on AMD Instinct GPUs", sections "Serving with ATOM / What we optimized", paragraph "Mono decode", and
  * "Serving with vLLM / What we optimized", paragraph on fused low-latency decode). It computes what moe_route_forward does
- * on the same packed weights, without the arrays of moe_routing, and nearer to the exact result: z and an expert's inner
- * values are kept in two BF16 parts, its output y in FP32 until the weighted sum. So outputs are near moe_route_forward's,
+ * on the same packed weights, without the arrays of moe_routing, and nearer to the exact result: z, the experts' inner values
+ * and the weighted sum are kept in two BF16 parts (16 bits), an expert's output y in FP32 until the sum, so that the
+ * output's own rounding is nearly all that it is off by. So outputs are near moe_route_forward's,
  * not the same bits; ids and weights follow from logits whose sums are added in another order too. A token's outputs are the
  * same bits whatever tokens come with it. It is the faster of the two for up to about eight tokens.
  * x: bf16 [T, Hin]; logit_bias: fp32 [E] or NULL; logits_out: fp32 [T, E] or NULL; topk_ids [T, K] and topk_w [T, K] or

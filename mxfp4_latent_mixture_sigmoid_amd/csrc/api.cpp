@@ -1037,7 +1037,7 @@ namespace {
 int decode_patience = DECODE_PATIENCE;
 
 struct DecodeLayout {
-    int64_t counters, claims, partial, logits, weights, chosen, list, pairs, z, z_rest, acat, h, total;
+    int64_t counters, claims, partial, logits, weights, chosen, list, pairs, z, z_rest, h, total;
     int64_t most;   // distinct experts
 };
 
@@ -1051,7 +1051,7 @@ DecodeLayout decode_layout(const moe_config *c, int64_t T)
         at = off;
         off = align_up(off + bytes);
     };
-    const int64_t lat = c->has_latent_proj ? 1 : 0, Lt = c->latent,
+    const int64_t lat = c->has_latent_proj ? 1 : 0, Lt = c->latent, shared = S * c->shared_inter,
                   groups = (Lt + DECODE_DOWN_COLUMNS - 1) / DECODE_DOWN_COLUMNS, quads = (T + 3) / 4;
     part(L.counters, (DECODE_SHARED_LINES + L.most + groups) * DECODE_COUNTER_WORDS * 4);
     part(L.claims, ((E + 15) / 16 * DECODE_ROUTER_PARTS + lat * (Lt + S * c->shared_inter + c->hidden) / 16 + quads * (1 + groups) +
@@ -1062,9 +1062,11 @@ DecodeLayout decode_layout(const moe_config *c, int64_t T)
     part(L.chosen, T * K * 4);
     part(L.list, L.most * 4);
     part(L.pairs, L.most * DECODE_MAX_T * 2);
-    part(L.z, lat * T * Lt * 2);
-    part(L.z_rest, lat * T * Lt * 2);
-    part(L.acat, lat * T * (Lt + S * c->shared_inter) * 2);
+    const int64_t z = off;
+    part(L.z, lat * T * (Lt + shared) * 2);
+    part(L.z_rest, lat * T * (Lt + shared) * 2);
+    // The size that callers have been told before is kept: zc and h_s had a matrix of their own.
+    off = std::max(off, z + 2 * align_up(lat * T * Lt * 2) + align_up(lat * T * (Lt + shared) * 2));
     part(L.h, 2 * T * K * c->inter * 2);
     L.total = off;
     return L;
@@ -1159,8 +1161,7 @@ moe_status moe_decode(moe_handle *h, const void *x, int32_t T, const float *logi
     a.z_rest = reinterpret_cast<uint16_t *>(ws + L.z_rest);
     a.most = (int)L.most;
     a.z = lat ? reinterpret_cast<uint16_t *>(ws + L.z) : const_cast<uint16_t *>(a.x);
-    a.acat = reinterpret_cast<uint16_t *>(ws + L.acat);
-    a.ldcat = (int)(c->latent + shared);
+    a.ldz = (int)(c->latent + shared);
     a.h = reinterpret_cast<uint16_t *>(ws + L.h);
     a.ids_out = topk_ids;
     a.weights_out = topk_w;

@@ -8,19 +8,21 @@
 //    latent  16 columns of z = x W_down^T
 //    top     the top-K of 4 tokens; the list of distinct experts and each one's tokens
 //    gate    (expert, 16 or 64 inner channels): h = silu(z Wg^T) (z Wu^T) of the expert's tokens
-//    shared  16 channels of h_s = bf16(silu(x Wg_s^T) (x Wu_s^T))
+//    shared  16 channels of h_s = silu(x Wg_s^T) (x Wu_s^T)
 //    down    (expert, 256 or 512 latent columns): y = h Wd^T of the expert's tokens, in FP32
-//    sums    (4 tokens, 256 latent columns): zc = bf16(sum w y), in slot order
+//    sums    (4 tokens, 256 latent columns): zc = sum w y, in slot order
 //    out     16 output columns: out = bf16([zc | h_s] [W_up | W_ds]^T)
 // so that the memory's rate is not lost at the borders of launches: an item's first weights are asked for before what it
 // waits for is there. One token takes 53 us (3.5 TB/s), and 68 as separate launches (moe_route_forward); 4 tokens 75 and
 // 82, 8 97 and 103, 16 170 and 136: with many experts an item's start, 5 us of claiming and looking up while its place
 // waits, costs more than the launches. One token's way: z after 16 us, the experts 19, h 31, y 37, zc 41, out 52.
 //
-// z and h are kept in two BF16 parts, the rounded value and what the rounding left: their rounding alone reaches every
-// expert's products (0.4% of the layer's output in the mean square; with both, zc's, h_s's and the output's own are what is
-// left, 0.24%). The remainders are rows 8 to 15 of the tile for up to 8 tokens, at no cost that was seen, and a second
-// operand for more (16 tokens: 190 us, 178 with h rounded, when it was added).
+// z, h, h_s and zc are kept in two BF16 parts, the rounded value and what the rounding left, 16 bits of each value: rounded to
+// one, z and h cost 0.4% of the layer's output in the mean square, h_s and zc 0.17%; with both parts the output's own
+// rounding is what is left, 0.17%. The remainders are rows 8 to 15 of the tile for up to 8 tokens, and a second operand
+// for more (16 tokens: 190 us, 178 with h rounded, when it was added). The output product reads twice the activations for
+// them: 4 tokens 75.4 us (74.8 without), 8 98.6 (97.0), 16 166 (166), where zc and h_s lie as z does; 80, 105 and 181 with
+// zc among y.
 //
 // Kinds wait for each other on flags. A workgroup takes the item of its number by claiming it; it waits for a flag PATIENCE
 // times, far longer than a call takes, and if the flag has not come by then (its workgroups may not even have started:
@@ -52,7 +54,9 @@ constexpr int ROWS = DECODE_MAX_T, HALF = ROWS / 2;
 constexpr int REST_WAVES = 4, ROUTER_PARTS = DECODE_ROUTER_PARTS;
 constexpr int FLAGS = WAVE;                 // places of a flag
 constexpr int STAGE_WORDS = DECODE_STAGE_WORDS;
-constexpr int LDS_WORDS = REST_WAVES * STAGE_WORDS + REST_WAVES * 512;   // of an item; three workgroups share a CU
+constexpr int OUT_STAGE_WORDS = DECODE_OUT_STAGE_WORDS;
+constexpr int LDS_WORDS = REST_WAVES * (STAGE_WORDS + 512 > OUT_STAGE_WORDS ? STAGE_WORDS + 512 : OUT_STAGE_WORDS);   // of an item
+static_assert((LDS_WORDS * 4 + 16 + 1279) / 1280 * 1280 * 3 <= 160 * 1024, "three workgroups share a CU");
 
 __device__ __forceinline__ uint32_t *counter(const DecodeArgs &a, int i) { return a.counters + i * DECODE_COUNTER_WORDS; }
 __device__ __forceinline__ uint32_t *flag(const DecodeArgs &a, int i, int place) { return counter(a, DECODE_FLAGS + i * FLAGS + place); }
@@ -107,11 +111,15 @@ __device__ __forceinline__ float total(const float *red, int stride, int at)
 // DEPTH steps ahead, the first before anything is known of the activations. Those go through the wave's part of LDS: all of
 // them where they fit (CHUNK = 0: few tokens), else CHUNK steps at a time, each chunk loaded while the one before it is
 // multiplied. (Straight to registers a step's operand is 64 bytes of every row: 8 tokens 111 us in place of 104.)
-template <int NB, int DEPTH, int CHUNK>
+//
+// REST: activations come with what their rounding to BF16 left, which is multiplied as well: 1, in rows 8 to 15 of the operand, of up
+// to 8 tokens; 2, as a second operand, of more.
+template <int NB, int DEPTH, int CHUNK, int REST = 0>
 struct Bf16Part {
     static_assert(CHUNK == 0 || DEPTH % CHUNK == 0, "slots");
+    static constexpr int WORDS = REST ? OUT_STAGE_WORDS : STAGE_WORDS, OPERANDS = REST == 2 ? 2 : 1;
     // Whether K values of T tokens, divided among the waves, fit their parts of LDS.
-    static __device__ bool fits(int T, int K, int waves) { return T * ((K / BF16_STEP + waves - 1) / waves * 16 + 4) <= STAGE_WORDS; }
+    static __device__ bool fits(int T, int K, int waves) { return T * (REST ? 2 : 1) * ((K / BF16_STEP + waves - 1) / waves * 16 + 4) <= WORDS; }
     u32x4_t b[DEPTH][NB];
     __amdgpu_buffer_rsrc_t w;
     int s0, s1, next, at, jump, last, tail;   // steps; the next step's first block
@@ -144,54 +152,83 @@ struct Bf16Part {
             load(i);
         asm volatile("" ::: "memory");   // issued here
     }
-    // get(row, k, in): 16 bytes of a token's activations from column k on, or zeros.
+    // get(row, k, in, i): 16 bytes of a token's activations from column k on, or zeros; i = 1: of their remainders.
+    struct Loaded {
+        u32x4_t v[REST ? 2 : 1];
+    };
     template <class Get>
-    __device__ __forceinline__ void finish(int T, uint32_t *stage, f32x4_t (&acc)[NB], Get get)
+    static __device__ __forceinline__ Loaded loaded(Get &get, int row, int k, bool in)
+    {
+        Loaded l;
+#pragma unroll
+        for (int i = 0; i < (REST ? 2 : 1); i++)
+            l.v[i] = get(row, k, in, i);
+        return l;
+    }
+    // The values to `at`, the remainders `rest` words further.
+    static __device__ __forceinline__ void put(const Loaded &l, uint32_t *at, int rest)
+    {
+#pragma unroll
+        for (int i = 0; i < (REST ? 2 : 1); i++)
+            *reinterpret_cast<u32x4_t *>(at + i * rest) = l.v[i];
+    }
+    // One step: `at` is this lane's place in the first operand, the second is `second` words further.
+    __device__ __forceinline__ void multiply(const uint32_t *at, int second, int slot, bool in, f32x4_t (&acc)[OPERANDS][NB])
+    {
+#pragma unroll
+        for (int p = 0; p < OPERANDS; p++) {
+            const u32x4_t x = *reinterpret_cast<const u32x4_t *>(at + p * second);
+#pragma unroll
+            for (int j = 0; j < NB; j++)
+                acc[p][j] = step(x, b[slot][j], acc[p][j], in);
+        }
+    }
+    template <class Get>
+    __device__ __forceinline__ void finish(int T, uint32_t *stage, f32x4_t (&acc)[OPERANDS][NB], Get get)
     {
         const int lane = lane_id(), n = s1 - s0;
         // rows past the tokens repeat the last one: their sums are not used. Steps past the end multiply zeros.
-        const int r = min(lane & 15, T - 1), c = lane >> 4;
+        const int row = lane & 15, r = min(REST == 1 ? row % HALF : row, T - 1), c = lane >> 4;
         if constexpr (CHUNK == 0) {
+            static_assert(REST < 2, "one operand");
             const int pitch = n * 16 + 4;   // words of a token's part in LDS
 #pragma unroll 1
             for (int i0 = 0; i0 < T * n * 4; i0 += 4 * WAVE) {
-                u32x4_t v[4];
+                Loaded v[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const int at = min(i0 + i * WAVE + lane, T * n * 4 - 1);
-                    v[i] = get(at / (n * 4), s0 * BF16_STEP + at % (n * 4) * 8, true);
+                    v[i] = loaded(get, at / (n * 4), s0 * BF16_STEP + at % (n * 4) * 8, true);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const int at = min(i0 + i * WAVE + lane, T * n * 4 - 1);
-                    *reinterpret_cast<u32x4_t *>(stage + at / (n * 4) * pitch + at % (n * 4) * 4) = v[i];
+                    put(v[i], stage + at / (n * 4) * pitch + at % (n * 4) * 4, T * pitch);
                 }
             }
-            const uint32_t *mine = stage + r * pitch + c * 4;
+            const uint32_t *mine = stage + ((REST == 1 && row >= HALF ? T : 0) + r) * pitch + c * 4;
 #pragma unroll 1
             for (int s = 0; s < n; s += DEPTH)
 #pragma unroll
                 for (int i = 0; i < DEPTH; i++) {
-                    const u32x4_t x = *reinterpret_cast<const u32x4_t *>(mine + min(s + i, n - 1) * 16);
-#pragma unroll
-                    for (int j = 0; j < NB; j++)
-                        acc[j] = step(x, b[i][j], acc[j], s + i < n);
+                    multiply(mine + min(s + i, n - 1) * 16, 0, i, s + i < n, acc);
                     load(i);
                     if (i % 4 == 3)
                         __builtin_amdgcn_sched_barrier(0);   // not all operands at once
                 }
         } else {
-            constexpr int PITCH = CHUNK * 16 + 4, PER_ROW = CHUNK * 4, PIECES = STAGE_WORDS / PITCH * PER_ROW / WAVE;
-            static_assert(STAGE_WORDS / PITCH * PER_ROW % WAVE == 0, "pieces");
-            u32x4_t v[PIECES];
+            constexpr int PITCH = CHUNK * 16 + 4, PER_ROW = CHUNK * 4, TOKENS = REST == 0 ? WORDS / PITCH : REST == 1 ? HALF : ROWS;
+            constexpr int PIECES = TOKENS * PER_ROW / WAVE, SECOND = TOKENS * PITCH;
+            static_assert(TOKENS * PER_ROW % WAVE == 0 && TOKENS * (REST ? 2 : 1) * PITCH <= WORDS, "pieces; room");
+            Loaded v[PIECES];
             auto fetch = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
                 for (int i = 0; i < PIECES; i++) {
-                    const int at = i * WAVE + lane, row = at / PER_ROW, col = at % PER_ROW;
-                    v[i] = get(row, (s0 + s) * BF16_STEP + col * 8, row < T && s + col / 4 < n);
+                    const int at = i * WAVE + lane, token = at / PER_ROW, col = at % PER_ROW;
+                    v[i] = loaded(get, token, (s0 + s) * BF16_STEP + col * 8, token < T && s + col / 4 < n);
                 }
             };
-            const uint32_t *mine = stage + r * PITCH + c * 4;
+            const uint32_t *mine = stage + (REST == 1 && row >= HALF ? SECOND : 0) + r * PITCH + c * 4;
             fetch(0);
 #pragma unroll 1
             for (int s = 0; s < n; s += DEPTH)
@@ -199,14 +236,11 @@ struct Bf16Part {
                 for (int h = 0; h < DEPTH; h += CHUNK) {
 #pragma unroll
                     for (int i = 0; i < PIECES; i++)
-                        *reinterpret_cast<u32x4_t *>(stage + (i * WAVE + lane) / PER_ROW * PITCH + (i * WAVE + lane) % PER_ROW * 4) = v[i];
+                        put(v[i], stage + (i * WAVE + lane) / PER_ROW * PITCH + (i * WAVE + lane) % PER_ROW * 4, SECOND);
                     fetch(s + h + CHUNK);
 #pragma unroll
                     for (int i = 0; i < CHUNK; i++) {
-                        const u32x4_t x = *reinterpret_cast<const u32x4_t *>(mine + i * 16);
-#pragma unroll
-                        for (int j = 0; j < NB; j++)
-                            acc[j] = step(x, b[h + i][j], acc[j], s + h + i < n);
+                        multiply(mine + i * 16, SECOND, h + i, s + h + i < n, acc);
                         load(h + i);
                         if (i % 4 == 3)
                             __builtin_amdgcn_sched_barrier(0);
@@ -320,12 +354,12 @@ __device__ __forceinline__ bool front_product(const DecodeArgs &a, const uint8_t
 {
     const int wv = wave_id();
     const auto x = flat_rsrc(a.x, (int64_t)a.T * a.Hin * 2);
-    f32x4_t acc[NB] = {};
+    f32x4_t acc[1][NB] = {};
     auto run = [&](auto part) __attribute__((always_inline)) {
         part.start(w, rows, a.Hin, block, part_of_k * REST_WAVES + wv, parts * REST_WAVES);
         if (!HELP && !claim<false>(a, blockIdx.x, sh))
             return false;
-        part.finish(a.T, lds + wv * STAGE_WORDS, acc, [&](int r, int k, bool in) __attribute__((always_inline)) { return fetch16<0>(x, in ? (r * a.Hin + k) * 2 : OUTSIDE); });
+        part.finish(a.T, lds + wv * STAGE_WORDS, acc, [&](int r, int k, bool in, int) __attribute__((always_inline)) { return fetch16<0>(x, in ? (r * a.Hin + k) * 2 : OUTSIDE); });
         return true;
     };
     using Staged = Bf16Part<NB, 16 / NB, 0>;
@@ -335,7 +369,7 @@ __device__ __forceinline__ bool front_product(const DecodeArgs &a, const uint8_t
     float *red = reinterpret_cast<float *>(lds);
 #pragma unroll
     for (int j = 0; j < NB; j++)
-        store_sums(red + (wv * NB + j) * 256, acc[j]);
+        store_sums(red + (wv * NB + j) * 256, acc[0][j]);
     __syncthreads();
     return true;
 }
@@ -367,9 +401,9 @@ __device__ __forceinline__ void latent_item(const DecodeArgs &a, int item, int i
         const float v0 = total<REST_WAVES>(red, 256, row * 16 + c), v1 = total<REST_WAVES>(red, 256, row * 16 + c + 1);
         uint32_t high, rest;
         split(v0, v1, high, rest);
-        const int at = (row * a.Lt + item * 16 + c) * 2;
-        store4_sc1(flat_rsrc(a.z, (int64_t)a.T * a.Lt * 2), at, high);
-        store4_sc1(flat_rsrc(a.z_rest, (int64_t)a.T * a.Lt * 2), at, rest);
+        const int at = (row * a.ldz + item * 16 + c) * 2;
+        store4_sc1(flat_rsrc(a.z, (int64_t)a.T * a.ldz * 2), at, high);
+        store4_sc1(flat_rsrc(a.z_rest, (int64_t)a.T * a.ldz * 2), at, rest);
     }
     stores_done();
     if (wave_id() != 0)
@@ -393,7 +427,11 @@ __device__ __forceinline__ void shared_item(const DecodeArgs &a, int item, uint3
 #pragma unroll
         for (int i = 0; i < 2; i++)
             v[i] = silu_f32(total<REST_WAVES>(red, 512, i)) * total<REST_WAVES>(red, 512, 256 + i);
-        store4_sc1(flat_rsrc(a.acat, (int64_t)a.T * a.ldcat * 2), (row * a.ldcat + a.Lt + item * 16 + c) * 2, pack_bf16x2(v[0], v[1]));
+        uint32_t high, rest;
+        split(v[0], v[1], high, rest);
+        const int at = (row * a.ldz + a.Lt + item * 16 + c) * 2;
+        store4_sc1(flat_rsrc(a.z, (int64_t)a.T * a.ldz * 2), at, high);
+        store4_sc1(flat_rsrc(a.z_rest, (int64_t)a.T * a.ldz * 2), at, rest);
     }
     arrive_out(a);
 }
@@ -730,14 +768,14 @@ __device__ __forceinline__ bool gate_many(const DecodeArgs &a, int item, const S
     // piece i of this thread: 8 values of row i (t / 16 ..): a token's z, or HALF or ROWS rows further its remainders.
     // Rows past the tokens are zeros, and everything in the first pass.
     int z_there = 0;
-    const auto z0 = flat_rsrc(a.z, (int64_t)a.T * a.Lt * 2), z1 = flat_rsrc(a.has_latent ? a.z_rest : a.z, (int64_t)a.T * a.Lt * 2);
+    const auto z0 = flat_rsrc(a.z, (int64_t)a.T * a.ldz * 2), z1 = flat_rsrc(a.has_latent ? a.z_rest : a.z, (int64_t)a.T * a.ldz * 2);
     u32x4_t zs[PIECES];
     auto fetch = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < PIECES; i++) {
             const int p = i * NTHR + t, row = p / (STEPS * 16), c = p % (STEPS * 16);
             const int token = row % (PARTS == 1 ? HALF : ROWS), k = s * MX_STEP + c * 8;
-            zs[i] = fetch16<CPOL_SC1>(row >= (PARTS == 1 ? HALF : ROWS) ? z1 : z0, z_there && k < a.Lt && token < a.T ? (token * a.Lt + k) * 2 : OUTSIDE);
+            zs[i] = fetch16<CPOL_SC1>(row >= (PARTS == 1 ? HALF : ROWS) ? z1 : z0, z_there && k < a.Lt && token < a.T ? (token * a.ldz + k) * 2 : OUTSIDE);
         }
     };
 #pragma unroll 1
@@ -981,10 +1019,17 @@ __device__ __forceinline__ bool sum_item(const DecodeArgs &a, int item, const Se
                 for (int i = 0; i < 4; i++)
                     v[i] = j0 + j < K ? fmaf(w[j], __uint_as_float(ys[j][i]), v[i]) : v[i];
         }
-        const auto to = a.has_latent ? window(a.acat, (int64_t)a.T * a.ldcat * 2, go) : window(a.out, (int64_t)a.T * a.Lt * 2, go);
-        const int at = live ? (token * (a.has_latent ? a.ldcat : a.Lt) + col) * 2 : OUTSIDE;
-        store4_sc1(to, at, pack_bf16x2(v[0], v[1]));
-        store4_sc1(to, at + 4, pack_bf16x2(v[2], v[3]));
+        // zc in the place of z, which every listed expert has been multiplied with: all their down items are done
+        const auto to = window(a.has_latent ? a.z : a.out, (int64_t)a.T * a.ldz * 2, go);
+        const auto left = window(a.z_rest, (int64_t)a.T * a.ldz * 2, go && a.has_latent);
+        const int at = live ? (token * a.ldz + col) * 2 : OUTSIDE;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            uint32_t high, rest;
+            split(v[2 * i], v[2 * i + 1], high, rest);
+            store4_sc1(to, at + 4 * i, high);
+            store4_sc1(left, at + 4 * i, rest);
+        }
     }
     if (a.has_latent)
         arrive_out(a);
@@ -994,33 +1039,46 @@ __device__ __forceinline__ bool sum_item(const DecodeArgs &a, int item, const Se
 template <bool FEW, bool HELP>
 __device__ __forceinline__ bool out_item(const DecodeArgs &a, int item, uint32_t *lds, uint32_t *sh)
 {
-    const int wv = wave_id(), t = threadIdx.x, row = t / 8, c = t % 8 * 2;
-    float *red = reinterpret_cast<float *>(lds + REST_WAVES * STAGE_WORDS);
+    const int wv = wave_id(), t = threadIdx.x, row = t / 8, c = t % 8 * 2, cat = a.ldz;
+    float *red = reinterpret_cast<float *>(lds);
     const auto out = flat_rsrc(a.out, (int64_t)a.T * a.H * 2);
     auto run = [&](auto part) __attribute__((always_inline)) {
+        using Part = decltype(part);
 #pragma unroll 1
         for (int go = !HELP && a.T <= 2 ? 0 : 1; go < 2; go++) {   // of more tokens it delays the weights (4: 84 us, 81 without)
-            part.start(a.w_out, a.H, a.ldcat, item, wv, REST_WAVES, go);
+            part.start(a.w_out, a.H, cat, item, wv, REST_WAVES, go);
             if (go && wait_for<HELP>(a, flag(a, DECODE_CAT_DONE, blockIdx.x % FLAGS), 1u, sh) < 0)
                 return false;
-            const auto acat = window(a.acat, (int64_t)a.T * a.ldcat * 2, go);
-            f32x4_t acc[1] = {};
-            part.finish(a.T, lds + wv * STAGE_WORDS, acc,
-                        [&](int r, int k, bool in) __attribute__((always_inline)) { return fetch16<CPOL_SC1>(acat, in ? (r * a.ldcat + k) * 2 : OUTSIDE); });
-            store_sums(red + wv * 256, acc[0]);
+            const auto high = window(a.z, (int64_t)a.T * cat * 2, go), rest = window(a.z_rest, (int64_t)a.T * cat * 2, go);
+            f32x4_t acc[Part::OPERANDS][1] = {};
+            part.finish(a.T, lds + wv * OUT_STAGE_WORDS, acc, [&](int r, int k, bool in, int i) __attribute__((always_inline)) {
+                return fetch16<CPOL_SC1>(i ? rest : high, in ? (r * cat + k) * 2 : OUTSIDE);
+            });
+            __syncthreads();   // the sums take the place of the activations
+            store_sums(red + wv * 256, FEW ? acc[0][0] : acc[0][0] + acc[Part::OPERANDS - 1][0]);
             __syncthreads();
-            if (row < a.T && row < ROWS)
-                __builtin_amdgcn_raw_buffer_store_b32((int)pack_bf16x2(total<REST_WAVES>(red, 256, row * 16 + c),
-                                                                       total<REST_WAVES>(red, 256, row * 16 + c + 1)),
-                                                      out, go ? (row * a.H + item * 16 + c) * 2 : OUTSIDE, 0, 0);
+            if (row < a.T && row < ROWS) {
+                float v[2] = {0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < REST_WAVES; w++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const float *p = red + w * 256 + row * 16 + c + i;
+                        v[i] += FEW ? p[0] + p[HALF * 16] : p[0];
+                    }
+                __builtin_amdgcn_raw_buffer_store_b32((int)pack_bf16x2(v[0], v[1]), out, go ? (row * a.H + item * 16 + c) * 2 : OUTSIDE, 0, 0);
+            }
             __syncthreads();
         }
         return true;
     };
-    if constexpr (FEW)
-        if (using Staged = Bf16Part<1, 16, 0>; Staged::fits(a.T, a.ldcat, REST_WAVES))
+    if constexpr (FEW) {
+        if (using Staged = Bf16Part<1, 16, 0, 1>; Staged::fits(a.T, cat, REST_WAVES))
             return run(Staged());
-    return run(Bf16Part<1, 14, FEW ? 14 : 7>());
+        return run(Bf16Part<1, 12, 6, 1>());
+    } else {
+        return run(Bf16Part<1, 12, 6, 2>());
+    }
 }
 
 // The kernel's arguments, read from memory again: they do not fit the scalar registers all at once.

@@ -9,7 +9,7 @@ namespace mxmoe {
 constexpr int DECODE_MAX_T = MOE_DECODE_MAX_T;   // the rows of a matrix-core tile
 
 constexpr int DECODE_MAX_E = 1024;
-constexpr int DECODE_MAX_WINDOW = 0x7FFF0000;    // bytes of a matrix, of h and of [zc | h_s]
+constexpr int DECODE_MAX_WINDOW = 0x7FFF0000;    // bytes of a matrix, of h, y and [z | h_s]
 
 // One to a cache line: counters (z has DECODE_ARMS and one more for their last arrivals); three flags, each in 64 places; then
 // a counter for every expert of the list and one for every 256 columns.
@@ -21,6 +21,7 @@ constexpr int DECODE_PATIENCE = 1000;        // times that a flag is asked for, 
 constexpr int DECODE_DOWN_COLUMNS = 256;     // of a workgroup in the down product
 constexpr int DECODE_ROUTER_PARTS = 4;       // workgroups that share 16 of the router's rows
 constexpr int DECODE_STAGE_WORDS = 1856;     // LDS of a wave for its activations
+constexpr int DECODE_OUT_STAGE_WORDS = 3200; // ... in the output product, whose activations come with their remainders
 
 // Work items, numbered kind after kind; a kind waits for earlier ones only.
 struct DecodeItems {
@@ -47,10 +48,9 @@ struct DecodeArgs {
     int32_t *list;                   // [most] distinct experts, ascending
     int16_t *pairs;                  // [most, 16] the pair of (expert, token), or -1
     int most;                        // min(T K, E)
-    uint16_t *z;                     // [T, Lt]; x itself without latent projections
-    uint16_t *z_rest;                // [T, Lt] what z's rounding left; unused without latent projections
-    uint16_t *acat;                  // [T, ldcat]: zc, then h_s
-    int ldcat;
+    uint16_t *z;                     // [T, ldz]: z, and zc in its place when every expert is done with it, then h_s; x itself without latent projections
+    uint16_t *z_rest;                // [T, ldz]: what their rounding left; unused without latent projections
+    int ldz;                         // Lt + shared
     uint16_t *h;                     // [2, T K, I]: and what its rounding left
     DecodeItems items;               // decode_items of the above
     // outputs
