@@ -155,8 +155,8 @@ struct Bf16 {
     using Args = Bf16Args;
     using Acc = f32x4_t;
     static constexpr bool APART = false;
-    static __device__ Acc mfma(u32x4_t a, u32x4_t b, Acc c) { return mfma16(as_bf16x8(a), as_bf16x8(b), c); }
-    static __device__ void mfma_acc(u32x4_t a, u32x4_t b, Acc &acc)
+    static __device__ __forceinline__ Acc mfma(u32x4_t a, u32x4_t b, Acc c) { return mfma16(as_bf16x8(a), as_bf16x8(b), c); }
+    static __device__ __forceinline__ void mfma_acc(u32x4_t a, u32x4_t b, Acc &acc)
     {
         asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
     }
@@ -166,7 +166,7 @@ struct Bf16 {
     struct Factors {
         f32x4_t bias, residual;
     };
-    static __device__ Factors load_factors(const Bf16Args &g, int r, int nb)
+    static __device__ __forceinline__ Factors load_factors(const Bf16Args &g, int r, int nb)
     {
         const int q = (threadIdx.x & (WAVE - 1)) >> 4, n = (g.glu ? nb / 2 : nb) * 16 + 4 * q;
         Factors v{{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -181,7 +181,7 @@ struct Bf16 {
     }
 
     // Outputs of one fragment of row block nb (a gate block with its up block's sums in `up` when glu).
-    static __device__ void emit(const Bf16Args &g, int r, int nb, const Factors &c, Acc sum, Acc up)
+    static __device__ __forceinline__ void emit(const Bf16Args &g, int r, int nb, const Factors &c, Acc sum, Acc up)
     {
         const int q = (threadIdx.x & (WAVE - 1)) >> 4, n = (g.glu ? nb / 2 : nb) * 16 + 4 * q;
         if (r >= g.T || n >= g.N)
@@ -208,7 +208,7 @@ struct Bf16 {
     template <int MF, int NF, bool GLU, bool>
     static constexpr int finish_bytes() { return 4 * MF * 8 * pitch<MF, NF>(); }
     template <int MF, int NF, bool GLU, bool>
-    static __device__ void finish(const Bf16Args &g, Acc (&acc)[MF][NF], u32x4_t *lds, int m0, int nb0, int wv)
+    static __device__ __forceinline__ void finish(const Bf16Args &g, Acc (&acc)[MF][NF], u32x4_t *lds, int m0, int nb0, int wv)
     {
         const int lane = threadIdx.x & (WAVE - 1), fa = wv / 2 * MF, fb = wv % 2 * NF;
         constexpr int PITCH = pitch<MF, NF>(), PIECES = (GLU ? NF / 2 : NF) * 2;   // pieces of a row

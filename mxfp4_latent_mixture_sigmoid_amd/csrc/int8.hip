@@ -32,11 +32,11 @@ struct Int8 {
     using Args = I8Args;
     using Acc = sums_t;
     static constexpr bool APART = true;
-    static __device__ Acc mfma(u32x4_t a, u32x4_t b, Acc c)
+    static __device__ __forceinline__ Acc mfma(u32x4_t a, u32x4_t b, Acc c)
     {
         return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(Acc, a), __builtin_bit_cast(Acc, b), c, 0, 0, 0);
     }
-    static __device__ void mfma_acc(u32x4_t a, u32x4_t b, Acc &acc)
+    static __device__ __forceinline__ void mfma_acc(u32x4_t a, u32x4_t b, Acc &acc)
     {
         asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
     }
@@ -50,7 +50,7 @@ struct Int8 {
 
     // The weights are the first matrix operand, so lane l of a fragment holds token row l % 16 and the packed
     // columns 4 (l / 16) .. +3 of row block nb. Rows and blocks past the end take the last ones' factors.
-    static __device__ Factors load_factors(const I8Args &g, int r, int nb)
+    static __device__ __forceinline__ Factors load_factors(const I8Args &g, int r, int nb)
     {
         const int q = (threadIdx.x & (WAVE - 1)) >> 4, at = min(nb, g.nblk - (g.glu ? 2 : 1)) * 16 + 4 * q;
         const float *other = g.glu ? g.sw + 16 : g.bias ? g.bias : g.sw;
@@ -62,7 +62,7 @@ struct Int8 {
     }
 
     // Outputs of one fragment of row block nb (a gate block with its up block's sums in `up` when glu).
-    static __device__ void emit(const I8Args &g, int r, int nb, const Factors &c, Acc sum, Acc up)
+    static __device__ __forceinline__ void emit(const I8Args &g, int r, int nb, const Factors &c, Acc sum, Acc up)
     {
         const int q = (threadIdx.x & (WAVE - 1)) >> 4, n = (g.glu ? nb / 2 : nb) * 16 + 4 * q;
         if (r >= g.T || n >= g.N)
@@ -80,7 +80,7 @@ struct Int8 {
     template <int MF, int NF, bool GLU, bool F32>
     static constexpr int finish_bytes() { return 4 * 16 * ((GLU ? NF / 2 : NF) * 16 * (F32 ? 4 : 2) + 16); }
     template <int MF, int NF, bool GLU, bool F32>
-    static __device__ void finish(const I8Args &g, Acc (&acc)[MF][NF], u32x4_t *lds, int m0, int nb0, int wv)
+    static __device__ __forceinline__ void finish(const I8Args &g, Acc (&acc)[MF][NF], u32x4_t *lds, int m0, int nb0, int wv)
     {
         const int lane = threadIdx.x & (WAVE - 1), r16 = lane & 15, fa = wv / 2 * MF, fb = wv % 2 * NF;
         constexpr int JO = GLU ? NF / 2 : NF, SIZE = F32 ? 4 : 2;        // output fragments, bytes per output

@@ -5,7 +5,8 @@
 // and where comments and figures speak of codes, two of them are one BF16 value.
 //
 // A product P supplies its arguments (ProductArgs and what its epilogue takes), the accumulator and its instruction,
-// and what becomes of the sums.
+// and what becomes of the sums. Its functions are inlined whatever their length: one that is called takes the sums by address,
+// which keeps them in memory through the whole main loop (8192 x 7168 x 14336 codes, FP32 outputs: 11.0 ms, and 0.61 so).
 #pragma once
 
 #include "dense.hpp"
