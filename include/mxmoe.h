@@ -422,8 +422,10 @@ void moe_linear_destroy(moe_linear *l);
  *   glu = 0:  out = a(x . w^T + bias) + residual
  *   glu = 1:  out = a(x . w^T) * (x . w_up^T) + residual
  * Everything after the sum is FP32, rounded once to out_type. A token's sums are added in an order that depends on the
- * sizes (T among them), so that its last bits may; the same call gives the same bits. silu and gelu_tanh use the
- * hardware's exponential: off by about 2 |v| 2^-24 of themselves where v is large and negative. */
+ * sizes (T among them), so that its last bits may; the same call gives the same bits. Activations of a finite v are off by at
+ * most, of themselves: gelu 24 x 2^-24; silu (24 + 6 |v|) 2^-24 and gelu_tanh (24 + 10 |q|) 2^-24 with its exponent q = sqrt(8 / pi)
+ * (v + 0.044715 v^3), since the argument of their exponential is rounded. Results below 2^-126 are 0, and those of silu from
+ * v = -87.3, of gelu_tanh from q = -87.3 down. */
 typedef enum {
     MOE_LINEAR_NONE = 0,       /* v                                                     */
     MOE_LINEAR_SILU = 1,       /* v / (1 + exp(-v))                                     */
