@@ -206,6 +206,7 @@ struct Bf16Part {
                     put(v[i], stage + at / (n * 4) * pitch + at % (n * 4) * 4, T * pitch);
                 }
             }
+            meet_lanes();
             const uint32_t *mine = stage + ((REST == 1 && row >= HALF ? T : 0) + r) * pitch + c * 4;
 #pragma unroll 1
             for (int s = 0; s < n; s += DEPTH)
@@ -237,6 +238,7 @@ struct Bf16Part {
 #pragma unroll
                     for (int i = 0; i < PIECES; i++)
                         put(v[i], stage + (i * WAVE + lane) / PER_ROW * PITCH + (i * WAVE + lane) % PER_ROW * 4, SECOND);
+                    meet_lanes();
                     fetch(s + h + CHUNK);
 #pragma unroll
                     for (int i = 0; i < CHUNK; i++) {
@@ -245,7 +247,7 @@ struct Bf16Part {
                         if (i % 4 == 3)
                             __builtin_amdgcn_sched_barrier(0);
                     }
-                    asm volatile("" ::: "memory");   // the chunk is read before it is overwritten
+                    meet_lanes();   // the chunk is read before it is overwritten
                 }
         }
     }
@@ -497,6 +499,7 @@ __device__ __forceinline__ void select_short(const DecodeArgs &a, int t, int go,
         total += (int)__popcll(all);
     }
     uint64_t mine = 0;
+    meet_lanes();
     if (total <= WAVE) {
         mine = lane < total ? scratch[lane] : 0;
         int rank = 0;
@@ -506,13 +509,16 @@ __device__ __forceinline__ void select_short(const DecodeArgs &a, int t, int go,
                                    (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)mine, m);
             rank += other > mine;
         }
+        meet_lanes();
         if (lane < total && rank < K)
             scratch[rank] = mine;
+        meet_lanes();
         mine = lane < K ? scratch[lane] : 0;
     } else {   // heavy ties: one maximum after another
 #pragma unroll
         for (int i = 0; i < QUADS * 4; i++)
             words[(i / 4 * WAVE + lane) * 4 + i % 4] = keys[i];
+        meet_lanes();
 #pragma unroll 1
         for (int k = 0; k < K; k++) {
             uint64_t best = 0;
@@ -709,6 +715,7 @@ __device__ __forceinline__ bool gate_one(const DecodeArgs &a, int item, const Se
                 *reinterpret_cast<u32x4_t *>(to + WAVE * 4 + pitch) = v3;
             }
         }
+        meet_lanes();
         f32x4_t acc[2] = {};
 #pragma unroll 1
         for (int s = 0; s < n; s += BATCH)

@@ -10,6 +10,7 @@
 #pragma once
 
 #include "dense.hpp"
+#include "wave.hpp"
 
 #include <type_traits>
 #include <utility>
@@ -378,16 +379,6 @@ __device__ inline void settle(A (&acc)[MF][NF])
 #pragma unroll
         for (int j = 0; j < NF; j++)
             asm volatile("" : "+a"(acc[f][j]));   // no copy of a sum moves across
-}
-
-// Between what lanes of a wave write to LDS and what its other lanes read of it, or write over it next: the memory
-// model orders the two only past a fence and a barrier, though a wave's accesses to LDS are done in order anyway, so
-// that neither costs an instruction here.
-__device__ inline void meet_lanes()
-{
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // MF and NF: row and column fragments per wave; tiles of 32 MF x 32 NF. 128-token tiles take 80 KiB of LDS or

@@ -58,6 +58,7 @@ __device__ inline void select_best(int K, const uint32_t *key, uint64_t *scratch
         for (int j = 0; j < SLOTS; j++)
             if (key[j] != 0u && key[j] >= bound)
                 scratch[pos++] = c[j];
+        meet_lanes();
         const uint64_t mine = lane < total ? scratch[lane] : 0;
         const uint32_t mh = (uint32_t)(mine >> 32), ml = (uint32_t)mine;
         int rank = 0;
@@ -65,9 +66,12 @@ __device__ inline void select_best(int K, const uint32_t *key, uint64_t *scratch
             const uint32_t oh = __builtin_amdgcn_readlane(mh, m), ol = __builtin_amdgcn_readlane(ml, m);
             rank += (oh > mh || (oh == mh && ol > ml)) ? 1 : 0;
         }
+        meet_lanes();
         if (lane < total && rank < K)
             scratch[rank] = mine;
+        meet_lanes();
         const uint64_t r = lane < K ? scratch[lane] : 0;
+        meet_lanes();   // the caller's next token
         my_key = (uint32_t)(r >> 32);
         my_id = (int)~(uint32_t)r;
     } else {

@@ -6,6 +6,16 @@
 
 namespace mxmoe {
 
+// Between what lanes of a wave write to LDS and what its other lanes read of it, or write over it next: the memory
+// model orders the two only past a fence and a barrier, though a wave's accesses to LDS are done in order anyway, so
+// that neither costs an instruction here.
+__device__ inline void meet_lanes()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // DPP controls (GFX9 encoding).
 constexpr int DPP_QUAD_1032 = 0xB1;   // quad_perm [1,0,3,2]
 constexpr int DPP_QUAD_2301 = 0x4E;   // quad_perm [2,3,0,1]
