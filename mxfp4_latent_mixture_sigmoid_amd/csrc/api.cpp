@@ -8,6 +8,7 @@
 #include <cstdlib>
 #include <new>
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 #include <vector>
 
@@ -1034,7 +1035,7 @@ moe_status moe_route_forward_static(moe_handle *h, const void *x, int32_t T, con
 
 namespace {
 
-int decode_patience = DECODE_PATIENCE;
+std::atomic<int> decode_patience{DECODE_PATIENCE};   // any thread's calls read it
 
 struct DecodeLayout {
     int64_t counters, claims, partial, logits, weights, chosen, list, pairs, z, z_rest, h, total;
@@ -1092,7 +1093,10 @@ bool decode_supported(const moe_config *c, int64_t T)
 
 extern "C" {
 
-void moe_decode_patience(int32_t times) { decode_patience = times < 0 ? DECODE_PATIENCE : times; }
+void moe_decode_patience(int32_t times) 
+{
+    decode_patience.store(times < 0 ? DECODE_PATIENCE : times, std::memory_order_relaxed);
+}
 
 moe_status moe_decode_query(const moe_config *cfg, int32_t T, size_t *workspace_bytes)
 {
@@ -1156,7 +1160,7 @@ moe_status moe_decode(moe_handle *h, const void *x, int32_t T, const float *logi
     a.pairs = reinterpret_cast<int16_t *>(ws + L.pairs);
     a.chosen = reinterpret_cast<int32_t *>(ws + L.chosen);
     a.claims = reinterpret_cast<uint32_t *>(ws + L.claims);
-    a.patience = decode_patience;
+    a.patience = decode_patience.load(std::memory_order_relaxed);
     a.partial = reinterpret_cast<float *>(ws + L.partial);
     a.z_rest = reinterpret_cast<uint16_t *>(ws + L.z_rest);
     a.most = (int)L.most;
