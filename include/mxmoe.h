@@ -436,7 +436,7 @@ typedef enum {
 #define MOE_DENSE_MAX_K 131072
 typedef struct {
     int32_t n;            /* output channels, >= 1                    */
-    int32_t k;            /* input width, 1..MOE_DENSE_MAX_K    */
+    int32_t k;            /* input width, 1..MOE_DENSE_MAX_K          */
     int32_t glu;          /* 0 or 1                                   */
     int32_t act;          /* moe_linear_act (of the gate when glu)    */
     int32_t out_type;     /* moe_type                                 */
@@ -452,17 +452,16 @@ typedef struct {
 typedef struct moe_dense moe_dense;
 
 /* As moe_linear_query, moe_linear_create and moe_linear_destroy. */
-moe_status moe_dense_query(const moe_dense_config *cfg, int32_t T_max, size_t *packed_bytes,
-                                 size_t *workspace_bytes);
-moe_status moe_dense_create(const moe_dense_config *cfg, const moe_dense_weights *w, void *packed,
-                                  size_t packed_bytes, void *stream, moe_dense **out);
+moe_status moe_dense_query(const moe_dense_config *cfg, int32_t T_max, size_t *packed_bytes, size_t *workspace_bytes);
+moe_status moe_dense_create(const moe_dense_config *cfg, const moe_dense_weights *w, void *packed, size_t packed_bytes,
+                            void *stream, moe_dense **out);
 /* The product for T >= 0 tokens (0 enqueues nothing). x: bf16 [T, k]; residual: [T, n] of res_type (moe_type), or NULL; it
  * may be out itself (same type, pointer and stride); out: out_type [T, n], must not overlap any other input. workspace: as
  * moe_linear_forward's; rows at 16-byte steps of at most 2^22 bytes from a 16-byte aligned address with k a multiple of 64
  * never need one. */
 moe_status moe_dense_forward(moe_dense *l, const void *x, int64_t ldx, const void *residual, int32_t res_type,
-                                   int64_t ldr, int32_t T, void *out, int64_t ldo, void *workspace, size_t workspace_bytes,
-                                   void *stream);
+                             int64_t ldr, int32_t T, void *out, int64_t ldo, void *workspace, size_t workspace_bytes,
+                             void *stream);
 void moe_dense_destroy(moe_dense *l);
 
 /* Static description of a status code. */

@@ -142,10 +142,9 @@ SIGNATURES = {
                                   ctypes.POINTER(c_vp)]),
     "moe_linear_forward": (c_i32, [c_vp, c_vp, c_i64, c_vp, c_i32, c_vp, c_i64, c_vp, c_size, c_vp]),
     "moe_linear_destroy": (None, [c_vp]),
-    "moe_dense_query": (c_i32, [ctypes.POINTER(DenseConfig), c_i32, ctypes.POINTER(c_size),
-                                      ctypes.POINTER(c_size)]),
-    "moe_dense_create": (c_i32, [ctypes.POINTER(DenseConfig), ctypes.POINTER(DenseWeights), c_vp, c_size,
-                                       c_vp, ctypes.POINTER(c_vp)]),
+    "moe_dense_query": (c_i32, [ctypes.POINTER(DenseConfig), c_i32, ctypes.POINTER(c_size), ctypes.POINTER(c_size)]),
+    "moe_dense_create": (c_i32, [ctypes.POINTER(DenseConfig), ctypes.POINTER(DenseWeights), c_vp, c_size, c_vp,
+                                 ctypes.POINTER(c_vp)]),
     "moe_dense_forward": (c_i32, [c_vp, c_vp, c_i64, c_vp, c_i32, c_i64, c_i32, c_vp, c_i64, c_vp, c_size, c_vp]),
     "moe_dense_destroy": (None, [c_vp]),
     "moe_strerror": (ctypes.c_char_p, [c_i32]),
@@ -338,7 +337,7 @@ def dense_create(cfg: DenseConfig, w, w_up, bias, packed, stream: int) -> c_vp:
     lw = DenseWeights(ptr(w), ptr(w_up), ptr(bias))
     h = c_vp()
     check(lib().moe_dense_create(ctypes.byref(cfg), ctypes.byref(lw), ptr(packed), packed.numel(), c_vp(stream),
-                                       ctypes.byref(h)), "moe_dense_create")
+                                 ctypes.byref(h)), "moe_dense_create")
     return h
 
 

