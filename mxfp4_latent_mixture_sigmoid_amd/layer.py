@@ -98,10 +98,10 @@ class MoELayer:
         """The whole layer for x [T, Hin] BF16 of at most 16 tokens, in one launch (and a small one that clears its
         counters): what route_forward computes, without its routing arrays, nearer to the exact result (z, the experts' inner
         values and the weighted sum are held in 16 bits, an expert's output in FP32, where route_forward rounds each to
-        BF16's 8), and a token's outputs are the same bits whatever tokens
-        come with it. Of one GPU's TP8 share 54 us for one token (route_forward 68), 75 for 4 (82), 99 for 8 (103), 122 for
-        9 (107), 166 for 16 (136): above eight tokens route_forward is the faster one. Outputs go into the given tensors if any (contiguous;
-        logits_out FP32 [T, E]). The call allocates its own workspace, so that calls may overlap on different streams and in
+        BF16's 8), and a token's outputs are the same bits whatever tokens come with it. Of one GPU's TP8 share 54 us for one
+        token (route_forward 68), 75 for 4 (82), 99 for 8 (103), 122 for 9 (107), 166 for 16 (136): above eight tokens
+        route_forward is the faster one. Outputs go into the given tensors if any (contiguous; logits_out FP32 [T, E]). The
+        call allocates its own workspace, so that calls may overlap on different streams and in
         captured graphs."""
         index = self.packed.get_device()
         if stream is not None and stream.device_index != index:
