@@ -51,6 +51,11 @@
 #include "select.hpp"
 #include "sync.hpp"
 
+// Each item is compiled several times (for the helpers, for up to 8 tokens and more), and has to give the same bits in each: a
+// product and a sum are one operation only where the code says so. Left to choose, the compiler took the remainder of
+// silu(g) u from the unrounded product in the helpers' copy of one token's gate item, and from the rounded one in the other.
+#pragma clang fp contract(off)
+
 namespace mxmoe {
 
 namespace {
